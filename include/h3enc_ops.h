@@ -323,6 +323,110 @@ H3ENC_API h3enc_status h3enc_op_embed(const int32_t *ids, const void *table, int
 H3ENC_API h3enc_status h3enc_op_vis_rank(const uint8_t *mask, int32_t S, int32_t n_vis, int32_t *vis_rank,
                                int32_t *status, void *stream);
 
+/* ---- decoding from a paged key/value cache ----
+ * The steps that extend an encoded prompt token by token (no counterpart on the pages,
+ * which stop at the prefill): a projection's q/k heads normed, rotated and stored in a
+ * cache, the attention of one new token of every sequence over it, and the eviction of
+ * the tokens that drew the least attention.  All three run without host synchronisation,
+ * read lengths and page numbers on the device, and can be captured in a CUDA graph.
+ *
+ * A cache holds the keys and values of one decoder layer in pages of page_size tokens;
+ * element e of kv head g of the token in place s of page p is
+ *   k[p * page_stride + (g * page_size + s) * head_dim + e]   (elements; v the same).
+ * A sequence's token i is in place i % page_size of page page_table[b * ld_table +
+ * i / page_size].  The pages of one layer may lie apart (page_stride), so that one
+ * allocation can hold K and V, or all layers, side by side.  E4M3 caches store
+ * e4m3(x / scale[g]) (fp32 division, rounded to nearest even, saturating at +-448) and
+ * stand for that value times scale[g].
+ * Requires page_size in {16, 32, 64, 128, 256}, head_dim in {64, 128}, k and v 16-byte
+ * aligned, page_stride >= n_kv_heads * page_size * head_dim, its bytes a multiple of 16
+ * and below 2^40, num_pages * page_size < 2^31. */
+typedef struct {
+    void *k, *v;
+    const float *k_scale, *v_scale;   /* [n_kv_heads], FP8_E4M3 only; NULL for BF16 */
+    int64_t page_stride;              /* elements from one page to the next */
+    int32_t num_pages, page_size, n_kv_heads, head_dim;
+    int32_t dtype;                    /* H3ENC_DTYPE_BF16 or H3ENC_DTYPE_FP8_E4M3 */
+} h3enc_kv_cache;
+
+/* Per-head q/k RMSNorm and rotation of a packed projection, and the K and V heads stored
+ * in a cache, in one pass (what h3enc_op_gemm_qkv_rope does in its epilogue, for a
+ * projection that comes from elsewhere: h3enc_op_gemm_fp8, h3enc_op_gemm_bias, few rows).
+ *   qkv [T, ld_qkv]: q head h at column h*d, k head g at (n_heads+g)*d, v head g at
+ *   (n_heads+n_kv_heads+g)*d.  Each q and k head becomes rope(rmsnorm(x, w_q or w_k, eps))
+ *   in fp32, rounded once: w_q / w_k NULL skips that norm, cos_tab = sin_tab = NULL the
+ *   rotation; tables of either layout of h3enc_op_rope_table_ex (cs_stride as there).
+ *   q_out [T, ld_q] and k_out [T, ld_k] (n_heads*d and n_kv_heads*d columns; NULL: not
+ *   written) may be qkv's own q and k columns (same leading dimension), and must not
+ *   overlap qkv or each other otherwise.
+ *   cache (or NULL) with slots [T]: k and v of row t go to place slots[t] % page_size of page
+ *   slots[t] / page_size.  A negative slot stores nothing (a padding row); one past the last
+ *   page stores nothing and sets status bit 2.  Rows that share a slot overwrite each
+ *   other in no stated order.
+ * Requires head_dim in {64, 128}, leading dimensions that are multiples of 8, operands
+ * 16-byte aligned, at least one of q_out, k_out and cache. */
+H3ENC_API h3enc_status h3enc_op_qk_norm_rope(const void *qkv, int64_t ld_qkv, int32_t T, int32_t n_heads,
+                                             int32_t n_kv_heads, int32_t head_dim, const void *w_q,
+                                             const void *w_k, float eps, const float *cos_tab,
+                                             const float *sin_tab, int32_t cs_stride, void *q_out, int64_t ld_q,
+                                             void *k_out, int64_t ld_k, const h3enc_kv_cache *cache,
+                                             const int32_t *slots, int32_t *status, void *stream);
+
+/* Attention of one new token of each of n_seqs sequences over the cache (the new token's
+ * own key and value already in it): for q head h, reading kv head h / (n_heads / n_kv_heads),
+ *   p_i = softmax_i(q . k_i / sqrt(d)) over i < seq_lens[b],   o = sum_i p_i v_i
+ * (fp32; o rounded to bf16 once; a sequence of length 0 gives a zero row).
+ *   q [n_seqs, ld_q], o [n_seqs, ld_o]: head h at column h*d; o must not overlap q.
+ *   page_table DEVICE int32 [n_seqs, ld_table], seq_lens DEVICE int32 [n_seqs]; max_len: a
+ *   bound on the lengths known to the host (ld_table * page_size >= max_len).  A length
+ *   outside [0, max_len] is clamped into it and a page number outside the cache reads as
+ *   zero keys and values; both set status bit 2.
+ *   weight_out (or NULL) [n_seqs, ld_weight], ld_weight >= max_len: for i < seq_lens[b],
+ *   weight_out[b][i] = weight_in[b][i] + sum over all q heads of p_i (weight_in NULL:
+ *   from 0; it may equal weight_out, and must not overlap it otherwise).  Entries
+ *   from the length on are left as they were.
+ *   workspace: h3enc_op_attention_decode_workspace_bytes() bytes, 256-byte aligned,
+ *   zero-filled once before its first use and then reused by calls of any sizes that fit.
+ *   Calls (and graphs that hold them) sharing it must not overlap on the GPU.
+ * The result does not depend on timing: the same inputs give the same bits on every run.
+ * Requires n_seqs <= 1024, n_heads % n_kv_heads == 0, leading dimensions of q and o that are
+ * multiples of 8, q and o 16-byte aligned. */
+H3ENC_API h3enc_status h3enc_op_attention_decode(const void *q, int64_t ld_q, void *o, int64_t ld_o,
+                                                 const h3enc_kv_cache *cache, const int32_t *page_table,
+                                                 int32_t ld_table, const int32_t *seq_lens, int32_t n_seqs,
+                                                 int32_t n_heads, int32_t max_len, const float *weight_in,
+                                                 float *weight_out, int64_t ld_weight, void *workspace,
+                                                 int64_t workspace_bytes, int32_t *status, void *stream);
+
+/* Workspace bytes of h3enc_op_attention_decode on the current device; with_weights: the
+ * call passes weight_out.  -1 without a device or for sizes the call refuses. */
+H3ENC_API int64_t h3enc_op_attention_decode_workspace_bytes(int32_t n_seqs, int32_t n_heads, int32_t max_len,
+                                                            int32_t with_weights);
+
+/* Eviction from the cache by accumulated attention weight.  A sequence longer than `budget`
+ * keeps budget tokens: its first `sink`, its last `recent` and, of the others, those of the
+ * largest weight (of equal ones the earlier; NaN counts as the smallest).  The kept tokens
+ * keep their order and move, K, V and weight, to the front.  Shorter sequences keep all.
+ *   page_table, seq_lens, max_len as for h3enc_op_attention_decode (lengths clamped the same way).
+ *   page_table_out NULL: in place, within the pages of page_table (which must not be shared
+ *   between sequences).  Otherwise DEVICE int32 [n_seqs, ld_table_out], ld_table_out *
+ *   page_size >= min(budget, max_len): token i of the result goes to page
+ *   page_table_out[b][i / page_size], pages that this call does not read; the source
+ *   pages stay as they were.  Tokens whose page number, on either side, lies
+ *   outside the cache are not moved and set status bit 2.
+ *   weight [n_seqs, ld_weight] in, weight_out [n_seqs, ld_weight_out] out (leading dimensions
+ *   >= max_len, no overlap): weight_out[b][i] = weight[b][kept[b][i]] for i < new_lens[b],
+ *   0 from there to max_len (tokens appended later start at 0).
+ *   kept int32 [n_seqs, ld_kept], ld_kept >= budget: the places the kept tokens had,
+ *   ascending, then -1 up to budget.  new_lens int32 [n_seqs] (may be seq_lens itself).
+ * Requires budget >= 1, sink + recent <= budget, n_seqs <= 1024. */
+H3ENC_API h3enc_status h3enc_op_cache_evict(const h3enc_kv_cache *cache, const int32_t *page_table, int32_t ld_table,
+                                            const int32_t *page_table_out, int32_t ld_table_out,
+                                            const int32_t *seq_lens, int32_t n_seqs, int32_t max_len, int32_t budget,
+                                            int32_t sink, int32_t recent, const float *weight, int64_t ld_weight,
+                                            float *weight_out, int64_t ld_weight_out, int32_t *kept, int64_t ld_kept,
+                                            int32_t *new_lens, int32_t *status, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

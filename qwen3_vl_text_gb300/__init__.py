@@ -29,7 +29,8 @@ __all__ = [
     "h3enc_op_attention_bidir_ws", "h3enc_op_attention_workspace_bytes",
     "h3vis_create", "h3vis_load_weights", "h3vis_finalize_weights", "h3vis_encode", "h3vis_get_status",
     "h3vis_last_error", "h3vis_launch_count", "h3vis_destroy", "VisionEncoder", "h3enc_op_attention", "h3enc_op_embed", "h3enc_op_vis_rank", "Encoder",
-    "KERNEL_CLASSES",
+    "KERNEL_CLASSES", "KVCache", "h3enc_op_qk_norm_rope", "h3enc_op_attention_decode",
+    "h3enc_op_attention_decode_workspace_bytes", "h3enc_op_cache_evict",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -65,6 +66,36 @@ class VisionConfig(ctypes.Structure):
                 ("out_hidden", ctypes.c_int32), ("num_position_embeddings", ctypes.c_int32),
                 ("num_deepstack", ctypes.c_int32), ("deepstack_indexes", ctypes.c_int32 * 8),
                 ("ln_eps", ctypes.c_float), ("rope_theta", ctypes.c_float), ("max_patches", ctypes.c_int32)]
+
+
+class KVCache(ctypes.Structure):
+    """h3enc_kv_cache over torch tensors k and v [num_pages, n_kv_heads, page_size, head_dim]
+    (bfloat16, or float8_e4m3fn with float32 k_scale and v_scale [n_kv_heads]); the pages may lie
+    apart (stride 0 of both tensors, the same), the rest is contiguous.  Keeps the tensors alive."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("page_stride", ctypes.c_int64), ("num_pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("dtype", ctypes.c_int32)]
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        import torch
+        pages, heads, size, dim = k.shape
+        if v.shape != k.shape or v.dtype != k.dtype or v.stride() != k.stride():
+            raise ValueError("KVCache: k and v differ in shape, type or strides")
+        if k.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
+            raise ValueError(f"KVCache: bfloat16 or float8_e4m3fn, not {k.dtype}")
+        stride = k.stride(0) if pages > 1 else max(k.stride(0), heads * size * dim)
+        if pages and k.stride()[1:] != (size * dim, dim, 1):
+            raise ValueError("KVCache: the heads, places and elements of a page must be contiguous")
+        for t in (k_scale, v_scale):
+            if t is not None and (t.dtype != torch.float32 or t.shape != (heads,) or not t.is_contiguous()):
+                raise ValueError("KVCache: scales are contiguous float32 [n_kv_heads]")
+        for t in (v, k_scale, v_scale):
+            if t is not None and t.device != k.device:
+                raise ValueError("KVCache: tensors on different devices")
+        super().__init__(k.data_ptr(), v.data_ptr(), _ptr(k_scale), _ptr(v_scale), stride, pages, size, heads, dim,
+                         2 if k.dtype == torch.float8_e4m3fn else 0)
+        self.tensors = (k, v, k_scale, v_scale)
 
 
 def _load():
@@ -134,6 +165,13 @@ _SIGS = {
     "h3enc_op_attention_bidir": ([_P, _P, _I32, _I32, _I32, _P, _I32, _P], _I32),
     "h3enc_op_attention_bidir_ws": ([_P, _P, _I32, _I32, _I32, _P, _I32, _P, _I64, _P], _I32),
     "h3enc_op_attention_workspace_bytes": ([_I32], _I64),
+    "h3enc_op_qk_norm_rope": ([_P, _I64, _I32, _I32, _I32, _I32, _P, _P, _F, _P, _P, _I32, _P, _I64, _P, _I64,
+                               ctypes.POINTER(KVCache), _P, _P, _P], _I32),
+    "h3enc_op_attention_decode": ([_P, _I64, _P, _I64, ctypes.POINTER(KVCache), _P, _I32, _P, _I32, _I32, _I32, _P, _P,
+                                   _I64, _P, _I64, _P, _P], _I32),
+    "h3enc_op_attention_decode_workspace_bytes": ([_I32, _I32, _I32, _I32], _I64),
+    "h3enc_op_cache_evict": ([ctypes.POINTER(KVCache), _P, _I32, _P, _I32, _P, _I32, _I32, _I32, _I32, _I32, _P, _I64,
+                              _P, _I64, _P, _I64, _P, _P, _P], _I32),
     "h3vis_create": ([ctypes.POINTER(VisionConfig), ctypes.POINTER(_P)], _I32),
     "h3vis_load_weights": ([_P, ctypes.c_char_p, _P, _I32, ctypes.POINTER(_I64), _I32, _I32], _I32),
     "h3vis_finalize_weights": ([_P], _I32),
@@ -528,6 +566,49 @@ def h3enc_op_attention_bidir_ws(qkv, o, S, heads, head_dim, workspace, cu_seqlen
     wbytes = workspace.numel() * workspace.element_size()
     return _check(lib.h3enc_op_attention_bidir_ws(_ptr(qkv), _ptr(o), S, heads, head_dim, cu, n_seqs,
                                                   _ptr(workspace), wbytes, _stream(stream)))
+
+
+def _ld(t, width):
+    """Leading dimension of a row-major matrix of `width` columns (a tensor's row stride)."""
+    return t.stride(0) if t is not None and not isinstance(t, int) and t.shape[0] > 1 else width
+
+
+def h3enc_op_qk_norm_rope(qkv, T, n_heads, n_kv_heads, head_dim, w_q, w_k, eps, cos_tab, sin_tab, cs_stride=0,
+                          q_out=None, k_out=None, cache=None, slots=None, status=None, stream=None):
+    """Per-head q/k RMSNorm and rotation of a packed projection; K and V also into a KVCache."""
+    return _check(lib.h3enc_op_qk_norm_rope(
+        _ptr(qkv), _ld(qkv, (n_heads + 2 * n_kv_heads) * head_dim), T, n_heads, n_kv_heads, head_dim, _ptr(w_q),
+        _ptr(w_k), eps, _ptr(cos_tab), _ptr(sin_tab), cs_stride, _ptr(q_out), _ld(q_out, n_heads * head_dim),
+        _ptr(k_out), _ld(k_out, n_kv_heads * head_dim), cache, _ptr(slots), _ptr(status), _stream(stream)))
+
+
+def h3enc_op_attention_decode_workspace_bytes(n_seqs, n_heads, max_len, with_weights=False) -> int:
+    return lib.h3enc_op_attention_decode_workspace_bytes(n_seqs, n_heads, max_len, 1 if with_weights else 0)
+
+
+def h3enc_op_attention_decode(q, o, cache, page_table, seq_lens, n_heads, max_len, workspace, weight_in=None,
+                              weight_out=None, status=None, stream=None):
+    """Attention of one new token per sequence over a KVCache: q, o [n_seqs, n_heads * head_dim],
+    page_table int32 [n_seqs, pages], seq_lens int32 [n_seqs], weights float32 [n_seqs, >= max_len]."""
+    n_seqs, width = seq_lens.shape[0], n_heads * cache.head_dim
+    ld_w = 0 if weight_out is None else _ld(weight_out, weight_out.shape[1])
+    if weight_in is not None and _ld(weight_in, ld_w) != ld_w:
+        raise ValueError("attention_decode: weight_in and weight_out have different row strides")
+    return _check(lib.h3enc_op_attention_decode(
+        _ptr(q), _ld(q, width), _ptr(o), _ld(o, width), cache, _ptr(page_table), _ld(page_table, page_table.shape[1]),
+        _ptr(seq_lens), n_seqs, n_heads, max_len, _ptr(weight_in), _ptr(weight_out), ld_w, _ptr(workspace),
+        0 if workspace is None else workspace.numel() * workspace.element_size(), _ptr(status), _stream(stream)))
+
+
+def h3enc_op_cache_evict(cache, page_table, seq_lens, max_len, budget, weight, weight_out, kept, new_lens,
+                         page_table_out=None, sink=0, recent=0, status=None, stream=None):
+    """Keep `budget` tokens per sequence by accumulated weight; in place, or into page_table_out's pages."""
+    out_ld = 0 if page_table_out is None else _ld(page_table_out, page_table_out.shape[1])
+    return _check(lib.h3enc_op_cache_evict(
+        cache, _ptr(page_table), _ld(page_table, page_table.shape[1]), _ptr(page_table_out), out_ld, _ptr(seq_lens),
+        seq_lens.shape[0], max_len, budget, sink, recent, _ptr(weight), _ld(weight, weight.shape[1]), _ptr(weight_out),
+        _ld(weight_out, weight_out.shape[1]), _ptr(kept), _ld(kept, kept.shape[1]), _ptr(new_lens), _ptr(status),
+        _stream(stream)))
 
 
 def h3vis_create(cfg: VisionConfig):

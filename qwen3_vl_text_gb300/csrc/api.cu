@@ -1438,3 +1438,191 @@ h3enc_status h3enc_op_vis_rank(const uint8_t *mask, int32_t S, int32_t n_vis, in
 }
 
 }  // extern "C"
+
+// ---------------------------------------------------------------- decoding from a paged cache
+
+namespace {
+
+bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+// Whether row-major matrices a [rows, ca] and b [rows, cb] (lda, ldb elements of es bytes from
+// row to row) may share an element.  With one leading dimension their columns are told apart
+// (slices of one packed buffer); otherwise their address ranges are.
+bool rows_overlap(const void *a, int64_t lda, int64_t ca, const void *b, int64_t ldb, int64_t cb, int64_t rows,
+                  int64_t es) {
+    const int64_t pa = (int64_t)reinterpret_cast<uintptr_t>(a), pb = (int64_t)reinterpret_cast<uintptr_t>(b);
+    const int64_t ea = pa + ((rows - 1) * lda + ca) * es, eb = pb + ((rows - 1) * ldb + cb) * es;
+    if (rows <= 0 || ea <= pb || eb <= pa) return false;
+    if (lda != ldb) return true;
+    const int64_t row = lda * es;
+    int64_t delta = (pb - pa) % row;   // where b's first column lies in a row of a
+    if (delta < 0) delta += row;
+    return delta < ca * es || delta + cb * es > row;
+}
+
+h3enc_status take_cache(const h3enc_kv_cache *c, const char *who, h3::KvCache *out) {
+    if (!c || !c->k || !c->v || !aligned16(c->k) || !aligned16(c->v))
+        return fail(nullptr, H3ENC_ERR_INVALID_ARG, "%s: cache NULL or not 16-byte aligned", who);
+    if (c->dtype != H3ENC_DTYPE_BF16 && c->dtype != H3ENC_DTYPE_FP8_E4M3)
+        return fail(nullptr, H3ENC_ERR_UNSUPPORTED, "%s: cache dtype must be BF16 or FP8_E4M3", who);
+    if (c->head_dim != 64 && c->head_dim != 128)
+        return fail(nullptr, H3ENC_ERR_UNSUPPORTED, "%s: cache head_dim must be 64 or 128", who);
+    int shift = 4;
+    while (shift < 8 && (1 << shift) != c->page_size) ++shift;
+    if ((1 << shift) != c->page_size)
+        return fail(nullptr, H3ENC_ERR_UNSUPPORTED, "%s: page_size must be 16, 32, 64, 128 or 256", who);
+    const bool f8 = c->dtype == H3ENC_DTYPE_FP8_E4M3;
+    const int64_t es = f8 ? 1 : 2;
+    if (c->n_kv_heads < 1 || c->num_pages < 1 || (int64_t)c->num_pages * c->page_size > INT32_MAX ||
+        c->page_stride < (int64_t)c->n_kv_heads * c->page_size * c->head_dim ||
+        c->page_stride >= (int64_t(1) << 40) / es || c->page_stride * es % 16)
+        return fail(nullptr, H3ENC_ERR_INVALID_ARG, "%s: bad cache sizes or page stride", who);
+    if (f8 ? (!c->k_scale || !c->v_scale) : (c->k_scale || c->v_scale))
+        return fail(nullptr, H3ENC_ERR_INVALID_ARG, "%s: an FP8_E4M3 cache needs k_scale and v_scale, a BF16 cache "
+                                                    "takes none", who);
+    *out = h3::KvCache{c->k, c->v, c->k_scale, c->v_scale, c->page_stride, c->num_pages, shift, c->n_kv_heads,
+                       c->head_dim, f8};
+    return H3ENC_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+h3enc_status h3enc_op_qk_norm_rope(const void *qkv, int64_t ld_qkv, int32_t T, int32_t n_heads, int32_t n_kv_heads,
+                                   int32_t head_dim, const void *w_q, const void *w_k, float eps,
+                                   const float *cos_tab, const float *sin_tab, int32_t cs_stride, void *q_out,
+                                   int64_t ld_q, void *k_out, int64_t ld_k, const h3enc_kv_cache *cache,
+                                   const int32_t *slots, int32_t *status, void *stream) {
+    const char *who = "qk_norm_rope";
+    if (T < 0 || n_heads < 1 || n_kv_heads < 1 || (head_dim != 64 && head_dim != 128) || n_heads > 65536 ||
+        n_kv_heads > 65536)
+        return fail(nullptr, H3ENC_ERR_INVALID_ARG, "%s: bad sizes", who);
+    const int64_t d = head_dim, cols = ((int64_t)n_heads + 2 * (int64_t)n_kv_heads) * d;
+    if (!qkv || !aligned16(qkv) || ld_qkv < cols || ld_qkv % 8)
+        return fail(nullptr, H3ENC_ERR_INVALID_ARG, "%s: qkv NULL, misaligned or its leading dimension bad", who);
+    if ((cos_tab == nullptr) != (sin_tab == nullptr) || !aligned16(cos_tab) || !aligned16(sin_tab) || cs_stride < 0 ||
+        (cs_stride && cs_stride < T))
+        return fail(nullptr, H3ENC_ERR_INVALID_ARG, "%s: one table NULL or misaligned, or table stride below T", who);
+    if (((w_q || w_k) && !(eps >= 0.f)) || !aligned16(w_q) || !aligned16(w_k))
+        return fail(nullptr, H3ENC_ERR_INVALID_ARG, "%s: norm weight misaligned or eps negative", who);
+    if (!q_out && !k_out && !cache) return fail(nullptr, H3ENC_ERR_INVALID_ARG, "%s: no output", who);
+    if ((q_out && (!aligned16(q_out) || ld_q < n_heads * d || ld_q % 8)) ||
+        (k_out && (!aligned16(k_out) || ld_k < n_kv_heads * d || ld_k % 8)))
+        return fail(nullptr, H3ENC_ERR_INVALID_ARG, "%s: output misaligned or its leading dimension bad", who);
+    const char *q_at = static_cast<const char *>(qkv), *k_at = q_at + n_heads * d * 2;
+    const auto in_place = [&](const void *out, const char *at, int64_t ld) {
+        return out == at && (ld == ld_qkv || T <= 1);
+    };
+    if ((q_out && !in_place(q_out, q_at, ld_q) &&
+         rows_overlap(qkv, ld_qkv, cols, q_out, ld_q, n_heads * d, T, 2)) ||
+        (k_out && !in_place(k_out, k_at, ld_k) &&
+         rows_overlap(qkv, ld_qkv, cols, k_out, ld_k, n_kv_heads * d, T, 2)) ||
+        (q_out && k_out && rows_overlap(q_out, ld_q, n_heads * d, k_out, ld_k, n_kv_heads * d, T, 2)))
+        return fail(nullptr, H3ENC_ERR_INVALID_ARG, "%s: outputs overlap qkv (other than in place) or each other", who);
+    h3::QkNormRope p{};
+    if (cache) {
+        const h3enc_status s = take_cache(cache, who, &p.cache);
+        if (s != H3ENC_OK) return s;
+        if (!slots || cache->n_kv_heads != n_kv_heads || cache->head_dim != head_dim)
+            return fail(nullptr, H3ENC_ERR_INVALID_ARG, "%s: slots NULL or the cache has other heads", who);
+        p.has_cache = true;
+    } else if (slots) {
+        return fail(nullptr, H3ENC_ERR_INVALID_ARG, "%s: slots without a cache", who);
+    }
+    if (T == 0) return H3ENC_OK;
+    p.qkv = static_cast<const bf16 *>(qkv); p.ld_qkv = ld_qkv;
+    p.T = T; p.nq = n_heads; p.nkv = n_kv_heads; p.d = head_dim;
+    p.wq = static_cast<const bf16 *>(w_q); p.wk = static_cast<const bf16 *>(w_k); p.eps = eps;
+    p.cos_t = cos_tab; p.sin_t = sin_tab; p.cs_rows = cs_stride;
+    p.q_out = static_cast<bf16 *>(q_out); p.ld_q = ld_q;
+    p.k_out = static_cast<bf16 *>(k_out); p.ld_k = ld_k;
+    p.slots = slots; p.status = status;
+    cudaError_t e = h3::launch_qk_norm_rope(p, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? H3ENC_OK : cuda_fail(nullptr, e, "qk_norm_rope launch");
+}
+
+int64_t h3enc_op_attention_decode_workspace_bytes(int32_t n_seqs, int32_t n_heads, int32_t max_len,
+                                                  int32_t with_weights) {
+    const int sms = h3::device_num_sms();
+    const size_t n = sms > 0 ? h3::attention_decode_workspace_bytes(sms, n_seqs, n_heads, max_len, with_weights != 0)
+                             : 0;
+    return n ? (int64_t)n : -1;
+}
+
+h3enc_status h3enc_op_attention_decode(const void *q, int64_t ld_q, void *o, int64_t ld_o, const h3enc_kv_cache *cache,
+                                       const int32_t *page_table, int32_t ld_table, const int32_t *seq_lens,
+                                       int32_t n_seqs, int32_t n_heads, int32_t max_len, const float *weight_in,
+                                       float *weight_out, int64_t ld_weight, void *workspace,
+                                       int64_t workspace_bytes, int32_t *status, void *stream) {
+    const char *who = "attention_decode";
+    h3::AttentionDecode p{};
+    const h3enc_status s = take_cache(cache, who, &p.cache);
+    if (s != H3ENC_OK) return s;
+    const int64_t width = (int64_t)n_heads * cache->head_dim;
+    if (n_seqs < 0 || n_seqs > h3::kMaxSeqs || n_heads < 1 || n_heads > 65536 || n_heads % cache->n_kv_heads ||
+        max_len < 0 || ld_table < 0 || (int64_t)ld_table * cache->page_size < max_len)
+        return fail(nullptr, H3ENC_ERR_INVALID_ARG, "%s: bad sizes, or the page table does not hold max_len", who);
+    if (n_seqs == 0) return H3ENC_OK;
+    if (!q || !o || !aligned16(q) || !aligned16(o) || ld_q < width || ld_o < width || ld_q % 8 || ld_o % 8 ||
+        (!page_table && max_len > 0) || !seq_lens)
+        return fail(nullptr, H3ENC_ERR_INVALID_ARG, "%s: NULL or misaligned operand, or a bad leading dimension", who);
+    if (rows_overlap(q, ld_q, width, o, ld_o, width, n_seqs, 2))
+        return fail(nullptr, H3ENC_ERR_INVALID_ARG, "%s: o overlaps q", who);
+    if ((weight_in && !weight_out) || (weight_out && ld_weight < max_len) ||
+        (weight_in && weight_in != weight_out &&
+         rows_overlap(weight_in, ld_weight, max_len, weight_out, ld_weight, max_len, n_seqs, 4)))
+        return fail(nullptr, H3ENC_ERR_INVALID_ARG, "%s: weight_in without weight_out or overlapping it, or ld_weight "
+                                                    "below max_len", who);
+    const int sms = h3::device_num_sms();
+    if (sms <= 0) return fail(nullptr, H3ENC_ERR_CUDA, "%s: no CUDA device", who);
+    const size_t need = h3::attention_decode_workspace_bytes(sms, n_seqs, n_heads, max_len, weight_out != nullptr);
+    if (!need) return fail(nullptr, H3ENC_ERR_UNSUPPORTED, "%s: sizes beyond 2^31 key tiles", who);
+    if (!workspace || workspace_bytes < 0 || (size_t)workspace_bytes < need ||
+        (reinterpret_cast<uintptr_t>(workspace) & 255))
+        return fail(nullptr, H3ENC_ERR_INVALID_ARG, "%s: workspace smaller than "
+                                                    "h3enc_op_attention_decode_workspace_bytes() or not 256-byte "
+                                                    "aligned", who);
+    p.q = static_cast<const bf16 *>(q); p.ld_q = ld_q;
+    p.o = static_cast<bf16 *>(o); p.ld_o = ld_o;
+    p.table = page_table; p.ld_table = ld_table;
+    p.seq_lens = seq_lens; p.n_seqs = n_seqs; p.nq = n_heads; p.max_len = max_len;
+    p.weight_in = weight_in; p.weight_out = weight_out; p.ld_weight = ld_weight;
+    p.workspace = workspace; p.status = status;
+    cudaError_t e = h3::launch_attention_decode(p, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? H3ENC_OK : cuda_fail(nullptr, e, "attention_decode launch");
+}
+
+h3enc_status h3enc_op_cache_evict(const h3enc_kv_cache *cache, const int32_t *page_table, int32_t ld_table,
+                                  const int32_t *page_table_out, int32_t ld_table_out, const int32_t *seq_lens,
+                                  int32_t n_seqs, int32_t max_len, int32_t budget, int32_t sink, int32_t recent,
+                                  const float *weight, int64_t ld_weight, float *weight_out, int64_t ld_weight_out,
+                                  int32_t *kept, int64_t ld_kept, int32_t *new_lens, int32_t *status, void *stream) {
+    const char *who = "cache_evict";
+    h3::CacheEvict p{};
+    const h3enc_status s = take_cache(cache, who, &p.cache);
+    if (s != H3ENC_OK) return s;
+    if (n_seqs < 0 || n_seqs > h3::kMaxSeqs || max_len < 0 || budget < 1 || sink < 0 || recent < 0 ||
+        (int64_t)sink + recent > budget)
+        return fail(nullptr, H3ENC_ERR_INVALID_ARG, "%s: bad sizes, or sink + recent above the budget", who);
+    const int64_t most = budget < max_len ? budget : max_len;
+    if (ld_table < 0 || (int64_t)ld_table * cache->page_size < max_len ||
+        (page_table_out && (ld_table_out < 0 || (int64_t)ld_table_out * cache->page_size < most)))
+        return fail(nullptr, H3ENC_ERR_INVALID_ARG, "%s: a page table does not hold the lengths", who);
+    if (n_seqs == 0) return H3ENC_OK;
+    if ((!page_table && max_len > 0) || !seq_lens || !weight || !weight_out || !kept || !new_lens ||
+        ld_weight < max_len || ld_weight_out < max_len || ld_kept < budget ||
+        rows_overlap(weight, ld_weight, max_len, weight_out, ld_weight_out, max_len, n_seqs, 4))
+        return fail(nullptr, H3ENC_ERR_INVALID_ARG, "%s: NULL operand, a bad leading dimension, or weight_out "
+                                                    "overlaps weight", who);
+    p.table = page_table; p.ld_table = ld_table;
+    p.table_out = page_table_out; p.ld_table_out = ld_table_out;
+    p.seq_lens = seq_lens; p.n_seqs = n_seqs; p.max_len = max_len;
+    p.budget = budget; p.sink = sink; p.recent = recent;
+    p.weight = weight; p.ld_weight = ld_weight; p.weight_out = weight_out; p.ld_weight_out = ld_weight_out;
+    p.kept = kept; p.ld_kept = ld_kept; p.new_lens = new_lens; p.status = status;
+    cudaError_t e = h3::launch_cache_evict(p, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? H3ENC_OK : cuda_fail(nullptr, e, "cache_evict launch");
+}
+
+}  // extern "C"

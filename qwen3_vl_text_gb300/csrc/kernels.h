@@ -162,6 +162,69 @@ cudaError_t pack_gate_up_rows(const bf16 *src, bf16 *W, int I, int K, int which,
 cudaError_t launch_merge_visual_rows(const int32_t *vis_rank, const bf16 *src, int n_vis, int hidden, bf16 *out,
                                      int S, cudaStream_t st);
 
+// ---- paged key/value cache (kv_cache.cu) and the attention of one new token over it
+// (attention_decode.cu).  Element e of kv head g of place s of page p lies at
+// p * page_stride + (g * page_size + s) * d + e; page_size = 1 << page_shift.
+struct KvCache {
+    void *k, *v;
+    const float *k_scale, *v_scale;   // [nkv], e4m3 only
+    long long page_stride;
+    int num_pages, page_shift, nkv, d;
+    bool f8;
+};
+struct QkNormRope {
+    const bf16 *qkv;
+    long long ld_qkv;
+    int T, nq, nkv, d;
+    const bf16 *wq, *wk;        // NULL: no norm
+    float eps;
+    const float *cos_t, *sin_t; // NULL: no rotation
+    int cs_rows;                // 0: [T, d/2], else the row-interleaved tables of that stride
+    bf16 *q_out, *k_out;        // NULL: not written
+    long long ld_q, ld_k;
+    bool has_cache;
+    KvCache cache;
+    const int32_t *slots;
+    int32_t *status;
+};
+cudaError_t launch_qk_norm_rope(const QkNormRope &p, cudaStream_t st);
+
+struct CacheEvict {
+    KvCache cache;
+    const int32_t *table, *table_out;   // table_out NULL: in place
+    int ld_table, ld_table_out;
+    const int32_t *seq_lens;
+    int n_seqs, max_len, budget, sink, recent;
+    const float *weight;
+    long long ld_weight;
+    float *weight_out;
+    long long ld_weight_out;
+    int32_t *kept;
+    long long ld_kept;
+    int32_t *new_lens;
+    int32_t *status;
+};
+cudaError_t launch_cache_evict(const CacheEvict &p, cudaStream_t st);
+
+struct AttentionDecode {
+    const bf16 *q;
+    bf16 *o;
+    long long ld_q, ld_o;
+    KvCache cache;
+    const int32_t *table;
+    int ld_table;
+    const int32_t *seq_lens;
+    int n_seqs, nq, max_len;
+    const float *weight_in;
+    float *weight_out;
+    long long ld_weight;
+    void *workspace;
+    int32_t *status;
+};
+// 0 for sizes the call refuses.
+size_t attention_decode_workspace_bytes(int num_sms, int n_seqs, int nq, int max_len, bool weights);
+cudaError_t launch_attention_decode(const AttentionDecode &p, cudaStream_t st);
+
 int device_num_sms();
 
 // Launch configuration with programmatic stream serialization (see pdl_wait in
