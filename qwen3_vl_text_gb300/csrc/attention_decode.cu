@@ -1,10 +1,28 @@
 // Attention of one new token of each sequence over a paged key/value cache.
 //
-// For q head h of kv group g: s_i = q . k_i / sqrt(d), o = sum_i softmax(s)_i v_i over the i < len
-// tokens of the sequence, in one pass over the keys with the running maximum m and sum l of the
-// softmax (scores in log2 units: p = 2^(s log2e - m)).
-#include <cuda_fp8.h>
-
+// For q head h of kv head g: s_i = q . k_i / sqrt(d), o = sum_i softmax(s)_i v_i over the len cached
+// tokens, in one pass over the keys with the running maximum m and sum l of the softmax (scores in
+// log2 units: p = 2^(s log2e - m)).
+//
+// What bounds it: every cached byte is read once, and the q heads of a kv head (nq/nkv of them) do
+// 2 flops each per byte pair: 8 flops a byte with 8 heads over bf16, far below the tensor cores'
+// rate, so the bound is the memory's.  Hence:
+//  * The keys of all (sequence, kv head) segments are laid end to end in tiles of 64 and cut into one
+//    equal run of tiles per CTA, one CTA per SM, whatever the lengths are: a run may end inside a
+//    segment, whose parts are then joined (below).  Lengths are read on the device.
+//  * A producer warp keeps up to STAGES tiles of K and V in flight through TMA (a box per page,
+//    one lane per box, page numbers fetched four tiles ahead); eight warps compute.
+//  * The products run on mma.sync m16n8k16 with the q heads as the 16 rows: there are at most 16 rows
+//    of work per key, which a 128-row tcgen05 tile would leave mostly empty, and a warp that
+//    holds scores, weights and output in its own registers needs no exchange with other warps per tile.
+//    Each warp takes 16 keys of a tile with its own m, l and output; warps 0-3 take the even tiles of
+//    the run and 4-7 the odd ones, so that one half's softmax overlaps the other's loads.
+//  * With at most 8 heads the rows 8-15 of the weight matrix P would be padding: they carry
+//    P's rounding remainder p - bf16(p) instead, so the value product loses nothing to the 8-bit mantissa
+//    at no cost (more than 8 heads: a second product).  e4m3 values are exact in f16, so that path
+//    runs in f16, with q scaled by a power of two per head into f16's range.
+#include <algorithm>
+#include <atomic>
 #include <climits>
 
 #include "common.cuh"
@@ -14,71 +32,615 @@ namespace h3 {
 
 namespace {
 
-constexpr int AD_WARPS = 8;
+constexpr int TK = 64;                  // keys per tile
+constexpr int CWARPS = 8;               // compute warps
+constexpr int AD_THREADS = (CWARPS + 1) * 32;
+constexpr int MAX_CTAS = 1024;          // arrival counters at the head of the workspace
+constexpr int PART_ROWS = 16;           // heads of a segment
+constexpr int AHEAD = 4;                // tiles whose page numbers are fetched ahead
 
-__device__ __forceinline__ float load_elem(const void *base, long long at, bool f8) {
-    if (f8) {
-        __nv_fp8_e4m3 x;
-        x.__x = static_cast<const uint8_t *>(base)[at];
-        return (float)x;
+template <int D, bool F8>
+struct Shape {
+    static constexpr int ROW = D * (F8 ? 1 : 2);            // bytes of a key
+    static constexpr int BOX = ROW < 128 ? 64 : 128;        // bytes of a box row (= swizzle width)
+    static constexpr int TILE = TK * ROW;                   // K or V of one tile
+    // even: a stage then always serves the same half of the warps, which sees each of its phases
+    static constexpr int STAGES = TILE >= 16384 ? 4 : (TILE >= 8192 ? 8 : 12);
+    static_assert(STAGES % 2 == 0, "stages alternate between the halves of the compute warps");
+    static constexpr int LDO = D + 8;                       // padded row of the output exchange
+    static constexpr int OFF_O = STAGES * 2 * TILE;
+    static constexpr int OFF_ML = OFF_O + CWARPS * 8 * LDO * 4;
+    static constexpr int OFF_PRE = OFF_ML + 2 * CWARPS * PART_ROWS * 4;
+    static constexpr int OFF_BAR = (OFF_PRE + (kMaxSeqs + 1) * 4 + 15) & ~15;
+    static constexpr int BYTES = OFF_BAR + 2 * STAGES * 8 + 64 + 1024;   // + alignment of the base
+};
+
+struct Args {
+    AttentionDecode p;
+    int group;      // q heads per kv head
+    int chunks;     // segments per kv head: ceil(group / 16)
+    int box_rows;   // places of a page one box covers
+    float *part;    // [cta][2][16][D] partial outputs, unnormalised
+    float2 *ml;     // [cta][2][16] their running maximum and sum
+    uint32_t *count;
+    float2 *stat;   // [n_seqs][nq] (m, 1/l), with weights
+    float *scores;  // [n_seqs][nq][ld_scores] scores in log2 units, with weights
+    long long ld_scores;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t a) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(a)
+                 : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t a) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(a)
+                 : "memory");
+}
+// C (16 x 8) += A (16 x 16) B (16 x 8), fp32 accumulation; bf16, or f16 operands with F8.
+template <bool F8>
+__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1) {
+    if constexpr (F8)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+                     "{%0,%1,%2,%3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+                     "{%0,%1,%2,%3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// Two e4m3 bytes -> two f16 (exact).
+__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t two) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)two));
+    return r;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ float2 unpack_f16x2(uint32_t v) {
+    float2 r;
+    asm("{.reg .f16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;}"
+        : "=f"(r.x), "=f"(r.y)
+        : "r"(v));
+    return r;
+}
+// p rounded to the operand type, and what the rounding left, rounded too.
+template <bool F8>
+__device__ __forceinline__ void split2(float a, float b, uint32_t &hi, uint32_t &lo) {
+    if constexpr (F8) {
+        hi = pack_f16x2(a, b);
+        const float2 r = unpack_f16x2(hi);
+        lo = pack_f16x2(a - r.x, b - r.y);
+    } else {
+        hi = pack_bf16x2(a, b);
+        lo = pack_bf16x2(a - bf16_lo(hi), b - bf16_hi(hi));
     }
-    return __bfloat162float(static_cast<const bf16 *>(base)[at]);
+}
+__device__ __forceinline__ void compute_sync() { asm volatile("bar.sync 1, %0;" ::"n"(CWARPS * 32) : "memory"); }
+
+// Byte offset of 16-byte chunk c of row r in a tile of swizzled box rows.
+template <int D, bool F8>
+__device__ __forceinline__ uint32_t chunk_at(int r, int c) {
+    using S = Shape<D, F8>;
+    if constexpr (S::BOX == 128) return (c >> 3) * (TK * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+    else return r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
 }
 
-// One CTA per (q head, sequence); its warps take the keys in turn, D / 32 elements per lane.
-template <int D>
-__global__ void __launch_bounds__(AD_WARPS * 32) attention_decode_kernel(const AttentionDecode p, float *scores,
-                                                                          float2 *stat, long long ld_scores) {
+// Walks the tiles of a run: segment (b, u) with u = kv head * chunks + chunk, tile j of it.
+struct Walk {
+    int b, u, j, len, tiles;
+    __device__ __forceinline__ void start(int t, const int *pre, const int32_t *lens, int n_seqs, int max_len) {
+        int lo = 0, hi = n_seqs;   // the last b with pre[b] <= t that has tiles
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (pre[mid] <= t) lo = mid;
+            else hi = mid;
+        }
+        b = lo;
+        load(lens, max_len);
+        const int off = t - pre[b];
+        u = off / tiles;
+        j = off - u * tiles;
+    }
+    __device__ __forceinline__ void load(const int32_t *lens, int max_len) {
+        len = min(max(lens[b], 0), max_len);
+        tiles = (len + TK - 1) / TK;
+    }
+    // next segment (its tile 0); the caller knows that one follows
+    __device__ __forceinline__ void next(int units, const int32_t *lens, int max_len) {
+        j = 0;
+        if (++u < units) return;
+        u = 0;
+        do {
+            ++b;
+            load(lens, max_len);
+        } while (tiles == 0);
+    }
+};
+
+template <int D, bool F8, bool WIDE>   // WIDE: more than 8 heads in a segment
+__global__ void __launch_bounds__(AD_THREADS, 1) attention_decode_kernel(const __grid_constant__ CUtensorMap tmK,
+                                                                          const __grid_constant__ CUtensorMap tmV,
+                                                                          const Args a) {
+    using S = Shape<D, F8>;
+    constexpr int STAGES = S::STAGES;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+    float *sm_o = reinterpret_cast<float *>(smem + S::OFF_O);
+    float *sm_m = reinterpret_cast<float *>(smem + S::OFF_ML), *sm_l = sm_m + CWARPS * PART_ROWS;
+    int *pre = reinterpret_cast<int *>(smem + S::OFF_PRE);
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + S::OFF_BAR), *empty = full + STAGES;
+    volatile int *abort = reinterpret_cast<volatile int *>(empty + STAGES);
+    int *s_last = const_cast<int *>(abort) + 1;
+    int *s_warp = s_last + 1;   // [9] scan of the warps' sums
+
+    const AttentionDecode &p = a.p;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int units = p.cache.nkv * a.chunks;
+
     pdl_trigger();
+    if (tid == 0) {
+        prefetch_tmap(&tmK);
+        prefetch_tmap(&tmV);
+        for (int i = 0; i < STAGES; ++i) {
+            mbar_init(full + i, 1);
+            mbar_init(empty + i, CWARPS / 2);
+        }
+        *abort = 0;
+        fence_barrier_init();
+    }
     pdl_wait();
-    constexpr int E = D / 32;
-    __shared__ float sm_o[AD_WARPS][D], sm_m[AD_WARPS], sm_l[AD_WARPS];
-    const int h = blockIdx.x, b = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int g = h / (p.nq / p.cache.nkv);
-    int len = p.seq_lens[b];
-    if (len < 0 || len > p.max_len) {
-        if (threadIdx.x == 0) report(p.status, ST_BOUNDS);
-        len = len < 0 ? 0 : p.max_len;
+
+    // pre[b] = tiles of the sequences before b: four sequences per thread, scanned over the block
+    {
+        int n[4], sum = 0;
+        #pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int b = 4 * tid + i;
+            n[i] = 0;
+            if (b < p.n_seqs) {
+                const int len = p.seq_lens[b], c = min(max(len, 0), p.max_len);
+                if (len != c && blockIdx.x == 0) report(p.status, ST_BOUNDS);
+                n[i] = (c + TK - 1) / TK * units;
+            }
+            sum += n[i];
+        }
+        int inc = sum;
+        #pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += v;
+        }
+        if (lane == 31) s_warp[warp] = inc;
+        __syncthreads();
+        int at = inc - sum;
+        for (int w = 0; w < warp; ++w) at += s_warp[w];
+        #pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int b = 4 * tid + i;
+            if (b <= p.n_seqs) pre[b] = at;
+            at += n[i];
+        }
+        __syncthreads();
     }
-    const float ks = p.cache.f8 ? p.cache.k_scale[g] : 1.f, vs = p.cache.f8 ? p.cache.v_scale[g] : 1.f;
-    const float scale = 1.4426950408889634f / sqrtf((float)D) * ks;
-    float q[E], o[E], m = -INFINITY, l = 0.f;
-    for (int e = 0; e < E; ++e) {
-        q[e] = __bfloat162float(p.q[b * p.ld_q + h * D + lane + 32 * e]);
-        o[e] = 0.f;
+    const long long T = pre[p.n_seqs];
+    const long long G = T < (long long)gridDim.x ? T : (long long)gridDim.x;   // CTAs that have a run
+
+    // sequences without tokens: zero rows
+    for (int b = blockIdx.x; b < p.n_seqs; b += gridDim.x)
+        if (pre[b + 1] == pre[b])
+            for (int i = tid; i < p.nq * D / 8; i += AD_THREADS)
+                *reinterpret_cast<uint4 *>(p.o + b * p.ld_o + 8 * i) = make_uint4(0, 0, 0, 0);
+    if ((long long)blockIdx.x >= G) return;
+    const int t0 = (int)(blockIdx.x * T / G), t1 = (int)((blockIdx.x + 1) * T / G);
+
+    Walk w;
+    w.start(t0, pre, p.seq_lens, p.n_seqs, p.max_len);
+
+    if (warp == CWARPS) {
+        // ------------------------------------------------ producer
+        const int boxes = TK / a.box_rows;
+        const int page_mask = (1 << p.cache.page_shift) - 1;
+        int nb[AHEAD], nu[AHEAD], ny[AHEAD], nn[AHEAD];   // page (-1: no box), unit, place, boxes of the tile
+        const auto fetch = [&](int i) {
+            const int key = w.j * TK + lane * a.box_rows;
+            nb[i] = -1;
+            nu[i] = w.u / a.chunks;
+            ny[i] = key & page_mask;
+            nn[i] = min(boxes, (w.len - w.j * TK + a.box_rows - 1) / a.box_rows);
+            if (lane < nn[i]) nb[i] = p.table[(long long)w.b * p.ld_table + (key >> p.cache.page_shift)];
+        };
+        int ahead = t0;
+        const auto advance = [&]() {
+            if (++ahead < t1 && ++w.j == w.tiles) w.next(units, p.seq_lens, p.max_len);
+        };
+        #pragma unroll
+        for (int i = 0; i < AHEAD; ++i)
+            if (ahead < t1) {
+                fetch(i);
+                advance();
+            }
+        int stage = 0, round = 0;
+        bool ok = true;
+        for (int t = t0; t < t1 && ok; t += AHEAD) {
+            #pragma unroll
+            for (int i = 0; i < AHEAD; ++i) {
+                if (t + i >= t1 || !ok) break;
+                if (round > 0) ok = mbar_wait(empty + stage, (round - 1) & 1, abort);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                uint8_t *k = smem + stage * 2 * S::TILE, *v = k + S::TILE;
+                if (lane == 0) mbar_arrive_expect_tx(full + stage, nn[i] * a.box_rows * S::ROW * 2);
+                __syncwarp();
+                if (lane < nn[i]) {
+                    int page = nb[i];
+                    if (page < 0 || page >= p.cache.num_pages) {
+                        report(p.status, ST_BOUNDS);
+                        page = p.cache.num_pages;   // outside the map: the box is filled with zeros
+                    }
+                    #pragma unroll
+                    for (int x = 0; x < S::ROW / S::BOX; ++x) {
+                        const int off = x * (TK * S::BOX) + lane * a.box_rows * S::BOX;
+                        const int col = x * (S::BOX / (F8 ? 1 : 2));
+                        tma_load_4d(k + off, &tmK, full + stage, col, ny[i], nu[i], page);
+                        tma_load_4d(v + off, &tmV, full + stage, col, ny[i], nu[i], page);
+                    }
+                }
+                if (ahead < t1) {
+                    fetch(i);
+                    advance();
+                }
+                if (++stage == STAGES) stage = 0, ++round;
+            }
+        }
+        if (!ok) {
+            // a wait ran out: leave once the copies in flight have landed (each of these waits is limited too)
+            if (lane == 0) {
+                report(p.status, ST_TIMEOUT);
+                *abort = 1;
+                const int never = 0;
+                const int issued = round * STAGES + stage;
+                for (int f = max(0, issued - STAGES); f < issued; ++f)
+                    mbar_wait(full + f % STAGES, (f / STAGES) & 1, &never);
+            }
+            __syncwarp();
+        }
+        return;
     }
-    const int mask = (1 << p.cache.page_shift) - 1;
-    for (int i = warp; i < len; i += AD_WARPS) {
-        const int page = p.table[(long long)b * p.ld_table + (i >> p.cache.page_shift)];
-        const bool ok = page >= 0 && page < p.cache.num_pages;
-        if (!ok && lane == 0) report(p.status, ST_BOUNDS);
-        const long long at =
-            page * p.cache.page_stride + (long long)((g << p.cache.page_shift) + (i & mask)) * D + lane;
-        float s = 0.f;
-        if (ok)
-            for (int e = 0; e < E; ++e) s = fmaf(q[e], load_elem(p.cache.k, at + 32 * e, p.cache.f8), s);
-        for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-        s *= scale;
-        if (scores && lane == 0) scores[((long long)b * p.nq + h) * ld_scores + i] = s;
-        const float mn = fmaxf(m, s), c = exp2f(m - mn), pr = exp2f(s - mn);
-        m = mn;
-        l = l * c + pr;
-        for (int e = 0; e < E; ++e)
-            o[e] = o[e] * c + (ok ? pr * load_elem(p.cache.v, at + 32 * e, p.cache.f8) : 0.f);
+
+    // ---------------------------------------------------- compute warps
+    const int g = lane >> 2, tq = lane & 3;   // fragment row and column pair
+    const float base_scale = 1.4426950408889634f / sqrtf((float)D);
+    const int half = warp >> 2, slice = (warp & 3) * 16;
+    // this lane's row and 16-byte chunk in the ldmatrix of 16 keys: K (keys 0-7 / 8-15 as the column
+    // tiles) and V (transposed, as the two halves of the contraction); e4m3 rows pair them the other way
+    const int row_v = (lane & 7) + ((lane >> 3) & 1) * 8, chunk_v = lane >> 4;
+    const int row_k = F8 ? row_v : (lane & 7) + (lane >> 4) * 8, chunk_k = F8 ? chunk_v : (lane >> 3) & 1;
+    int stage = 0, round = 0, parity = 0;
+
+    for (int t = t0; t < t1;) {
+        const int seg = t - w.j, seg_end = seg + w.tiles;   // this segment's tiles in the whole row of tiles
+        const int j1 = min(w.tiles, t1 - seg);              // this run's part of it: [w.j, j1)
+        const int kvh = w.u / a.chunks, h0 = kvh * a.group + (w.u % a.chunks) * PART_ROWS;
+        const int rows = min(PART_ROWS, a.group - (w.u % a.chunks) * PART_ROWS);   // heads of the segment
+
+        // q as the A operand: rows = heads, the contraction over d in steps of 16
+        uint32_t qa[D / 16][WIDE ? 4 : 2];
+        float scale0 = base_scale, scale1 = base_scale;
+        {
+            const bf16 *q0 = p.q + w.b * p.ld_q + (long long)(h0 + g) * D, *q1 = q0 + 8 * D;
+            const bool in0 = g < rows, in1 = WIDE && g + 8 < rows;
+            #pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+                // bf16: columns 2t, 2t+1 and 2t+8, 2t+9 of the step; e4m3: 4t .. 4t+3 (the bytes a
+                // lane holds of a key), the same order on both sides of the product
+                const int c0 = 16 * k + (F8 ? 4 * tq : 2 * tq), c1 = c0 + (F8 ? 2 : 8);
+                qa[k][0] = in0 ? *reinterpret_cast<const uint32_t *>(q0 + c0) : 0u;
+                qa[k][1] = in0 ? *reinterpret_cast<const uint32_t *>(q0 + c1) : 0u;
+                if constexpr (WIDE) {
+                    qa[k][2] = in1 ? *reinterpret_cast<const uint32_t *>(q1 + c0) : 0u;
+                    qa[k][3] = in1 ? *reinterpret_cast<const uint32_t *>(q1 + c1) : 0u;
+                }
+            }
+            if constexpr (F8) {
+                const float ks = p.cache.k_scale[kvh];
+                #pragma unroll
+                for (int r = 0; r < (WIDE ? 2 : 1); ++r) {
+                    float top = 0.f;
+                    #pragma unroll
+                    for (int k = 0; k < D / 16; ++k)
+                        #pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            top = fmaxf(top, fmaxf(fabsf(bf16_lo(qa[k][2 * r + i])), fabsf(bf16_hi(qa[k][2 * r + i]))));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                    // the largest |q| goes to [2^14, 2^15): exact but for elements 2^-29 of it and smaller
+                    const int e = max((int)(__float_as_uint(top) >> 23) - 127, -100);
+                    const float up = __uint_as_float((uint32_t)(14 - e + 127) << 23);
+                    const float down = __uint_as_float((uint32_t)(e - 14 + 127) << 23);
+                    #pragma unroll
+                    for (int k = 0; k < D / 16; ++k)
+                        #pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            uint32_t &x = qa[k][2 * r + i];
+                            x = pack_f16x2(bf16_lo(x) * up, bf16_hi(x) * up);
+                        }
+                    (r ? scale1 : scale0) = base_scale * ks * down;
+                }
+            }
+        }
+
+        float o[D / 8][4];
+        #pragma unroll
+        for (int i = 0; i < D / 8; ++i)
+            #pragma unroll
+            for (int k = 0; k < 4; ++k) o[i][k] = 0.f;
+        float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+
+        for (; w.j < j1; ++w.j, ++t, parity ^= 1) {
+            if (parity == half) {
+                if (!mbar_wait(full + stage, round & 1, abort)) {
+                    // give up on the data, keep the control flow (barriers, counters) to the end
+                    if (lane == 0) {
+                        report(p.status, ST_TIMEOUT);
+                        *abort = 1;
+                    }
+                    __syncwarp();
+                }
+                const int key0 = w.j * TK + slice;
+                if (key0 < w.len) {
+                    const uint32_t kt = smem_u32(smem + stage * 2 * S::TILE), vt = kt + S::TILE;
+                    float s[2][4] = {};
+                    if constexpr (F8) {
+                        #pragma unroll
+                        for (int k = 0; k < D / 16; k += 2) {
+                            uint32_t r[4];   // (keys 0-7, 8-15) x (step k, k + 1)
+                            ldsm4(r, kt + chunk_at<D, F8>(slice + row_k, k + chunk_k));
+                            #pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                mma<F8>(s[i & 1], qa[k + i / 2][0], WIDE ? qa[k + i / 2][WIDE ? 2 : 0] : 0u, qa[k + i / 2][1],
+                                        WIDE ? qa[k + i / 2][WIDE ? 3 : 0] : 0u, e4m3x2_f16x2(r[i]),
+                                        e4m3x2_f16x2(r[i] >> 16));
+                        }
+                    } else {
+                        #pragma unroll
+                        for (int k = 0; k < D / 16; ++k) {
+                            uint32_t r[4];
+                            ldsm4(r, kt + chunk_at<D, F8>(slice + row_k, 2 * k + chunk_k));
+                            #pragma unroll
+                            for (int i = 0; i < 2; ++i)
+                                mma<F8>(s[i], qa[k][0], WIDE ? qa[k][WIDE ? 2 : 0] : 0u, qa[k][1],
+                                        WIDE ? qa[k][WIDE ? 3 : 0] : 0u, r[2 * i], r[2 * i + 1]);
+                        }
+                    }
+                    const bool tail = key0 + 16 > w.len;
+                    float x0 = -INFINITY, x1 = -INFINITY;
+                    #pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        #pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            s[i][k] *= scale0;
+                            if (WIDE) s[i][2 + k] *= scale1;
+                            if (tail && key0 + 8 * i + 2 * tq + k >= w.len) s[i][k] = s[i][2 + k] = -INFINITY;
+                            x0 = fmaxf(x0, s[i][k]);
+                            if (WIDE) x1 = fmaxf(x1, s[i][2 + k]);
+                        }
+                    if (a.scores) {
+                        #pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            float *dst = a.scores + ((long long)w.b * p.nq + h0 + g) * a.ld_scores + key0 + 8 * i + 2 * tq;
+                            if (g < rows) *reinterpret_cast<float2 *>(dst) = make_float2(s[i][0], s[i][1]);
+                            if (WIDE && g + 8 < rows)
+                                *reinterpret_cast<float2 *>(dst + 8 * a.ld_scores) = make_float2(s[i][2], s[i][3]);
+                        }
+                    }
+                    x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 1));
+                    x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 2));
+                    if (WIDE) {
+                        x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 1));
+                        x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 2));
+                    }
+                    // a larger maximum: rescale what has been summed (the first slice scales zeros)
+                    if (__any_sync(0xffffffffu, x0 > m0 || (WIDE && x1 > m1))) {
+                        const float n0 = fmaxf(m0, x0), c0 = n0 == -INFINITY ? 1.f : ex2(m0 - n0);
+                        float c1 = c0;
+                        m0 = n0;
+                        l0 *= c0;
+                        if (WIDE) {
+                            const float n1 = fmaxf(m1, x1);
+                            c1 = n1 == -INFINITY ? 1.f : ex2(m1 - n1);
+                            m1 = n1;
+                            l1 *= c1;
+                        }
+                        #pragma unroll
+                        for (int i = 0; i < D / 8; ++i) {
+                            o[i][0] *= c0;
+                            o[i][1] *= c0;
+                            o[i][2] *= c1;
+                            o[i][3] *= c1;
+                        }
+                    }
+                    const float z0 = m0 == -INFINITY ? 0.f : m0, z1 = m1 == -INFINITY ? 0.f : m1;
+                    #pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        #pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            s[i][k] = ex2(s[i][k] - z0);
+                            l0 += s[i][k];
+                            if (WIDE) {
+                                s[i][2 + k] = ex2(s[i][2 + k] - z1);
+                                l1 += s[i][2 + k];
+                            }
+                        }
+                    uint32_t hi[4], lo[4];   // the A operand's four registers
+                    split2<F8>(s[0][0], s[0][1], hi[0], lo[0]);
+                    split2<F8>(s[1][0], s[1][1], hi[2], lo[2]);
+                    if (WIDE) {
+                        split2<F8>(s[0][2], s[0][3], hi[1], lo[1]);
+                        split2<F8>(s[1][2], s[1][3], hi[3], lo[3]);
+                    } else {
+                        hi[1] = lo[0];
+                        hi[3] = lo[2];
+                    }
+                    // values behind the sequence may be anything (0 * NaN): cleared in the last slice
+                    uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
+                    if (tail) {
+                        const int left = w.len - key0 - 2 * tq;
+                        keep0 = (left > 0 ? 0xffffu : 0u) | (left > 1 ? 0xffff0000u : 0u);
+                        keep1 = (left > 8 ? 0xffffu : 0u) | (left > 9 ? 0xffff0000u : 0u);
+                    }
+                    #pragma unroll
+                    for (int c = 0; c < S::ROW / 16; c += 2) {
+                        uint32_t r[4];   // (keys 0-7, 8-15) x (chunk c, c + 1)
+                        ldsm4t(r, vt + chunk_at<D, F8>(slice + row_v, c + chunk_v));
+                        if (tail) {
+                            r[0] &= keep0;
+                            r[1] &= keep1;
+                            r[2] &= keep0;
+                            r[3] &= keep1;
+                        }
+                        #pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            if constexpr (F8) {
+                                // a lane holds columns 2n, 2n + 1 of two keys: even and odd columns as two tiles
+                                #pragma unroll
+                                for (int odd = 0; odd < 2; ++odd) {
+                                    const uint32_t sel = odd ? 0x31u : 0x20u;
+                                    const uint32_t b0 = e4m3x2_f16x2(__byte_perm(r[2 * i], 0u, sel));
+                                    const uint32_t b1 = e4m3x2_f16x2(__byte_perm(r[2 * i + 1], 0u, sel));
+                                    mma<F8>(o[2 * (c + i) + odd], hi[0], hi[1], hi[2], hi[3], b0, b1);
+                                    if (WIDE) mma<F8>(o[2 * (c + i) + odd], lo[0], lo[1], lo[2], lo[3], b0, b1);
+                                }
+                            } else {
+                                mma<F8>(o[c + i], hi[0], hi[1], hi[2], hi[3], r[2 * i], r[2 * i + 1]);
+                                if (WIDE) mma<F8>(o[c + i], lo[0], lo[1], lo[2], lo[3], r[2 * i], r[2 * i + 1]);
+                            }
+                        }
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(empty + stage);
+            }
+            if (++stage == STAGES) stage = 0, ++round;
+        }
+
+        // ------------------------------------------------ join the warps' parts
+        l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
+        l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
+        if (WIDE) {
+            l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
+            l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+        }
+        if (tq == 0) {
+            sm_m[warp * PART_ROWS + g] = m0;
+            sm_l[warp * PART_ROWS + g] = l0;
+            sm_m[warp * PART_ROWS + g + 8] = m1;
+            sm_l[warp * PART_ROWS + g + 8] = l1;
+        }
+        compute_sync();
+        const bool whole = seg >= t0 && seg_end <= t1;
+        const float vs = F8 ? p.cache.v_scale[kvh] : 1.f;
+        const int slot = 2 * blockIdx.x + (seg < t0 ? 0 : 1);
+        const int trow = tid / (D / 4), tcol = tid % (D / 4) * 4;   // this thread's output in the sums below
+        #pragma unroll
+        for (int r8 = 0; r8 < (WIDE ? 16 : 8); r8 += 8) {
+            float top = -INFINITY;
+            #pragma unroll
+            for (int i = 0; i < CWARPS; ++i) top = fmaxf(top, sm_m[i * PART_ROWS + r8 + g]);
+            const float mine = r8 ? m1 : m0, f = mine == -INFINITY ? 0.f : ex2(mine - top);
+            float *dst = sm_o + (warp * 8 + g) * S::LDO;
+            #pragma unroll
+            for (int i = 0; i < D / 8; ++i) {
+                const float a0 = WIDE ? o[i][r8 / 4] : o[i][0] + o[i][2], a1 = WIDE ? o[i][r8 / 4 + 1] : o[i][1] + o[i][3];
+                const int c0 = F8 ? 16 * (i / 2) + 4 * tq + (i & 1) : 8 * i + 2 * tq;
+                dst[c0] = a0 * f;
+                dst[c0 + (F8 ? 2 : 1)] = a1 * f;
+            }
+            compute_sync();
+            if (trow < 8 && r8 + trow < rows) {
+                float mm = -INFINITY, ll = 0.f;
+                #pragma unroll
+                for (int i = 0; i < CWARPS; ++i) mm = fmaxf(mm, sm_m[i * PART_ROWS + r8 + trow]);
+                float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+                #pragma unroll
+                for (int i = 0; i < CWARPS; ++i) {
+                    const float wm = sm_m[i * PART_ROWS + r8 + trow];
+                    ll += wm == -INFINITY ? 0.f : sm_l[i * PART_ROWS + r8 + trow] * ex2(wm - mm);
+                    const float4 x = *reinterpret_cast<const float4 *>(sm_o + (i * 8 + trow) * S::LDO + tcol);
+                    acc.x += x.x;
+                    acc.y += x.y;
+                    acc.z += x.z;
+                    acc.w += x.w;
+                }
+                if (whole) {
+                    const int h = h0 + r8 + trow;
+                    const float inv = 1.f / ll, f2 = inv * vs;
+                    *reinterpret_cast<uint2 *>(p.o + w.b * p.ld_o + (long long)h * D + tcol) =
+                        make_uint2(pack_bf16x2(acc.x * f2, acc.y * f2), pack_bf16x2(acc.z * f2, acc.w * f2));
+                    if (a.stat && tcol == 0) a.stat[(long long)w.b * p.nq + h] = make_float2(mm, inv);
+                } else {
+                    *reinterpret_cast<float4 *>(a.part + ((long long)slot * PART_ROWS + r8 + trow) * D + tcol) = acc;
+                    if (tcol == 0) a.ml[slot * PART_ROWS + r8 + trow] = make_float2(mm, ll);
+                }
+            }
+            compute_sync();
+        }
+        if (!whole) {
+            // the CTA whose part arrives last joins the parts, in the order of the keys
+            const int first = (int)((((long long)seg + 1) * G - 1) / T), last = (int)(((long long)seg_end * G - 1) / T);
+            __threadfence();
+            compute_sync();
+            if (tid == 0) {
+                const uint32_t before = atomicAdd(a.count + first, 1u);
+                *s_last = before == (uint32_t)(last - first);
+                if (*s_last) a.count[first] = 0u;   // for the next call
+            }
+            compute_sync();
+            if (*s_last) {
+                __threadfence();
+                #pragma unroll
+                for (int r8 = 0; r8 < (WIDE ? 16 : 8); r8 += 8)
+                    if (trow < 8 && r8 + trow < rows) {
+                        // part of CTA c: its slot 1 if the segment begins in its run, else 0
+                        const auto at = [&](int c) { return (2 * c + (c == first ? 1 : 0)) * PART_ROWS + r8 + trow; };
+                        float mm = -INFINITY, ll = 0.f;
+                        for (int c = first; c <= last; ++c) mm = fmaxf(mm, __ldcg(a.ml + at(c)).x);
+                        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+                        #pragma unroll 4
+                        for (int c = first; c <= last; ++c) {
+                            const float2 x = __ldcg(a.ml + at(c));
+                            const float4 y = __ldcg(reinterpret_cast<const float4 *>(a.part + (long long)at(c) * D + tcol));
+                            const float f = x.x == -INFINITY ? 0.f : ex2(x.x - mm);
+                            ll = fmaf(x.y, f, ll);
+                            acc.x = fmaf(y.x, f, acc.x);
+                            acc.y = fmaf(y.y, f, acc.y);
+                            acc.z = fmaf(y.z, f, acc.z);
+                            acc.w = fmaf(y.w, f, acc.w);
+                        }
+                        const int h = h0 + r8 + trow;
+                        const float inv = 1.f / ll, f2 = inv * vs;
+                        *reinterpret_cast<uint2 *>(p.o + w.b * p.ld_o + (long long)h * D + tcol) =
+                            make_uint2(pack_bf16x2(acc.x * f2, acc.y * f2), pack_bf16x2(acc.z * f2, acc.w * f2));
+                        if (a.stat && tcol == 0) a.stat[(long long)w.b * p.nq + h] = make_float2(mm, inv);
+                    }
+            }
+        }
+        if (t < t1) w.next(units, p.seq_lens, p.max_len);
     }
-    for (int e = 0; e < E; ++e) sm_o[warp][lane + 32 * e] = o[e];
-    if (lane == 0) sm_m[warp] = m, sm_l[warp] = l;
-    __syncthreads();
-    float mm = -INFINITY;
-    for (int w = 0; w < AD_WARPS; ++w) mm = fmaxf(mm, sm_m[w]);
-    float ll = 0.f;
-    for (int w = 0; w < AD_WARPS; ++w) ll += len ? sm_l[w] * exp2f(sm_m[w] - mm) : 0.f;
-    for (int e = threadIdx.x; e < D; e += blockDim.x) {
-        float acc = 0.f;
-        for (int w = 0; w < AD_WARPS; ++w) acc += len ? sm_o[w][e] * exp2f(sm_m[w] - mm) : 0.f;
-        p.o[b * p.ld_o + h * D + e] = __float2bfloat16_rn(len ? acc / ll * vs : 0.f);
-    }
-    if (stat && threadIdx.x == 0) stat[b * p.nq + h] = make_float2(mm, 1.f / ll);
 }
 
 // weight_out[b][i] = weight_in[b][i] + sum over the q heads, in order, of their p_i.
@@ -91,38 +653,96 @@ __global__ void __launch_bounds__(256) attention_weight_kernel(const AttentionDe
     if (i >= len) return;
     float acc = 0.f;
     for (int h = 0; h < p.nq; ++h) {
-        const float2 ml = stat[b * p.nq + h];
-        acc += exp2f(scores[((long long)b * p.nq + h) * ld_scores + i] - ml.x) * ml.y;
+        const float2 ml = stat[(long long)b * p.nq + h];
+        acc = fmaf(ex2(scores[((long long)b * p.nq + h) * ld_scores + i] - ml.x), ml.y, acc);
     }
     p.weight_out[b * p.ld_weight + i] = (p.weight_in ? p.weight_in[b * p.ld_weight + i] : 0.f) + acc;
 }
 
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 
+// Workspace: arrival counters, partial outputs, their (m, l), then with weights (m, 1/l) and scores.
+struct Layout {
+    size_t part, ml, stat, scores, bytes;
+    long long ld_scores;
+};
+Layout layout(int ctas, int n_seqs, int nq, int max_len, bool weights) {
+    Layout y;
+    y.part = MAX_CTAS * sizeof(uint32_t);
+    y.ml = y.part + (size_t)ctas * 2 * PART_ROWS * 128 * sizeof(float);
+    y.stat = y.ml + up256((size_t)ctas * 2 * PART_ROWS * sizeof(float2));
+    y.ld_scores = (max_len + TK - 1) / TK * TK;
+    y.scores = y.stat + (weights ? up256((size_t)n_seqs * nq * sizeof(float2)) : 0);
+    y.bytes = y.scores + (weights ? (size_t)n_seqs * nq * (size_t)y.ld_scores * sizeof(float) : 0);
+    return y;
+}
+
+template <int D, bool F8, bool WIDE>
+cudaError_t launch_kernel(const CUtensorMap &tk, const CUtensorMap &tv, const Args &a, int grid, cudaStream_t st) {
+    static std::atomic<bool> ready[kMaxDevices];   // the shared-memory opt-in, per device
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+    constexpr int bytes = Shape<D, F8>::BYTES;
+    static_assert(bytes <= 232448, "shared memory of one CTA");
+    if (!ready[dev].load()) {
+        cudaError_t e = cudaFuncSetAttribute(attention_decode_kernel<D, F8, WIDE>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e != cudaSuccess) return e;
+        ready[dev].store(true);
+    }
+    cudaLaunchAttribute at[1];
+    cudaLaunchConfig_t cfg = pdl_config(dim3(grid), dim3(AD_THREADS), bytes, st, at);
+    return cudaLaunchKernelEx(&cfg, attention_decode_kernel<D, F8, WIDE>, tk, tv, a);
+}
+
 }  // namespace
 
 size_t attention_decode_workspace_bytes(int num_sms, int n_seqs, int nq, int max_len, bool weights) {
-    if (num_sms <= 0 || n_seqs < 0 || n_seqs > kMaxSeqs || nq < 1 || nq > 65536 || max_len < 0) return 0;
-    size_t n = 256;
-    if (weights)
-        n += up256((size_t)n_seqs * nq * sizeof(float2)) + (size_t)n_seqs * nq * up256((size_t)max_len * 4);
-    return n;
+    if (num_sms <= 0 || num_sms > MAX_CTAS || n_seqs < 0 || n_seqs > kMaxSeqs || nq < 1 || nq > 65536 || max_len < 0 ||
+        (long long)n_seqs * nq * (((long long)max_len + TK - 1) / TK) > INT_MAX)
+        return 0;
+    return layout(num_sms, n_seqs, nq, max_len, weights).bytes;
 }
 
 cudaError_t launch_attention_decode(const AttentionDecode &p, cudaStream_t st) {
     if (p.n_seqs <= 0) return cudaSuccess;
-    char *ws = static_cast<char *>(p.workspace) + 256;
-    float2 *stat = p.weight_out ? reinterpret_cast<float2 *>(ws) : nullptr;
-    float *scores = p.weight_out ? reinterpret_cast<float *>(ws + up256((size_t)p.n_seqs * p.nq * sizeof(float2)))
-                                 : nullptr;
-    const long long ld = (long long)up256((size_t)p.max_len * 4) / 4;
-    cudaLaunchAttribute at[1];
-    cudaLaunchConfig_t cfg = pdl_config(dim3(p.nq, p.n_seqs), dim3(AD_WARPS * 32), 0, st, at);
-    cudaError_t e = cudaLaunchKernelEx(&cfg, p.cache.d == 128 ? attention_decode_kernel<128> : attention_decode_kernel<64>,
-                                       p, scores, stat, ld);
+    const int sms = device_num_sms();
+    const Layout y = layout(sms, p.n_seqs, p.nq, p.max_len, p.weight_out != nullptr);
+    char *ws = static_cast<char *>(p.workspace);
+    Args a{};
+    a.p = p;
+    a.group = p.nq / p.cache.nkv;
+    a.chunks = (a.group + PART_ROWS - 1) / PART_ROWS;
+    a.box_rows = std::min(TK, 1 << p.cache.page_shift);
+    a.count = reinterpret_cast<uint32_t *>(ws);
+    a.part = reinterpret_cast<float *>(ws + y.part);
+    a.ml = reinterpret_cast<float2 *>(ws + y.ml);
+    if (p.weight_out) {
+        a.stat = reinterpret_cast<float2 *>(ws + y.stat);
+        a.scores = reinterpret_cast<float *>(ws + y.scores);
+        a.ld_scores = y.ld_scores;
+    }
+    CUtensorMap tk, tv;
+    if (!make_tmap_cache(&tk, p.cache, p.cache.k) || !make_tmap_cache(&tv, p.cache, p.cache.v))
+        return cudaErrorInvalidValue;
+    // one CTA per SM, fewer where the lengths cannot hold as many tiles
+    const long long most = (long long)p.n_seqs * p.cache.nkv * a.chunks * ((p.max_len + TK - 1) / TK);
+    const int grid = (int)std::min<long long>(sms, std::max<long long>(most, 1));
+    cudaError_t e;
+    if (p.cache.d == 128)
+        e = p.cache.f8 ? (a.group > 8 ? launch_kernel<128, true, true>(tk, tv, a, grid, st)
+                                      : launch_kernel<128, true, false>(tk, tv, a, grid, st))
+                       : (a.group > 8 ? launch_kernel<128, false, true>(tk, tv, a, grid, st)
+                                      : launch_kernel<128, false, false>(tk, tv, a, grid, st));
+    else
+        e = p.cache.f8 ? (a.group > 8 ? launch_kernel<64, true, true>(tk, tv, a, grid, st)
+                                      : launch_kernel<64, true, false>(tk, tv, a, grid, st))
+                       : (a.group > 8 ? launch_kernel<64, false, true>(tk, tv, a, grid, st)
+                                      : launch_kernel<64, false, false>(tk, tv, a, grid, st));
     if (e != cudaSuccess || !p.weight_out || p.max_len == 0) return e;
-    cfg = pdl_config(dim3((p.max_len + 255) / 256, p.n_seqs), dim3(256), 0, st, at);
-    return cudaLaunchKernelEx(&cfg, attention_weight_kernel, p, (const float *)scores, (const float2 *)stat, ld);
+    cudaLaunchAttribute at[1];
+    cudaLaunchConfig_t cfg = pdl_config(dim3((p.max_len + 255) / 256, p.n_seqs), dim3(256), 0, st, at);
+    return cudaLaunchKernelEx(&cfg, attention_weight_kernel, p, (const float *)a.scores, (const float2 *)a.stat, a.ld_scores);
 }
 
 }  // namespace h3

@@ -1230,6 +1230,22 @@ bool make_tmap_rows(CUtensorMap *m, const void *ptr, uint64_t rows, uint64_t col
     return r == CUDA_SUCCESS;
 }
 
+bool make_tmap_cache(CUtensorMap *m, const KvCache &c, const void *base) {
+    PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t es = c.f8 ? 1 : 2, page = cuuint64_t(1) << c.page_shift;
+    cuuint64_t dims[4] = {(cuuint64_t)c.d, page, (cuuint64_t)c.nkv, (cuuint64_t)c.num_pages};
+    cuuint64_t strides[3] = {c.d * es, page * c.d * es, (cuuint64_t)c.page_stride * es};
+    const int row = c.d * (int)es < 128 ? 64 : 128;   // bytes
+    cuuint32_t box[4] = {(cuuint32_t)(row / es), (cuuint32_t)(page < 64 ? page : 64), 1, 1};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    CUresult r = fn(m, c.f8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base),
+                    dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                    row == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+}
+
 bool make_tmap_rows_e4m3(CUtensorMap *m, const void *ptr, uint64_t rows, uint64_t cols, uint32_t box_rows) {
     PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
     if (!fn || rows == 0 || cols == 0 || cols % 16 != 0 || (reinterpret_cast<uintptr_t>(ptr) & 15)) return false;

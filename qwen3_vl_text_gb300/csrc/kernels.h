@@ -221,6 +221,10 @@ struct AttentionDecode {
     void *workspace;
     int32_t *status;
 };
+// Tensor map of the cache's keys or values (`base` = cache.k or cache.v) as [page][kv head][place]
+// [element], read in boxes of min(page_size, 64) places x 128 bytes (64 for e4m3 with d = 64) of one
+// head, swizzled by that width.  False if the driver refuses it.
+bool make_tmap_cache(CUtensorMap *m, const KvCache &cache, const void *base);
 // 0 for sizes the call refuses.
 size_t attention_decode_workspace_bytes(int num_sms, int n_seqs, int nq, int max_len, bool weights);
 cudaError_t launch_attention_decode(const AttentionDecode &p, cudaStream_t st);
