@@ -11,7 +11,7 @@
 //    equal run of tiles per CTA, one CTA per SM, whatever the lengths are: a run may end inside a
 //    segment, whose parts are then joined (below).  Lengths are read on the device.
 //  * A producer warp keeps up to STAGES tiles of K and V in flight through TMA (a box per page,
-//    one lane per box, page numbers fetched four tiles ahead); eight warps compute.
+//    one lane per box, their page numbers looked up a batch ahead); eight warps compute.
 //  * The products run on mma.sync m16n8k16 with the q heads as the 16 rows: there are at most 16 rows
 //    of work per key, which a 128-row tcgen05 tile would leave mostly empty, and a warp that
 //    holds scores, weights and output in its own registers needs no exchange with other warps per tile.
@@ -37,7 +37,6 @@ constexpr int CWARPS = 8;               // compute warps
 constexpr int AD_THREADS = (CWARPS + 1) * 32;
 constexpr int MAX_CTAS = 1024;          // arrival counters at the head of the workspace
 constexpr int PART_ROWS = 16;           // heads of a segment
-constexpr int AHEAD = 4;                // tiles whose page numbers are fetched ahead
 
 template <int D, bool F8>
 struct Shape {
@@ -253,59 +252,55 @@ __global__ void __launch_bounds__(AD_THREADS, 1) attention_decode_kernel(const _
 
     if (warp == CWARPS) {
         // ------------------------------------------------ producer
-        const int boxes = TK / a.box_rows;
+        // A batch of 32 boxes, one per lane, is looked up while the batch before it is issued: a lane
+        // finds its tile's segment and its box's page, and later issues that box itself.
+        const int boxes = TK / a.box_rows, per = 32 / boxes;   // boxes of a tile, tiles of a batch
         const int page_mask = (1 << p.cache.page_shift) - 1;
-        int nb[AHEAD], nu[AHEAD], ny[AHEAD], nn[AHEAD];   // page (-1: no box), unit, place, boxes of the tile
-        const auto fetch = [&](int i) {
-            const int key = w.j * TK + lane * a.box_rows;
-            nb[i] = -1;
-            nu[i] = w.u / a.chunks;
-            ny[i] = key & page_mask;
-            nn[i] = min(boxes, (w.len - w.j * TK + a.box_rows - 1) / a.box_rows);
-            if (lane < nn[i]) nb[i] = p.table[(long long)w.b * p.ld_table + (key >> p.cache.page_shift)];
+        struct Box {
+            int page, place, head, n;   // n: boxes that the tile has
         };
-        int ahead = t0;
-        const auto advance = [&]() {
-            if (++ahead < t1 && ++w.j == w.tiles) w.next(units, p.seq_lens, p.max_len);
+        const auto look_up = [&](int t) {
+            Box x{0, 0, 0, 0};
+            if (t >= t1) return x;
+            Walk v;
+            v.start(t, pre, p.seq_lens, p.n_seqs, p.max_len);
+            const int key = v.j * TK + lane % boxes * a.box_rows;
+            x.n = min(boxes, (v.len - v.j * TK + a.box_rows - 1) / a.box_rows);
+            x.head = v.u / a.chunks;
+            x.place = key & page_mask;
+            if (lane % boxes < x.n) x.page = p.table[(long long)v.b * p.ld_table + (key >> p.cache.page_shift)];
+            return x;
         };
-        #pragma unroll
-        for (int i = 0; i < AHEAD; ++i)
-            if (ahead < t1) {
-                fetch(i);
-                advance();
-            }
         int stage = 0, round = 0;
         bool ok = true;
-        for (int t = t0; t < t1 && ok; t += AHEAD) {
-            #pragma unroll
-            for (int i = 0; i < AHEAD; ++i) {
-                if (t + i >= t1 || !ok) break;
+        Box cur = look_up(t0 + lane / boxes);
+        for (int tb = t0; tb < t1 && ok; tb += per) {
+            const Box next = look_up(tb + per + lane / boxes);
+            for (int i = 0; i < per && tb + i < t1; ++i) {
                 if (round > 0) ok = mbar_wait(empty + stage, (round - 1) & 1, abort);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 uint8_t *k = smem + stage * 2 * S::TILE, *v = k + S::TILE;
-                if (lane == 0) mbar_arrive_expect_tx(full + stage, nn[i] * a.box_rows * S::ROW * 2);
+                if (lane == i * boxes) mbar_arrive_expect_tx(full + stage, cur.n * a.box_rows * S::ROW * 2);
                 __syncwarp();
-                if (lane < nn[i]) {
-                    int page = nb[i];
+                const int box = lane - i * boxes;
+                if (box >= 0 && box < cur.n) {
+                    int page = cur.page;
                     if (page < 0 || page >= p.cache.num_pages) {
                         report(p.status, ST_BOUNDS);
                         page = p.cache.num_pages;   // outside the map: the box is filled with zeros
                     }
                     #pragma unroll
                     for (int x = 0; x < S::ROW / S::BOX; ++x) {
-                        const int off = x * (TK * S::BOX) + lane * a.box_rows * S::BOX;
+                        const int off = x * (TK * S::BOX) + box * a.box_rows * S::BOX;
                         const int col = x * (S::BOX / (F8 ? 1 : 2));
-                        tma_load_4d(k + off, &tmK, full + stage, col, ny[i], nu[i], page);
-                        tma_load_4d(v + off, &tmV, full + stage, col, ny[i], nu[i], page);
+                        tma_load_4d(k + off, &tmK, full + stage, col, cur.place, cur.head, page);
+                        tma_load_4d(v + off, &tmV, full + stage, col, cur.place, cur.head, page);
                     }
-                }
-                if (ahead < t1) {
-                    fetch(i);
-                    advance();
                 }
                 if (++stage == STAGES) stage = 0, ++round;
             }
+            cur = next;
         }
         if (!ok) {
             // a wait ran out: leave once the copies in flight have landed (each of these waits is limited too)
@@ -643,20 +638,40 @@ __global__ void __launch_bounds__(AD_THREADS, 1) attention_decode_kernel(const _
     }
 }
 
-// weight_out[b][i] = weight_in[b][i] + sum over the q heads, in order, of their p_i.
+// weight_out[b][i] = weight_in[b][i] + sum over the q heads of their p_i, from the stored scores and
+// each head's (m, 1/l).  A CTA takes 64 keys of a sequence, two per lane (256 contiguous bytes a warp
+// load); warp w sums the heads w, w + 8, ... in order and the eight sums are added in order, so the
+// result is the same on every run.  Reads 4 bytes per head and key, mostly from L2 where the
+// attention left them.
 __global__ void __launch_bounds__(256) attention_weight_kernel(const AttentionDecode p, const float *scores,
                                                                const float2 *stat, long long ld_scores) {
+    __shared__ float2 part[8][32];
     pdl_trigger();
     pdl_wait();
-    const int b = blockIdx.y, i = blockIdx.x * blockDim.x + threadIdx.x;
+    const int b = blockIdx.y, i0 = blockIdx.x * TK, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int len = min(max(p.seq_lens[b], 0), p.max_len);
-    if (i >= len) return;
-    float acc = 0.f;
-    for (int h = 0; h < p.nq; ++h) {
-        const float2 ml = stat[(long long)b * p.nq + h];
-        acc = fmaf(ex2(scores[((long long)b * p.nq + h) * ld_scores + i] - ml.x), ml.y, acc);
+    if (i0 >= len) return;
+    const float *s = scores + (long long)b * p.nq * ld_scores + i0 + 2 * lane;   // scores are stored in whole slices of 16
+    const float2 *st = stat + (long long)b * p.nq;
+    const bool in = i0 + 2 * lane < len;
+    float2 acc = make_float2(0.f, 0.f);
+    if (in) {
+        #pragma unroll 8
+        for (int h = warp; h < p.nq; h += 8) {
+            const float2 x = *reinterpret_cast<const float2 *>(s + h * ld_scores), ml = st[h];
+            acc.x = fmaf(ex2(x.x - ml.x), ml.y, acc.x);
+            acc.y = fmaf(ex2(x.y - ml.x), ml.y, acc.y);
+        }
     }
-    p.weight_out[b * p.ld_weight + i] = (p.weight_in ? p.weight_in[b * p.ld_weight + i] : 0.f) + acc;
+    part[warp][lane] = acc;
+    __syncthreads();
+    const int i = i0 + threadIdx.x;
+    if (threadIdx.x < TK && i < len) {
+        float sum = 0.f;
+        #pragma unroll
+        for (int w = 0; w < 8; ++w) sum += reinterpret_cast<const float *>(part[w])[threadIdx.x];
+        p.weight_out[b * p.ld_weight + i] = (p.weight_in ? p.weight_in[b * p.ld_weight + i] : 0.f) + sum;
+    }
 }
 
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
@@ -741,7 +756,7 @@ cudaError_t launch_attention_decode(const AttentionDecode &p, cudaStream_t st) {
                                       : launch_kernel<64, false, false>(tk, tv, a, grid, st));
     if (e != cudaSuccess || !p.weight_out || p.max_len == 0) return e;
     cudaLaunchAttribute at[1];
-    cudaLaunchConfig_t cfg = pdl_config(dim3((p.max_len + 255) / 256, p.n_seqs), dim3(256), 0, st, at);
+    cudaLaunchConfig_t cfg = pdl_config(dim3((p.max_len + TK - 1) / TK, p.n_seqs), dim3(256), 0, st, at);
     return cudaLaunchKernelEx(&cfg, attention_weight_kernel, p, (const float *)a.scores, (const float2 *)a.stat, a.ld_scores);
 }
 
