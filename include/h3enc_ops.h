@@ -389,8 +389,8 @@ H3ENC_API h3enc_status h3enc_op_qk_norm_rope(const void *qkv, int64_t ld_qkv, in
  *   zero-filled once before its first use and then reused by calls of any sizes that fit.
  *   Calls (and graphs that hold them) sharing it must not overlap on the GPU.
  * The result does not depend on timing: the same inputs give the same bits on every run.
- * Requires n_seqs <= 1024, n_heads % n_kv_heads == 0, leading dimensions of q and o that are
- * multiples of 8, q and o 16-byte aligned. */
+ * Requires n_seqs <= 1024, max_len <= 2^30, n_heads % n_kv_heads == 0, leading dimensions of
+ * q and o that are multiples of 8, q and o 16-byte aligned. */
 H3ENC_API h3enc_status h3enc_op_attention_decode(const void *q, int64_t ld_q, void *o, int64_t ld_o,
                                                  const h3enc_kv_cache *cache, const int32_t *page_table,
                                                  int32_t ld_table, const int32_t *seq_lens, int32_t n_seqs,
@@ -419,7 +419,7 @@ H3ENC_API int64_t h3enc_op_attention_decode_workspace_bytes(int32_t n_seqs, int3
  *   0 from there to max_len (tokens appended later start at 0).
  *   kept int32 [n_seqs, ld_kept], ld_kept >= budget: the places the kept tokens had,
  *   ascending, then -1 up to budget.  new_lens int32 [n_seqs] (may be seq_lens itself).
- * Requires budget >= 1, sink + recent <= budget, n_seqs <= 1024. */
+ * Requires budget >= 1, sink + recent <= budget, n_seqs <= 1024, max_len <= 2^30. */
 H3ENC_API h3enc_status h3enc_op_cache_evict(const h3enc_kv_cache *cache, const int32_t *page_table, int32_t ld_table,
                                             const int32_t *page_table_out, int32_t ld_table_out,
                                             const int32_t *seq_lens, int32_t n_seqs, int32_t max_len, int32_t budget,

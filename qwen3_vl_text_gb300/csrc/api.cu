@@ -1561,7 +1561,7 @@ h3enc_status h3enc_op_attention_decode(const void *q, int64_t ld_q, void *o, int
     if (s != H3ENC_OK) return s;
     const int64_t width = (int64_t)n_heads * cache->head_dim;
     if (n_seqs < 0 || n_seqs > h3::kMaxSeqs || n_heads < 1 || n_heads > 65536 || n_heads % cache->n_kv_heads ||
-        max_len < 0 || ld_table < 0 || (int64_t)ld_table * cache->page_size < max_len)
+        max_len < 0 || max_len > h3::kMaxCacheLen || ld_table < 0 || (int64_t)ld_table * cache->page_size < max_len)
         return fail(nullptr, H3ENC_ERR_INVALID_ARG, "%s: bad sizes, or the page table does not hold max_len", who);
     if (n_seqs == 0) return H3ENC_OK;
     if (!q || !o || !aligned16(q) || !aligned16(o) || ld_q < width || ld_o < width || ld_q % 8 || ld_o % 8 ||
@@ -1602,7 +1602,7 @@ h3enc_status h3enc_op_cache_evict(const h3enc_kv_cache *cache, const int32_t *pa
     h3::CacheEvict p{};
     const h3enc_status s = take_cache(cache, who, &p.cache);
     if (s != H3ENC_OK) return s;
-    if (n_seqs < 0 || n_seqs > h3::kMaxSeqs || max_len < 0 || budget < 1 || sink < 0 || recent < 0 ||
+    if (n_seqs < 0 || n_seqs > h3::kMaxSeqs || max_len < 0 || max_len > h3::kMaxCacheLen || budget < 1 || sink < 0 || recent < 0 ||
         (int64_t)sink + recent > budget)
         return fail(nullptr, H3ENC_ERR_INVALID_ARG, "%s: bad sizes, or sink + recent above the budget", who);
     const int64_t most = budget < max_len ? budget : max_len;

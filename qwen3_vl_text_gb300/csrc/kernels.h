@@ -165,6 +165,7 @@ cudaError_t launch_merge_visual_rows(const int32_t *vis_rank, const bf16 *src, i
 // ---- paged key/value cache (kv_cache.cu) and the attention of one new token over it
 // (attention_decode.cu).  Element e of kv head g of place s of page p lies at
 // p * page_stride + (g * page_size + s) * d + e; page_size = 1 << page_shift.
+constexpr int kMaxCacheLen = 1 << 30;   // tokens of a sequence: sums of lengths and strides stay in 32 bits
 struct KvCache {
     void *k, *v;
     const float *k_scale, *v_scale;   // [nkv], e4m3 only

@@ -8,6 +8,8 @@
 // _apply_rotary_pos_emb); the pages hold no cache.
 #include <cuda_fp8.h>
 
+#include <atomic>
+
 #include "common.cuh"
 #include "kernels.h"
 
@@ -135,6 +137,10 @@ __global__ void __launch_bounds__(QK_THREADS) qk_norm_rope_kernel(const QkNormRo
 // ---------------------------------------------------------------- eviction
 
 constexpr int SEL_THREADS = 1024;
+constexpr int SEL_BLOCK = 32 * SEL_THREADS;   // tokens of one block of the placing pass
+constexpr int SEL_CACHE = 49152;              // keys a CTA holds in shared memory (192 KB)
+constexpr int SEL_PER_CTA = 8192;             // tokens per CTA from which the cluster grows
+constexpr int BINS = 2048;
 
 // Order of the weights as unsigned integers: larger key, larger weight; both zeros alike, NaN lowest.
 __device__ __forceinline__ uint32_t weight_key(float w) {
@@ -143,149 +149,260 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
     return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-__device__ __forceinline__ int clamped_len(const int32_t *lens, int b, int max_len, int32_t *status, bool say) {
-    const int len = lens[b];
-    if (len >= 0 && len <= max_len) return len;
-    if (say) report(status, ST_BOUNDS);
-    return len < 0 ? 0 : max_len;
+// Inclusive scan over the block (1024 threads); sums [32] shared.
+__device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t *sums) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    #pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t u = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += u;
+    }
+    __syncthreads();   // the last use of sums is over
+    if (lane == 31) sums[warp] = v;
+    __syncthreads();
+    uint32_t w = sums[lane];
+    #pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t u = __shfl_up_sync(0xffffffffu, w, o);
+        if (lane >= o) w += u;
+    }
+    const uint32_t before = __shfl_sync(0xffffffffu, w, (warp + 31) & 31);   // sum of the warps before this one
+    return v + (warp ? before : 0u);
 }
 
-// One CTA per sequence.  Finds the budget-th largest key of the unprotected tokens digit by
-// digit (8 bits a pass, a histogram of the tokens that match the digits so far), then walks the
-// tokens in order and gives each kept one its new place.
-__global__ void __launch_bounds__(SEL_THREADS) evict_select_kernel(const CacheEvict p) {
+__device__ __forceinline__ uint32_t ld_cluster(const uint32_t *p, uint32_t rank) {
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(mapa_shared(smem_u32(p), rank)) : "memory");
+    return v;
+}
+
+// One cluster of 1 to 8 CTAs per sequence, each with a contiguous part of its tokens, whose keys it
+// holds in shared memory (what does not fit is read again).  The budget-th largest key of the
+// unprotected tokens is found in three digits (11, 11 and 10 bits): a histogram of the tokens that
+// match the digits so far, summed over the cluster, scanned from the top by all threads.  Then the
+// tokens are counted in order and each kept one is written to its place.  What bounds it is the chain of these
+// steps (a few microseconds), not the 4 bytes per token.
+template <bool CLUSTER>
+__global__ void __launch_bounds__(SEL_THREADS, 1) evict_select_kernel(const CacheEvict p, int cached) {
+    extern __shared__ uint32_t keys[];            // [cached]
+    __shared__ uint32_t hist[3][BINS];
+    __shared__ uint32_t sums[32], s_digit, s_need, s_count[2];
     pdl_trigger();
     pdl_wait();
-    __shared__ uint32_t hist[256];
-    __shared__ uint32_t s_prefix, s_need;
-    __shared__ uint32_t wsum[2][32];
-    const int b = blockIdx.x, tid = threadIdx.x;
-    const int len = clamped_len(p.seq_lens, b, p.max_len, p.status, tid == 0);
-    const float *w = p.weight + b * p.ld_weight;
-    const int first = min(p.sink, len), last = len - min(p.recent, len);   // candidates [first, last)
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t rank = CLUSTER ? cluster_ctarank() : 0u;
+    const int ranks = CLUSTER ? (int)gridDim.x : 1, b = blockIdx.y;
+    int len = p.seq_lens[b];
+    if (len < 0 || len > p.max_len) {
+        if (tid == 0 && rank == 0) report(p.status, ST_BOUNDS);
+        len = len < 0 ? 0 : p.max_len;
+    }
+    const int per = (len + ranks - 1) / ranks;                 // this CTA's tokens [begin, begin + n)
+    const int begin = min((int)rank * per, len), n = min(per, len - begin);
+    const float *w = p.weight + b * p.ld_weight + begin;
+    const int first = min(p.sink, len) - begin, last = len - min(p.recent, len) - begin;   // candidates [first, last)
     const bool all = len <= p.budget;
-    uint32_t prefix = 0, need = 0;
-    if (!all) {
-        need = (uint32_t)(p.budget - p.sink - p.recent);
-        for (int shift = 24; shift >= 0 && need > 0; shift -= 8) {
-            for (int i = tid; i < 256; i += SEL_THREADS) hist[i] = 0;
-            __syncthreads();
-            for (int i = first + tid; i < last; i += SEL_THREADS) {
-                const uint32_t k = weight_key(w[i]);
-                if (shift == 24 || (k >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&hist[(k >> shift) & 255], 1u);
+    const uint32_t wanted = all ? 0u : (uint32_t)(p.budget - p.sink - p.recent);   // of the candidates
+    uint32_t prefix = 0, need = wanted;
+    const auto key_of = [&](int i) { return i < cached ? keys[i] : weight_key(w[i]); };
+    if (wanted) {
+        for (int i = tid; i < 3 * BINS; i += SEL_THREADS) hist[i / BINS][i % BINS] = 0;
+        #pragma unroll 4
+        for (int i = tid; i < min(n, cached); i += SEL_THREADS) keys[i] = weight_key(w[i]);
+        __syncthreads();
+        #pragma unroll
+        for (int pass = 0; pass < 3; ++pass) {
+            const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0), bits = pass == 2 ? 10 : 11;
+            uint32_t *h = hist[pass];
+            for (int i = max(first, 0) + tid; i < min(last, n); i += SEL_THREADS) {
+                const uint32_t k = key_of(i);
+                if (pass == 0 || (k >> (shift + bits)) == (prefix >> (shift + bits)))
+                    atomicAdd(&h[(k >> shift) & ((1u << bits) - 1)], 1u);
+            }
+            if (CLUSTER) cluster_sync();
+            else __syncthreads();
+            // thread t: the bins 2047 - 2t and 2046 - 2t, so that the scan runs from the largest down
+            uint32_t c0 = 0, c1 = 0;
+            const int top = BINS - 1 - 2 * tid;
+            if (CLUSTER) {
+                for (int r = 0; r < ranks; ++r) {
+                    c0 += ld_cluster(h + top, r);
+                    c1 += ld_cluster(h + top - 1, r);
+                }
+            } else {
+                c0 = h[top];
+                c1 = h[top - 1];
+            }
+            const uint32_t upto = block_scan(c0 + c1, sums), before = upto - c0 - c1;
+            if (before < need && need <= upto) {   // exactly one thread
+                const bool in0 = need <= before + c0;
+                s_digit = in0 ? top : top - 1;
+                s_need = need - before - (in0 ? 0u : c0);
             }
             __syncthreads();
-            if (tid == 0) {
-                uint32_t left = need;
-                int digit = 255;
-                while (digit > 0 && hist[digit] < left) left -= hist[digit--];
-                s_prefix = prefix | ((uint32_t)digit << shift);
-                s_need = left;
-            }
-            __syncthreads();
-            prefix = s_prefix;
-            need = s_need;   // how many of the tokens that equal the prefix so far are kept
+            prefix |= s_digit << shift;
+            need = s_need;   // of the tokens that match the digits so far, this many are kept
         }
-        if (p.budget == p.sink + p.recent) prefix = 0xffffffffu;   // none of the candidates (no key is that large)
+    }
+    // kept for certain: protected tokens and larger keys; of the equal ones the first `need`
+    const auto sort_of = [&](int i, bool &sure, bool &eq) {
+        sure = all || i < first || i >= last;
+        eq = false;
+        if (!sure && wanted) {
+            const uint32_t k = key_of(i);
+            sure = k > prefix;
+            eq = k == prefix;
+        }
+    };
+    uint32_t base_sure = 0, base_eq = 0;   // of the tokens before this CTA's (before this block's)
+    if constexpr (CLUSTER) {
+        uint32_t cs = 0, ce = 0;
+        for (int i = tid; i < n; i += SEL_THREADS) {
+            bool sure, eq;
+            sort_of(i, sure, eq);
+            cs += sure;
+            ce += eq;
+        }
+        cs = block_scan(cs, sums);
+        if (tid == SEL_THREADS - 1) s_count[0] = cs;
+        ce = block_scan(ce, sums);
+        if (tid == SEL_THREADS - 1) s_count[1] = ce;
+        cluster_sync();
+        for (uint32_t r = 0; r < rank; ++r) {
+            base_sure += ld_cluster(s_count, r);
+            base_eq += ld_cluster(s_count + 1, r);
+        }
     }
     int32_t *kept = p.kept + b * p.ld_kept;
     float *wo = p.weight_out + b * p.ld_weight_out;
-    uint32_t base_keep = 0, base_eq = 0;
-    for (int i0 = 0; i0 < len; i0 += SEL_THREADS) {
-        const int i = i0 + tid;
-        float v = 0.f;
-        bool sure = false, eq = false;
-        if (i < len) {
-            v = w[i];
-            if (all || i < first || i >= last) sure = true;
-            else {
-                const uint32_t k = weight_key(v);
-                sure = k > prefix;
-                eq = k == prefix;
+    uint32_t *counts = hist[0];   // [32 rows of 1024 tokens][32 warps], both counts in one word (each <= 32768)
+    for (int i0 = 0; i0 < n; i0 += SEL_BLOCK) {
+        const int rows = (min(n - i0, SEL_BLOCK) + SEL_THREADS - 1) / SEL_THREADS;
+        __syncthreads();
+        for (int r = 0; r < rows; ++r) {
+            const int i = i0 + r * SEL_THREADS + tid;
+            bool sure = false, eq = false;
+            if (i < n) sort_of(i, sure, eq);
+            const uint32_t ms = __ballot_sync(0xffffffffu, sure), me = __ballot_sync(0xffffffffu, eq);
+            if (lane == 0) counts[r * 32 + warp] = (uint32_t)__popc(ms) << 16 | (uint32_t)__popc(me);
+        }
+        __syncthreads();
+        const uint32_t own = tid < 32 * rows ? counts[tid] : 0u;
+        const uint32_t inc = block_scan(own, sums);
+        counts[tid] = inc - own;
+        if (tid == SEL_THREADS - 1) s_need = inc;   // the block's total
+        __syncthreads();
+        for (int r = 0; r < rows; ++r) {
+            const int i = i0 + r * SEL_THREADS + tid;
+            bool sure = false, eq = false;
+            if (i < n) sort_of(i, sure, eq);
+            const uint32_t ms = __ballot_sync(0xffffffffu, sure), me = __ballot_sync(0xffffffffu, eq);
+            const uint32_t below = (1u << lane) - 1, at = counts[r * 32 + warp];
+            const uint32_t ns = base_sure + (at >> 16) + __popc(ms & below);
+            const uint32_t ne = base_eq + (at & 0xffffu) + __popc(me & below);
+            if (sure || (eq && ne < need)) {
+                const uint32_t to = ns + min(ne, need);
+                kept[to] = begin + i;
+                wo[to] = w[i];
             }
         }
-        const uint32_t ms = __ballot_sync(0xffffffffu, sure), me = __ballot_sync(0xffffffffu, eq);
-        const int lane = tid & 31, warp = tid >> 5;
-        if (lane == 0) {
-            wsum[0][warp] = __popc(ms);
-            wsum[1][warp] = __popc(me);
-        }
-        __syncthreads();
-        uint32_t ns = 0, ne = 0, ts = 0, te = 0;
-        for (int k = 0; k < 32; ++k) {
-            if (k < warp) ns += wsum[0][k], ne += wsum[1][k];
-            ts += wsum[0][k];
-            te += wsum[1][k];
-        }
-        const uint32_t below = (1u << lane) - 1;
-        ns += __popc(ms & below);
-        ne += base_eq + __popc(me & below);
-        const uint32_t at = base_keep + ns + (min(ne, need) - min(base_eq, need));
-        if (sure || (eq && ne < need)) {
-            kept[at] = i;
-            wo[at] = v;
-        }
-        base_keep += ts + (min(base_eq + te, need) - min(base_eq, need));
-        base_eq += te;
-        __syncthreads();
+        base_sure += s_need >> 16;
+        base_eq += s_need & 0xffffu;
     }
-    for (int i = (int)base_keep + tid; i < p.budget; i += SEL_THREADS) kept[i] = -1;
-    for (int i = (int)base_keep + tid; i < p.max_len; i += SEL_THREADS) wo[i] = 0.f;
-    if (tid == 0) p.new_lens[b] = (int32_t)base_keep;
+    // the rest of the rows, by all CTAs of the cluster
+    const int total = all ? len : p.budget;
+    for (int i = total + (int)rank * SEL_THREADS + tid; i < p.max_len; i += ranks * SEL_THREADS) wo[i] = 0.f;
+    for (int i = total + (int)rank * SEL_THREADS + tid; i < p.budget; i += ranks * SEL_THREADS) kept[i] = -1;
+    // new_lens may be seq_lens: every thread has read the length (and the other CTAs' counts)
+    if (CLUSTER) cluster_sync();
+    else __syncthreads();
+    if (tid == 0 && rank == 0) p.new_lens[b] = total;
 }
 
 constexpr int MOVE_THREADS = 256;
-constexpr int MOVE_VECS = 8;   // 16-byte vectors in flight per thread
 
-// Moves the kept rows of one kv head's K (blockIdx.y even) or V (odd) of one sequence.  A CTA
-// takes chunks of rows blockIdx.x, + gridDim.x, ...; in place (gridDim.x = 1) the chunks go in
-// order: a row moves to its own index or a smaller one, so a chunk's sources are never behind its
-// own first row, and no store of an earlier chunk reaches them; the barrier keeps a chunk's
-// stores behind its own loads.
+// Moves rows of the kept tokens: a chunk of CHUNK_VECS / (16-byte vectors of a row) tokens at a time, whose
+// source and target places are looked up once and serve the chunk's rows of the CTA's planes (K and V
+// of the kv heads blockIdx.y, + gridDim.y, ...).  In place (gridDim.x = 1) a CTA takes the chunks in
+// order: a token moves to its own index or a smaller one, so no source of a chunk lies before the
+// chunk's first token, where the stores of earlier chunks end; the barrier keeps a chunk's own stores
+// behind its loads.  Bound by the bytes: every row is read and written once.
+template <bool IN_PLACE>
 __global__ void __launch_bounds__(MOVE_THREADS) evict_move_kernel(const CacheEvict p) {
+    constexpr int VECS = IN_PLACE ? 8 : 4;              // 16-byte vectors of a plane per thread
+    constexpr int CHUNK_VECS = MOVE_THREADS * VECS, MAX_ROWS = CHUNK_VECS / 4;
+    __shared__ long long s_src[MAX_ROWS], s_dst[MAX_ROWS];   // byte offsets in the pool (kv head 0), -1: no move
     pdl_trigger();
     pdl_wait();
-    const int b = blockIdx.z, g = blockIdx.y >> 1;
-    const int row_vecs = p.cache.d * (p.cache.f8 ? 1 : 2) / 16;   // 4, 8 or 16
-    char *pool = static_cast<char *>((blockIdx.y & 1) ? p.cache.v : p.cache.k);
+    const int b = blockIdx.z, tid = threadIdx.x;
+    const int shift = p.cache.page_shift, mask = (1 << shift) - 1;
+    const int row_bytes = p.cache.d * (p.cache.f8 ? 1 : 2), row_shift = 31 - __clz(row_bytes / 16);   // 4, 8 or 16 vectors
     const long long page_bytes = p.cache.page_stride * (p.cache.f8 ? 1 : 2);
-    const int rows = MOVE_THREADS * MOVE_VECS / row_vecs, per = MOVE_THREADS / row_vecs;
+    const long long head_bytes = (long long)row_bytes << shift;
+    const int rows = CHUNK_VECS >> row_shift;
     const int n = p.new_lens[b];
     const int32_t *kept = p.kept + b * p.ld_kept;
     const int32_t *ti = p.table + (long long)b * p.ld_table;
-    const int32_t *to = p.table_out ? p.table_out + (long long)b * p.ld_table_out : ti;
-    const int vec = threadIdx.x % row_vecs;
-    const int mask = (1 << p.cache.page_shift) - 1;
-    const auto place = [&](const int32_t *table, int i) -> char * {
-        const int page = table[i >> p.cache.page_shift];
-        if (page < 0 || page >= p.cache.num_pages) return nullptr;
-        return pool + page * page_bytes + ((long long)((g << p.cache.page_shift) + (i & mask)) * row_vecs + vec) * 16;
-    };
+    const int32_t *to = IN_PLACE ? ti : p.table_out + (long long)b * p.ld_table_out;
+    const int planes = 2 * p.cache.nkv, vec = (tid & ((1 << row_shift) - 1)) * 16;
     for (int r0 = blockIdx.x * rows; r0 < n; r0 += rows * gridDim.x) {
-        uint4 v[MOVE_VECS];
-        char *dst[MOVE_VECS];
-        #pragma unroll
-        for (int k = 0; k < MOVE_VECS; ++k) {
-            const int r = r0 + k * per + threadIdx.x / row_vecs;
-            dst[k] = nullptr;
-            if (r < n) {
-                const char *src = place(ti, kept[r]);
-                dst[k] = place(to, r);
-                if (!src || !dst[k]) {
+        __syncthreads();
+        for (int r = tid; r < rows; r += MOVE_THREADS) {
+            long long src = -1, dst = -1;
+            if (r0 + r < n) {
+                const int from = kept[r0 + r], a = ti[from >> shift], c = to[(r0 + r) >> shift];
+                if (a < 0 || a >= p.cache.num_pages || c < 0 || c >= p.cache.num_pages) {
                     report(p.status, ST_BOUNDS);
-                    dst[k] = nullptr;
-                } else if (src == dst[k]) {
-                    dst[k] = nullptr;   // already in its place
                 } else {
-                    v[k] = *reinterpret_cast<const uint4 *>(src);
+                    src = a * page_bytes + (long long)(from & mask) * row_bytes;
+                    dst = c * page_bytes + (long long)((r0 + r) & mask) * row_bytes;
+                    if (src == dst) dst = -1;   // already there
                 }
             }
+            s_src[r] = src;
+            s_dst[r] = dst;
         }
-        if (!p.table_out) __syncthreads();
-        #pragma unroll
-        for (int k = 0; k < MOVE_VECS; ++k)
-            if (dst[k]) *reinterpret_cast<uint4 *>(dst[k]) = v[k];
+        __syncthreads();
+        for (int q = blockIdx.y; q < planes; q += gridDim.y) {
+            char *pool = static_cast<char *>((q & 1) ? p.cache.v : p.cache.k) + (q >> 1) * head_bytes + vec;
+            uint4 v[VECS];
+            #pragma unroll
+            for (int k = 0; k < VECS; ++k) {
+                const int r = (k * MOVE_THREADS + tid) >> row_shift;
+                if (s_dst[r] >= 0) v[k] = *reinterpret_cast<const uint4 *>(pool + s_src[r]);
+            }
+            if (IN_PLACE) __syncthreads();
+            #pragma unroll
+            for (int k = 0; k < VECS; ++k) {
+                const int r = (k * MOVE_THREADS + tid) >> row_shift;
+                if (s_dst[r] >= 0) *reinterpret_cast<uint4 *>(pool + s_dst[r]) = v[k];
+            }
+        }
     }
+}
+
+template <bool CLUSTER>
+cudaError_t launch_select(const CacheEvict &p, int ranks, cudaStream_t st) {
+    static std::atomic<bool> ready[kMaxDevices];   // the shared-memory opt-in, per device
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+    if (!ready[dev].load()) {
+        cudaError_t e = cudaFuncSetAttribute(evict_select_kernel<CLUSTER>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             SEL_CACHE * 4);
+        if (e != cudaSuccess) return e;
+        ready[dev].store(true);
+    }
+    const int per = (p.max_len + ranks - 1) / ranks, cached = per < SEL_CACHE ? per : SEL_CACHE;
+    cudaLaunchAttribute at[2];
+    cudaLaunchConfig_t cfg = pdl_config(dim3(ranks, p.n_seqs), dim3(SEL_THREADS), (size_t)cached * 4, st, at);
+    if (CLUSTER) {
+        at[1].id = cudaLaunchAttributeClusterDimension;
+        at[1].val.clusterDim.x = ranks;
+        at[1].val.clusterDim.y = 1;
+        at[1].val.clusterDim.z = 1;
+        cfg.numAttrs = 2;
+    }
+    return cudaLaunchKernelEx(&cfg, evict_select_kernel<CLUSTER>, p, cached);
 }
 
 }  // namespace
@@ -305,15 +422,21 @@ cudaError_t launch_qk_norm_rope(const QkNormRope &p, cudaStream_t st) {
 
 cudaError_t launch_cache_evict(const CacheEvict &p, cudaStream_t st) {
     if (p.n_seqs <= 0) return cudaSuccess;
-    cudaLaunchAttribute at[1];
-    cudaLaunchConfig_t cfg = pdl_config(dim3(p.n_seqs), dim3(SEL_THREADS), 0, st, at);
-    cudaError_t e = cudaLaunchKernelEx(&cfg, evict_select_kernel, p);
+    int ranks = 1;
+    while (ranks < 8 && p.max_len > ranks * SEL_PER_CTA) ranks *= 2;
+    cudaError_t e = ranks > 1 ? launch_select<true>(p, ranks, st) : launch_select<false>(p, 1, st);
     if (e != cudaSuccess || p.max_len == 0) return e;
+    // planes of a chunk over several CTAs where the chunks alone are too few to fill the SMs
+    const int row_vecs = p.cache.d * (p.cache.f8 ? 1 : 2) / 16, planes = 2 * p.cache.nkv;
     const int most = p.budget < p.max_len ? p.budget : p.max_len;
-    const int rows = MOVE_THREADS * MOVE_VECS / (p.cache.d * (p.cache.f8 ? 1 : 2) / 16);
-    cfg = pdl_config(dim3(p.table_out ? (most + rows - 1) / rows : 1, 2 * p.cache.nkv, p.n_seqs), dim3(MOVE_THREADS), 0,
-                     st, at);
-    return cudaLaunchKernelEx(&cfg, evict_move_kernel, p);
+    const int rows = MOVE_THREADS * 4 / row_vecs, chunks = p.table_out ? (most + rows - 1) / rows : 1;
+    const long long ctas = (long long)chunks * p.n_seqs, want = 8LL * device_num_sms();
+    int gy = (int)(ctas >= want ? 1 : (want + ctas - 1) / ctas);
+    if (gy > planes) gy = planes;
+    if (!p.table_out) gy = planes < 65535 ? planes : 65535;
+    cudaLaunchAttribute at[1];
+    cudaLaunchConfig_t cfg = pdl_config(dim3(chunks, gy, p.n_seqs), dim3(MOVE_THREADS), 0, st, at);
+    return cudaLaunchKernelEx(&cfg, p.table_out ? evict_move_kernel<false> : evict_move_kernel<true>, p);
 }
 
 }  // namespace h3

@@ -137,7 +137,7 @@ def test_qk_norm_rope_of_no_rows_does_nothing(Q):
 
 
 @pytest.mark.parametrize("kw", [
-    dict(n=-1), dict(n=1025), dict(nq=0), dict(nq=3), dict(max_len=-1), dict(max_len=65), dict(ld_table=-1),
+    dict(n=-1), dict(n=1025), dict(nq=0), dict(nq=3), dict(max_len=-1), dict(max_len=65), dict(ld_table=-1), dict(max_len=2 ** 30 + 1, ld_table=2 ** 27),
     dict(q=None), dict(o=None), dict(q=(1 << 20) + 8), dict(ld_q=252), dict(ld_q=260), dict(ld_o=128), dict(table=None),
     dict(lens=None), dict(o=1 << 20), dict(o=(1 << 20) + 256), dict(w_in=16), dict(w_out=16, ld_w=63),
     dict(w_out=1 << 12, w_in=(1 << 12) + 4)])
@@ -150,7 +150,7 @@ def test_attention_decode_of_no_sequences_does_nothing(Q):
 
 
 @pytest.mark.parametrize("kw", [
-    dict(n=-1), dict(n=1025), dict(max_len=-1), dict(max_len=65), dict(budget=0), dict(sink=-1), dict(recent=-1),
+    dict(n=-1), dict(n=1025), dict(max_len=-1), dict(max_len=65), dict(max_len=2 ** 30 + 1, ld_table=2 ** 27, ld_w=2 ** 31, ld_w_out=2 ** 31), dict(budget=0), dict(sink=-1), dict(recent=-1),
     dict(sink=20, recent=13), dict(sink=2 ** 31 - 1, recent=2 ** 31 - 1), dict(table=None), dict(lens=None),
     dict(w=None), dict(w_out=None), dict(kept=None), dict(new=None), dict(ld_w=63), dict(ld_w_out=63),
     dict(ld_kept=31), dict(w_out=1 << 20), dict(w_out=(1 << 20) + 4), dict(table_out=16, ld_out=1)])
