@@ -45,83 +45,91 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
 }
 
 constexpr int QK_THREADS = 256;
+constexpr int QK_BATCH = 5;   // head vectors a lane group loads before it works on the first (64 + 2 x 8 heads of 128: all)
 
-// D / 8 lanes per head vector, eight elements (16 bytes) each; lane l and lane l ^ (D/16) hold the
-// two halves of a rotation pair.  A CTA takes one row and the heads blockIdx.y * 256/(D/8)
-// onwards in steps of the grid.
+// D / 8 lanes (a group) per head vector, eight elements (16 bytes) each; lane l and lane l ^ (D/16)
+// hold the two halves of a rotation pair.  Each row has 1 << gshift groups of a CTA, which take its heads in
+// turn (blockIdx.y: every gridDim.y-th turn), so the row's rotary factors stay in registers; a CTA takes as many
+// rows as it has groups for.
 template <int D>
-__global__ void __launch_bounds__(QK_THREADS) qk_norm_rope_kernel(const QkNormRope p) {
+__global__ void __launch_bounds__(QK_THREADS) qk_norm_rope_kernel(const QkNormRope p, int gshift) {
+    constexpr int LANES = D / 8, GROUPS = QK_THREADS / LANES;
     pdl_trigger();
     pdl_wait();
-    constexpr int LANES = D / 8, HEADS = QK_THREADS / LANES;
-    const int t = blockIdx.x;
-    const int lane = threadIdx.x % LANES;
-    const int heads = p.nq + 2 * p.nkv;
+    const int lane = threadIdx.x % LANES, group = threadIdx.x / LANES;
+    const int t = blockIdx.x * (GROUPS >> gshift) + (group >> gshift);
+    const bool row = t < p.T;
+    const int heads = row ? p.nq + 2 * p.nkv : 0;
+    const int step = gridDim.y << gshift;
+    const int first = (blockIdx.y << gshift) + (group & ((1 << gshift) - 1));
+    const bf16 *src = p.qkv + t * p.ld_qkv + 8 * lane;
     const int j0 = (8 * lane) % (D / 2);
     const bool upper = lane >= LANES / 2;
-    int page = -1, place = 0;
-    if (p.has_cache) {
-        const int slot = p.slots[t];
-        if (slot >= 0) {
-            page = slot >> p.cache.page_shift;
-            place = slot & ((1 << p.cache.page_shift) - 1);
-            if (page >= p.cache.num_pages) {
-                if (threadIdx.x == 0 && blockIdx.y == 0) report(p.status, ST_BOUNDS);
-                page = -1;
-            }
-        }
-    }
     float cs[8], sn[8];
-    if (p.cos_t) {
+    int slot = -1;
+    const bool rotate = p.cos_t != nullptr;
+    // the same number of turns for every lane of a warp (the shuffles below need them all)
+    for (int h0 = 0; h0 < p.nq + 2 * p.nkv; h0 += QK_BATCH * step) {
+        uint4 raw[QK_BATCH];
         #pragma unroll
-        for (int i = 0; i < 8; i += 4) {
-            const long long at = p.cs_rows ? ((long long)((j0 + i) / 4) * p.cs_rows + t) * 4
-                                           : (long long)t * (D / 2) + j0 + i;
-            *reinterpret_cast<float4 *>(cs + i) = *reinterpret_cast<const float4 *>(p.cos_t + at);
-            *reinterpret_cast<float4 *>(sn + i) = *reinterpret_cast<const float4 *>(p.sin_t + at);
+        for (int u = 0; u < QK_BATCH; ++u) {
+            const int h = h0 + first + u * step;
+            raw[u] = h < heads ? *reinterpret_cast<const uint4 *>(src + (long long)h * D) : make_uint4(0, 0, 0, 0);
         }
-        #pragma unroll
-        for (int i = 0; i < 8; ++i) sn[i] = upper ? sn[i] : -sn[i];   // y = x cos + partner * (-+ sin)
-    }
-    // whole groups of lanes share a head, so the shuffles below stay inside it; the trip count is
-    // the same for every lane of a warp
-    const int step = HEADS * gridDim.y;
-    for (int h0 = blockIdx.y * HEADS; h0 < heads; h0 += step) {
-        const int h = h0 + threadIdx.x / LANES;
-        const bool in = h < heads;
-        const bool is_q = h < p.nq, is_v = h >= p.nq + p.nkv;
-        float x[8];
-        unpack8(in ? *reinterpret_cast<const uint4 *>(p.qkv + t * p.ld_qkv + (long long)h * D + 8 * lane)
-                   : make_uint4(0, 0, 0, 0), x);
-        const bf16 *w = is_q ? p.wq : p.wk;
-        float ss = 0.f;
-        #pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
-        #pragma unroll
-        for (int o = LANES / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        if (in && !is_v && w) {
-            const float r = 1.0f / sqrtf(ss / (float)D + p.eps);
-            float g[8];
-            unpack8(*reinterpret_cast<const uint4 *>(w + 8 * lane), g);
-            #pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = x[i] * r * g[i];
-        }
-        if (p.cos_t) {
-            #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float y = __shfl_xor_sync(0xffffffffu, x[i], LANES / 2);
-                if (!is_v) x[i] = fmaf(x[i], cs[i], y * sn[i]);
+        if (h0 == 0) {   // behind the first loads: what the row's heads share
+            if (p.has_cache && row) slot = p.slots[t];
+            if (rotate && row) {
+                #pragma unroll
+                for (int i = 0; i < 8; i += 4) {
+                    const long long at = p.cs_rows ? ((long long)((j0 + i) / 4) * p.cs_rows + t) * 4
+                                                   : (long long)t * (D / 2) + j0 + i;
+                    *reinterpret_cast<float4 *>(cs + i) = *reinterpret_cast<const float4 *>(p.cos_t + at);
+                    *reinterpret_cast<float4 *>(sn + i) = *reinterpret_cast<const float4 *>(p.sin_t + at);
+                }
+                #pragma unroll
+                for (int i = 0; i < 8; ++i) sn[i] = upper ? sn[i] : -sn[i];   // y = x cos + partner * (-+ sin)
             }
         }
-        if (!in) continue;
-        if (is_q) {
-            if (p.q_out) *reinterpret_cast<uint4 *>(p.q_out + t * p.ld_q + (long long)h * D + 8 * lane) = pack8(x);
-            continue;
-        }
-        const int g = is_v ? h - p.nq - p.nkv : h - p.nq;
-        if (!is_v && p.k_out)
-            *reinterpret_cast<uint4 *>(p.k_out + t * p.ld_k + (long long)g * D + 8 * lane) = pack8(x);
-        if (page >= 0) {
+        #pragma unroll
+        for (int u = 0; u < QK_BATCH; ++u) {
+            const int h = h0 + first + u * step;
+            const bool in = h < heads, is_q = h < p.nq, is_v = h >= p.nq + p.nkv;
+            float x[8];
+            unpack8(raw[u], x);
+            const bf16 *w = is_q ? p.wq : p.wk;
+            float ss = 0.f;
+            #pragma unroll
+            for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
+            #pragma unroll
+            for (int o = LANES / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            if (in && !is_v && w) {
+                const float r = 1.0f / sqrtf(ss / (float)D + p.eps);
+                float g[8];
+                unpack8(*reinterpret_cast<const uint4 *>(w + 8 * lane), g);
+                #pragma unroll
+                for (int i = 0; i < 8; ++i) x[i] = x[i] * r * g[i];
+            }
+            if (rotate) {
+                #pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float y = __shfl_xor_sync(0xffffffffu, x[i], LANES / 2);
+                    if (in && !is_v) x[i] = fmaf(x[i], cs[i], y * sn[i]);
+                }
+            }
+            if (!in) continue;
+            if (is_q) {
+                if (p.q_out) *reinterpret_cast<uint4 *>(p.q_out + t * p.ld_q + (long long)h * D + 8 * lane) = pack8(x);
+                continue;
+            }
+            const int g = is_v ? h - p.nq - p.nkv : h - p.nq;
+            if (!is_v && p.k_out)
+                *reinterpret_cast<uint4 *>(p.k_out + t * p.ld_k + (long long)g * D + 8 * lane) = pack8(x);
+            if (slot < 0) continue;
+            const int page = slot >> p.cache.page_shift, place = slot & ((1 << p.cache.page_shift) - 1);
+            if (page >= p.cache.num_pages) {
+                if (lane == 0) report(p.status, ST_BOUNDS);
+                continue;
+            }
             const long long at = page * p.cache.page_stride +
                                  ((long long)((g << p.cache.page_shift) + place)) * D + 8 * lane;
             void *dst = is_v ? p.cache.v : p.cache.k;
@@ -138,7 +146,8 @@ __global__ void __launch_bounds__(QK_THREADS) qk_norm_rope_kernel(const QkNormRo
 
 constexpr int SEL_THREADS = 1024;
 constexpr int SEL_BLOCK = 32 * SEL_THREADS;   // tokens of one block of the placing pass
-constexpr int SEL_CACHE = 49152;              // keys a CTA holds in shared memory (192 KB)
+constexpr int SEL_CACHE = 49152;              // weights a CTA holds in shared memory (192 KB)
+constexpr int SEL_RANKS = 8;                  // CTAs of a cluster, at most
 constexpr int SEL_PER_CTA = 8192;             // tokens per CTA from which the cluster grows
 constexpr int BINS = 2048;
 
@@ -170,26 +179,34 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t *sums) {
     return v + (warp ? before : 0u);
 }
 
-__device__ __forceinline__ uint32_t ld_cluster(const uint32_t *p, uint32_t rank) {
-    uint32_t v;
-    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(mapa_shared(smem_u32(p), rank)) : "memory");
+// The pair of words at this shared-memory place in CTA `rank` of the cluster.
+__device__ __forceinline__ uint2 ld_cluster2(const uint32_t *p, uint32_t rank) {
+    uint2 v;
+    asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];"
+                 : "=r"(v.x), "=r"(v.y)
+                 : "r"(mapa_shared(smem_u32(p), rank))
+                 : "memory");
     return v;
 }
 
-// One cluster of 1 to 8 CTAs per sequence, each with a contiguous part of its tokens, whose keys it
-// holds in shared memory (what does not fit is read again).  The budget-th largest key of the
-// unprotected tokens is found in three digits (11, 11 and 10 bits): a histogram of the tokens that
-// match the digits so far, summed over the cluster, scanned from the top by all threads.  Then the
-// tokens are counted in order and each kept one is written to its place.  What bounds it is the chain of these
-// steps (a few microseconds), not the 4 bytes per token.
+// One cluster of 1 to 8 CTAs per sequence, each with a contiguous part of its tokens, whose weights
+// it holds in shared memory (what does not fit is read again).  The budget-th largest key of the
+// unprotected tokens is found in up to three digits (11, 11 and 10 bits): a histogram of the tokens that
+// match the digits so far, summed over the cluster, scanned from the top by all threads; it ends
+// early when the digit's whole bin is kept, which two digits almost always reach unless weights are equal.
+// Then the tokens are counted in order and each kept one is written to its place.  What bounds it is
+// the chain of these steps (some microseconds), not the 4 bytes per token.
 template <bool CLUSTER>
 __global__ void __launch_bounds__(SEL_THREADS, 1) evict_select_kernel(const CacheEvict p, int cached) {
-    extern __shared__ uint32_t keys[];            // [cached]
-    __shared__ uint32_t hist[3][BINS];
-    __shared__ uint32_t sums[32], s_digit, s_need, s_count[2];
+    extern __shared__ float held[];               // [cached] weights
+    __shared__ __align__(8) uint32_t hist[3][BINS];
+    __shared__ __align__(8) uint32_t s_count[2];
+    __shared__ uint32_t sums[32], s_digit, s_need, s_full;
     pdl_trigger();
-    pdl_wait();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    for (int i = tid; i < 3 * BINS; i += SEL_THREADS) hist[i / BINS][i % BINS] = 0;
+    if (tid < 2) s_count[tid] = 0;
+    pdl_wait();
     const uint32_t rank = CLUSTER ? cluster_ctarank() : 0u;
     const int ranks = CLUSTER ? (int)gridDim.x : 1, b = blockIdx.y;
     int len = p.seq_lens[b];
@@ -204,85 +221,99 @@ __global__ void __launch_bounds__(SEL_THREADS, 1) evict_select_kernel(const Cach
     const bool all = len <= p.budget;
     const uint32_t wanted = all ? 0u : (uint32_t)(p.budget - p.sink - p.recent);   // of the candidates
     uint32_t prefix = 0, need = wanted;
-    const auto key_of = [&](int i) { return i < cached ? keys[i] : weight_key(w[i]); };
-    if (wanted) {
-        for (int i = tid; i < 3 * BINS; i += SEL_THREADS) hist[i / BINS][i % BINS] = 0;
+    int cut = 0;   // keys are compared without their lowest `cut` bits
+    #pragma unroll 4
+    for (int i = tid; i < min(n, cached); i += SEL_THREADS) held[i] = w[i];
+    const auto weight_of = [&](int i) { return i < cached ? held[i] : w[i]; };
+    __syncthreads();
+    for (int pass = 0; pass < 3 && wanted; ++pass) {
+        const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0), bits = pass == 2 ? 10 : 11;
+        const uint32_t mask = (1u << bits) - 1, high = pass == 0 ? 0u : 0xffffffffu << (shift + bits);
+        uint32_t *h = hist[pass];
         #pragma unroll 4
-        for (int i = tid; i < min(n, cached); i += SEL_THREADS) keys[i] = weight_key(w[i]);
-        __syncthreads();
-        #pragma unroll
-        for (int pass = 0; pass < 3; ++pass) {
-            const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0), bits = pass == 2 ? 10 : 11;
-            uint32_t *h = hist[pass];
-            for (int i = max(first, 0) + tid; i < min(last, n); i += SEL_THREADS) {
-                const uint32_t k = key_of(i);
-                if (pass == 0 || (k >> (shift + bits)) == (prefix >> (shift + bits)))
-                    atomicAdd(&h[(k >> shift) & ((1u << bits) - 1)], 1u);
-            }
-            if (CLUSTER) cluster_sync();
-            else __syncthreads();
-            // thread t: the bins 2047 - 2t and 2046 - 2t, so that the scan runs from the largest down
-            uint32_t c0 = 0, c1 = 0;
-            const int top = BINS - 1 - 2 * tid;
-            if (CLUSTER) {
-                for (int r = 0; r < ranks; ++r) {
-                    c0 += ld_cluster(h + top, r);
-                    c1 += ld_cluster(h + top - 1, r);
-                }
-            } else {
-                c0 = h[top];
-                c1 = h[top - 1];
-            }
-            const uint32_t upto = block_scan(c0 + c1, sums), before = upto - c0 - c1;
-            if (before < need && need <= upto) {   // exactly one thread
-                const bool in0 = need <= before + c0;
-                s_digit = in0 ? top : top - 1;
-                s_need = need - before - (in0 ? 0u : c0);
-            }
-            __syncthreads();
-            prefix |= s_digit << shift;
-            need = s_need;   // of the tokens that match the digits so far, this many are kept
+        for (int i = max(first, 0) + tid; i < min(last, n); i += SEL_THREADS) {
+            const uint32_t k = weight_key(weight_of(i));
+            if (((k ^ prefix) & high) == 0) atomicAdd(&h[(k >> shift) & mask], 1u);
         }
+        if (CLUSTER) cluster_sync();
+        else __syncthreads();
+        // thread t: the bins 2047 - 2t and 2046 - 2t, so that the scan runs from the largest down
+        const int low = BINS - 2 - 2 * tid;
+        uint2 c = make_uint2(0, 0);
+        if constexpr (CLUSTER) {
+            uint2 v[SEL_RANKS];
+            #pragma unroll
+            for (int r = 0; r < SEL_RANKS; ++r) v[r] = r < ranks ? ld_cluster2(h + low, r) : make_uint2(0, 0);
+            #pragma unroll
+            for (int r = 0; r < SEL_RANKS; ++r) {
+                c.x += v[r].x;
+                c.y += v[r].y;
+            }
+        } else {
+            c = *reinterpret_cast<const uint2 *>(h + low);
+        }
+        const uint32_t upto = block_scan(c.x + c.y, sums), before = upto - c.x - c.y;
+        if (before < need && need <= upto) {   // exactly one thread
+            const bool in_high = need <= before + c.y;
+            s_digit = in_high ? low + 1 : low;
+            s_need = need - before - (in_high ? 0u : c.y);
+            s_full = in_high ? c.y : c.x;
+        }
+        __syncthreads();
+        prefix |= s_digit << shift;
+        need = s_need;   // of the tokens that match the digits so far, this many are kept
+        cut = shift;
+        if (s_full == need) break;
     }
     // kept for certain: protected tokens and larger keys; of the equal ones the first `need`
-    const auto sort_of = [&](int i, bool &sure, bool &eq) {
+    const auto sort_of = [&](int i, float v, bool &sure, bool &eq) {
         sure = all || i < first || i >= last;
         eq = false;
         if (!sure && wanted) {
-            const uint32_t k = key_of(i);
-            sure = k > prefix;
-            eq = k == prefix;
+            const uint32_t k = weight_key(v) >> cut;
+            sure = k > prefix >> cut;
+            eq = k == prefix >> cut;
         }
     };
     uint32_t base_sure = 0, base_eq = 0;   // of the tokens before this CTA's (before this block's)
     if constexpr (CLUSTER) {
         uint32_t cs = 0, ce = 0;
+        #pragma unroll 4
         for (int i = tid; i < n; i += SEL_THREADS) {
             bool sure, eq;
-            sort_of(i, sure, eq);
+            sort_of(i, weight_of(i), sure, eq);
             cs += sure;
             ce += eq;
         }
-        cs = block_scan(cs, sums);
-        if (tid == SEL_THREADS - 1) s_count[0] = cs;
-        ce = block_scan(ce, sums);
-        if (tid == SEL_THREADS - 1) s_count[1] = ce;
+        cs = __reduce_add_sync(0xffffffffu, cs);
+        ce = __reduce_add_sync(0xffffffffu, ce);
+        if (lane == 0) {
+            atomicAdd(&s_count[0], cs);
+            atomicAdd(&s_count[1], ce);
+        }
         cluster_sync();
-        for (uint32_t r = 0; r < rank; ++r) {
-            base_sure += ld_cluster(s_count, r);
-            base_eq += ld_cluster(s_count + 1, r);
+        uint2 v[SEL_RANKS];
+        #pragma unroll
+        for (int r = 0; r < SEL_RANKS; ++r) v[r] = r < (int)rank ? ld_cluster2(s_count, r) : make_uint2(0, 0);
+        #pragma unroll
+        for (int r = 0; r < SEL_RANKS; ++r) {
+            base_sure += v[r].x;
+            base_eq += v[r].y;
         }
     }
     int32_t *kept = p.kept + b * p.ld_kept;
     float *wo = p.weight_out + b * p.ld_weight_out;
-    uint32_t *counts = hist[0];   // [32 rows of 1024 tokens][32 warps], both counts in one word (each <= 32768)
+    // counts in hist[0] (its last readers in the cluster are behind a barrier): [32 rows of 1024
+    // tokens][32 warps], both counts in one word (a block holds at most 32768 of each)
+    uint32_t *counts = hist[0];
     for (int i0 = 0; i0 < n; i0 += SEL_BLOCK) {
         const int rows = (min(n - i0, SEL_BLOCK) + SEL_THREADS - 1) / SEL_THREADS;
         __syncthreads();
+        #pragma unroll 4
         for (int r = 0; r < rows; ++r) {
             const int i = i0 + r * SEL_THREADS + tid;
             bool sure = false, eq = false;
-            if (i < n) sort_of(i, sure, eq);
+            if (i < n) sort_of(i, weight_of(i), sure, eq);
             const uint32_t ms = __ballot_sync(0xffffffffu, sure), me = __ballot_sync(0xffffffffu, eq);
             if (lane == 0) counts[r * 32 + warp] = (uint32_t)__popc(ms) << 16 | (uint32_t)__popc(me);
         }
@@ -292,10 +323,15 @@ __global__ void __launch_bounds__(SEL_THREADS, 1) evict_select_kernel(const Cach
         counts[tid] = inc - own;
         if (tid == SEL_THREADS - 1) s_need = inc;   // the block's total
         __syncthreads();
+        #pragma unroll 4
         for (int r = 0; r < rows; ++r) {
             const int i = i0 + r * SEL_THREADS + tid;
             bool sure = false, eq = false;
-            if (i < n) sort_of(i, sure, eq);
+            float v = 0.f;
+            if (i < n) {
+                v = weight_of(i);
+                sort_of(i, v, sure, eq);
+            }
             const uint32_t ms = __ballot_sync(0xffffffffu, sure), me = __ballot_sync(0xffffffffu, eq);
             const uint32_t below = (1u << lane) - 1, at = counts[r * 32 + warp];
             const uint32_t ns = base_sure + (at >> 16) + __popc(ms & below);
@@ -303,7 +339,7 @@ __global__ void __launch_bounds__(SEL_THREADS, 1) evict_select_kernel(const Cach
             if (sure || (eq && ne < need)) {
                 const uint32_t to = ns + min(ne, need);
                 kept[to] = begin + i;
-                wo[to] = w[i];
+                wo[to] = v;
             }
         }
         base_sure += s_need >> 16;
@@ -409,15 +445,17 @@ cudaError_t launch_select(const CacheEvict &p, int ranks, cudaStream_t st) {
 
 cudaError_t launch_qk_norm_rope(const QkNormRope &p, cudaStream_t st) {
     if (p.T <= 0) return cudaSuccess;
-    const int per = QK_THREADS / (p.d / 8), groups = (p.nq + 2 * p.nkv + per - 1) / per;
-    // few rows: the heads of a row over several CTAs
-    const int sms = device_num_sms();
-    int gy = 1;
-    if (p.T < 2 * sms) gy = (2 * sms + p.T - 1) / p.T;
-    if (gy > groups) gy = groups;
+    const int groups = QK_THREADS / (p.d / 8), heads = p.nq + 2 * p.nkv;
+    int gshift = 0;   // groups of a row: a power of two up to a whole CTA's
+    while ((1 << gshift) < groups && (1 << gshift) < heads) ++gshift;
+    const int per_cta = groups >> gshift, rows = (p.T + per_cta - 1) / per_cta;
+    // few rows: the turns of a row's heads over several CTAs
+    const int turns = (heads + (1 << gshift) - 1) >> gshift, sms = device_num_sms();
+    int gy = rows < 4 * sms ? (4 * sms + rows - 1) / rows : 1;
+    if (gy > turns) gy = turns;
     cudaLaunchAttribute at[1];
-    cudaLaunchConfig_t cfg = pdl_config(dim3(p.T, gy), dim3(QK_THREADS), 0, st, at);
-    return cudaLaunchKernelEx(&cfg, p.d == 128 ? qk_norm_rope_kernel<128> : qk_norm_rope_kernel<64>, p);
+    cudaLaunchConfig_t cfg = pdl_config(dim3(rows, gy), dim3(QK_THREADS), 0, st, at);
+    return cudaLaunchKernelEx(&cfg, p.d == 128 ? qk_norm_rope_kernel<128> : qk_norm_rope_kernel<64>, p, gshift);
 }
 
 cudaError_t launch_cache_evict(const CacheEvict &p, cudaStream_t st) {
