@@ -45,15 +45,17 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
 }
 
 constexpr int QK_THREADS = 256;
-constexpr int QK_BATCH = 5;   // head vectors a lane group loads before it works on the first (64 + 2 x 8 heads of 128: all)
 
-// D / 8 lanes (a group) per head vector, eight elements (16 bytes) each; lane l and lane l ^ (D/16)
-// hold the two halves of a rotation pair.  Each row has 1 << gshift groups of a CTA, which take its heads in
-// turn (blockIdx.y: every gridDim.y-th turn), so the row's rotary factors stay in registers; a CTA takes as many
-// rows as it has groups for.
-template <int D>
+// D / 16 lanes (a group) per head vector; lane l holds the elements 8l .. 8l + 7 of both halves, so
+// that a rotation pair never leaves its lane.  Each row has 1 << gshift groups of a CTA, which take
+// its heads in turn (blockIdx.y: every gridDim.y-th turn), so the row's rotary factors stay in
+// registers; a CTA takes as many rows as it has groups for.  BATCH: head vectors a group loads before it works on
+// the first; 3 where a group has several turns (8192 rows of 80 heads of 128: 61.7 us = 5.8 TB/s, with
+// 1, 2 and 5: 71.8, 65.3 and 64.9), else 1 (4595 rows of 8 heads of 64: 3.5 us, with 3: 4.2).  Bound by the
+// bytes, closely followed by the issue of instructions: 8 bytes per lane and shuffled rotation partners took 93 us.
+template <int D, int BATCH>
 __global__ void __launch_bounds__(QK_THREADS) qk_norm_rope_kernel(const QkNormRope p, int gshift) {
-    constexpr int LANES = D / 8, GROUPS = QK_THREADS / LANES;
+    constexpr int LANES = D / 16, GROUPS = QK_THREADS / LANES;
     pdl_trigger();
     pdl_wait();
     const int lane = threadIdx.x % LANES, group = threadIdx.x / LANES;
@@ -63,67 +65,84 @@ __global__ void __launch_bounds__(QK_THREADS) qk_norm_rope_kernel(const QkNormRo
     const int step = gridDim.y << gshift;
     const int first = (blockIdx.y << gshift) + (group & ((1 << gshift) - 1));
     const bf16 *src = p.qkv + t * p.ld_qkv + 8 * lane;
-    const int j0 = (8 * lane) % (D / 2);
-    const bool upper = lane >= LANES / 2;
     float cs[8], sn[8];
     int slot = -1;
     const bool rotate = p.cos_t != nullptr;
     // the same number of turns for every lane of a warp (the shuffles below need them all)
-    for (int h0 = 0; h0 < p.nq + 2 * p.nkv; h0 += QK_BATCH * step) {
-        uint4 raw[QK_BATCH];
+    for (int h0 = 0; h0 < p.nq + 2 * p.nkv; h0 += BATCH * step) {
+        uint4 raw[BATCH][2];
         #pragma unroll
-        for (int u = 0; u < QK_BATCH; ++u) {
+        for (int u = 0; u < BATCH; ++u) {
             const int h = h0 + first + u * step;
-            raw[u] = h < heads ? *reinterpret_cast<const uint4 *>(src + (long long)h * D) : make_uint4(0, 0, 0, 0);
+            raw[u][0] = raw[u][1] = make_uint4(0, 0, 0, 0);
+            if (h < heads) {
+                const uint4 *v = reinterpret_cast<const uint4 *>(src + (long long)h * D);
+                raw[u][0] = v[0];
+                raw[u][1] = v[D / 16];
+            }
         }
         if (h0 == 0) {   // behind the first loads: what the row's heads share
             if (p.has_cache && row) slot = p.slots[t];
             if (rotate && row) {
                 #pragma unroll
                 for (int i = 0; i < 8; i += 4) {
-                    const long long at = p.cs_rows ? ((long long)((j0 + i) / 4) * p.cs_rows + t) * 4
-                                                   : (long long)t * (D / 2) + j0 + i;
+                    const long long at = p.cs_rows ? ((long long)(2 * lane + i / 4) * p.cs_rows + t) * 4
+                                                   : (long long)t * (D / 2) + 8 * lane + i;
                     *reinterpret_cast<float4 *>(cs + i) = *reinterpret_cast<const float4 *>(p.cos_t + at);
                     *reinterpret_cast<float4 *>(sn + i) = *reinterpret_cast<const float4 *>(p.sin_t + at);
                 }
-                #pragma unroll
-                for (int i = 0; i < 8; ++i) sn[i] = upper ? sn[i] : -sn[i];   // y = x cos + partner * (-+ sin)
             }
         }
         #pragma unroll
-        for (int u = 0; u < QK_BATCH; ++u) {
+        for (int u = 0; u < BATCH; ++u) {
             const int h = h0 + first + u * step;
             const bool in = h < heads, is_q = h < p.nq, is_v = h >= p.nq + p.nkv;
-            float x[8];
-            unpack8(raw[u], x);
+            float x[8], y[8];
+            unpack8(raw[u][0], x);
+            unpack8(raw[u][1], y);
             const bf16 *w = is_q ? p.wq : p.wk;
             float ss = 0.f;
             #pragma unroll
-            for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
+            for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], fmaf(y[i], y[i], ss));
             #pragma unroll
             for (int o = LANES / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-            if (in && !is_v && w) {
-                const float r = 1.0f / sqrtf(ss / (float)D + p.eps);
-                float g[8];
-                unpack8(*reinterpret_cast<const uint4 *>(w + 8 * lane), g);
-                #pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] = x[i] * r * g[i];
-            }
-            if (rotate) {
-                #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float y = __shfl_xor_sync(0xffffffffu, x[i], LANES / 2);
-                    if (in && !is_v) x[i] = fmaf(x[i], cs[i], y * sn[i]);
-                }
-            }
             if (!in) continue;
+            if (!is_v) {
+                if (w) {
+                    const float r = rsqrtf(ss / (float)D + p.eps);   // within 2 ulp
+                    float g[8];
+                    unpack8(*reinterpret_cast<const uint4 *>(w + 8 * lane), g);
+                    #pragma unroll
+                    for (int i = 0; i < 8; ++i) x[i] *= r * g[i];
+                    unpack8(*reinterpret_cast<const uint4 *>(w + D / 2 + 8 * lane), g);
+                    #pragma unroll
+                    for (int i = 0; i < 8; ++i) y[i] *= r * g[i];
+                }
+                if (rotate) {
+                    #pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float a = x[i];
+                        x[i] = fmaf(a, cs[i], -(y[i] * sn[i]));
+                        y[i] = fmaf(y[i], cs[i], a * sn[i]);
+                    }
+                }
+                raw[u][0] = pack8(x);
+                raw[u][1] = pack8(y);
+            }
             if (is_q) {
-                if (p.q_out) *reinterpret_cast<uint4 *>(p.q_out + t * p.ld_q + (long long)h * D + 8 * lane) = pack8(x);
+                if (p.q_out) {
+                    uint4 *dst = reinterpret_cast<uint4 *>(p.q_out + t * p.ld_q + (long long)h * D + 8 * lane);
+                    dst[0] = raw[u][0];
+                    dst[D / 16] = raw[u][1];
+                }
                 continue;
             }
             const int g = is_v ? h - p.nq - p.nkv : h - p.nq;
-            if (!is_v && p.k_out)
-                *reinterpret_cast<uint4 *>(p.k_out + t * p.ld_k + (long long)g * D + 8 * lane) = pack8(x);
+            if (!is_v && p.k_out) {
+                uint4 *dst = reinterpret_cast<uint4 *>(p.k_out + t * p.ld_k + (long long)g * D + 8 * lane);
+                dst[0] = raw[u][0];
+                dst[D / 16] = raw[u][1];
+            }
             if (slot < 0) continue;
             const int page = slot >> p.cache.page_shift, place = slot & ((1 << p.cache.page_shift) - 1);
             if (page >= p.cache.num_pages) {
@@ -133,11 +152,16 @@ __global__ void __launch_bounds__(QK_THREADS) qk_norm_rope_kernel(const QkNormRo
             const long long at = page * p.cache.page_stride +
                                  ((long long)((g << p.cache.page_shift) + place)) * D + 8 * lane;
             void *dst = is_v ? p.cache.v : p.cache.k;
-            if (p.cache.f8)
-                *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(dst) + at) =
-                    quant8(x, (is_v ? p.cache.v_scale : p.cache.k_scale)[g]);
-            else
-                *reinterpret_cast<uint4 *>(static_cast<bf16 *>(dst) + at) = pack8(x);
+            if (p.cache.f8) {
+                const float scale = (is_v ? p.cache.v_scale : p.cache.k_scale)[g];
+                uint2 *out = reinterpret_cast<uint2 *>(static_cast<uint8_t *>(dst) + at);
+                out[0] = quant8(x, scale);
+                out[D / 16] = quant8(y, scale);
+            } else {
+                uint4 *out = reinterpret_cast<uint4 *>(static_cast<bf16 *>(dst) + at);
+                out[0] = raw[u][0];
+                out[D / 16] = raw[u][1];
+            }
         }
     }
 }
@@ -445,17 +469,24 @@ cudaError_t launch_select(const CacheEvict &p, int ranks, cudaStream_t st) {
 
 cudaError_t launch_qk_norm_rope(const QkNormRope &p, cudaStream_t st) {
     if (p.T <= 0) return cudaSuccess;
-    const int groups = QK_THREADS / (p.d / 8), heads = p.nq + 2 * p.nkv;
-    int gshift = 0;   // groups of a row: a power of two up to a whole CTA's
-    while ((1 << gshift) < groups && (1 << gshift) < heads) ++gshift;
+    // groups of a row: the power of two, up to a whole CTA's, that leaves the fewest of them idle in
+    // the last turn (the largest of such); for few rows the largest, as it has the fewest turns
+    const int groups = QK_THREADS / (p.d / 16), heads = p.nq + 2 * p.nkv, sms = device_num_sms();
+    int gshift = 0, waste = 0;
+    for (int g = 1; (1 << g) <= groups && (1 << (g - 1)) < heads; ++g) {
+        const int idle = ((heads + (1 << g) - 1) >> g << g) - heads;
+        if (idle <= waste || p.T < sms) gshift = g, waste = idle;
+    }
     const int per_cta = groups >> gshift, rows = (p.T + per_cta - 1) / per_cta;
     // few rows: the turns of a row's heads over several CTAs
-    const int turns = (heads + (1 << gshift) - 1) >> gshift, sms = device_num_sms();
+    const int turns = (heads + (1 << gshift) - 1) >> gshift;
     int gy = rows < 4 * sms ? (4 * sms + rows - 1) / rows : 1;
     if (gy > turns) gy = turns;
     cudaLaunchAttribute at[1];
     cudaLaunchConfig_t cfg = pdl_config(dim3(rows, gy), dim3(QK_THREADS), 0, st, at);
-    return cudaLaunchKernelEx(&cfg, p.d == 128 ? qk_norm_rope_kernel<128> : qk_norm_rope_kernel<64>, p, gshift);
+    if (turns > gy)
+        return cudaLaunchKernelEx(&cfg, p.d == 128 ? qk_norm_rope_kernel<128, 3> : qk_norm_rope_kernel<64, 3>, p, gshift);
+    return cudaLaunchKernelEx(&cfg, p.d == 128 ? qk_norm_rope_kernel<128, 1> : qk_norm_rope_kernel<64, 1>, p, gshift);
 }
 
 cudaError_t launch_cache_evict(const CacheEvict &p, cudaStream_t st) {
