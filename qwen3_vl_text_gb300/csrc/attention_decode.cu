@@ -7,16 +7,16 @@
 // What bounds it: every cached byte is read once, and the q heads of a kv head (nq/nkv of them) do
 // 2 flops each per byte pair: 8 flops a byte with 8 heads over bf16, far below the tensor cores'
 // rate, so the bound is the memory's.  Hence:
-//  * The keys of all (sequence, kv head) segments are laid end to end in tiles of 64 and cut into one
+//  * The keys of all (sequence, kv head) segments are laid end to end in tiles of 64 (e4m3: 128) and cut into one
 //    equal run of tiles per CTA, one CTA per SM, whatever the lengths are: a run may end inside a
 //    segment, whose parts are then joined (below).  Lengths are read on the device.
 //  * A producer warp keeps up to STAGES tiles of K and V in flight through TMA (a box per page,
-//    one lane per box, their page numbers looked up a batch ahead); eight warps compute.
+//    one lane per box, their page numbers looked up a batch ahead); eight or twelve warps compute.
 //  * The products run on mma.sync m16n8k16 with the q heads as the 16 rows: there are at most 16 rows
 //    of work per key, which a 128-row tcgen05 tile would leave mostly empty, and a warp that
 //    holds scores, weights and output in its own registers needs no exchange with other warps per tile.
-//    Each warp takes 16 keys of a tile with its own m, l and output; warps 0-3 take the even tiles of
-//    the run and 4-7 the odd ones, so that one half's softmax overlaps the other's loads.
+//    Each warp takes 16 (32) keys of a tile with its own m, l and output; groups of four warps take the
+//    tiles of the run in turn, so that their chains of product, softmax and product overlap.
 //  * With at most 8 heads the rows 8-15 of the weight matrix P would be padding: they carry
 //    P's rounding remainder p - bf16(p) instead, so the value product loses nothing to the 8-bit mantissa
 //    at no cost (more than 8 heads: a second product).  e4m3 values are exact in f16, so that path
@@ -32,26 +32,29 @@ namespace h3 {
 
 namespace {
 
-constexpr int TK = 64;                  // keys per tile
-constexpr int CWARPS = 8;               // compute warps
-constexpr int AD_THREADS = (CWARPS + 1) * 32;
+constexpr int WK = 64;                  // keys per CTA of the weight sums; score rows are padded to it
 constexpr int MAX_CTAS = 1024;          // arrival counters at the head of the workspace
 constexpr int PART_ROWS = 16;           // heads of a segment
 
-template <int D, bool F8>
+template <int D, bool F8, bool WIDE>
 struct Shape {
+    // groups of four compute warps, which take the tiles of a run in turn
+    static constexpr int GROUPS = 2;
+    static constexpr int TK = F8 ? 128 : 64;                // keys per tile
+    static constexpr int KS = TK / 4, NT = KS / 8;          // keys of a warp, in column tiles of 8
+    static constexpr int CWARPS = 4 * GROUPS, THREADS = (CWARPS + 1) * 32;
     static constexpr int ROW = D * (F8 ? 1 : 2);            // bytes of a key
     static constexpr int BOX = ROW < 128 ? 64 : 128;        // bytes of a box row (= swizzle width)
     static constexpr int TILE = TK * ROW;                   // K or V of one tile
-    // even: a stage then always serves the same half of the warps, which sees each of its phases
-    static constexpr int STAGES = TILE >= 16384 ? 4 : (TILE >= 8192 ? 8 : 12);
-    static_assert(STAGES % 2 == 0, "stages alternate between the halves of the compute warps");
+    // a multiple of the groups: a stage then always serves the same group, which sees each of its phases
+    static constexpr int STAGES = TILE >= 16384 ? 4 : 8;
     static constexpr int LDO = D + 8;                       // padded row of the output exchange
     static constexpr int OFF_O = STAGES * 2 * TILE;
     static constexpr int OFF_ML = OFF_O + CWARPS * 8 * LDO * 4;
     static constexpr int OFF_PRE = OFF_ML + 2 * CWARPS * PART_ROWS * 4;
-    static constexpr int OFF_BAR = (OFF_PRE + (kMaxSeqs + 1) * 4 + 15) & ~15;
-    static constexpr int BYTES = OFF_BAR + 2 * STAGES * 8 + 64 + 1024;   // + alignment of the base
+    static constexpr int OFF_LEN = OFF_PRE + (kMaxSeqs + 1) * 4;
+    static constexpr int OFF_BAR = (OFF_LEN + kMaxSeqs * 4 + 15) & ~15;
+    static constexpr int BYTES = OFF_BAR + 2 * STAGES * 8 + 80 + 1024;   // + alignment of the base
 };
 
 struct Args {
@@ -129,63 +132,67 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t &hi, uint32_t 
         lo = pack_bf16x2(a - bf16_lo(hi), b - bf16_hi(hi));
     }
 }
-__device__ __forceinline__ void compute_sync() { asm volatile("bar.sync 1, %0;" ::"n"(CWARPS * 32) : "memory"); }
+template <int THREADS>
+__device__ __forceinline__ void compute_sync() {
+    asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory");
+}
 
 // Byte offset of 16-byte chunk c of row r in a tile of swizzled box rows.
 template <int D, bool F8>
 __device__ __forceinline__ uint32_t chunk_at(int r, int c) {
-    using S = Shape<D, F8>;
-    if constexpr (S::BOX == 128) return (c >> 3) * (TK * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+    constexpr int TK = Shape<D, F8, false>::TK;
+    if constexpr (Shape<D, F8, false>::BOX == 128) return (c >> 3) * (TK * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
     else return r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
 }
 
-// Walks the tiles of a run: segment (b, u) with u = kv head * chunks + chunk, tile j of it.
+// Walks the tiles (of TK keys) of a run: segment (b, u) with u = kv head * chunks + chunk, tile j of it.
+template <int TK>
 struct Walk {
     int b, u, j, len, tiles;
-    __device__ __forceinline__ void start(int t, const int *pre, const int32_t *lens, int n_seqs, int max_len) {
-        int lo = 0, hi = n_seqs;   // the last b with pre[b] <= t that has tiles
+    __device__ __forceinline__ void start(int t, const int *pre, const int *lens, int n_seqs) {
+        int lo = 0, hi = n_seqs;   // the b with pre[b] <= t < pre[b + 1]
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
             if (pre[mid] <= t) lo = mid;
             else hi = mid;
         }
         b = lo;
-        load(lens, max_len);
+        load(lens);
         const int off = t - pre[b];
         u = off / tiles;
         j = off - u * tiles;
     }
-    __device__ __forceinline__ void load(const int32_t *lens, int max_len) {
-        len = min(max(lens[b], 0), max_len);
+    __device__ __forceinline__ void load(const int *lens) {
+        len = lens[b];
         tiles = (len + TK - 1) / TK;
     }
     // next segment (its tile 0); the caller knows that one follows
-    __device__ __forceinline__ void next(int units, const int32_t *lens, int max_len) {
+    __device__ __forceinline__ void next(int units, const int *lens) {
         j = 0;
         if (++u < units) return;
         u = 0;
         do {
             ++b;
-            load(lens, max_len);
+            load(lens);
         } while (tiles == 0);
     }
 };
 
 template <int D, bool F8, bool WIDE>   // WIDE: more than 8 heads in a segment
-__global__ void __launch_bounds__(AD_THREADS, 1) attention_decode_kernel(const __grid_constant__ CUtensorMap tmK,
-                                                                          const __grid_constant__ CUtensorMap tmV,
-                                                                          const Args a) {
-    using S = Shape<D, F8>;
-    constexpr int STAGES = S::STAGES;
+__global__ void __launch_bounds__(Shape<D, F8, WIDE>::THREADS, 1)
+    attention_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                            const Args a) {
+    using S = Shape<D, F8, WIDE>;
+    constexpr int STAGES = S::STAGES, CWARPS = S::CWARPS, TK = S::TK, NT = S::NT;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     float *sm_o = reinterpret_cast<float *>(smem + S::OFF_O);
     float *sm_m = reinterpret_cast<float *>(smem + S::OFF_ML), *sm_l = sm_m + CWARPS * PART_ROWS;
-    int *pre = reinterpret_cast<int *>(smem + S::OFF_PRE);
+    int *pre = reinterpret_cast<int *>(smem + S::OFF_PRE), *lens = reinterpret_cast<int *>(smem + S::OFF_LEN);
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + S::OFF_BAR), *empty = full + STAGES;
     volatile int *abort = reinterpret_cast<volatile int *>(empty + STAGES);
     int *s_last = const_cast<int *>(abort) + 1;
-    int *s_warp = s_last + 1;   // [9] scan of the warps' sums
+    int *s_warp = s_last + 1;   // [CWARPS + 1] scan of the warps' sums
 
     const AttentionDecode &p = a.p;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -197,7 +204,7 @@ __global__ void __launch_bounds__(AD_THREADS, 1) attention_decode_kernel(const _
         prefetch_tmap(&tmV);
         for (int i = 0; i < STAGES; ++i) {
             mbar_init(full + i, 1);
-            mbar_init(empty + i, CWARPS / 2);
+            mbar_init(empty + i, 4);
         }
         *abort = 0;
         fence_barrier_init();
@@ -213,6 +220,7 @@ __global__ void __launch_bounds__(AD_THREADS, 1) attention_decode_kernel(const _
             n[i] = 0;
             if (b < p.n_seqs) {
                 const int len = p.seq_lens[b], c = min(max(len, 0), p.max_len);
+                lens[b] = c;
                 if (len != c && blockIdx.x == 0) report(p.status, ST_BOUNDS);
                 n[i] = (c + TK - 1) / TK * units;
             }
@@ -242,13 +250,13 @@ __global__ void __launch_bounds__(AD_THREADS, 1) attention_decode_kernel(const _
     // sequences without tokens: zero rows
     for (int b = blockIdx.x; b < p.n_seqs; b += gridDim.x)
         if (pre[b + 1] == pre[b])
-            for (int i = tid; i < p.nq * D / 8; i += AD_THREADS)
+            for (int i = tid; i < p.nq * D / 8; i += S::THREADS)
                 *reinterpret_cast<uint4 *>(p.o + b * p.ld_o + 8 * i) = make_uint4(0, 0, 0, 0);
     if ((long long)blockIdx.x >= G) return;
     const int t0 = (int)(blockIdx.x * T / G), t1 = (int)((blockIdx.x + 1) * T / G);
 
-    Walk w;
-    w.start(t0, pre, p.seq_lens, p.n_seqs, p.max_len);
+    Walk<TK> w;
+    w.start(t0, pre, lens, p.n_seqs);
 
     if (warp == CWARPS) {
         // ------------------------------------------------ producer
@@ -262,8 +270,8 @@ __global__ void __launch_bounds__(AD_THREADS, 1) attention_decode_kernel(const _
         const auto look_up = [&](int t) {
             Box x{0, 0, 0, 0};
             if (t >= t1) return x;
-            Walk v;
-            v.start(t, pre, p.seq_lens, p.n_seqs, p.max_len);
+            Walk<TK> v;
+            v.start(t, pre, lens, p.n_seqs);
             const int key = v.j * TK + lane % boxes * a.box_rows;
             x.n = min(boxes, (v.len - v.j * TK + a.box_rows - 1) / a.box_rows);
             x.head = v.u / a.chunks;
@@ -320,12 +328,12 @@ __global__ void __launch_bounds__(AD_THREADS, 1) attention_decode_kernel(const _
     // ---------------------------------------------------- compute warps
     const int g = lane >> 2, tq = lane & 3;   // fragment row and column pair
     const float base_scale = 1.4426950408889634f / sqrtf((float)D);
-    const int half = warp >> 2, slice = (warp & 3) * 16;
+    const int group = warp >> 2, slice = (warp & 3) * S::KS;
     // this lane's row and 16-byte chunk in the ldmatrix of 16 keys: K (keys 0-7 / 8-15 as the column
     // tiles) and V (transposed, as the two halves of the contraction); e4m3 rows pair them the other way
     const int row_v = (lane & 7) + ((lane >> 3) & 1) * 8, chunk_v = lane >> 4;
     const int row_k = F8 ? row_v : (lane & 7) + (lane >> 4) * 8, chunk_k = F8 ? chunk_v : (lane >> 3) & 1;
-    int stage = 0, round = 0, parity = 0;
+    int stage = 0, round = 0, turn = 0;   // turn: the group whose tile this is
 
     for (int t = t0; t < t1;) {
         const int seg = t - w.j, seg_end = seg + w.tiles;   // this segment's tiles in the whole row of tiles
@@ -386,8 +394,8 @@ __global__ void __launch_bounds__(AD_THREADS, 1) attention_decode_kernel(const _
             for (int k = 0; k < 4; ++k) o[i][k] = 0.f;
         float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
 
-        for (; w.j < j1; ++w.j, ++t, parity ^= 1) {
-            if (parity == half) {
+        for (; w.j < j1; ++w.j, ++t, turn = turn + 1 == S::GROUPS ? 0 : turn + 1) {
+            if (turn == group) {
                 if (!mbar_wait(full + stage, round & 1, abort)) {
                     // give up on the data, keep the control flow (barriers, counters) to the end
                     if (lane == 0) {
@@ -399,48 +407,57 @@ __global__ void __launch_bounds__(AD_THREADS, 1) attention_decode_kernel(const _
                 const int key0 = w.j * TK + slice;
                 if (key0 < w.len) {
                     const uint32_t kt = smem_u32(smem + stage * 2 * S::TILE), vt = kt + S::TILE;
-                    float s[2][4] = {};
+                    float s[NT][4] = {};
                     if constexpr (F8) {
                         #pragma unroll
-                        for (int k = 0; k < D / 16; k += 2) {
-                            uint32_t r[4];   // (keys 0-7, 8-15) x (step k, k + 1)
-                            ldsm4(r, kt + chunk_at<D, F8>(slice + row_k, k + chunk_k));
+                        for (int k = 0; k < D / 16; k += 2)
                             #pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                mma<F8>(s[i & 1], qa[k + i / 2][0], WIDE ? qa[k + i / 2][WIDE ? 2 : 0] : 0u, qa[k + i / 2][1],
-                                        WIDE ? qa[k + i / 2][WIDE ? 3 : 0] : 0u, e4m3x2_f16x2(r[i]),
-                                        e4m3x2_f16x2(r[i] >> 16));
-                        }
+                            for (int n = 0; n < NT; n += 2) {
+                                uint32_t r[4];   // (keys 0-7, 8-15) x (step k, k + 1)
+                                ldsm4(r, kt + chunk_at<D, F8>(slice + 8 * n + row_k, k + chunk_k));
+                                #pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    mma<F8>(s[n + (i & 1)], qa[k + i / 2][0], WIDE ? qa[k + i / 2][WIDE ? 2 : 0] : 0u,
+                                            qa[k + i / 2][1], WIDE ? qa[k + i / 2][WIDE ? 3 : 0] : 0u,
+                                            e4m3x2_f16x2(r[i]), e4m3x2_f16x2(r[i] >> 16));
+                            }
                     } else {
+                        float s2[NT][4] = {};   // even and odd steps: two chains of products per key tile
                         #pragma unroll
-                        for (int k = 0; k < D / 16; ++k) {
-                            uint32_t r[4];
-                            ldsm4(r, kt + chunk_at<D, F8>(slice + row_k, 2 * k + chunk_k));
+                        for (int k = 0; k < D / 16; ++k)
                             #pragma unroll
-                            for (int i = 0; i < 2; ++i)
-                                mma<F8>(s[i], qa[k][0], WIDE ? qa[k][WIDE ? 2 : 0] : 0u, qa[k][1],
-                                        WIDE ? qa[k][WIDE ? 3 : 0] : 0u, r[2 * i], r[2 * i + 1]);
-                        }
+                            for (int n = 0; n < NT; n += 2) {
+                                uint32_t r[4];
+                                ldsm4(r, kt + chunk_at<D, F8>(slice + 8 * n + row_k, 2 * k + chunk_k));
+                                #pragma unroll
+                                for (int i = 0; i < 2; ++i)
+                                    mma<F8>(k & 1 ? s2[n + i] : s[n + i], qa[k][0], WIDE ? qa[k][WIDE ? 2 : 0] : 0u, qa[k][1],
+                                            WIDE ? qa[k][WIDE ? 3 : 0] : 0u, r[2 * i], r[2 * i + 1]);
+                            }
+                        #pragma unroll
+                        for (int n = 0; n < NT; ++n)
+                            #pragma unroll
+                            for (int k = 0; k < 4; ++k) s[n][k] += s2[n][k];
                     }
-                    const bool tail = key0 + 16 > w.len;
+                    const bool tail = key0 + S::KS > w.len;
                     float x0 = -INFINITY, x1 = -INFINITY;
                     #pragma unroll
-                    for (int i = 0; i < 2; ++i)
+                    for (int n = 0; n < NT; ++n)
                         #pragma unroll
                         for (int k = 0; k < 2; ++k) {
-                            s[i][k] *= scale0;
-                            if (WIDE) s[i][2 + k] *= scale1;
-                            if (tail && key0 + 8 * i + 2 * tq + k >= w.len) s[i][k] = s[i][2 + k] = -INFINITY;
-                            x0 = fmaxf(x0, s[i][k]);
-                            if (WIDE) x1 = fmaxf(x1, s[i][2 + k]);
+                            s[n][k] *= scale0;
+                            if (WIDE) s[n][2 + k] *= scale1;
+                            if (tail && key0 + 8 * n + 2 * tq + k >= w.len) s[n][k] = s[n][2 + k] = -INFINITY;
+                            x0 = fmaxf(x0, s[n][k]);
+                            if (WIDE) x1 = fmaxf(x1, s[n][2 + k]);
                         }
                     if (a.scores) {
                         #pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            float *dst = a.scores + ((long long)w.b * p.nq + h0 + g) * a.ld_scores + key0 + 8 * i + 2 * tq;
-                            if (g < rows) *reinterpret_cast<float2 *>(dst) = make_float2(s[i][0], s[i][1]);
+                        for (int n = 0; n < NT; ++n) {
+                            float *dst = a.scores + ((long long)w.b * p.nq + h0 + g) * a.ld_scores + key0 + 8 * n + 2 * tq;
+                            if (g < rows) *reinterpret_cast<float2 *>(dst) = make_float2(s[n][0], s[n][1]);
                             if (WIDE && g + 8 < rows)
-                                *reinterpret_cast<float2 *>(dst + 8 * a.ld_scores) = make_float2(s[i][2], s[i][3]);
+                                *reinterpret_cast<float2 *>(dst + 8 * a.ld_scores) = make_float2(s[n][2], s[n][3]);
                         }
                     }
                     x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 1));
@@ -471,58 +488,61 @@ __global__ void __launch_bounds__(AD_THREADS, 1) attention_decode_kernel(const _
                     }
                     const float z0 = m0 == -INFINITY ? 0.f : m0, z1 = m1 == -INFINITY ? 0.f : m1;
                     #pragma unroll
-                    for (int i = 0; i < 2; ++i)
+                    for (int n = 0; n < NT; ++n)
                         #pragma unroll
                         for (int k = 0; k < 2; ++k) {
-                            s[i][k] = ex2(s[i][k] - z0);
-                            l0 += s[i][k];
+                            s[n][k] = ex2(s[n][k] - z0);
+                            l0 += s[n][k];
                             if (WIDE) {
-                                s[i][2 + k] = ex2(s[i][2 + k] - z1);
-                                l1 += s[i][2 + k];
+                                s[n][2 + k] = ex2(s[n][2 + k] - z1);
+                                l1 += s[n][2 + k];
                             }
                         }
-                    uint32_t hi[4], lo[4];   // the A operand's four registers
-                    split2<F8>(s[0][0], s[0][1], hi[0], lo[0]);
-                    split2<F8>(s[1][0], s[1][1], hi[2], lo[2]);
-                    if (WIDE) {
-                        split2<F8>(s[0][2], s[0][3], hi[1], lo[1]);
-                        split2<F8>(s[1][2], s[1][3], hi[3], lo[3]);
-                    } else {
-                        hi[1] = lo[0];
-                        hi[3] = lo[2];
-                    }
-                    // values behind the sequence may be anything (0 * NaN): cleared in the last slice
-                    uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
-                    if (tail) {
-                        const int left = w.len - key0 - 2 * tq;
-                        keep0 = (left > 0 ? 0xffffu : 0u) | (left > 1 ? 0xffff0000u : 0u);
-                        keep1 = (left > 8 ? 0xffffu : 0u) | (left > 9 ? 0xffff0000u : 0u);
-                    }
                     #pragma unroll
-                    for (int c = 0; c < S::ROW / 16; c += 2) {
-                        uint32_t r[4];   // (keys 0-7, 8-15) x (chunk c, c + 1)
-                        ldsm4t(r, vt + chunk_at<D, F8>(slice + row_v, c + chunk_v));
+                    for (int y = 0; y < NT / 2; ++y) {   // 16 keys at a time
+                        uint32_t hi[4], lo[4];   // the A operand's four registers
+                        split2<F8>(s[2 * y][0], s[2 * y][1], hi[0], lo[0]);
+                        split2<F8>(s[2 * y + 1][0], s[2 * y + 1][1], hi[2], lo[2]);
+                        if (WIDE) {
+                            split2<F8>(s[2 * y][2], s[2 * y][3], hi[1], lo[1]);
+                            split2<F8>(s[2 * y + 1][2], s[2 * y + 1][3], hi[3], lo[3]);
+                        } else {
+                            hi[1] = lo[0];
+                            hi[3] = lo[2];
+                        }
+                        // values behind the sequence may be anything (0 * NaN): cleared in the last slice
+                        uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
                         if (tail) {
-                            r[0] &= keep0;
-                            r[1] &= keep1;
-                            r[2] &= keep0;
-                            r[3] &= keep1;
+                            const int left = w.len - key0 - 16 * y - 2 * tq;
+                            keep0 = (left > 0 ? 0xffffu : 0u) | (left > 1 ? 0xffff0000u : 0u);
+                            keep1 = (left > 8 ? 0xffffu : 0u) | (left > 9 ? 0xffff0000u : 0u);
                         }
                         #pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            if constexpr (F8) {
-                                // a lane holds columns 2n, 2n + 1 of two keys: even and odd columns as two tiles
-                                #pragma unroll
-                                for (int odd = 0; odd < 2; ++odd) {
-                                    const uint32_t sel = odd ? 0x31u : 0x20u;
-                                    const uint32_t b0 = e4m3x2_f16x2(__byte_perm(r[2 * i], 0u, sel));
-                                    const uint32_t b1 = e4m3x2_f16x2(__byte_perm(r[2 * i + 1], 0u, sel));
-                                    mma<F8>(o[2 * (c + i) + odd], hi[0], hi[1], hi[2], hi[3], b0, b1);
-                                    if (WIDE) mma<F8>(o[2 * (c + i) + odd], lo[0], lo[1], lo[2], lo[3], b0, b1);
+                        for (int c = 0; c < S::ROW / 16; c += 2) {
+                            uint32_t r[4];   // (keys 0-7, 8-15) x (chunk c, c + 1)
+                            ldsm4t(r, vt + chunk_at<D, F8>(slice + 16 * y + row_v, c + chunk_v));
+                            if (tail) {
+                                r[0] &= keep0;
+                                r[1] &= keep1;
+                                r[2] &= keep0;
+                                r[3] &= keep1;
+                            }
+                            #pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                if constexpr (F8) {
+                                    // a lane holds columns 2n, 2n + 1 of two keys: even and odd columns as two tiles
+                                    #pragma unroll
+                                    for (int odd = 0; odd < 2; ++odd) {
+                                        const uint32_t sel = odd ? 0x31u : 0x20u;
+                                        const uint32_t b0 = e4m3x2_f16x2(__byte_perm(r[2 * i], 0u, sel));
+                                        const uint32_t b1 = e4m3x2_f16x2(__byte_perm(r[2 * i + 1], 0u, sel));
+                                        mma<F8>(o[2 * (c + i) + odd], hi[0], hi[1], hi[2], hi[3], b0, b1);
+                                        if (WIDE) mma<F8>(o[2 * (c + i) + odd], lo[0], lo[1], lo[2], lo[3], b0, b1);
+                                    }
+                                } else {
+                                    mma<F8>(o[c + i], hi[0], hi[1], hi[2], hi[3], r[2 * i], r[2 * i + 1]);
+                                    if (WIDE) mma<F8>(o[c + i], lo[0], lo[1], lo[2], lo[3], r[2 * i], r[2 * i + 1]);
                                 }
-                            } else {
-                                mma<F8>(o[c + i], hi[0], hi[1], hi[2], hi[3], r[2 * i], r[2 * i + 1]);
-                                if (WIDE) mma<F8>(o[c + i], lo[0], lo[1], lo[2], lo[3], r[2 * i], r[2 * i + 1]);
                             }
                         }
                     }
@@ -546,7 +566,7 @@ __global__ void __launch_bounds__(AD_THREADS, 1) attention_decode_kernel(const _
             sm_m[warp * PART_ROWS + g + 8] = m1;
             sm_l[warp * PART_ROWS + g + 8] = l1;
         }
-        compute_sync();
+        compute_sync<CWARPS * 32>();
         const bool whole = seg >= t0 && seg_end <= t1;
         const float vs = F8 ? p.cache.v_scale[kvh] : 1.f;
         const int slot = 2 * blockIdx.x + (seg < t0 ? 0 : 1);
@@ -558,14 +578,18 @@ __global__ void __launch_bounds__(AD_THREADS, 1) attention_decode_kernel(const _
             for (int i = 0; i < CWARPS; ++i) top = fmaxf(top, sm_m[i * PART_ROWS + r8 + g]);
             const float mine = r8 ? m1 : m0, f = mine == -INFINITY ? 0.f : ex2(mine - top);
             float *dst = sm_o + (warp * 8 + g) * S::LDO;
+            const auto out = [&](int i, int k) { return (WIDE ? o[i][r8 / 4 + k] : o[i][k] + o[i][k + 2]) * f; };
             #pragma unroll
-            for (int i = 0; i < D / 8; ++i) {
-                const float a0 = WIDE ? o[i][r8 / 4] : o[i][0] + o[i][2], a1 = WIDE ? o[i][r8 / 4 + 1] : o[i][1] + o[i][3];
-                const int c0 = F8 ? 16 * (i / 2) + 4 * tq + (i & 1) : 8 * i + 2 * tq;
-                dst[c0] = a0 * f;
-                dst[c0 + (F8 ? 2 : 1)] = a1 * f;
+            for (int i = 0; i < D / 8; i += 2) {
+                if constexpr (F8) {   // even and odd columns of 16
+                    *reinterpret_cast<float4 *>(dst + 8 * i + 4 * tq) =
+                        make_float4(out(i, 0), out(i + 1, 0), out(i, 1), out(i + 1, 1));
+                } else {
+                    *reinterpret_cast<float2 *>(dst + 8 * i + 2 * tq) = make_float2(out(i, 0), out(i, 1));
+                    *reinterpret_cast<float2 *>(dst + 8 * i + 8 + 2 * tq) = make_float2(out(i + 1, 0), out(i + 1, 1));
+                }
             }
-            compute_sync();
+            compute_sync<CWARPS * 32>();
             if (trow < 8 && r8 + trow < rows) {
                 float mm = -INFINITY, ll = 0.f;
                 #pragma unroll
@@ -592,21 +616,20 @@ __global__ void __launch_bounds__(AD_THREADS, 1) attention_decode_kernel(const _
                     if (tcol == 0) a.ml[slot * PART_ROWS + r8 + trow] = make_float2(mm, ll);
                 }
             }
-            compute_sync();
+            compute_sync<CWARPS * 32>();
         }
         if (!whole) {
             // the CTA whose part arrives last joins the parts, in the order of the keys
             const int first = (int)((((long long)seg + 1) * G - 1) / T), last = (int)(((long long)seg_end * G - 1) / T);
-            __threadfence();
-            compute_sync();
+            // (the barrier at the end of the loop above orders all threads' parts before thread 0's release)
             if (tid == 0) {
-                const uint32_t before = atomicAdd(a.count + first, 1u);
+                uint32_t before;
+                asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(before) : "l"(a.count + first) : "memory");
                 *s_last = before == (uint32_t)(last - first);
                 if (*s_last) a.count[first] = 0u;   // for the next call
             }
-            compute_sync();
+            compute_sync<CWARPS * 32>();
             if (*s_last) {
-                __threadfence();
                 #pragma unroll
                 for (int r8 = 0; r8 < (WIDE ? 16 : 8); r8 += 8)
                     if (trow < 8 && r8 + trow < rows) {
@@ -634,7 +657,7 @@ __global__ void __launch_bounds__(AD_THREADS, 1) attention_decode_kernel(const _
                     }
             }
         }
-        if (t < t1) w.next(units, p.seq_lens, p.max_len);
+        if (t < t1) w.next(units, lens);
     }
 }
 
@@ -648,7 +671,7 @@ __global__ void __launch_bounds__(256) attention_weight_kernel(const AttentionDe
     __shared__ float2 part[8][32];
     pdl_trigger();
     pdl_wait();
-    const int b = blockIdx.y, i0 = blockIdx.x * TK, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int b = blockIdx.y, i0 = blockIdx.x * WK, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int len = min(max(p.seq_lens[b], 0), p.max_len);
     if (i0 >= len) return;
     const float *s = scores + (long long)b * p.nq * ld_scores + i0 + 2 * lane;   // scores are stored in whole slices of 16
@@ -666,7 +689,7 @@ __global__ void __launch_bounds__(256) attention_weight_kernel(const AttentionDe
     part[warp][lane] = acc;
     __syncthreads();
     const int i = i0 + threadIdx.x;
-    if (threadIdx.x < TK && i < len) {
+    if (threadIdx.x < WK && i < len) {
         float sum = 0.f;
         #pragma unroll
         for (int w = 0; w < 8; ++w) sum += reinterpret_cast<const float *>(part[w])[threadIdx.x];
@@ -686,7 +709,7 @@ Layout layout(int ctas, int n_seqs, int nq, int max_len, bool weights) {
     y.part = MAX_CTAS * sizeof(uint32_t);
     y.ml = y.part + (size_t)ctas * 2 * PART_ROWS * 128 * sizeof(float);
     y.stat = y.ml + up256((size_t)ctas * 2 * PART_ROWS * sizeof(float2));
-    y.ld_scores = (max_len + TK - 1) / TK * TK;
+    y.ld_scores = (max_len + WK - 1) / WK * WK;
     y.scores = y.stat + (weights ? up256((size_t)n_seqs * nq * sizeof(float2)) : 0);
     y.bytes = y.scores + (weights ? (size_t)n_seqs * nq * (size_t)y.ld_scores * sizeof(float) : 0);
     return y;
@@ -697,7 +720,7 @@ cudaError_t launch_kernel(const CUtensorMap &tk, const CUtensorMap &tv, const Ar
     static std::atomic<bool> ready[kMaxDevices];   // the shared-memory opt-in, per device
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
-    constexpr int bytes = Shape<D, F8>::BYTES;
+    constexpr int bytes = Shape<D, F8, WIDE>::BYTES;
     static_assert(bytes <= 232448, "shared memory of one CTA");
     if (!ready[dev].load()) {
         cudaError_t e = cudaFuncSetAttribute(attention_decode_kernel<D, F8, WIDE>,
@@ -706,7 +729,7 @@ cudaError_t launch_kernel(const CUtensorMap &tk, const CUtensorMap &tv, const Ar
         ready[dev].store(true);
     }
     cudaLaunchAttribute at[1];
-    cudaLaunchConfig_t cfg = pdl_config(dim3(grid), dim3(AD_THREADS), bytes, st, at);
+    cudaLaunchConfig_t cfg = pdl_config(dim3(grid), dim3(Shape<D, F8, WIDE>::THREADS), bytes, st, at);
     return cudaLaunchKernelEx(&cfg, attention_decode_kernel<D, F8, WIDE>, tk, tv, a);
 }
 
@@ -714,7 +737,7 @@ cudaError_t launch_kernel(const CUtensorMap &tk, const CUtensorMap &tv, const Ar
 
 size_t attention_decode_workspace_bytes(int num_sms, int n_seqs, int nq, int max_len, bool weights) {
     if (num_sms <= 0 || num_sms > MAX_CTAS || n_seqs < 0 || n_seqs > kMaxSeqs || nq < 1 || nq > 65536 || max_len < 0 ||
-        (long long)n_seqs * nq * (((long long)max_len + TK - 1) / TK) > INT_MAX)
+        (long long)n_seqs * nq * (((long long)max_len + 63) / 64) > INT_MAX)   // tiles of 64 or 128 keys
         return 0;
     return layout(num_sms, n_seqs, nq, max_len, weights).bytes;
 }
@@ -728,7 +751,7 @@ cudaError_t launch_attention_decode(const AttentionDecode &p, cudaStream_t st) {
     a.p = p;
     a.group = p.nq / p.cache.nkv;
     a.chunks = (a.group + PART_ROWS - 1) / PART_ROWS;
-    a.box_rows = std::min(TK, 1 << p.cache.page_shift);
+    a.box_rows = std::min(64, 1 << p.cache.page_shift);
     a.count = reinterpret_cast<uint32_t *>(ws);
     a.part = reinterpret_cast<float *>(ws + y.part);
     a.ml = reinterpret_cast<float2 *>(ws + y.ml);
@@ -741,7 +764,7 @@ cudaError_t launch_attention_decode(const AttentionDecode &p, cudaStream_t st) {
     if (!make_tmap_cache(&tk, p.cache, p.cache.k) || !make_tmap_cache(&tv, p.cache, p.cache.v))
         return cudaErrorInvalidValue;
     // one CTA per SM, fewer where the lengths cannot hold as many tiles
-    const long long most = (long long)p.n_seqs * p.cache.nkv * a.chunks * ((p.max_len + TK - 1) / TK);
+    const long long most = (long long)p.n_seqs * p.cache.nkv * a.chunks * ((p.max_len + (p.cache.f8 ? 127 : 63)) / (p.cache.f8 ? 128 : 64));
     const int grid = (int)std::min<long long>(sms, std::max<long long>(most, 1));
     cudaError_t e;
     if (p.cache.d == 128)
@@ -756,7 +779,7 @@ cudaError_t launch_attention_decode(const AttentionDecode &p, cudaStream_t st) {
                                       : launch_kernel<64, false, false>(tk, tv, a, grid, st));
     if (e != cudaSuccess || !p.weight_out || p.max_len == 0) return e;
     cudaLaunchAttribute at[1];
-    cudaLaunchConfig_t cfg = pdl_config(dim3((p.max_len + TK - 1) / TK, p.n_seqs), dim3(256), 0, st, at);
+    cudaLaunchConfig_t cfg = pdl_config(dim3((p.max_len + WK - 1) / WK, p.n_seqs), dim3(256), 0, st, at);
     return cudaLaunchKernelEx(&cfg, attention_weight_kernel, p, (const float *)a.scores, (const float2 *)a.stat, a.ld_scores);
 }
 
