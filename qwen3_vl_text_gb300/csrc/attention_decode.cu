@@ -53,15 +53,17 @@ struct Shape {
     static constexpr int OFF_ML = OFF_O + CWARPS * 8 * LDO * 4;
     static constexpr int OFF_PRE = OFF_ML + 2 * CWARPS * PART_ROWS * 4;
     static constexpr int OFF_LEN = OFF_PRE + (kMaxSeqs + 1) * 4;
-    static constexpr int OFF_BAR = (OFF_LEN + kMaxSeqs * 4 + 15) & ~15;
-    static constexpr int BYTES = OFF_BAR + 2 * STAGES * 8 + 80 + 1024;   // + alignment of the base
+    static constexpr int LDQ = 2 * D + 16;                  // padded row of q (bytes)
+    static constexpr int OFF_Q = (OFF_LEN + kMaxSeqs * 4 + 15) & ~15;
+    static constexpr int OFF_BAR = OFF_Q + 2 * PART_ROWS * LDQ;
+    static constexpr int BYTES = OFF_BAR + (2 * STAGES + 4) * 8 + 80 + 1024;   // + alignment of the base
 };
 
 struct Args {
     AttentionDecode p;
     int group;      // q heads per kv head
     int chunks;     // segments per kv head: ceil(group / 16)
-    int box_rows;   // places of a page one box covers
+    int box_shift;  // log2 of the places of a page one box covers
     float *part;    // [cta][2][16][D] partial outputs, unnormalised
     float2 *ml;     // [cta][2][16] their running maximum and sum
     uint32_t *count;
@@ -190,9 +192,10 @@ __global__ void __launch_bounds__(Shape<D, F8, WIDE>::THREADS, 1)
     float *sm_m = reinterpret_cast<float *>(smem + S::OFF_ML), *sm_l = sm_m + CWARPS * PART_ROWS;
     int *pre = reinterpret_cast<int *>(smem + S::OFF_PRE), *lens = reinterpret_cast<int *>(smem + S::OFF_LEN);
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + S::OFF_BAR), *empty = full + STAGES;
-    volatile int *abort = reinterpret_cast<volatile int *>(empty + STAGES);
-    int *s_last = const_cast<int *>(abort) + 1;
-    int *s_warp = s_last + 1;   // [CWARPS + 1] scan of the warps' sums
+    uint64_t *q_full = empty + STAGES, *q_empty = q_full + 2;
+    volatile int *abort = reinterpret_cast<volatile int *>(q_empty + 2);
+    int *s_last = const_cast<int *>(abort) + 1;   // [2]
+    int *s_warp = s_last + 2;   // [CWARPS + 1] scan of the warps' sums
 
     const AttentionDecode &p = a.p;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -205,6 +208,10 @@ __global__ void __launch_bounds__(Shape<D, F8, WIDE>::THREADS, 1)
         for (int i = 0; i < STAGES; ++i) {
             mbar_init(full + i, 1);
             mbar_init(empty + i, 4);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(q_full + i, 1);
+            mbar_init(q_empty + i, CWARPS);
         }
         *abort = 0;
         fence_barrier_init();
@@ -244,16 +251,21 @@ __global__ void __launch_bounds__(Shape<D, F8, WIDE>::THREADS, 1)
         }
         __syncthreads();
     }
-    const long long T = pre[p.n_seqs];
-    const long long G = T < (long long)gridDim.x ? T : (long long)gridDim.x;   // CTAs that have a run
-
+    // the run of CTA c: T / G tiles, one more for the first T % G
+    const unsigned T = (unsigned)pre[p.n_seqs], G = min(T, gridDim.x);   // CTAs that have a run
     // sequences without tokens: zero rows
     for (int b = blockIdx.x; b < p.n_seqs; b += gridDim.x)
         if (pre[b + 1] == pre[b])
             for (int i = tid; i < p.nq * D / 8; i += S::THREADS)
                 *reinterpret_cast<uint4 *>(p.o + b * p.ld_o + 8 * i) = make_uint4(0, 0, 0, 0);
-    if ((long long)blockIdx.x >= G) return;
-    const int t0 = (int)(blockIdx.x * T / G), t1 = (int)((blockIdx.x + 1) * T / G);
+    if (blockIdx.x >= G) return;
+    const unsigned run = T / G, longer = T - run * G;
+    const int t0 = (int)(blockIdx.x * run + min(blockIdx.x, longer)), t1 = t0 + (int)(run + (blockIdx.x < longer));
+    const auto owner = [&](int t) {   // the CTA whose run holds tile t
+        const unsigned split = longer * (run + 1);
+        return (int)((unsigned)t < split ? (unsigned)t / (run + 1) : longer + ((unsigned)t - split) / run);
+    };
+    const auto kv_head = [&](int u) { return a.chunks == 1 ? u : u / a.chunks; };
 
     Walk<TK> w;
     w.start(t0, pre, lens, p.n_seqs);
@@ -262,37 +274,57 @@ __global__ void __launch_bounds__(Shape<D, F8, WIDE>::THREADS, 1)
         // ------------------------------------------------ producer
         // A batch of 32 boxes, one per lane, is looked up while the batch before it is issued: a lane
         // finds its tile's segment and its box's page, and later issues that box itself.
-        const int boxes = TK / a.box_rows, per = 32 / boxes;   // boxes of a tile, tiles of a batch
+        const int tile_shift = (TK == 128 ? 7 : 6) - a.box_shift;   // log2 of the boxes of a tile
+        const int boxes = 1 << tile_shift, per = 32 >> tile_shift;  // boxes of a tile, tiles of a batch
+        const int my_tile = lane >> tile_shift, my_box = lane & (boxes - 1);
         const int page_mask = (1 << p.cache.page_shift) - 1;
         struct Box {
             int page, place, head, n;   // n: boxes that the tile has
+            int b, u;                   // the tile's segment if it is the run's first of it, else b = -1
         };
         const auto look_up = [&](int t) {
-            Box x{0, 0, 0, 0};
+            Box x{0, 0, 0, 0, -1, 0};
             if (t >= t1) return x;
             Walk<TK> v;
             v.start(t, pre, lens, p.n_seqs);
-            const int key = v.j * TK + lane % boxes * a.box_rows;
-            x.n = min(boxes, (v.len - v.j * TK + a.box_rows - 1) / a.box_rows);
-            x.head = v.u / a.chunks;
+            const int key = v.j * TK + (my_box << a.box_shift);
+            x.n = min(boxes, (v.len - v.j * TK + (1 << a.box_shift) - 1) >> a.box_shift);
+            x.head = kv_head(v.u);
+            if (v.j == 0 || t == t0) x.b = v.b, x.u = v.u;
             x.place = key & page_mask;
-            if (lane % boxes < x.n) x.page = p.table[(long long)v.b * p.ld_table + (key >> p.cache.page_shift)];
+            if (my_box < x.n) x.page = p.table[(long long)v.b * p.ld_table + (key >> p.cache.page_shift)];
             return x;
         };
-        int stage = 0, round = 0;
+        int stage = 0, round = 0, segs = 0;
         bool ok = true;
-        Box cur = look_up(t0 + lane / boxes);
+        Box cur = look_up(t0 + my_tile);
         for (int tb = t0; tb < t1 && ok; tb += per) {
-            const Box next = look_up(tb + per + lane / boxes);
+            const Box next = look_up(tb + per + my_tile);
             for (int i = 0; i < per && tb + i < t1; ++i) {
+                // a segment's q rows come first, into one of two buffers
+                const int qb = __shfl_sync(0xffffffffu, cur.b, i * boxes), qu = __shfl_sync(0xffffffffu, cur.u, i * boxes);
+                if (qb >= 0) {
+                    const int buf = segs & 1;
+                    if (segs > 1) ok = mbar_wait(q_empty + buf, ((segs >> 1) - 1) & 1, abort);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    const int head = kv_head(qu), chunk = qu - head * a.chunks;
+                    const int rows = min(PART_ROWS, a.group - chunk * PART_ROWS);
+                    if (lane == 0) mbar_arrive_expect_tx(q_full + buf, rows * D * 2);
+                    __syncwarp();
+                    if (lane < rows)
+                        bulk_load(smem + S::OFF_Q + (buf * PART_ROWS + lane) * S::LDQ,
+                                  p.q + qb * p.ld_q + (long long)(head * a.group + chunk * PART_ROWS + lane) * D, D * 2,
+                                  q_full + buf);
+                    ++segs;
+                }
                 if (round > 0) ok = mbar_wait(empty + stage, (round - 1) & 1, abort);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 uint8_t *k = smem + stage * 2 * S::TILE, *v = k + S::TILE;
-                if (lane == i * boxes) mbar_arrive_expect_tx(full + stage, cur.n * a.box_rows * S::ROW * 2);
+                if (lane == i * boxes) mbar_arrive_expect_tx(full + stage, (cur.n << a.box_shift) * S::ROW * 2);
                 __syncwarp();
-                const int box = lane - i * boxes;
-                if (box >= 0 && box < cur.n) {
+                if (my_tile == i && my_box < cur.n) {
                     int page = cur.page;
                     if (page < 0 || page >= p.cache.num_pages) {
                         report(p.status, ST_BOUNDS);
@@ -300,7 +332,7 @@ __global__ void __launch_bounds__(Shape<D, F8, WIDE>::THREADS, 1)
                     }
                     #pragma unroll
                     for (int x = 0; x < S::ROW / S::BOX; ++x) {
-                        const int off = x * (TK * S::BOX) + box * a.box_rows * S::BOX;
+                        const int off = x * (TK * S::BOX) + (my_box << a.box_shift) * S::BOX;
                         const int col = x * (S::BOX / (F8 ? 1 : 2));
                         tma_load_4d(k + off, &tmK, full + stage, col, cur.place, cur.head, page);
                         tma_load_4d(v + off, &tmV, full + stage, col, cur.place, cur.head, page);
@@ -319,6 +351,7 @@ __global__ void __launch_bounds__(Shape<D, F8, WIDE>::THREADS, 1)
                 const int issued = round * STAGES + stage;
                 for (int f = max(0, issued - STAGES); f < issued; ++f)
                     mbar_wait(full + f % STAGES, (f / STAGES) & 1, &never);
+                for (int f = max(0, segs - 2); f < segs; ++f) mbar_wait(q_full + (f & 1), (f >> 1) & 1, &never);
             }
             __syncwarp();
         }
@@ -334,31 +367,55 @@ __global__ void __launch_bounds__(Shape<D, F8, WIDE>::THREADS, 1)
     const int row_v = (lane & 7) + ((lane >> 3) & 1) * 8, chunk_v = lane >> 4;
     const int row_k = F8 ? row_v : (lane & 7) + (lane >> 4) * 8, chunk_k = F8 ? chunk_v : (lane >> 3) & 1;
     int stage = 0, round = 0, turn = 0;   // turn: the group whose tile this is
+    // parts of segments that other CTAs share, joined at the end: [0] the run's first segment if it
+    // began before the run, [1] its last if it goes on behind it
+    struct Part {
+        int b, u, seg, seg_end;
+    } shared[2];
+    shared[0].b = shared[1].b = -1;
+    const int trow = tid / (D / 4), tcol = tid % (D / 4) * 4;   // this thread's output in the sums of the joins
+    const auto store = [&](int b, int h, float4 v, float m, float l, float vs) {
+        const float inv = 1.f / l, f = inv * vs;
+        *reinterpret_cast<uint2 *>(p.o + b * p.ld_o + (long long)h * D + tcol) =
+            make_uint2(pack_bf16x2(v.x * f, v.y * f), pack_bf16x2(v.z * f, v.w * f));
+        if (a.stat && tcol == 0) a.stat[(long long)b * p.nq + h] = make_float2(m, inv);
+    };
+    const auto give_up = [&]() {   // on the data; the control flow (barriers, counters) goes on to the end
+        if (lane == 0) {
+            report(p.status, ST_TIMEOUT);
+            *abort = 1;
+        }
+        __syncwarp();
+    };
+    int segs = 0;
 
-    for (int t = t0; t < t1;) {
+    for (int t = t0; t < t1; ++segs) {
         const int seg = t - w.j, seg_end = seg + w.tiles;   // this segment's tiles in the whole row of tiles
         const int j1 = min(w.tiles, t1 - seg);              // this run's part of it: [w.j, j1)
-        const int kvh = w.u / a.chunks, h0 = kvh * a.group + (w.u % a.chunks) * PART_ROWS;
-        const int rows = min(PART_ROWS, a.group - (w.u % a.chunks) * PART_ROWS);   // heads of the segment
+        const int kvh = kv_head(w.u), chunk = w.u - kvh * a.chunks, h0 = kvh * a.group + chunk * PART_ROWS;
+        const int rows = min(PART_ROWS, a.group - chunk * PART_ROWS);   // heads of the segment
 
         // q as the A operand: rows = heads, the contraction over d in steps of 16
         uint32_t qa[D / 16][WIDE ? 4 : 2];
         float scale0 = base_scale, scale1 = base_scale;
         {
-            const bf16 *q0 = p.q + w.b * p.ld_q + (long long)(h0 + g) * D, *q1 = q0 + 8 * D;
+            if (!mbar_wait(q_full + (segs & 1), (segs >> 1) & 1, abort)) give_up();
+            const uint8_t *q0 = smem + S::OFF_Q + ((segs & 1) * PART_ROWS + g) * S::LDQ, *q1 = q0 + 8 * S::LDQ;
             const bool in0 = g < rows, in1 = WIDE && g + 8 < rows;
             #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
                 // bf16: columns 2t, 2t+1 and 2t+8, 2t+9 of the step; e4m3: 4t .. 4t+3 (the bytes a
                 // lane holds of a key), the same order on both sides of the product
                 const int c0 = 16 * k + (F8 ? 4 * tq : 2 * tq), c1 = c0 + (F8 ? 2 : 8);
-                qa[k][0] = in0 ? *reinterpret_cast<const uint32_t *>(q0 + c0) : 0u;
-                qa[k][1] = in0 ? *reinterpret_cast<const uint32_t *>(q0 + c1) : 0u;
+                qa[k][0] = in0 ? *reinterpret_cast<const uint32_t *>(q0 + 2 * c0) : 0u;
+                qa[k][1] = in0 ? *reinterpret_cast<const uint32_t *>(q0 + 2 * c1) : 0u;
                 if constexpr (WIDE) {
-                    qa[k][2] = in1 ? *reinterpret_cast<const uint32_t *>(q1 + c0) : 0u;
-                    qa[k][3] = in1 ? *reinterpret_cast<const uint32_t *>(q1 + c1) : 0u;
+                    qa[k][2] = in1 ? *reinterpret_cast<const uint32_t *>(q1 + 2 * c0) : 0u;
+                    qa[k][3] = in1 ? *reinterpret_cast<const uint32_t *>(q1 + 2 * c1) : 0u;
                 }
             }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(q_empty + (segs & 1));
             if constexpr (F8) {
                 const float ks = p.cache.k_scale[kvh];
                 #pragma unroll
@@ -396,14 +453,7 @@ __global__ void __launch_bounds__(Shape<D, F8, WIDE>::THREADS, 1)
 
         for (; w.j < j1; ++w.j, ++t, turn = turn + 1 == S::GROUPS ? 0 : turn + 1) {
             if (turn == group) {
-                if (!mbar_wait(full + stage, round & 1, abort)) {
-                    // give up on the data, keep the control flow (barriers, counters) to the end
-                    if (lane == 0) {
-                        report(p.status, ST_TIMEOUT);
-                        *abort = 1;
-                    }
-                    __syncwarp();
-                }
+                if (!mbar_wait(full + stage, round & 1, abort)) give_up();
                 const int key0 = w.j * TK + slice;
                 if (key0 < w.len) {
                     const uint32_t kt = smem_u32(smem + stage * 2 * S::TILE), vt = kt + S::TILE;
@@ -570,7 +620,7 @@ __global__ void __launch_bounds__(Shape<D, F8, WIDE>::THREADS, 1)
         const bool whole = seg >= t0 && seg_end <= t1;
         const float vs = F8 ? p.cache.v_scale[kvh] : 1.f;
         const int slot = 2 * blockIdx.x + (seg < t0 ? 0 : 1);
-        const int trow = tid / (D / 4), tcol = tid % (D / 4) * 4;   // this thread's output in the sums below
+        if (!whole) shared[seg < t0 ? 0 : 1] = Part{w.b, w.u, seg, seg_end};
         #pragma unroll
         for (int r8 = 0; r8 < (WIDE ? 16 : 8); r8 += 8) {
             float top = -INFINITY;
@@ -606,11 +656,7 @@ __global__ void __launch_bounds__(Shape<D, F8, WIDE>::THREADS, 1)
                     acc.w += x.w;
                 }
                 if (whole) {
-                    const int h = h0 + r8 + trow;
-                    const float inv = 1.f / ll, f2 = inv * vs;
-                    *reinterpret_cast<uint2 *>(p.o + w.b * p.ld_o + (long long)h * D + tcol) =
-                        make_uint2(pack_bf16x2(acc.x * f2, acc.y * f2), pack_bf16x2(acc.z * f2, acc.w * f2));
-                    if (a.stat && tcol == 0) a.stat[(long long)w.b * p.nq + h] = make_float2(mm, inv);
+                    store(w.b, h0 + r8 + trow, acc, mm, ll, vs);
                 } else {
                     *reinterpret_cast<float4 *>(a.part + ((long long)slot * PART_ROWS + r8 + trow) * D + tcol) = acc;
                     if (tcol == 0) a.ml[slot * PART_ROWS + r8 + trow] = make_float2(mm, ll);
@@ -618,46 +664,74 @@ __global__ void __launch_bounds__(Shape<D, F8, WIDE>::THREADS, 1)
             }
             compute_sync<CWARPS * 32>();
         }
-        if (!whole) {
-            // the CTA whose part arrives last joins the parts, in the order of the keys
-            const int first = (int)((((long long)seg + 1) * G - 1) / T), last = (int)(((long long)seg_end * G - 1) / T);
-            // (the barrier at the end of the loop above orders all threads' parts before thread 0's release)
-            if (tid == 0) {
-                uint32_t before;
-                asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(before) : "l"(a.count + first) : "memory");
-                *s_last = before == (uint32_t)(last - first);
-                if (*s_last) a.count[first] = 0u;   // for the next call
-            }
-            compute_sync<CWARPS * 32>();
-            if (*s_last) {
-                #pragma unroll
-                for (int r8 = 0; r8 < (WIDE ? 16 : 8); r8 += 8)
-                    if (trow < 8 && r8 + trow < rows) {
-                        // part of CTA c: its slot 1 if the segment begins in its run, else 0
-                        const auto at = [&](int c) { return (2 * c + (c == first ? 1 : 0)) * PART_ROWS + r8 + trow; };
-                        float mm = -INFINITY, ll = 0.f;
-                        for (int c = first; c <= last; ++c) mm = fmaxf(mm, __ldcg(a.ml + at(c)).x);
-                        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-                        #pragma unroll 4
-                        for (int c = first; c <= last; ++c) {
-                            const float2 x = __ldcg(a.ml + at(c));
-                            const float4 y = __ldcg(reinterpret_cast<const float4 *>(a.part + (long long)at(c) * D + tcol));
-                            const float f = x.x == -INFINITY ? 0.f : ex2(x.x - mm);
-                            ll = fmaf(x.y, f, ll);
-                            acc.x = fmaf(y.x, f, acc.x);
-                            acc.y = fmaf(y.y, f, acc.y);
-                            acc.z = fmaf(y.z, f, acc.z);
-                            acc.w = fmaf(y.w, f, acc.w);
-                        }
-                        const int h = h0 + r8 + trow;
-                        const float inv = 1.f / ll, f2 = inv * vs;
-                        *reinterpret_cast<uint2 *>(p.o + w.b * p.ld_o + (long long)h * D + tcol) =
-                            make_uint2(pack_bf16x2(acc.x * f2, acc.y * f2), pack_bf16x2(acc.z * f2, acc.w * f2));
-                        if (a.stat && tcol == 0) a.stat[(long long)w.b * p.nq + h] = make_float2(mm, inv);
-                    }
+        if (t < t1) w.next(units, lens);
+    }
+
+    // ---------------------------------------------------- join the parts of shared segments
+    // The CTA whose part arrives last joins them, in the order of the keys.  (The barrier at the end of the
+    // loop above orders all threads' parts before the release.)
+    if (shared[0].b < 0 && shared[1].b < 0) return;
+    if (tid < 2) {
+        const Part &x = shared[tid];
+        s_last[tid] = 0;
+        if (x.b >= 0) {
+            const int first = owner(x.seg), last = owner(x.seg_end - 1);
+            uint32_t before;
+            asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(before) : "l"(a.count + first) : "memory");
+            if (before == (uint32_t)(last - first)) {
+                a.count[first] = 0u;   // for the next call
+                s_last[tid] = 1;
             }
         }
-        if (t < t1) w.next(units, lens);
+    }
+    compute_sync<CWARPS * 32>();
+    #pragma unroll 1
+    for (int x = 0; x < 2; ++x) {
+        if (!s_last[x]) continue;
+        const Part y = x ? shared[1] : shared[0];
+        const int first = owner(y.seg), n = owner(y.seg_end - 1) - first + 1;
+        const int kvh = kv_head(y.u), chunk = y.u - kvh * a.chunks;
+        const int rows = min(PART_ROWS, a.group - chunk * PART_ROWS);
+        const float vs = F8 ? p.cache.v_scale[kvh] : 1.f;
+        #pragma unroll 1
+        for (int r8 = 0; r8 < rows && trow < 8; r8 += 8) {   // D / 4 lanes per row (trow: whole warps)
+            // up to BATCH parts at a time, all their loads in flight: this lane's four columns of each, and of one
+            // part (lane li: part i0 + li) the row's maximum and sum
+            constexpr int LPR = D / 4, BATCH = LPR < 24 ? LPR : 24;
+            const int li = lane % LPR, row = r8 + trow;   // (rows past the segment's last hold anything: not stored)
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+            float mm = -INFINITY, ll = 0.f;
+            for (int i0 = 0; i0 < n; i0 += BATCH) {
+                // slot 1 of the first CTA (the segment begins in its run), slot 0 of the others
+                const auto at = [&](int i) { return (long long)(2 * (first + i) + (i == 0 ? 1 : 0)) * PART_ROWS + row; };
+                float2 ml = make_float2(-INFINITY, 0.f);
+                if (li < BATCH && i0 + li < n) ml = __ldcg(a.ml + at(i0 + li));
+                float4 v[BATCH];
+                #pragma unroll
+                for (int k = 0; k < BATCH; ++k)
+                    v[k] = i0 + k < n ? __ldcg(reinterpret_cast<const float4 *>(a.part + at(i0 + k) * D + tcol))
+                                      : make_float4(0.f, 0.f, 0.f, 0.f);
+                float top = ml.x;
+                #pragma unroll
+                for (int off = LPR / 2; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+                top = fmaxf(top, mm);
+                const float c = mm == -INFINITY ? 0.f : ex2(mm - top), f = ml.x == -INFINITY ? 0.f : ex2(ml.x - top);
+                mm = top;
+                ll = fmaf(ll, c, ml.y * f);
+                acc = make_float4(acc.x * c, acc.y * c, acc.z * c, acc.w * c);
+                #pragma unroll
+                for (int k = 0; k < BATCH; ++k) {
+                    const float fk = __shfl_sync(0xffffffffu, f, k, LPR);   // 0 past the last part
+                    acc.x = fmaf(v[k].x, fk, acc.x);
+                    acc.y = fmaf(v[k].y, fk, acc.y);
+                    acc.z = fmaf(v[k].z, fk, acc.z);
+                    acc.w = fmaf(v[k].w, fk, acc.w);
+                }
+            }
+            #pragma unroll
+            for (int off = LPR / 2; off > 0; off >>= 1) ll += __shfl_xor_sync(0xffffffffu, ll, off);
+            if (row < rows) store(y.b, kvh * a.group + chunk * PART_ROWS + row, acc, mm, ll, vs);
+        }
     }
 }
 
@@ -751,7 +825,7 @@ cudaError_t launch_attention_decode(const AttentionDecode &p, cudaStream_t st) {
     a.p = p;
     a.group = p.nq / p.cache.nkv;
     a.chunks = (a.group + PART_ROWS - 1) / PART_ROWS;
-    a.box_rows = std::min(64, 1 << p.cache.page_shift);
+    a.box_shift = std::min(6, p.cache.page_shift);
     a.count = reinterpret_cast<uint32_t *>(ws);
     a.part = reinterpret_cast<float *>(ws + y.part);
     a.ml = reinterpret_cast<float2 *>(ws + y.ml);
