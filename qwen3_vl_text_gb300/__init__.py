@@ -570,9 +570,13 @@ def h3enc_op_attention_bidir_ws(qkv, o, S, heads, head_dim, workspace, cu_seqlen
                                                   _ptr(workspace), wbytes, _stream(stream)))
 
 
-def _ld(t, width):
-    """Leading dimension of a row-major matrix of `width` columns (a tensor's row stride)."""
-    return t.stride(0) if t is not None and not isinstance(t, int) and t.shape[0] > 1 else width
+def _ld(t, need):
+    """Leading dimension of a row-major matrix: a tensor's row stride (of a single row, whose stride means
+    nothing, at least its width); `need` for an address or None."""
+    if t is None or isinstance(t, int):
+        return need
+    s = t.stride(0)
+    return s if s >= need or t.shape[0] != 1 else t.shape[1]
 
 
 def h3enc_op_qk_norm_rope(qkv, T, n_heads, n_kv_heads, head_dim, w_q, w_k, eps, cos_tab, sin_tab, cs_stride=0,
@@ -592,25 +596,26 @@ def h3enc_op_attention_decode(q, o, cache, page_table, seq_lens, n_heads, max_le
                               weight_out=None, status=None, stream=None):
     """Attention of one new token per sequence over a KVCache: q, o [n_seqs, n_heads * head_dim],
     page_table int32 [n_seqs, pages], seq_lens int32 [n_seqs], weights float32 [n_seqs, >= max_len]."""
-    n_seqs, width = seq_lens.shape[0], n_heads * cache.head_dim
-    ld_w = 0 if weight_out is None else _ld(weight_out, weight_out.shape[1])
-    if weight_in is not None and _ld(weight_in, ld_w) != ld_w:
+    width = n_heads * cache.head_dim
+    ld_w = _ld(weight_out, max_len)
+    if weight_in is not None and weight_in is not weight_out and seq_lens.numel() > 1 and _ld(weight_in, ld_w) != ld_w:
         raise ValueError("attention_decode: weight_in and weight_out have different row strides")
     return _check(lib.h3enc_op_attention_decode(
-        _ptr(q), _ld(q, width), _ptr(o), _ld(o, width), cache, _ptr(page_table), _ld(page_table, page_table.shape[1]),
-        _ptr(seq_lens), n_seqs, n_heads, max_len, _ptr(weight_in), _ptr(weight_out), ld_w, _ptr(workspace),
+        _ptr(q), _ld(q, width), _ptr(o), _ld(o, width), cache, _ptr(page_table),
+        _ld(page_table, -(-max_len // cache.page_size)), _ptr(seq_lens), seq_lens.numel(), n_heads, max_len,
+        _ptr(weight_in), _ptr(weight_out), ld_w, _ptr(workspace),
         0 if workspace is None else workspace.numel() * workspace.element_size(), _ptr(status), _stream(stream)))
 
 
 def h3enc_op_cache_evict(cache, page_table, seq_lens, max_len, budget, weight, weight_out, kept, new_lens,
                          page_table_out=None, sink=0, recent=0, status=None, stream=None):
     """Keep `budget` tokens per sequence by accumulated weight; in place, or into page_table_out's pages."""
-    out_ld = 0 if page_table_out is None else _ld(page_table_out, page_table_out.shape[1])
+    size = cache.page_size
     return _check(lib.h3enc_op_cache_evict(
-        cache, _ptr(page_table), _ld(page_table, page_table.shape[1]), _ptr(page_table_out), out_ld, _ptr(seq_lens),
-        seq_lens.shape[0], max_len, budget, sink, recent, _ptr(weight), _ld(weight, weight.shape[1]), _ptr(weight_out),
-        _ld(weight_out, weight_out.shape[1]), _ptr(kept), _ld(kept, kept.shape[1]), _ptr(new_lens), _ptr(status),
-        _stream(stream)))
+        cache, _ptr(page_table), _ld(page_table, -(-max_len // size)), _ptr(page_table_out),
+        _ld(page_table_out, -(-min(budget, max_len) // size)), _ptr(seq_lens), seq_lens.numel(), max_len, budget, sink,
+        recent, _ptr(weight), _ld(weight, max_len), _ptr(weight_out), _ld(weight_out, max_len), _ptr(kept),
+        _ld(kept, budget), _ptr(new_lens), _ptr(status), _stream(stream)))
 
 
 def h3vis_create(cfg: VisionConfig):

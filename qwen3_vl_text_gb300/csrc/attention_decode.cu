@@ -399,6 +399,7 @@ __global__ void __launch_bounds__(Shape<D, F8, WIDE>::THREADS, 1)
         uint32_t qa[D / 16][WIDE ? 4 : 2];
         float scale0 = base_scale, scale1 = base_scale;
         {
+            const float ks = F8 ? p.cache.k_scale[kvh] : 1.f;   // (its load goes out before the wait)
             if (!mbar_wait(q_full + (segs & 1), (segs >> 1) & 1, abort)) give_up();
             const uint8_t *q0 = smem + S::OFF_Q + ((segs & 1) * PART_ROWS + g) * S::LDQ, *q1 = q0 + 8 * S::LDQ;
             const bool in0 = g < rows, in1 = WIDE && g + 8 < rows;
@@ -417,7 +418,6 @@ __global__ void __launch_bounds__(Shape<D, F8, WIDE>::THREADS, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(q_empty + (segs & 1));
             if constexpr (F8) {
-                const float ks = p.cache.k_scale[kvh];
                 #pragma unroll
                 for (int r = 0; r < (WIDE ? 2 : 1); ++r) {
                     float top = 0.f;
