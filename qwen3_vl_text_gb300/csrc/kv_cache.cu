@@ -170,8 +170,7 @@ __global__ void __launch_bounds__(QK_THREADS) qk_norm_rope_kernel(const QkNormRo
 
 constexpr int SEL_THREADS = 1024;
 constexpr int SEL_BLOCK = 32 * SEL_THREADS;   // tokens of one block of the placing pass
-constexpr int SEL_CACHE = 49152;              // weights a CTA holds in shared memory (192 KB)
-constexpr int SEL_RANKS = 8;                  // CTAs of a cluster, at most
+constexpr int SEL_CACHE = 45056;              // weights a CTA holds in shared memory (176 KB)
 constexpr int SEL_PER_CTA = 8192;             // tokens per CTA from which the cluster grows
 constexpr int BINS = 2048;
 
@@ -203,33 +202,38 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t *sums) {
     return v + (warp ? before : 0u);
 }
 
-// The pair of words at this shared-memory place in CTA `rank` of the cluster.
-__device__ __forceinline__ uint2 ld_cluster2(const uint32_t *p, uint32_t rank) {
-    uint2 v;
-    asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];"
-                 : "=r"(v.x), "=r"(v.y)
-                 : "r"(mapa_shared(smem_u32(p), rank))
+// Adds to the word at this shared-memory place in CTA `rank` of the cluster.
+__device__ __forceinline__ void add_cluster(uint32_t *p, uint32_t rank, uint32_t v) {
+    asm volatile("red.relaxed.cluster.shared::cluster.add.u32 [%0], %1;" ::"r"(mapa_shared(smem_u32(p), rank)), "r"(v)
                  : "memory");
-    return v;
 }
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 // One cluster of 1 to 8 CTAs per sequence, each with a contiguous part of its tokens, whose weights
 // it holds in shared memory (what does not fit is read again).  The budget-th largest key of the
 // unprotected tokens is found in up to three digits (11, 11 and 10 bits): a histogram of the tokens that
-// match the digits so far, summed over the cluster, scanned from the top by all threads; it ends
-// early when the digit's whole bin is kept, which two digits almost always reach unless weights are equal.
-// Then the tokens are counted in order and each kept one is written to its place.  What bounds it is
-// the chain of these steps (some microseconds), not the 4 bytes per token.
+// match the digits so far, scanned from the top by all threads; it ends early when the digit's whole bin is
+// kept, which two digits almost always reach unless weights are equal.  In a cluster every CTA adds the bins
+// that it has anything in to all CTAs' sums (few are filled; reading all histograms took 2.2 us a digit).
+// Then the tokens are counted in order, as bit masks of 32, and each kept one is written to its place.
+// What bounds it is the chain of these steps (some microseconds), not the 4 bytes per token.
 template <bool CLUSTER>
 __global__ void __launch_bounds__(SEL_THREADS, 1) evict_select_kernel(const CacheEvict p, int cached) {
     extern __shared__ float held[];               // [cached] weights
-    __shared__ __align__(8) uint32_t hist[3][BINS];
-    __shared__ __align__(8) uint32_t s_count[2];
-    __shared__ uint32_t sums[32], s_digit, s_need, s_full;
+    __shared__ __align__(8) uint32_t hist[BINS];
+    __shared__ __align__(8) uint32_t sum[CLUSTER ? 3 : 1][BINS];   // over the cluster, one per digit
+    __shared__ uint32_t mask_sure[SEL_BLOCK / 32], mask_eq[SEL_BLOCK / 32];
+    __shared__ uint32_t sums[32], s_base[2], s_digit, s_need, s_full, s_total;
     pdl_trigger();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    for (int i = tid; i < 3 * BINS; i += SEL_THREADS) hist[i / BINS][i % BINS] = 0;
-    if (tid < 2) s_count[tid] = 0;
+    for (int i = tid; i < BINS; i += SEL_THREADS) {
+        hist[i] = 0;
+        #pragma unroll
+        for (int k = 0; k < (CLUSTER ? 3 : 1); ++k) sum[k][i] = 0;
+    }
+    if (tid < 2) s_base[tid] = 0;
+    if (CLUSTER) cluster_arrive();   // the sums may be added to once all CTAs have cleared theirs
     pdl_wait();
     const uint32_t rank = CLUSTER ? cluster_ctarank() : 0u;
     const int ranks = CLUSTER ? (int)gridDim.x : 1, b = blockIdx.y;
@@ -249,32 +253,28 @@ __global__ void __launch_bounds__(SEL_THREADS, 1) evict_select_kernel(const Cach
     #pragma unroll 4
     for (int i = tid; i < min(n, cached); i += SEL_THREADS) held[i] = w[i];
     const auto weight_of = [&](int i) { return i < cached ? held[i] : w[i]; };
+    if (CLUSTER) cluster_wait();
     __syncthreads();
     for (int pass = 0; pass < 3 && wanted; ++pass) {
         const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0), bits = pass == 2 ? 10 : 11;
         const uint32_t mask = (1u << bits) - 1, high = pass == 0 ? 0u : 0xffffffffu << (shift + bits);
-        uint32_t *h = hist[pass];
         #pragma unroll 4
         for (int i = max(first, 0) + tid; i < min(last, n); i += SEL_THREADS) {
             const uint32_t k = weight_key(weight_of(i));
-            if (((k ^ prefix) & high) == 0) atomicAdd(&h[(k >> shift) & mask], 1u);
+            if (((k ^ prefix) & high) == 0) atomicAdd(&hist[(k >> shift) & mask], 1u);
         }
-        if (CLUSTER) cluster_sync();
-        else __syncthreads();
+        __syncthreads();
         // thread t: the bins 2047 - 2t and 2046 - 2t, so that the scan runs from the largest down
         const int low = BINS - 2 - 2 * tid;
-        uint2 c = make_uint2(0, 0);
-        if constexpr (CLUSTER) {
-            uint2 v[SEL_RANKS];
-            #pragma unroll
-            for (int r = 0; r < SEL_RANKS; ++r) v[r] = r < ranks ? ld_cluster2(h + low, r) : make_uint2(0, 0);
-            #pragma unroll
-            for (int r = 0; r < SEL_RANKS; ++r) {
-                c.x += v[r].x;
-                c.y += v[r].y;
+        uint2 c = *reinterpret_cast<const uint2 *>(hist + low);
+        *reinterpret_cast<uint2 *>(hist + low) = make_uint2(0, 0);   // for the next digit
+        if (CLUSTER) {
+            for (int r = 0; r < ranks; ++r) {
+                if (c.x) add_cluster(&sum[pass][low], r, c.x);
+                if (c.y) add_cluster(&sum[pass][low + 1], r, c.y);
             }
-        } else {
-            c = *reinterpret_cast<const uint2 *>(h + low);
+            cluster_sync();
+            c = *reinterpret_cast<const uint2 *>(sum[pass] + low);
         }
         const uint32_t upto = block_scan(c.x + c.y, sums), before = upto - c.x - c.y;
         if (before < need && need <= upto) {   // exactly one thread
@@ -290,92 +290,89 @@ __global__ void __launch_bounds__(SEL_THREADS, 1) evict_select_kernel(const Cach
         if (s_full == need) break;
     }
     // kept for certain: protected tokens and larger keys; of the equal ones the first `need`
-    const auto sort_of = [&](int i, float v, bool &sure, bool &eq) {
+    const auto sort_of = [&](int i, bool &sure, bool &eq) {
         sure = all || i < first || i >= last;
         eq = false;
         if (!sure && wanted) {
-            const uint32_t k = weight_key(v) >> cut;
+            const uint32_t k = weight_key(weight_of(i)) >> cut;
             sure = k > prefix >> cut;
             eq = k == prefix >> cut;
         }
     };
-    uint32_t base_sure = 0, base_eq = 0;   // of the tokens before this CTA's (before this block's)
-    if constexpr (CLUSTER) {
-        uint32_t cs = 0, ce = 0;
+    // The masks of a block of 32 rows of 1024 tokens, and thread t's count of both kinds before mask t, in one word
+    // (a block holds at most 32768 of each); s_total: the block's.
+    const auto mark = [&](int i0, int rows) {
+        __syncthreads();
         #pragma unroll 4
-        for (int i = tid; i < n; i += SEL_THREADS) {
-            bool sure, eq;
-            sort_of(i, weight_of(i), sure, eq);
-            cs += sure;
-            ce += eq;
+        for (int r = 0; r < rows; ++r) {
+            const int i = i0 + r * SEL_THREADS + tid;
+            bool sure = false, eq = false;
+            if (i < n) sort_of(i, sure, eq);
+            const uint32_t ms = __ballot_sync(0xffffffffu, sure), me = __ballot_sync(0xffffffffu, eq);
+            if (lane == 0) {
+                mask_sure[r * 32 + warp] = ms;
+                mask_eq[r * 32 + warp] = me;
+            }
         }
-        cs = __reduce_add_sync(0xffffffffu, cs);
-        ce = __reduce_add_sync(0xffffffffu, ce);
-        if (lane == 0) {
-            atomicAdd(&s_count[0], cs);
-            atomicAdd(&s_count[1], ce);
+        __syncthreads();
+        const uint32_t own = tid < 32 * rows ? (uint32_t)__popc(mask_sure[tid]) << 16 | (uint32_t)__popc(mask_eq[tid]) : 0u;
+        const uint32_t inc = block_scan(own, sums);
+        hist[tid] = inc - own;   // (the digits are done with the histogram)
+        if (tid == SEL_THREADS - 1) s_total = inc;
+        __syncthreads();
+    };
+    const auto rows_of = [&](int i0) { return (min(n - i0, SEL_BLOCK) + SEL_THREADS - 1) / SEL_THREADS; };
+    uint32_t base_sure = 0, base_eq = 0;   // of the tokens before this CTA's (before this block's)
+    if (CLUSTER) {
+        uint32_t cs, ce;
+        if (n <= SEL_BLOCK) {
+            mark(0, rows_of(0));
+            cs = s_total >> 16;
+            ce = s_total & 0xffffu;
+        } else {   // more than a block: counted first, marked again below
+            cs = ce = 0;
+            for (int i0 = 0; i0 < n; i0 += SEL_BLOCK) {
+                mark(i0, rows_of(i0));
+                cs += s_total >> 16;
+                ce += s_total & 0xffffu;
+            }
         }
-        cluster_sync();
-        uint2 v[SEL_RANKS];
-        #pragma unroll
-        for (int r = 0; r < SEL_RANKS; ++r) v[r] = r < (int)rank ? ld_cluster2(s_count, r) : make_uint2(0, 0);
-        #pragma unroll
-        for (int r = 0; r < SEL_RANKS; ++r) {
-            base_sure += v[r].x;
-            base_eq += v[r].y;
+        if (tid < ranks && tid > (int)rank) {
+            add_cluster(&s_base[0], tid, cs);
+            add_cluster(&s_base[1], tid, ce);
         }
+        cluster_sync();   // (the last access to another CTA's memory is before it)
+        base_sure = s_base[0];
+        base_eq = s_base[1];
     }
     int32_t *kept = p.kept + b * p.ld_kept;
     float *wo = p.weight_out + b * p.ld_weight_out;
-    // counts in hist[0] (its last readers in the cluster are behind a barrier): [32 rows of 1024
-    // tokens][32 warps], both counts in one word (a block holds at most 32768 of each)
-    uint32_t *counts = hist[0];
     for (int i0 = 0; i0 < n; i0 += SEL_BLOCK) {
-        const int rows = (min(n - i0, SEL_BLOCK) + SEL_THREADS - 1) / SEL_THREADS;
-        __syncthreads();
+        const int rows = rows_of(i0);
+        if (!CLUSTER || n > SEL_BLOCK) mark(i0, rows);
+        const uint32_t below = (1u << lane) - 1;
         #pragma unroll 4
         for (int r = 0; r < rows; ++r) {
-            const int i = i0 + r * SEL_THREADS + tid;
-            bool sure = false, eq = false;
-            if (i < n) sort_of(i, weight_of(i), sure, eq);
-            const uint32_t ms = __ballot_sync(0xffffffffu, sure), me = __ballot_sync(0xffffffffu, eq);
-            if (lane == 0) counts[r * 32 + warp] = (uint32_t)__popc(ms) << 16 | (uint32_t)__popc(me);
-        }
-        __syncthreads();
-        const uint32_t own = tid < 32 * rows ? counts[tid] : 0u;
-        const uint32_t inc = block_scan(own, sums);
-        counts[tid] = inc - own;
-        if (tid == SEL_THREADS - 1) s_need = inc;   // the block's total
-        __syncthreads();
-        #pragma unroll 4
-        for (int r = 0; r < rows; ++r) {
-            const int i = i0 + r * SEL_THREADS + tid;
-            bool sure = false, eq = false;
-            float v = 0.f;
-            if (i < n) {
-                v = weight_of(i);
-                sort_of(i, v, sure, eq);
-            }
-            const uint32_t ms = __ballot_sync(0xffffffffu, sure), me = __ballot_sync(0xffffffffu, eq);
-            const uint32_t below = (1u << lane) - 1, at = counts[r * 32 + warp];
+            const uint32_t ms = mask_sure[r * 32 + warp], me = mask_eq[r * 32 + warp], at = hist[r * 32 + warp];
             const uint32_t ns = base_sure + (at >> 16) + __popc(ms & below);
             const uint32_t ne = base_eq + (at & 0xffffu) + __popc(me & below);
-            if (sure || (eq && ne < need)) {
+            if ((ms >> lane & 1) || ((me >> lane & 1) && ne < need)) {
+                const int i = i0 + r * SEL_THREADS + tid;
                 const uint32_t to = ns + min(ne, need);
                 kept[to] = begin + i;
-                wo[to] = v;
+                wo[to] = weight_of(i);
             }
         }
-        base_sure += s_need >> 16;
-        base_eq += s_need & 0xffffu;
+        base_sure += s_total >> 16;
+        base_eq += s_total & 0xffffu;
     }
     // the rest of the rows, by all CTAs of the cluster
     const int total = all ? len : p.budget;
     for (int i = total + (int)rank * SEL_THREADS + tid; i < p.max_len; i += ranks * SEL_THREADS) wo[i] = 0.f;
     for (int i = total + (int)rank * SEL_THREADS + tid; i < p.budget; i += ranks * SEL_THREADS) kept[i] = -1;
-    // new_lens may be seq_lens: every thread has read the length (and the other CTAs' counts)
-    if (CLUSTER) cluster_sync();
-    else __syncthreads();
+    // new_lens may be seq_lens: every thread of the sequence has read the length (in a cluster: before the
+    // barrier above)
+    __syncthreads();
     if (tid == 0 && rank == 0) p.new_lens[b] = total;
 }
 
