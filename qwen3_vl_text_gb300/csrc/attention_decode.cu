@@ -32,7 +32,7 @@ namespace h3 {
 
 namespace {
 
-constexpr int WK = 64;                  // keys per CTA of the weight sums; score rows are padded to it
+constexpr int WK = 128;                 // keys per CTA of the weight sums; score rows are padded to it
 constexpr int MAX_CTAS = 1024;          // arrival counters at the head of the workspace
 constexpr int PART_ROWS = 16;           // heads of a segment
 
@@ -736,38 +736,40 @@ __global__ void __launch_bounds__(Shape<D, F8, WIDE>::THREADS, 1)
 }
 
 // weight_out[b][i] = weight_in[b][i] + sum over the q heads of their p_i, from the stored scores and
-// each head's (m, 1/l).  A CTA takes 64 keys of a sequence, two per lane (256 contiguous bytes a warp
+// each head's (m, 1/l).  A CTA takes 128 keys of a sequence, four per lane (512 contiguous bytes a warp
 // load); warp w sums the heads w, w + 8, ... in order and the eight sums are added in order, so the
 // result is the same on every run.  Reads 4 bytes per head and key, mostly from L2 where the
 // attention left them.
 __global__ void __launch_bounds__(256) attention_weight_kernel(const AttentionDecode p, const float *scores,
                                                                const float2 *stat, long long ld_scores) {
-    __shared__ float2 part[8][32];
+    __shared__ float4 part[8][WK / 4];
     pdl_trigger();
     pdl_wait();
     const int b = blockIdx.y, i0 = blockIdx.x * WK, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int len = min(max(p.seq_lens[b], 0), p.max_len);
     if (i0 >= len) return;
-    const float *s = scores + (long long)b * p.nq * ld_scores + i0 + 2 * lane;   // scores are stored in whole slices of 16
+    const int i = i0 + threadIdx.x;
+    const bool out = threadIdx.x < WK && i < len;
+    const float start = out && p.weight_in ? p.weight_in[b * p.ld_weight + i] : 0.f;
+    const float *s = scores + (long long)b * p.nq * ld_scores + i0 + 4 * lane;   // rows are padded to WK
     const float2 *st = stat + (long long)b * p.nq;
-    const bool in = i0 + 2 * lane < len;
-    float2 acc = make_float2(0.f, 0.f);
-    if (in) {
-        #pragma unroll 8
-        for (int h = warp; h < p.nq; h += 8) {
-            const float2 x = *reinterpret_cast<const float2 *>(s + h * ld_scores), ml = st[h];
-            acc.x = fmaf(ex2(x.x - ml.x), ml.y, acc.x);
-            acc.y = fmaf(ex2(x.y - ml.x), ml.y, acc.y);
-        }
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    #pragma unroll 8
+    for (int h = warp; h < p.nq; h += 8) {
+        const float4 x = *reinterpret_cast<const float4 *>(s + h * ld_scores);   // (behind the sequence: anything, unused)
+        const float2 ml = st[h];
+        acc.x = fmaf(ex2(x.x - ml.x), ml.y, acc.x);
+        acc.y = fmaf(ex2(x.y - ml.x), ml.y, acc.y);
+        acc.z = fmaf(ex2(x.z - ml.x), ml.y, acc.z);
+        acc.w = fmaf(ex2(x.w - ml.x), ml.y, acc.w);
     }
     part[warp][lane] = acc;
     __syncthreads();
-    const int i = i0 + threadIdx.x;
-    if (threadIdx.x < WK && i < len) {
+    if (out) {
         float sum = 0.f;
         #pragma unroll
         for (int w = 0; w < 8; ++w) sum += reinterpret_cast<const float *>(part[w])[threadIdx.x];
-        p.weight_out[b * p.ld_weight + i] = (p.weight_in ? p.weight_in[b * p.ld_weight + i] : 0.f) + sum;
+        p.weight_out[b * p.ld_weight + i] = start + sum;
     }
 }
 
