@@ -10,8 +10,8 @@
 //  * The keys of all (sequence, kv head) segments are laid end to end in tiles of 64 (e4m3: 128) and cut into one
 //    equal run of tiles per CTA, one CTA per SM, whatever the lengths are: a run may end inside a
 //    segment, whose parts are then joined (below).  Lengths are read on the device.
-//  * A producer warp keeps up to STAGES tiles of K and V in flight through TMA (a box per page,
-//    one lane per box, their page numbers looked up a batch ahead); eight or twelve warps compute.
+//  * Two producer warps, one for K and one for V, keep up to STAGES tiles in flight through TMA (a box
+//    per page, one lane per box, their page numbers looked up a batch ahead); eight warps compute.
 //  * The products run on mma.sync m16n8k16 with the q heads as the 16 rows: there are at most 16 rows
 //    of work per key, which a 128-row tcgen05 tile would leave mostly empty, and a warp that
 //    holds scores, weights and output in its own registers needs no exchange with other warps per tile.
@@ -42,7 +42,7 @@ struct Shape {
     static constexpr int GROUPS = 2;
     static constexpr int TK = F8 ? 128 : 64;                // keys per tile
     static constexpr int KS = TK / 4, NT = KS / 8;          // keys of a warp, in column tiles of 8
-    static constexpr int CWARPS = 4 * GROUPS, THREADS = (CWARPS + 1) * 32;
+    static constexpr int CWARPS = 4 * GROUPS, THREADS = (CWARPS + 2) * 32;
     static constexpr int ROW = D * (F8 ? 1 : 2);            // bytes of a key
     static constexpr int BOX = ROW < 128 ? 64 : 128;        // bytes of a box row (= swizzle width)
     static constexpr int TILE = TK * ROW;                   // K or V of one tile
@@ -195,7 +195,7 @@ __global__ void __launch_bounds__(Shape<D, F8, WIDE>::THREADS, 1)
     uint64_t *q_full = empty + STAGES, *q_empty = q_full + 2;
     volatile int *abort = reinterpret_cast<volatile int *>(q_empty + 2);
     int *s_last = const_cast<int *>(abort) + 1;   // [2]
-    int *s_warp = s_last + 2;   // [CWARPS + 1] scan of the warps' sums
+    int *s_warp = s_last + 2;   // [CWARPS + 2] scan of the warps' sums
 
     const AttentionDecode &p = a.p;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -206,7 +206,7 @@ __global__ void __launch_bounds__(Shape<D, F8, WIDE>::THREADS, 1)
         prefetch_tmap(&tmK);
         prefetch_tmap(&tmV);
         for (int i = 0; i < STAGES; ++i) {
-            mbar_init(full + i, 1);
+            mbar_init(full + i, 2);
             mbar_init(empty + i, 4);
         }
         for (int i = 0; i < 2; ++i) {
@@ -270,8 +270,9 @@ __global__ void __launch_bounds__(Shape<D, F8, WIDE>::THREADS, 1)
     Walk<TK> w;
     w.start(t0, pre, lens, p.n_seqs);
 
-    if (warp == CWARPS) {
-        // ------------------------------------------------ producer
+    if (warp >= CWARPS) {
+        // ------------------------------------------------ producers: q and K, V
+        const bool is_v = warp > CWARPS;
         // A batch of 32 boxes, one per lane, is looked up while the batch before it is issued: a lane
         // finds its tile's segment and its box's page, and later issues that box itself.
         const int tile_shift = (TK == 128 ? 7 : 6) - a.box_shift;   // log2 of the boxes of a tile
@@ -303,7 +304,7 @@ __global__ void __launch_bounds__(Shape<D, F8, WIDE>::THREADS, 1)
             for (int i = 0; i < per && tb + i < t1; ++i) {
                 // a segment's q rows come first, into one of two buffers
                 const int qb = __shfl_sync(0xffffffffu, cur.b, i * boxes), qu = __shfl_sync(0xffffffffu, cur.u, i * boxes);
-                if (qb >= 0) {
+                if (qb >= 0 && !is_v) {
                     const int buf = segs & 1;
                     if (segs > 1) ok = mbar_wait(q_empty + buf, ((segs >> 1) - 1) & 1, abort);
                     ok = __all_sync(0xffffffffu, ok);
@@ -321,8 +322,8 @@ __global__ void __launch_bounds__(Shape<D, F8, WIDE>::THREADS, 1)
                 if (round > 0) ok = mbar_wait(empty + stage, (round - 1) & 1, abort);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
-                uint8_t *k = smem + stage * 2 * S::TILE, *v = k + S::TILE;
-                if (lane == i * boxes) mbar_arrive_expect_tx(full + stage, (cur.n << a.box_shift) * S::ROW * 2);
+                uint8_t *tile = smem + (stage * 2 + is_v) * S::TILE;
+                if (lane == i * boxes) mbar_arrive_expect_tx(full + stage, (cur.n << a.box_shift) * S::ROW);
                 __syncwarp();
                 if (my_tile == i && my_box < cur.n) {
                     int page = cur.page;
@@ -331,12 +332,9 @@ __global__ void __launch_bounds__(Shape<D, F8, WIDE>::THREADS, 1)
                         page = p.cache.num_pages;   // outside the map: the box is filled with zeros
                     }
                     #pragma unroll
-                    for (int x = 0; x < S::ROW / S::BOX; ++x) {
-                        const int off = x * (TK * S::BOX) + (my_box << a.box_shift) * S::BOX;
-                        const int col = x * (S::BOX / (F8 ? 1 : 2));
-                        tma_load_4d(k + off, &tmK, full + stage, col, cur.place, cur.head, page);
-                        tma_load_4d(v + off, &tmV, full + stage, col, cur.place, cur.head, page);
-                    }
+                    for (int x = 0; x < S::ROW / S::BOX; ++x)
+                        tma_load_4d(tile + x * (TK * S::BOX) + (my_box << a.box_shift) * S::BOX, is_v ? &tmV : &tmK,
+                                    full + stage, x * (S::BOX / (F8 ? 1 : 2)), cur.place, cur.head, page);
                 }
                 if (++stage == STAGES) stage = 0, ++round;
             }
@@ -782,7 +780,7 @@ struct Layout {
 };
 Layout layout(int ctas, int n_seqs, int nq, int max_len, bool weights) {
     Layout y;
-    y.part = MAX_CTAS * sizeof(uint32_t);
+    y.part = 3 * MAX_CTAS * sizeof(uint32_t);
     y.ml = y.part + (size_t)ctas * 2 * PART_ROWS * 128 * sizeof(float);
     y.stat = y.ml + up256((size_t)ctas * 2 * PART_ROWS * sizeof(float2));
     y.ld_scores = (max_len + WK - 1) / WK * WK;
