@@ -84,8 +84,9 @@ class KVCache(ctypes.Structure):
             raise ValueError("KVCache: k and v differ in shape, type or strides")
         if k.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
             raise ValueError(f"KVCache: bfloat16 or float8_e4m3fn, not {k.dtype}")
-        stride = k.stride(0) if pages > 1 else max(k.stride(0), heads * size * dim)
-        if pages and k.stride()[1:] != (size * dim, dim, 1):
+        dense = (heads * size * dim, size * dim, dim, 1)
+        stride = k.stride(0) if pages > 1 else dense[0]
+        if any(n > 1 and st != d for n, st, d in zip(k.shape[1:], k.stride()[1:], dense[1:])):
             raise ValueError("KVCache: the heads, places and elements of a page must be contiguous")
         for t in (k_scale, v_scale):
             if t is not None and (t.dtype != torch.float32 or t.shape != (heads,) or not t.is_contiguous()):

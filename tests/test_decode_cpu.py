@@ -177,6 +177,11 @@ def test_kv_cache_checks_its_tensors(Q):
     assert (c.num_pages, c.n_kv_heads, c.page_size, c.head_dim, c.dtype, c.page_stride) == (3, 2, 16, 64, 0, 2048)
     both = torch.zeros(3, 2, 2, 16, 64, dtype=torch.bfloat16)             # K and V side by side
     assert Q.KVCache(both[:, 0], both[:, 1]).page_stride == 4096
+    one = torch.zeros(3, 16, 2, 64, dtype=torch.bfloat16)[:, :, :1].transpose(1, 2)     # one head: places 128 apart
+    with pytest.raises(ValueError):
+        Q.KVCache(one, one)
+    one = torch.zeros(16, 1, 64, dtype=torch.bfloat16).as_strided((1, 1, 16, 64), (7, 5, 64, 1))   # strides of size 1
+    assert Q.KVCache(one, one).page_stride == 16 * 64
     s = torch.ones(2)
     assert Q.KVCache(k.to(torch.float8_e4m3fn), k.to(torch.float8_e4m3fn), s, s).dtype == 2
     for a, b, ks, vs in ((k, k[:2], None, None), (k.half(), k.half(), None, None), (k, k.float(), None, None),

@@ -244,6 +244,7 @@ CASES = [
     ([15, 16, 17, 33, 250, 0, 0], 4, 2, 64, BF16, 16), ([700, 3, 511], 16, 16, 64, E4M3, 128),
     ([300, 999, 64], 64, 8, 128, E4M3, 16), ([513, 77], 32, 1, 64, BF16, 256), ([200, 1000], 48, 2, 128, BF16, 64),
     ([345, 12], 40, 1, 128, E4M3, 32), ([20000], 8, 1, 128, BF16, 128), ([9001], 12, 4, 64, E4M3, 64),
+    ([9000, 30000], 12, 1, 64, BF16, 32), ([40000], 16, 1, 128, BF16, 64), ([30000, 5], 24, 2, 128, E4M3, 16),
     ([5000, 1, 0, 3333], 28, 4, 128, BF16, 256), ([31] * 200, 2, 1, 64, BF16, 16), ([130] * 70 + [0] * 9, 8, 4, 128, BF16, 64),
 ]
 
@@ -424,6 +425,33 @@ def test_attention_decode_calls_of_other_sizes_share_a_workspace():
             _check_attention(o, q, kv, seq.tolist(), nq, d, None, w)
 
 
+def test_attention_decode_on_two_streams_at_once():
+    """Calls on two streams, each with its own workspace and outputs, against the same calls alone."""
+    cases = [_attend_case(_gen(40 + i), [3000, 17, 900], 16, 2, 128, BF16, 64) for i in range(2)]
+    spaces = [_workspace(3, 16, 3000, True) for _ in cases]
+    outs = [(torch.empty(3, 16 * 128, device="cuda", dtype=torch.bfloat16), torch.zeros(3, 3000, device="cuda")) for _ in cases]
+
+    def call(i, o, w):
+        cache, table, seq, q, _ = cases[i]
+        Q.h3enc_op_attention_decode(q, o, cache, table, seq, 16, 3000, spaces[i], None, w)
+
+    alone = []
+    for i in range(2):
+        call(i, *outs[i])
+        alone.append([t.clone() for t in outs[i]])
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    for _ in range(20):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                for t in outs[i]:
+                    t.zero_()
+                call(i, *outs[i])
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(a, b) for a, b in zip(outs[i], alone[i]))
+
+
 def test_attention_decode_refuses_a_small_or_misaligned_workspace():
     cache, table, seq, q, _ = _attend_case(_gen(15), [50], 8, 2, 64, BF16, 16)
     o = torch.empty(1, 8 * 64, device="cuda", dtype=torch.bfloat16)
@@ -458,7 +486,7 @@ def _weights(g, n, cols, kind):
     ([2100, 2049, 2048], 1, 64, BF16, 256, 2048, 0, 1, "equal"),
     ([777], 3, 128, BF16, 16, 1, 0, 0, "odd"), ([1500, 1024], 2, 64, BF16, 64, 1023, 7, 0, "odd"),
     ([9000], 1, 128, BF16, 128, 4500, 16, 512, "ties"), ([33000], 1, 64, E4M3, 256, 8000, 4, 64, "spread"),
-    ([70000, 100], 1, 64, E4M3, 256, 100, 1, 1, "odd")])
+    ([70000, 100], 1, 64, E4M3, 256, 100, 1, 1, "odd"), ([400000, 270001], 1, 64, E4M3, 256, 150000, 9, 5000, "ties")])
 @pytest.mark.parametrize("in_place", [True, False])
 def test_cache_evict(lens, nkv, d, dtype, page, budget, sink, recent, kind, in_place):
     g = _gen(sum(lens) + budget)
@@ -528,6 +556,56 @@ def test_cache_evict_bad_pages_and_lengths_are_reported():
 
 
 # ---------------------------------------------------------------- together
+
+def test_decode_step_captured_in_a_graph():
+    """One decode step (norm, rotation and store; attention with weights; eviction into other pages)
+    captured once and replayed on other projections, slots, lengths and weights, against the eager calls."""
+    g = _gen(31)
+    n, nq, nkv, d, page, top, budget = 3, 16, 4, 64, 16, 200, 96
+    cols, out_cols = -(-top // page), -(-budget // page)
+    pages = n * (cols + out_cols)
+    wq, wk = ((1 + 0.1 * torch.randn(2, d, device="cuda", generator=g)).to(torch.bfloat16)).unbind(0)
+    ids = torch.randperm(pages, device="cuda", generator=g).to(torch.int32)
+    table, out = ids[:n * cols].view(n, cols), ids[n * cols:].view(n, out_cols)
+    ws = _workspace(n, nq, top, True)
+
+    def fresh(seed):
+        h = _gen(seed)
+        lens = torch.randint(1, top, (n,), device="cuda", generator=h, dtype=torch.int32)
+        at = (lens - 1).long()
+        return dict(kv=_randn(h, 2, pages, nkv, page, d), qkv=_randn(h, n, (nq + 2 * nkv) * d), lens=lens,
+                    slots=(table[torch.arange(n, device="cuda"), at // page] * page + at % page).to(torch.int32),
+                    cos=torch.randn(n, d // 2, device="cuda", generator=h).cos(), sin=torch.zeros(n, d // 2, device="cuda"),
+                    w=torch.rand(n, top, device="cuda", generator=h), w2=torch.zeros(n, top, device="cuda"),
+                    o=torch.zeros(n, nq * d, device="cuda", dtype=torch.bfloat16), q=torch.zeros(n, nq * d, device="cuda",
+                                                                                                dtype=torch.bfloat16),
+                    kept=torch.zeros(n, budget, device="cuda", dtype=torch.int32),
+                    new=torch.zeros(n, device="cuda", dtype=torch.int32))
+
+    def step(s):
+        cache = Q.KVCache(s["kv"][0], s["kv"][1])
+        Q.h3enc_op_qk_norm_rope(s["qkv"], n, nq, nkv, d, wq, wk, 1e-6, s["cos"], s["sin"], 0, s["q"], cache=cache,
+                                slots=s["slots"])
+        Q.h3enc_op_attention_decode(s["q"], s["o"], cache, table, s["lens"], nq, top, ws, s["w"], s["w"])
+        Q.h3enc_op_cache_evict(cache, table, s["lens"], top, budget, s["w"], s["w2"], s["kept"], s["new"],
+                               page_table_out=out, sink=2, recent=20)
+
+    static = fresh(0)
+    step(static)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(static)
+    for seed in (1, 2, 3):
+        want, start = fresh(seed), fresh(seed)
+        step(want)
+        for name, t in start.items():
+            static[name].copy_(t)
+        graph.replay()
+        torch.cuda.synchronize()
+        for name, t in want.items():
+            assert torch.equal(static[name], t), name
+
 
 @pytest.mark.parametrize("dtype,heads", [(BF16, (8, 2, 64)), (E4M3, (16, 2, 128))])
 def test_prompt_then_decode_with_eviction(dtype, heads):
