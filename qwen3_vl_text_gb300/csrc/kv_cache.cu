@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(QK_THREADS) qk_norm_rope_kernel(const QkNormRo
 constexpr int SEL_THREADS = 1024;
 constexpr int SEL_BLOCK = 32 * SEL_THREADS;   // tokens of one block of the placing pass
 constexpr int SEL_CACHE = 45056;              // weights a CTA holds in shared memory (176 KB)
-constexpr int SEL_PER_CTA = 8192;             // tokens per CTA from which the cluster grows
+constexpr int SEL_PER_CTA = 4096;             // tokens per CTA from which the cluster grows
 constexpr int BINS = 2048;
 
 // Order of the weights as unsigned integers: larger key, larger weight; both zeros alike, NaN lowest.
@@ -210,7 +210,7 @@ __device__ __forceinline__ void add_cluster(uint32_t *p, uint32_t rank, uint32_t
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
-// One cluster of 1 to 8 CTAs per sequence, each with a contiguous part of its tokens, whose weights
+// One CTA, or a cluster of up to 16, per sequence, each with a contiguous part of its tokens, whose weights
 // it holds in shared memory (what does not fit is read again).  The budget-th largest key of the
 // unprotected tokens is found in up to three digits (11, 11 and 10 bits): a histogram of the tokens that
 // match the digits so far, scanned from the top by all threads; it ends early when the digit's whole bin is
@@ -438,27 +438,43 @@ __global__ void __launch_bounds__(MOVE_THREADS) evict_move_kernel(const CacheEvi
     }
 }
 
+constexpr int SEL_RANKS = 16;   // CTAs of a cluster, at most; more than 8 where the device can place such a cluster
+
 template <bool CLUSTER>
 cudaError_t launch_select(const CacheEvict &p, int ranks, cudaStream_t st) {
-    static std::atomic<bool> ready[kMaxDevices];   // the shared-memory opt-in, per device
+    static std::atomic<int> most[kMaxDevices];   // per device, once its shared memory is opted in: the largest cluster
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
-    if (!ready[dev].load()) {
+    cudaLaunchAttribute at[2];
+    const auto config = [&](int r, size_t bytes) {
+        cudaLaunchConfig_t cfg = pdl_config(dim3(r, p.n_seqs), dim3(SEL_THREADS), bytes, st, at);
+        if (CLUSTER) {
+            at[1].id = cudaLaunchAttributeClusterDimension;
+            at[1].val.clusterDim.x = r;
+            at[1].val.clusterDim.y = 1;
+            at[1].val.clusterDim.z = 1;
+            cfg.numAttrs = 2;
+        }
+        return cfg;
+    };
+    if (most[dev].load() == 0) {
         cudaError_t e = cudaFuncSetAttribute(evict_select_kernel<CLUSTER>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              SEL_CACHE * 4);
         if (e != cudaSuccess) return e;
-        ready[dev].store(true);
+        int found = 8;
+        if (CLUSTER && cudaFuncSetAttribute(evict_select_kernel<CLUSTER>, cudaFuncAttributeNonPortableClusterSizeAllowed,
+                                            1) == cudaSuccess) {
+            int clusters = 0;
+            const cudaLaunchConfig_t cfg = config(SEL_RANKS, SEL_CACHE * 4);
+            if (cudaOccupancyMaxActiveClusters(&clusters, evict_select_kernel<CLUSTER>, &cfg) == cudaSuccess && clusters > 0)
+                found = SEL_RANKS;
+        }
+        cudaGetLastError();   // a refused size leaves an error behind
+        most[dev].store(found);
     }
+    if (ranks > most[dev].load()) ranks = most[dev].load();
     const int per = (p.max_len + ranks - 1) / ranks, cached = per < SEL_CACHE ? per : SEL_CACHE;
-    cudaLaunchAttribute at[2];
-    cudaLaunchConfig_t cfg = pdl_config(dim3(ranks, p.n_seqs), dim3(SEL_THREADS), (size_t)cached * 4, st, at);
-    if (CLUSTER) {
-        at[1].id = cudaLaunchAttributeClusterDimension;
-        at[1].val.clusterDim.x = ranks;
-        at[1].val.clusterDim.y = 1;
-        at[1].val.clusterDim.z = 1;
-        cfg.numAttrs = 2;
-    }
+    const cudaLaunchConfig_t cfg = config(ranks, (size_t)cached * 4);
     return cudaLaunchKernelEx(&cfg, evict_select_kernel<CLUSTER>, p, cached);
 }
 
@@ -489,7 +505,7 @@ cudaError_t launch_qk_norm_rope(const QkNormRope &p, cudaStream_t st) {
 cudaError_t launch_cache_evict(const CacheEvict &p, cudaStream_t st) {
     if (p.n_seqs <= 0) return cudaSuccess;
     int ranks = 1;
-    while (ranks < 8 && p.max_len > ranks * SEL_PER_CTA) ranks *= 2;
+    while (ranks < SEL_RANKS && p.max_len > ranks * SEL_PER_CTA) ranks *= 2;
     cudaError_t e = ranks > 1 ? launch_select<true>(p, ranks, st) : launch_select<false>(p, 1, st);
     if (e != cudaSuccess || p.max_len == 0) return e;
     // planes of a chunk over several CTAs where the chunks alone are too few to fill the SMs
