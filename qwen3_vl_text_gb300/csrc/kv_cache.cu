@@ -8,6 +8,7 @@
 // _apply_rotary_pos_emb); the pages hold no cache.
 #include <cuda_fp8.h>
 
+#include <algorithm>
 #include <atomic>
 
 #include "common.cuh"
@@ -378,61 +379,116 @@ __global__ void __launch_bounds__(SEL_THREADS, 1) evict_select_kernel(const Cach
 
 constexpr int MOVE_THREADS = 256;
 
-// Moves rows of the kept tokens: a chunk of CHUNK_VECS / (16-byte vectors of a row) tokens at a time, whose
-// source and target places are looked up once and serve the chunk's rows of the CTA's planes (K and V
-// of the kv heads blockIdx.y, + gridDim.y, ...).  In place (gridDim.x = 1) a CTA takes the chunks in
-// order: a token moves to its own index or a smaller one, so no source of a chunk lies before the
-// chunk's first token, where the stores of earlier chunks end; the barrier keeps a chunk's own stores
-// behind its loads.  Bound by the bytes: every row is read and written once.
-template <bool IN_PLACE>
-__global__ void __launch_bounds__(MOVE_THREADS) evict_move_kernel(const CacheEvict p) {
-    constexpr int VECS = IN_PLACE ? 8 : 4;              // 16-byte vectors of a plane per thread
-    constexpr int CHUNK_VECS = MOVE_THREADS * VECS, MAX_ROWS = CHUNK_VECS / 4;
-    __shared__ long long s_src[MAX_ROWS], s_dst[MAX_ROWS];   // byte offsets in the pool (kv head 0), -1: no move
+// Where the rows (of kv head 0) of the kept tokens i0 + r were and go, r = tid, tid + MOVE_THREADS, ... < rows, as byte
+// offsets in the pool; to: -1 if the token does not move.  All loads of a step are in flight together.
+template <int MAX_ROWS>
+__device__ __forceinline__ void look_up(const CacheEvict &p, int b, int i0, int rows, int n, const int32_t *table_out,
+                                        long long *from, long long *to) {
+    constexpr int N = (MAX_ROWS + MOVE_THREADS - 1) / MOVE_THREADS;
+    const int shift = p.cache.page_shift, mask = (1 << shift) - 1;
+    const int row_bytes = p.cache.d * (p.cache.f8 ? 1 : 2);
+    const long long page_bytes = p.cache.page_stride * (p.cache.f8 ? 1 : 2);
+    int k[N], src[N], dst[N];
+    #pragma unroll
+    for (int j = 0; j < N; ++j) {
+        const int r = threadIdx.x + j * MOVE_THREADS;
+        k[j] = r < rows && i0 + r < n ? p.kept[b * p.ld_kept + i0 + r] : -1;
+    }
+    #pragma unroll
+    for (int j = 0; j < N; ++j) {
+        src[j] = k[j] >= 0 ? p.table[(long long)b * p.ld_table + (k[j] >> shift)] : -1;
+        dst[j] = k[j] >= 0 ? table_out[(i0 + (int)threadIdx.x + j * MOVE_THREADS) >> shift] : -1;
+    }
+    #pragma unroll
+    for (int j = 0; j < N; ++j) {
+        const int r = threadIdx.x + j * MOVE_THREADS;
+        long long f = -1, t = -1;
+        if (k[j] >= 0) {
+            if (src[j] < 0 || src[j] >= p.cache.num_pages || dst[j] < 0 || dst[j] >= p.cache.num_pages) {
+                report(p.status, ST_BOUNDS);
+            } else {
+                f = src[j] * page_bytes + (long long)(k[j] & mask) * row_bytes;
+                t = dst[j] * page_bytes + (long long)((i0 + r) & mask) * row_bytes;
+                if (f == t) t = -1;   // already there
+            }
+        }
+        if (r < rows) {
+            from[r] = f;
+            to[r] = t;
+        }
+    }
+}
+
+// Copies the kept tokens into other pages: a CTA looks up the places of a chunk of tokens once and moves the
+// chunk's rows of K and V of the kv heads (planes blockIdx.y, + gridDim.y, ...).  Bound by the bytes: every row is
+// read and written once (32 sequences of 4096 tokens of 4 KB: 158 us, 6.8 TB/s).
+__global__ void __launch_bounds__(MOVE_THREADS) evict_copy_kernel(const CacheEvict p) {
+    constexpr int VECS = 4, MAX_ROWS = MOVE_THREADS * VECS / 4;   // 16-byte vectors of a plane per thread; rows of 4 vectors
+    __shared__ long long s_src[MAX_ROWS], s_dst[MAX_ROWS];
     pdl_trigger();
     pdl_wait();
     const int b = blockIdx.z, tid = threadIdx.x;
-    const int shift = p.cache.page_shift, mask = (1 << shift) - 1;
-    const int row_bytes = p.cache.d * (p.cache.f8 ? 1 : 2), row_shift = 31 - __clz(row_bytes / 16);   // 4, 8 or 16 vectors
-    const long long page_bytes = p.cache.page_stride * (p.cache.f8 ? 1 : 2);
-    const long long head_bytes = (long long)row_bytes << shift;
-    const int rows = CHUNK_VECS >> row_shift;
-    const int n = p.new_lens[b];
-    const int32_t *kept = p.kept + b * p.ld_kept;
-    const int32_t *ti = p.table + (long long)b * p.ld_table;
-    const int32_t *to = IN_PLACE ? ti : p.table_out + (long long)b * p.ld_table_out;
-    const int planes = 2 * p.cache.nkv, vec = (tid & ((1 << row_shift) - 1)) * 16;
-    for (int r0 = blockIdx.x * rows; r0 < n; r0 += rows * gridDim.x) {
-        __syncthreads();
-        for (int r = tid; r < rows; r += MOVE_THREADS) {
-            long long src = -1, dst = -1;
-            if (r0 + r < n) {
-                const int from = kept[r0 + r], a = ti[from >> shift], c = to[(r0 + r) >> shift];
-                if (a < 0 || a >= p.cache.num_pages || c < 0 || c >= p.cache.num_pages) {
-                    report(p.status, ST_BOUNDS);
-                } else {
-                    src = a * page_bytes + (long long)(from & mask) * row_bytes;
-                    dst = c * page_bytes + (long long)((r0 + r) & mask) * row_bytes;
-                    if (src == dst) dst = -1;   // already there
-                }
-            }
-            s_src[r] = src;
-            s_dst[r] = dst;
+    const int row_bytes = p.cache.d * (p.cache.f8 ? 1 : 2), vec_shift = 31 - __clz(row_bytes / 16);
+    const long long head_bytes = (long long)row_bytes << p.cache.page_shift;
+    const int rows = (MOVE_THREADS * VECS) >> vec_shift, r0 = blockIdx.x * rows, n = p.new_lens[b];
+    if (r0 >= n) return;
+    look_up<MAX_ROWS>(p, b, r0, rows, n, p.table_out + (long long)b * p.ld_table_out, s_src, s_dst);
+    __syncthreads();
+    for (int q = blockIdx.y; q < 2 * p.cache.nkv; q += gridDim.y) {
+        char *pool = static_cast<char *>((q & 1) ? p.cache.v : p.cache.k) + (q >> 1) * head_bytes +
+                     (tid & ((1 << vec_shift) - 1)) * 16;
+        uint4 v[VECS];
+        #pragma unroll
+        for (int k = 0; k < VECS; ++k) {
+            const int r = (k * MOVE_THREADS + tid) >> vec_shift;
+            if (s_dst[r] >= 0) v[k] = *reinterpret_cast<const uint4 *>(pool + s_src[r]);
         }
+        #pragma unroll
+        for (int k = 0; k < VECS; ++k) {
+            const int r = (k * MOVE_THREADS + tid) >> vec_shift;
+            if (s_dst[r] >= 0) *reinterpret_cast<uint4 *>(pool + s_dst[r]) = v[k];
+        }
+    }
+}
+
+// Packs the kept tokens in place.  A CTA takes a slice (2^slice_shift 16-byte vectors) of one plane's rows through
+// all chunks of tokens in order: a token moves to its own index or a smaller one, so no source of a chunk lies
+// before the chunk's first token, where the stores of earlier chunks end; the barrier keeps a chunk's own
+// stores behind its loads.  With few sequences the chain of chunks bounds it, so the slices are then narrow, the
+// chunks long, and the places of the next chunk looked up while this one's rows are loaded (one sequence of
+// 4608 tokens cut to 4096, both launches: 23 us, with whole rows and nothing ahead 52 us; 32 of them 149 us).
+__global__ void __launch_bounds__(MOVE_THREADS, 4) evict_pack_kernel(const CacheEvict p, int slice_shift) {
+    constexpr int VECS = 8, MAX_ROWS = MOVE_THREADS * VECS / 2;
+    __shared__ long long s_src[2][MAX_ROWS], s_dst[2][MAX_ROWS];
+    pdl_trigger();
+    pdl_wait();
+    const int b = blockIdx.z, tid = threadIdx.x;
+    const int row_bytes = p.cache.d * (p.cache.f8 ? 1 : 2), slices = (row_bytes / 16) >> slice_shift;
+    const long long head_bytes = (long long)row_bytes << p.cache.page_shift;
+    const int rows = (MOVE_THREADS * VECS) >> slice_shift, n = p.new_lens[b];
+    const auto next = [&](int r0, int buf) {
+        look_up<MAX_ROWS>(p, b, r0, rows, n, p.table + (long long)b * p.ld_table, s_src[buf], s_dst[buf]);
+    };
+    for (int q = blockIdx.y; q < 2 * p.cache.nkv * slices; q += gridDim.y) {
+        const int slice = q % slices, plane = q / slices;
+        char *pool = static_cast<char *>((plane & 1) ? p.cache.v : p.cache.k) + (plane >> 1) * head_bytes +
+                     ((slice << slice_shift) + (tid & ((1 << slice_shift) - 1))) * 16;
         __syncthreads();
-        for (int q = blockIdx.y; q < planes; q += gridDim.y) {
-            char *pool = static_cast<char *>((q & 1) ? p.cache.v : p.cache.k) + (q >> 1) * head_bytes + vec;
+        next(0, 0);
+        __syncthreads();
+        for (int r0 = 0, buf = 0; r0 < n; r0 += rows, buf ^= 1) {
             uint4 v[VECS];
             #pragma unroll
             for (int k = 0; k < VECS; ++k) {
-                const int r = (k * MOVE_THREADS + tid) >> row_shift;
-                if (s_dst[r] >= 0) v[k] = *reinterpret_cast<const uint4 *>(pool + s_src[r]);
+                const int r = (k * MOVE_THREADS + tid) >> slice_shift;
+                if (s_dst[buf][r] >= 0) v[k] = *reinterpret_cast<const uint4 *>(pool + s_src[buf][r]);
             }
-            if (IN_PLACE) __syncthreads();
+            if (r0 + rows < n) next(r0 + rows, buf ^ 1);
+            __syncthreads();
             #pragma unroll
             for (int k = 0; k < VECS; ++k) {
-                const int r = (k * MOVE_THREADS + tid) >> row_shift;
-                if (s_dst[r] >= 0) *reinterpret_cast<uint4 *>(pool + s_dst[r]) = v[k];
+                const int r = (k * MOVE_THREADS + tid) >> slice_shift;
+                if (s_dst[buf][r] >= 0) *reinterpret_cast<uint4 *>(pool + s_dst[buf][r]) = v[k];
             }
         }
     }
@@ -508,17 +564,25 @@ cudaError_t launch_cache_evict(const CacheEvict &p, cudaStream_t st) {
     while (ranks < SEL_RANKS && p.max_len > ranks * SEL_PER_CTA) ranks *= 2;
     cudaError_t e = ranks > 1 ? launch_select<true>(p, ranks, st) : launch_select<false>(p, 1, st);
     if (e != cudaSuccess || p.max_len == 0) return e;
-    // planes of a chunk over several CTAs where the chunks alone are too few to fill the SMs
-    const int row_vecs = p.cache.d * (p.cache.f8 ? 1 : 2) / 16, planes = 2 * p.cache.nkv;
+    const int row_vecs = p.cache.d * (p.cache.f8 ? 1 : 2) / 16, sms = device_num_sms();   // 4, 8 or 16
     const int most = p.budget < p.max_len ? p.budget : p.max_len;
-    const int rows = MOVE_THREADS * 4 / row_vecs, chunks = p.table_out ? (most + rows - 1) / rows : 1;
-    const long long ctas = (long long)chunks * p.n_seqs, want = 8LL * device_num_sms();
-    int gy = (int)(ctas >= want ? 1 : (want + ctas - 1) / ctas);
-    if (gy > planes) gy = planes;
-    if (!p.table_out) gy = planes < 65535 ? planes : 65535;
+    const int vec_shift = 31 - __builtin_clz((unsigned)row_vecs);
+    const long long planes = 2LL * p.cache.nkv;
     cudaLaunchAttribute at[1];
-    cudaLaunchConfig_t cfg = pdl_config(dim3(chunks, gy, p.n_seqs), dim3(MOVE_THREADS), 0, st, at);
-    return cudaLaunchKernelEx(&cfg, p.table_out ? evict_move_kernel<false> : evict_move_kernel<true>, p);
+    if (p.table_out) {
+        // the planes of a chunk over several CTAs where the chunks alone are too few to fill the SMs
+        const int rows = (MOVE_THREADS * 4) >> vec_shift, chunks = (most + rows - 1) / rows;
+        const long long ctas = (long long)chunks * p.n_seqs, want = 8LL * sms;
+        const long long gy = std::min(planes, ctas >= want ? 1 : (want + ctas - 1) / ctas);
+        cudaLaunchConfig_t cfg = pdl_config(dim3(chunks, (unsigned)gy, p.n_seqs), dim3(MOVE_THREADS), 0, st, at);
+        return cudaLaunchKernelEx(&cfg, evict_copy_kernel, p);
+    }
+    // slices down to a sector of 32 bytes where the planes alone are too few
+    int slice_shift = vec_shift;
+    while (slice_shift > 1 && (planes << (vec_shift - slice_shift)) * p.n_seqs < 2 * sms) --slice_shift;
+    const long long gy = std::min(planes << (vec_shift - slice_shift), 65535LL);
+    cudaLaunchConfig_t cfg = pdl_config(dim3(1, (unsigned)gy, p.n_seqs), dim3(MOVE_THREADS), 0, st, at);
+    return cudaLaunchKernelEx(&cfg, evict_pack_kernel, p, slice_shift);
 }
 
 }  // namespace h3
