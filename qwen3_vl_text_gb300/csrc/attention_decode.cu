@@ -21,6 +21,11 @@
 //    P's rounding remainder p - bf16(p) instead, so the value product loses nothing to the 8-bit mantissa
 //    at no cost (more than 8 heads: a second product).  e4m3 values are exact in f16, so that path
 //    runs in f16, with q scaled by a power of two per head into f16's range.
+// Measured (64 q heads over 8 kv heads of 128, pages of 64): 64 sequences of 5000 to 8192 tokens in bf16, 1.7 GB,
+// 248-251 us = 6.8 TB/s, the measured copy rate; in e4m3 140 us (5.9 TB/s: the conversions of every key and value
+// to f16 then take most of the time between two tiles); one sequence of 1025 tokens 7.2 us, which is
+// the chain length -> page number -> tile -> products -> join across CTAs.  A call's fixed part is about
+// 8 us: 2.5 until the first tile lands, the rest the joins at the end and the spread of the SMs' rates.
 #include <algorithm>
 #include <atomic>
 #include <climits>
