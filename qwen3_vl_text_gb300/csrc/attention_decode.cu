@@ -40,38 +40,43 @@ namespace {
 
 constexpr int WK = 128;                 // keys per CTA of the weight sums; score rows are padded to it
 constexpr int MAX_CTAS = 1024;          // arrival counters at the head of the workspace
-constexpr int PART_ROWS = 16;           // heads of a segment
+constexpr int WROWS = 16;               // heads of a warp: the rows of a product
+constexpr int MAX_ROWS = 32;            // heads of a segment, at most
 
-template <int D, bool F8, bool WIDE>
+// BLOCKS: blocks of 8 heads of a segment: 1, 2, or 4
+template <int D, bool F8, int BLOCKS>
 struct Shape {
-    // groups of four compute warps, which take the tiles of a run in turn
+    // Two groups of four compute warps.  Segments of up to 16 heads: they take the tiles of a run in turn.  Of up
+    // to 32 (SPLIT): both take every tile, 16 heads each, so that a key is read once for 32 heads.
     static constexpr int GROUPS = 2;
+    static constexpr bool SPLIT = BLOCKS == 4;
+    static constexpr int ROWS = SPLIT ? 32 : 16;            // rows kept for a segment's heads
     static constexpr int TK = F8 ? 128 : 64;                // keys per tile
     static constexpr int KS = TK / 4, NT = KS / 8;          // keys of a warp, in column tiles of 8
     static constexpr int CWARPS = 4 * GROUPS, THREADS = (CWARPS + 2) * 32;
     static constexpr int ROW = D * (F8 ? 1 : 2);            // bytes of a key
     static constexpr int BOX = ROW < 128 ? 64 : 128;        // bytes of a box row (= swizzle width)
     static constexpr int TILE = TK * ROW;                   // K or V of one tile
-    // a multiple of the groups: a stage then always serves the same group, which sees each of its phases
+    // a multiple of the groups: a stage then always serves the same group, or both, which see each of its phases
     static constexpr int STAGES = TILE >= 16384 ? 4 : 8;
     static constexpr int LDO = D + 8;                       // padded row of the output exchange
     static constexpr int OFF_O = STAGES * 2 * TILE;
     static constexpr int OFF_ML = OFF_O + CWARPS * 8 * LDO * 4;
-    static constexpr int OFF_PRE = OFF_ML + 2 * CWARPS * PART_ROWS * 4;
+    static constexpr int OFF_PRE = OFF_ML + 2 * CWARPS * WROWS * 4;
     static constexpr int OFF_LEN = OFF_PRE + (kMaxSeqs + 1) * 4;
     static constexpr int LDQ = 2 * D + 16;                  // padded row of q (bytes)
     static constexpr int OFF_Q = (OFF_LEN + kMaxSeqs * 4 + 15) & ~15;
-    static constexpr int OFF_BAR = OFF_Q + 2 * PART_ROWS * LDQ;
+    static constexpr int OFF_BAR = OFF_Q + 2 * ROWS * LDQ;
     static constexpr int BYTES = OFF_BAR + (2 * STAGES + 4) * 8 + 80 + 1024;   // + alignment of the base
 };
 
 struct Args {
     AttentionDecode p;
     int group;      // q heads per kv head
-    int chunks;     // segments per kv head: ceil(group / 16)
+    int chunks;     // segments per kv head: ceil(group / 16), or / 32 above 16
     int box_shift;  // log2 of the places of a page one box covers
-    float *part;    // [cta][2][16][D] partial outputs, unnormalised
-    float2 *ml;     // [cta][2][16] their running maximum and sum
+    float *part;    // [cta][2][ROWS][D] partial outputs, unnormalised
+    float2 *ml;     // [cta][2][ROWS] their running maximum and sum
     uint32_t *count;
     float2 *stat;   // [n_seqs][nq] (m, 1/l), with weights
     float *scores;  // [n_seqs][nq][ld_scores] scores in log2 units, with weights
@@ -148,8 +153,8 @@ __device__ __forceinline__ void compute_sync() {
 // Byte offset of 16-byte chunk c of row r in a tile of swizzled box rows.
 template <int D, bool F8>
 __device__ __forceinline__ uint32_t chunk_at(int r, int c) {
-    constexpr int TK = Shape<D, F8, false>::TK;
-    if constexpr (Shape<D, F8, false>::BOX == 128) return (c >> 3) * (TK * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+    constexpr int TK = Shape<D, F8, 1>::TK;
+    if constexpr (Shape<D, F8, 1>::BOX == 128) return (c >> 3) * (TK * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
     else return r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
 }
 
@@ -186,16 +191,17 @@ struct Walk {
     }
 };
 
-template <int D, bool F8, bool WIDE>   // WIDE: more than 8 heads in a segment
-__global__ void __launch_bounds__(Shape<D, F8, WIDE>::THREADS, 1)
+template <int D, bool F8, int BLOCKS>
+__global__ void __launch_bounds__(Shape<D, F8, BLOCKS>::THREADS, 1)
     attention_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                             const Args a) {
-    using S = Shape<D, F8, WIDE>;
-    constexpr int STAGES = S::STAGES, CWARPS = S::CWARPS, TK = S::TK, NT = S::NT;
+    using S = Shape<D, F8, BLOCKS>;
+    constexpr int STAGES = S::STAGES, CWARPS = S::CWARPS, TK = S::TK, NT = S::NT, ROWS = S::ROWS;
+    constexpr bool WIDE = BLOCKS > 1, SPLIT = S::SPLIT;   // WIDE: a warp has more than 8 heads
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     float *sm_o = reinterpret_cast<float *>(smem + S::OFF_O);
-    float *sm_m = reinterpret_cast<float *>(smem + S::OFF_ML), *sm_l = sm_m + CWARPS * PART_ROWS;
+    float *sm_m = reinterpret_cast<float *>(smem + S::OFF_ML), *sm_l = sm_m + CWARPS * WROWS;
     int *pre = reinterpret_cast<int *>(smem + S::OFF_PRE), *lens = reinterpret_cast<int *>(smem + S::OFF_LEN);
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + S::OFF_BAR), *empty = full + STAGES;
     uint64_t *q_full = empty + STAGES, *q_empty = q_full + 2;
@@ -213,7 +219,7 @@ __global__ void __launch_bounds__(Shape<D, F8, WIDE>::THREADS, 1)
         prefetch_tmap(&tmV);
         for (int i = 0; i < STAGES; ++i) {
             mbar_init(full + i, 2);
-            mbar_init(empty + i, 4);
+            mbar_init(empty + i, SPLIT ? CWARPS : 4);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(q_full + i, 1);
@@ -316,12 +322,12 @@ __global__ void __launch_bounds__(Shape<D, F8, WIDE>::THREADS, 1)
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
                     const int head = kv_head(qu), chunk = qu - head * a.chunks;
-                    const int rows = min(PART_ROWS, a.group - chunk * PART_ROWS);
+                    const int rows = min(ROWS, a.group - chunk * ROWS);
                     if (lane == 0) mbar_arrive_expect_tx(q_full + buf, rows * D * 2);
                     __syncwarp();
                     if (lane < rows)
-                        bulk_load(smem + S::OFF_Q + (buf * PART_ROWS + lane) * S::LDQ,
-                                  p.q + qb * p.ld_q + (long long)(head * a.group + chunk * PART_ROWS + lane) * D, D * 2,
+                        bulk_load(smem + S::OFF_Q + (buf * ROWS + lane) * S::LDQ,
+                                  p.q + qb * p.ld_q + (long long)(head * a.group + chunk * ROWS + lane) * D, D * 2,
                                   q_full + buf);
                     ++segs;
                 }
@@ -366,6 +372,7 @@ __global__ void __launch_bounds__(Shape<D, F8, WIDE>::THREADS, 1)
     const int g = lane >> 2, tq = lane & 3;   // fragment row and column pair
     const float base_scale = 1.4426950408889634f / sqrtf((float)D);
     const int group = warp >> 2, slice = (warp & 3) * S::KS;
+    const int wrow = SPLIT ? group * WROWS : 0;   // this warp's first row of the segment's
     // this lane's row and 16-byte chunk in the ldmatrix of 16 keys: K (keys 0-7 / 8-15 as the column
     // tiles) and V (transposed, as the two halves of the contraction); e4m3 rows pair them the other way
     const int row_v = (lane & 7) + ((lane >> 3) & 1) * 8, chunk_v = lane >> 4;
@@ -396,8 +403,8 @@ __global__ void __launch_bounds__(Shape<D, F8, WIDE>::THREADS, 1)
     for (int t = t0; t < t1; ++segs) {
         const int seg = t - w.j, seg_end = seg + w.tiles;   // this segment's tiles in the whole row of tiles
         const int j1 = min(w.tiles, t1 - seg);              // this run's part of it: [w.j, j1)
-        const int kvh = kv_head(w.u), chunk = w.u - kvh * a.chunks, h0 = kvh * a.group + chunk * PART_ROWS;
-        const int rows = min(PART_ROWS, a.group - chunk * PART_ROWS);   // heads of the segment
+        const int kvh = kv_head(w.u), chunk = w.u - kvh * a.chunks, h0 = kvh * a.group + chunk * ROWS;
+        const int rows = min(ROWS, a.group - chunk * ROWS);   // heads of the segment
 
         // q as the A operand: rows = heads, the contraction over d in steps of 16
         uint32_t qa[D / 16][WIDE ? 4 : 2];
@@ -405,8 +412,8 @@ __global__ void __launch_bounds__(Shape<D, F8, WIDE>::THREADS, 1)
         {
             const float ks = F8 ? p.cache.k_scale[kvh] : 1.f;   // (its load goes out before the wait)
             if (!mbar_wait(q_full + (segs & 1), (segs >> 1) & 1, abort)) give_up();
-            const uint8_t *q0 = smem + S::OFF_Q + ((segs & 1) * PART_ROWS + g) * S::LDQ, *q1 = q0 + 8 * S::LDQ;
-            const bool in0 = g < rows, in1 = WIDE && g + 8 < rows;
+            const uint8_t *q0 = smem + S::OFF_Q + ((segs & 1) * ROWS + wrow + g) * S::LDQ, *q1 = q0 + 8 * S::LDQ;
+            const bool in0 = wrow + g < rows, in1 = WIDE && wrow + g + 8 < rows;
             #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
                 // bf16: columns 2t, 2t+1 and 2t+8, 2t+9 of the step; e4m3: 4t .. 4t+3 (the bytes a
@@ -456,7 +463,7 @@ __global__ void __launch_bounds__(Shape<D, F8, WIDE>::THREADS, 1)
         float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
 
         for (; w.j < j1; ++w.j, ++t, turn = turn + 1 == S::GROUPS ? 0 : turn + 1) {
-            if (turn == group) {
+            if (SPLIT || turn == group) {
                 if (!mbar_wait(full + stage, round & 1, abort)) give_up();
                 const int key0 = w.j * TK + slice;
                 if (key0 < w.len) {
@@ -508,9 +515,9 @@ __global__ void __launch_bounds__(Shape<D, F8, WIDE>::THREADS, 1)
                     if (a.scores) {
                         #pragma unroll
                         for (int n = 0; n < NT; ++n) {
-                            float *dst = a.scores + ((long long)w.b * p.nq + h0 + g) * a.ld_scores + key0 + 8 * n + 2 * tq;
-                            if (g < rows) *reinterpret_cast<float2 *>(dst) = make_float2(s[n][0], s[n][1]);
-                            if (WIDE && g + 8 < rows)
+                            float *dst = a.scores + ((long long)w.b * p.nq + h0 + wrow + g) * a.ld_scores + key0 + 8 * n + 2 * tq;
+                            if (wrow + g < rows) *reinterpret_cast<float2 *>(dst) = make_float2(s[n][0], s[n][1]);
+                            if (WIDE && wrow + g + 8 < rows)
                                 *reinterpret_cast<float2 *>(dst + 8 * a.ld_scores) = make_float2(s[n][2], s[n][3]);
                         }
                     }
@@ -615,10 +622,10 @@ __global__ void __launch_bounds__(Shape<D, F8, WIDE>::THREADS, 1)
             l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
         }
         if (tq == 0) {
-            sm_m[warp * PART_ROWS + g] = m0;
-            sm_l[warp * PART_ROWS + g] = l0;
-            sm_m[warp * PART_ROWS + g + 8] = m1;
-            sm_l[warp * PART_ROWS + g + 8] = l1;
+            sm_m[warp * WROWS + g] = m0;
+            sm_l[warp * WROWS + g] = l0;
+            sm_m[warp * WROWS + g + 8] = m1;
+            sm_l[warp * WROWS + g + 8] = l1;
         }
         compute_sync<CWARPS * 32>();
         const bool whole = seg >= t0 && seg_end <= t1;
@@ -627,9 +634,11 @@ __global__ void __launch_bounds__(Shape<D, F8, WIDE>::THREADS, 1)
         if (!whole) shared[seg < t0 ? 0 : 1] = Part{w.b, w.u, seg, seg_end};
         #pragma unroll
         for (int r8 = 0; r8 < (WIDE ? 16 : 8); r8 += 8) {
+            // the warps that share rows: all, or (SPLIT) those of a group
+            constexpr int SHARE = SPLIT ? 4 : CWARPS;
             float top = -INFINITY;
             #pragma unroll
-            for (int i = 0; i < CWARPS; ++i) top = fmaxf(top, sm_m[i * PART_ROWS + r8 + g]);
+            for (int i = 0; i < SHARE; ++i) top = fmaxf(top, sm_m[((SPLIT ? 4 * group : 0) + i) * WROWS + r8 + g]);
             const float mine = r8 ? m1 : m0, f = mine == -INFINITY ? 0.f : ex2(mine - top);
             float *dst = sm_o + (warp * 8 + g) * S::LDO;
             const auto out = [&](int i, int k) { return (WIDE ? o[i][r8 / 4 + k] : o[i][k] + o[i][k + 2]) * f; };
@@ -644,15 +653,18 @@ __global__ void __launch_bounds__(Shape<D, F8, WIDE>::THREADS, 1)
                 }
             }
             compute_sync<CWARPS * 32>();
-            if (trow < 8 && r8 + trow < rows) {
+            #pragma unroll
+            for (int q = 0; q < (SPLIT ? 2 : 1); ++q) {
+                const int row = q * WROWS + r8 + trow;
+                if (trow >= 8 || row >= rows) continue;
                 float mm = -INFINITY, ll = 0.f;
                 #pragma unroll
-                for (int i = 0; i < CWARPS; ++i) mm = fmaxf(mm, sm_m[i * PART_ROWS + r8 + trow]);
+                for (int i = q * 4; i < q * 4 + SHARE; ++i) mm = fmaxf(mm, sm_m[i * WROWS + r8 + trow]);
                 float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
                 #pragma unroll
-                for (int i = 0; i < CWARPS; ++i) {
-                    const float wm = sm_m[i * PART_ROWS + r8 + trow];
-                    ll += wm == -INFINITY ? 0.f : sm_l[i * PART_ROWS + r8 + trow] * ex2(wm - mm);
+                for (int i = q * 4; i < q * 4 + SHARE; ++i) {
+                    const float wm = sm_m[i * WROWS + r8 + trow];
+                    ll += wm == -INFINITY ? 0.f : sm_l[i * WROWS + r8 + trow] * ex2(wm - mm);
                     const float4 x = *reinterpret_cast<const float4 *>(sm_o + (i * 8 + trow) * S::LDO + tcol);
                     acc.x += x.x;
                     acc.y += x.y;
@@ -660,10 +672,10 @@ __global__ void __launch_bounds__(Shape<D, F8, WIDE>::THREADS, 1)
                     acc.w += x.w;
                 }
                 if (whole) {
-                    store(w.b, h0 + r8 + trow, acc, mm, ll, vs);
+                    store(w.b, h0 + row, acc, mm, ll, vs);
                 } else {
-                    *reinterpret_cast<float4 *>(a.part + ((long long)slot * PART_ROWS + r8 + trow) * D + tcol) = acc;
-                    if (tcol == 0) a.ml[slot * PART_ROWS + r8 + trow] = make_float2(mm, ll);
+                    *reinterpret_cast<float4 *>(a.part + ((long long)slot * ROWS + row) * D + tcol) = acc;
+                    if (tcol == 0) a.ml[slot * ROWS + row] = make_float2(mm, ll);
                 }
             }
             compute_sync<CWARPS * 32>();
@@ -705,7 +717,7 @@ __global__ void __launch_bounds__(Shape<D, F8, WIDE>::THREADS, 1)
         const Part y = x ? shared[1] : shared[0];
         const int first = owner(y.seg), n = owner(y.seg_end - 1) - first + 1, begin = group_of(first, n);
         const int kvh = kv_head(y.u), chunk = y.u - kvh * a.chunks;
-        const int rows = min(PART_ROWS, a.group - chunk * PART_ROWS);
+        const int rows = min(ROWS, a.group - chunk * ROWS);
         const float vs = F8 ? p.cache.v_scale[kvh] : 1.f;
         // The parts begin, begin + STEP, ... (count of them): up to BATCH at a time, all their loads in flight.  A lane
         // takes four columns of each, and of one part (lane li: part li of the batch) the row's maximum and sum.
@@ -713,10 +725,10 @@ __global__ void __launch_bounds__(Shape<D, F8, WIDE>::THREADS, 1)
             constexpr int STEP = decltype(step)::value;
             #pragma unroll 1
             for (int r0 = 0; r0 < rows; r0 += CWARPS * 32 / LPR) {
-                const int li = lane % LPR, row = (r0 + trow) % PART_ROWS;   // (rows past the segment's last: not stored)
-                const long long head = (long long)slot_of(first, begin) * PART_ROWS + row;   // the first, then the others
-                const long long rest = (long long)(2 * (first + begin)) * PART_ROWS + row;
-                const auto at = [&](int k) { return k == 0 ? head : rest + k * (2 * STEP * PART_ROWS); };
+                const int li = lane % LPR, row = (r0 + trow) % ROWS;   // (rows past the segment's last: not stored)
+                const long long head = (long long)slot_of(first, begin) * ROWS + row;   // the first, then the others
+                const long long rest = (long long)(2 * (first + begin)) * ROWS + row;
+                const auto at = [&](int k) { return k == 0 ? head : rest + k * (2 * STEP * ROWS); };
                 float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
                 float mm = -INFINITY, ll = 0.f;
                 for (int i0 = 0; i0 < count; i0 += BATCH) {
@@ -748,7 +760,7 @@ __global__ void __launch_bounds__(Shape<D, F8, WIDE>::THREADS, 1)
                 for (int off = LPR / 2; off > 0; off >>= 1) ll += __shfl_xor_sync(0xffffffffu, ll, off);
                 if (r0 + trow < rows) {
                     if (final) {
-                        store(y.b, kvh * a.group + chunk * PART_ROWS + row, acc, mm, ll, vs);
+                        store(y.b, kvh * a.group + chunk * ROWS + row, acc, mm, ll, vs);
                     } else {
                         *reinterpret_cast<float4 *>(a.part + head * D + tcol) = acc;
                         if (tcol == 0) a.ml[head] = make_float2(mm, ll);
@@ -815,30 +827,30 @@ struct Layout {
 Layout layout(int ctas, int n_seqs, int nq, int max_len, bool weights) {
     Layout y;
     y.part = 3 * MAX_CTAS * sizeof(uint32_t);
-    y.ml = y.part + (size_t)ctas * 2 * PART_ROWS * 128 * sizeof(float);
-    y.stat = y.ml + up256((size_t)ctas * 2 * PART_ROWS * sizeof(float2));
+    y.ml = y.part + (size_t)ctas * 2 * MAX_ROWS * 128 * sizeof(float);
+    y.stat = y.ml + up256((size_t)ctas * 2 * MAX_ROWS * sizeof(float2));
     y.ld_scores = (max_len + WK - 1) / WK * WK;
     y.scores = y.stat + (weights ? up256((size_t)n_seqs * nq * sizeof(float2)) : 0);
     y.bytes = y.scores + (weights ? (size_t)n_seqs * nq * (size_t)y.ld_scores * sizeof(float) : 0);
     return y;
 }
 
-template <int D, bool F8, bool WIDE>
+template <int D, bool F8, int BLOCKS>
 cudaError_t launch_kernel(const CUtensorMap &tk, const CUtensorMap &tv, const Args &a, int grid, cudaStream_t st) {
     static std::atomic<bool> ready[kMaxDevices];   // the shared-memory opt-in, per device
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
-    constexpr int bytes = Shape<D, F8, WIDE>::BYTES;
+    constexpr int bytes = Shape<D, F8, BLOCKS>::BYTES;
     static_assert(bytes <= 232448, "shared memory of one CTA");
     if (!ready[dev].load()) {
-        cudaError_t e = cudaFuncSetAttribute(attention_decode_kernel<D, F8, WIDE>,
+        cudaError_t e = cudaFuncSetAttribute(attention_decode_kernel<D, F8, BLOCKS>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e != cudaSuccess) return e;
         ready[dev].store(true);
     }
     cudaLaunchAttribute at[1];
-    cudaLaunchConfig_t cfg = pdl_config(dim3(grid), dim3(Shape<D, F8, WIDE>::THREADS), bytes, st, at);
-    return cudaLaunchKernelEx(&cfg, attention_decode_kernel<D, F8, WIDE>, tk, tv, a);
+    cudaLaunchConfig_t cfg = pdl_config(dim3(grid), dim3(Shape<D, F8, BLOCKS>::THREADS), bytes, st, at);
+    return cudaLaunchKernelEx(&cfg, attention_decode_kernel<D, F8, BLOCKS>, tk, tv, a);
 }
 
 }  // namespace
@@ -858,7 +870,14 @@ cudaError_t launch_attention_decode(const AttentionDecode &p, cudaStream_t st) {
     Args a{};
     a.p = p;
     a.group = p.nq / p.cache.nkv;
-    a.chunks = (a.group + PART_ROWS - 1) / PART_ROWS;
+    // More than 16 heads of a kv head: segments of 32 heads read a key once, segments of 16 once for every 16
+    // heads but from L2 where the cache fits there, with twice the segments and half the rows to join.  40 q heads over 2 kv
+    // heads of 128, 32 and 8 sequences of 20,000 to 24,000 tokens (787 and 197 MB by max_len): 124 and 45 us against
+    // 213 and 54; 64 over 1, two sequences (25 MB): 32 us against 23; e4m3, 8 sequences (98 MB): 45 against 43.
+    const double bytes = 2.0 * p.n_seqs * p.max_len * p.cache.nkv * p.cache.d * (p.cache.f8 ? 1 : 2);
+    const bool split = a.group > WROWS && bytes > 1e8;
+    const int rows = split ? 2 * WROWS : WROWS;   // heads of a segment
+    a.chunks = (a.group + rows - 1) / rows;
     a.box_shift = std::min(6, p.cache.page_shift);
     a.count = reinterpret_cast<uint32_t *>(ws);
     a.part = reinterpret_cast<float *>(ws + y.part);
@@ -874,17 +893,17 @@ cudaError_t launch_attention_decode(const AttentionDecode &p, cudaStream_t st) {
     // one CTA per SM, fewer where the lengths cannot hold as many tiles
     const long long most = (long long)p.n_seqs * p.cache.nkv * a.chunks * ((p.max_len + (p.cache.f8 ? 127 : 63)) / (p.cache.f8 ? 128 : 64));
     const int grid = (int)std::min<long long>(sms, std::max<long long>(most, 1));
-    cudaError_t e;
-    if (p.cache.d == 128)
-        e = p.cache.f8 ? (a.group > 8 ? launch_kernel<128, true, true>(tk, tv, a, grid, st)
-                                      : launch_kernel<128, true, false>(tk, tv, a, grid, st))
-                       : (a.group > 8 ? launch_kernel<128, false, true>(tk, tv, a, grid, st)
-                                      : launch_kernel<128, false, false>(tk, tv, a, grid, st));
-    else
-        e = p.cache.f8 ? (a.group > 8 ? launch_kernel<64, true, true>(tk, tv, a, grid, st)
-                                      : launch_kernel<64, true, false>(tk, tv, a, grid, st))
-                       : (a.group > 8 ? launch_kernel<64, false, true>(tk, tv, a, grid, st)
-                                      : launch_kernel<64, false, false>(tk, tv, a, grid, st));
+    const auto run = [&](auto d, auto f8) {
+        constexpr int D = decltype(d)::value;
+        constexpr bool F8 = decltype(f8)::value;
+        return a.group <= 8 ? launch_kernel<D, F8, 1>(tk, tv, a, grid, st)
+                            : (split ? launch_kernel<D, F8, 4>(tk, tv, a, grid, st)
+                                     : launch_kernel<D, F8, 2>(tk, tv, a, grid, st));
+    };
+    const std::integral_constant<int, 128> d128;
+    const std::integral_constant<int, 64> d64;
+    const cudaError_t e = p.cache.d == 128 ? (p.cache.f8 ? run(d128, std::true_type{}) : run(d128, std::false_type{}))
+                                           : (p.cache.f8 ? run(d64, std::true_type{}) : run(d64, std::false_type{}));
     if (e != cudaSuccess || !p.weight_out || p.max_len == 0) return e;
     cudaLaunchAttribute at[1];
     cudaLaunchConfig_t cfg = pdl_config(dim3((p.max_len + WK - 1) / WK, p.n_seqs), dim3(256), 0, st, at);

@@ -245,6 +245,8 @@ CASES = [
     ([300, 999, 64], 64, 8, 128, E4M3, 16), ([513, 77], 32, 1, 64, BF16, 256), ([200, 1000], 48, 2, 128, BF16, 64),
     ([345, 12], 40, 1, 128, E4M3, 32), ([20000], 8, 1, 128, BF16, 128), ([9001], 12, 4, 64, E4M3, 64),
     ([9000, 30000], 12, 1, 64, BF16, 32), ([40000], 16, 1, 128, BF16, 64), ([30000, 5], 24, 2, 128, E4M3, 16),
+    ([110000], 40, 2, 128, BF16, 64), ([205000, 33], 76, 4, 64, E4M3, 256),       # segments of 32 heads (over 100 MB)
+    ([700, 65], 64, 1, 128, BF16, 16), ([30000], 40, 2, 128, E4M3, 64), ([129, 20000], 20, 1, 64, E4M3, 32),
     ([5000, 1, 0, 3333], 28, 4, 128, BF16, 256), ([31] * 200, 2, 1, 64, BF16, 16), ([130] * 70 + [0] * 9, 8, 4, 128, BF16, 64),
 ]
 
