@@ -199,12 +199,21 @@ def _ptr(t):
     return t.data_ptr()
 
 
+_current_stream = None   # the current stream's address: a Stream object takes 3.1 us, this 0.3
+
+
 def _stream(stream):
     if stream is None:
-        import torch
-        device = torch.cuda.current_device()
-        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # the address alone: 0.4 us, a Stream object 3.1 us
-        return raw(device) if raw is not None else torch.cuda.current_stream(device).cuda_stream
+        global _current_stream
+        if _current_stream is None:
+            import torch
+            torch.cuda.current_stream()   # initialises CUDA, or raises
+            raw, device = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
+            if raw is not None and device is not None:
+                _current_stream = lambda: raw(device())                                 # noqa: E731
+            else:
+                _current_stream = lambda: torch.cuda.current_stream().cuda_stream       # noqa: E731
+        return _current_stream()
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
@@ -571,22 +580,22 @@ def h3enc_op_attention_bidir_ws(qkv, o, S, heads, head_dim, workspace, cu_seqlen
                                                   _ptr(workspace), wbytes, _stream(stream)))
 
 
-def _ld(t, need):
-    """Leading dimension of a row-major matrix: a tensor's row stride (of a single row, whose stride means
-    nothing, at least its width); `need` for an address or None."""
-    if t is None or isinstance(t, int):
-        return need
-    s = t.stride(0)
-    return s if s >= need or t.shape[0] != 1 else t.shape[1]
-
+# The decoding calls take tensors only (no bare addresses) and are written out flat: their host time is what bounds the
+# small ones.  A single row's stride means nothing, so its leading dimension is the width that is needed.
 
 def h3enc_op_qk_norm_rope(qkv, T, n_heads, n_kv_heads, head_dim, w_q, w_k, eps, cos_tab, sin_tab, cs_stride=0,
                           q_out=None, k_out=None, cache=None, slots=None, status=None, stream=None):
     """Per-head q/k RMSNorm and rotation of a packed projection; K and V also into a KVCache."""
+    many = T > 1
     return _check(lib.h3enc_op_qk_norm_rope(
-        _ptr(qkv), _ld(qkv, (n_heads + 2 * n_kv_heads) * head_dim), T, n_heads, n_kv_heads, head_dim, _ptr(w_q),
-        _ptr(w_k), eps, _ptr(cos_tab), _ptr(sin_tab), cs_stride, _ptr(q_out), _ld(q_out, n_heads * head_dim),
-        _ptr(k_out), _ld(k_out, n_kv_heads * head_dim), cache, _ptr(slots), _ptr(status), _stream(stream)))
+        qkv.data_ptr(), qkv.stride(0) if many else (n_heads + 2 * n_kv_heads) * head_dim, T, n_heads, n_kv_heads,
+        head_dim, None if w_q is None else w_q.data_ptr(), None if w_k is None else w_k.data_ptr(), eps,
+        None if cos_tab is None else cos_tab.data_ptr(), None if sin_tab is None else sin_tab.data_ptr(), cs_stride,
+        None if q_out is None else q_out.data_ptr(),
+        q_out.stride(0) if many and q_out is not None else n_heads * head_dim,
+        None if k_out is None else k_out.data_ptr(),
+        k_out.stride(0) if many and k_out is not None else n_kv_heads * head_dim, cache,
+        None if slots is None else slots.data_ptr(), None if status is None else status.data_ptr(), _stream(stream)))
 
 
 def h3enc_op_attention_decode_workspace_bytes(n_seqs, n_heads, max_len, with_weights=False) -> int:
@@ -597,26 +606,39 @@ def h3enc_op_attention_decode(q, o, cache, page_table, seq_lens, n_heads, max_le
                               weight_out=None, status=None, stream=None):
     """Attention of one new token per sequence over a KVCache: q, o [n_seqs, n_heads * head_dim],
     page_table int32 [n_seqs, pages], seq_lens int32 [n_seqs], weights float32 [n_seqs, >= max_len]."""
-    width = n_heads * cache.head_dim
-    ld_w = _ld(weight_out, max_len)
-    if weight_in is not None and weight_in is not weight_out and seq_lens.numel() > 1 and _ld(weight_in, ld_w) != ld_w:
-        raise ValueError("attention_decode: weight_in and weight_out have different row strides")
+    n = seq_lens.numel()
+    if n > 1:
+        ld_q, ld_o, ld_t = q.stride(0), o.stride(0), page_table.stride(0)
+        ld_w = 0 if weight_out is None else weight_out.stride(0)
+        if weight_in is not None and weight_in is not weight_out and weight_in.stride(0) != ld_w:
+            raise ValueError("attention_decode: weight_in and weight_out have different row strides")
+    else:
+        ld_q = ld_o = n_heads * cache.head_dim
+        ld_t = page_table.shape[1]
+        ld_w = 0 if weight_out is None else weight_out.shape[1]
     return _check(lib.h3enc_op_attention_decode(
-        _ptr(q), _ld(q, width), _ptr(o), _ld(o, width), cache, _ptr(page_table),
-        _ld(page_table, -(-max_len // cache.page_size)), _ptr(seq_lens), seq_lens.numel(), n_heads, max_len,
-        _ptr(weight_in), _ptr(weight_out), ld_w, _ptr(workspace),
-        0 if workspace is None else workspace.numel() * workspace.element_size(), _ptr(status), _stream(stream)))
+        q.data_ptr(), ld_q, o.data_ptr(), ld_o, cache, page_table.data_ptr(), ld_t, seq_lens.data_ptr(), n, n_heads,
+        max_len, None if weight_in is None else weight_in.data_ptr(),
+        None if weight_out is None else weight_out.data_ptr(), ld_w,
+        None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.nbytes,
+        None if status is None else status.data_ptr(), _stream(stream)))
 
 
 def h3enc_op_cache_evict(cache, page_table, seq_lens, max_len, budget, weight, weight_out, kept, new_lens,
                          page_table_out=None, sink=0, recent=0, status=None, stream=None):
     """Keep `budget` tokens per sequence by accumulated weight; in place, or into page_table_out's pages."""
-    size = cache.page_size
+    n = seq_lens.numel()
+    if n > 1:
+        ld_t, ld_w, ld_w2, ld_k = page_table.stride(0), weight.stride(0), weight_out.stride(0), kept.stride(0)
+        ld_t2 = 0 if page_table_out is None else page_table_out.stride(0)
+    else:
+        ld_t, ld_w, ld_w2, ld_k = page_table.shape[1], weight.shape[1], weight_out.shape[1], kept.shape[1]
+        ld_t2 = 0 if page_table_out is None else page_table_out.shape[1]
     return _check(lib.h3enc_op_cache_evict(
-        cache, _ptr(page_table), _ld(page_table, -(-max_len // size)), _ptr(page_table_out),
-        _ld(page_table_out, -(-min(budget, max_len) // size)), _ptr(seq_lens), seq_lens.numel(), max_len, budget, sink,
-        recent, _ptr(weight), _ld(weight, max_len), _ptr(weight_out), _ld(weight_out, max_len), _ptr(kept),
-        _ld(kept, budget), _ptr(new_lens), _ptr(status), _stream(stream)))
+        cache, page_table.data_ptr(), ld_t, None if page_table_out is None else page_table_out.data_ptr(), ld_t2,
+        seq_lens.data_ptr(), n, max_len, budget, sink, recent, weight.data_ptr(), ld_w, weight_out.data_ptr(), ld_w2,
+        kept.data_ptr(), ld_k, new_lens.data_ptr(),
+        None if status is None else status.data_ptr(), _stream(stream)))
 
 
 def h3vis_create(cfg: VisionConfig):
