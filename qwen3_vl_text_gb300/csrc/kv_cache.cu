@@ -208,6 +208,9 @@ __device__ __forceinline__ void add_cluster(uint32_t *p, uint32_t rank, uint32_t
     asm volatile("red.relaxed.cluster.shared::cluster.add.u32 [%0], %1;" ::"r"(mapa_shared(smem_u32(p), rank)), "r"(v)
                  : "memory");
 }
+__device__ __forceinline__ void set_cluster(uint32_t *p, uint32_t rank, uint32_t v) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(mapa_shared(smem_u32(p), rank)), "r"(v) : "memory");
+}
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
@@ -216,17 +219,18 @@ __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.w
 // unprotected tokens is found in up to three digits (11, 11 and 10 bits): a histogram of the tokens that
 // match the digits so far, scanned from the top by all threads; it ends early when the digit's whole bin is
 // kept, which two digits almost always reach unless weights are equal.  In a cluster every CTA adds the bins
-// that it has anything in to all CTAs' sums (few are filled; reading all histograms took 2.2 us a digit).
+// that it has anything in to the first one's sums, which finds the digit for all.
 // Then the tokens are counted in order, as bit masks of 32, and each kept one is written to its place.
 // What bounds it is the chain of these steps, not the 4 bytes per token: 8 us for 32 sequences of 4608 tokens,
-// 13 us for one of 65,537.
+// 11 us for one of 65,537.
 template <bool CLUSTER>
 __global__ void __launch_bounds__(SEL_THREADS, 1) evict_select_kernel(const CacheEvict p, int cached) {
     extern __shared__ float held[];               // [cached] weights
     __shared__ __align__(8) uint32_t hist[BINS];
     __shared__ __align__(8) uint32_t sum[CLUSTER ? 3 : 1][BINS];   // over the cluster, one per digit
     __shared__ uint32_t mask_sure[SEL_BLOCK / 32], mask_eq[SEL_BLOCK / 32];
-    __shared__ uint32_t sums[32], s_base[2], s_digit, s_need, s_full, s_total;
+    __shared__ uint32_t sums[32], s_base[2], s_total;
+    __shared__ uint32_t s_found[3];   // the digit, how many of its bin are kept, how many it holds
     pdl_trigger();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     for (int i = tid; i < BINS; i += SEL_THREADS) {
@@ -271,25 +275,29 @@ __global__ void __launch_bounds__(SEL_THREADS, 1) evict_select_kernel(const Cach
         uint2 c = *reinterpret_cast<const uint2 *>(hist + low);
         *reinterpret_cast<uint2 *>(hist + low) = make_uint2(0, 0);   // for the next digit
         if (CLUSTER) {
-            for (int r = 0; r < ranks; ++r) {
-                if (c.x) add_cluster(&sum[pass][low], r, c.x);
-                if (c.y) add_cluster(&sum[pass][low + 1], r, c.y);
-            }
+            if (c.x) add_cluster(&sum[pass][low], 0, c.x);
+            if (c.y) add_cluster(&sum[pass][low + 1], 0, c.y);
             cluster_sync();
             c = *reinterpret_cast<const uint2 *>(sum[pass] + low);
         }
-        const uint32_t upto = block_scan(c.x + c.y, sums), before = upto - c.x - c.y;
-        if (before < need && need <= upto) {   // exactly one thread
-            const bool in_high = need <= before + c.y;
-            s_digit = in_high ? low + 1 : low;
-            s_need = need - before - (in_high ? 0u : c.y);
-            s_full = in_high ? c.y : c.x;
+        if (rank == 0) {
+            const uint32_t upto = block_scan(c.x + c.y, sums), before = upto - c.x - c.y;
+            if (before < need && need <= upto) {   // exactly one thread
+                const bool in_high = need <= before + c.y;
+                s_found[0] = in_high ? low + 1 : low;
+                s_found[1] = need - before - (in_high ? 0u : c.y);
+                s_found[2] = in_high ? c.y : c.x;
+            }
+            __syncthreads();
+            if (CLUSTER && tid > 0 && tid < ranks)
+                #pragma unroll
+                for (int i = 0; i < 3; ++i) set_cluster(&s_found[i], tid, s_found[i]);
         }
-        __syncthreads();
-        prefix |= s_digit << shift;
-        need = s_need;   // of the tokens that match the digits so far, this many are kept
+        if (CLUSTER) cluster_sync();
+        prefix |= s_found[0] << shift;
+        need = s_found[1];   // of the tokens that match the digits so far, this many are kept
         cut = shift;
-        if (s_full == need) break;
+        if (s_found[2] == need) break;
     }
     // kept for certain: protected tokens and larger keys; of the equal ones the first `need`
     const auto sort_of = [&](int i, bool &sure, bool &eq) {
