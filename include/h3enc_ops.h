@@ -339,7 +339,7 @@ H3ENC_API h3enc_status h3enc_op_vis_rank(const uint8_t *mask, int32_t S, int32_t
  * e4m3(x / scale[g]) (fp32 division, rounded to nearest even, saturating at +-448) and
  * stand for that value times scale[g].
  * Requires page_size in {16, 32, 64, 128, 256}, head_dim in {64, 128}, k and v 16-byte
- * aligned, page_stride >= n_kv_heads * page_size * head_dim, its bytes a multiple of 16
+ * aligned, n_kv_heads <= 65536, page_stride >= n_kv_heads * page_size * head_dim, its bytes a multiple of 16
  * and below 2^40, num_pages * page_size < 2^31. */
 typedef struct {
     void *k, *v;

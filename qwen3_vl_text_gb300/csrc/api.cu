@@ -1450,14 +1450,15 @@ bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 
 // (slices of one packed buffer); otherwise their address ranges are.
 bool rows_overlap(const void *a, int64_t lda, int64_t ca, const void *b, int64_t ldb, int64_t cb, int64_t rows,
                   int64_t es) {
-    const int64_t pa = (int64_t)reinterpret_cast<uintptr_t>(a), pb = (int64_t)reinterpret_cast<uintptr_t>(b);
-    const int64_t ea = pa + ((rows - 1) * lda + ca) * es, eb = pb + ((rows - 1) * ldb + cb) * es;
+    using Wide = __int128;   // a leading dimension may be any 64-bit number
+    const Wide pa = reinterpret_cast<uintptr_t>(a), pb = reinterpret_cast<uintptr_t>(b);
+    const Wide ea = pa + ((Wide)(rows - 1) * lda + ca) * es, eb = pb + ((Wide)(rows - 1) * ldb + cb) * es;
     if (rows <= 0 || ea <= pb || eb <= pa) return false;
     if (lda != ldb) return true;
-    const int64_t row = lda * es;
-    int64_t delta = (pb - pa) % row;   // where b's first column lies in a row of a
+    const Wide row = (Wide)lda * es;
+    Wide delta = (pb - pa) % row;   // where b's first column lies in a row of a
     if (delta < 0) delta += row;
-    return delta < ca * es || delta + cb * es > row;
+    return delta < (Wide)ca * es || delta + (Wide)cb * es > row;
 }
 
 h3enc_status take_cache(const h3enc_kv_cache *c, const char *who, h3::KvCache *out) {
@@ -1473,7 +1474,7 @@ h3enc_status take_cache(const h3enc_kv_cache *c, const char *who, h3::KvCache *o
         return fail(nullptr, H3ENC_ERR_UNSUPPORTED, "%s: page_size must be 16, 32, 64, 128 or 256", who);
     const bool f8 = c->dtype == H3ENC_DTYPE_FP8_E4M3;
     const int64_t es = f8 ? 1 : 2;
-    if (c->n_kv_heads < 1 || c->num_pages < 1 || (int64_t)c->num_pages * c->page_size > INT32_MAX ||
+    if (c->n_kv_heads < 1 || c->n_kv_heads > 65536 || c->num_pages < 1 || (int64_t)c->num_pages * c->page_size > INT32_MAX ||
         c->page_stride < (int64_t)c->n_kv_heads * c->page_size * c->head_dim ||
         c->page_stride >= (int64_t(1) << 40) / es || c->page_stride * es % 16)
         return fail(nullptr, H3ENC_ERR_INVALID_ARG, "%s: bad cache sizes or page stride", who);

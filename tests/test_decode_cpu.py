@@ -68,7 +68,7 @@ def _cache(Q, **kw):
 BAD_CACHES = [(dict(k=None), 2), (dict(v=8), 2), (dict(dtype=1), 6), (dict(head_dim=96), 6), (dict(page_size=8), 6),
               (dict(page_size=48), 6), (dict(page_size=512), 6), (dict(page_stride=2 * 16 * 64 - 8), 2),
               (dict(page_stride=2 * 16 * 64 + 4), 2), (dict(page_stride=1 << 40), 2), (dict(num_pages=0), 2),
-              (dict(num_pages=1 << 28), 2), (dict(n_kv_heads=0), 2), (dict(dtype=2), 2),
+              (dict(num_pages=1 << 28), 2), (dict(n_kv_heads=0), 2), (dict(n_kv_heads=65537, page_stride=65537 * 16 * 64), 2), (dict(dtype=2), 2),
               (dict(dtype=2, k_scale=64), 2), (dict(k_scale=64), 2), (dict(v_scale=64), 2)]
 
 
@@ -117,7 +117,7 @@ def test_bad_caches_are_refused_by_every_entry(Q, kw, code):
 
 @pytest.mark.parametrize("kw", [
     dict(T=-1), dict(nq=0), dict(nkv=0), dict(d=96), dict(qkv=None), dict(qkv=(1 << 20) + 8), dict(ld_qkv=511),
-    dict(ld_qkv=508), dict(ld_qkv=516), dict(cos=None), dict(sin=None), dict(cos=20), dict(cs=2), dict(cs=-1),
+    dict(ld_qkv=508), dict(ld_qkv=516), dict(ld_qkv=1 << 62), dict(cos=None), dict(sin=None), dict(cos=20), dict(cs=2), dict(cs=-1),
     dict(eps=-1.0), dict(eps=float("nan")), dict(wq=8), dict(q=None), dict(q=(1 << 24) + 2), dict(ld_q=255),
     dict(ld_q=252), dict(k=1 << 25, ld_k=64), dict(q=(1 << 20) + 16),                # overlaps qkv, not in place
     dict(q=1 << 20, ld_q=520), dict(k=1 << 20, ld_k=512), dict(k=1 << 24, ld_k=128), dict(slots=16)])
@@ -138,7 +138,7 @@ def test_qk_norm_rope_of_no_rows_does_nothing(Q):
 
 @pytest.mark.parametrize("kw", [
     dict(n=-1), dict(n=1025), dict(nq=0), dict(nq=3), dict(max_len=-1), dict(max_len=65), dict(ld_table=-1), dict(max_len=2 ** 30 + 1, ld_table=2 ** 27),
-    dict(q=None), dict(o=None), dict(q=(1 << 20) + 8), dict(ld_q=252), dict(ld_q=260), dict(ld_o=128), dict(table=None),
+    dict(q=None), dict(o=None), dict(q=(1 << 20) + 8), dict(ld_q=252), dict(ld_q=260), dict(ld_q=1 << 62, ld_o=1 << 61), dict(ld_o=128), dict(table=None),
     dict(lens=None), dict(o=1 << 20), dict(o=(1 << 20) + 256), dict(w_in=16), dict(w_out=16, ld_w=63),
     dict(w_out=1 << 12, w_in=(1 << 12) + 4)])
 def test_attention_decode_refuses(Q, kw):
