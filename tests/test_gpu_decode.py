@@ -557,6 +557,20 @@ def test_cache_evict_bad_pages_and_lengths_are_reported():
     assert int(status.item()) == 2 and new.tolist() == [0, 5]
 
 
+def test_decoding_of_sequences_without_any_token():
+    """max_len = 0: no page table at all, zero rows from the attention, nothing kept by the eviction."""
+    g = _gen(21)
+    cache = _pool(g, 2, 2, 16, 64, BF16)
+    seq, table = torch.zeros(3, dtype=torch.int32, device="cuda"), torch.zeros(3, 0, dtype=torch.int32, device="cuda")
+    q, o = _randn(g, 3, 8 * 64), torch.full((3, 8 * 64), 9.0, device="cuda", dtype=torch.bfloat16)
+    w = torch.zeros(3, 4, device="cuda")
+    Q.h3enc_op_attention_decode(q, o, cache, table, seq, 8, 0, _workspace(3, 8, 0, True), None, w)
+    assert not o.any()
+    kept, new = torch.zeros(3, 5, dtype=torch.int32, device="cuda"), torch.full((3,), 7, dtype=torch.int32, device="cuda")
+    Q.h3enc_op_cache_evict(cache, table, seq, 0, 5, w, torch.ones_like(w), kept, new)
+    assert (kept == -1).all() and not new.any()
+
+
 # ---------------------------------------------------------------- together
 
 def test_decode_step_captured_in_a_graph():
