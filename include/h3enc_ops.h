@@ -340,7 +340,8 @@ H3ENC_API h3enc_status h3enc_op_vis_rank(const uint8_t *mask, int32_t S, int32_t
  * stand for that value times scale[g].
  * Requires page_size in {16, 32, 64, 128, 256}, head_dim in {64, 128}, k and v 16-byte
  * aligned, n_kv_heads <= 65536, page_stride >= n_kv_heads * page_size * head_dim, its bytes a multiple of 16
- * and below 2^40, num_pages * page_size < 2^31. */
+ * and below 2^40, num_pages * page_size < 2^31.  Another dtype, head_dim or page_size is
+ * H3ENC_ERR_UNSUPPORTED, the rest H3ENC_ERR_INVALID_ARG. */
 typedef struct {
     void *k, *v;
     const float *k_scale, *v_scale;   /* [n_kv_heads], FP8_E4M3 only; NULL for BF16 */
@@ -388,7 +389,8 @@ H3ENC_API h3enc_status h3enc_op_qk_norm_rope(const void *qkv, int64_t ld_qkv, in
  *   workspace: h3enc_op_attention_decode_workspace_bytes() bytes, 256-byte aligned,
  *   zero-filled once before its first use and then reused by calls of any sizes that fit.
  *   Calls (and graphs that hold them) sharing it must not overlap on the GPU.
- * The result does not depend on timing: the same inputs give the same bits on every run.
+ * The result does not depend on timing: the same inputs give the same bits on every run.  A
+ * bounded wait that runs out sets status bit 1; the outputs are then undefined.
  * Requires n_seqs <= 1024, max_len <= 2^30, n_heads % n_kv_heads == 0, leading dimensions of
  * q and o that are multiples of 8, q and o 16-byte aligned. */
 H3ENC_API h3enc_status h3enc_op_attention_decode(const void *q, int64_t ld_q, void *o, int64_t ld_o,
