@@ -20,7 +20,9 @@
 //  * With at most 8 heads the rows 8-15 of the weight matrix P would be padding: they carry
 //    P's rounding remainder p - bf16(p) instead, so the value product loses nothing to the 8-bit mantissa
 //    at no cost (more than 8 heads: a second product).  e4m3 values are exact in f16, so that path
-//    runs in f16, with q scaled by a power of two per head into f16's range.
+//    runs in f16, with q scaled by a power of two per head into f16's range and p by 2^14: f16 ends at
+//    2^-24, so the two halves then leave an error of at most 2^-39 of a warp's largest weight, far below the
+//    fp32 sums; unscaled, every weight under 2^-25 of the largest would be lost to o but counted in l.
 // Measured (64 q heads over 8 kv heads of 128, pages of 64): 64 sequences of 5000 to 8192 tokens in bf16, 1.7 GB,
 // 248-251 us = 6.8 TB/s, the measured copy rate; in e4m3 140 us (5.9 TB/s: the conversions of every key and value
 // to f16 then take most of the time between two tiles); one sequence of 1025 tokens 7.2 us, which is
@@ -56,6 +58,7 @@ struct Shape {
     static constexpr int CWARPS = 4 * GROUPS, THREADS = (CWARPS + 2) * 32;
     static constexpr int ROW = D * (F8 ? 1 : 2);            // bytes of a key
     static constexpr int BOX = ROW < 128 ? 64 : 128;        // bytes of a box row (= swizzle width)
+    static constexpr float UP = F8 ? 16384.f : 1.f;         // weights, and so l and o, are held times this
     static constexpr int TILE = TK * ROW;                   // K or V of one tile
     // a multiple of the groups: a stage then always serves the same group, or both, which see each of its phases
     static constexpr int STAGES = TILE >= 16384 ? 4 : 8;
@@ -389,7 +392,7 @@ __global__ void __launch_bounds__(Shape<D, F8, BLOCKS>::THREADS, 1)
         const float inv = 1.f / l, f = inv * vs;
         *reinterpret_cast<uint2 *>(p.o + b * p.ld_o + (long long)h * D + tcol) =
             make_uint2(pack_bf16x2(v.x * f, v.y * f), pack_bf16x2(v.z * f, v.w * f));
-        if (a.stat && tcol == 0) a.stat[(long long)b * p.nq + h] = make_float2(m, inv);
+        if (a.stat && tcol == 0) a.stat[(long long)b * p.nq + h] = make_float2(m, inv * S::UP);
     };
     const auto give_up = [&]() {   // on the data; the control flow (barriers, counters) goes on to the end
         if (lane == 0) {
@@ -552,10 +555,10 @@ __global__ void __launch_bounds__(Shape<D, F8, BLOCKS>::THREADS, 1)
                     for (int n = 0; n < NT; ++n)
                         #pragma unroll
                         for (int k = 0; k < 2; ++k) {
-                            s[n][k] = ex2(s[n][k] - z0);
+                            s[n][k] = ex2(s[n][k] - z0) * S::UP;
                             l0 += s[n][k];
                             if (WIDE) {
-                                s[n][2 + k] = ex2(s[n][2 + k] - z1);
+                                s[n][2 + k] = ex2(s[n][2 + k] - z1) * S::UP;
                                 l1 += s[n][2 + k];
                             }
                         }

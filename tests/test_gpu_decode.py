@@ -306,6 +306,34 @@ def test_attention_decode_of_large_and_small_scores(dtype):
             _check_attention(o, x, kv, lens, nq, d)
 
 
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+@pytest.mark.parametrize("n,L,nq,nkv,d,bound", [
+    (32, 1000, 64, 8, 128, 1000), (20, 8192, 16, 2, 128, 8192), (30, 1500, 4, 2, 64, 1500), (20, 3000, 24, 2, 64, 3000),
+    (60, 1111, 40, 2, 128, 16384)])                            # the last: segments of 32 heads (by the bound)
+def test_attention_decode_of_a_sink_and_a_long_light_tail(n, L, nq, nkv, d, bound, dtype):
+    """One key of score 16 to 22 above all others and of value zero: the output is the sum of the many
+    light keys, every one of them far below 2^-20 of the largest weight.  Many segments, so that a
+    warp holds the sink together with a long part of the tail."""
+    g, page = _gen(n + L), 64
+    lens = [L - i for i in range(n)]
+    cache, table, seq, q, _ = _attend_case(g, lens, nq, nkv, d, dtype, page, spare=1 + (bound - L) // page)
+    q = q.clone()
+    q.view(n, nq, d)[..., 0] = 64.0
+    k = [_randn(g, x, nkv, d) for x in lens]
+    v = [1 + _randn(g, x, nkv, d) for x in lens]               # a mean, so that a lost share shows
+    for b in range(n):
+        at = (37 * b) % lens[b]
+        k[b][..., 0] = 0
+        k[b][at] = 0
+        k[b][at, :, 0] = (16 + b % 7) * d ** 0.5 / 64.0
+        v[b][at] = 0
+    kv = _fill(cache, table, lens, k, v)
+    o = torch.empty(n, nq * d, device="cuda", dtype=torch.bfloat16)
+    w = torch.zeros(n, bound, device="cuda")
+    Q.h3enc_op_attention_decode(q, o, cache, table, seq, nq, bound, _workspace(n, nq, bound, True), None, w)
+    _check_attention(o, q, kv, lens, nq, d, None, w)
+
+
 def test_attention_decode_bad_pages_and_lengths_are_reported():
     lens, nq, nkv, d, page = [100, 64], 8, 2, 64, 16
     g = _gen(10)
