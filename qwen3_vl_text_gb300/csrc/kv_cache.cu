@@ -463,9 +463,11 @@ __global__ void __launch_bounds__(MOVE_THREADS) evict_copy_kernel(const CacheEvi
 // Packs the kept tokens in place.  A CTA takes a slice (2^slice_shift 16-byte vectors) of one plane's rows through
 // all chunks of tokens in order: a token moves to its own index or a smaller one, so no source of a chunk lies
 // before the chunk's first token, where the stores of earlier chunks end; the barrier keeps a chunk's own
-// stores behind its loads.  With few sequences the chain of chunks bounds it, so the slices are then narrow, the
-// chunks long, and the places of the next chunk looked up while this one's rows are loaded (one sequence of
-// 4608 tokens cut to 4096, both launches: 23 us, with whole rows and nothing ahead 52 us; 32 of them 149 us).
+// stores behind its loads, and the one behind the stores keeps the places they go by until all warps have used
+// them (a third buffer of places instead: 159 against 148 us for the 32 sequences below).  With few sequences the chain of
+// chunks bounds it, so the slices are then narrow, the chunks long, and the places of the next chunk looked up
+// while this one's rows are loaded (one sequence of 4608 tokens cut to 4096, both launches: 23 us, with whole rows
+// and nothing ahead 52 us; 32 of them 148 us).
 __global__ void __launch_bounds__(MOVE_THREADS, 4) evict_pack_kernel(const CacheEvict p, int slice_shift) {
     constexpr int VECS = 8, MAX_ROWS = MOVE_THREADS * VECS / 2;
     __shared__ long long s_src[2][MAX_ROWS], s_dst[2][MAX_ROWS];
@@ -499,6 +501,7 @@ __global__ void __launch_bounds__(MOVE_THREADS, 4) evict_pack_kernel(const Cache
                 const int r = (k * MOVE_THREADS + tid) >> slice_shift;
                 if (s_dst[buf][r] >= 0) *reinterpret_cast<uint4 *>(pool + s_dst[buf][r]) = v[k];
             }
+            __syncthreads();
         }
     }
 }

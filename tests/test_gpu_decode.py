@@ -555,6 +555,41 @@ def test_cache_evict(lens, nkv, d, dtype, page, budget, sink, recent, kind, in_p
         assert torch.equal(_raw(pool), x)
 
 
+@pytest.mark.parametrize("n,nkv,d,dtype,budget", [
+    (20, 8, 128, BF16, 900), (12, 8, 128, BF16, 1500), (12, 4, 128, BF16, 2900), (3, 1, 128, BF16, 5300),   # 128 to 1024 rows a chunk
+    (20, 8, 128, E4M3, 1500), (12, 8, 128, E4M3, 2900), (2, 2, 128, E4M3, 5300), (40, 4, 64, E4M3, 2900), (40, 4, 64, BF16, 1500)])
+def test_cache_evict_in_place_in_many_chunks(n, nkv, d, dtype, budget):
+    """At least five chunks of rows per CTA, at every width of a slice, while another stream copies memory: the
+    whole pool, from the same start, the same every time."""
+    g, page = _gen(n * d + budget), 64
+    top = budget + budget // 3
+    lens = [top - 11 * i for i in range(n)]
+    cols = -(-top // page)
+    cache = _pool(g, n * cols, nkv, page, d, dtype)
+    start = [torch.randint(-100, 100, _raw(t).shape, device="cuda", generator=g).to(_raw(t).dtype) for t in cache.tensors[:2]]
+    table = _table(g, n, cols, n * cols)
+    w = _weights(g, n, top, "spread")
+    want, wc = [t.clone() for t in start], w.cpu().numpy()
+    for b, L in enumerate(lens):
+        keep = O.decode.keep_heaviest(wc[b], L, budget, 4, 64)
+        i, j = torch.tensor(keep, device="cuda"), torch.arange(len(keep), device="cuda")
+        for to, old in zip(want, start):
+            to[table[b, j // page].long(), :, j % page] = old[table[b, i // page].long(), :, i % page]
+    seq, new = torch.tensor(lens, dtype=torch.int32, device="cuda"), torch.empty(n, dtype=torch.int32, device="cuda")
+    kept, w_out = torch.empty(n, budget, dtype=torch.int32, device="cuda"), torch.empty_like(w)
+    a, side = torch.empty(1 << 28, dtype=torch.uint8, device="cuda"), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(100):
+        with torch.cuda.stream(side):
+            a[1 << 27:] = a[:1 << 27]
+        for t, old in zip(cache.tensors[:2], start):
+            _raw(t).copy_(old)
+        Q.h3enc_op_cache_evict(cache, table, seq, top, budget, w, w_out, kept, new, sink=4, recent=64)
+        for t, x in zip(cache.tensors[:2], want):
+            assert torch.equal(_raw(t), x)
+    torch.cuda.synchronize()
+
+
 def test_cache_evict_bad_pages_and_lengths_are_reported():
     g = _gen(20)
     nkv, d, page = 2, 64, 16
