@@ -148,6 +148,12 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t &hi, uint32_t 
         lo = pack_bf16x2(a - bf16_lo(hi), b - bf16_hi(hi));
     }
 }
+// Two bf16 with their magnitudes held to the largest finite one (NaN too).
+__device__ __forceinline__ uint32_t finite2(uint32_t v) {
+    uint32_t r;
+    asm("min.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(0x7f7f7f7fu), "r"(v));
+    return r;
+}
 template <int THREADS>
 __device__ __forceinline__ void compute_sync() {
     asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory");
@@ -605,7 +611,8 @@ __global__ void __launch_bounds__(Shape<D, F8, BLOCKS>::THREADS, 1)
                                     }
                                 } else {
                                     mma<F8>(o[c + i], hi[0], hi[1], hi[2], hi[3], r[2 * i], r[2 * i + 1]);
-                                    if (WIDE) mma<F8>(o[c + i], lo[0], lo[1], lo[2], lo[3], r[2 * i], r[2 * i + 1]);
+                                    // an infinite value is in the sum already: times a remainder of 0 or less it would be NaN
+                                    if (WIDE) mma<F8>(o[c + i], lo[0], lo[1], lo[2], lo[3], finite2(r[2 * i]), finite2(r[2 * i + 1]));
                                 }
                             }
                         }
@@ -644,7 +651,11 @@ __global__ void __launch_bounds__(Shape<D, F8, BLOCKS>::THREADS, 1)
             for (int i = 0; i < SHARE; ++i) top = fmaxf(top, sm_m[((SPLIT ? 4 * group : 0) + i) * WROWS + r8 + g]);
             const float mine = r8 ? m1 : m0, f = mine == -INFINITY ? 0.f : ex2(mine - top);
             float *dst = sm_o + (warp * 8 + g) * S::LDO;
-            const auto out = [&](int i, int k) { return (WIDE ? o[i][r8 / 4 + k] : o[i][k] + o[i][k + 2]) * f; };
+            const auto out = [&](int i, int k) {
+                if constexpr (WIDE) return o[i][r8 / 4 + k] * f;
+                // (an infinite sum stays: the remainders' is NaN there)
+                return (fabsf(o[i][k]) == INFINITY ? o[i][k] : o[i][k] + o[i][k + 2]) * f;
+            };
             #pragma unroll
             for (int i = 0; i < D / 8; i += 2) {
                 if constexpr (F8) {   // even and odd columns of 16

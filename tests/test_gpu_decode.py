@@ -334,6 +334,48 @@ def test_attention_decode_of_a_sink_and_a_long_light_tail(n, L, nq, nkv, d, boun
     _check_attention(o, q, kv, lens, nq, d, None, w)
 
 
+@pytest.mark.parametrize("nq,nkv,d,lens,bound", [
+    (8, 2, 128, [300, 1, 64], 300), (6, 3, 64, [77, 2000], 2000), (24, 2, 128, [300, 1, 64], 300), (16, 1, 64, [77, 2000], 2000),
+    (40, 1, 128, [300, 1, 200], 400000), (24, 1, 64, [5000, 17], 400000)])       # the last two: segments of 32 heads
+def test_attention_decode_of_infinite_values(nq, nkv, d, lens, bound):
+    """Infinite values of positive weight give an infinite output, of both signs or NaN among them NaN, and leave the
+    other elements alone; a key of score minus infinity counts for nothing."""
+    g, n, page = _gen(nq + d), len(lens), 64
+    cache, table, seq, q, _ = _attend_case(g, lens, nq, nkv, d, BF16, page, spare=bound // page + 1)
+    q = q.clone()
+    q.view(n, nq, d)[..., 0] = q.view(n, nq, d)[..., 0].abs() + 0.5
+    k, v = [_randn(g, L, nkv, d) for L in lens], [_randn(g, L, nkv, d) for L in lens]
+    inf = float("inf")
+    for b, L in enumerate(lens):
+        v[b][0, :, 1] = inf
+        v[b][L - 1, :, 2] = -inf
+        v[b][L // 2, :, 3] = float("nan")
+        if L > 1:
+            v[b][L // 3, :, 4] = v[b][L - 1, :, 4] = inf
+            v[b][0, :, 5], v[b][L - 1, :, 5] = inf, -inf
+            k[b][L // 2 + 1 if L > 20 else 0, :, 0] = -inf
+            if L <= 20:
+                v[b][0, :, 1] = v[b][0, :, 5] = 0.5            # (0 * inf)
+    kv = _fill(cache, table, lens, k, v)
+    o = torch.empty(n, nq * d, device="cuda", dtype=torch.bfloat16)
+    w = torch.zeros(n, bound, device="cuda")
+    Q.h3enc_op_attention_decode(q, o, cache, table, seq, nq, bound, _workspace(n, nq, bound, True), None, w)
+    for b, L in enumerate(lens):
+        got, qb = _f64(o[b]).reshape(nq, d), _f64(q[b]).reshape(nq, d)
+        at = np.isfinite(kv[b][0]).all(axis=(1, 2))            # without the key of no weight: the same sums
+        kb, vb = kv[b][0][at], kv[b][1][at]
+        with np.errstate(invalid="ignore"):
+            want = O.decode.attend_one(qb, kb, vb)[0]
+        assert not np.isfinite(want[:, [1, 2, 3]]).all(axis=1).any()
+        assert np.array_equal(np.isnan(got), np.isnan(want)) and np.array_equal(np.isinf(got), np.isinf(want))
+        assert (np.sign(got) == np.sign(want))[np.isinf(want)].all()
+        at0 = w[b, :L].cpu().numpy()[~at]
+        assert (at0 == 0).all() and np.isfinite(w[b, :L].cpu().numpy()).all()
+        cols = np.isfinite(vb).all(axis=(0, 1))                # (elements that are finite in every key)
+        kz, vz, gz = kb, np.where(cols, vb, 0.0), torch.from_numpy(np.where(cols, got, 0.0).reshape(-1))
+        _check_attention(gz[None], q[b:b + 1], [(kz, vz)], [len(kb)], nq, d)
+
+
 def test_attention_decode_bad_pages_and_lengths_are_reported():
     lens, nq, nkv, d, page = [100, 64], 8, 2, 64, 16
     g = _gen(10)
