@@ -376,7 +376,8 @@ H3ENC_API h3enc_status h3enc_op_qk_norm_rope(const void *qkv, int64_t ld_qkv, in
 /* Attention of one new token of each of n_seqs sequences over the cache (the new token's
  * own key and value already in it): for q head h, reading kv head h / (n_heads / n_kv_heads),
  *   p_i = softmax_i(q . k_i / sqrt(d)) over i < seq_lens[b],   o = sum_i p_i v_i
- * (fp32; o rounded to bf16 once; a sequence of length 0 gives a zero row).
+ * (fp32; o rounded to bf16 once; a sequence of length 0 gives a zero row; weights below
+ * 2^-126 of the largest count as 0, also times an infinite value, which is NaN).
  *   q [n_seqs, ld_q], o [n_seqs, ld_o]: head h at column h*d; o must not overlap q.
  *   page_table DEVICE int32 [n_seqs, ld_table], seq_lens DEVICE int32 [n_seqs]; max_len: a
  *   bound on the lengths known to the host (ld_table * page_size >= max_len).  A length

@@ -148,7 +148,8 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t &hi, uint32_t 
         lo = pack_bf16x2(a - bf16_lo(hi), b - bf16_hi(hi));
     }
 }
-// Two bf16 with their magnitudes held to the largest finite one (NaN too).
+// Two bf16 with their magnitudes held to the largest finite one (NaN too).  One instruction per two values of V:
+// 3% where segments have 32 heads (32 sequences of 20,000 to 24,000 tokens 124 -> 128 us), nothing measurable elsewhere.
 __device__ __forceinline__ uint32_t finite2(uint32_t v) {
     uint32_t r;
     asm("min.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(0x7f7f7f7fu), "r"(v));
@@ -886,7 +887,7 @@ cudaError_t launch_attention_decode(const AttentionDecode &p, cudaStream_t st) {
     a.group = p.nq / p.cache.nkv;
     // More than 16 heads of a kv head: segments of 32 heads read a key once, segments of 16 once for every 16
     // heads but from L2 where the cache fits there, with twice the segments and half the rows to join.  40 q heads over 2 kv
-    // heads of 128, 32 and 8 sequences of 20,000 to 24,000 tokens (787 and 197 MB by max_len): 124 and 45 us against
+    // heads of 128, 32 and 8 sequences of 20,000 to 24,000 tokens (787 and 197 MB by max_len): 128 and 46 us against
     // 213 and 54; 64 over 1, two sequences (25 MB): 32 us against 23; e4m3, 8 sequences (98 MB): 45 against 43.
     const double bytes = 2.0 * p.n_seqs * p.max_len * p.cache.nkv * p.cache.d * (p.cache.f8 ? 1 : 2);
     const bool split = a.group > WROWS && bytes > 1e8;
