@@ -97,6 +97,7 @@ class KVCache(ctypes.Structure):
         super().__init__(k.data_ptr(), v.data_ptr(), _ptr(k_scale), _ptr(v_scale), stride, pages, size, heads, dim,
                          2 if k.dtype == torch.float8_e4m3fn else 0)
         self.tensors = (k, v, k_scale, v_scale)
+        self.device_index = k.get_device()
 
 
 def _load():
@@ -166,13 +167,14 @@ _SIGS = {
     "h3enc_op_attention_bidir": ([_P, _P, _I32, _I32, _I32, _P, _I32, _P], _I32),
     "h3enc_op_attention_bidir_ws": ([_P, _P, _I32, _I32, _I32, _P, _I32, _P, _I64, _P], _I32),
     "h3enc_op_attention_workspace_bytes": ([_I32], _I64),
-    "h3enc_op_qk_norm_rope": ([_P, _I64, _I32, _I32, _I32, _I32, _P, _P, _F, _P, _P, _I32, _P, _I64, _P, _I64,
-                               ctypes.POINTER(KVCache), _P, _P, _P], _I32),
-    "h3enc_op_attention_decode": ([_P, _I64, _P, _I64, ctypes.POINTER(KVCache), _P, _I32, _P, _I32, _I32, _I32, _P, _P,
-                                   _I64, _P, _I64, _P, _P], _I32),
+    # (integers as _P: both machines pass an address and an integer of 64 or 32 bits alike, and a ctypes address takes
+    # 80 ns to convert where an integer takes 140)
+    "h3enc_op_qk_norm_rope": ([_P, _P, _P, _P, _P, _P, _P, _P, _F, _P, _P, _P, _P, _P, _P, _P, ctypes.POINTER(KVCache),
+                               _P, _P, _P], _I32),
+    "h3enc_op_attention_decode": ([_P, _P, _P, _P, ctypes.POINTER(KVCache), _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P,
+                                   _P, _P], _I32),
     "h3enc_op_attention_decode_workspace_bytes": ([_I32, _I32, _I32, _I32], _I64),
-    "h3enc_op_cache_evict": ([ctypes.POINTER(KVCache), _P, _I32, _P, _I32, _P, _I32, _I32, _I32, _I32, _I32, _P, _I64,
-                              _P, _I64, _P, _I64, _P, _P, _P], _I32),
+    "h3enc_op_cache_evict": ([ctypes.POINTER(KVCache)] + [_P] * 19, _I32),
     "h3vis_create": ([ctypes.POINTER(VisionConfig), ctypes.POINTER(_P)], _I32),
     "h3vis_load_weights": ([_P, ctypes.c_char_p, _P, _I32, ctypes.POINTER(_I64), _I32, _I32], _I32),
     "h3vis_finalize_weights": ([_P], _I32),
@@ -199,21 +201,25 @@ def _ptr(t):
     return t.data_ptr()
 
 
-_current_stream = None   # the current stream's address: a Stream object takes 3.1 us, this 0.3
+_raw = None   # (current device, address of its current stream): Device and Stream objects take 1 and 3.1 us, these 0.1 and 0.2
+
+
+def _raw_calls():
+    global _raw
+    if _raw is None:
+        import torch
+        torch.cuda.current_stream()   # initialises CUDA, or raises
+        raw, device = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
+        if raw is None or device is None:
+            raw, device = lambda d: torch.cuda.current_stream(d).cuda_stream, torch.cuda.current_device   # noqa: E731
+        _raw = device, raw
+    return _raw
 
 
 def _stream(stream):
     if stream is None:
-        global _current_stream
-        if _current_stream is None:
-            import torch
-            torch.cuda.current_stream()   # initialises CUDA, or raises
-            raw, device = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
-            if raw is not None and device is not None:
-                _current_stream = lambda: raw(device())                                 # noqa: E731
-            else:
-                _current_stream = lambda: torch.cuda.current_stream().cuda_stream       # noqa: E731
-        return _current_stream()
+        device, raw = _raw or _raw_calls()
+        return raw(device())
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
@@ -580,22 +586,84 @@ def h3enc_op_attention_bidir_ws(qkv, o, S, heads, head_dim, workspace, cu_seqlen
                                                   _ptr(workspace), wbytes, _stream(stream)))
 
 
-# The decoding calls take tensors only (no bare addresses) and are written out flat: their host time is what bounds the
-# small ones.  A single row's stride means nothing, so its leading dimension is the width that is needed.
+# The decoding calls take tensors only (no bare addresses) and check what the C entry cannot see: type, device, and
+# that the rows and elements that the call reads are there.  They are written out flat: their host time is what
+# bounds the small ones.
+
+_BF16 = _I32T = _F32T = None
+
+
+def _types():
+    global _BF16, _I32T, _F32T
+    import torch
+    _BF16, _I32T, _F32T = torch.bfloat16, torch.int32, torch.float32
+
+
+def _vec(who, name, t, dtype, dev, n):
+    """Address of a contiguous tensor of at least n elements."""
+    if t.dtype is dtype and t.get_device() == dev and t.is_contiguous() and t.numel() >= n:
+        return t.data_ptr()
+    _common(who, name, t, dtype, dev)
+    raise H3encError(2, f"{who}: {name} must be contiguous and of {n} elements at least, not {tuple(t.shape)} "
+                        f"with strides {t.stride()}")
+
+
+def _mat(who, name, t, dtype, dev, rows, width):
+    """(address, leading dimension) of at least `rows` rows, each contiguous and of at least `width` elements.  A single
+    row's stride means nothing: its leading dimension is the width."""
+    if t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
+        ld = width if rows < 2 else t.stride()[0]
+        if ld >= width and t.numel() >= rows * ld:
+            return t.data_ptr(), ld
+    _common(who, name, t, dtype, dev)
+    shape, strides, inner = t.shape, t.stride(), 1
+    for i in range(len(shape) - 1, 0, -1):
+        if shape[i] != 1 and strides[i] != inner:
+            inner = -1
+            break
+        inner *= shape[i]
+    if rows and (not shape or shape[0] < rows or inner < width):
+        raise H3encError(2, f"{who}: {name} must be {rows} contiguous rows of {width} elements at least, not {tuple(shape)} "
+                            f"with strides {strides}")
+    return t.data_ptr(), width if rows < 2 else strides[0]
+
+
+def _common(who, name, t, dtype, dev):
+    if t.dtype is not dtype:
+        raise H3encError(2, f"{who}: {name} must be {dtype}, not {t.dtype}")
+    if t.get_device() != dev:
+        raise H3encError(2, f"{who}: {name} is on {t.device}, the current device is cuda:{dev}")
+
+
+def _refuse_cache(who, cache, dev):
+    raise H3encError(2, f"{who}: the cache is on {cache.tensors[0].device}, the current device is cuda:{dev}")
+
 
 def h3enc_op_qk_norm_rope(qkv, T, n_heads, n_kv_heads, head_dim, w_q, w_k, eps, cos_tab, sin_tab, cs_stride=0,
                           q_out=None, k_out=None, cache=None, slots=None, status=None, stream=None):
-    """Per-head q/k RMSNorm and rotation of a packed projection; K and V also into a KVCache."""
-    many = T > 1
+    """Per-head q/k RMSNorm and rotation of a packed projection; K and V also into a KVCache.  bfloat16 rows and
+    weights, float32 tables, int32 slots [T]."""
+    if _BF16 is None:
+        _types()
+    who, (device, raw) = "qk_norm_rope", _raw or _raw_calls()
+    dev = device()
+    if cache is not None and cache.device_index != dev:
+        _refuse_cache(who, cache, dev)
+    qkv, ld_qkv = _mat(who, "qkv", qkv, _BF16, dev, T, (n_heads + 2 * n_kv_heads) * head_dim)
+    ld_q = ld_k = 0
+    if q_out is not None:
+        q_out, ld_q = _mat(who, "q_out", q_out, _BF16, dev, T, n_heads * head_dim)
+    if k_out is not None:
+        k_out, ld_k = _mat(who, "k_out", k_out, _BF16, dev, T, n_kv_heads * head_dim)
+    n = 0 if T < 1 else (((head_dim // 8 - 1) * cs_stride + T) * 4 if cs_stride else T * head_dim // 2)   # read of a table
     return _check(lib.h3enc_op_qk_norm_rope(
-        qkv.data_ptr(), qkv.stride(0) if many else (n_heads + 2 * n_kv_heads) * head_dim, T, n_heads, n_kv_heads,
-        head_dim, None if w_q is None else w_q.data_ptr(), None if w_k is None else w_k.data_ptr(), eps,
-        None if cos_tab is None else cos_tab.data_ptr(), None if sin_tab is None else sin_tab.data_ptr(), cs_stride,
-        None if q_out is None else q_out.data_ptr(),
-        q_out.stride(0) if many and q_out is not None else n_heads * head_dim,
-        None if k_out is None else k_out.data_ptr(),
-        k_out.stride(0) if many and k_out is not None else n_kv_heads * head_dim, cache,
-        None if slots is None else slots.data_ptr(), None if status is None else status.data_ptr(), _stream(stream)))
+        qkv, ld_qkv, T, n_heads, n_kv_heads, head_dim,
+        None if w_q is None else _vec(who, "w_q", w_q, _BF16, dev, head_dim),
+        None if w_k is None else _vec(who, "w_k", w_k, _BF16, dev, head_dim), eps,
+        None if cos_tab is None else _vec(who, "cos_tab", cos_tab, _F32T, dev, n),
+        None if sin_tab is None else _vec(who, "sin_tab", sin_tab, _F32T, dev, n), cs_stride, q_out, ld_q, k_out, ld_k,
+        cache, None if slots is None else _vec(who, "slots", slots, _I32T, dev, T),
+        None if status is None else _vec(who, "status", status, _I32T, dev, 1), raw(dev) if stream is None else _stream(stream)))
 
 
 def h3enc_op_attention_decode_workspace_bytes(n_seqs, n_heads, max_len, with_weights=False) -> int:
@@ -604,41 +672,61 @@ def h3enc_op_attention_decode_workspace_bytes(n_seqs, n_heads, max_len, with_wei
 
 def h3enc_op_attention_decode(q, o, cache, page_table, seq_lens, n_heads, max_len, workspace, weight_in=None,
                               weight_out=None, status=None, stream=None):
-    """Attention of one new token per sequence over a KVCache: q, o [n_seqs, n_heads * head_dim],
+    """Attention of one new token per sequence over a KVCache: bfloat16 q, o [n_seqs, n_heads * head_dim],
     page_table int32 [n_seqs, pages], seq_lens int32 [n_seqs], weights float32 [n_seqs, >= max_len]."""
-    n = seq_lens.numel()
-    if n > 1:
-        ld_q, ld_o, ld_t = q.stride(0), o.stride(0), page_table.stride(0)
-        ld_w = 0 if weight_out is None else weight_out.stride(0)
-        if weight_in is not None and weight_in is not weight_out and weight_in.stride(0) != ld_w:
-            raise ValueError("attention_decode: weight_in and weight_out have different row strides")
-    else:
-        ld_q = ld_o = n_heads * cache.head_dim
-        ld_t = page_table.shape[1]
-        ld_w = 0 if weight_out is None else weight_out.shape[1]
+    if _BF16 is None:
+        _types()
+    who, n, (device, raw) = "attention_decode", seq_lens.numel(), _raw or _raw_calls()
+    dev = device()
+    if cache.device_index != dev:
+        _refuse_cache(who, cache, dev)
+    width = n_heads * cache.head_dim
+    q, ld_q = _mat(who, "q", q, _BF16, dev, n, width)
+    o, ld_o = _mat(who, "o", o, _BF16, dev, n, width)
+    page_table, ld_t = _mat(who, "page_table", page_table, _I32T, dev, n, -(-max_len // cache.page_size))
+    ld_w = 0
+    if weight_out is not None:
+        same = weight_in is weight_out
+        weight_out, ld_w = _mat(who, "weight_out", weight_out, _F32T, dev, n, max_len)
+        if same:
+            weight_in = weight_out
+        elif weight_in is not None:
+            weight_in, ld = _mat(who, "weight_in", weight_in, _F32T, dev, n, max_len)
+            if ld != ld_w:
+                raise ValueError("attention_decode: weight_in and weight_out have different row strides")
+    elif weight_in is not None:
+        weight_in, ld_w = _mat(who, "weight_in", weight_in, _F32T, dev, n, max_len)
+    if workspace is not None and (not workspace.is_contiguous() or workspace.get_device() != dev):
+        raise H3encError(2, f"{who}: workspace not contiguous, or on {workspace.device} with cuda:{dev} the current device")
     return _check(lib.h3enc_op_attention_decode(
-        q.data_ptr(), ld_q, o.data_ptr(), ld_o, cache, page_table.data_ptr(), ld_t, seq_lens.data_ptr(), n, n_heads,
-        max_len, None if weight_in is None else weight_in.data_ptr(),
-        None if weight_out is None else weight_out.data_ptr(), ld_w,
+        q, ld_q, o, ld_o, cache, page_table, ld_t, _vec(who, "seq_lens", seq_lens, _I32T, dev, n), n, n_heads, max_len,
+        weight_in, weight_out, ld_w,
         None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.nbytes,
-        None if status is None else status.data_ptr(), _stream(stream)))
+        None if status is None else _vec(who, "status", status, _I32T, dev, 1), raw(dev) if stream is None else _stream(stream)))
 
 
 def h3enc_op_cache_evict(cache, page_table, seq_lens, max_len, budget, weight, weight_out, kept, new_lens,
                          page_table_out=None, sink=0, recent=0, status=None, stream=None):
-    """Keep `budget` tokens per sequence by accumulated weight; in place, or into page_table_out's pages."""
-    n = seq_lens.numel()
-    if n > 1:
-        ld_t, ld_w, ld_w2, ld_k = page_table.stride(0), weight.stride(0), weight_out.stride(0), kept.stride(0)
-        ld_t2 = 0 if page_table_out is None else page_table_out.stride(0)
-    else:
-        ld_t, ld_w, ld_w2, ld_k = page_table.shape[1], weight.shape[1], weight_out.shape[1], kept.shape[1]
-        ld_t2 = 0 if page_table_out is None else page_table_out.shape[1]
+    """Keep `budget` tokens per sequence by accumulated weight; in place, or into page_table_out's pages.  int32
+    page tables [n_seqs, pages], lengths [n_seqs] and kept [n_seqs, >= budget], float32 weights [n_seqs, >= max_len]."""
+    if _BF16 is None:
+        _types()
+    who, n, page, (device, raw) = "cache_evict", seq_lens.numel(), cache.page_size, _raw or _raw_calls()
+    dev = device()
+    if cache.device_index != dev:
+        _refuse_cache(who, cache, dev)
+    page_table, ld_t = _mat(who, "page_table", page_table, _I32T, dev, n, -(-max_len // page))
+    ld_t2 = 0
+    if page_table_out is not None:
+        page_table_out, ld_t2 = _mat(who, "page_table_out", page_table_out, _I32T, dev, n, -(-min(budget, max_len) // page))
+    weight, ld_w = _mat(who, "weight", weight, _F32T, dev, n, max_len)
+    weight_out, ld_w2 = _mat(who, "weight_out", weight_out, _F32T, dev, n, max_len)
+    kept, ld_k = _mat(who, "kept", kept, _I32T, dev, n, budget)
     return _check(lib.h3enc_op_cache_evict(
-        cache, page_table.data_ptr(), ld_t, None if page_table_out is None else page_table_out.data_ptr(), ld_t2,
-        seq_lens.data_ptr(), n, max_len, budget, sink, recent, weight.data_ptr(), ld_w, weight_out.data_ptr(), ld_w2,
-        kept.data_ptr(), ld_k, new_lens.data_ptr(),
-        None if status is None else status.data_ptr(), _stream(stream)))
+        cache, page_table, ld_t, page_table_out, ld_t2, _vec(who, "seq_lens", seq_lens, _I32T, dev, n), n, max_len, budget,
+        sink, recent, weight, ld_w, weight_out, ld_w2, kept, ld_k,
+        _vec(who, "new_lens", new_lens, _I32T, dev, n),
+        None if status is None else _vec(who, "status", status, _I32T, dev, 1), raw(dev) if stream is None else _stream(stream)))
 
 
 def h3vis_create(cfg: VisionConfig):

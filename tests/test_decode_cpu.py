@@ -189,3 +189,124 @@ def test_kv_cache_checks_its_tensors(Q):
         with pytest.raises(ValueError):
             Q.KVCache(a, b, ks, vs)
     assert ctypes.sizeof(Q.KVCache) == 64
+
+
+# ---------------------------------------------------------------- what the Python calls check of their tensors
+
+class _Record:
+    """Stands in for the library: keeps a call's arguments and succeeds."""
+    def __getattr__(self, name):
+        def call(*args):
+            self.args = args
+            return 0
+        return call
+
+
+@pytest.fixture
+def on_cpu(Q, monkeypatch):
+    """The calls with host tensors taken for the current device's, and nothing behind them."""
+    torch = pytest.importorskip("torch")
+    rec = _Record()
+    monkeypatch.setattr(Q, "lib", rec)
+    monkeypatch.setattr(Q, "_raw", (lambda: -1, lambda device: 0))
+    return Q, torch, rec
+
+
+def _tensors(torch, T=3, nq=4, nkv=2, d=64, page=16, max_len=40, budget=24):
+    bf, i32 = torch.bfloat16, torch.int32
+    n = T
+    return dict(qkv=torch.zeros(T, (nq + 2 * nkv) * d, dtype=bf), w_q=torch.zeros(d, dtype=bf), w_k=torch.zeros(d, dtype=bf),
+                cos=torch.zeros(T, d // 2), sin=torch.zeros(T, d // 2), q=torch.zeros(T, nq * d, dtype=bf),
+                k=torch.zeros(T, nkv * d, dtype=bf), slots=torch.zeros(T, dtype=i32), status=torch.zeros(1, dtype=i32),
+                o=torch.zeros(T, nq * d, dtype=bf), table=torch.zeros(n, 3, dtype=i32), lens=torch.zeros(n, dtype=i32),
+                w=torch.zeros(n, max_len), w_out=torch.zeros(n, max_len), ws=torch.zeros(512, dtype=torch.uint8),
+                table_out=torch.zeros(n, 2, dtype=i32), kept=torch.zeros(n, budget, dtype=i32),
+                new=torch.zeros(n, dtype=i32), pool=torch.zeros(9, nkv, page, d, dtype=bf))
+
+
+def _py_rope(Q, t, T=3, cs_stride=0):
+    return Q.h3enc_op_qk_norm_rope(t["qkv"], T, 4, 2, 64, t["w_q"], t["w_k"], 1e-6, t["cos"], t["sin"], cs_stride, t["q"],
+                                   t["k"], cache=Q.KVCache(t["pool"], t["pool"]), slots=t["slots"], status=t["status"])
+
+
+def _py_attend(Q, t):
+    return Q.h3enc_op_attention_decode(t["q"], t["o"], Q.KVCache(t["pool"], t["pool"]), t["table"], t["lens"], 4, 40,
+                                       t["ws"], t["w"], t["w_out"], status=t["status"])
+
+
+def _py_evict(Q, t):
+    return Q.h3enc_op_cache_evict(Q.KVCache(t["pool"], t["pool"]), t["table"], t["lens"], 40, 24, t["w"], t["w_out"],
+                                  t["kept"], t["new"], page_table_out=t["table_out"], status=t["status"])
+
+
+PY_CALLS = [(_py_rope, ("qkv", "w_q", "w_k", "cos", "sin", "q", "k", "slots", "status")),
+            (_py_attend, ("q", "o", "table", "lens", "w", "w_out", "status")),
+            (_py_evict, ("table", "table_out", "lens", "w", "w_out", "kept", "new", "status"))]
+
+
+@pytest.mark.parametrize("call,names", PY_CALLS)
+def test_tensors_of_another_type_order_or_size_are_refused(on_cpu, call, names):
+    Q, torch, rec = on_cpu
+    call(Q, _tensors(torch))
+    other = {torch.int32: torch.int64, torch.float32: torch.bfloat16, torch.bfloat16: torch.float32}
+    for name in names:
+        good = _tensors(torch)[name]
+        bad = [good.to(other[good.dtype])]
+        if name != "status":
+            bad.append(good.new_zeros([2 * x for x in good.shape])[tuple([slice(None, None, 2)] * good.dim())])   # every other one
+            if name != "lens":                                        # (its size is the number of sequences)
+                bad.append(good[:-1])                                 # a row, or an element, too few
+        if good.dim() == 2:
+            bad.append(good.new_zeros(good.shape[::-1]).t())          # columns first
+            wide = good.new_zeros(good.shape[0], good.shape[1] + 64)
+            bad.append(wide[:, :good.shape[1] - 1])                   # the last column is not in the slice
+        for t in bad:
+            rec.args = None
+            with pytest.raises(Q.H3encError) as e:
+                call(Q, dict(_tensors(torch), **{name: t}))
+            assert e.value.code == 2 and rec.args is None, (name, tuple(t.shape), t.stride())
+
+
+@pytest.mark.parametrize("call,names", PY_CALLS)
+def test_tensors_on_another_device_are_refused(on_cpu, call, names, monkeypatch):
+    Q, torch, rec = on_cpu
+    monkeypatch.setattr(Q, "_raw", (lambda: 0, lambda device: 0))
+    t = _tensors(torch)
+    with pytest.raises(Q.H3encError) as e:
+        call(Q, t)                                                    # the cache too
+    assert e.value.code == 2 and "current device" in str(e.value)
+    monkeypatch.setattr(Q.KVCache, "device_index", property(lambda self: 0, lambda self, i: None), raising=False)
+    with pytest.raises(Q.H3encError) as e:
+        call(Q, t)
+    assert e.value.code == 2 and "current device" in str(e.value)
+
+
+def test_slices_single_rows_and_views_are_taken(on_cpu):
+    Q, torch, rec = on_cpu
+    t = _tensors(torch)
+    wide = torch.zeros(5, 1024, dtype=torch.bfloat16)
+    _py_rope(Q, dict(t, qkv=wide[:, 8:520], q=wide[:, 600:856]))      # slices of wider rows, more rows than needed
+    assert rec.args[:3] == (wide.data_ptr() + 16, 1024, 3) and rec.args[12:14] == (wide.data_ptr() + 1200, 1024)
+    assert rec.args[14:16] == (t["k"].data_ptr(), 128)
+    _py_rope(Q, dict(t, q=t["q"].view(3, 4, 64)))                     # heads as a dimension
+    assert rec.args[12:14] == (t["q"].data_ptr(), 256)
+    one = dict(t, qkv=wide[4:, 8:520], q=wide[2:, 8:264])             # one row: its stride means nothing
+    _py_rope(Q, one, T=1)
+    assert rec.args[1] == 512 and rec.args[13] == 256
+    _py_rope(Q, dict(t, qkv=wide[0, 8:520]), T=1)
+    grouped = torch.zeros(8, 32, 4)                                   # the row-interleaved tables
+    _py_rope(Q, dict(t, cos=grouped, sin=grouped), cs_stride=32)
+    with pytest.raises(Q.H3encError):
+        _py_rope(Q, dict(t, cos=grouped[:7], sin=grouped), cs_stride=32)
+    _py_rope(Q, t, T=0)
+    table = torch.zeros(4, 7, dtype=torch.int32)
+    _py_attend(Q, dict(t, table=table[1:, 2:]))
+    assert rec.args[5:7] == (table.data_ptr() + 36, 7)
+    _py_attend(Q, dict(t, w=t["w_out"]))                              # in place
+    assert rec.args[11] == rec.args[12] == t["w_out"].data_ptr()
+    with pytest.raises(ValueError):
+        _py_attend(Q, dict(t, w=torch.zeros(3, 50)))
+    _py_evict(Q, dict(t, new=t["lens"], kept=torch.zeros(3, 30, dtype=torch.int32)[:, :24]))
+    assert rec.args[16] == 30 and rec.args[17] == t["lens"].data_ptr()
+    Q.h3enc_op_attention_decode(t["q"], t["o"], Q.KVCache(t["pool"], t["pool"]), torch.zeros(3, 0, dtype=torch.int32),
+                                t["lens"], 4, 0, t["ws"], None, torch.zeros(3, 0))     # no tokens, no pages
