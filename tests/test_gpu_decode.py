@@ -534,6 +534,14 @@ def test_attention_decode_refuses_a_small_or_misaligned_workspace():
         assert e.value.code == 2
 
 
+def test_attention_decode_workspace_of_sizes_that_the_call_refuses():
+    size = Q.h3enc_op_attention_decode_workspace_bytes
+    assert 0 < size(1, 8, 2 ** 30) < 2 ** 30 and size(1, 1, 2 ** 30, True) >= 4 * 2 ** 30
+    for weights in (False, True):
+        for max_len in (2 ** 30 + 1, 2 ** 31 - 127, 2 ** 31 - 1):
+            assert size(1, 1, max_len, weights) == -1
+
+
 # ---------------------------------------------------------------- eviction
 
 def _weights(g, n, cols, kind):
