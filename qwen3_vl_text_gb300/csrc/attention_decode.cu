@@ -873,7 +873,8 @@ cudaError_t launch_kernel(const CUtensorMap &tk, const CUtensorMap &tv, const Ar
 size_t attention_decode_workspace_bytes(int num_sms, int n_seqs, int nq, int max_len, bool weights) {
     if (num_sms <= 0 || num_sms > MAX_CTAS || n_seqs < 0 || n_seqs > kMaxSeqs || nq < 1 || nq > 65536 || max_len < 0 ||
         max_len > kMaxCacheLen ||
-        (long long)n_seqs * nq * (((long long)max_len + 63) / 64) > INT_MAX)   // tiles of 64 or 128 keys
+        // tiles of 64 or 128 keys, counted in 32 bits; the producers look up to two batches of 32 boxes past a run's end
+        (long long)n_seqs * nq * (((long long)max_len + 63) / 64) > INT_MAX - 64)
         return 0;
     return layout(num_sms, n_seqs, nq, max_len, weights).bytes;
 }

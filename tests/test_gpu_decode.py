@@ -542,6 +542,20 @@ def test_attention_decode_workspace_of_sizes_that_the_call_refuses():
             assert size(1, 1, max_len, weights) == -1
 
 
+def test_attention_decode_counts_its_tiles_in_32_bits():
+    """2^31 - 2 = 154 * 13,944,699 tiles of 64 keys: the look-ahead behind the last of them would overflow."""
+    size = Q.h3enc_op_attention_decode_workspace_bytes
+    assert size(1, 154, 13944699 * 64) == -1 and size(154, 1, 13944699 * 64 - 63) == -1
+    assert size(1, 154, 13944698 * 64) > 0                    # 2^31 - 156
+    cache, table, seq, q, _ = _attend_case(_gen(16), [50], 154, 154, 64, BF16, 16)
+    wide = torch.full((1, 13944699 * 4), -1, dtype=torch.int32, device="cuda")
+    wide[:, :table.shape[1]] = table
+    o = torch.empty(1, 154 * 64, device="cuda", dtype=torch.bfloat16)
+    with pytest.raises(Q.H3encError) as e:
+        Q.h3enc_op_attention_decode(q, o, cache, wide, seq, 154, 13944699 * 64, _workspace(1, 154, 64))
+    assert e.value.code == 6
+
+
 # ---------------------------------------------------------------- eviction
 
 def _weights(g, n, cols, kind):
