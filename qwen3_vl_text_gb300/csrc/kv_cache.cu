@@ -379,7 +379,7 @@ __global__ void __launch_bounds__(SEL_THREADS, 1) evict_select_kernel(const Cach
     // the rest of the rows, by all CTAs of the cluster
     const int total = all ? len : p.budget;
     for (int i = total + (int)rank * SEL_THREADS + tid; i < p.max_len; i += ranks * SEL_THREADS) wo[i] = 0.f;
-    for (int i = total + (int)rank * SEL_THREADS + tid; i < p.budget; i += ranks * SEL_THREADS) kept[i] = -1;
+    for (long long i = total + (int)rank * SEL_THREADS + tid; i < p.budget; i += ranks * SEL_THREADS) kept[i] = -1;
     // new_lens may be seq_lens: every thread of the sequence has read the length (in a cluster: before the
     // barrier above)
     __syncthreads();

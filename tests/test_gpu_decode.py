@@ -684,6 +684,28 @@ def test_cache_evict_bad_pages_and_lengths_are_reported():
     assert int(status.item()) == 2 and new.tolist() == [0, 5]
 
 
+@pytest.mark.parametrize("top", [60, 5000])
+def test_cache_evict_of_the_largest_budget(top):
+    """A budget of 2^31 - 1: everything is kept, and -1 fills the row of 8.6 GB to its end and not further."""
+    g, budget = _gen(22), 2 ** 31 - 1
+    cache = _pool(g, -(-top // 16), 1, 16, 64, BF16)
+    for t in cache.tensors[:2]:
+        t.copy_(_randn(g, *t.shape))
+    before = [t.clone() for t in cache.tensors[:2]]
+    table = torch.arange(cache.num_pages, dtype=torch.int32, device="cuda")[None]
+    w, w_out = torch.rand(1, top, device="cuda", generator=g), torch.empty(1, top, device="cuda")
+    guard = 1 << 15
+    buf = torch.full((guard + budget + guard,), -9, dtype=torch.int32, device="cuda")
+    kept, new = buf[guard:guard + budget][None], torch.zeros(1, dtype=torch.int32, device="cuda")
+    Q.h3enc_op_cache_evict(cache, table, torch.tensor([top - 7], dtype=torch.int32, device="cuda"), top, budget, w, w_out, kept, new)
+    assert int(new) == top - 7 and kept[0, :top - 7].tolist() == list(range(top - 7))
+    rest = kept[0, top - 7:]
+    assert int(rest.min()) == -1 and int(rest.max()) == -1
+    assert (buf[:guard] == -9).all() and (buf[guard + budget:] == -9).all()
+    assert torch.equal(w_out[0, :top - 7], w[0, :top - 7]) and not w_out[0, top - 7:].any()
+    assert all(torch.equal(t, x) for t, x in zip(cache.tensors[:2], before))
+
+
 def test_decoding_of_sequences_without_any_token():
     """max_len = 0: no page table at all, zero rows from the attention, nothing kept by the eviction."""
     g = _gen(21)
