@@ -1611,7 +1611,7 @@ h3enc_status h3enc_op_cache_evict(const h3enc_kv_cache *cache, const int32_t *pa
         (page_table_out && (ld_table_out < 0 || (int64_t)ld_table_out * cache->page_size < most)))
         return fail(nullptr, H3ENC_ERR_INVALID_ARG, "%s: a page table does not hold the lengths", who);
     if (n_seqs == 0) return H3ENC_OK;
-    if ((!page_table && max_len > 0) || !seq_lens || !weight || !weight_out || !kept || !new_lens ||
+    if ((max_len > 0 && (!page_table || !weight || !weight_out)) || !seq_lens || !kept || !new_lens ||
         ld_weight < max_len || ld_weight_out < max_len || ld_kept < budget ||
         rows_overlap(weight, ld_weight, max_len, weight_out, ld_weight_out, max_len, n_seqs, 4))
         return fail(nullptr, H3ENC_ERR_INVALID_ARG, "%s: NULL operand, a bad leading dimension, or weight_out "

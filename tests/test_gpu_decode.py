@@ -720,6 +720,16 @@ def test_decoding_of_sequences_without_any_token():
     assert (kept == -1).all() and not new.any()
 
 
+def test_cache_evict_of_rows_without_any_place():
+    """max_len = 0 with weights and page tables of no columns (which have no address)."""
+    cache, none = _pool(_gen(23), 2, 2, 16, 64, BF16), torch.zeros(2, 0, device="cuda")
+    seq, kept = torch.zeros(2, dtype=torch.int32, device="cuda"), torch.zeros(2, 5, dtype=torch.int32, device="cuda")
+    new, table = torch.full((2,), 7, dtype=torch.int32, device="cuda"), none.to(torch.int32)
+    for out in (None, table):
+        Q.h3enc_op_cache_evict(cache, table, seq, 0, 5, none, none.clone(), kept.zero_(), new.fill_(7), page_table_out=out)
+        assert (kept == -1).all() and not new.any()
+
+
 # ---------------------------------------------------------------- together
 
 def test_decode_step_captured_in_a_graph():
