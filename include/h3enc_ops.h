@@ -376,8 +376,9 @@ H3ENC_API h3enc_status h3enc_op_qk_norm_rope(const void *qkv, int64_t ld_qkv, in
 /* Attention of one new token of each of n_seqs sequences over the cache (the new token's
  * own key and value already in it): for q head h, reading kv head h / (n_heads / n_kv_heads),
  *   p_i = softmax_i(q . k_i / sqrt(d)) over i < seq_lens[b],   o = sum_i p_i v_i
- * (fp32; o rounded to bf16 once; a sequence of length 0 gives a zero row; weights below
- * 2^-126 of the largest count as 0, also times an infinite value, which is NaN).
+ * (fp32, but p enters the second sum with 16 bits, 22 for E4M3; o rounded to bf16 once; a
+ * sequence of length 0 gives a zero row; weights below 2^-126 of the largest count as 0,
+ * also times an infinite value, which is NaN).
  *   q [n_seqs, ld_q], o [n_seqs, ld_o]: head h at column h*d; o must not overlap q.
  *   page_table DEVICE int32 [n_seqs, ld_table], seq_lens DEVICE int32 [n_seqs]; max_len: a
  *   bound on the lengths known to the host (ld_table * page_size >= max_len).  A length
@@ -412,7 +413,7 @@ H3ENC_API int64_t h3enc_op_attention_decode_workspace_bytes(int32_t n_seqs, int3
  * keep their order and move, K, V and weight, to the front.  Shorter sequences keep all.
  *   page_table, seq_lens, max_len as for h3enc_op_attention_decode (lengths clamped the same way).
  *   page_table_out NULL: in place, within the pages of page_table (which must not be shared
- *   between sequences).  Otherwise DEVICE int32 [n_seqs, ld_table_out], ld_table_out *
+ *   between sequences, nor appear twice in one).  Otherwise DEVICE int32 [n_seqs, ld_table_out], ld_table_out *
  *   page_size >= min(budget, max_len): token i of the result goes to page
  *   page_table_out[b][i / page_size], pages that this call does not read; the source
  *   pages stay as they were.  Tokens whose page number, on either side, lies

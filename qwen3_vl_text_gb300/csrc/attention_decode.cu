@@ -24,10 +24,11 @@
 //    2^-24, so the two halves then leave an error of at most 2^-39 of a warp's largest weight, far below the
 //    fp32 sums; unscaled, every weight under 2^-25 of the largest would be lost to o but counted in l.
 // Measured (64 q heads over 8 kv heads of 128, pages of 64): 64 sequences of 5000 to 8192 tokens in bf16, 1.7 GB,
-// 248-251 us = 6.8 TB/s, the measured copy rate; in e4m3 140 us (5.9 TB/s: the conversions of every key and value
-// to f16 then take most of the time between two tiles); one sequence of 1025 tokens 7.2 us, which is
-// the chain length -> page number -> tile -> products -> join across CTAs.  A call's fixed part is about
-// 8 us: 2.5 until the first tile lands, the rest the joins at the end and the spread of the SMs' rates.
+// 248-251 us = 6.8 TB/s, the measured copy rate; in e4m3 139-140 us (6.0 TB/s: the conversions of every key and value
+// to f16 then take most of the time between two tiles); one sequence of 1025 tokens 7.3 us, which is
+// the chain length -> page number -> tile -> products -> join across CTAs.  Calls that fill the SMs take 8 to
+// 12 us more than their bytes at the copy rate (16 of those sequences 70 us, 62.5 of them bytes): 2.5 until the first tile
+// lands, the rest the joins at the end and the spread of the SMs' rates.
 #include <algorithm>
 #include <atomic>
 #include <climits>
@@ -890,7 +891,7 @@ cudaError_t launch_attention_decode(const AttentionDecode &p, cudaStream_t st) {
     // More than 16 heads of a kv head: segments of 32 heads read a key once, segments of 16 once for every 16
     // heads but from L2 where the cache fits there, with twice the segments and half the rows to join.  40 q heads over 2 kv
     // heads of 128, 32 and 8 sequences of 20,000 to 24,000 tokens (787 and 197 MB by max_len): 128 and 46 us against
-    // 213 and 54; 64 over 1, two sequences (25 MB): 32 us against 23; e4m3, 8 sequences (98 MB): 45 against 43.
+    // 211 and 54; 64 over 1, two sequences of 25,000 (25 MB): 35 us against 24; e4m3, 8 sequences (98 MB): 45 against 43.
     const double bytes = 2.0 * p.n_seqs * p.max_len * p.cache.nkv * p.cache.d * (p.cache.f8 ? 1 : 2);
     const bool split = a.group > WROWS && bytes > 1e8;
     const int rows = split ? 2 * WROWS : WROWS;   // heads of a segment

@@ -221,8 +221,8 @@ __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.w
 // kept, which two digits almost always reach unless weights are equal.  In a cluster every CTA adds the bins
 // that it has anything in to the first one's sums, which finds the digit for all.
 // Then the tokens are counted in order, as bit masks of 32, and each kept one is written to its place.
-// What bounds it is the chain of these steps, not the 4 bytes per token: 8 us for 32 sequences of 4608 tokens,
-// 11 us for one of 65,537.
+// What bounds it is the chain of these steps, not the 4 bytes per token: back to back 8.1 us for 32 sequences of 4608 tokens,
+// 10.8 us for one of 65,537 (the first with cold caches, under ncu: 12.4).
 template <bool CLUSTER>
 __global__ void __launch_bounds__(SEL_THREADS, 1) evict_select_kernel(const CacheEvict p, int cached) {
     extern __shared__ float held[];               // [cached] weights
