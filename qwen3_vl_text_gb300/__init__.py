@@ -167,14 +167,13 @@ _SIGS = {
     "h3enc_op_attention_bidir": ([_P, _P, _I32, _I32, _I32, _P, _I32, _P], _I32),
     "h3enc_op_attention_bidir_ws": ([_P, _P, _I32, _I32, _I32, _P, _I32, _P, _I64, _P], _I32),
     "h3enc_op_attention_workspace_bytes": ([_I32], _I64),
-    # (integers as _P: both machines pass an address and an integer of 64 or 32 bits alike, and a ctypes address takes
-    # 80 ns to convert where an integer takes 140)
-    "h3enc_op_qk_norm_rope": ([_P, _P, _P, _P, _P, _P, _P, _P, _F, _P, _P, _P, _P, _P, _P, _P, ctypes.POINTER(KVCache),
-                               _P, _P, _P], _I32),
-    "h3enc_op_attention_decode": ([_P, _P, _P, _P, ctypes.POINTER(KVCache), _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P,
-                                   _P, _P], _I32),
+    "h3enc_op_qk_norm_rope": ([_P, _I64, _I32, _I32, _I32, _I32, _P, _P, _F, _P, _P, _I32, _P, _I64, _P, _I64,
+                               ctypes.POINTER(KVCache), _P, _P, _P], _I32),
+    "h3enc_op_attention_decode": ([_P, _I64, _P, _I64, ctypes.POINTER(KVCache), _P, _I32, _P, _I32, _I32, _I32, _P, _P,
+                                   _I64, _P, _I64, _P, _P], _I32),
     "h3enc_op_attention_decode_workspace_bytes": ([_I32, _I32, _I32, _I32], _I64),
-    "h3enc_op_cache_evict": ([ctypes.POINTER(KVCache)] + [_P] * 19, _I32),
+    "h3enc_op_cache_evict": ([ctypes.POINTER(KVCache), _P, _I32, _P, _I32, _P, _I32, _I32, _I32, _I32, _I32, _P, _I64,
+                              _P, _I64, _P, _I64, _P, _P, _P], _I32),
     "h3vis_create": ([ctypes.POINTER(VisionConfig), ctypes.POINTER(_P)], _I32),
     "h3vis_load_weights": ([_P, ctypes.c_char_p, _P, _I32, ctypes.POINTER(_I64), _I32, _I32], _I32),
     "h3vis_finalize_weights": ([_P], _I32),

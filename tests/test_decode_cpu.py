@@ -281,6 +281,26 @@ def test_tensors_on_another_device_are_refused(on_cpu, call, names, monkeypatch)
     assert e.value.code == 2 and "current device" in str(e.value)
 
 
+@pytest.mark.parametrize("call", [_py_rope, _py_attend, _py_evict])
+def test_sizes_may_be_any_integers(Q, call, monkeypatch):
+    """numpy integers and tensors of one element, through the real argument types, up to the C entry's own refusal."""
+    torch = pytest.importorskip("torch")
+    monkeypatch.setattr(Q, "_raw", (lambda: -1, lambda device: 0))
+    t = _tensors(torch)
+    for of in (int, np.int32, np.int64, torch.tensor):
+        cache = Q.KVCache(t["pool"], t["pool"])
+        with pytest.raises(Q.H3encError) as e:
+            if call is _py_rope:
+                Q.h3enc_op_qk_norm_rope(t["qkv"], of(3), of(4), of(2), of(64), t["w_q"], t["w_k"], -1e-6, t["cos"], t["sin"],
+                                        of(0), t["q"], t["k"], cache=cache, slots=t["slots"])
+            elif call is _py_attend:
+                Q.h3enc_op_attention_decode(t["q"], t["o"], cache, t["table"], t["lens"], of(3), of(40), t["ws"])
+            else:
+                Q.h3enc_op_cache_evict(cache, t["table"], t["lens"], of(40), of(24), t["w"], t["w_out"], t["kept"], t["new"],
+                                       sink=of(20), recent=of(5))
+        assert e.value.code == 2
+
+
 def test_slices_single_rows_and_views_are_taken(on_cpu):
     Q, torch, rec = on_cpu
     t = _tensors(torch)
