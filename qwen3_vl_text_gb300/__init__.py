@@ -595,7 +595,7 @@ _BF16 = _I32T = _F32T = None
 def _types():
     global _BF16, _I32T, _F32T
     import torch
-    _BF16, _I32T, _F32T = torch.bfloat16, torch.int32, torch.float32
+    _I32T, _F32T, _BF16 = torch.int32, torch.float32, torch.bfloat16   # _BF16 last: the calls, of any thread, look at it
 
 
 def _vec(who, name, t, dtype, dev, n):
