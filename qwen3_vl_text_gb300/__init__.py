@@ -608,14 +608,18 @@ def _vec(who, name, t, dtype, dev, n):
 
 
 def _mat(who, name, t, dtype, dev, rows, width):
-    """(address, leading dimension) of at least `rows` rows, each contiguous and of at least `width` elements.  A single
-    row's stride means nothing: its leading dimension is the width."""
-    if t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
-        ld = width if rows < 2 else t.stride()[0]
-        if ld >= width and t.numel() >= rows * ld:
-            return t.data_ptr(), ld
+    """(address, leading dimension) of at least `rows` rows, each contiguous and of at least `width` elements; a vector
+    is rows of `width`.  A single row's stride means nothing: its leading dimension is the width."""
+    try:
+        (n, m), (ld, step) = t.shape, t.stride()
+        if step == 1 and m >= width and n >= rows and t.dtype is dtype and t.get_device() == dev:
+            return t.data_ptr(), width if rows < 2 else ld
+    except ValueError:   # not two dimensions
+        pass
     _common(who, name, t, dtype, dev)
     shape, strides, inner = t.shape, t.stride(), 1
+    if len(shape) == 1 and strides[0] == 1 and shape[0] >= rows * width:
+        return t.data_ptr(), width
     for i in range(len(shape) - 1, 0, -1):
         if shape[i] != 1 and strides[i] != inner:
             inner = -1

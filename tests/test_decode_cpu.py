@@ -314,6 +314,12 @@ def test_slices_single_rows_and_views_are_taken(on_cpu):
     _py_rope(Q, one, T=1)
     assert rec.args[1] == 512 and rec.args[13] == 256
     _py_rope(Q, dict(t, qkv=wide[0, 8:520]), T=1)
+    with pytest.raises(Q.H3encError):                                 # the row is short, although more rows follow
+        _py_rope(Q, dict(t, q=torch.zeros(2, 128, dtype=torch.bfloat16)), T=1)
+    for name, short in (("table", torch.zeros(4, 2, dtype=torch.int32)), ("w", torch.zeros(2, 39))):
+        with pytest.raises(Q.H3encError):
+            _py_attend(Q, dict(t, lens=t["lens"][:1], **{name: short}))
+    _py_attend(Q, dict(t, lens=t["lens"][:1], table=torch.zeros(3, dtype=torch.int32)))
     grouped = torch.zeros(8, 32, 4)                                   # the row-interleaved tables
     _py_rope(Q, dict(t, cos=grouped, sin=grouped), cs_stride=32)
     with pytest.raises(Q.H3encError):
