@@ -394,7 +394,8 @@ H3ENC_API h3enc_status h3enc_op_qk_norm_rope(const void *qkv, int64_t ld_qkv, in
  * The result does not depend on timing: the same inputs give the same bits on every run.  A
  * bounded wait that runs out sets status bit 1; the outputs are then undefined.
  * Requires n_seqs <= 1024, max_len <= 2^30, n_heads % n_kv_heads == 0, leading dimensions of
- * q and o that are multiples of 8, q and o 16-byte aligned. */
+ * q and o that are multiples of 8, q and o 16-byte aligned; n_seqs * n_heads * ceil(max_len / 64)
+ * above 2^31 - 65 is H3ENC_ERR_UNSUPPORTED. */
 H3ENC_API h3enc_status h3enc_op_attention_decode(const void *q, int64_t ld_q, void *o, int64_t ld_o,
                                                  const h3enc_kv_cache *cache, const int32_t *page_table,
                                                  int32_t ld_table, const int32_t *seq_lens, int32_t n_seqs,

@@ -687,6 +687,8 @@ def h3enc_op_attention_decode(q, o, cache, page_table, seq_lens, n_heads, max_le
     q, ld_q = _mat(who, "q", q, _BF16, dev, n, width)
     o, ld_o = _mat(who, "o", o, _BF16, dev, n, width)
     page_table, ld_t = _mat(who, "page_table", page_table, _I32T, dev, n, -(-max_len // cache.page_size))
+    if ld_t > 0x7fffffff:      # (a C argument of 32 bits: it would be cut off)
+        raise H3encError(2, f"{who}: the rows of page_table lie too far apart")
     ld_w = 0
     if weight_out is not None:
         same = weight_in is weight_out
@@ -722,6 +724,8 @@ def h3enc_op_cache_evict(cache, page_table, seq_lens, max_len, budget, weight, w
     ld_t2 = 0
     if page_table_out is not None:
         page_table_out, ld_t2 = _mat(who, "page_table_out", page_table_out, _I32T, dev, n, -(-min(budget, max_len) // page))
+    if ld_t > 0x7fffffff or ld_t2 > 0x7fffffff or not 0 <= sink <= budget or not 0 <= recent <= budget:
+        raise H3encError(2, f"{who}: the rows of a page table lie too far apart, or bad sizes")   # (C arguments of 32 bits)
     weight, ld_w = _mat(who, "weight", weight, _F32T, dev, n, max_len)
     weight_out, ld_w2 = _mat(who, "weight_out", weight_out, _F32T, dev, n, max_len)
     kept, ld_k = _mat(who, "kept", kept, _I32T, dev, n, budget)

@@ -301,6 +301,27 @@ def test_sizes_may_be_any_integers(Q, call, monkeypatch):
         assert e.value.code == 2
 
 
+def test_numbers_beyond_a_32_bit_argument_are_refused(on_cpu):
+    Q, torch, rec = on_cpu
+    t = _tensors(torch)
+    far = torch.empty_strided((3, 3), (2 ** 32 + 8, 1), dtype=torch.int32, device="meta")     # 8 if it is cut off
+    c = Q.KVCache(t["pool"], t["pool"])
+    for call in (lambda: _py_attend(Q, dict(t, table=far)), lambda: _py_evict(Q, dict(t, table=far)),
+                 lambda: _py_evict(Q, dict(t, table_out=far)),
+                 lambda: Q.h3enc_op_cache_evict(c, t["table"], t["lens"], 40, 24, t["w"], t["w_out"], t["kept"], t["new"],
+                                                sink=2 ** 32 + 3),
+                 lambda: Q.h3enc_op_cache_evict(c, t["table"], t["lens"], 40, 24, t["w"], t["w_out"], t["kept"], t["new"],
+                                                recent=-2 ** 32 + 3),
+                 lambda: Q.h3enc_op_cache_evict(c, t["table"], t["lens"], 40, 2 ** 32 + 24, t["w"], t["w_out"], t["kept"],
+                                                t["new"]),
+                 lambda: Q.h3enc_op_attention_decode(t["q"], t["o"], c, t["table"], t["lens"], 4, 2 ** 32 + 40, t["ws"]),
+                 lambda: _py_rope(Q, t, T=2 ** 32 + 3)):
+        rec.args = None
+        with pytest.raises(Q.H3encError) as e:
+            call()
+        assert e.value.code == 2 and rec.args is None
+
+
 def test_slices_single_rows_and_views_are_taken(on_cpu):
     Q, torch, rec = on_cpu
     t = _tensors(torch)
