@@ -432,6 +432,54 @@ H3ENC_API h3enc_status h3enc_op_cache_evict(const h3enc_kv_cache *cache, const i
                                             float *weight_out, int64_t ld_weight_out, int32_t *kept, int64_t ld_kept,
                                             int32_t *new_lens, int32_t *status, void *stream);
 
+/* Rotary positions, for h3enc_op_rope_append: the first rotary_dim elements of a head rotate in pairs, pair j by the angle
+ * position * w_j with w_j = theta^(-2j / rotary_dim), scaled for contexts longer than original_len tokens:
+ *   ROPE_LINEAR      w_j / factor
+ *   ROPE_WAVELENGTH  with n_j = original_len w_j / 2 pi, the turns of pair j over the original context, and
+ *                    s = clamp((n_j - low_turns) / (high_turns - low_turns), 0, 1):  w_j (s + (1 - s) / factor)
+ *   ROPE_YARN        with dim(n) = rotary_dim ln(original_len / (2 pi n)) / (2 ln theta), a = max(floor(dim(high_turns)), 0),
+ *                    e = min(ceil(dim(low_turns)), rotary_dim - 1) and s = clamp((j - a) / max(e - a, 0.001), 0, 1):
+ *                    w_j (1 - s) + (w_j / factor) s
+ * cos and sin are multiplied by magnitude.  Angles are exact to the last bits of fp32 at every position (they are reduced
+ * as 64-bit fractions of a turn), but for w_j's own rounding to 53 bits. */
+enum { H3ENC_ROPE_PLAIN = 0, H3ENC_ROPE_LINEAR = 1, H3ENC_ROPE_WAVELENGTH = 2, H3ENC_ROPE_YARN = 3 };
+typedef struct {
+    int32_t rotary_dim;    /* a multiple of 16, at most head_dim */
+    int32_t interleaved;   /* 0: pairs (j, j + rotary_dim/2); 1: pairs (2j, 2j + 1) */
+    int32_t scaling;       /* H3ENC_ROPE_* */
+    int32_t original_len;  /* WAVELENGTH and YARN: >= 1 */
+    double theta;          /* > 0; YARN: > 1 */
+    double factor;         /* > 0; PLAIN ignores it */
+    double low_turns, high_turns;   /* WAVELENGTH, YARN: 0 < low < high; both 0: 1 and 4, YARN 1 and 32 */
+    double magnitude;      /* > 0; 0: 1, YARN with a factor above 1: 0.1 ln(factor) + 1 */
+    int32_t section[3];    /* {0, 0, 0}: one position per row; else three-axis positions, pair j by axis(j) of
+                              h3enc_op_rope_table, and the sections sum to rotary_dim/2 */
+} h3enc_rope;
+
+/* New rows of a packed projection normed, rotated and appended to their sequences in a cache, in one pass: what
+ * h3enc_op_qk_norm_rope does with slots and tables that the caller makes, by page table, lengths and positions alone.
+ *   qkv [T, ld_qkv], w_q, w_k, eps, q_out, k_out and their in-place rules as for h3enc_op_qk_norm_rope.  Each q and k
+ *   head becomes rotate(rmsnorm(x)) in fp32, rounded once (w_q / w_k NULL: no norm; rope NULL: no rotation).
+ *   seq_lens DEVICE int32 [n_seqs]: each sequence's tokens, the new ones counted in.  cu_rows DEVICE int32 [n_seqs + 1]:
+ *   rows [cu_rows[b], cu_rows[b + 1]) are the last tokens of sequence b, in order; NULL: row b is the last token
+ *   of sequence b.  Rows of no sequence are left as they were in every output.
+ *   positions DEVICE int32 [1 or 3 axes, ld_positions] (of any sign); NULL: a row's position is its token's index in
+ *   its sequence.
+ *   cache (or NULL) with page_table DEVICE int32 [n_seqs, ld_table], ld_table * page_size >= max_len: k and v of token i
+ *   of sequence b go to place i % page_size of page page_table[b][i / page_size].  A token outside [0, max_len)
+ *   or on a page outside the cache is not stored and sets status bit 2 (its q_out and k_out are written).
+ *   Without a cache, seq_lens may be NULL too (n_seqs 0, cu_rows NULL): all T rows are rotated by `positions`, which must
+ *   then be given if rope is.
+ * Requires head_dim in {64, 128}, n_seqs <= 1024, max_len <= 2^30, leading dimensions that are multiples of 8, operands
+ * 16-byte aligned, at least one of q_out, k_out and cache. */
+H3ENC_API h3enc_status h3enc_op_rope_append(const void *qkv, int64_t ld_qkv, int32_t T, int32_t n_heads,
+                                            int32_t n_kv_heads, int32_t head_dim, const void *w_q, const void *w_k,
+                                            float eps, const h3enc_rope *rope, const int32_t *positions,
+                                            int64_t ld_positions, void *q_out, int64_t ld_q, void *k_out, int64_t ld_k,
+                                            const h3enc_kv_cache *cache, const int32_t *page_table, int32_t ld_table,
+                                            const int32_t *seq_lens, const int32_t *cu_rows, int32_t n_seqs,
+                                            int32_t max_len, int32_t *status, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

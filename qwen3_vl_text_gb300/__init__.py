@@ -31,6 +31,7 @@ __all__ = [
     "h3vis_last_error", "h3vis_launch_count", "h3vis_destroy", "VisionEncoder", "h3enc_op_attention", "h3enc_op_embed", "h3enc_op_vis_rank", "Encoder",
     "KERNEL_CLASSES", "KVCache", "h3enc_op_qk_norm_rope", "h3enc_op_attention_decode",
     "h3enc_op_attention_decode_workspace_bytes", "h3enc_op_cache_evict",
+    "Rope", "h3enc_op_rope_append",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -98,6 +99,27 @@ class KVCache(ctypes.Structure):
                          2 if k.dtype == torch.float8_e4m3fn else 0)
         self.tensors = (k, v, k_scale, v_scale)
         self.device_index = k.get_device()
+
+
+class Rope(ctypes.Structure):
+    """h3enc_rope: which elements of a head rotate, in which pairs, and at which (scaled) frequencies.  scaling: "none",
+    "linear", "wavelength" or "yarn"; section: the three-axis positions' (t, h, w) shares of the rotary_dim / 2 pairs."""
+    _fields_ = [("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("scaling", ctypes.c_int32),
+                ("original_len", ctypes.c_int32), ("theta", ctypes.c_double), ("factor", ctypes.c_double),
+                ("low_turns", ctypes.c_double), ("high_turns", ctypes.c_double), ("magnitude", ctypes.c_double),
+                ("section", ctypes.c_int32 * 3)]
+    SCALINGS = ("none", "linear", "wavelength", "yarn")
+
+    def __init__(self, rotary_dim, theta, interleaved=False, scaling="none", factor=1.0, original_len=0, low_turns=0.0,
+                 high_turns=0.0, magnitude=0.0, section=None):
+        if scaling not in self.SCALINGS:
+            raise ValueError(f"Rope: scaling must be one of {self.SCALINGS}, not {scaling!r}")
+        section = tuple(section) if section is not None else (0, 0, 0)
+        if len(section) != 3 or not all(-2 ** 31 <= x < 2 ** 31 for x in (rotary_dim, original_len, *section)):
+            raise ValueError("Rope: bad sizes")
+        super().__init__(rotary_dim, 1 if interleaved else 0, self.SCALINGS.index(scaling), original_len, theta, factor,
+                         low_turns, high_turns, magnitude, (ctypes.c_int32 * 3)(*section))
+        self.axes = 3 if any(section) else 1
 
 
 def _load():
@@ -169,6 +191,8 @@ _SIGS = {
     "h3enc_op_attention_workspace_bytes": ([_I32], _I64),
     "h3enc_op_qk_norm_rope": ([_P, _I64, _I32, _I32, _I32, _I32, _P, _P, _F, _P, _P, _I32, _P, _I64, _P, _I64,
                                ctypes.POINTER(KVCache), _P, _P, _P], _I32),
+    "h3enc_op_rope_append": ([_P, _I64, _I32, _I32, _I32, _I32, _P, _P, _F, ctypes.POINTER(Rope), _P, _I64, _P, _I64, _P,
+                              _I64, ctypes.POINTER(KVCache), _P, _I32, _P, _P, _I32, _I32, _P, _P], _I32),
     "h3enc_op_attention_decode": ([_P, _I64, _P, _I64, ctypes.POINTER(KVCache), _P, _I32, _P, _I32, _I32, _I32, _P, _P,
                                    _I64, _P, _I64, _P, _P], _I32),
     "h3enc_op_attention_decode_workspace_bytes": ([_I32, _I32, _I32, _I32], _I64),
@@ -666,6 +690,42 @@ def h3enc_op_qk_norm_rope(qkv, T, n_heads, n_kv_heads, head_dim, w_q, w_k, eps, 
         None if cos_tab is None else _vec(who, "cos_tab", cos_tab, _F32T, dev, n),
         None if sin_tab is None else _vec(who, "sin_tab", sin_tab, _F32T, dev, n), cs_stride, q_out, ld_q, k_out, ld_k,
         cache, None if slots is None else _vec(who, "slots", slots, _I32T, dev, T),
+        None if status is None else _vec(who, "status", status, _I32T, dev, 1), raw(dev) if stream is None else _stream(stream)))
+
+
+def h3enc_op_rope_append(qkv, T, n_heads, n_kv_heads, head_dim, w_q, w_k, eps, rope, positions=None, q_out=None,
+                         k_out=None, cache=None, page_table=None, seq_lens=None, max_len=0, cu_rows=None, status=None,
+                         stream=None):
+    """Per-head q/k RMSNorm and rotation (a Rope, or None) of new rows, K and V appended to their sequences in a KVCache.
+    bfloat16 rows and weights; int32 positions [T] or [3, T], page_table [n_seqs, pages], seq_lens [n_seqs] (new rows counted in),
+    cu_rows [n_seqs + 1] (None: row b is the new token of sequence b)."""
+    if _BF16 is None:
+        _types()
+    who, (device, raw) = "rope_append", _raw or _raw_calls()
+    dev = device()
+    if cache is not None and cache.device_index != dev:
+        _refuse_cache(who, cache, dev)
+    qkv, ld_qkv = _mat(who, "qkv", qkv, _BF16, dev, T, (n_heads + 2 * n_kv_heads) * head_dim)
+    ld_q = ld_k = ld_p = ld_t = n = 0
+    if q_out is not None:
+        q_out, ld_q = _mat(who, "q_out", q_out, _BF16, dev, T, n_heads * head_dim)
+    if k_out is not None:
+        k_out, ld_k = _mat(who, "k_out", k_out, _BF16, dev, T, n_kv_heads * head_dim)
+    if positions is not None:
+        positions, ld_p = _mat(who, "positions", positions, _I32T, dev, 1 if rope is None else rope.axes, T)
+    if seq_lens is not None:
+        n = seq_lens.numel()
+        seq_lens = _vec(who, "seq_lens", seq_lens, _I32T, dev, n)
+    if page_table is not None:
+        page_table, ld_t = _mat(who, "page_table", page_table, _I32T, dev, n, 0 if cache is None else -(-max_len // cache.page_size))
+        if ld_t > 0x7fffffff:      # (a C argument of 32 bits: it would be cut off)
+            raise H3encError(2, f"{who}: the rows of page_table lie too far apart")
+    return _check(lib.h3enc_op_rope_append(
+        qkv, ld_qkv, T, n_heads, n_kv_heads, head_dim,
+        None if w_q is None else _vec(who, "w_q", w_q, _BF16, dev, head_dim),
+        None if w_k is None else _vec(who, "w_k", w_k, _BF16, dev, head_dim), eps, rope, positions, ld_p, q_out, ld_q,
+        k_out, ld_k, cache, page_table, ld_t, seq_lens,
+        None if cu_rows is None else _vec(who, "cu_rows", cu_rows, _I32T, dev, n + 1), n, max_len,
         None if status is None else _vec(who, "status", status, _I32T, dev, 1), raw(dev) if stream is None else _stream(stream)))
 
 

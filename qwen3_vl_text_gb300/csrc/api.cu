@@ -9,6 +9,7 @@
 // forward (page "vllm-omni vllm_omni/diffusion/models/minimax_h3/encoder.py").
 // The hidden state lives in the caller's output buffer for the whole encode.
 #include <algorithm>
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstdlib>
@@ -1461,6 +1462,35 @@ bool rows_overlap(const void *a, int64_t lda, int64_t ca, const void *b, int64_t
     return delta < (Wide)ca * es || delta + (Wide)cb * es > row;
 }
 
+// The rows that h3enc_op_qk_norm_rope and h3enc_op_rope_append read and write.
+h3enc_status check_qkv_rows(const char *who, const void *qkv, int64_t ld_qkv, int32_t T, int32_t n_heads, int32_t n_kv_heads,
+                            int32_t head_dim, const void *w_q, const void *w_k, float eps, const void *q_out, int64_t ld_q,
+                            const void *k_out, int64_t ld_k, bool cache) {
+    if (T < 0 || n_heads < 1 || n_kv_heads < 1 || (head_dim != 64 && head_dim != 128) || n_heads > 65536 ||
+        n_kv_heads > 65536)
+        return fail(nullptr, H3ENC_ERR_INVALID_ARG, "%s: bad sizes", who);
+    const int64_t d = head_dim, cols = ((int64_t)n_heads + 2 * (int64_t)n_kv_heads) * d;
+    if (!qkv || !aligned16(qkv) || ld_qkv < cols || ld_qkv % 8)
+        return fail(nullptr, H3ENC_ERR_INVALID_ARG, "%s: qkv NULL, misaligned or its leading dimension bad", who);
+    if (((w_q || w_k) && !(eps >= 0.f)) || !aligned16(w_q) || !aligned16(w_k))
+        return fail(nullptr, H3ENC_ERR_INVALID_ARG, "%s: norm weight misaligned or eps negative", who);
+    if (!q_out && !k_out && !cache) return fail(nullptr, H3ENC_ERR_INVALID_ARG, "%s: no output", who);
+    if ((q_out && (!aligned16(q_out) || ld_q < n_heads * d || ld_q % 8)) ||
+        (k_out && (!aligned16(k_out) || ld_k < n_kv_heads * d || ld_k % 8)))
+        return fail(nullptr, H3ENC_ERR_INVALID_ARG, "%s: output misaligned or its leading dimension bad", who);
+    const char *q_at = static_cast<const char *>(qkv), *k_at = q_at + n_heads * d * 2;
+    const auto in_place = [&](const void *out, const char *at, int64_t ld) {
+        return out == at && (ld == ld_qkv || T <= 1);
+    };
+    if ((q_out && !in_place(q_out, q_at, ld_q) &&
+         rows_overlap(qkv, ld_qkv, cols, q_out, ld_q, n_heads * d, T, 2)) ||
+        (k_out && !in_place(k_out, k_at, ld_k) &&
+         rows_overlap(qkv, ld_qkv, cols, k_out, ld_k, n_kv_heads * d, T, 2)) ||
+        (q_out && k_out && rows_overlap(q_out, ld_q, n_heads * d, k_out, ld_k, n_kv_heads * d, T, 2)))
+        return fail(nullptr, H3ENC_ERR_INVALID_ARG, "%s: outputs overlap qkv (other than in place) or each other", who);
+    return H3ENC_OK;
+}
+
 h3enc_status take_cache(const h3enc_kv_cache *c, const char *who, h3::KvCache *out) {
     if (!c || !c->k || !c->v || !aligned16(c->k) || !aligned16(c->v))
         return fail(nullptr, H3ENC_ERR_INVALID_ARG, "%s: cache NULL or not 16-byte aligned", who);
@@ -1496,31 +1526,12 @@ h3enc_status h3enc_op_qk_norm_rope(const void *qkv, int64_t ld_qkv, int32_t T, i
                                    int64_t ld_q, void *k_out, int64_t ld_k, const h3enc_kv_cache *cache,
                                    const int32_t *slots, int32_t *status, void *stream) {
     const char *who = "qk_norm_rope";
-    if (T < 0 || n_heads < 1 || n_kv_heads < 1 || (head_dim != 64 && head_dim != 128) || n_heads > 65536 ||
-        n_kv_heads > 65536)
-        return fail(nullptr, H3ENC_ERR_INVALID_ARG, "%s: bad sizes", who);
-    const int64_t d = head_dim, cols = ((int64_t)n_heads + 2 * (int64_t)n_kv_heads) * d;
-    if (!qkv || !aligned16(qkv) || ld_qkv < cols || ld_qkv % 8)
-        return fail(nullptr, H3ENC_ERR_INVALID_ARG, "%s: qkv NULL, misaligned or its leading dimension bad", who);
+    const h3enc_status bad = check_qkv_rows(who, qkv, ld_qkv, T, n_heads, n_kv_heads, head_dim, w_q, w_k, eps, q_out, ld_q,
+                                            k_out, ld_k, cache != nullptr);
+    if (bad != H3ENC_OK) return bad;
     if ((cos_tab == nullptr) != (sin_tab == nullptr) || !aligned16(cos_tab) || !aligned16(sin_tab) || cs_stride < 0 ||
         (cs_stride && cs_stride < T))
         return fail(nullptr, H3ENC_ERR_INVALID_ARG, "%s: one table NULL or misaligned, or table stride below T", who);
-    if (((w_q || w_k) && !(eps >= 0.f)) || !aligned16(w_q) || !aligned16(w_k))
-        return fail(nullptr, H3ENC_ERR_INVALID_ARG, "%s: norm weight misaligned or eps negative", who);
-    if (!q_out && !k_out && !cache) return fail(nullptr, H3ENC_ERR_INVALID_ARG, "%s: no output", who);
-    if ((q_out && (!aligned16(q_out) || ld_q < n_heads * d || ld_q % 8)) ||
-        (k_out && (!aligned16(k_out) || ld_k < n_kv_heads * d || ld_k % 8)))
-        return fail(nullptr, H3ENC_ERR_INVALID_ARG, "%s: output misaligned or its leading dimension bad", who);
-    const char *q_at = static_cast<const char *>(qkv), *k_at = q_at + n_heads * d * 2;
-    const auto in_place = [&](const void *out, const char *at, int64_t ld) {
-        return out == at && (ld == ld_qkv || T <= 1);
-    };
-    if ((q_out && !in_place(q_out, q_at, ld_q) &&
-         rows_overlap(qkv, ld_qkv, cols, q_out, ld_q, n_heads * d, T, 2)) ||
-        (k_out && !in_place(k_out, k_at, ld_k) &&
-         rows_overlap(qkv, ld_qkv, cols, k_out, ld_k, n_kv_heads * d, T, 2)) ||
-        (q_out && k_out && rows_overlap(q_out, ld_q, n_heads * d, k_out, ld_k, n_kv_heads * d, T, 2)))
-        return fail(nullptr, H3ENC_ERR_INVALID_ARG, "%s: outputs overlap qkv (other than in place) or each other", who);
     h3::QkNormRope p{};
     if (cache) {
         const h3enc_status s = take_cache(cache, who, &p.cache);
@@ -1624,6 +1635,114 @@ h3enc_status h3enc_op_cache_evict(const h3enc_kv_cache *cache, const int32_t *pa
     p.kept = kept; p.ld_kept = ld_kept; p.new_lens = new_lens; p.status = status;
     cudaError_t e = h3::launch_cache_evict(p, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? H3ENC_OK : cuda_fail(nullptr, e, "cache_evict launch");
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------- a decoder that reads an encoder's states
+
+namespace {
+
+// The scaled frequencies of `r` as 64-bit fractions of a turn per position; false if it is not valid for heads of head_dim.
+bool take_rope(const h3enc_rope &r, int32_t head_dim, h3::RopeAppend *p) {
+    const auto positive = [](double x) { return x > 0 && std::isfinite(x); };
+    const bool ramped = r.scaling == H3ENC_ROPE_WAVELENGTH || r.scaling == H3ENC_ROPE_YARN;
+    if (r.rotary_dim < 16 || r.rotary_dim % 16 || r.rotary_dim > head_dim || r.scaling < H3ENC_ROPE_PLAIN ||
+        r.scaling > H3ENC_ROPE_YARN || !positive(r.theta) || (r.scaling && !positive(r.factor)) ||
+        !(r.magnitude == 0 || positive(r.magnitude)))
+        return false;
+    double low = r.low_turns, high = r.high_turns;
+    if (low == 0 && high == 0) low = 1, high = r.scaling == H3ENC_ROPE_YARN ? 32 : 4;
+    if (ramped && (r.original_len < 1 || !positive(low) || !positive(high) || !(low < high) ||
+                   (r.scaling == H3ENC_ROPE_YARN && !(r.theta > 1))))
+        return false;
+    const int half = r.rotary_dim / 2;
+    const bool axes = r.section[0] || r.section[1] || r.section[2];
+    for (int i = 0; axes && i < 3; ++i)
+        if (r.section[i] < 0 || r.section[i] > half) return false;
+    if (axes && r.section[0] + r.section[1] + r.section[2] != half) return false;
+    const double two_pi = 6.283185307179586476925;
+    const auto dim = [&](double n) { return r.rotary_dim * std::log(r.original_len / (two_pi * n)) / (2 * std::log(r.theta)); };
+    double begin = 0, end = 0;
+    if (r.scaling == H3ENC_ROPE_YARN) {
+        begin = std::max(std::floor(dim(high)), 0.0);
+        end = std::min(std::ceil(dim(low)), r.rotary_dim - 1.0);
+    }
+    const auto clamp01 = [](double x) { return x < 0 ? 0 : x > 1 ? 1 : x; };
+    for (int j = 0; j < half; ++j) {
+        double w = std::pow(r.theta, -2.0 * j / r.rotary_dim);
+        if (r.scaling == H3ENC_ROPE_LINEAR) {
+            w /= r.factor;
+        } else if (r.scaling == H3ENC_ROPE_WAVELENGTH) {
+            const double s = clamp01((r.original_len * w / two_pi - low) / (high - low));
+            w *= s + (1 - s) / r.factor;
+        } else if (r.scaling == H3ENC_ROPE_YARN) {
+            const double s = clamp01((j - begin) / std::max(end - begin, 0.001));
+            w = w * (1 - s) + w / r.factor * s;
+        }
+        const double turns = w / two_pi;
+        if (!std::isfinite(turns)) return false;
+        p->turns[j] = (unsigned long long)std::ldexp(turns - std::floor(turns), 64);
+        if (axes && j % 3 == 1 && j < 3 * r.section[1]) p->axis1 |= 1ull << j;
+        if (axes && j % 3 == 2 && j < 3 * r.section[2]) p->axis2 |= 1ull << j;
+    }
+    p->rot = r.rotary_dim;
+    p->interleaved = r.interleaved != 0;
+    p->axes = axes ? 3 : 1;
+    p->magnitude = (float)(r.magnitude > 0 ? r.magnitude
+                           : r.scaling == H3ENC_ROPE_YARN && r.factor > 1 ? 0.1 * std::log(r.factor) + 1 : 1.0);
+    return true;
+}
+
+}  // namespace
+
+extern "C" {
+
+h3enc_status h3enc_op_rope_append(const void *qkv, int64_t ld_qkv, int32_t T, int32_t n_heads, int32_t n_kv_heads,
+                                  int32_t head_dim, const void *w_q, const void *w_k, float eps, const h3enc_rope *rope,
+                                  const int32_t *positions, int64_t ld_positions, void *q_out, int64_t ld_q, void *k_out,
+                                  int64_t ld_k, const h3enc_kv_cache *cache, const int32_t *page_table, int32_t ld_table,
+                                  const int32_t *seq_lens, const int32_t *cu_rows, int32_t n_seqs, int32_t max_len,
+                                  int32_t *status, void *stream) {
+    const char *who = "rope_append";
+    h3enc_status s = check_qkv_rows(who, qkv, ld_qkv, T, n_heads, n_kv_heads, head_dim, w_q, w_k, eps, q_out, ld_q, k_out,
+                                    ld_k, cache != nullptr);
+    if (s != H3ENC_OK) return s;
+    h3::RopeAppend p{};
+    p.axes = 1;
+    if (rope && !take_rope(*rope, head_dim, &p))
+        return fail(nullptr, H3ENC_ERR_INVALID_ARG, "%s: bad rotary parameters", who);
+    if (n_seqs < 0 || n_seqs > h3::kMaxSeqs || max_len < 0 || max_len > h3::kMaxCacheLen)
+        return fail(nullptr, H3ENC_ERR_INVALID_ARG, "%s: bad sizes", who);
+    if (cache) {
+        s = take_cache(cache, who, &p.cache);
+        if (s != H3ENC_OK) return s;
+        if (cache->n_kv_heads != n_kv_heads || cache->head_dim != head_dim)
+            return fail(nullptr, H3ENC_ERR_INVALID_ARG, "%s: the cache has other heads", who);
+        if (ld_table < 0 || (int64_t)ld_table * cache->page_size < max_len || (!page_table && max_len > 0 && n_seqs > 0))
+            return fail(nullptr, H3ENC_ERR_INVALID_ARG, "%s: page_table NULL or does not hold max_len", who);
+        p.has_cache = true;
+    } else if (page_table) {
+        return fail(nullptr, H3ENC_ERR_INVALID_ARG, "%s: page_table without a cache", who);
+    }
+    if (seq_lens ? n_seqs == 0 && T > 0 : n_seqs > 0 || cu_rows || cache)
+        return fail(nullptr, H3ENC_ERR_INVALID_ARG, "%s: seq_lens without sequences, or sequences, cu_rows or a cache "
+                                                    "without seq_lens", who);
+    if (positions ? ld_positions < T : rope && !seq_lens)
+        return fail(nullptr, H3ENC_ERR_INVALID_ARG, "%s: positions NULL without seq_lens, or their leading dimension below T",
+                    who);
+    if (T == 0) return H3ENC_OK;
+    p.qkv = static_cast<const bf16 *>(qkv); p.ld_qkv = ld_qkv;
+    p.T = T; p.nq = n_heads; p.nkv = n_kv_heads; p.d = head_dim;
+    p.wq = static_cast<const bf16 *>(w_q); p.wk = static_cast<const bf16 *>(w_k); p.eps = eps;
+    p.positions = positions; p.ld_pos = ld_positions;
+    p.q_out = static_cast<bf16 *>(q_out); p.ld_q = ld_q;
+    p.k_out = static_cast<bf16 *>(k_out); p.ld_k = ld_k;
+    p.table = page_table; p.ld_table = ld_table;
+    p.seq_lens = seq_lens; p.cu_rows = cu_rows; p.n_seqs = n_seqs; p.max_len = max_len;
+    p.status = status;
+    cudaError_t e = h3::launch_rope_append(p, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? H3ENC_OK : cuda_fail(nullptr, e, "rope_append launch");
 }
 
 }  // extern "C"

@@ -190,6 +190,33 @@ struct QkNormRope {
 };
 cudaError_t launch_qk_norm_rope(const QkNormRope &p, cudaStream_t st);
 
+// New rows normed, rotated and appended to their sequences (rope_append.cu).  Row t of sequence b (rows
+// [cu_rows[b], cu_rows[b + 1]), or row b alone with cu_rows NULL) is the token in place seq_lens[b] - (rows of b from t on).
+struct RopeAppend {
+    const bf16 *qkv;
+    long long ld_qkv;
+    int T, nq, nkv, d;
+    const bf16 *wq, *wk;        // NULL: no norm
+    float eps;
+    int rot, interleaved;       // rot 0: no rotation
+    float magnitude;            // factor on cos and sin
+    unsigned long long turns[kMaxHalfDim];    // 2^64 times the turns of frequency j per position, modulo 2^64
+    unsigned long long axis1, axis2;          // frequencies that go by the second / third axis of the positions
+    const int32_t *positions;   // [axes, ld_pos], NULL: the places
+    long long ld_pos;
+    int axes;
+    bf16 *q_out, *k_out;        // NULL: not written
+    long long ld_q, ld_k;
+    bool has_cache;
+    KvCache cache;
+    const int32_t *table;
+    int ld_table;
+    const int32_t *seq_lens, *cu_rows;   // seq_lens NULL: every row counts, by positions alone
+    int n_seqs, max_len;
+    int32_t *status;
+};
+cudaError_t launch_rope_append(const RopeAppend &p, cudaStream_t st);
+
 struct CacheEvict {
     KvCache cache;
     const int32_t *table, *table_out;   // table_out NULL: in place

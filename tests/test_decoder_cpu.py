@@ -1,0 +1,204 @@
+"""A decoder that reads an encoder's states, without a GPU: the oracle against hand-made cases, and every
+refusal of the entry points before they touch CUDA."""
+import math
+
+import numpy as np
+import pytest
+
+import oracle as O
+
+
+@pytest.fixture(scope="module")
+def Q():
+    import __graft_entry__
+    __graft_entry__._build_module().build()
+    import qwen3_vl_text_gb300
+    return qwen3_vl_text_gb300
+
+
+# ---------------------------------------------------------------- oracle pins
+
+def test_frequencies_by_hand():
+    w, m = O.decoder.frequencies(8, 16.0)
+    assert np.allclose(w, [1, 0.5, 0.25, 0.125]) and m == 1
+    assert np.allclose(O.decoder.frequencies(8, 16.0, "linear", 4.0)[0], w / 4)
+    # 64 tokens: 10.2, 5.1, 2.5 and 1.3 turns; kept from 5, stretched whole below 2
+    s = (32 * 0.25 / math.pi - 2) / 3
+    got, m = O.decoder.frequencies(8, 16.0, "wavelength", 8.0, 64, 2.0, 5.0)
+    assert np.allclose(got, [1, 0.5, 0.25 * (s + (1 - s) / 8), 0.125 / 8]) and m == 1
+    # pair j turns 10.2 / 2^j times: 8 and 2 turns lie at j = 0.35 and 2.35, so the ramp runs from 0 to 3
+    got, m = O.decoder.frequencies(8, 16.0, "yarn", 8.0, 64, 2.0, 8.0)
+    assert np.allclose(got, [1, 0.5 * (2 / 3 + 1 / 24), 0.25 * (1 / 3 + 1 / 12), 0.125 / 8])
+    assert m == pytest.approx(0.1 * math.log(8) + 1)
+    assert O.decoder.frequencies(8, 16.0, "yarn", 8.0, 64, magnitude=1.0)[1] == 1
+
+
+def test_axes_are_those_of_the_prefill_tables():
+    section = (24, 20, 20)
+    axes = [O.decoder.axis_of(j, section) for j in range(64)]
+    assert axes == [0, 1, 2] * 20 + [0] * 4
+
+
+def test_rotate_by_hand():
+    x = np.arange(1.0, 9.0).reshape(1, 1, 8)
+    quarter = np.full((1, 2), math.pi / 2)
+    assert np.allclose(O.decoder.rotate(x, quarter, 1.0, False), [[[-3, -4, 1, 2, 5, 6, 7, 8]]])
+    assert np.allclose(O.decoder.rotate(x, quarter, 2.0, True), [[[-4, 2, -8, 6, 5, 6, 7, 8]]])
+
+
+def test_append_places_by_hand():
+    assert O.decoder.append_places(6, [4, 9, 7], [0, 2, 2, 5]) == [(0, 2), (0, 3), (2, 4), (2, 5), (2, 6), None]
+    assert O.decoder.append_places(3, [4, 1], None) == [(0, 3), (1, 0), None]
+
+
+# ---------------------------------------------------------------- refusals
+
+def _cache(Q, **kw):
+    c = Q.KVCache.__new__(Q.KVCache)
+    base = dict(k=4096, v=8192, k_scale=None, v_scale=None, page_stride=2 * 16 * 64, num_pages=4, page_size=16,
+                n_kv_heads=2, head_dim=64, dtype=0)
+    base.update(kw)
+    for name, value in base.items():
+        setattr(c, name, value)
+    return c
+
+
+BAD_CACHES = [(dict(k=None), 2), (dict(v=8), 2), (dict(dtype=1), 6), (dict(head_dim=96), 6), (dict(page_size=8), 6),
+              (dict(page_size=48), 6), (dict(page_stride=2 * 16 * 64 - 8), 2), (dict(page_stride=2 * 16 * 64 + 4), 2),
+              (dict(num_pages=0), 2), (dict(n_kv_heads=0), 2), (dict(dtype=2), 2), (dict(k_scale=64), 2)]
+
+
+def _append(Q, cache=None, rope=None, **kw):
+    a = dict(qkv=1 << 20, ld_qkv=512, T=3, nq=4, nkv=2, d=64, wq=16, wk=16, eps=1e-6, pos=None, ld_pos=3, q=1 << 24,
+             ld_q=256, k=None, ld_k=128, table=16, ld_table=4, lens=16, cu=16, n=2, max_len=64)
+    if cache is None:
+        a.update(table=None, ld_table=0)
+    a.update(kw)
+    Q._check(Q.lib.h3enc_op_rope_append(
+        a["qkv"], a["ld_qkv"], a["T"], a["nq"], a["nkv"], a["d"], a["wq"], a["wk"], a["eps"], rope, a["pos"], a["ld_pos"],
+        a["q"], a["ld_q"], a["k"], a["ld_k"], cache, a["table"], a["ld_table"], a["lens"], a["cu"], a["n"], a["max_len"],
+        None, None))
+
+
+def _refused(Q, code, call, *args, **kw):
+    with pytest.raises(Q.H3encError) as e:
+        call(Q, *args, **kw)
+    assert e.value.code == code, str(e.value)
+    assert Q.h3enc_last_error(None)
+
+
+@pytest.mark.parametrize("kw,code", BAD_CACHES)
+def test_bad_caches_are_refused(Q, kw, code):
+    _refused(Q, code, _append, _cache(Q, **kw))
+
+
+@pytest.mark.parametrize("kw", [
+    dict(T=-1), dict(nq=0), dict(nkv=0), dict(d=96), dict(qkv=None), dict(qkv=(1 << 20) + 8), dict(ld_qkv=511),
+    dict(ld_qkv=508), dict(ld_qkv=516), dict(eps=-1.0), dict(wq=8), dict(q=None), dict(q=(1 << 24) + 2), dict(ld_q=252),
+    dict(k=1 << 25, ld_k=64), dict(q=(1 << 20) + 16), dict(q=1 << 20, ld_q=520), dict(k=1 << 24, ld_k=128),
+    dict(n=-1), dict(n=1025), dict(max_len=-1), dict(max_len=2 ** 30 + 1), dict(table=16), dict(lens=None),
+    dict(lens=None, cu=None), dict(lens=None, n=0), dict(n=0), dict(pos=16, ld_pos=2)])
+def test_rope_append_refuses(Q, kw):
+    _refused(Q, 2, _append, **kw)
+
+
+@pytest.mark.parametrize("kw", [dict(table=None), dict(ld_table=3), dict(ld_table=-1), dict(max_len=65), dict(nkv=1, ld_qkv=384),
+                                dict(d=128, ld_qkv=1024, ld_q=512), dict(lens=None), dict(lens=None, n=0, cu=None)])
+def test_rope_append_to_a_cache_refuses(Q, kw):
+    _refused(Q, 2, _append, _cache(Q), **kw)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(rotary_dim=0), dict(rotary_dim=8), dict(rotary_dim=40), dict(rotary_dim=80), dict(rotary_dim=-16), dict(theta=0.0),
+    dict(theta=-2.0), dict(theta=math.inf), dict(theta=math.nan), dict(factor=0.0, scaling="linear"),
+    dict(factor=math.nan, scaling="linear"), dict(magnitude=-1.0), dict(magnitude=math.nan), dict(magnitude=math.inf),
+    dict(scaling="yarn", factor=4.0), dict(scaling="wavelength", factor=4.0, original_len=0),
+    dict(scaling="yarn", factor=4.0, original_len=64, theta=1.0), dict(scaling="yarn", factor=4.0, original_len=64, theta=0.5),
+    dict(scaling="wavelength", factor=4.0, original_len=64, low_turns=4.0, high_turns=4.0),
+    dict(scaling="yarn", factor=4.0, original_len=64, low_turns=1.0), dict(section=(8, 8, 8)), dict(section=(40, -4, -4)),
+    dict(section=(0, 0, 31)), dict(theta=1e-320)])
+def test_rope_append_refuses_rotary_parameters(Q, kw):
+    _refused(Q, 2, _append, rope=Q.Rope(**{**dict(rotary_dim=64, theta=1e4), **kw}))
+
+
+def test_rope_append_refuses_an_unknown_scaling(Q):
+    for scaling in (-1, 4):
+        r = Q.Rope(64, 1e4)
+        r.scaling = scaling
+        _refused(Q, 2, _append, rope=r)
+    with pytest.raises(ValueError):
+        Q.Rope(64, 1e4, scaling="ntk")
+    with pytest.raises(ValueError):
+        Q.Rope(64, 1e4, section=(16, 16))
+    with pytest.raises(ValueError):
+        Q.Rope(2 ** 32 + 64, 1e4)
+
+
+def test_rope_append_needs_positions_without_lengths(Q):
+    _refused(Q, 2, _append, rope=Q.Rope(64, 1e4), lens=None, cu=None, n=0)
+
+
+def test_rope_append_of_no_rows_does_nothing(Q):
+    _append(Q, T=0)
+    _append(Q, _cache(Q), Q.Rope(32, 1e4), T=0, n=0)
+    _append(Q, T=0, q=1 << 20, ld_q=512, k=(1 << 20) + 512, ld_k=512)     # in place
+
+
+# ---------------------------------------------------------------- what the Python calls check of their tensors
+
+class _Record:
+    """Stands in for the library: keeps a call's arguments and succeeds."""
+    def __getattr__(self, name):
+        def call(*args):
+            self.args = args
+            return 0
+        return call
+
+
+@pytest.fixture
+def recorded(Q, monkeypatch):
+    rec = _Record()
+    monkeypatch.setattr(Q, "lib", rec)
+    monkeypatch.setattr(Q, "_raw", (lambda: -1, lambda d: 77))     # the "device" of CPU tensors
+    return rec
+
+
+def _refuses(Q, call, args, name, tensor):
+    with pytest.raises(Q.H3encError) as e:
+        call(**{**args, name: tensor})
+    assert e.value.code == 2 and name in str(e.value), str(e.value)
+
+
+def _wrong(torch, t, rows):
+    """Tensors that may not stand where t does: another type, fewer rows, rows that are too narrow, gaps."""
+    out = [t.double() if t.dtype == torch.float32 else t.float(), t[:0] if rows else t[..., :0]]
+    if t.dim() == 2:
+        out += [t[:, :-1], torch.cat([t, t], 1)[:, ::2]]
+    return out
+
+
+def test_rope_append_checks_its_tensors(Q, recorded):
+    torch = pytest.importorskip("torch")
+    bf, i32 = dict(dtype=torch.bfloat16), dict(dtype=torch.int32)
+    k = torch.zeros(5, 2, 16, 64, **bf)
+    a = dict(qkv=torch.zeros(6, 512, **bf), T=6, n_heads=4, n_kv_heads=2, head_dim=64, w_q=torch.ones(64, **bf),
+             w_k=torch.ones(64, **bf), eps=1e-6, rope=Q.Rope(64, 1e4, section=(12, 10, 10)), positions=torch.zeros(3, 6, **i32),
+             q_out=torch.zeros(6, 256, **bf), k_out=torch.zeros(6, 128, **bf), cache=Q.KVCache(k, k),
+             page_table=torch.zeros(3, 4, **i32), seq_lens=torch.zeros(3, **i32), max_len=64, cu_rows=torch.zeros(4, **i32),
+             status=torch.zeros(1, **i32))
+    Q.h3enc_op_rope_append(**a)
+    got = recorded.args
+    assert got[:6] == (a["qkv"].data_ptr(), 512, 6, 4, 2, 64) and got[9].axes == 3 and got[11] == 6 and got[-1] == 77
+    assert got[17:23] == (a["page_table"].data_ptr(), 4, a["seq_lens"].data_ptr(), a["cu_rows"].data_ptr(), 3, 64)
+    for name in ("qkv", "w_q", "w_k", "positions", "q_out", "k_out", "page_table", "cu_rows", "status"):
+        for bad in _wrong(torch, a[name], True):
+            _refuses(Q, Q.h3enc_op_rope_append, a, name, bad)
+    _refuses(Q, Q.h3enc_op_rope_append, a, "seq_lens", torch.zeros(3))
+    _refuses(Q, Q.h3enc_op_rope_append, a, "positions", torch.zeros(6, **i32))     # three axes wanted
+    _refuses(Q, Q.h3enc_op_rope_append, a, "page_table", torch.zeros(2, 4, **i32))
+    a["rope"] = Q.Rope(64, 1e4)
+    a["positions"] = torch.zeros(6, **i32)
+    Q.h3enc_op_rope_append(**a)
+    a.update(rope=None, positions=None, cache=None, page_table=None, seq_lens=None, cu_rows=None, max_len=0, status=None)
+    Q.h3enc_op_rope_append(**a)
+    assert recorded.args[9:12] == (None, None, 0) and recorded.args[16:23] == (None, None, 0, None, None, 0, 0)
