@@ -31,7 +31,9 @@ __all__ = [
     "h3vis_last_error", "h3vis_launch_count", "h3vis_destroy", "VisionEncoder", "h3enc_op_attention", "h3enc_op_embed", "h3enc_op_vis_rank", "Encoder",
     "KERNEL_CLASSES", "KVCache", "h3enc_op_qk_norm_rope", "h3enc_op_attention_decode",
     "h3enc_op_attention_decode_workspace_bytes", "h3enc_op_cache_evict",
-    "Rope", "h3enc_op_rope_append",
+    "Rope", "h3enc_op_rope_append", "h3enc_op_attention_decode_shared",
+    "h3enc_op_attention_decode_shared_workspace_bytes", "h3enc_op_attention_cross",
+    "h3enc_op_attention_cross_workspace_bytes",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -193,6 +195,12 @@ _SIGS = {
                                ctypes.POINTER(KVCache), _P, _P, _P], _I32),
     "h3enc_op_rope_append": ([_P, _I64, _I32, _I32, _I32, _I32, _P, _P, _F, ctypes.POINTER(Rope), _P, _I64, _P, _I64, _P,
                               _I64, ctypes.POINTER(KVCache), _P, _I32, _P, _P, _I32, _I32, _P, _P], _I32),
+    "h3enc_op_attention_decode_shared": ([_P, _I64, _P, _I64, ctypes.POINTER(KVCache), _P, _I32, _P, _P, _I32, _I32, _P, _I32,
+                                          _P, _I32, _I32, _I32, _P, _P, _I64, _P, _I64, _P, _P], _I32),
+    "h3enc_op_attention_decode_shared_workspace_bytes": ([_I32, _I32, _I32, _I32], _I64),
+    "h3enc_op_attention_cross": ([_P, _I64, _P, _I64, _P, _I64, _P, _I64, _I32, _I32, _I32, _I32, _I32, _P, _P, _I32, _P, _I64,
+                                  _P, _P], _I32),
+    "h3enc_op_attention_cross_workspace_bytes": ([_I32], _I64),
     "h3enc_op_attention_decode": ([_P, _I64, _P, _I64, ctypes.POINTER(KVCache), _P, _I32, _P, _I32, _I32, _I32, _P, _P,
                                    _I64, _P, _I64, _P, _P], _I32),
     "h3enc_op_attention_decode_workspace_bytes": ([_I32, _I32, _I32, _I32], _I64),
@@ -766,6 +774,81 @@ def h3enc_op_attention_decode(q, o, cache, page_table, seq_lens, n_heads, max_le
     return _check(lib.h3enc_op_attention_decode(
         q, ld_q, o, ld_o, cache, page_table, ld_t, _vec(who, "seq_lens", seq_lens, _I32T, dev, n), n, n_heads, max_len,
         weight_in, weight_out, ld_w,
+        None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.nbytes,
+        None if status is None else _vec(who, "status", status, _I32T, dev, 1), raw(dev) if stream is None else _stream(stream)))
+
+
+def h3enc_op_attention_decode_shared_workspace_bytes(n_seqs, n_heads, max_len, with_weights=False) -> int:
+    return lib.h3enc_op_attention_decode_shared_workspace_bytes(n_seqs, n_heads, max_len, 1 if with_weights else 0)
+
+
+def h3enc_op_attention_decode_shared(q, o, cache, prefix_table, prefix_lens, max_prefix, page_table, seq_lens, n_heads,
+                                     max_len, workspace, prefix_rows=None, weight_in=None, weight_out=None, status=None,
+                                     stream=None):
+    """Attention of one new token per sequence over a shared prefix and its own tokens in a KVCache: as
+    h3enc_op_attention_decode, with int32 prefix_table [n_prefixes, pages], prefix_lens [n_prefixes] and prefix_rows
+    [n_prefixes + 1] (None: one prefix for all)."""
+    if _BF16 is None:
+        _types()
+    who, n, groups, (device, raw) = "attention_decode_shared", seq_lens.numel(), prefix_lens.numel(), _raw or _raw_calls()
+    dev = device()
+    if cache.device_index != dev:
+        _refuse_cache(who, cache, dev)
+    width, page = n_heads * cache.head_dim, cache.page_size
+    q, ld_q = _mat(who, "q", q, _BF16, dev, n, width)
+    o, ld_o = _mat(who, "o", o, _BF16, dev, n, width)
+    prefix_table, ld_p = _mat(who, "prefix_table", prefix_table, _I32T, dev, groups, -(-max_prefix // page))
+    page_table, ld_t = _mat(who, "page_table", page_table, _I32T, dev, n, -(-max_len // page))
+    if ld_t > 0x7fffffff or ld_p > 0x7fffffff:      # (C arguments of 32 bits: they would be cut off)
+        raise H3encError(2, f"{who}: the rows of a page table lie too far apart")
+    ld_w = 0
+    if weight_out is not None:
+        same = weight_in is weight_out
+        weight_out, ld_w = _mat(who, "weight_out", weight_out, _F32T, dev, n, max_len)
+        if same:
+            weight_in = weight_out
+        elif weight_in is not None:
+            weight_in, ld = _mat(who, "weight_in", weight_in, _F32T, dev, n, max_len)
+            if ld != ld_w:
+                raise H3encError(2, f"{who}: weight_in and weight_out have different row strides")
+    elif weight_in is not None:
+        weight_in, ld_w = _mat(who, "weight_in", weight_in, _F32T, dev, n, max_len)
+    if workspace is not None and (not workspace.is_contiguous() or workspace.get_device() != dev):
+        raise H3encError(2, f"{who}: workspace not contiguous, or on {workspace.device} with cuda:{dev} the current device")
+    return _check(lib.h3enc_op_attention_decode_shared(
+        q, ld_q, o, ld_o, cache, prefix_table, ld_p, _vec(who, "prefix_lens", prefix_lens, _I32T, dev, groups),
+        None if prefix_rows is None else _vec(who, "prefix_rows", prefix_rows, _I32T, dev, groups + 1), groups, max_prefix,
+        page_table, ld_t, _vec(who, "seq_lens", seq_lens, _I32T, dev, n), n, n_heads, max_len, weight_in, weight_out, ld_w,
+        None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.nbytes,
+        None if status is None else _vec(who, "status", status, _I32T, dev, 1), raw(dev) if stream is None else _stream(stream)))
+
+
+def h3enc_op_attention_cross_workspace_bytes(head_dim) -> int:
+    return lib.h3enc_op_attention_cross_workspace_bytes(head_dim)
+
+
+def h3enc_op_attention_cross(q, k, v, o, n_heads, n_kv_heads, head_dim, workspace, cu_q=None, cu_k=None, status=None,
+                             stream=None):
+    """Cross attention of packed bfloat16 rows q, o [Tq, n_heads * head_dim] over k, v [Tk, n_kv_heads * head_dim] (rows may lie
+    apart); int32 cu_q, cu_k [n_seqs + 1] (None: one sequence of all rows)."""
+    if _BF16 is None:
+        _types()
+    who, (device, raw) = "attention_cross", _raw or _raw_calls()
+    dev, Tq, Tk, n = device(), q.shape[0], k.shape[0], 1
+    q, ld_q = _mat(who, "q", q, _BF16, dev, Tq, n_heads * head_dim)
+    o, ld_o = _mat(who, "o", o, _BF16, dev, Tq, n_heads * head_dim)
+    k, ld_k = _mat(who, "k", k, _BF16, dev, Tk, n_kv_heads * head_dim)
+    v, ld_v = _mat(who, "v", v, _BF16, dev, Tk, n_kv_heads * head_dim)
+    if cu_q is not None or cu_k is not None:
+        n = (cu_k if cu_q is None else cu_q).numel() - 1
+        if n < 0:
+            raise H3encError(2, f"{who}: cu_q and cu_k hold one offset more than there are sequences")
+    if workspace is not None and (not workspace.is_contiguous() or workspace.get_device() != dev):
+        raise H3encError(2, f"{who}: workspace not contiguous, or on {workspace.device} with cuda:{dev} the current device")
+    return _check(lib.h3enc_op_attention_cross(
+        q, ld_q, k, ld_k, v, ld_v, o, ld_o, Tq, Tk, n_heads, n_kv_heads, head_dim,
+        None if cu_q is None else _vec(who, "cu_q", cu_q, _I32T, dev, n + 1),
+        None if cu_k is None else _vec(who, "cu_k", cu_k, _I32T, dev, n + 1), n,
         None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.nbytes,
         None if status is None else _vec(who, "status", status, _I32T, dev, 1), raw(dev) if stream is None else _stream(stream)))
 

@@ -1446,20 +1446,24 @@ namespace {
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
-// Whether row-major matrices a [rows, ca] and b [rows, cb] (lda, ldb elements of es bytes from
+// Whether row-major matrices a [na, ca] and b [nb, cb] (lda, ldb elements of es bytes from
 // row to row) may share an element.  With one leading dimension their columns are told apart
 // (slices of one packed buffer); otherwise their address ranges are.
-bool rows_overlap(const void *a, int64_t lda, int64_t ca, const void *b, int64_t ldb, int64_t cb, int64_t rows,
+bool rows_overlap(const void *a, int64_t lda, int64_t ca, int64_t na, const void *b, int64_t ldb, int64_t cb, int64_t nb,
                   int64_t es) {
     using Wide = __int128;   // a leading dimension may be any 64-bit number
     const Wide pa = reinterpret_cast<uintptr_t>(a), pb = reinterpret_cast<uintptr_t>(b);
-    const Wide ea = pa + ((Wide)(rows - 1) * lda + ca) * es, eb = pb + ((Wide)(rows - 1) * ldb + cb) * es;
-    if (rows <= 0 || ea <= pb || eb <= pa) return false;
+    const Wide ea = pa + ((Wide)(na - 1) * lda + ca) * es, eb = pb + ((Wide)(nb - 1) * ldb + cb) * es;
+    if (na <= 0 || nb <= 0 || ea <= pb || eb <= pa) return false;
     if (lda != ldb) return true;
     const Wide row = (Wide)lda * es;
     Wide delta = (pb - pa) % row;   // where b's first column lies in a row of a
     if (delta < 0) delta += row;
     return delta < (Wide)ca * es || delta + (Wide)cb * es > row;
+}
+bool rows_overlap(const void *a, int64_t lda, int64_t ca, const void *b, int64_t ldb, int64_t cb, int64_t rows,
+                  int64_t es) {
+    return rows_overlap(a, lda, ca, rows, b, ldb, cb, rows, es);
 }
 
 // The rows that h3enc_op_qk_norm_rope and h3enc_op_rope_append read and write.
@@ -1516,6 +1520,44 @@ h3enc_status take_cache(const h3enc_kv_cache *c, const char *who, h3::KvCache *o
     return H3ENC_OK;
 }
 
+// The arguments that h3enc_op_attention_decode and h3enc_op_attention_decode_shared have in common, all but the
+// workspace's size: `need` is what the decoding kernel takes of it.
+h3enc_status take_decode(const char *who, const void *q, int64_t ld_q, void *o, int64_t ld_o, const h3enc_kv_cache *cache,
+                         const int32_t *page_table, int32_t ld_table, const int32_t *seq_lens, int32_t n_seqs,
+                         int32_t n_heads, int32_t max_len, const float *weight_in, float *weight_out, int64_t ld_weight,
+                         void *workspace, int32_t *status, h3::AttentionDecode *out, size_t *need) {
+    h3::AttentionDecode p{};
+    const h3enc_status s = take_cache(cache, who, &p.cache);
+    if (s != H3ENC_OK) return s;
+    const int64_t width = (int64_t)n_heads * cache->head_dim;
+    if (n_seqs < 0 || n_seqs > h3::kMaxSeqs || n_heads < 1 || n_heads > 65536 || n_heads % cache->n_kv_heads ||
+        max_len < 0 || max_len > h3::kMaxCacheLen || ld_table < 0 || (int64_t)ld_table * cache->page_size < max_len)
+        return fail(nullptr, H3ENC_ERR_INVALID_ARG, "%s: bad sizes, or the page table does not hold max_len", who);
+    if (n_seqs == 0) return H3ENC_OK;
+    if (!q || !o || !aligned16(q) || !aligned16(o) || ld_q < width || ld_o < width || ld_q % 8 || ld_o % 8 ||
+        (!page_table && max_len > 0) || !seq_lens)
+        return fail(nullptr, H3ENC_ERR_INVALID_ARG, "%s: NULL or misaligned operand, or a bad leading dimension", who);
+    if (rows_overlap(q, ld_q, width, o, ld_o, width, n_seqs, 2))
+        return fail(nullptr, H3ENC_ERR_INVALID_ARG, "%s: o overlaps q", who);
+    if ((weight_in && !weight_out) || (weight_out && ld_weight < max_len) ||
+        (weight_in && weight_in != weight_out &&
+         rows_overlap(weight_in, ld_weight, max_len, weight_out, ld_weight, max_len, n_seqs, 4)))
+        return fail(nullptr, H3ENC_ERR_INVALID_ARG, "%s: weight_in without weight_out or overlapping it, or ld_weight "
+                                                    "below max_len", who);
+    const int sms = h3::device_num_sms();
+    if (sms <= 0) return fail(nullptr, H3ENC_ERR_CUDA, "%s: no CUDA device", who);
+    *need = h3::attention_decode_workspace_bytes(sms, n_seqs, n_heads, max_len, weight_out != nullptr);
+    if (!*need) return fail(nullptr, H3ENC_ERR_UNSUPPORTED, "%s: sizes beyond 2^31 key tiles", who);
+    p.q = static_cast<const bf16 *>(q); p.ld_q = ld_q;
+    p.o = static_cast<bf16 *>(o); p.ld_o = ld_o;
+    p.table = page_table; p.ld_table = ld_table;
+    p.seq_lens = seq_lens; p.n_seqs = n_seqs; p.nq = n_heads; p.max_len = max_len;
+    p.weight_in = weight_in; p.weight_out = weight_out; p.ld_weight = ld_weight;
+    p.workspace = workspace; p.status = status;
+    *out = p;
+    return H3ENC_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -1569,38 +1611,15 @@ h3enc_status h3enc_op_attention_decode(const void *q, int64_t ld_q, void *o, int
                                        int64_t workspace_bytes, int32_t *status, void *stream) {
     const char *who = "attention_decode";
     h3::AttentionDecode p{};
-    const h3enc_status s = take_cache(cache, who, &p.cache);
-    if (s != H3ENC_OK) return s;
-    const int64_t width = (int64_t)n_heads * cache->head_dim;
-    if (n_seqs < 0 || n_seqs > h3::kMaxSeqs || n_heads < 1 || n_heads > 65536 || n_heads % cache->n_kv_heads ||
-        max_len < 0 || max_len > h3::kMaxCacheLen || ld_table < 0 || (int64_t)ld_table * cache->page_size < max_len)
-        return fail(nullptr, H3ENC_ERR_INVALID_ARG, "%s: bad sizes, or the page table does not hold max_len", who);
-    if (n_seqs == 0) return H3ENC_OK;
-    if (!q || !o || !aligned16(q) || !aligned16(o) || ld_q < width || ld_o < width || ld_q % 8 || ld_o % 8 ||
-        (!page_table && max_len > 0) || !seq_lens)
-        return fail(nullptr, H3ENC_ERR_INVALID_ARG, "%s: NULL or misaligned operand, or a bad leading dimension", who);
-    if (rows_overlap(q, ld_q, width, o, ld_o, width, n_seqs, 2))
-        return fail(nullptr, H3ENC_ERR_INVALID_ARG, "%s: o overlaps q", who);
-    if ((weight_in && !weight_out) || (weight_out && ld_weight < max_len) ||
-        (weight_in && weight_in != weight_out &&
-         rows_overlap(weight_in, ld_weight, max_len, weight_out, ld_weight, max_len, n_seqs, 4)))
-        return fail(nullptr, H3ENC_ERR_INVALID_ARG, "%s: weight_in without weight_out or overlapping it, or ld_weight "
-                                                    "below max_len", who);
-    const int sms = h3::device_num_sms();
-    if (sms <= 0) return fail(nullptr, H3ENC_ERR_CUDA, "%s: no CUDA device", who);
-    const size_t need = h3::attention_decode_workspace_bytes(sms, n_seqs, n_heads, max_len, weight_out != nullptr);
-    if (!need) return fail(nullptr, H3ENC_ERR_UNSUPPORTED, "%s: sizes beyond 2^31 key tiles", who);
+    size_t need = 0;
+    const h3enc_status s = take_decode(who, q, ld_q, o, ld_o, cache, page_table, ld_table, seq_lens, n_seqs, n_heads, max_len,
+                                       weight_in, weight_out, ld_weight, workspace, status, &p, &need);
+    if (s != H3ENC_OK || n_seqs == 0) return s;
     if (!workspace || workspace_bytes < 0 || (size_t)workspace_bytes < need ||
         (reinterpret_cast<uintptr_t>(workspace) & 255))
         return fail(nullptr, H3ENC_ERR_INVALID_ARG, "%s: workspace smaller than "
                                                     "h3enc_op_attention_decode_workspace_bytes() or not 256-byte "
                                                     "aligned", who);
-    p.q = static_cast<const bf16 *>(q); p.ld_q = ld_q;
-    p.o = static_cast<bf16 *>(o); p.ld_o = ld_o;
-    p.table = page_table; p.ld_table = ld_table;
-    p.seq_lens = seq_lens; p.n_seqs = n_seqs; p.nq = n_heads; p.max_len = max_len;
-    p.weight_in = weight_in; p.weight_out = weight_out; p.ld_weight = ld_weight;
-    p.workspace = workspace; p.status = status;
     cudaError_t e = h3::launch_attention_decode(p, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? H3ENC_OK : cuda_fail(nullptr, e, "attention_decode launch");
 }
@@ -1642,6 +1661,22 @@ h3enc_status h3enc_op_cache_evict(const h3enc_kv_cache *cache, const int32_t *pa
 // ---------------------------------------------------------------- a decoder that reads an encoder's states
 
 namespace {
+
+// Workspace of h3enc_op_attention_decode_shared: the decoding kernel's (its counters at the head), the prefixes' parts, what they
+// leave for the decoding kernel.
+struct SharedWorkspace {
+    size_t cross, pre_ml, pre_o, bytes;
+};
+SharedWorkspace shared_workspace(int sms, size_t decode, int32_t n_seqs, int32_t n_heads) {
+    const auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
+    const size_t rows = (size_t)n_seqs * n_heads;
+    SharedWorkspace y;
+    y.cross = up(decode);
+    y.pre_ml = y.cross + up(h3::attention_cross_workspace_bytes(sms, 128));
+    y.pre_o = y.pre_ml + up(rows * 8);
+    y.bytes = y.pre_o + up(rows * 128 * 4);
+    return y;
+}
 
 // The scaled frequencies of `r` as 64-bit fractions of a turn per position; false if it is not valid for heads of head_dim.
 bool take_rope(const h3enc_rope &r, int32_t head_dim, h3::RopeAppend *p) {
@@ -1743,6 +1778,106 @@ h3enc_status h3enc_op_rope_append(const void *qkv, int64_t ld_qkv, int32_t T, in
     p.status = status;
     cudaError_t e = h3::launch_rope_append(p, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? H3ENC_OK : cuda_fail(nullptr, e, "rope_append launch");
+}
+
+int64_t h3enc_op_attention_decode_shared_workspace_bytes(int32_t n_seqs, int32_t n_heads, int32_t max_len,
+                                                         int32_t with_weights) {
+    const int sms = h3::device_num_sms();
+    const size_t n = sms > 0 ? h3::attention_decode_workspace_bytes(sms, n_seqs, n_heads, max_len, with_weights != 0) : 0;
+    return n ? (int64_t)shared_workspace(sms, n, n_seqs, n_heads).bytes : -1;
+}
+
+h3enc_status h3enc_op_attention_decode_shared(
+    const void *q, int64_t ld_q, void *o, int64_t ld_o, const h3enc_kv_cache *cache, const int32_t *prefix_table,
+    int32_t ld_prefix, const int32_t *prefix_lens, const int32_t *prefix_rows, int32_t n_prefixes, int32_t max_prefix,
+    const int32_t *page_table, int32_t ld_table, const int32_t *seq_lens, int32_t n_seqs, int32_t n_heads, int32_t max_len,
+    const float *weight_in, float *weight_out, int64_t ld_weight, void *workspace, int64_t workspace_bytes, int32_t *status,
+    void *stream) {
+    const char *who = "attention_decode_shared";
+    h3::AttentionDecode p{};
+    size_t need = 0;
+    h3enc_status s = take_cache(cache, who, &p.cache);
+    if (s != H3ENC_OK) return s;
+    if (n_prefixes < 0 || n_prefixes > h3::kMaxSeqs || max_prefix < 0 || max_prefix > h3::kMaxCacheLen || ld_prefix < 0 ||
+        (n_prefixes > 0 && (int64_t)ld_prefix * cache->page_size < max_prefix) || (n_prefixes > 1 && !prefix_rows))
+        return fail(nullptr, H3ENC_ERR_INVALID_ARG, "%s: bad sizes, prefix_table does not hold max_prefix, or several prefixes "
+                                                    "without prefix_rows", who);
+    if (n_prefixes > 0 && (!prefix_lens || (!prefix_table && max_prefix > 0)))
+        return fail(nullptr, H3ENC_ERR_INVALID_ARG, "%s: prefix_lens or prefix_table NULL", who);
+    if (ld_q >= int64_t(1) << 39) return fail(nullptr, H3ENC_ERR_INVALID_ARG, "%s: ld_q too large", who);
+    s = take_decode(who, q, ld_q, o, ld_o, cache, page_table, ld_table, seq_lens, n_seqs, n_heads, max_len, weight_in,
+                    weight_out, ld_weight, workspace, status, &p, &need);
+    if (s != H3ENC_OK || n_seqs == 0) return s;
+    if (h3::attention_cross_weight(n_seqs, max_prefix, n_prefixes, n_heads, cache->n_kv_heads) < 0)
+        return fail(nullptr, H3ENC_ERR_UNSUPPORTED, "%s: sizes beyond 2e9 key tiles of prefixes", who);
+    const SharedWorkspace y = shared_workspace(h3::device_num_sms(), need, n_seqs, n_heads);
+    if (!workspace || workspace_bytes < 0 || (size_t)workspace_bytes < y.bytes ||
+        (reinterpret_cast<uintptr_t>(workspace) & 255))
+        return fail(nullptr, H3ENC_ERR_INVALID_ARG, "%s: workspace smaller than "
+                                                    "h3enc_op_attention_decode_shared_workspace_bytes() or not 256-byte "
+                                                    "aligned", who);
+    cudaError_t e = cudaSuccess;
+    if (n_prefixes > 0) {
+        char *ws = static_cast<char *>(workspace);
+        h3::AttentionCross c{};
+        c.q = p.q; c.ld_q = ld_q; c.Tq = n_seqs; c.max_keys = max_prefix;
+        c.n_segs = n_prefixes; c.nq = n_heads; c.nkv = cache->n_kv_heads; c.d = cache->head_dim;
+        c.cu_q = prefix_rows; c.key_lens = prefix_lens; c.table = prefix_table; c.ld_table = ld_prefix;
+        c.cache = p.cache;
+        c.pre_ml = reinterpret_cast<float2 *>(ws + y.pre_ml);
+        c.pre_o = reinterpret_cast<float *>(ws + y.pre_o);
+        c.workspace = ws + y.cross; c.status = status;
+        p.pre_o = c.pre_o; p.pre_ml = c.pre_ml;
+        e = h3::launch_attention_cross(c, static_cast<cudaStream_t>(stream));
+    }
+    if (e == cudaSuccess) e = h3::launch_attention_decode(p, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? H3ENC_OK : cuda_fail(nullptr, e, "attention_decode_shared launch");
+}
+
+int64_t h3enc_op_attention_cross_workspace_bytes(int32_t head_dim) {
+    const int sms = h3::device_num_sms();
+    return sms > 0 && (head_dim == 64 || head_dim == 128) ? (int64_t)h3::attention_cross_workspace_bytes(sms, head_dim) : -1;
+}
+
+h3enc_status h3enc_op_attention_cross(const void *q, int64_t ld_q, const void *k, int64_t ld_k, const void *v,
+                                      int64_t ld_v, void *o, int64_t ld_o, int32_t Tq, int32_t Tk, int32_t n_heads,
+                                      int32_t n_kv_heads, int32_t head_dim, const int32_t *cu_q, const int32_t *cu_k,
+                                      int32_t n_seqs, void *workspace, int64_t workspace_bytes, int32_t *status,
+                                      void *stream) {
+    const char *who = "attention_cross";
+    if (head_dim != 64 && head_dim != 128)
+        return fail(nullptr, H3ENC_ERR_UNSUPPORTED, "%s: head_dim must be 64 or 128", who);
+    if (Tq < 0 || Tq > h3::kMaxCacheLen || Tk < 0 || Tk > h3::kMaxCacheLen || n_heads < 1 || n_heads > 65536 ||
+        n_kv_heads < 1 || n_heads % n_kv_heads || n_seqs < 0 || n_seqs > h3::kMaxSeqs ||
+        ((!cu_q || !cu_k) && n_seqs > 1))
+        return fail(nullptr, H3ENC_ERR_INVALID_ARG, "%s: bad sizes, or several sequences without offsets", who);
+    if (Tq == 0 || n_seqs == 0) return H3ENC_OK;
+    const int64_t d = head_dim, width = n_heads * d, kv_width = n_kv_heads * d, most = int64_t(1) << 39;
+    if (!q || !o || !aligned16(q) || !aligned16(o) || ld_q < width || ld_o < width || ld_q % 8 || ld_o % 8 || ld_q >= most ||
+        (Tk > 0 && (!k || !v || !aligned16(k) || !aligned16(v) || ld_k < kv_width || ld_v < kv_width || ld_k % 8 ||
+                    ld_v % 8 || ld_k >= most || ld_v >= most)))
+        return fail(nullptr, H3ENC_ERR_INVALID_ARG, "%s: NULL or misaligned operand, or a bad leading dimension", who);
+    if (rows_overlap(q, ld_q, width, o, ld_o, width, Tq, 2) || rows_overlap(k, ld_k, kv_width, Tk, o, ld_o, width, Tq, 2) ||
+        rows_overlap(v, ld_v, kv_width, Tk, o, ld_o, width, Tq, 2))
+        return fail(nullptr, H3ENC_ERR_INVALID_ARG, "%s: o overlaps q, k or v", who);
+    if (h3::attention_cross_weight(Tq, Tk, n_seqs, n_heads, n_kv_heads) < 0)
+        return fail(nullptr, H3ENC_ERR_UNSUPPORTED, "%s: sizes beyond 2e9 key tiles", who);
+    const int sms = h3::device_num_sms();
+    if (sms <= 0) return fail(nullptr, H3ENC_ERR_CUDA, "%s: no CUDA device", who);
+    if (!workspace || workspace_bytes < 0 || (size_t)workspace_bytes < h3::attention_cross_workspace_bytes(sms, head_dim) ||
+        (reinterpret_cast<uintptr_t>(workspace) & 255))
+        return fail(nullptr, H3ENC_ERR_INVALID_ARG, "%s: workspace smaller than "
+                                                    "h3enc_op_attention_cross_workspace_bytes() or not 256-byte aligned", who);
+    h3::AttentionCross p{};
+    p.q = static_cast<const bf16 *>(q); p.ld_q = ld_q;
+    p.k = static_cast<const bf16 *>(k); p.ld_k = ld_k;
+    p.v = static_cast<const bf16 *>(v); p.ld_v = ld_v;
+    p.o = static_cast<bf16 *>(o); p.ld_o = ld_o;
+    p.Tq = Tq; p.max_keys = Tk; p.n_segs = n_seqs; p.nq = n_heads; p.nkv = n_kv_heads; p.d = head_dim;
+    p.cu_q = cu_q; p.cu_k = cu_k;
+    p.workspace = workspace; p.status = status;
+    cudaError_t e = h3::launch_attention_cross(p, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? H3ENC_OK : cuda_fail(nullptr, e, "attention_cross launch");
 }
 
 }  // extern "C"

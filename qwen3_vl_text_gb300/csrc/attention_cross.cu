@@ -1,0 +1,936 @@
+// Attention of packed query rows over keys and values of another length, on the tcgen05 tensor cores: cross attention
+// to an encoder's states, and the part of a shared prefix in the attention of one new token (attention_decode.cu
+// adds each sequence's own tokens).
+//
+//   o[t, h] = sum_i p_i v_i,  p = softmax_i(q[t, h] . k_i / sqrt(d)) over all keys i of t's segment, kv head h / (nq / nkv)
+//
+// No mask but the segment's end, so the rows of a kv head's whole group of q heads share every key: a tile's 128 rows are
+// (token, head of the group) pairs, 128 / group tokens at a time, fetched as one box of a tensor map of q as [token][kv
+// head][head of the group][element].  One token of a group of 8 heads is 8 rows of one tile, 4096 tokens are 256 full ones.
+//
+// Work: an item is a pair of row tiles (or a last single one) of one kv head of one segment, in steps of 128 keys.  The
+// steps of all items are laid end to end, a step of a pair counted twice, and cut into one equal run per CTA, one CTA per
+// SM, whatever the lengths are (read on the device).  A run may end inside an item, whose parts (unnormalised output,
+// running maximum and sum, fp32) go to the workspace and are joined in key order by a second launch: the
+// result does not depend on timing.
+//   warp 0       TMA: K, Q_A, Q_B, V, K, V, ... (page numbers looked up a batch of tiles ahead)
+//   warp 1       TMEM; tcgen05.mma from one thread: S_t = Q_t K_j^T, O_t += P_t V_j, the two tiles in turn, so that
+//                the tensor core works on one tile while the other's softmax runs; P read from TMEM
+//   warps 2-5    softmax of tile A, 6-9 of tile B: a thread per row; the maximum is raised lazily
+//   warps 10-13  (e4m3 pages) convert raw tiles to f16 ones
+// P enters the value product in bf16 (off by up to 2^-8 of each weight, as the rounded output is of itself; a second product for
+// the remainder would halve the rate where the tensor core bounds); e4m3 pages: in f16 (2^-11), times 2^13, as f16 ends at 2^-24.  Rows of no token are computed on what lies in shared memory and never stored.
+#include <algorithm>
+#include <atomic>
+#include <climits>
+#include <cmath>
+#include <type_traits>
+
+#include "common.cuh"
+#include "kernels.h"
+
+namespace h3 {
+
+namespace {
+
+constexpr int TQ = 128, TK = 128;
+enum { ROWS = 0, PAGES = 1, PAGES8 = 2 };   // keys: packed rows, bf16 pages, e4m3 pages
+
+template <int D, int MODE>
+struct Shape {
+    static constexpr bool F8 = MODE == PAGES8;
+    static constexpr int THREADS = F8 ? 448 : 320;
+    static constexpr int ATOM = TQ * 128;                  // 64 columns of a 128-row tile
+    static constexpr int TILE = TK * D * 2;                // one operand tile
+    static constexpr int NS = (D == 128 ? 2 : 4) / (F8 ? 2 : 1);   // K tiles, and V tiles, held
+    static constexpr int RAW = TK * D;                     // one e4m3 tile
+    static constexpr int RS = F8 ? (D == 128 ? 5 : 8) : 0;
+    static constexpr int OFF_Q = 0;
+    static constexpr int OFF_K = OFF_Q + 2 * TILE;
+    static constexpr int OFF_V = OFF_K + NS * TILE;
+    static constexpr int OFF_RAW = OFF_V + NS * TILE;
+    static constexpr int OFF_SEG = OFF_RAW + RS * RAW;     // pre, cq, ck
+    static constexpr int OFF_BAR = OFF_SEG + 3 * 4 * (kMaxSeqs + 4);
+    static constexpr int BARS = 4 * NS + 13 + 2 * RS;
+    static constexpr int BYTES = OFF_BAR + BARS * 8 + 128 + 1024;   // + alignment of the base
+    static constexpr float UP = F8 ? 8192.f : 1.f;         // weights, and so l and o, are held times this
+    static constexpr float UP_LOG2 = F8 ? 13.f : 0.f;
+    // the maximum is raised when it grew by more than this (log2): weights reach 2^8, f16 ones 2^15 with UP
+    static constexpr float RAISE = F8 ? 2.f : 8.f;
+};
+
+struct Args {
+    AttentionCross p;
+    int group, gc, chunks, tok;   // q heads per kv head; rows of a token in a tile, tiles' shares of a group; tokens of a tile
+    int box_shift;                // log2 of the places of a page that one box covers
+    float scale_log2;
+    float *part;                  // [cta][slot][tile][D][128] partial outputs, unnormalised
+    float2 *ml;                   // [cta][slot][tile][128] their running maximum and sum
+    int4 *desc;                   // [cta][2] the item whose first part is this CTA's slot 1: (row of its first token,
+                                  // tokens of A, tokens of B, unit), (parts, -, -, -)
+};
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint64_t f32x2(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void f32x2_split(uint64_t r, float &lo, float &hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(r));
+}
+__device__ __forceinline__ uint64_t ffma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t fadd2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float fmax3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+// Two e4m3 bytes -> two f16 (exact).
+__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t two) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)two));
+    return r;
+}
+__device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *m, uint64_t *bar, int32_t x, int32_t y, int32_t z) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
+        : "memory");
+}
+
+// The segments, in shared memory: tokens [cq[s], cq[s + 1]), keys [ck[s], ck[s + 1]) or (pages) the first ck[s] of s;
+// pre[s]: weight of the segments before s.
+struct Segments {
+    const int *pre, *cq, *ck;
+};
+template <int MODE>
+__device__ __forceinline__ int seg_keys(const Segments &g, int s) {
+    return MODE == ROWS ? max(g.ck[s + 1] - g.ck[s], 0) : g.ck[s];
+}
+__device__ __forceinline__ int seg_tokens(const Segments &g, int s) { return max(g.cq[s + 1] - g.cq[s], 0); }
+
+// Walks the items of a run [w, end) of weights.
+template <int MODE>
+struct Walk {
+    int w, end, s;
+    // the item: its segment s, unit, first token in the segment, tokens of its tiles (n_b 0: single), key tiles of
+    // the whole item and of this run [j0, j1), keys, and the weights [start, start + weight * steps)
+    int u, tok0, n_a, n_b, steps, j0, j1, len, start, weight;
+
+    __device__ __forceinline__ void begin(int w0, int w1, const Segments &g, int n_segs) {
+        w = w0;
+        end = w1;
+        int lo = 0, hi = n_segs;   // the s with pre[s] <= w0 < pre[s + 1]
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (g.pre[mid] <= w0) lo = mid;
+            else hi = mid;
+        }
+        s = lo;
+    }
+    __device__ __forceinline__ bool next(const Segments &g, int tok) {
+        while (w < end) {
+            while (g.pre[s + 1] <= w) ++s;
+            len = seg_keys<MODE>(g, s);
+            steps = (len + TK - 1) / TK;
+            const int n = seg_tokens(g, s), tiles = (n + tok - 1) / tok, pairs = tiles >> 1;
+            int off = w - g.pre[s];
+            u = off / (tiles * steps);
+            off -= u * tiles * steps;
+            const int blk = min(off / (2 * steps), pairs);
+            weight = blk < pairs ? 2 : 1;
+            start = w - (off - blk * 2 * steps);
+            tok0 = blk * 2 * tok;
+            n_a = min(tok, n - tok0);
+            n_b = weight == 2 ? min(tok, n - tok0 - tok) : 0;
+            const int stop = min(start + weight * steps, end);
+            j0 = (w - start + weight - 1) / weight;
+            j1 = (stop - start + weight - 1) / weight;
+            w = stop;
+            if (j0 < j1) return true;
+        }
+        return false;
+    }
+};
+
+// The runs: T / G weights each, one more for the first T % G.
+struct Runs {
+    unsigned run, longer;
+    __device__ __forceinline__ Runs(unsigned T, unsigned G) : run(G ? T / G : 0), longer(T - run * G) {}
+    __device__ __forceinline__ int first(unsigned c) const { return (int)(c * run + min(c, longer)); }
+    __device__ __forceinline__ int owner(unsigned w) const {
+        const unsigned split = longer * (run + 1);
+        return (int)(w < split ? w / (run + 1) : longer + (w - split) / run);
+    }
+};
+
+template <int D, int MODE>
+__global__ void __launch_bounds__(Shape<D, MODE>::THREADS, 1)
+    attention_cross_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                           const __grid_constant__ CUtensorMap tmV, const __grid_constant__ Args a) {
+    using S = Shape<D, MODE>;
+    constexpr bool F8 = S::F8;
+    constexpr int NS = S::NS, RS = S::RS;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+    uint8_t *sQ = smem + S::OFF_Q, *sK = smem + S::OFF_K, *sV = smem + S::OFF_V, *sRaw = smem + S::OFF_RAW;
+    int *pre = reinterpret_cast<int *>(smem + S::OFF_SEG), *cq = pre + kMaxSeqs + 4, *ck = cq + kMaxSeqs + 4;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + S::OFF_BAR);
+    uint64_t *k_full = bars, *v_full = k_full + NS, *k_empty = v_full + NS, *v_empty = k_empty + NS;
+    uint64_t *q_full = v_empty + NS, *q_ready = q_full + 2, *q_empty = q_ready + 2;   // [2] row tile, from here on
+    uint64_t *s_full = q_empty + 2, *p_full = s_full + 2, *pv_done = p_full + 2, *drain = pv_done + 2;
+    uint64_t *raw_full = drain + 1, *raw_empty = raw_full + RS;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(raw_empty + RS);
+    volatile int *abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    int *s_warp = reinterpret_cast<int *>(tmem_slot + 2);   // [14] scan of the warps' sums
+
+    const AttentionCross &p = a.p;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int units = p.nkv * a.chunks;
+
+    pdl_trigger();
+    if (tid == 0) {
+        for (int i = 0; i < NS; ++i) {
+            mbar_init(k_full + i, F8 ? 4 : 1);
+            mbar_init(v_full + i, F8 ? 4 : 1);
+            mbar_init(k_empty + i, 1);
+            mbar_init(v_empty + i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(q_full + i, 1);
+            mbar_init(q_ready + i, 4);
+            mbar_init(q_empty + i, 1);
+            mbar_init(s_full + i, 1);
+            mbar_init(p_full + i, 4);
+            mbar_init(pv_done + i, 1);
+        }
+        mbar_init(drain, 1);
+        for (int i = 0; i < RS; ++i) {
+            mbar_init(raw_full + i, 1);
+            mbar_init(raw_empty + i, 4);
+        }
+        *abort = 0;
+        fence_barrier_init();
+        prefetch_tmap(&tmQ);
+        prefetch_tmap(&tmK);
+        prefetch_tmap(&tmV);
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_slot, 512);
+        tmem_relinquish();
+    }
+    pdl_wait();
+
+    // the segments, clamped into what the call covers, and their weights: four per thread, scanned over the block
+    bool any_pair = false, any_empty = false;
+    {
+        bool bad = false;
+        for (int i = tid; i <= p.n_segs; i += S::THREADS) {
+            const int q = p.cu_q ? p.cu_q[i] : i ? p.Tq : 0;
+            cq[i] = min(max(q, 0), p.Tq);
+            bad |= q != cq[i];
+            if (MODE == ROWS || i < p.n_segs) {
+                const int k = MODE != ROWS ? p.key_lens[i] : p.cu_k ? p.cu_k[i] : i ? p.max_keys : 0;
+                ck[i] = min(max(k, 0), p.max_keys);
+                bad |= k != ck[i];
+            }
+        }
+        __syncthreads();
+        const Segments g{pre, cq, ck};
+        int n[4], sum = 0;
+        #pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int s = 4 * tid + i;
+            n[i] = 0;
+            if (s < p.n_segs) {
+                const int tokens = seg_tokens(g, s), tiles = (tokens + a.tok - 1) / a.tok, keys = seg_keys<MODE>(g, s);
+                n[i] = (keys + TK - 1) / TK * tiles * units;
+                any_pair |= tiles > 1 && keys > 0;
+                any_empty |= tokens > 0 && keys == 0;
+                bad |= cq[s + 1] < cq[s] || (MODE == ROWS && ck[s + 1] < ck[s]);
+            }
+            sum += n[i];
+        }
+        if (MODE != ROWS) any_empty |= cq[0] > 0 || cq[p.n_segs] < p.Tq;
+        if (bad && blockIdx.x == 0) report(p.status, ST_BOUNDS);
+        int inc = sum;
+        #pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += v;
+        }
+        if (lane == 31) s_warp[warp] = inc;
+        any_pair = __syncthreads_or(any_pair);
+        int at = inc - sum;
+        for (int w = 0; w < warp; ++w) at += s_warp[w];
+        #pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int s = 4 * tid + i;
+            if (s <= p.n_segs) pre[s] = at;
+            at += n[i];
+        }
+        tc_fence_before();
+        any_empty = __syncthreads_or(any_empty);
+        tc_fence_after();
+    }
+    const uint32_t tmem_base = *tmem_slot;
+    const Segments g{pre, cq, ck};
+    // A run is at least a step long, whichever items there are: parts of an item are then those of consecutive CTAs.
+    const unsigned T = (unsigned)pre[p.n_segs], G = min(any_pair ? T / 2 : T, gridDim.x);
+    const Runs runs(T, G);
+    const int w0 = blockIdx.x < G ? runs.first(blockIdx.x) : 0, w1 = blockIdx.x < G ? runs.first(blockIdx.x + 1) : 0;
+
+    // rows without any key: zeros, or (prefixes) an empty part
+    if (any_empty) {
+        const auto fill = [&](int t0, int t1) {
+            const long long step = (long long)gridDim.x * S::THREADS, at = (long long)blockIdx.x * S::THREADS + tid;
+            if (MODE == ROWS) {
+                const int vecs = p.nq * D / 8;
+                for (long long i = at; i < (long long)(t1 - t0) * vecs; i += step)
+                    *reinterpret_cast<uint4 *>(p.o + (t0 + i / vecs) * p.ld_o + i % vecs * 8) = make_uint4(0, 0, 0, 0);
+            } else {
+                for (long long i = at; i < (long long)(t1 - t0) * p.nq; i += step)
+                    p.pre_ml[(long long)t0 * p.nq + i] = make_float2(-INFINITY, 0.f);
+            }
+        };
+        for (int s = 0; s < p.n_segs; ++s)
+            if (seg_keys<MODE>(g, s) == 0 && seg_tokens(g, s) > 0) fill(cq[s], cq[s + 1]);
+        if (MODE != ROWS) {
+            if (cq[0] > 0) fill(0, cq[0]);
+            if (cq[p.n_segs] < p.Tq) fill(cq[p.n_segs], p.Tq);
+        }
+    }
+
+    Walk<MODE> w;
+    w.begin(w0, w1, g, p.n_segs);
+    const auto kv_head = [&](int u) { return a.chunks == 1 ? u : u / a.chunks; };
+
+    if (warp == 0) {
+        // ------------------------------------------------ producer
+        const int tile_shift = 7 - a.box_shift, boxes = 1 << tile_shift, per = 32 >> tile_shift;   // boxes of a tile, tiles of a batch
+        const int my_tile = lane >> tile_shift, my_box = lane & (boxes - 1);
+        const int page_mask = MODE == ROWS ? 0 : (1 << p.cache.page_shift) - 1;
+        bool ok = true;
+        uint32_t gk = 0, gv = 0, gr = 0, nq_loaded[2] = {0, 0};
+        const auto wait = [&](uint64_t *bar, uint32_t parity) {
+            ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, abort));
+            return ok;
+        };
+        while (ok && w.next(g, a.tok)) {
+            const int head = kv_head(w.u), chunk = w.u - head * a.chunks;
+            const auto look_up = [&](int j) {   // page of this lane's box in the batch of tiles from j on
+                const int key = (j + my_tile) * TK + (my_box << a.box_shift);
+                if (MODE == ROWS || j + my_tile >= w.j1 || key >= w.len) return 0;
+                return p.table[(long long)w.s * p.ld_table + (key >> p.cache.page_shift)];
+            };
+            int page = look_up(w.j0), next_page = 0, batch = w.j0;
+            // tile j of K or V into dst, on bar
+            const auto load = [&](int j, const CUtensorMap *m, uint8_t *dst, uint64_t *bar) {
+                if constexpr (MODE == ROWS) {
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(bar, S::TILE);
+                        for (int c = 0; c < D / 64; ++c)
+                            tma_load_3d(dst + c * S::ATOM, m, bar, c * 64, head, g.ck[w.s] + j * TK);
+                    }
+                } else {
+                    const int n = min(boxes, (w.len - j * TK + (1 << a.box_shift) - 1) >> a.box_shift);
+                    if (lane == 0) mbar_arrive_expect_tx(bar, (n << a.box_shift) * D * (F8 ? 1 : 2));
+                    __syncwarp();
+                    if (my_tile == j - batch && my_box < n) {
+                        int pg = page;
+                        if (pg < 0 || pg >= p.cache.num_pages) {
+                            report(p.status, ST_BOUNDS);
+                            pg = p.cache.num_pages;   // outside the map: the box is filled with zeros
+                        }
+                        const int place = (j * TK + (my_box << a.box_shift)) & page_mask;
+                        if constexpr (F8) {
+                            tma_load_4d(dst + (my_box << a.box_shift) * D, m, bar, 0, place, head, pg);
+                        } else {
+                            for (int c = 0; c < D / 64; ++c)
+                                tma_load_4d(dst + c * S::ATOM + (my_box << a.box_shift) * 128, m, bar, c * 64, place, head, pg);
+                        }
+                    }
+                }
+            };
+            const auto load_raw = [&](int j, const CUtensorMap *m) {
+                const int s = gr % (RS ? RS : 1), round = gr / (RS ? RS : 1);
+                if (round > 0 && !wait(raw_empty + s, (round - 1) & 1)) return;
+                load(j, m, sRaw + s * S::RAW, raw_full + s);
+                ++gr;
+            };
+            for (int j = w.j0; j < w.j1; ++j) {
+                if (MODE != ROWS) {
+                    if (j == batch + per) batch = j, page = next_page;
+                    if (j == batch) next_page = look_up(j + per);
+                }
+                if constexpr (F8) {
+                    load_raw(j, &tmK);
+                    if (!ok) break;
+                } else {
+                    if (gk >= NS && !wait(k_empty + gk % NS, (gk / NS - 1) & 1)) break;
+                    load(j, &tmK, sK + gk % NS * S::TILE, k_full + gk % NS);
+                    ++gk;
+                }
+                if (j == w.j0) {
+                    for (int t = 0; t < (w.n_b > 0 ? 2 : 1); ++t) {
+                        if (nq_loaded[t] > 0 && !wait(q_empty + t, (nq_loaded[t] - 1) & 1)) break;
+                        ++nq_loaded[t];
+                        if (lane == 0) {
+                            mbar_arrive_expect_tx(q_full + t, a.tok * a.gc * D * 2);
+                            for (int c = 0; c < D / 64; ++c)
+                                tma_load_4d(sQ + t * S::TILE + c * S::ATOM, &tmQ, q_full + t, c * 64, chunk * TQ, head,
+                                            cq[w.s] + w.tok0 + t * a.tok);
+                        }
+                    }
+                    if (!ok) break;
+                }
+                if constexpr (F8) {
+                    load_raw(j, &tmV);
+                    if (!ok) break;
+                } else {
+                    if (gv >= NS && !wait(v_empty + gv % NS, (gv / NS - 1) & 1)) break;
+                    load(j, &tmV, sV + gv % NS * S::TILE, v_full + gv % NS);
+                    ++gv;
+                }
+                __syncwarp();
+            }
+        }
+        if (!ok) {
+            // a wait ran out: leave once the copies in flight have landed (each of these waits is limited too)
+            if (lane == 0) {
+                report(p.status, ST_TIMEOUT);
+                *abort = 1;
+                const int never = 0;
+                if constexpr (F8) {
+                    for (uint32_t f = gr > RS ? gr - RS : 0; f < gr; ++f) mbar_wait(raw_full + f % RS, (f / RS) & 1, &never);
+                } else {
+                    for (uint32_t f = gk > NS ? gk - NS : 0; f < gk; ++f) mbar_wait(k_full + f % NS, (f / NS) & 1, &never);
+                    for (uint32_t f = gv > NS ? gv - NS : 0; f < gv; ++f) mbar_wait(v_full + f % NS, (f / NS) & 1, &never);
+                }
+                for (int t = 0; t < 2; ++t)
+                    if (nq_loaded[t]) mbar_wait(q_full + t, (nq_loaded[t] - 1) & 1, &never);
+            }
+            __syncwarp();
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------ products
+        constexpr uint32_t kind = F8 ? 0u : (1u << 7) | (1u << 10);   // A and B f16, or bf16
+        constexpr uint32_t base = (1u << 4) | kind | ((uint32_t)(TQ >> 4) << 24);
+        constexpr uint32_t idesc_s = base | ((uint32_t)(TK >> 3) << 17);
+        constexpr uint32_t idesc_o = base | ((uint32_t)(D >> 3) << 17) | (1u << 16);   // B (V) is MN-major
+        bool ok = true;
+        uint32_t gk = 0, gv = 0;          // ring positions of the next K tile to multiply first, the current V tile
+        uint32_t np[2] = {0, 0}, nq_used[2] = {0, 0};
+        const auto wait = [&](uint64_t *bar, uint32_t parity) {
+            ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, abort));
+            return ok;
+        };
+        // S_t = Q_t K^T for ring position pos
+        const auto issue_s = [&](int t, uint32_t pos) {
+            if (!wait(k_full + pos % NS, (pos / NS) & 1)) return;
+            tc_fence_after();
+            if (lane == 0) {
+                const uint32_t qa = smem_u32(sQ + t * S::TILE), kb = smem_u32(sK + pos % NS * S::TILE);
+                #pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t off = (kk >> 2) * S::ATOM + (kk & 3) * 32;
+                    umma_bf16(tmem_base + t * TQ, sdesc_sw128(qa + off), sdesc_sw128(kb + off), idesc_s, kk > 0);
+                }
+                umma_commit(s_full + t);
+            }
+            __syncwarp();
+        };
+        // O_t (+)= P_t V, P_t in the first 64 columns of tile t's S.  Values behind the segment may be anything (0 * NaN):
+        // the rows from `valid` on are cleared first.
+        const auto issue_pv = [&](int t, uint32_t pos, bool first, int valid) {
+            if (!wait(v_full + pos % NS, (pos / NS) & 1)) return;
+            uint8_t *tile = sV + pos % NS * S::TILE;
+            if (!F8 && t == 0 && valid < TK) {
+                for (int i = valid * 8 + lane; i < TK * 8; i += 32)
+                    #pragma unroll
+                    for (int c = 0; c < D / 64; ++c)
+                        *reinterpret_cast<uint4 *>(tile + c * S::ATOM + i * 16) = make_uint4(0, 0, 0, 0);
+                fence_proxy_async_smem();
+                __syncwarp();
+            }
+            if (!wait(p_full + t, np[t] & 1)) return;
+            ++np[t];
+            tc_fence_after();
+            if (lane == 0) {
+                const uint32_t vb = smem_u32(tile), pt = tmem_base + (uint32_t)(t * TQ);
+                #pragma unroll
+                for (int kk = 0; kk < TK / 16; ++kk)
+                    umma_bf16_ts(tmem_base + 256 + t * 128, pt + kk * 8, sdesc_sw128_mn(vb + kk * 2048, S::ATOM, 1024),
+                                 idesc_o, (!first || kk > 0) ? 1u : 0u);
+                umma_commit(pv_done + t);
+            }
+            __syncwarp();
+        };
+        const auto commit = [&](uint64_t *bar) {
+            if (lane == 0) umma_commit(bar);
+            __syncwarp();
+        };
+        while (ok && w.next(g, a.tok)) {
+            const int n = w.j1 - w.j0, last = w.n_b > 0 ? 1 : 0;   // last: the last tile that uses a key tile
+            for (int t = 0; t <= last && ok; ++t) {
+                if (!wait((F8 ? q_ready : q_full) + t, nq_used[t] & 1)) break;
+                ++nq_used[t];
+                issue_s(t, gk);
+                if (ok && n == 1) commit(q_empty + t);
+            }
+            if (!ok) break;
+            commit(k_empty + gk % NS);
+            for (int j = 0; j < n && ok; ++j, ++gv) {
+                for (int t = 0; t <= last && ok; ++t) {
+                    issue_pv(t, gv, j == 0, w.len - (w.j0 + j) * TK);
+                    if (!ok) break;
+                    if (t == last) commit(v_empty + gv % NS);
+                    if (j + 1 < n) {
+                        issue_s(t, gk + j + 1);
+                        if (!ok) break;
+                        if (j + 2 == n) commit(q_empty + t);   // the item's last scores of this tile
+                        if (t == last) commit(k_empty + (gk + j + 1) % NS);
+                    }
+                }
+            }
+            gk += n;
+        }
+        if (lane == 0) {
+            if (!ok) {
+                report(p.status, ST_TIMEOUT);
+                *abort = 1;
+            }
+            umma_commit(drain);
+            const int never = 0;
+            mbar_wait(drain, 0, &never);
+        }
+        __syncwarp();
+    } else if (warp < 10) {
+        // ------------------------------------------------ softmax
+        const int t = (warp - 2) >> 2, quarter = warp & 3;
+        const int r = quarter * 32 + lane;            // row of the tile = TMEM lane
+        const int r_tok = r / a.gc, r_head = r - r_tok * a.gc;
+        const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
+        const uint32_t tS = tmem_base + lane_off + (uint32_t)(t * TQ);
+        const uint32_t tO = tmem_base + lane_off + (uint32_t)(256 + t * 128);
+        uint32_t c = 0, items = 0;                    // steps and items of this row tile so far (barrier phases)
+        bool good = true;
+        const bool scribe = warp == 2 && lane == 0;
+        if (scribe) a.desc[2 * blockIdx.x + 1] = make_int4(0, 0, 0, 0);
+        const auto wait = [&](uint64_t *bar, uint32_t parity) {
+            good = __all_sync(0xffffffffu, mbar_wait(bar, parity, abort));
+            return good;
+        };
+        while (good && w.next(g, a.tok)) {
+            const int n_tok = t ? w.n_b : w.n_a;
+            if (n_tok == 0) continue;
+            const bool busy = quarter * 32 < n_tok * a.gc;   // this warp has rows of tokens
+            const int head = kv_head(w.u), chunk = w.u - head * a.chunks;
+            float scale = a.scale_log2;
+            if constexpr (F8) {
+                // q to f16 in place: a row's largest |q| goes to [2^14, 2^15): exact but for elements 2^-29 of it and smaller
+                if (!wait(q_full + t, items & 1)) break;
+                if (busy) {
+                    const float ks = p.cache.k_scale[head];
+                    uint8_t *row = sQ + t * S::TILE + r * 128;
+                    const auto at = [&](int ch) {
+                        return reinterpret_cast<uint4 *>(row + (ch >> 3) * S::ATOM + (((ch & 7) ^ (r & 7)) << 4));
+                    };
+                    float top = 0.f;
+                    #pragma unroll 4
+                    for (int ch = 0; ch < D / 8; ++ch) {
+                        const uint4 x = *at(ch);
+                        const uint32_t v[4] = {x.x, x.y, x.z, x.w};
+                        #pragma unroll
+                        for (int i = 0; i < 4; ++i) top = fmax3(top, fabsf(bf16_lo(v[i])), fabsf(bf16_hi(v[i])));
+                    }
+                    const int e = max((int)(__float_as_uint(top) >> 23) - 127, -100);
+                    const float up = copysignf(__uint_as_float((uint32_t)(14 - e + 127) << 23), ks);
+                    // (a scale of 0 still masks: -inf times a small number)
+                    scale = fmaxf(a.scale_log2 * fabsf(ks) * __uint_as_float((uint32_t)(e - 14 + 127) << 23), 1e-37f);
+                    #pragma unroll 4
+                    for (int ch = 0; ch < D / 8; ++ch) {
+                        uint4 x = *at(ch);
+                        uint32_t *v = &x.x;
+                        x.x = pack_f16x2(bf16_lo(v[0]) * up, bf16_hi(v[0]) * up);
+                        x.y = pack_f16x2(bf16_lo(x.y) * up, bf16_hi(x.y) * up);
+                        x.z = pack_f16x2(bf16_lo(x.z) * up, bf16_hi(x.z) * up);
+                        x.w = pack_f16x2(bf16_lo(x.w) * up, bf16_hi(x.w) * up);
+                        *at(ch) = x;
+                    }
+                    fence_proxy_async_smem();
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(q_ready + t);
+                ++items;
+            }
+            float m_use = -INFINITY, l = 0.f;
+            for (int j = w.j0; j < w.j1; ++j, ++c) {
+                if (!wait(s_full + t, c & 1)) break;
+                if (busy) {
+                    tc_fence_after();
+                    const int valid = w.len - j * TK;    // keys of the tile
+                    float mt;
+                    uint32_t v[F8 ? 64 : TK];
+                    if constexpr (F8) {
+                        // two passes over S: the converters leave too few registers for a whole row
+                        mt = -INFINITY;
+                        #pragma unroll
+                        for (int q = 0; q < 4; q += 2) {
+                            tmem_ld32(tS + 32 * q, *reinterpret_cast<uint32_t (*)[32]>(&v[0]));
+                            tmem_ld32(tS + 32 * q + 32, *reinterpret_cast<uint32_t (*)[32]>(&v[32]));
+                            tmem_ld_wait();
+                            if (valid < TK) {
+                                #pragma unroll
+                                for (int i = 0; i < 64; ++i)
+                                    if (32 * q + i >= valid) v[i] = __float_as_uint(-INFINITY);
+                            }
+                            float mx[4] = {mt, mt, mt, mt};
+                            #pragma unroll
+                            for (int i = 0; i < 64; i += 2)
+                                mx[i >> 1 & 3] = fmax3(mx[i >> 1 & 3], __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
+                            mt = fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]);
+                        }
+                        mt *= scale;
+                    } else {
+                        tmem_ld32(tS, *reinterpret_cast<uint32_t (*)[32]>(&v[0]));
+                        tmem_ld32(tS + 32, *reinterpret_cast<uint32_t (*)[32]>(&v[32]));
+                        tmem_ld32(tS + 64, *reinterpret_cast<uint32_t (*)[32]>(&v[F8 ? 0 : 64]));
+                        tmem_ld32(tS + 96, *reinterpret_cast<uint32_t (*)[32]>(&v[F8 ? 0 : 96]));
+                        tmem_ld_wait();
+                        if (valid < TK) {
+                            #pragma unroll
+                            for (int i = 0; i < TK; ++i)
+                                if (i >= valid) v[F8 ? 0 : i] = __float_as_uint(-INFINITY);
+                        }
+                        // three-input maxima: chain u takes scores u, u + 8, ..., u + 120
+                        float mx[8];
+                        #pragma unroll
+                        for (int u = 0; u < 8; ++u) {
+                            float m = __uint_as_float(v[u]);
+                            #pragma unroll
+                            for (int k = 1; k < 15; k += 2)
+                                m = fmax3(m, __uint_as_float(v[F8 ? 0 : u + 8 * k]), __uint_as_float(v[F8 ? 0 : u + 8 * k + 8]));
+                            mx[u] = fmaxf(m, __uint_as_float(v[F8 ? 0 : u + 120]));
+                        }
+                        mt = fmaxf(fmax3(mx[0], mx[1], mx[2]), fmax3(fmax3(mx[3], mx[4], mx[5]), mx[6], mx[7])) * scale;
+                    }
+                    float alpha = 1.f;
+                    bool raise = false;
+                    if (j == w.j0) {
+                        m_use = mt;
+                    } else if (mt > m_use + S::RAISE) {
+                        alpha = ex2(m_use - mt);
+                        m_use = mt;
+                        raise = true;
+                    }
+                    // P = 2^(s * scale - m) (times UP), packed in pairs over the first 64 columns of this row of S
+                    const float off = m_use == -INFINITY ? 0.f : S::UP_LOG2 - m_use;   // (only -inf scores so far: weights 0)
+                    const uint64_t scale2 = f32x2(scale, scale), off2 = f32x2(off, off);
+                    uint64_t rs2[4] = {0ull, 0ull, 0ull, 0ull};
+                    #pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        if constexpr (F8) {
+                            tmem_ld32(tS + 64 * h, *reinterpret_cast<uint32_t (*)[32]>(&v[0]));
+                            tmem_ld32(tS + 64 * h + 32, *reinterpret_cast<uint32_t (*)[32]>(&v[32]));
+                            tmem_ld_wait();
+                            if (valid < TK) {
+                                #pragma unroll
+                                for (int i = 0; i < 64; ++i)
+                                    if (64 * h + i >= valid) v[i] = __float_as_uint(-INFINITY);
+                            }
+                        }
+                        uint32_t pk[32];
+                        #pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            const int at = (F8 ? 0 : 64 * h) + 2 * i;
+                            float x0, x1;
+                            f32x2_split(ffma2(f32x2(__uint_as_float(v[at]), __uint_as_float(v[at + 1])), scale2, off2), x0, x1);
+                            const float p0 = ex2(x0), p1 = ex2(x1);
+                            rs2[i & 3] = fadd2(rs2[i & 3], f32x2(p0, p1));
+                            pk[i] = F8 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
+                        }
+                        tmem_st32(tS + 32 * h, pk);
+                    }
+                    float rs = 0.f;
+                    #pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        float r0, r1;
+                        f32x2_split(rs2[q], r0, r1);
+                        rs += r0 + r1;
+                    }
+                    l = l * alpha + rs;
+                    // O is rescaled after the previous product of this tile has completed
+                    if (__any_sync(0xffffffffu, raise)) {
+                        if (!wait(pv_done + t, (c - 1) & 1)) break;
+                        tc_fence_after();
+                        #pragma unroll 1
+                        for (int cc = 0; cc < D / 32; ++cc) {
+                            uint32_t o[32];
+                            tmem_ld32(tO + cc * 32, o);
+                            tmem_ld_wait();
+                            #pragma unroll
+                            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+                            tmem_st32(tO + cc * 32, o);
+                        }
+                    }
+                    tmem_st_wait();
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_full + t);
+            }
+            if (!good) break;
+            // The next item's first product (which overwrites O) waits for this warp's next P, written after these reads.
+            if (!wait(pv_done + t, (c - 1) & 1)) break;
+            tc_fence_after();
+            const bool whole = w.j0 == 0 && w.j1 == w.steps;
+            const int row0 = cq[w.s] + w.tok0;
+            if (scribe && !whole && w.j0 == 0) {
+                a.desc[2 * blockIdx.x] = make_int4(row0, w.n_a, w.n_b, w.u);
+                const int parts = runs.owner(w.start + w.weight * (w.steps - 1)) - (int)blockIdx.x + 1;
+                a.desc[2 * blockIdx.x + 1] = make_int4(parts, 0, 0, 0);
+            }
+            if (!busy) continue;
+            const bool live = r_tok < n_tok && r_tok < a.tok && chunk * TQ + r_head < a.group;
+            const long long row = row0 + t * a.tok + r_tok;
+            const int h = head * a.group + chunk * TQ + r_head;
+            if (!whole) {
+                const long long slot = (long long)(2 * blockIdx.x + (w.j0 == 0 ? 1 : 0)) * 2 + t;
+                float *dst = a.part + slot * (D * 128) + r;
+                #pragma unroll 1
+                for (int cc = 0; cc < D / 32; ++cc) {
+                    uint32_t o[32];
+                    tmem_ld32(tO + cc * 32, o);
+                    tmem_ld_wait();
+                    if (live) {
+                        #pragma unroll
+                        for (int i = 0; i < 32; ++i) dst[(cc * 32 + i) * 128] = __uint_as_float(o[i]);
+                    }
+                }
+                if (live) a.ml[slot * 128 + r] = make_float2(m_use, l);
+                continue;
+            }
+            const float f = MODE == ROWS ? 1.f / l : 1.f / S::UP;
+            #pragma unroll 1
+            for (int cc = 0; cc < D / 32; ++cc) {
+                uint32_t o[32];
+                tmem_ld32(tO + cc * 32, o);
+                tmem_ld_wait();
+                if (!live) continue;
+                if constexpr (MODE == ROWS) {
+                    uint4 *dst = reinterpret_cast<uint4 *>(p.o + row * p.ld_o + (long long)h * D + cc * 32);
+                    #pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const auto pair = [&](int i) {
+                            return pack_bf16x2(__uint_as_float(o[8 * q + i]) * f, __uint_as_float(o[8 * q + i + 1]) * f);
+                        };
+                        dst[q] = make_uint4(pair(0), pair(2), pair(4), pair(6));
+                    }
+                } else {
+                    float4 *dst = reinterpret_cast<float4 *>(p.pre_o + (row * p.nq + h) * D + cc * 32);
+                    #pragma unroll
+                    for (int q = 0; q < 8; ++q)
+                        dst[q] = make_float4(__uint_as_float(o[4 * q]) * f, __uint_as_float(o[4 * q + 1]) * f,
+                                             __uint_as_float(o[4 * q + 2]) * f, __uint_as_float(o[4 * q + 3]) * f);
+                }
+            }
+            if (MODE != ROWS && live) p.pre_ml[row * p.nq + h] = make_float2(m_use, l * f);
+        }
+        if (!good && lane == 0) {
+            report(p.status, ST_TIMEOUT);
+            *abort = 1;
+        }
+    } else if constexpr (F8) {
+        // ------------------------------------------------ e4m3 -> f16
+        const int ct = tid - 320;
+        uint32_t gr = 0, gt = 0;   // raw tiles, key tiles so far
+        bool good = true;
+        const auto wait = [&](uint64_t *bar, uint32_t parity) {
+            good = __all_sync(0xffffffffu, mbar_wait(bar, parity, abort));
+            return good;
+        };
+        const auto convert = [&](uint8_t *dst, uint64_t *full, uint64_t *empty, int keep) {
+            const int s = gr % RS;
+            if (!wait(raw_full + s, (gr / RS) & 1)) return;
+            if (gt >= NS && !wait(empty + gt % NS, (gt / NS - 1) & 1)) return;
+            const uint8_t *src = sRaw + s * S::RAW;
+            uint8_t *out = dst + gt % NS * S::TILE;
+            #pragma unroll
+            for (int i = 0; i < TK * D / 16 / 128; ++i) {
+                const int chunk = i * 128 + ct, row = chunk / (D / 16), c = 2 * (chunk % (D / 16));
+                uint4 x = *reinterpret_cast<const uint4 *>(src + chunk * 16);
+                if (row >= keep) x = make_uint4(0, 0, 0, 0);   // values behind the segment may be anything (0 * NaN)
+                uint8_t *at = out + (c >> 3) * S::ATOM + row * 128;
+                *reinterpret_cast<uint4 *>(at + (((c & 7) ^ (row & 7)) << 4)) =
+                    make_uint4(e4m3x2_f16x2(x.x), e4m3x2_f16x2(x.x >> 16), e4m3x2_f16x2(x.y), e4m3x2_f16x2(x.y >> 16));
+                *reinterpret_cast<uint4 *>(at + ((((c & 7) + 1) ^ (row & 7)) << 4)) =
+                    make_uint4(e4m3x2_f16x2(x.z), e4m3x2_f16x2(x.z >> 16), e4m3x2_f16x2(x.w), e4m3x2_f16x2(x.w >> 16));
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(full + gt % NS);
+                mbar_arrive(raw_empty + s);
+            }
+            ++gr;
+        };
+        while (good && w.next(g, a.tok))
+            for (int j = w.j0; j < w.j1 && good; ++j, ++gt) {
+                convert(sK, k_full, k_empty, TK);
+                if (good) convert(sV, v_full, v_empty, w.len - j * TK);
+            }
+        if (!good && lane == 0) {
+            report(p.status, ST_TIMEOUT);
+            *abort = 1;
+        }
+    }
+
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem_base, 512);
+    }
+}
+
+// Joins the parts of the items that several CTAs shared, in key order: part 0 is slot 1 of CTA blockIdx.x, part i slot 0 of CTA
+// blockIdx.x + i.  blockIdx.y: row tile and quarter of it (a lane per row); blockIdx.z: 32 columns, four per warp.
+template <int D, int MODE>
+__global__ void __launch_bounds__(256) attention_cross_join_kernel(const __grid_constant__ Args a) {
+    pdl_trigger();
+    pdl_wait();
+    const AttentionCross &p = a.p;
+    const int n = __ldcg(a.desc + 2 * blockIdx.x + 1).x;
+    if (n == 0) return;
+    const int4 it = __ldcg(a.desc + 2 * blockIdx.x);
+    const int t = blockIdx.y >> 2, r = (blockIdx.y & 3) * 32 + (threadIdx.x & 31), col = blockIdx.z * 32 + (threadIdx.x >> 5) * 4;
+    const int r_tok = r / a.gc, r_head = r - r_tok * a.gc;
+    const int head = it.w / a.chunks, chunk = it.w - head * a.chunks;
+    if (r_tok >= (t ? it.z : it.y) || r_tok >= a.tok || chunk * TQ + r_head >= a.group) return;
+    const auto slot = [&](int i) { return (long long)(2 * (blockIdx.x + i) + (i == 0 ? 1 : 0)) * 2 + t; };
+    float top = -INFINITY;
+    #pragma unroll 8
+    for (int i = 0; i < n; ++i) top = fmaxf(top, __ldcg(a.ml + slot(i) * 128 + r).x);
+    const float base = top == -INFINITY ? 0.f : top;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float l = 0.f;
+    #pragma unroll 8
+    for (int i = 0; i < n; ++i) {
+        const float2 ml = __ldcg(a.ml + slot(i) * 128 + r);
+        const float *src = a.part + slot(i) * (D * 128) + (long long)col * 128 + r;
+        const float f = ex2(ml.x - base);
+        l = fmaf(ml.y, f, l);
+        acc.x = fmaf(__ldcg(src), f, acc.x);
+        acc.y = fmaf(__ldcg(src + 128), f, acc.y);
+        acc.z = fmaf(__ldcg(src + 256), f, acc.z);
+        acc.w = fmaf(__ldcg(src + 384), f, acc.w);
+    }
+    const long long row = it.x + t * a.tok + r_tok;
+    const int h = head * a.group + chunk * TQ + r_head;
+    if (MODE == ROWS) {
+        const float f = 1.f / l;
+        *reinterpret_cast<uint2 *>(p.o + row * p.ld_o + (long long)h * D + col) =
+            make_uint2(pack_bf16x2(acc.x * f, acc.y * f), pack_bf16x2(acc.z * f, acc.w * f));
+    } else {
+        constexpr float f = 1.f / Shape<D, MODE>::UP;
+        *reinterpret_cast<float4 *>(p.pre_o + (row * p.nq + h) * D + col) = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
+        if (col == 0) p.pre_ml[row * p.nq + h] = make_float2(top, l * f);
+    }
+}
+
+size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
+
+template <int D, int MODE>
+cudaError_t launch(const AttentionCross &p, Args &a, int sms, long long most, cudaStream_t st) {
+    using S = Shape<D, MODE>;
+    static_assert(S::BYTES <= 232448, "shared memory of one CTA");
+    static std::atomic<bool> ready[kMaxDevices];   // the shared-memory opt-in, per device
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+    if (!ready[dev].load()) {
+        cudaError_t e = cudaFuncSetAttribute(attention_cross_kernel<D, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::BYTES);
+        if (e != cudaSuccess) return e;
+        ready[dev].store(true);
+    }
+    char *ws = static_cast<char *>(p.workspace);
+    a.desc = reinterpret_cast<int4 *>(ws);
+    a.ml = reinterpret_cast<float2 *>(ws + up256((size_t)sms * 2 * sizeof(int4)));
+    a.part = reinterpret_cast<float *>(a.ml + (size_t)sms * 4 * 128);
+    CUtensorMap tq, tk, tv;
+    bool ok = make_tmap_heads(&tq, p.q, D, a.group, p.nkv, p.Tq, p.ld_q, a.gc, a.tok);
+    if (MODE == ROWS) {
+        // (without any key nothing is loaded; a map still needs an address)
+        const bool any = p.max_keys > 0;
+        ok = ok && make_tmap_heads(&tk, any ? p.k : p.q, D, 1, any ? p.nkv : 1, any ? p.max_keys : 1, any ? p.ld_k : D, 0, TK) &&
+             make_tmap_heads(&tv, any ? p.v : p.q, D, 1, any ? p.nkv : 1, any ? p.max_keys : 1, any ? p.ld_v : D, 0, TK);
+    } else {
+        ok = ok && make_tmap_pages(&tk, p.cache, p.cache.k, 1 << a.box_shift) &&
+             make_tmap_pages(&tv, p.cache, p.cache.v, 1 << a.box_shift);
+    }
+    if (!ok) return cudaErrorInvalidValue;
+    const int grid = (int)std::min<long long>(sms, std::max<long long>(most, 1));
+    cudaLaunchAttribute at[1];
+    cudaLaunchConfig_t cfg = pdl_config(dim3(grid), dim3(S::THREADS), S::BYTES, st, at);
+    cudaError_t e = cudaLaunchKernelEx(&cfg, attention_cross_kernel<D, MODE>, tq, tk, tv, a);
+    if (e != cudaSuccess) return e;
+    cfg = pdl_config(dim3(grid, 8, D / 32), dim3(256), 0, st, at);
+    return cudaLaunchKernelEx(&cfg, attention_cross_join_kernel<D, MODE>, a);
+}
+
+}  // namespace
+
+size_t attention_cross_workspace_bytes(int num_sms, int d) {
+    return up256((size_t)num_sms * 2 * sizeof(int4)) + (size_t)num_sms * 4 * 128 * (sizeof(float2) + d * sizeof(float));
+}
+
+long long attention_cross_weight(int Tq, int max_keys, int n_segs, int nq, int nkv) {
+    const int group = nq / nkv, gc = std::min(group, TQ), chunks = (group + TQ - 1) / TQ, tok = TQ / gc;
+    // (every segment's last tile of rows may be partial)
+    const double tiles = (double)Tq / tok + std::min(n_segs, Tq);
+    const double steps = (double)max_keys / TK + 1;
+    const double most = (double)nkv * chunks * tiles * steps;
+    return most > 2e9 ? -1 : (long long)most;
+}
+
+cudaError_t launch_attention_cross(const AttentionCross &p, cudaStream_t st) {
+    if (p.Tq <= 0 || p.n_segs <= 0) return cudaSuccess;
+    const int sms = device_num_sms();
+    if (sms <= 0) return cudaErrorNoDevice;
+    Args a{};
+    a.p = p;
+    a.group = p.nq / p.nkv;
+    a.gc = std::min(a.group, TQ);
+    a.chunks = (a.group + TQ - 1) / TQ;
+    a.tok = TQ / a.gc;
+    const bool pages = p.key_lens != nullptr;
+    a.box_shift = pages ? std::min(7, p.cache.page_shift) : 7;
+    const int d = p.d;
+    a.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)d));
+    const long long most = attention_cross_weight(p.Tq, p.max_keys, p.n_segs, p.nq, p.nkv);
+    if (!pages) return d == 128 ? launch<128, ROWS>(p, a, sms, most, st) : launch<64, ROWS>(p, a, sms, most, st);
+    if (p.cache.f8) return d == 128 ? launch<128, PAGES8>(p, a, sms, most, st) : launch<64, PAGES8>(p, a, sms, most, st);
+    return d == 128 ? launch<128, PAGES>(p, a, sms, most, st) : launch<64, PAGES>(p, a, sms, most, st);
+}
+
+}  // namespace h3

@@ -202,7 +202,8 @@ struct Walk {
     }
 };
 
-template <int D, bool F8, int BLOCKS>
+// PRE: each sequence's tokens follow a prefix, whose part attention_cross.cu has left in pre_o and pre_ml.
+template <int D, bool F8, int BLOCKS, bool PRE>
 __global__ void __launch_bounds__(Shape<D, F8, BLOCKS>::THREADS, 1)
     attention_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                             const Args a) {
@@ -276,11 +277,24 @@ __global__ void __launch_bounds__(Shape<D, F8, BLOCKS>::THREADS, 1)
     }
     // the run of CTA c: T / G tiles, one more for the first T % G
     const unsigned T = (unsigned)pre[p.n_seqs], G = min(T, gridDim.x);   // CTAs that have a run
-    // sequences without tokens: zero rows
+    // sequences without tokens: zero rows, or what their prefix gives
     for (int b = blockIdx.x; b < p.n_seqs; b += gridDim.x)
         if (pre[b + 1] == pre[b])
-            for (int i = tid; i < p.nq * D / 8; i += S::THREADS)
-                *reinterpret_cast<uint4 *>(p.o + b * p.ld_o + 8 * i) = make_uint4(0, 0, 0, 0);
+            for (int i = tid; i < p.nq * D / 8; i += S::THREADS) {
+                uint4 x = make_uint4(0, 0, 0, 0);
+                if constexpr (PRE) {
+                    const long long at = (long long)b * p.nq + i / (D / 8);
+                    const float l = __ldcg(p.pre_ml + at).y;
+                    if (l != 0.f) {
+                        const float4 *v = reinterpret_cast<const float4 *>(p.pre_o + at * D + i % (D / 8) * 8);
+                        const float4 y = __ldcg(v), z = __ldcg(v + 1);
+                        const float f = (F8 ? p.cache.v_scale[i / (D / 8) / a.group] : 1.f) / l;
+                        x = make_uint4(pack_bf16x2(y.x * f, y.y * f), pack_bf16x2(y.z * f, y.w * f),
+                                       pack_bf16x2(z.x * f, z.y * f), pack_bf16x2(z.z * f, z.w * f));
+                    }
+                }
+                *reinterpret_cast<uint4 *>(p.o + b * p.ld_o + 8 * i) = x;
+            }
     if (blockIdx.x >= G) return;
     const unsigned run = T / G, longer = T - run * G;
     const int t0 = (int)(blockIdx.x * run + min(blockIdx.x, longer)), t1 = t0 + (int)(run + (blockIdx.x < longer));
@@ -397,6 +411,18 @@ __global__ void __launch_bounds__(Shape<D, F8, BLOCKS>::THREADS, 1)
     shared[0].b = shared[1].b = -1;
     const int trow = tid / (D / 4), tcol = tid % (D / 4) * 4;   // this thread's output in the sums of the joins
     const auto store = [&](int b, int h, float4 v, float m, float l, float vs) {
+        if constexpr (PRE) {   // one more part
+            const long long at = (long long)b * p.nq + h;
+            const float2 ml = __ldcg(p.pre_ml + at);
+            if (ml.y != 0.f) {   // (no value is read where the prefix is empty)
+                const float4 x = __ldcg(reinterpret_cast<const float4 *>(p.pre_o + at * D + tcol));
+                const float top = fmaxf(m, ml.x), c = m == -INFINITY ? 0.f : ex2(m - top);
+                const float e = ml.x == -INFINITY ? 0.f : ex2(ml.x - top) * S::UP;
+                v = make_float4(fmaf(v.x, c, x.x * e), fmaf(v.y, c, x.y * e), fmaf(v.z, c, x.z * e), fmaf(v.w, c, x.w * e));
+                l = fmaf(l, c, ml.y * e);
+                m = top;
+            }
+        }
         const float inv = 1.f / l, f = inv * vs;
         *reinterpret_cast<uint2 *>(p.o + b * p.ld_o + (long long)h * D + tcol) =
             make_uint2(pack_bf16x2(v.x * f, v.y * f), pack_bf16x2(v.z * f, v.w * f));
@@ -851,7 +877,7 @@ Layout layout(int ctas, int n_seqs, int nq, int max_len, bool weights) {
     return y;
 }
 
-template <int D, bool F8, int BLOCKS>
+template <int D, bool F8, int BLOCKS, bool PRE>
 cudaError_t launch_kernel(const CUtensorMap &tk, const CUtensorMap &tv, const Args &a, int grid, cudaStream_t st) {
     static std::atomic<bool> ready[kMaxDevices];   // the shared-memory opt-in, per device
     int dev = 0;
@@ -859,14 +885,14 @@ cudaError_t launch_kernel(const CUtensorMap &tk, const CUtensorMap &tv, const Ar
     constexpr int bytes = Shape<D, F8, BLOCKS>::BYTES;
     static_assert(bytes <= 232448, "shared memory of one CTA");
     if (!ready[dev].load()) {
-        cudaError_t e = cudaFuncSetAttribute(attention_decode_kernel<D, F8, BLOCKS>,
+        cudaError_t e = cudaFuncSetAttribute(attention_decode_kernel<D, F8, BLOCKS, PRE>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e != cudaSuccess) return e;
         ready[dev].store(true);
     }
     cudaLaunchAttribute at[1];
     cudaLaunchConfig_t cfg = pdl_config(dim3(grid), dim3(Shape<D, F8, BLOCKS>::THREADS), bytes, st, at);
-    return cudaLaunchKernelEx(&cfg, attention_decode_kernel<D, F8, BLOCKS>, tk, tv, a);
+    return cudaLaunchKernelEx(&cfg, attention_decode_kernel<D, F8, BLOCKS, PRE>, tk, tv, a);
 }
 
 }  // namespace
@@ -914,9 +940,13 @@ cudaError_t launch_attention_decode(const AttentionDecode &p, cudaStream_t st) {
     const auto run = [&](auto d, auto f8) {
         constexpr int D = decltype(d)::value;
         constexpr bool F8 = decltype(f8)::value;
-        return a.group <= 8 ? launch_kernel<D, F8, 1>(tk, tv, a, grid, st)
-                            : (split ? launch_kernel<D, F8, 4>(tk, tv, a, grid, st)
-                                     : launch_kernel<D, F8, 2>(tk, tv, a, grid, st));
+        const auto with = [&](auto pre) {
+            constexpr bool PRE = decltype(pre)::value;
+            return a.group <= 8 ? launch_kernel<D, F8, 1, PRE>(tk, tv, a, grid, st)
+                                : (split ? launch_kernel<D, F8, 4, PRE>(tk, tv, a, grid, st)
+                                         : launch_kernel<D, F8, 2, PRE>(tk, tv, a, grid, st));
+        };
+        return p.pre_o ? with(std::true_type{}) : with(std::false_type{});
     };
     const std::integral_constant<int, 128> d128;
     const std::integral_constant<int, 64> d64;

@@ -1246,6 +1246,38 @@ bool make_tmap_cache(CUtensorMap *m, const KvCache &c, const void *base) {
     return r == CUDA_SUCCESS;
 }
 
+bool make_tmap_heads(CUtensorMap *m, const bf16 *base, int d, int group, int nkv, long long rows, long long ld, int heads_box,
+                     int rows_box) {
+    PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)group, (cuuint64_t)nkv, (cuuint64_t)rows};
+    const cuuint64_t strides[3] = {(cuuint64_t)d * 2, (cuuint64_t)group * d * 2, (cuuint64_t)ld * 2};
+    const cuuint32_t box[4] = {64, (cuuint32_t)heads_box, 1, (cuuint32_t)rows_box};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    // (one head per kv head and box: without that dimension)
+    const cuuint64_t dims3[3] = {dims[0], dims[2], dims[3]}, strides3[2] = {strides[1], strides[2]};
+    const cuuint32_t box3[3] = {64, 1, (cuuint32_t)rows_box};
+    CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, heads_box ? 4 : 3, const_cast<bf16 *>(base), heads_box ? dims : dims3,
+                    heads_box ? strides : strides3, heads_box ? box : box3, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+}
+
+bool make_tmap_pages(CUtensorMap *m, const KvCache &c, const void *base, int places) {
+    PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t es = c.f8 ? 1 : 2, page = cuuint64_t(1) << c.page_shift;
+    const cuuint64_t dims[4] = {(cuuint64_t)c.d, page, (cuuint64_t)c.nkv, (cuuint64_t)c.num_pages};
+    const cuuint64_t strides[3] = {c.d * es, page * c.d * es, (cuuint64_t)c.page_stride * es};
+    const cuuint32_t box[4] = {c.f8 ? (cuuint32_t)c.d : 64u, (cuuint32_t)places, 1, 1};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    CUresult r = fn(m, c.f8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base),
+                    dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                    c.f8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+}
+
 bool make_tmap_rows_e4m3(CUtensorMap *m, const void *ptr, uint64_t rows, uint64_t cols, uint32_t box_rows) {
     PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
     if (!fn || rows == 0 || cols == 0 || cols % 16 != 0 || (reinterpret_cast<uintptr_t>(ptr) & 15)) return false;

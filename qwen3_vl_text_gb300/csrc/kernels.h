@@ -246,9 +246,41 @@ struct AttentionDecode {
     const float *weight_in;
     float *weight_out;
     long long ld_weight;
+    const float *pre_o;      // what launch_attention_cross left of a prefix in front of the tokens; NULL: none
+    const float2 *pre_ml;
     void *workspace;
     int32_t *status;
 };
+// Attention of packed rows over keys of another length (attention_cross.cu): segment s's tokens [cu_q[s], cu_q[s + 1]) of q over
+// rows [cu_k[s], cu_k[s + 1]) of k and v, or (key_lens set: prefixes) over the first key_lens[s] tokens of row s of the page
+// table, with the result left for launch_attention_decode in pre_o and pre_ml.
+struct AttentionCross {
+    const bf16 *q, *k, *v;
+    bf16 *o;
+    long long ld_q, ld_k, ld_v, ld_o;
+    int Tq, max_keys;                 // rows of q; rows of k and v, or the bound on key_lens
+    int n_segs, nq, nkv, d;
+    const int32_t *cu_q, *cu_k;       // NULL: one segment
+    const int32_t *key_lens, *table;
+    int ld_table;
+    KvCache cache;
+    float *pre_o;                     // [Tq][nq][d] sums of 2^(s - m) v (e4m3: without v's scale)
+    float2 *pre_ml;                   // [Tq][nq] m (log2 units) and the sum of 2^(s - m); l = 0: no keys
+    void *workspace;
+    int32_t *status;
+};
+size_t attention_cross_workspace_bytes(int num_sms, int d);
+// Bound on the steps (of a row tile and 128 keys) of a call; -1 where they pass 2e9.
+long long attention_cross_weight(int Tq, int max_keys, int n_segs, int nq, int nkv);
+cudaError_t launch_attention_cross(const AttentionCross &p, cudaStream_t st);
+// Tensor map of bf16 rows as [row][kv head][head of the group][element], read in boxes of `rows_box` rows x `heads_box` heads x 64
+// elements (heads_box 0: [row][head][element]), swizzled by 128 bytes.  False if the driver refuses it.
+bool make_tmap_heads(CUtensorMap *m, const bf16 *base, int d, int group, int nkv, long long rows, long long ld, int heads_box,
+                     int rows_box);
+// Tensor map of the cache's keys or values in boxes of `places` places of one head: bf16 64 elements wide and swizzled by 128
+// bytes, e4m3 whole rows without swizzle.
+bool make_tmap_pages(CUtensorMap *m, const KvCache &cache, const void *base, int places);
+
 // Tensor map of the cache's keys or values (`base` = cache.k or cache.v) as [page][kv head][place]
 // [element], read in boxes of min(page_size, 64) places x 128 bytes (64 for e4m3 with d = 64) of one
 // head, swizzled by that width.  False if the driver refuses it.

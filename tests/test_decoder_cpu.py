@@ -202,3 +202,133 @@ def test_rope_append_checks_its_tensors(Q, recorded):
     a.update(rope=None, positions=None, cache=None, page_table=None, seq_lens=None, cu_rows=None, max_len=0, status=None)
     Q.h3enc_op_rope_append(**a)
     assert recorded.args[9:12] == (None, None, 0) and recorded.args[16:23] == (None, None, 0, None, None, 0, 0)
+
+
+# ---------------------------------------------------------------- shared prefixes and cross attention: refusals
+
+def test_attend_prefix_and_cross_by_hand():
+    rng = np.random.default_rng(2)
+    q, k, v = rng.standard_normal((5, 6, 8)), rng.standard_normal((9, 2, 8)), rng.standard_normal((9, 2, 8))
+    o = O.decoder.cross(q, k, v)
+    for t in range(5):
+        one, p = O.decode.attend_one(q[t], k, v)
+        assert np.allclose(o[t], one, rtol=1e-12, atol=1e-14)
+        both, own = O.decoder.attend_prefix(q[t], k[:4], v[:4], k[4:], v[4:])
+        assert np.allclose(both, one) and np.allclose(own, p[:, 4:])
+    assert not O.decoder.cross(q, k[:0], v[:0]).any()
+
+
+def _shared(Q, cache, **kw):
+    a = dict(q=1 << 20, ld_q=256, o=1 << 24, ld_o=256, ptable=16, ld_p=4, plens=16, prows=16, groups=2, max_prefix=64,
+             table=16, ld_table=4, lens=16, n=2, nq=4, max_len=64, w_in=None, w_out=None, ld_w=64, ws=256, ws_bytes=1 << 40)
+    a.update(kw)
+    Q._check(Q.lib.h3enc_op_attention_decode_shared(
+        a["q"], a["ld_q"], a["o"], a["ld_o"], cache, a["ptable"], a["ld_p"], a["plens"], a["prows"], a["groups"],
+        a["max_prefix"], a["table"], a["ld_table"], a["lens"], a["n"], a["nq"], a["max_len"], a["w_in"], a["w_out"],
+        a["ld_w"], a["ws"], a["ws_bytes"], None, None))
+
+
+def _cross(Q, **kw):
+    a = dict(q=1 << 20, ld_q=256, k=1 << 22, ld_k=256, v=(1 << 22) + 256, ld_v=256, o=1 << 24, ld_o=256, Tq=5, Tk=7, nq=4, nkv=2,
+             d=64, cu_q=16, cu_k=16, n=2, ws=256, ws_bytes=1 << 40)
+    a.update(kw)
+    Q._check(Q.lib.h3enc_op_attention_cross(
+        a["q"], a["ld_q"], a["k"], a["ld_k"], a["v"], a["ld_v"], a["o"], a["ld_o"], a["Tq"], a["Tk"], a["nq"], a["nkv"],
+        a["d"], a["cu_q"], a["cu_k"], a["n"], a["ws"], a["ws_bytes"], None, None))
+
+
+@pytest.mark.parametrize("kw,code", BAD_CACHES)
+def test_bad_caches_are_refused_behind_prefixes(Q, kw, code):
+    _refused(Q, code, _shared, _cache(Q, **kw))
+
+
+@pytest.mark.parametrize("kw", [
+    dict(groups=-1), dict(groups=1025), dict(max_prefix=-1), dict(max_prefix=65), dict(max_prefix=2 ** 30 + 1, ld_p=2 ** 27),
+    dict(ld_p=-1), dict(ld_p=3), dict(prows=None), dict(plens=None), dict(ptable=None), dict(ld_q=1 << 39),
+    dict(n=-1), dict(n=1025), dict(nq=0), dict(nq=3), dict(max_len=-1), dict(max_len=65), dict(q=None), dict(o=None),
+    dict(q=(1 << 20) + 8), dict(ld_q=252), dict(ld_o=128), dict(table=None), dict(lens=None), dict(o=1 << 20), dict(w_in=16),
+    dict(w_out=16, ld_w=63)])
+def test_attention_decode_shared_refuses(Q, kw):
+    _refused(Q, 2, _shared, _cache(Q), **kw)
+
+
+def test_attention_decode_shared_of_no_sequences_does_nothing(Q):
+    _shared(Q, _cache(Q), n=0)
+    _shared(Q, _cache(Q), n=0, groups=0, prows=None, plens=None, ptable=None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(d=96), 6), (dict(Tq=-1), 2), (dict(Tk=-1), 2), (dict(Tq=2 ** 30 + 1), 2), (dict(nq=0), 2), (dict(nq=5), 2),
+    (dict(nkv=0), 2), (dict(nq=65538), 2), (dict(n=-1), 2), (dict(n=1025), 2), (dict(cu_q=None), 2), (dict(cu_k=None), 2),
+    (dict(q=None), 2), (dict(k=None), 2), (dict(v=None), 2), (dict(o=None), 2), (dict(q=(1 << 20) + 2), 2), (dict(k=(1 << 22) + 2), 2),
+    (dict(v=(1 << 22) + 8), 2), (dict(o=(1 << 24) + 8), 2), (dict(ld_q=248), 2), (dict(ld_q=260), 2), (dict(ld_k=120), 2),
+    (dict(ld_v=132), 2), (dict(ld_o=252), 2), (dict(ld_k=1 << 39), 2), (dict(ld_q=1 << 39), 2), (dict(o=1 << 20), 2),
+    (dict(o=(1 << 20) + 512 * 4), 2), (dict(o=1 << 22), 2), (dict(o=(1 << 22) + 256), 2),
+    (dict(Tq=2 ** 26, Tk=2 ** 26, q=0, o=1 << 50, k=1 << 55, v=1 << 56), 2), (dict(Tq=2 ** 26, Tk=2 ** 26, o=1 << 50, k=1 << 55, v=1 << 56), 6)])
+def test_attention_cross_refuses(Q, kw, code):
+    _refused(Q, code, _cross, **kw)
+
+
+def test_attention_cross_takes_states_right_behind_its_output(Q):
+    """o's own rows end where k begins, however many rows k has (refused for its workspace, after that check)."""
+    with pytest.raises(Q.H3encError) as e:
+        _cross(Q, o=1 << 24, k=(1 << 24) + 5 * 512, v=(1 << 24) + 5 * 512 + 256, Tk=700, ws=None)
+    assert "overlap" not in str(e.value)
+
+
+def test_attention_cross_of_nothing_does_nothing(Q):
+    _cross(Q, Tq=0)
+    _cross(Q, n=0)
+
+
+def test_workspace_sizes_without_a_gpu_or_for_refused_sizes(Q):
+    torch = pytest.importorskip("torch")
+    if not torch.cuda.is_available():
+        assert Q.h3enc_op_attention_decode_shared_workspace_bytes(1, 8, 100) == -1
+        assert Q.h3enc_op_attention_cross_workspace_bytes(128) == -1
+    assert Q.h3enc_op_attention_cross_workspace_bytes(96) == -1
+    for bad in ((-1, 8, 100), (1025, 8, 100), (1, 0, 100), (1, 8, -1)):
+        assert Q.h3enc_op_attention_decode_shared_workspace_bytes(*bad) == -1
+
+
+def test_attention_decode_shared_checks_its_tensors(Q, recorded):
+    torch = pytest.importorskip("torch")
+    bf, i32 = dict(dtype=torch.bfloat16), dict(dtype=torch.int32)
+    k = torch.zeros(5, 2, 16, 64, **bf)
+    a = dict(q=torch.zeros(3, 256, **bf), o=torch.zeros(3, 256, **bf), cache=Q.KVCache(k, k),
+             prefix_table=torch.zeros(2, 5, **i32), prefix_lens=torch.zeros(2, **i32), max_prefix=80,
+             page_table=torch.zeros(3, 4, **i32), seq_lens=torch.zeros(3, **i32), n_heads=4, max_len=64,
+             workspace=torch.zeros(64, dtype=torch.uint8), prefix_rows=torch.zeros(3, **i32),
+             weight_in=torch.zeros(3, 64), weight_out=torch.zeros(3, 64), status=torch.zeros(1, **i32))
+    Q.h3enc_op_attention_decode_shared(**a)
+    got = recorded.args
+    assert got[5:11] == (a["prefix_table"].data_ptr(), 5, a["prefix_lens"].data_ptr(), a["prefix_rows"].data_ptr(), 2, 80)
+    assert got[11:17] == (a["page_table"].data_ptr(), 4, a["seq_lens"].data_ptr(), 3, 4, 64) and got[21] == 64
+    for name in ("q", "o", "prefix_table", "prefix_rows", "page_table", "weight_in", "weight_out", "status"):
+        for bad in _wrong(torch, a[name], True):
+            _refuses(Q, Q.h3enc_op_attention_decode_shared, a, name, bad)
+    for name in ("prefix_lens", "seq_lens"):
+        _refuses(Q, Q.h3enc_op_attention_decode_shared, a, name, a[name].float())
+    _refuses(Q, Q.h3enc_op_attention_decode_shared, a, "workspace", torch.zeros(64, dtype=torch.uint8)[::2])
+
+
+def test_attention_cross_checks_its_tensors(Q, recorded):
+    torch = pytest.importorskip("torch")
+    bf, i32 = dict(dtype=torch.bfloat16), dict(dtype=torch.int32)
+    kv = torch.zeros(9, 256, **bf)
+    a = dict(q=torch.zeros(6, 256, **bf), k=kv[:, :128], v=kv[:, 128:], o=torch.zeros(6, 256, **bf), n_heads=4, n_kv_heads=2,
+             head_dim=64, workspace=torch.zeros(64, dtype=torch.uint8), cu_q=torch.zeros(4, **i32), cu_k=torch.zeros(4, **i32),
+             status=torch.zeros(1, **i32))
+    Q.h3enc_op_attention_cross(**a)
+    got = recorded.args
+    assert got[1] == 256 and got[2:6] == (kv.data_ptr(), 256, kv.data_ptr() + 256, 256)
+    assert got[8:16] == (6, 9, 4, 2, 64, a["cu_q"].data_ptr(), a["cu_k"].data_ptr(), 3)
+    for name in ("q", "k", "v", "o"):
+        for bad in (a[name].float(), a[name][:, :-1], torch.cat([a[name], a[name]], 1)[:, ::2]):
+            _refuses(Q, Q.h3enc_op_attention_cross, a, name, bad)
+    for name, bad in (("v", kv[:8, 128:]), ("o", a["o"][:5]), ("cu_k", torch.zeros(3, **i32)), ("cu_q", torch.zeros(4)),
+                      ("cu_q", torch.zeros(0, **i32)), ("status", torch.zeros(1)), ("workspace", torch.zeros(64)[::2])):
+        _refuses(Q, Q.h3enc_op_attention_cross, a, name, bad)
+    a.update(cu_q=None, cu_k=None)
+    Q.h3enc_op_attention_cross(**a)
+    assert recorded.args[13:16] == (None, None, 1)

@@ -7,6 +7,11 @@ Tolerances.  A bf16 output is rounded once: half a step, 2^-8 of the value, plus
 Rotation: the angle is a 64-bit fraction of a turn, so cos and sin are off by less than 2^-21 of the magnitude (fp32
 rounding of the fraction and of sincospi), and the norm's factor by 2^-21: at most 2^-19 of a pair's length.
 An e4m3 value is off by half a step: 2^-4 of the value, 2^-10 at least.
+Attention: with S1 = max_i sum_e |q_e k_ie| / sqrt(d), the fp32 score of d products is off by at most DELTA = 16 * 2^-24 * S1
+(16 accumulation steps of 16 products, and the same again for the base-2 exponent), so a weight by a factor of at most
+1 + 2 DELTA; it enters the value product in bf16, 2^-8 of it (f16 behind an e4m3 cache: 2^-11, and at least 2^-37
+absolutely; a sequence's own tokens: two halves, 2^-16).  With A = sum_i p_i |v_i| the output is off by A times that, 2^-18 A for
+fp32 sums and the joins, and half a step of bf16.  An accumulated weight is off by 2 DELTA + 2^-18 of sum_h p_h.
 """
 import numpy as np
 import pytest
@@ -291,3 +296,376 @@ def test_rope_append_captured_and_replayed_with_other_lengths():
     angle = (want[-1][1].cpu().numpy() - 1.0)[:, None] * O.decoder.frequencies(d, 1e4)[0]
     y = O.decoder.rotate(_f64(want[-1][0]).reshape(n, 8, d)[:, :nq], angle, 1.0, False)
     _check_bf16(_f64(q_out).reshape(y.shape), y, 2.0 ** -19 * _pair_length(y, d, False))
+
+
+# ---------------------------------------------------------------- cross attention
+
+def _score_bound(q, k):
+    """S1 of one sequence: q [M, nq, d], k [L, nkv, d]."""
+    nq, nkv = q.shape[1], k.shape[1]
+    return max(float((np.abs(q[:, h]) @ np.abs(k[:, h * nkv // nq]).T).max()) for h in range(nq)) / q.shape[2] ** 0.5
+
+
+def _check_cross(got, q, k, v, p_err=2.0 ** -8):
+    want = O.decoder.cross(q, k, v)
+    if not len(k):
+        assert not got.any()
+        return
+    delta = 16 * 2.0 ** -24 * _score_bound(q, k)
+    A = O.decoder.cross(q, k, np.abs(v))
+    _check_bf16(got, want, A * (2 * delta + p_err + 2.0 ** -18) * (1 + 2.0 ** -7))
+
+
+def _cross_ws(d):
+    # of any content: filled with NaN bits
+    return torch.full((Q.h3enc_op_attention_cross_workspace_bytes(d),), 255, dtype=torch.uint8, device="cuda")
+
+
+CROSS = [
+    ([1], [1], 1, 1, 64), ([1], [1], 64, 8, 128), ([1], [1024], 64, 8, 128), ([1], [5000], 12, 1, 64),
+    ([1] * 7, [0, 1, 127, 128, 129, 300, 256], 40, 2, 128), ([3, 0, 130, 1, 33], [128, 50, 0, 700, 5], 8, 8, 64),
+    ([300], [513], 4, 2, 64), ([257, 129], [640, 77], 28, 4, 128), ([40], [333], 10, 10, 128), ([700], [129], 2, 1, 128),
+    ([5, 9], [260, 1], 130, 1, 64), ([70], [200], 256, 2, 64), ([2] * 150, [3 + i % 200 for i in range(150)], 4, 1, 128),
+    ([1000], [64], 18, 18, 64), ([31], [9000], 5, 1, 128), ([513, 1], [1, 4097], 20, 4, 64)]
+
+
+@pytest.mark.parametrize("qlens,klens,nq,nkv,d", CROSS)
+def test_attention_cross(qlens, klens, nq, nkv, d):
+    g = _gen(sum(qlens) + sum(klens) + nq)
+    before, behind = 3, 5                                     # rows of no sequence; NaN on the key side
+    Tq, Tk = sum(qlens) + before + behind, sum(klens) + before + behind
+    q = _randn(g, Tq, nq * d + 16, scale=2.0)[:, 8:8 + nq * d]
+    kv = _randn(g, Tk, 2 * nkv * d + 24)
+    kv[:before] = float("nan")
+    kv[Tk - behind:] = float("nan")
+    k, v = kv[:, :nkv * d], kv[:, nkv * d + 8:2 * nkv * d + 8]
+    o = torch.full((Tq, nq * d + 8), 7.0, device="cuda", dtype=torch.bfloat16)
+    cu_q, cu_k = (_i32(before + np.concatenate([[0], np.cumsum(x)])) for x in (qlens, klens))
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ws = _cross_ws(d)
+    Q.h3enc_op_attention_cross(q, k, v, o[:, :nq * d], nq, nkv, d, ws, cu_q, cu_k, status)
+    assert int(status.item()) == 0
+    assert (o[:before] == 7).all() and (o[Tq - behind:] == 7).all() and (o[:, nq * d:] == 7).all()
+    qf, kf, vf = _f64(q).reshape(Tq, nq, d), _f64(k).reshape(Tk, nkv, d), _f64(v).reshape(Tk, nkv, d)
+    got = _f64(o[:, :nq * d]).reshape(Tq, nq, d)
+    a = b = before
+    for m, n in zip(qlens, klens):
+        if m:
+            _check_cross(got[a:a + m], qf[a:a + m], kf[b:b + n], vf[b:b + n])
+        a, b = a + m, b + n
+    # again, on another stream, in a workspace that holds the last call's: the same bits
+    again = torch.zeros(Tq, nq * d, device="cuda", dtype=torch.bfloat16)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        Q.h3enc_op_attention_cross(q, k, v, again, nq, nkv, d, ws, cu_q, cu_k)
+    side.synchronize()
+    live = slice(before, Tq - behind)
+    assert torch.equal(again[live], o[live, :nq * d])
+
+
+def test_attention_cross_of_one_sequence_needs_no_offsets():
+    g = _gen(1)
+    q, kv = _randn(g, 50, 256), _randn(g, 200, 256)
+    a, b = (torch.zeros(50, 256, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    Q.h3enc_op_attention_cross(q, kv[:, :128], kv[:, 128:], a, 4, 2, 64, _cross_ws(64))
+    Q.h3enc_op_attention_cross(q, kv[:, :128], kv[:, 128:], b, 4, 2, 64, _cross_ws(64), _i32([0, 50]), None)
+    assert torch.equal(a, b)
+    _check_cross(_f64(a).reshape(50, 4, 64), _f64(q).reshape(50, 4, 64), _f64(kv[:, :128]).reshape(200, 2, 64),
+                 _f64(kv[:, 128:]).reshape(200, 2, 64))
+    Q.h3enc_op_attention_cross(q, kv[:0, :128], kv[:0, 128:], a, 4, 2, 64, _cross_ws(64))       # no states at all
+    assert not a.any()
+    Q.h3enc_op_attention_cross(q[:0], kv[:, :128], kv[:, 128:], a[:0], 4, 2, 64, _cross_ws(64))
+
+
+def test_attention_cross_infinite_and_masked_values():
+    """An infinite value where every weight is above 0 is an infinite output of that column and head; a score of -inf
+    is a weight of 0; NaN and infinities of another sequence reach nothing."""
+    g = _gen(2)
+    L, d = 300, 64
+    q, k, v = _randn(g, 8, d), _randn(g, L + 200, d), _randn(g, L + 200, d)
+    k[L:], v[L:] = float("nan"), float("inf")
+    v[17, 5] = float("inf")
+    v[200, 6] = float("-inf")
+    o = torch.zeros(8, d, device="cuda", dtype=torch.bfloat16)
+    Q.h3enc_op_attention_cross(q, k, v, o, 1, 1, d, _cross_ws(d), _i32([0, 8, 8]), _i32([0, L, L + 200]))
+    assert (o[:, 5] == float("inf")).all() and (o[:, 6] == float("-inf")).all()
+    rest = [i for i in range(d) if i not in (5, 6)]
+    clean = v[:L].clone()
+    clean[:, 5:7] = 0
+    want = O.decoder.cross(_f64(q)[:, None], _f64(k[:L])[:, None], _f64(clean)[:, None])[:, 0]
+    assert np.abs(_f64(o)[:, rest] - want[:, rest]).max() < 2.0 ** -6
+    # keys that every query scores -inf: the first tile, and a part of the last
+    q2, k2 = q.abs() + 0.5, k[:L].clone()
+    k2[:140, 0], k2[290:, 0] = float("-inf"), float("-inf")
+    Q.h3enc_op_attention_cross(q2, k2, clean, o, 1, 1, d, _cross_ws(d))
+    _check_cross(_f64(o)[:, None], _f64(q2)[:, None], _f64(k2[140:290])[:, None], _f64(clean[140:290])[:, None])
+
+
+def test_attention_cross_far_apart_scores():
+    """One key far above the others, in the first, a middle and the last tile: the raised maximum and the joined parts."""
+    g = _gen(3)
+    L, d = 2000, 128
+    q, v = _randn(g, 16, d), _randn(g, L, d)
+    for at in (0, 1000, L - 1):
+        k = _randn(g, L, d)
+        k[at] = (q[3].float() * 20).to(torch.bfloat16)
+        o = torch.zeros(16, d, device="cuda", dtype=torch.bfloat16)
+        Q.h3enc_op_attention_cross(q, k, v, o, 1, 1, d, _cross_ws(d))
+        _check_cross(_f64(o)[:, None], _f64(q)[:, None], _f64(k)[:, None], _f64(v)[:, None])
+
+
+@pytest.mark.parametrize("cu_q,cu_k", [([0, 5, 3, 8], [0, 10, 20, 30]), ([0, 3, 5, 8], [0, 20, 10, 30]), ([0, 3, 5, 9], [0, 10, 20, 30]),
+                                       ([-1, 3, 5, 8], [0, 10, 20, 30]), ([0, 3, 5, 8], [0, 10, 20, 2 ** 31 - 1]),
+                                       ([2 ** 31 - 1, -5, 8, 8], [9, 9, -9, 30])])
+def test_attention_cross_reports_bad_offsets(cu_q, cu_k):
+    g = _gen(4)
+    q, k = _randn(g, 8, 128), _randn(g, 30, 128)
+    o = torch.full((10, 128), 7.0, device="cuda", dtype=torch.bfloat16)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    Q.h3enc_op_attention_cross(q, k, k, o[:8], 2, 2, 64, _cross_ws(64), _i32(cu_q), _i32(cu_k), status)
+    assert int(status.item()) == 2 and (o[8:] == 7).all()
+    # the sequences whose offsets are sound are right
+    if cu_q == [0, 3, 5, 8]:
+        assert np.isfinite(_f64(o[:8])).all()
+        _check_cross(_f64(o[:3]).reshape(3, 2, 64), _f64(q[:3]).reshape(3, 2, 64), *(_f64(k[:cu_k[1]]).reshape(-1, 2, 64),) * 2)
+
+
+def test_attention_cross_captured_and_replayed_with_other_lengths():
+    g = _gen(5)
+    nq, nkv, d = 8, 2, 128
+    q, kv = _randn(g, 100, nq * d), _randn(g, 1500, 2 * nkv * d)
+    k, v = kv[:, :nkv * d], kv[:, nkv * d:]
+    o = torch.zeros(100, nq * d, device="cuda", dtype=torch.bfloat16)
+    cu_q, cu_k, ws = _i32([0, 100, 100]), _i32([0, 1500, 1500]), _cross_ws(d)
+    Q.h3enc_op_attention_cross(q, k, v, o, nq, nkv, d, ws, cu_q, cu_k)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        Q.h3enc_op_attention_cross(q, k, v, o, nq, nkv, d, ws, cu_q, cu_k)
+    for a, b in (([0, 100, 100], [0, 1500, 1500]), ([0, 1, 100], [0, 1, 1500]), ([0, 60, 61], [0, 700, 700])):
+        cu_q.copy_(_i32(a))
+        cu_k.copy_(_i32(b))
+        o.fill_(3.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        for i in range(2):
+            s, e = slice(a[i], a[i + 1]), slice(b[i], b[i + 1])
+            if a[i] < a[i + 1]:
+                _check_cross(_f64(o[s]).reshape(-1, nq, d), _f64(q[s]).reshape(-1, nq, d), _f64(k[e]).reshape(-1, nkv, d),
+                             _f64(v[e]).reshape(-1, nkv, d))
+        assert (o[a[2]:] == 3).all()
+
+
+# ---------------------------------------------------------------- attention behind shared prefixes
+
+def _fill(cache, table, lens, k, v):
+    """Stores k, v [n][L, nkv, d] (float) through torch; returns the values the cache stands for."""
+    kp, vp, ks, vs = cache.tensors
+    page, out = cache.page_size, []
+    for b, n in enumerate(lens):
+        got = []
+        for pool, x, sc in ((kp, k[b], ks), (vp, v[b], vs)):
+            x = x[:n].float()
+            x = x.to(torch.bfloat16) if sc is None else (x / sc[:, None]).clamp(-448, 448).to(torch.float8_e4m3fn)
+            i = torch.arange(n, device="cuda")
+            _raw(pool)[table[b, i // page].long(), :, i % page] = _raw(x)
+            got.append(_f64(x) * (1.0 if sc is None else _f64(sc)[:, None]))
+        out.append(got)
+    return out
+
+
+SHARED = [
+    # sequences of each group, lengths of the prefixes, own lengths
+    ([1], [1], [0], 1, 1, 64, BF16, 16), ([1], [1000], [1], 64, 8, 128, BF16, 64), ([4], [129], [20, 0, 60, 1], 64, 8, 128, BF16, 128),
+    ([1, 0, 3, 2], [700, 50, 0, 127], [5, 100, 3, 0, 40, 260], 4, 2, 64, BF16, 16), ([40], [640], [i * 7 for i in range(40)], 8, 1, 128, BF16, 32),
+    ([2], [5000], [3, 9], 130, 1, 64, BF16, 256), ([17], [300], [1] * 17, 40, 2, 128, BF16, 64), ([70], [256], [2] * 70, 7, 7, 64, BF16, 16),
+    ([1], [1], [0], 2, 1, 64, E4M3, 16), ([1], [1000], [1], 64, 8, 128, E4M3, 64), ([5], [257], [20, 0, 60, 1, 300], 28, 4, 128, E4M3, 128),
+    ([1, 0, 3, 2], [700, 50, 0, 127], [5, 100, 3, 0, 40, 260], 4, 2, 64, E4M3, 32), ([40], [900], [i * 3 for i in range(40)], 20, 4, 64, E4M3, 256),
+    ([33], [4000], [10] * 33, 12, 1, 128, E4M3, 16)]
+
+
+@pytest.mark.parametrize("groups,plens,lens,nq,nkv,d,dtype,page", SHARED)
+def test_attention_decode_shared(groups, plens, lens, nq, nkv, d, dtype, page):
+    g = _gen(sum(plens) + sum(lens) + nq)
+    n, rows = len(lens), np.concatenate([[0], np.cumsum(groups)])
+    assert rows[-1] == n
+    max_prefix, max_len = max(plens), max(max(lens), 1)
+    pcols, cols = -(-max_prefix // page), -(-max_len // page)
+    pages = len(plens) * pcols + n * cols + 2
+    cache = _pool(g, pages, nkv, page, d, dtype, apart=16)
+    ids = torch.randperm(pages, device="cuda", generator=g).to(torch.int32)
+    ptable = torch.cat([ids[:len(plens) * pcols].view(len(plens), pcols), ids.new_full((len(plens), 2), -1)], 1).contiguous()
+    table = ids[len(plens) * pcols:][:n * cols].view(n, cols).contiguous()
+
+    def tokens(ls):
+        return [torch.randn(x, nkv, d, device="cuda", generator=g) for x in ls], [torch.randn(x, nkv, d, device="cuda", generator=g) for x in ls]
+
+    pre, mine = _fill(cache, ptable, plens, *tokens(plens)), _fill(cache, table, lens, *tokens(lens))
+    q = _randn(g, n, nq * d + 8, scale=2.0)[:, :nq * d]
+    o = torch.full((n + 1, nq * d + 8), 7.0, device="cuda", dtype=torch.bfloat16)
+    w_in = torch.rand(n, max_len + 3, device="cuda", generator=g)
+    w_out = torch.full_like(w_in, -5.0)
+    ws = torch.zeros(Q.h3enc_op_attention_decode_shared_workspace_bytes(n, nq, max_len, True), dtype=torch.uint8, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    prefix_rows = _i32(rows) if len(groups) > 1 else None
+    args = (cache, ptable, _i32(plens), max_prefix, table, _i32(lens), nq, max_len, ws)
+    Q.h3enc_op_attention_decode_shared(q, o[:n, :nq * d], *args, prefix_rows=prefix_rows, weight_in=w_in, weight_out=w_out,
+                                       status=status)
+    assert int(status.item()) == 0
+    assert (o[n:] == 7).all() and (o[:, nq * d:] == 7).all()
+    qf, got = _f64(q).reshape(n, nq, d), _f64(o[:n, :nq * d]).reshape(n, nq, d)
+    p_err = 2.0 ** -8 if dtype == BF16 else 2.0 ** -11
+    m = nq // nkv
+    for b in range(n):
+        (pk, pv), (k, v) = pre[int(np.searchsorted(rows, b, side="right")) - 1], mine[b]
+        want, p = O.decoder.attend_prefix(qf[b], pk, pv, k, v)
+        if not len(pk) + len(k):
+            assert not got[b].any()
+            continue
+        delta = 16 * 2.0 ** -24 * _score_bound(qf[b][None], np.concatenate([pk, k]))
+        A = O.decoder.attend_prefix(qf[b], pk, np.abs(pv), k, np.abs(v))[0]
+        light = 2.0 ** -37 * np.abs(pv).sum(0).repeat(m, 0) if dtype == E4M3 and len(pk) else 0.0
+        _check_bf16(got[b], want, (A * (2 * delta + p_err + 2.0 ** -16 + 2.0 ** -18) + light) * (1 + 2.0 ** -7))
+        w = _f64(w_out[b])
+        assert (w[lens[b]:] == -5).all()
+        p = p.sum(0)
+        assert (np.abs(w[:lens[b]] - _f64(w_in[b])[:lens[b]] - p) <= (2 * delta + 2.0 ** -18) * p + 2.0 ** -22 * (1 + p)).all()
+    # without weights, again, on another stream: the same bits
+    again = torch.zeros(n, nq * d, device="cuda", dtype=torch.bfloat16)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        Q.h3enc_op_attention_decode_shared(q, again, *args, prefix_rows=prefix_rows)
+    side.synchronize()
+    assert torch.equal(again, o[:n, :nq * d])
+
+
+def test_attention_decode_shared_without_prefixes_is_attention_decode():
+    g = _gen(11)
+    n, nq, nkv, d, page = 5, 8, 2, 128, 16
+    cache = _pool(g, 40, nkv, page, d, BF16)
+    table, lens = _table(g, n, 8, 40), [100, 0, 1, 128, 33]
+    _fill(cache, table, lens, *([torch.randn(x, nkv, d, device="cuda", generator=g) for x in lens] for _ in range(2)))
+    q = _randn(g, n, nq * d)
+    a, b, c = (torch.zeros(n, nq * d, device="cuda", dtype=torch.bfloat16) for _ in range(3))
+    ws = torch.zeros(Q.h3enc_op_attention_decode_shared_workspace_bytes(n, nq, 128), dtype=torch.uint8, device="cuda")
+    Q.h3enc_op_attention_decode(q, a, cache, table, _i32(lens), nq, 128, ws)
+    Q.h3enc_op_attention_decode_shared(q, b, cache, table[:0], _i32([]), 0, table, _i32(lens), nq, 128, ws)
+    assert torch.equal(a, b)
+    # sequences of no group, and a group whose prefix is empty, have none either
+    Q.h3enc_op_attention_decode_shared(q, c, cache, table[:2], _i32([0, 0]), 64, table, _i32(lens), nq, 128, ws,
+                                       prefix_rows=_i32([1, 2, 4]))
+    assert torch.equal(a, c)
+    Q.h3enc_op_attention_decode(q, c, cache, table, _i32(lens), nq, 128, ws)      # the workspace serves both
+    assert torch.equal(a, c)
+
+
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+def test_attention_decode_shared_reports_bad_pages_and_lengths(dtype):
+    """A page outside the cache reads as zero keys and values; a length outside its bound is clamped into it."""
+    g = _gen(12)
+    n, nq, nkv, d, page = 3, 4, 2, 64, 16
+    cache = _pool(g, 30, nkv, page, d, dtype)
+    ids = torch.randperm(30, device="cuda", generator=g).to(torch.int32)
+    ptable, table = ids[:8].view(1, 8).contiguous(), ids[8:14].view(3, 2).contiguous()
+    pk, pv = ([torch.randn(120, nkv, d, device="cuda", generator=g)] for _ in range(2))
+    k, v = ([torch.randn(20, nkv, d, device="cuda", generator=g) for _ in range(n)] for _ in range(2))
+    (pk, pv), = _fill(cache, ptable, [120], pk, pv)
+    own = _fill(cache, table, [20] * n, k, v)
+    q, o = _randn(g, n, nq * d), torch.zeros(n, nq * d, device="cuda", dtype=torch.bfloat16)
+    ws = torch.zeros(Q.h3enc_op_attention_decode_shared_workspace_bytes(n, nq, 32), dtype=torch.uint8, device="cuda")
+
+    def check(bad_page, prefix_len, max_prefix):
+        t = ptable.clone()
+        if bad_page is not None:
+            t[0, 2] = bad_page
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        Q.h3enc_op_attention_decode_shared(q, o, cache, t, _i32([prefix_len]), max_prefix, table, _i32([20] * n), nq, 32, ws,
+                                           status=status)
+        assert int(status.item()) == 2
+        length = min(max(prefix_len, 0), max_prefix)
+        kk, vv = pk[:length].copy(), pv[:length].copy()
+        if bad_page is not None:
+            kk[32:48], vv[32:48] = 0, 0
+        for b in range(n):
+            want, _ = O.decoder.attend_prefix(_f64(q[b]).reshape(nq, d), kk, vv, *own[b])
+            assert np.abs(_f64(o[b]).reshape(nq, d) - want).max() <= 2.0 ** -6
+
+    for page_no in (-1, 30, 2 ** 31 - 1, -(2 ** 31)):
+        check(page_no, 120, 120)
+    check(None, 121, 120)
+    check(None, -3, 120)
+    check(None, 2 ** 31 - 1, 33)
+
+
+# ---------------------------------------------------------------- a run of them together
+
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+def test_decode_steps_of_a_decoder_that_reads_an_encoder(dtype):
+    """Three steps of one captured graph: append (rotated by place), self attention behind a shared prompt, cross attention to the
+    states of each sequence's own prompt.  The oracle follows the bf16 tensors between the calls."""
+    g = _gen(13)
+    n, nq, nkv, d, page, P = 6, 8, 2, 64, 16, 200
+    plens, start = [P, 77], [0, 3, 15, 16, 40, 1]
+    cache = _pool(g, 2 * 13 + n * 4, nkv, page, d, dtype)
+    ids = torch.randperm(2 * 13 + n * 4, device="cuda", generator=g).to(torch.int32)
+    ptable, table = ids[:26].view(2, 13).contiguous(), ids[26:].view(n, 4).contiguous()
+    rnd = lambda ls: [torch.randn(x, nkv, d, device="cuda", generator=g) for x in ls]   # noqa: E731
+    pre, own = _fill(cache, ptable, plens, rnd(plens), rnd(plens)), _fill(cache, table, start, rnd(start), rnd(start))
+    klens = [1, 130, 77, 512, 0, 300]
+    states = _randn(g, sum(klens), 2 * nkv * d)
+    cu_k = np.concatenate([[0], np.cumsum(klens)])
+    rope_args, rope = _rope("yarn", d)
+    qkv, lens = torch.zeros(n, (nq + 2 * nkv) * d, device="cuda", dtype=torch.bfloat16), _i32(start)
+    o1, o2 = (torch.zeros(n, nq * d, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    rows, places = _i32([0, 4, 6]), torch.zeros(1, n, dtype=torch.int32, device="cuda")
+    ws = torch.zeros(Q.h3enc_op_attention_decode_shared_workspace_bytes(n, nq, 64), dtype=torch.uint8, device="cuda")
+    ws2, cuq, cuk = _cross_ws(d), _i32(list(range(n + 1))), _i32(cu_k)
+    behind = _i32([P] * 4 + [77] * 2)
+    plen_t, status = _i32(plens), torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def step():
+        lens.add_(1)
+        places[0].copy_(lens + behind - 1)         # a token's position counts its prefix
+        Q.h3enc_op_rope_append(qkv, n, nq, nkv, d, None, None, 0.0, rope, places[0], qkv[:, :nq * d], cache=cache, page_table=table,
+                               seq_lens=lens, max_len=64, status=status)
+        Q.h3enc_op_attention_decode_shared(qkv[:, :nq * d], o1, cache, ptable, plen_t, P, table, lens, nq, 64, ws, prefix_rows=rows,
+                                           status=status)
+        Q.h3enc_op_attention_cross(o1, states[:, :nkv * d], states[:, nkv * d:], o2, nq, nkv, d, ws2, cuq, cuk, status)
+
+    step()                                         # (warm-up outside the capture; undone)
+    lens.copy_(_i32(start))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    lens.copy_(_i32(start))
+    w, magnitude = O.decoder.frequencies(**{k: x for k, x in rope_args.items()})
+    sf = _f64(states).reshape(-1, 2, nkv, d)
+    p_err = 2.0 ** -8 if dtype == BF16 else 2.0 ** -11
+    for i in range(3):
+        rowsin = _randn(g, n, (nq + 2 * nkv) * d)
+        qkv.copy_(rowsin)
+        graph.replay()
+        x = _f64(rowsin).reshape(n, nq + 2 * nkv, d)
+        kp, vp, ks, vs = cache.tensors
+        for b in range(n):
+            at = start[b] + i
+            angle = ((plens[0 if b < 4 else 1] + at) * w)[None]
+            want_q = O.decoder.rotate(x[b:b + 1, :nq], angle, magnitude, False)[0]
+            q = _f64(qkv[b, :nq * d]).reshape(nq, d)
+            _check_bf16(q, want_q, 2.0 ** -19 * _pair_length(want_q, d, False))
+            new = [_f64(_raw(t)[table[b, at // page].long(), :, at % page].view(t.dtype)) * (1 if sc is None else _f64(sc)[:, None])
+                   for t, sc in ((kp, ks), (vp, vs))]
+            want_k = O.decoder.rotate(x[b:b + 1, nq:nq + nkv], angle, magnitude, False)[0]
+            step_size = 2.0 ** -8 * np.abs(want_k) if dtype == BF16 else 2.0 ** -4 * np.abs(want_k) + 2.0 ** -10 * _f64(ks)[:, None]
+            assert (np.abs(new[0] - want_k) <= step_size * (1 + 2.0 ** -10) + 2.0 ** -19 * _pair_length(want_k, d, False)).all()
+            own[b] = [np.concatenate([old, y[None]]) for old, y in zip(own[b], new)]
+            pk, pv = pre[0 if b < 4 else 1]
+            want, _ = O.decoder.attend_prefix(q, pk, pv, *own[b])
+            A = O.decoder.attend_prefix(q, pk, np.abs(pv), own[b][0], np.abs(own[b][1]))[0]
+            delta = 16 * 2.0 ** -24 * _score_bound(q[None], np.concatenate([pk, own[b][0]]))
+            got = _f64(o1[b]).reshape(nq, d)
+            _check_bf16(got, want, A * (2 * delta + p_err + 2.0 ** -15))
+            s = sf[cu_k[b]:cu_k[b + 1]]
+            _check_cross(_f64(o2[b:b + 1]).reshape(1, nq, d), got[None], s[:, 0], s[:, 1])
+    assert int(status.item()) == 0
