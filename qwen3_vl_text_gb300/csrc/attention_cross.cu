@@ -8,18 +8,23 @@
 // (token, head of the group) pairs, 128 / group tokens at a time, fetched as one box of a tensor map of q as [token][kv
 // head][head of the group][element].  One token of a group of 8 heads is 8 rows of one tile, 4096 tokens are 256 full ones.
 //
-// Work: an item is a pair of row tiles (or a last single one) of one kv head of one segment, in steps of 128 keys.  The
-// steps of all items are laid end to end, a step of a pair counted twice, and cut into one equal run per CTA, one CTA per
-// SM, whatever the lengths are (read on the device).  A run may end inside an item, whose parts (unnormalised output,
-// running maximum and sum, fp32) go to the workspace and are joined in key order by a second launch: the
-// result does not depend on timing.
-//   warp 0       TMA: K, Q_A, Q_B, V, K, V, ... (page numbers looked up a batch of tiles ahead)
-//   warp 1       TMEM; tcgen05.mma from one thread: S_t = Q_t K_j^T, O_t += P_t V_j, the two tiles in turn, so that
-//                the tensor core works on one tile while the other's softmax runs; P read from TMEM
-//   warps 2-5    softmax of tile A, 6-9 of tile B: a thread per row; the maximum is raised lazily
-//   warps 10-13  (e4m3 pages) convert raw tiles to f16 ones
+// Work: an item is a pair of row tiles A and B, or a last single one, of one kv head of one segment, in steps of 128 keys.  A
+// pair shares every step; a single tile is run as A and B too, A on the even steps and B on the odd ones, and their
+// results are merged at the end.  Items weigh 2 per step (single 1), and FIXED for their beginning and end; their weights are laid end
+// to end and cut into one equal run per CTA, one CTA per SM, whatever the lengths are (read on the device); a step goes to the run
+// that holds its first weight.  A run may end inside an item, whose parts (unnormalised output, running
+// maximum and sum, fp32) go to the workspace and are joined in key order by a second launch: the result does not depend
+// on timing.
+//   warps 0-3    softmax of tile A, 4-7 of tile B: a thread per row; the running maximum is raised lazily; an item's end:
+//                O / l -> bf16 -> global, or the part
+//   warp 8       TMA: K, Q_A, Q_B, V, K, V, ... (page numbers looked up a batch of tiles ahead)
+//   warps 9, 10  tcgen05.mma, from one thread each: S_t = Q_t K_j^T and O_t += P_t V_j of tile A and of tile B; the tensor
+//                cores work on one tile while the other's softmax runs; P is read from TMEM (allocated by warp 8)
+//   warp 11      finds the items of the run and hands them to the others through a ring
+//   warps 12-15  (e4m3 pages) convert raw tiles to f16 ones
 // P enters the value product in bf16 (off by up to 2^-8 of each weight, as the rounded output is of itself; a second product for
-// the remainder would halve the rate where the tensor core bounds); e4m3 pages: in f16 (2^-11), times 2^13, as f16 ends at 2^-24.  Rows of no token are computed on what lies in shared memory and never stored.
+// the remainder would halve the rate where the tensor core bounds); e4m3 pages: in f16 (2^-11), times 2^13, as f16 ends at
+// 2^-24.  Rows of no token are computed on what lies in shared memory and never stored.
 #include <algorithm>
 #include <atomic>
 #include <climits>
@@ -36,10 +41,38 @@ namespace {
 constexpr int TQ = 128, TK = 128;
 enum { ROWS = 0, PAGES = 1, PAGES8 = 2 };   // keys: packed rows, bf16 pages, e4m3 pages
 
+// mbar_wait in fewer instructions: the code of this kernel's roles competes for the SM's instruction cache (with waits, masks and
+// copies of loops written out at every place, 96 KB, every role waited for instructions).
+__device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, const volatile int *abort) {
+    const uint32_t a = smem_u32(bar);
+    bool done = mbar_try_wait(a, parity);
+    const long long t0 = done ? 0 : clock64();
+    #pragma unroll 1
+    while (!done) {
+        if (*abort || clock64() - t0 > kSpinLimitCycles) break;
+        done = mbar_try_wait(a, parity);
+    }
+    return done;
+}
+
+// An item as one warp hands it to the others.
+struct __align__(16) Item {
+    int row0, n_a, n_b;     // row of its first token, tokens of its tiles (n_b 0: single)
+    int head, chunk;        // kv head and share of its group
+    int j0, j1, len, key0;  // steps of this run [j0, j1) (none: the run is over), keys; their first row, or the segment
+    int whole, parts;       // all steps are this run's; parts of the item if its first is this run's and others follow, else 0
+    int pos;                // key tiles of the run before it
+    // steps of row tile t: the first, and the distance of the next
+    __device__ __forceinline__ int first(int t) const { return j0 + (n_b ? 0 : t); }
+    __device__ __forceinline__ int stride() const { return n_b ? 1 : 2; }
+    __device__ __forceinline__ bool active(int t) const { return first(t) < j1; }
+};
+constexpr int ITEMS = 8;
+
 template <int D, int MODE>
 struct Shape {
     static constexpr bool F8 = MODE == PAGES8;
-    static constexpr int THREADS = F8 ? 448 : 320;
+    static constexpr int THREADS = F8 ? 512 : 384;
     static constexpr int ATOM = TQ * 128;                  // 64 columns of a 128-row tile
     static constexpr int TILE = TK * D * 2;                // one operand tile
     static constexpr int NS = (D == 128 ? 2 : 4) / (F8 ? 2 : 1);   // K tiles, and V tiles, held
@@ -50,8 +83,12 @@ struct Shape {
     static constexpr int OFF_V = OFF_K + NS * TILE;
     static constexpr int OFF_RAW = OFF_V + NS * TILE;
     static constexpr int OFF_SEG = OFF_RAW + RS * RAW;     // pre, cq, ck
-    static constexpr int OFF_BAR = OFF_SEG + 3 * 4 * (kMaxSeqs + 4);
-    static constexpr int BARS = 4 * NS + 13 + 2 * RS;
+    static constexpr int OFF_ITEM = OFF_SEG + 3 * 4 * (kMaxSeqs + 4);  // ring of items
+    static constexpr int OFF_ML = OFF_ITEM + ITEMS * (int)sizeof(Item);   // [128] (m, l) of tile B's share of a single tile's rows
+    static constexpr int OFF_OUT = OFF_ML + 128 * 8;       // 32 rows x 64 bytes of output per softmax warp
+    static constexpr int OFF_BAR = OFF_OUT + (MODE == ROWS ? 8 * 2048 : 0);
+    static constexpr int BARS = 4 * NS + 18 + 2 * ITEMS + 2 * RS;
+    static constexpr int READERS = 11 + (F8 ? 4 : 0);      // warps that read an item
     static constexpr int BYTES = OFF_BAR + BARS * 8 + 128 + 1024;   // + alignment of the base
     static constexpr float UP = F8 ? 8192.f : 1.f;         // weights, and so l and o, are held times this
     static constexpr float UP_LOG2 = F8 ? 13.f : 0.f;
@@ -62,6 +99,7 @@ struct Shape {
 struct Args {
     AttentionCross p;
     int group, gc, chunks, tok;   // q heads per kv head; rows of a token in a tile, tiles' shares of a group; tokens of a tile
+    unsigned inv_gc;              // ceil(2^16 / gc): row * inv_gc >> 16 = row / gc for row < 128
     int box_shift;                // log2 of the places of a page that one box covers
     float scale_log2;
     float *part;                  // [cta][slot][tile][D][128] partial outputs, unnormalised
@@ -117,6 +155,35 @@ __device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *m, uin
         : "memory");
 }
 
+// Hint: bring the box at these element coordinates into L2.
+__device__ __forceinline__ void tma_prefetch_4d(const CUtensorMap *m, int32_t x, int32_t y, int32_t z, int32_t w) {
+    asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];" ::"l"(
+                     reinterpret_cast<uint64_t>(m)),
+                 "r"(x), "r"(y), "r"(z), "r"(w)
+                 : "memory");
+}
+// tcgen05.mma with descriptors given by their low words (address and leading offset); the high words are constant.
+// One addition per operand (with whole descriptors 2% slower).
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);   // stride 1024 bytes, version 1, 128-byte swizzle
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+        "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
+        "r"(a_lo), "r"(b_lo), "r"(idesc), "r"((uint32_t)accumulate), "n"(kDescHi)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc, bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\t"
+        "mov.b64 db, {%2, %5};\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d),
+        "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"((uint32_t)accumulate), "n"(kDescHi)
+        : "memory");
+}
+
 // The segments, in shared memory: tokens [cq[s], cq[s + 1]), keys [ck[s], ck[s + 1]) or (pages) the first ck[s] of s;
 // pre[s]: weight of the segments before s.
 struct Segments {
@@ -128,17 +195,30 @@ __device__ __forceinline__ int seg_keys(const Segments &g, int s) {
 }
 __device__ __forceinline__ int seg_tokens(const Segments &g, int s) { return max(g.cq[s + 1] - g.cq[s], 0); }
 
-// Walks the items of a run [w, end) of weights.
+constexpr int FIXED = 2;   // weight of an item's beginning and end (a pair's step: 2)
+
+// Walks the items of a run [w0, end) of weights.
 template <int MODE>
 struct Walk {
-    int w, end, s;
-    // the item: its segment s, unit, first token in the segment, tokens of its tiles (n_b 0: single), key tiles of
-    // the whole item and of this run [j0, j1), keys, and the weights [start, start + weight * steps)
-    int u, tok0, n_a, n_b, steps, j0, j1, len, start, weight;
+    // the segment: index, keys, steps, tokens, tiles
+    int s, len, steps, n, tiles;
+    // the item: kv head and share of its group, block of two tiles, first token in the segment, tokens of its tiles
+    // (n_b 0: single), steps of this run [j0, j1), first weight, weight of a step - 1
+    int head, chunk, blk, tok0, n_a, n_b, j0, j1, start, shift;
+    int w0, end;
 
-    __device__ __forceinline__ void begin(int w0, int w1, const Segments &g, int n_segs) {
-        w = w0;
-        end = w1;
+    __device__ __forceinline__ void load(const Segments &g, int tok) {
+        len = seg_keys<MODE>(g, s);
+        steps = (len + TK - 1) / TK;
+        n = seg_tokens(g, s);
+        tiles = (n + tok - 1) / tok;
+    }
+    __device__ __forceinline__ void begin(int first, int behind, const Segments &g, int n_segs, int tok, int chunks) {
+        w0 = first;
+        end = behind;
+        start = behind;
+        j1 = -1;
+        if (first >= behind) return;
         int lo = 0, hi = n_segs;   // the s with pre[s] <= w0 < pre[s + 1]
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
@@ -146,29 +226,44 @@ struct Walk {
             else hi = mid;
         }
         s = lo;
+        load(g, tok);
+        int off = w0 - g.pre[s];
+        const int pair = 2 * steps + FIXED, unit = (tiles >> 1) * pair + (tiles & 1) * (steps + FIXED), u = off / unit;
+        off -= u * unit;
+        head = u / chunks;
+        chunk = u - head * chunks;
+        blk = min(off / pair, tiles >> 1);
+        start = w0 - (off - blk * pair);
     }
-    __device__ __forceinline__ bool next(const Segments &g, int tok) {
-        while (w < end) {
-            while (g.pre[s + 1] <= w) ++s;
-            len = seg_keys<MODE>(g, s);
-            steps = (len + TK - 1) / TK;
-            const int n = seg_tokens(g, s), tiles = (n + tok - 1) / tok, pairs = tiles >> 1;
-            int off = w - g.pre[s];
-            u = off / (tiles * steps);
-            off -= u * tiles * steps;
-            const int blk = min(off / (2 * steps), pairs);
-            weight = blk < pairs ? 2 : 1;
-            start = w - (off - blk * 2 * steps);
+    __device__ __forceinline__ int weight() const { return (steps << shift) + FIXED; }
+    __device__ __forceinline__ bool next(const Segments &g, int tok, int chunks, int nkv) {
+        while (true) {
+            if (j1 >= 0 && start < end) {   // on from the item before
+                start += weight();
+                if (start >= end) return false;
+                if (2 * ++blk >= tiles) {
+                    blk = 0;
+                    if (++chunk == chunks) {
+                        chunk = 0;
+                        if (++head == nkv) {
+                            head = 0;
+                            do ++s;
+                            while (g.pre[s + 1] == g.pre[s]);
+                            load(g, tok);
+                        }
+                    }
+                }
+            }
+            if (start >= end) return false;
+            shift = 2 * blk + 1 < tiles ? 1 : 0;
             tok0 = blk * 2 * tok;
             n_a = min(tok, n - tok0);
-            n_b = weight == 2 ? min(tok, n - tok0 - tok) : 0;
-            const int stop = min(start + weight * steps, end);
-            j0 = (w - start + weight - 1) / weight;
-            j1 = (stop - start + weight - 1) / weight;
-            w = stop;
+            n_b = shift ? min(tok, n - tok0 - tok) : 0;
+            // step j belongs to the run that holds weight start + (j << shift)
+            j0 = max((w0 - start + shift) >> shift, 0);
+            j1 = min((end - start + shift) >> shift, steps);
             if (j0 < j1) return true;
         }
-        return false;
     }
 };
 
@@ -194,26 +289,28 @@ __global__ void __launch_bounds__(Shape<D, MODE>::THREADS, 1)
     uint8_t *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     uint8_t *sQ = smem + S::OFF_Q, *sK = smem + S::OFF_K, *sV = smem + S::OFF_V, *sRaw = smem + S::OFF_RAW;
     int *pre = reinterpret_cast<int *>(smem + S::OFF_SEG), *cq = pre + kMaxSeqs + 4, *ck = cq + kMaxSeqs + 4;
+    Item *ring = reinterpret_cast<Item *>(smem + S::OFF_ITEM);
+    float2 *ml_s = reinterpret_cast<float2 *>(smem + S::OFF_ML);
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + S::OFF_BAR);
     uint64_t *k_full = bars, *v_full = k_full + NS, *k_empty = v_full + NS, *v_empty = k_empty + NS;
     uint64_t *q_full = v_empty + NS, *q_ready = q_full + 2, *q_empty = q_ready + 2;   // [2] row tile, from here on
-    uint64_t *s_full = q_empty + 2, *p_full = s_full + 2, *pv_done = p_full + 2, *drain = pv_done + 2;
-    uint64_t *raw_full = drain + 1, *raw_empty = raw_full + RS;
+    uint64_t *s_full = q_empty + 2, *p_full = s_full + 2, *pv_done = p_full + 2, *l_full = pv_done + 2, *o_free = l_full + 1;   // [1], [1]
+    uint64_t *turn = o_free + 1, *drain = turn + 2, *item_full = drain + 2, *item_empty = item_full + ITEMS;
+    uint64_t *raw_full = item_empty + ITEMS, *raw_empty = raw_full + RS;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(raw_empty + RS);
     volatile int *abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
-    int *s_warp = reinterpret_cast<int *>(tmem_slot + 2);   // [14] scan of the warps' sums
+    int *s_warp = reinterpret_cast<int *>(tmem_slot + 2);   // [20] scan of the warps' sums
 
     const AttentionCross &p = a.p;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int units = p.nkv * a.chunks;
 
     pdl_trigger();
     if (tid == 0) {
         for (int i = 0; i < NS; ++i) {
             mbar_init(k_full + i, F8 ? 4 : 1);
             mbar_init(v_full + i, F8 ? 4 : 1);
-            mbar_init(k_empty + i, 1);
-            mbar_init(v_empty + i, 1);
+            mbar_init(k_empty + i, 2);
+            mbar_init(v_empty + i, 2);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(q_full + i, 1);
@@ -222,8 +319,15 @@ __global__ void __launch_bounds__(Shape<D, MODE>::THREADS, 1)
             mbar_init(s_full + i, 1);
             mbar_init(p_full + i, 4);
             mbar_init(pv_done + i, 1);
+            mbar_init(turn + i, 1);
+            mbar_init(drain + i, 1);
         }
-        mbar_init(drain, 1);
+        mbar_init(l_full, 4);
+        mbar_init(o_free, 4);
+        for (int i = 0; i < ITEMS; ++i) {
+            mbar_init(item_full + i, 1);
+            mbar_init(item_empty + i, S::READERS);
+        }
         for (int i = 0; i < RS; ++i) {
             mbar_init(raw_full + i, 1);
             mbar_init(raw_empty + i, 4);
@@ -234,14 +338,15 @@ __global__ void __launch_bounds__(Shape<D, MODE>::THREADS, 1)
         prefetch_tmap(&tmK);
         prefetch_tmap(&tmV);
     }
-    if (warp == 1) {
+    if (warp == 8) {
         tmem_alloc(tmem_slot, 512);
         tmem_relinquish();
     }
     pdl_wait();
 
     // the segments, clamped into what the call covers, and their weights: four per thread, scanned over the block
-    bool any_pair = false, any_empty = false;
+    bool any_empty = false;
+    const int units = p.nkv * a.chunks;
     {
         bool bad = false;
         for (int i = tid; i <= p.n_segs; i += S::THREADS) {
@@ -263,8 +368,8 @@ __global__ void __launch_bounds__(Shape<D, MODE>::THREADS, 1)
             n[i] = 0;
             if (s < p.n_segs) {
                 const int tokens = seg_tokens(g, s), tiles = (tokens + a.tok - 1) / a.tok, keys = seg_keys<MODE>(g, s);
-                n[i] = (keys + TK - 1) / TK * tiles * units;
-                any_pair |= tiles > 1 && keys > 0;
+                const int steps = (keys + TK - 1) / TK;
+                if (keys > 0) n[i] = units * ((tiles >> 1) * (2 * steps + FIXED) + (tiles & 1) * (steps + FIXED));
                 any_empty |= tokens > 0 && keys == 0;
                 bad |= cq[s + 1] < cq[s] || (MODE == ROWS && ck[s + 1] < ck[s]);
             }
@@ -279,7 +384,7 @@ __global__ void __launch_bounds__(Shape<D, MODE>::THREADS, 1)
             if (lane >= o) inc += v;
         }
         if (lane == 31) s_warp[warp] = inc;
-        any_pair = __syncthreads_or(any_pair);
+        __syncthreads();
         int at = inc - sum;
         for (int w = 0; w < warp; ++w) at += s_warp[w];
         #pragma unroll
@@ -294,22 +399,21 @@ __global__ void __launch_bounds__(Shape<D, MODE>::THREADS, 1)
     }
     const uint32_t tmem_base = *tmem_slot;
     const Segments g{pre, cq, ck};
-    // A run is at least a step long, whichever items there are: parts of an item are then those of consecutive CTAs.
-    const unsigned T = (unsigned)pre[p.n_segs], G = min(any_pair ? T / 2 : T, gridDim.x);
+    // A run has a step's weight at least: the parts of an item are then those of consecutive CTAs.
+    const unsigned T = (unsigned)pre[p.n_segs], G = min(T / 2, gridDim.x);
     const Runs runs(T, G);
-    const int w0 = blockIdx.x < G ? runs.first(blockIdx.x) : 0, w1 = blockIdx.x < G ? runs.first(blockIdx.x + 1) : 0;
 
     // rows without any key: zeros, or (prefixes) an empty part
     if (any_empty) {
         const auto fill = [&](int t0, int t1) {
-            const long long step = (long long)gridDim.x * S::THREADS, at = (long long)blockIdx.x * S::THREADS + tid;
-            if (MODE == ROWS) {
-                const int vecs = p.nq * D / 8;
-                for (long long i = at; i < (long long)(t1 - t0) * vecs; i += step)
-                    *reinterpret_cast<uint4 *>(p.o + (t0 + i / vecs) * p.ld_o + i % vecs * 8) = make_uint4(0, 0, 0, 0);
-            } else {
-                for (long long i = at; i < (long long)(t1 - t0) * p.nq; i += step)
-                    p.pre_ml[(long long)t0 * p.nq + i] = make_float2(-INFINITY, 0.f);
+            const int step = gridDim.x * S::THREADS / 32, at = blockIdx.x * (S::THREADS / 32) + warp;
+            for (int r = t0 + at; r < t1; r += step) {   // a row of every head per warp
+                if (MODE == ROWS) {
+                    for (int i = lane; i < p.nq * D / 8; i += 32)
+                        *reinterpret_cast<uint4 *>(p.o + r * p.ld_o + i * 8) = make_uint4(0, 0, 0, 0);
+                } else {
+                    for (int i = lane; i < p.nq; i += 32) p.pre_ml[(long long)r * p.nq + i] = make_float2(-INFINITY, 0.f);
+                }
             }
         };
         for (int s = 0; s < p.n_segs; ++s)
@@ -320,11 +424,292 @@ __global__ void __launch_bounds__(Shape<D, MODE>::THREADS, 1)
         }
     }
 
-    Walk<MODE> w;
-    w.begin(w0, w1, g, p.n_segs);
-    const auto kv_head = [&](int u) { return a.chunks == 1 ? u : u / a.chunks; };
+    // A wait that runs out, in any warp, ends the CTA: *abort lets all other waits return, and no warp waits otherwise.
+    const auto wait_on = [&](uint64_t *bar, uint32_t parity) {   // by a whole warp
+        const bool good = __all_sync(0xffffffffu, wait_bar(bar, parity, abort));
+        if (!good && lane == 0) {
+            report(p.status, ST_TIMEOUT);
+            *abort = 1;
+        }
+        return good;
+    };
+    // Items are read in the ring, where they stay until every warp has given them back.
+    const auto give_back = [&](uint32_t i) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(item_empty + i % ITEMS);
+    };
 
-    if (warp == 0) {
+    if (warp < 8) {
+        // ------------------------------------------------ softmax
+        const int t = warp >> 2, quarter = warp & 3;
+        const int r = quarter * 32 + lane;            // row of the tile = TMEM lane
+        const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
+        const uint32_t tS = tmem_base + lane_off + (uint32_t)(t * TQ);
+        const uint32_t tO = tmem_base + lane_off + (uint32_t)(256 + t * 128);
+        const int r_tok = r * a.inv_gc >> 16, r_head = r - r_tok * a.gc;
+        if (warp == 0 && lane == 0) a.desc[2 * blockIdx.x + 1] = make_int4(0, 0, 0, 0);
+        // steps and items of this row tile, steps of tile B, single items with shares of both so far (barrier phases)
+        uint32_t c = 0, items = 0, c_b = 0, shares = 0;
+        bool good = true;
+        for (uint32_t it = 0; good; give_back(it++)) {
+            if (!(good = wait_on(item_full + it % ITEMS, (it / ITEMS) & 1))) break;
+            const Item &w = ring[it % ITEMS];
+            if (w.j0 >= w.j1) break;
+            if (!w.active(t)) continue;
+            const int n_tok = t && w.n_b ? w.n_b : w.n_a;
+            const bool busy = quarter * 32 < n_tok * a.gc;   // this warp has rows of tokens
+            float scale = a.scale_log2;
+            if constexpr (F8) {
+                // q to f16 in place: a row's largest |q| goes to [2^14, 2^15): exact but for elements 2^-29 of it and smaller
+                if (!(good = wait_on(q_full + t, items & 1))) break;
+                if (busy) {
+                    const float ks = p.cache.k_scale[w.head];
+                    uint8_t *row = sQ + t * S::TILE + r * 128;
+                    const auto at = [&](int ch) {
+                        return reinterpret_cast<uint4 *>(row + (ch >> 3) * S::ATOM + (((ch & 7) ^ (r & 7)) << 4));
+                    };
+                    float top = 0.f;
+                    #pragma unroll 4
+                    for (int ch = 0; ch < D / 8; ++ch) {
+                        const uint4 x = *at(ch);
+                        const uint32_t v[4] = {x.x, x.y, x.z, x.w};
+                        #pragma unroll
+                        for (int i = 0; i < 4; ++i) top = fmax3(top, fabsf(bf16_lo(v[i])), fabsf(bf16_hi(v[i])));
+                    }
+                    const int e = max((int)(__float_as_uint(top) >> 23) - 127, -100);
+                    const float up = copysignf(__uint_as_float((uint32_t)(14 - e + 127) << 23), ks);
+                    // (a scale of 0 still masks: -inf times a small number)
+                    scale = fmaxf(a.scale_log2 * fabsf(ks) * __uint_as_float((uint32_t)(e - 14 + 127) << 23), 1e-37f);
+                    #pragma unroll 4
+                    for (int ch = 0; ch < D / 8; ++ch) {
+                        uint4 x = *at(ch);
+                        x.x = pack_f16x2(bf16_lo(x.x) * up, bf16_hi(x.x) * up);
+                        x.y = pack_f16x2(bf16_lo(x.y) * up, bf16_hi(x.y) * up);
+                        x.z = pack_f16x2(bf16_lo(x.z) * up, bf16_hi(x.z) * up);
+                        x.w = pack_f16x2(bf16_lo(x.w) * up, bf16_hi(x.w) * up);
+                        *at(ch) = x;
+                    }
+                    fence_proxy_async_smem();
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(q_ready + t);
+            }
+            float m_use = -INFINITY, l = 0.f;
+            const int first = w.first(t), stride = w.stride(), end = w.j1;
+            for (int j = first; j < end; j += stride, ++c) {
+                if (!(good = wait_on(s_full + t, c & 1))) break;
+                const int valid = w.len - j * TK;    // keys of the tile
+                if (busy) {
+                    tc_fence_after();
+                    constexpr int HELD = F8 ? 64 : TK;   // scores held at a time (e4m3: too few registers for a row, S is read twice)
+                    uint32_t v[HELD];
+                    float mx[8];
+                    #pragma unroll
+                    for (int u = 0; u < 8; ++u) mx[u] = -INFINITY;
+                    const auto load = [&](int at) {
+                        #pragma unroll
+                        for (int q = 0; q < HELD; q += 32) tmem_ld32(tS + at + q, *reinterpret_cast<uint32_t (*)[32]>(&v[q]));
+                        tmem_ld_wait();
+                    };
+                    // scores behind the segment: -inf, in place
+                    #pragma unroll 1
+                    for (int at = valid & ~31; at < TK; at += 32) {
+                        uint32_t x[32];
+                        tmem_ld32(tS + at, x);
+                        tmem_ld_wait();
+                        #pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (at + i >= valid) x[i] = __float_as_uint(-INFINITY);
+                        tmem_st32(tS + at, x);
+                        tmem_st_wait();
+                    }
+                    #pragma unroll
+                    for (int at = 0; at < TK; at += HELD) {
+                        load(at);
+                        #pragma unroll
+                        for (int k = 0; k < HELD; k += 16)   // three-input maxima: chain u takes scores u, u + 8, ...
+                            #pragma unroll
+                            for (int u = 0; u < 8; ++u)
+                                mx[u] = fmax3(mx[u], __uint_as_float(v[k + u]), __uint_as_float(v[k + u + 8]));
+                    }
+                    const float mt =
+                        fmaxf(fmax3(mx[0], mx[1], mx[2]), fmax3(fmax3(mx[3], mx[4], mx[5]), mx[6], mx[7])) * scale;
+                    float alpha = 1.f;
+                    bool raise = false;
+                    if (j == first) {
+                        m_use = mt;
+                    } else if (mt > m_use + S::RAISE) {
+                        alpha = ex2(m_use - mt);
+                        m_use = mt;
+                        raise = true;
+                    }
+                    // P = 2^(s * scale - m) (times UP), packed in pairs over the first 64 columns of this row of S
+                    const float off = m_use == -INFINITY ? 0.f : S::UP_LOG2 - m_use;   // (only -inf scores so far: weights 0)
+                    const uint64_t scale2 = f32x2(scale, scale), off2 = f32x2(off, off);
+                    uint64_t rs2[4] = {0ull, 0ull, 0ull, 0ull};
+                    #pragma unroll
+                    for (int at = 0; at < TK; at += HELD) {
+                        if (F8) load(at);
+                        #pragma unroll
+                        for (int q = 0; q < HELD; q += 32) {
+                            uint32_t pk[16];
+                            #pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                float x0, x1;
+                                f32x2_split(ffma2(f32x2(__uint_as_float(v[q + 2 * i]), __uint_as_float(v[q + 2 * i + 1])), scale2,
+                                                  off2), x0, x1);
+                                const float p0 = ex2(x0), p1 = ex2(x1);
+                                rs2[i & 3] = fadd2(rs2[i & 3], f32x2(p0, p1));
+                                pk[i] = F8 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
+                            }
+                            tmem_st16(tS + (at + q) / 2, pk);
+                        }
+                    }
+                    float rs = 0.f;
+                    #pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        float r0, r1;
+                        f32x2_split(rs2[q], r0, r1);
+                        rs += r0 + r1;
+                    }
+                    l = l * alpha + rs;
+                    // O is rescaled after the previous product of this tile has completed
+                    if (__any_sync(0xffffffffu, raise)) {
+                        if (!(good = wait_on(pv_done + t, (c - 1) & 1))) break;
+                        tc_fence_after();
+                        #pragma unroll 1
+                        for (int cc = 0; cc < D / 32; ++cc) {
+                            uint32_t o[32];
+                            tmem_ld32(tO + cc * 32, o);
+                            tmem_ld_wait();
+                            #pragma unroll
+                            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+                            tmem_st32(tO + cc * 32, o);
+                        }
+                    }
+                    tmem_st_wait();
+                }
+                if (!F8 && valid < TK && (t == 0 || w.n_b == 0)) {
+                    // values behind the segment may be anything (0 * NaN): cleared by the warps of the first tile that
+                    // uses them, before their P is announced
+                    const uint32_t at = w.pos + (j - w.j0);
+                    if (!(good = wait_on(v_full + at % NS, (at / NS) & 1))) break;
+                    uint8_t *tile = sV + at % NS * S::TILE;
+                    for (int i = valid * 8 + r; i < TK * 8; i += 128)
+                        #pragma unroll
+                        for (int cc = 0; cc < D / 64; ++cc)
+                            *reinterpret_cast<uint4 *>(tile + cc * S::ATOM + i * 16) = make_uint4(0, 0, 0, 0);
+                    fence_proxy_async_smem();
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_full + t);
+            }
+            if (!good) break;
+            ++items;
+            const bool whole = w.whole, single = w.n_b == 0, merge = single && w.active(1);
+            float2 ml = make_float2(m_use, l);
+            if (single && t == 1) {
+                // tile A's warps merge the two shares of a single tile; the last such item's must have been read
+                if (shares > 0) good = wait_on(o_free, (shares - 1) & 1);
+                ++shares;
+                ml_s[r] = ml;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(l_full);
+                continue;
+            }
+            // The next item's first product (which overwrites O) waits for this warp's next P, written after these reads.
+            good = wait_on(pv_done + t, (c - 1) & 1);
+            float f0 = 1.f, f1 = 0.f;
+            if (t == 0 && w.active(1)) c_b += single ? (end - first) >> 1 : end - first;
+            if (merge) {   // (tile B's softmax has seen its products before the last)
+                good = good && wait_on(l_full, shares++ & 1) && wait_on(pv_done + 1, (c_b - 1) & 1);
+                const float2 y = ml_s[r];
+                const float top = fmaxf(ml.x, y.x), none = top == -INFINITY ? 0.f : top;
+                f0 = ex2(ml.x - none);
+                f1 = ex2(y.x - none);
+                ml = make_float2(top, ml.y * f0 + y.y * f1);
+            }
+            if (!good) break;
+            tc_fence_after();
+            if (warp == 0 && lane == 0 && w.parts) {
+                a.desc[2 * blockIdx.x] = make_int4(w.row0, w.n_a, w.n_b, w.head * a.chunks + w.chunk);
+                a.desc[2 * blockIdx.x + 1] = make_int4(w.parts, 0, 0, 0);
+            }
+            const bool live = busy && r_tok < n_tok && r_tok < a.tok && w.chunk * TQ + r_head < a.group;
+            const long long row = w.row0 + t * a.tok + r_tok;
+            const int qh = w.head * a.group + w.chunk * TQ + r_head;
+            const long long slot = (long long)(2 * blockIdx.x + (w.j0 == 0 ? 1 : 0)) * 2 + t;   // of a part
+            if (whole) {
+                const float f = MODE == ROWS ? 1.f / ml.y : 1.f / S::UP;
+                f0 *= f;
+                f1 *= f;
+            }
+            uint8_t *buf = smem + S::OFF_OUT + warp * 2048;
+            bf16 *base = MODE != ROWS ? nullptr
+                                      : p.o + (long long)(w.row0 + t * a.tok) * p.ld_o +
+                                            (long long)(w.head * a.group + w.chunk * TQ) * D + (lane & 3) * 8;
+            const int heads = a.group - w.chunk * TQ, toks = min(n_tok, a.tok);
+            #pragma unroll 1
+            for (int col = busy ? 0 : D; col < D; col += 32) {
+                // O (of the two halves) of 32 columns, scaled
+                uint32_t x[32];
+                tmem_ld32(tO + col, x);
+                tmem_ld_wait();
+                #pragma unroll
+                for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * f0);
+                if (merge) {
+                    uint32_t y[32];
+                    tmem_ld32(tO + 128 + col, y);
+                    tmem_ld_wait();
+                    #pragma unroll
+                    for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(fmaf(__uint_as_float(y[i]), f1, __uint_as_float(x[i])));
+                }
+                if (!whole) {
+                    float *dst = a.part + slot * (D * 128) + col * 128 + r;
+                    if (live) {
+                        #pragma unroll
+                        for (int i = 0; i < 32; ++i) dst[i * 128] = __uint_as_float(x[i]);
+                    }
+                } else if constexpr (MODE == ROWS) {
+                    // Through shared memory, so that four lanes write 64 bytes of one row (a lane's own row in pieces of
+                    // 16 bytes touches 32 lines per store: three times as long).
+                    #pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const auto pair = [&](int i) {
+                            return pack_bf16x2(__uint_as_float(x[8 * q + i]), __uint_as_float(x[8 * q + i + 1]));
+                        };
+                        *reinterpret_cast<uint4 *>(buf + lane * 64 + ((q ^ (lane >> 1 & 3)) << 4)) =
+                            make_uint4(pair(0), pair(2), pair(4), pair(6));
+                    }
+                    __syncwarp();
+                    #pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int rr = 8 * i + (lane >> 2);
+                        const uint4 out = *reinterpret_cast<const uint4 *>(buf + rr * 64 + (((lane & 3) ^ (rr >> 1 & 3)) << 4));
+                        const int tk = (quarter * 32 + rr) * a.inv_gc >> 16, hd = quarter * 32 + rr - tk * a.gc;
+                        if (tk < toks && hd < heads) *reinterpret_cast<uint4 *>(base + tk * p.ld_o + hd * D + col) = out;
+                    }
+                    __syncwarp();
+                } else {
+                    float4 *dst = reinterpret_cast<float4 *>(p.pre_o + (row * p.nq + qh) * D + col);
+                    if (live) {
+                        #pragma unroll
+                        for (int q = 0; q < 8; ++q)
+                            dst[q] = make_float4(__uint_as_float(x[4 * q]), __uint_as_float(x[4 * q + 1]),
+                                                 __uint_as_float(x[4 * q + 2]), __uint_as_float(x[4 * q + 3]));
+                    }
+                }
+            }
+            if (live && !whole) a.ml[slot * 128 + r] = ml;
+            if (MODE != ROWS && live && whole) p.pre_ml[row * p.nq + qh] = make_float2(ml.x, ml.y / S::UP);
+            if (merge) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(o_free);
+            }
+        }
+    } else if (warp == 8) {
         // ------------------------------------------------ producer
         const int tile_shift = 7 - a.box_shift, boxes = 1 << tile_shift, per = 32 >> tile_shift;   // boxes of a tile, tiles of a batch
         const int my_tile = lane >> tile_shift, my_box = lane & (boxes - 1);
@@ -332,15 +717,18 @@ __global__ void __launch_bounds__(Shape<D, MODE>::THREADS, 1)
         bool ok = true;
         uint32_t gk = 0, gv = 0, gr = 0, nq_loaded[2] = {0, 0};
         const auto wait = [&](uint64_t *bar, uint32_t parity) {
-            ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, abort));
+            ok = __all_sync(0xffffffffu, wait_bar(bar, parity, abort));
             return ok;
         };
-        while (ok && w.next(g, a.tok)) {
-            const int head = kv_head(w.u), chunk = w.u - head * a.chunks;
+        for (uint32_t it = 0; ok; give_back(it++)) {
+            if (!wait(item_full + it % ITEMS, (it / ITEMS) & 1)) break;
+            const Item &w = ring[it % ITEMS];
+            if (w.j0 >= w.j1) break;
+            const int head = w.head;
             const auto look_up = [&](int j) {   // page of this lane's box in the batch of tiles from j on
                 const int key = (j + my_tile) * TK + (my_box << a.box_shift);
                 if (MODE == ROWS || j + my_tile >= w.j1 || key >= w.len) return 0;
-                return p.table[(long long)w.s * p.ld_table + (key >> p.cache.page_shift)];
+                return p.table[(long long)w.key0 * p.ld_table + (key >> p.cache.page_shift)];
             };
             int page = look_up(w.j0), next_page = 0, batch = w.j0;
             // tile j of K or V into dst, on bar
@@ -349,7 +737,7 @@ __global__ void __launch_bounds__(Shape<D, MODE>::THREADS, 1)
                     if (lane == 0) {
                         mbar_arrive_expect_tx(bar, S::TILE);
                         for (int c = 0; c < D / 64; ++c)
-                            tma_load_3d(dst + c * S::ATOM, m, bar, c * 64, head, g.ck[w.s] + j * TK);
+                            tma_load_3d(dst + c * S::ATOM, m, bar, c * 64, head, w.key0 + j * TK);
                     }
                 } else {
                     const int n = min(boxes, (w.len - j * TK + (1 << a.box_shift) - 1) >> a.box_shift);
@@ -391,15 +779,24 @@ __global__ void __launch_bounds__(Shape<D, MODE>::THREADS, 1)
                     ++gk;
                 }
                 if (j == w.j0) {
-                    for (int t = 0; t < (w.n_b > 0 ? 2 : 1); ++t) {
+                    for (int t = 0; t < (w.active(1) ? 2 : 1); ++t) {   // (a single tile's rows for both)
                         if (nq_loaded[t] > 0 && !wait(q_empty + t, (nq_loaded[t] - 1) & 1)) break;
                         ++nq_loaded[t];
                         if (lane == 0) {
                             mbar_arrive_expect_tx(q_full + t, a.tok * a.gc * D * 2);
                             for (int c = 0; c < D / 64; ++c)
-                                tma_load_4d(sQ + t * S::TILE + c * S::ATOM, &tmQ, q_full + t, c * 64, chunk * TQ, head,
-                                            cq[w.s] + w.tok0 + t * a.tok);
+                                tma_load_4d(sQ + t * S::TILE + c * S::ATOM, &tmQ, q_full + t, c * 64, w.chunk * TQ, head,
+                                            w.row0 + (w.n_b ? t * a.tok : 0));
                         }
+                    }
+                    // the next item's rows on their way to L2, if it is known (their tiles are free once this one's last scores are done)
+                    const uint32_t ahead = it + 1;
+                    if (ok && mbar_try_wait(smem_u32(item_full + ahead % ITEMS), (ahead / ITEMS) & 1) && lane == 0) {
+                        const Item &x = ring[ahead % ITEMS];
+                        if (x.j0 < x.j1)
+                            for (int t = 0; t < (x.n_b > 0 ? 2 : 1); ++t)
+                                for (int c = 0; c < D / 64; ++c)
+                                    tma_prefetch_4d(&tmQ, c * 64, x.chunk * TQ, x.head, x.row0 + t * a.tok);
                     }
                     if (!ok) break;
                 }
@@ -421,358 +818,165 @@ __global__ void __launch_bounds__(Shape<D, MODE>::THREADS, 1)
                 *abort = 1;
                 const int never = 0;
                 if constexpr (F8) {
-                    for (uint32_t f = gr > RS ? gr - RS : 0; f < gr; ++f) mbar_wait(raw_full + f % RS, (f / RS) & 1, &never);
+                    for (uint32_t f = gr > RS ? gr - RS : 0; f < gr; ++f) wait_bar(raw_full + f % RS, (f / RS) & 1, &never);
                 } else {
-                    for (uint32_t f = gk > NS ? gk - NS : 0; f < gk; ++f) mbar_wait(k_full + f % NS, (f / NS) & 1, &never);
-                    for (uint32_t f = gv > NS ? gv - NS : 0; f < gv; ++f) mbar_wait(v_full + f % NS, (f / NS) & 1, &never);
+                    for (uint32_t f = gk > NS ? gk - NS : 0; f < gk; ++f) wait_bar(k_full + f % NS, (f / NS) & 1, &never);
+                    for (uint32_t f = gv > NS ? gv - NS : 0; f < gv; ++f) wait_bar(v_full + f % NS, (f / NS) & 1, &never);
                 }
                 for (int t = 0; t < 2; ++t)
-                    if (nq_loaded[t]) mbar_wait(q_full + t, (nq_loaded[t] - 1) & 1, &never);
+                    if (nq_loaded[t]) wait_bar(q_full + t, (nq_loaded[t] - 1) & 1, &never);
             }
             __syncwarp();
         }
-    } else if (warp == 1) {
-        // ------------------------------------------------ products
+    } else if (warp < 11) {
+        // ------------------------------------------------ products: one thread for each row tile
+        // A product of 128 x 128 x 16 takes 64 cycles, and its issue about as long; a wait or a commit costs the issuing
+        // thread 50 to 90 more, so with one thread for both tiles the tensor cores stood still a third of the time (4096
+        // tokens over 4096 keys, 64 heads over 8 of 128: 440 us instead of 392).
         constexpr uint32_t kind = F8 ? 0u : (1u << 7) | (1u << 10);   // A and B f16, or bf16
         constexpr uint32_t base = (1u << 4) | kind | ((uint32_t)(TQ >> 4) << 24);
         constexpr uint32_t idesc_s = base | ((uint32_t)(TK >> 3) << 17);
         constexpr uint32_t idesc_o = base | ((uint32_t)(D >> 3) << 17) | (1u << 16);   // B (V) is MN-major
-        bool ok = true;
-        uint32_t gk = 0, gv = 0;          // ring positions of the next K tile to multiply first, the current V tile
-        uint32_t np[2] = {0, 0}, nq_used[2] = {0, 0};
-        const auto wait = [&](uint64_t *bar, uint32_t parity) {
-            ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, abort));
-            return ok;
-        };
-        // S_t = Q_t K^T for ring position pos
-        const auto issue_s = [&](int t, uint32_t pos) {
-            if (!wait(k_full + pos % NS, (pos / NS) & 1)) return;
-            tc_fence_after();
-            if (lane == 0) {
-                const uint32_t qa = smem_u32(sQ + t * S::TILE), kb = smem_u32(sK + pos % NS * S::TILE);
-                #pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                    const uint32_t off = (kk >> 2) * S::ATOM + (kk & 3) * 32;
-                    umma_bf16(tmem_base + t * TQ, sdesc_sw128(qa + off), sdesc_sw128(kb + off), idesc_s, kk > 0);
-                }
-                umma_commit(s_full + t);
-            }
-            __syncwarp();
-        };
-        // O_t (+)= P_t V, P_t in the first 64 columns of tile t's S.  Values behind the segment may be anything (0 * NaN):
-        // the rows from `valid` on are cleared first.
-        const auto issue_pv = [&](int t, uint32_t pos, bool first, int valid) {
-            if (!wait(v_full + pos % NS, (pos / NS) & 1)) return;
-            uint8_t *tile = sV + pos % NS * S::TILE;
-            if (!F8 && t == 0 && valid < TK) {
-                for (int i = valid * 8 + lane; i < TK * 8; i += 32)
-                    #pragma unroll
-                    for (int c = 0; c < D / 64; ++c)
-                        *reinterpret_cast<uint4 *>(tile + c * S::ATOM + i * 16) = make_uint4(0, 0, 0, 0);
-                fence_proxy_async_smem();
-                __syncwarp();
-            }
-            if (!wait(p_full + t, np[t] & 1)) return;
-            ++np[t];
-            tc_fence_after();
-            if (lane == 0) {
-                const uint32_t vb = smem_u32(tile), pt = tmem_base + (uint32_t)(t * TQ);
-                #pragma unroll
-                for (int kk = 0; kk < TK / 16; ++kk)
-                    umma_bf16_ts(tmem_base + 256 + t * 128, pt + kk * 8, sdesc_sw128_mn(vb + kk * 2048, S::ATOM, 1024),
-                                 idesc_o, (!first || kk > 0) ? 1u : 0u);
-                umma_commit(pv_done + t);
-            }
-            __syncwarp();
-        };
-        const auto commit = [&](uint64_t *bar) {
-            if (lane == 0) umma_commit(bar);
-            __syncwarp();
-        };
-        while (ok && w.next(g, a.tok)) {
-            const int n = w.j1 - w.j0, last = w.n_b > 0 ? 1 : 0;   // last: the last tile that uses a key tile
-            for (int t = 0; t <= last && ok; ++t) {
-                if (!wait((F8 ? q_ready : q_full) + t, nq_used[t] & 1)) break;
-                ++nq_used[t];
-                issue_s(t, gk);
-                if (ok && n == 1) commit(q_empty + t);
-            }
-            if (!ok) break;
-            commit(k_empty + gk % NS);
-            for (int j = 0; j < n && ok; ++j, ++gv) {
-                for (int t = 0; t <= last && ok; ++t) {
-                    issue_pv(t, gv, j == 0, w.len - (w.j0 + j) * TK);
-                    if (!ok) break;
-                    if (t == last) commit(v_empty + gv % NS);
-                    if (j + 1 < n) {
-                        issue_s(t, gk + j + 1);
-                        if (!ok) break;
-                        if (j + 2 == n) commit(q_empty + t);   // the item's last scores of this tile
-                        if (t == last) commit(k_empty + (gk + j + 1) % NS);
-                    }
-                }
-            }
-            gk += n;
-        }
         if (lane == 0) {
+            const int t = warp - 9;
+            const uint32_t q_lo = (smem_u32(sQ + t * S::TILE) >> 4) | (1u << 16);   // (K-major: the leading offset is not used)
+            const uint32_t k_lo = (smem_u32(sK) >> 4) | (1u << 16);
+            const uint32_t v_lo = (smem_u32(sV) >> 4) | ((uint32_t)(S::ATOM >> 4) << 16);   // MN-major: 64 columns, ATOM bytes apart
+            const uint32_t tS = tmem_base + t * TQ, tO = tmem_base + 256 + t * 128;
+            bool ok = true;
+            uint32_t gk = 0, gv = 0, np = 0, items = 0, turns = 0, merged = 0;   // ring positions; P tiles, items, turns, shares of single items of this row tile
+            // K and V tiles are released by both threads; those of the other tile's steps at once
+            const auto skip_k = [&]() {
+                ok = wait_bar(k_full + gk % NS, (gk / NS) & 1, abort);
+                if (ok) mbar_arrive(k_empty + gk++ % NS);
+                return ok;
+            };
+            const auto skip_v = [&]() {
+                ok = wait_bar(v_full + gv % NS, (gv / NS) & 1, abort);
+                if (ok) mbar_arrive(v_empty + gv++ % NS);
+                return ok;
+            };
+            for (uint32_t it = 0; ok; mbar_arrive(item_empty + it++ % ITEMS)) {
+                ok = wait_bar(item_full + it % ITEMS, (it / ITEMS) & 1, abort);
+                if (!ok) break;
+                const Item &w = ring[it % ITEMS];
+                if (w.j0 >= w.j1) break;
+                const bool both = w.n_b > 0;
+                if (!w.active(t)) {
+                    for (int j = w.j0; j < w.j1 && ok; ++j) ok = skip_k() && skip_v();
+                    continue;
+                }
+                ok = wait_bar((F8 ? q_ready : q_full) + t, items & 1, abort);
+                const int begin = w.j0, first = w.first(t), stride = w.stride(), end = w.j1;
+                if (ok && first > begin) skip_k();
+                // The first scores, then each step's value product with the next step's scores.  A pair's tiles take turns (else both
+                // would do the same at the same time, and the tensor cores stand still during both softmaxes: 590 us
+                // in the case above).  Of a single tile's steps every other one is this thread's; each K and V tile between
+                // two of its own is released before it waits for a later one (they arrive in the order K, V, K, V, ...).
+                #pragma unroll 1
+                for (int j = first - stride; j < end && ok; j += stride) {
+                    if (j >= first) {   // O_t (+)= P_t V, P_t in the first 64 columns of tile t's S
+                        const uint32_t s = gv % NS;
+                        ok = wait_bar(v_full + s, (gv / NS) & 1, abort) && wait_bar(p_full + t, np++ & 1, abort);
+                        // the share of the single item before is still being read
+                        if (ok && j == first && t == 1 && merged) ok = wait_bar(o_free, (merged - 1) & 1, abort);
+                    }
+                    if (!ok) break;
+                    if (j >= first) {
+                        if (both && (t == 1 || turns > 0)) ok = wait_bar(turn + t, (turns - (t == 0)) & 1, abort);
+                        if (!ok) break;
+                        const uint32_t s = gv++ % NS, vb = v_lo + s * (S::TILE >> 4);
+                        tc_fence_after();
+                        #pragma unroll
+                        for (int kk = 0; kk < TK / 16; ++kk)
+                            mma_ts(tO, tS + kk * 8, vb + kk * (2048 >> 4), idesc_o, j > first || kk > 0);
+                        umma_commit(pv_done + t);
+                        umma_commit(v_empty + s);
+                    }
+                    if (j + stride < end) {   // S_t = Q_t K^T
+                        const uint32_t s = gk % NS, kb = k_lo + s * (S::TILE >> 4);
+                        ok = wait_bar(k_full + s, (gk / NS) & 1, abort);
+                        if (!ok) break;
+                        ++gk;
+                        tc_fence_after();
+                        #pragma unroll
+                        for (int kk = 0; kk < D / 16; ++kk) {
+                            const uint32_t off = ((kk >> 2) * S::ATOM + (kk & 3) * 32) >> 4;
+                            mma_ss(tS, q_lo + off, kb + off, idesc_s, kk > 0);
+                        }
+                        if (both && j >= first) mbar_arrive(turn + (t ^ 1));
+                        umma_commit(s_full + t);
+                        umma_commit(k_empty + s);
+                        if (j + 2 * stride >= end) umma_commit(q_empty + t);   // the item's last scores of this tile
+                        if (!both) {
+                            if (j + 1 >= begin) skip_v();
+                            if (ok && j + 3 < end) skip_k();
+                        }
+                    } else if (both) {
+                        mbar_arrive(turn + (t ^ 1));
+                    } else if (j + 1 < end) {
+                        skip_v();   // the other thread's last
+                    }
+                    turns += both && j >= first;
+                }
+                if (t == 1 && !both) ++merged;
+                ++items;
+            }
             if (!ok) {
                 report(p.status, ST_TIMEOUT);
                 *abort = 1;
             }
-            umma_commit(drain);
+            umma_commit(drain + t);
             const int never = 0;
-            mbar_wait(drain, 0, &never);
+            wait_bar(drain + t, 0, &never);
         }
         __syncwarp();
-    } else if (warp < 10) {
-        // ------------------------------------------------ softmax
-        const int t = (warp - 2) >> 2, quarter = warp & 3;
-        const int r = quarter * 32 + lane;            // row of the tile = TMEM lane
-        const int r_tok = r / a.gc, r_head = r - r_tok * a.gc;
-        const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
-        const uint32_t tS = tmem_base + lane_off + (uint32_t)(t * TQ);
-        const uint32_t tO = tmem_base + lane_off + (uint32_t)(256 + t * 128);
-        uint32_t c = 0, items = 0;                    // steps and items of this row tile so far (barrier phases)
-        bool good = true;
-        const bool scribe = warp == 2 && lane == 0;
-        if (scribe) a.desc[2 * blockIdx.x + 1] = make_int4(0, 0, 0, 0);
-        const auto wait = [&](uint64_t *bar, uint32_t parity) {
-            good = __all_sync(0xffffffffu, mbar_wait(bar, parity, abort));
-            return good;
-        };
-        while (good && w.next(g, a.tok)) {
-            const int n_tok = t ? w.n_b : w.n_a;
-            if (n_tok == 0) continue;
-            const bool busy = quarter * 32 < n_tok * a.gc;   // this warp has rows of tokens
-            const int head = kv_head(w.u), chunk = w.u - head * a.chunks;
-            float scale = a.scale_log2;
-            if constexpr (F8) {
-                // q to f16 in place: a row's largest |q| goes to [2^14, 2^15): exact but for elements 2^-29 of it and smaller
-                if (!wait(q_full + t, items & 1)) break;
-                if (busy) {
-                    const float ks = p.cache.k_scale[head];
-                    uint8_t *row = sQ + t * S::TILE + r * 128;
-                    const auto at = [&](int ch) {
-                        return reinterpret_cast<uint4 *>(row + (ch >> 3) * S::ATOM + (((ch & 7) ^ (r & 7)) << 4));
-                    };
-                    float top = 0.f;
-                    #pragma unroll 4
-                    for (int ch = 0; ch < D / 8; ++ch) {
-                        const uint4 x = *at(ch);
-                        const uint32_t v[4] = {x.x, x.y, x.z, x.w};
-                        #pragma unroll
-                        for (int i = 0; i < 4; ++i) top = fmax3(top, fabsf(bf16_lo(v[i])), fabsf(bf16_hi(v[i])));
-                    }
-                    const int e = max((int)(__float_as_uint(top) >> 23) - 127, -100);
-                    const float up = copysignf(__uint_as_float((uint32_t)(14 - e + 127) << 23), ks);
-                    // (a scale of 0 still masks: -inf times a small number)
-                    scale = fmaxf(a.scale_log2 * fabsf(ks) * __uint_as_float((uint32_t)(e - 14 + 127) << 23), 1e-37f);
-                    #pragma unroll 4
-                    for (int ch = 0; ch < D / 8; ++ch) {
-                        uint4 x = *at(ch);
-                        uint32_t *v = &x.x;
-                        x.x = pack_f16x2(bf16_lo(v[0]) * up, bf16_hi(v[0]) * up);
-                        x.y = pack_f16x2(bf16_lo(x.y) * up, bf16_hi(x.y) * up);
-                        x.z = pack_f16x2(bf16_lo(x.z) * up, bf16_hi(x.z) * up);
-                        x.w = pack_f16x2(bf16_lo(x.w) * up, bf16_hi(x.w) * up);
-                        *at(ch) = x;
-                    }
-                    fence_proxy_async_smem();
+    } else if (warp == 11) {
+        if (lane == 0) {
+            // ------------------------------------------------ the items of the run, handed to the other warps
+            Walk<MODE> w;
+            const bool any = blockIdx.x < G;
+            w.begin(any ? runs.first(blockIdx.x) : 0, any ? runs.first(blockIdx.x + 1) : 0, g, p.n_segs, a.tok, a.chunks);
+            bool ok = true, more = true;
+            int pos = 0;
+            for (uint32_t it = 0; ok && more; ++it) {
+                if (it >= ITEMS) ok = wait_bar(item_empty + it % ITEMS, (it / ITEMS - 1) & 1, abort);
+                if (!ok) break;
+                more = w.next(g, a.tok, a.chunks, p.nkv);
+                Item &x = ring[it % ITEMS];
+                x.j0 = more ? w.j0 : 0;
+                x.j1 = more ? w.j1 : 0;
+                if (more) {
+                    x.row0 = cq[w.s] + w.tok0;
+                    x.n_a = w.n_a;
+                    x.n_b = w.n_b;
+                    x.head = w.head;
+                    x.chunk = w.chunk;
+                    x.len = w.len;
+                    x.key0 = MODE == ROWS ? ck[w.s] : w.s;
+                    x.whole = w.j0 == 0 && w.j1 == w.steps;
+                    x.parts = w.j0 == 0 && w.j1 < w.steps
+                                  ? runs.owner(w.start + ((w.steps - 1) << w.shift)) - (int)blockIdx.x + 1
+                                  : 0;
+                    x.pos = pos;
+                    pos += w.j1 - w.j0;
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(q_ready + t);
-                ++items;
+                mbar_arrive(item_full + it % ITEMS);
             }
-            float m_use = -INFINITY, l = 0.f;
-            for (int j = w.j0; j < w.j1; ++j, ++c) {
-                if (!wait(s_full + t, c & 1)) break;
-                if (busy) {
-                    tc_fence_after();
-                    const int valid = w.len - j * TK;    // keys of the tile
-                    float mt;
-                    uint32_t v[F8 ? 64 : TK];
-                    if constexpr (F8) {
-                        // two passes over S: the converters leave too few registers for a whole row
-                        mt = -INFINITY;
-                        #pragma unroll
-                        for (int q = 0; q < 4; q += 2) {
-                            tmem_ld32(tS + 32 * q, *reinterpret_cast<uint32_t (*)[32]>(&v[0]));
-                            tmem_ld32(tS + 32 * q + 32, *reinterpret_cast<uint32_t (*)[32]>(&v[32]));
-                            tmem_ld_wait();
-                            if (valid < TK) {
-                                #pragma unroll
-                                for (int i = 0; i < 64; ++i)
-                                    if (32 * q + i >= valid) v[i] = __float_as_uint(-INFINITY);
-                            }
-                            float mx[4] = {mt, mt, mt, mt};
-                            #pragma unroll
-                            for (int i = 0; i < 64; i += 2)
-                                mx[i >> 1 & 3] = fmax3(mx[i >> 1 & 3], __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
-                            mt = fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]);
-                        }
-                        mt *= scale;
-                    } else {
-                        tmem_ld32(tS, *reinterpret_cast<uint32_t (*)[32]>(&v[0]));
-                        tmem_ld32(tS + 32, *reinterpret_cast<uint32_t (*)[32]>(&v[32]));
-                        tmem_ld32(tS + 64, *reinterpret_cast<uint32_t (*)[32]>(&v[F8 ? 0 : 64]));
-                        tmem_ld32(tS + 96, *reinterpret_cast<uint32_t (*)[32]>(&v[F8 ? 0 : 96]));
-                        tmem_ld_wait();
-                        if (valid < TK) {
-                            #pragma unroll
-                            for (int i = 0; i < TK; ++i)
-                                if (i >= valid) v[F8 ? 0 : i] = __float_as_uint(-INFINITY);
-                        }
-                        // three-input maxima: chain u takes scores u, u + 8, ..., u + 120
-                        float mx[8];
-                        #pragma unroll
-                        for (int u = 0; u < 8; ++u) {
-                            float m = __uint_as_float(v[u]);
-                            #pragma unroll
-                            for (int k = 1; k < 15; k += 2)
-                                m = fmax3(m, __uint_as_float(v[F8 ? 0 : u + 8 * k]), __uint_as_float(v[F8 ? 0 : u + 8 * k + 8]));
-                            mx[u] = fmaxf(m, __uint_as_float(v[F8 ? 0 : u + 120]));
-                        }
-                        mt = fmaxf(fmax3(mx[0], mx[1], mx[2]), fmax3(fmax3(mx[3], mx[4], mx[5]), mx[6], mx[7])) * scale;
-                    }
-                    float alpha = 1.f;
-                    bool raise = false;
-                    if (j == w.j0) {
-                        m_use = mt;
-                    } else if (mt > m_use + S::RAISE) {
-                        alpha = ex2(m_use - mt);
-                        m_use = mt;
-                        raise = true;
-                    }
-                    // P = 2^(s * scale - m) (times UP), packed in pairs over the first 64 columns of this row of S
-                    const float off = m_use == -INFINITY ? 0.f : S::UP_LOG2 - m_use;   // (only -inf scores so far: weights 0)
-                    const uint64_t scale2 = f32x2(scale, scale), off2 = f32x2(off, off);
-                    uint64_t rs2[4] = {0ull, 0ull, 0ull, 0ull};
-                    #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        if constexpr (F8) {
-                            tmem_ld32(tS + 64 * h, *reinterpret_cast<uint32_t (*)[32]>(&v[0]));
-                            tmem_ld32(tS + 64 * h + 32, *reinterpret_cast<uint32_t (*)[32]>(&v[32]));
-                            tmem_ld_wait();
-                            if (valid < TK) {
-                                #pragma unroll
-                                for (int i = 0; i < 64; ++i)
-                                    if (64 * h + i >= valid) v[i] = __float_as_uint(-INFINITY);
-                            }
-                        }
-                        uint32_t pk[32];
-                        #pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            const int at = (F8 ? 0 : 64 * h) + 2 * i;
-                            float x0, x1;
-                            f32x2_split(ffma2(f32x2(__uint_as_float(v[at]), __uint_as_float(v[at + 1])), scale2, off2), x0, x1);
-                            const float p0 = ex2(x0), p1 = ex2(x1);
-                            rs2[i & 3] = fadd2(rs2[i & 3], f32x2(p0, p1));
-                            pk[i] = F8 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
-                        }
-                        tmem_st32(tS + 32 * h, pk);
-                    }
-                    float rs = 0.f;
-                    #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        float r0, r1;
-                        f32x2_split(rs2[q], r0, r1);
-                        rs += r0 + r1;
-                    }
-                    l = l * alpha + rs;
-                    // O is rescaled after the previous product of this tile has completed
-                    if (__any_sync(0xffffffffu, raise)) {
-                        if (!wait(pv_done + t, (c - 1) & 1)) break;
-                        tc_fence_after();
-                        #pragma unroll 1
-                        for (int cc = 0; cc < D / 32; ++cc) {
-                            uint32_t o[32];
-                            tmem_ld32(tO + cc * 32, o);
-                            tmem_ld_wait();
-                            #pragma unroll
-                            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-                            tmem_st32(tO + cc * 32, o);
-                        }
-                    }
-                    tmem_st_wait();
-                }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(p_full + t);
+            if (!ok) {
+                report(p.status, ST_TIMEOUT);
+                *abort = 1;
             }
-            if (!good) break;
-            // The next item's first product (which overwrites O) waits for this warp's next P, written after these reads.
-            if (!wait(pv_done + t, (c - 1) & 1)) break;
-            tc_fence_after();
-            const bool whole = w.j0 == 0 && w.j1 == w.steps;
-            const int row0 = cq[w.s] + w.tok0;
-            if (scribe && !whole && w.j0 == 0) {
-                a.desc[2 * blockIdx.x] = make_int4(row0, w.n_a, w.n_b, w.u);
-                const int parts = runs.owner(w.start + w.weight * (w.steps - 1)) - (int)blockIdx.x + 1;
-                a.desc[2 * blockIdx.x + 1] = make_int4(parts, 0, 0, 0);
-            }
-            if (!busy) continue;
-            const bool live = r_tok < n_tok && r_tok < a.tok && chunk * TQ + r_head < a.group;
-            const long long row = row0 + t * a.tok + r_tok;
-            const int h = head * a.group + chunk * TQ + r_head;
-            if (!whole) {
-                const long long slot = (long long)(2 * blockIdx.x + (w.j0 == 0 ? 1 : 0)) * 2 + t;
-                float *dst = a.part + slot * (D * 128) + r;
-                #pragma unroll 1
-                for (int cc = 0; cc < D / 32; ++cc) {
-                    uint32_t o[32];
-                    tmem_ld32(tO + cc * 32, o);
-                    tmem_ld_wait();
-                    if (live) {
-                        #pragma unroll
-                        for (int i = 0; i < 32; ++i) dst[(cc * 32 + i) * 128] = __uint_as_float(o[i]);
-                    }
-                }
-                if (live) a.ml[slot * 128 + r] = make_float2(m_use, l);
-                continue;
-            }
-            const float f = MODE == ROWS ? 1.f / l : 1.f / S::UP;
-            #pragma unroll 1
-            for (int cc = 0; cc < D / 32; ++cc) {
-                uint32_t o[32];
-                tmem_ld32(tO + cc * 32, o);
-                tmem_ld_wait();
-                if (!live) continue;
-                if constexpr (MODE == ROWS) {
-                    uint4 *dst = reinterpret_cast<uint4 *>(p.o + row * p.ld_o + (long long)h * D + cc * 32);
-                    #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const auto pair = [&](int i) {
-                            return pack_bf16x2(__uint_as_float(o[8 * q + i]) * f, __uint_as_float(o[8 * q + i + 1]) * f);
-                        };
-                        dst[q] = make_uint4(pair(0), pair(2), pair(4), pair(6));
-                    }
-                } else {
-                    float4 *dst = reinterpret_cast<float4 *>(p.pre_o + (row * p.nq + h) * D + cc * 32);
-                    #pragma unroll
-                    for (int q = 0; q < 8; ++q)
-                        dst[q] = make_float4(__uint_as_float(o[4 * q]) * f, __uint_as_float(o[4 * q + 1]) * f,
-                                             __uint_as_float(o[4 * q + 2]) * f, __uint_as_float(o[4 * q + 3]) * f);
-                }
-            }
-            if (MODE != ROWS && live) p.pre_ml[row * p.nq + h] = make_float2(m_use, l * f);
-        }
-        if (!good && lane == 0) {
-            report(p.status, ST_TIMEOUT);
-            *abort = 1;
         }
     } else if constexpr (F8) {
         // ------------------------------------------------ e4m3 -> f16
-        const int ct = tid - 320;
+        const int ct = tid - 12 * 32;
         uint32_t gr = 0, gt = 0;   // raw tiles, key tiles so far
         bool good = true;
-        const auto wait = [&](uint64_t *bar, uint32_t parity) {
-            good = __all_sync(0xffffffffu, mbar_wait(bar, parity, abort));
-            return good;
-        };
         const auto convert = [&](uint8_t *dst, uint64_t *full, uint64_t *empty, int keep) {
             const int s = gr % RS;
-            if (!wait(raw_full + s, (gr / RS) & 1)) return;
-            if (gt >= NS && !wait(empty + gt % NS, (gt / NS - 1) & 1)) return;
+            good = wait_on(raw_full + s, (gr / RS) & 1) && (gt < NS || wait_on(empty + gt % NS, (gt / NS - 1) & 1));
+            if (!good) return;
             const uint8_t *src = sRaw + s * S::RAW;
             uint8_t *out = dst + gt % NS * S::TILE;
             #pragma unroll
@@ -794,21 +998,21 @@ __global__ void __launch_bounds__(Shape<D, MODE>::THREADS, 1)
             }
             ++gr;
         };
-        while (good && w.next(g, a.tok))
+        for (uint32_t it = 0; good; give_back(it++)) {
+            if (!(good = wait_on(item_full + it % ITEMS, (it / ITEMS) & 1))) break;
+            const Item &w = ring[it % ITEMS];
+            if (w.j0 >= w.j1) break;
             for (int j = w.j0; j < w.j1 && good; ++j, ++gt) {
                 convert(sK, k_full, k_empty, TK);
                 if (good) convert(sV, v_full, v_empty, w.len - j * TK);
             }
-        if (!good && lane == 0) {
-            report(p.status, ST_TIMEOUT);
-            *abort = 1;
         }
     }
 
     __syncwarp();
     tc_fence_before();
     __syncthreads();
-    if (warp == 1) {
+    if (warp == 8) {
         tc_fence_after();
         tmem_dealloc(tmem_base, 512);
     }
@@ -907,10 +1111,10 @@ size_t attention_cross_workspace_bytes(int num_sms, int d) {
 long long attention_cross_weight(int Tq, int max_keys, int n_segs, int nq, int nkv) {
     const int group = nq / nkv, gc = std::min(group, TQ), chunks = (group + TQ - 1) / TQ, tok = TQ / gc;
     // (every segment's last tile of rows may be partial)
-    const double tiles = (double)Tq / tok + std::min(n_segs, Tq);
+    const double tiles = (double)Tq / (2 * tok) + std::min(n_segs, Tq);
     const double steps = (double)max_keys / TK + 1;
-    const double most = (double)nkv * chunks * tiles * steps;
-    return most > 2e9 ? -1 : (long long)most;
+    const double most = (double)nkv * chunks * tiles * (2 * steps + FIXED);
+    return most > 2e9 ? -1 : (long long)most + 1;
 }
 
 cudaError_t launch_attention_cross(const AttentionCross &p, cudaStream_t st) {
@@ -923,6 +1127,7 @@ cudaError_t launch_attention_cross(const AttentionCross &p, cudaStream_t st) {
     a.gc = std::min(a.group, TQ);
     a.chunks = (a.group + TQ - 1) / TQ;
     a.tok = TQ / a.gc;
+    a.inv_gc = (65536 + a.gc - 1) / a.gc;
     const bool pages = p.key_lens != nullptr;
     a.box_shift = pages ? std::min(7, p.cache.page_shift) : 7;
     const int d = p.d;
