@@ -60,7 +60,7 @@ struct __align__(16) Item {
     int row0, n_a, n_b;     // row of its first token, tokens of its tiles (n_b 0: single)
     int head, chunk;        // kv head and share of its group
     int j0, j1, len, key0;  // steps of this run [j0, j1) (none: the run is over), keys; their first row, or the segment
-    int whole, parts;       // all steps are this run's; parts of the item if its first is this run's and others follow, else 0
+    int parts, owner;       // parts of the item (0: all of its steps are this run's) and the CTA that has the first
     int pos;                // key tiles of the run before it
     // steps of row tile t: the first, and the distance of the next
     __device__ __forceinline__ int first(int t) const { return j0 + (n_b ? 0 : t); }
@@ -75,19 +75,20 @@ struct Shape {
     static constexpr int THREADS = F8 ? 512 : 384;
     static constexpr int ATOM = TQ * 128;                  // 64 columns of a 128-row tile
     static constexpr int TILE = TK * D * 2;                // one operand tile
-    static constexpr int NS = (D == 128 ? 2 : 4) / (F8 ? 2 : 1);   // K tiles, and V tiles, held
+    // K and V tiles held; e4m3: a K tile is free again as soon as its scores are done, a V tile only behind the softmax
+    static constexpr int NSK = (D == 128 ? 2 : 4) / (F8 ? 2 : 1), NSV = D == 128 ? 2 : 4;
     static constexpr int RAW = TK * D;                     // one e4m3 tile
-    static constexpr int RS = F8 ? (D == 128 ? 5 : 8) : 0;
+    static constexpr int RS = F8 ? (D == 128 ? 3 : 8) : 0;
     static constexpr int OFF_Q = 0;
     static constexpr int OFF_K = OFF_Q + 2 * TILE;
-    static constexpr int OFF_V = OFF_K + NS * TILE;
-    static constexpr int OFF_RAW = OFF_V + NS * TILE;
+    static constexpr int OFF_V = OFF_K + NSK * TILE;
+    static constexpr int OFF_RAW = OFF_V + NSV * TILE;
     static constexpr int OFF_SEG = OFF_RAW + RS * RAW;     // pre, cq, ck
     static constexpr int OFF_ITEM = OFF_SEG + 3 * 4 * (kMaxSeqs + 4);  // ring of items
     static constexpr int OFF_ML = OFF_ITEM + ITEMS * (int)sizeof(Item);   // [128] (m, l) of tile B's share of a single tile's rows
     static constexpr int OFF_OUT = OFF_ML + 128 * 8;       // 32 rows x 64 bytes of output per softmax warp
     static constexpr int OFF_BAR = OFF_OUT + (MODE == ROWS ? 8 * 2048 : 0);
-    static constexpr int BARS = 4 * NS + 18 + 2 * ITEMS + 2 * RS;
+    static constexpr int BARS = 2 * NSK + 2 * NSV + 18 + 2 * ITEMS + 2 * RS;
     static constexpr int READERS = 11 + (F8 ? 4 : 0);      // warps that read an item
     static constexpr int BYTES = OFF_BAR + BARS * 8 + 128 + 1024;   // + alignment of the base
     static constexpr float UP = F8 ? 8192.f : 1.f;         // weights, and so l and o, are held times this
@@ -104,8 +105,8 @@ struct Args {
     float scale_log2;
     float *part;                  // [cta][slot][tile][D][128] partial outputs, unnormalised
     float2 *ml;                   // [cta][slot][tile][128] their running maximum and sum
-    int4 *desc;                   // [cta][2] the item whose first part is this CTA's slot 1: (row of its first token,
-                                  // tokens of A, tokens of B, unit), (parts, -, -, -)
+    int4 *desc;                   // [cta][slot][2] the item of that part: (row of its first token, tokens of A, tokens of B,
+                                  // unit), (parts, CTA of the first, -, -); parts 0: no part
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -284,7 +285,7 @@ __global__ void __launch_bounds__(Shape<D, MODE>::THREADS, 1)
                            const __grid_constant__ CUtensorMap tmV, const __grid_constant__ Args a) {
     using S = Shape<D, MODE>;
     constexpr bool F8 = S::F8;
-    constexpr int NS = S::NS, RS = S::RS;
+    constexpr int NSK = S::NSK, NSV = S::NSV, RS = S::RS;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     uint8_t *sQ = smem + S::OFF_Q, *sK = smem + S::OFF_K, *sV = smem + S::OFF_V, *sRaw = smem + S::OFF_RAW;
@@ -292,8 +293,8 @@ __global__ void __launch_bounds__(Shape<D, MODE>::THREADS, 1)
     Item *ring = reinterpret_cast<Item *>(smem + S::OFF_ITEM);
     float2 *ml_s = reinterpret_cast<float2 *>(smem + S::OFF_ML);
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + S::OFF_BAR);
-    uint64_t *k_full = bars, *v_full = k_full + NS, *k_empty = v_full + NS, *v_empty = k_empty + NS;
-    uint64_t *q_full = v_empty + NS, *q_ready = q_full + 2, *q_empty = q_ready + 2;   // [2] row tile, from here on
+    uint64_t *k_full = bars, *v_full = k_full + NSK, *k_empty = v_full + NSV, *v_empty = k_empty + NSK;
+    uint64_t *q_full = v_empty + NSV, *q_ready = q_full + 2, *q_empty = q_ready + 2;   // [2] row tile, from here on
     uint64_t *s_full = q_empty + 2, *p_full = s_full + 2, *pv_done = p_full + 2, *l_full = pv_done + 2, *o_free = l_full + 1;   // [1], [1]
     uint64_t *turn = o_free + 1, *drain = turn + 2, *item_full = drain + 2, *item_empty = item_full + ITEMS;
     uint64_t *raw_full = item_empty + ITEMS, *raw_empty = raw_full + RS;
@@ -306,10 +307,12 @@ __global__ void __launch_bounds__(Shape<D, MODE>::THREADS, 1)
 
     pdl_trigger();
     if (tid == 0) {
-        for (int i = 0; i < NS; ++i) {
+        for (int i = 0; i < NSK; ++i) {
             mbar_init(k_full + i, F8 ? 4 : 1);
-            mbar_init(v_full + i, F8 ? 4 : 1);
             mbar_init(k_empty + i, 2);
+        }
+        for (int i = 0; i < NSV; ++i) {
+            mbar_init(v_full + i, F8 ? 4 : 1);
             mbar_init(v_empty + i, 2);
         }
         for (int i = 0; i < 2; ++i) {
@@ -447,7 +450,8 @@ __global__ void __launch_bounds__(Shape<D, MODE>::THREADS, 1)
         const uint32_t tS = tmem_base + lane_off + (uint32_t)(t * TQ);
         const uint32_t tO = tmem_base + lane_off + (uint32_t)(256 + t * 128);
         const int r_tok = r * a.inv_gc >> 16, r_head = r - r_tok * a.gc;
-        if (warp == 0 && lane == 0) a.desc[2 * blockIdx.x + 1] = make_int4(0, 0, 0, 0);
+        if (warp == 0 && lane < 2) a.desc[2 * (2 * blockIdx.x + lane) + 1] = make_int4(0, 0, 0, 0);
+        __syncwarp();
         // steps and items of this row tile, steps of tile B, single items with shares of both so far (barrier phases)
         uint32_t c = 0, items = 0, c_b = 0, shares = 0;
         bool good = true;
@@ -593,8 +597,8 @@ __global__ void __launch_bounds__(Shape<D, MODE>::THREADS, 1)
                     // values behind the segment may be anything (0 * NaN): cleared by the warps of the first tile that
                     // uses them, before their P is announced
                     const uint32_t at = w.pos + (j - w.j0);
-                    if (!(good = wait_on(v_full + at % NS, (at / NS) & 1))) break;
-                    uint8_t *tile = sV + at % NS * S::TILE;
+                    if (!(good = wait_on(v_full + at % NSV, (at / NSV) & 1))) break;
+                    uint8_t *tile = sV + at % NSV * S::TILE;
                     for (int i = valid * 8 + r; i < TK * 8; i += 128)
                         #pragma unroll
                         for (int cc = 0; cc < D / 64; ++cc)
@@ -607,7 +611,7 @@ __global__ void __launch_bounds__(Shape<D, MODE>::THREADS, 1)
             }
             if (!good) break;
             ++items;
-            const bool whole = w.whole, single = w.n_b == 0, merge = single && w.active(1);
+            const bool whole = w.parts == 0, single = w.n_b == 0, merge = single && w.active(1);
             float2 ml = make_float2(m_use, l);
             if (single && t == 1) {
                 // tile A's warps merge the two shares of a single tile; the last such item's must have been read
@@ -632,9 +636,10 @@ __global__ void __launch_bounds__(Shape<D, MODE>::THREADS, 1)
             }
             if (!good) break;
             tc_fence_after();
-            if (warp == 0 && lane == 0 && w.parts) {
-                a.desc[2 * blockIdx.x] = make_int4(w.row0, w.n_a, w.n_b, w.head * a.chunks + w.chunk);
-                a.desc[2 * blockIdx.x + 1] = make_int4(w.parts, 0, 0, 0);
+            if (!whole && warp == 0 && lane == 0) {
+                int4 *d = a.desc + 2 * (2 * blockIdx.x + (w.j0 == 0 ? 1 : 0));
+                d[0] = make_int4(w.row0, w.n_a, w.n_b, w.head * a.chunks + w.chunk);
+                d[1] = make_int4(w.parts, w.owner, 0, 0);
             }
             const bool live = busy && r_tok < n_tok && r_tok < a.tok && w.chunk * TQ + r_head < a.group;
             const long long row = w.row0 + t * a.tok + r_tok;
@@ -774,8 +779,8 @@ __global__ void __launch_bounds__(Shape<D, MODE>::THREADS, 1)
                     load_raw(j, &tmK);
                     if (!ok) break;
                 } else {
-                    if (gk >= NS && !wait(k_empty + gk % NS, (gk / NS - 1) & 1)) break;
-                    load(j, &tmK, sK + gk % NS * S::TILE, k_full + gk % NS);
+                    if (gk >= NSK && !wait(k_empty + gk % NSK, (gk / NSK - 1) & 1)) break;
+                    load(j, &tmK, sK + gk % NSK * S::TILE, k_full + gk % NSK);
                     ++gk;
                 }
                 if (j == w.j0) {
@@ -804,8 +809,8 @@ __global__ void __launch_bounds__(Shape<D, MODE>::THREADS, 1)
                     load_raw(j, &tmV);
                     if (!ok) break;
                 } else {
-                    if (gv >= NS && !wait(v_empty + gv % NS, (gv / NS - 1) & 1)) break;
-                    load(j, &tmV, sV + gv % NS * S::TILE, v_full + gv % NS);
+                    if (gv >= NSV && !wait(v_empty + gv % NSV, (gv / NSV - 1) & 1)) break;
+                    load(j, &tmV, sV + gv % NSV * S::TILE, v_full + gv % NSV);
                     ++gv;
                 }
                 __syncwarp();
@@ -820,8 +825,8 @@ __global__ void __launch_bounds__(Shape<D, MODE>::THREADS, 1)
                 if constexpr (F8) {
                     for (uint32_t f = gr > RS ? gr - RS : 0; f < gr; ++f) wait_bar(raw_full + f % RS, (f / RS) & 1, &never);
                 } else {
-                    for (uint32_t f = gk > NS ? gk - NS : 0; f < gk; ++f) wait_bar(k_full + f % NS, (f / NS) & 1, &never);
-                    for (uint32_t f = gv > NS ? gv - NS : 0; f < gv; ++f) wait_bar(v_full + f % NS, (f / NS) & 1, &never);
+                    for (uint32_t f = gk > NSK ? gk - NSK : 0; f < gk; ++f) wait_bar(k_full + f % NSK, (f / NSK) & 1, &never);
+                    for (uint32_t f = gv > NSV ? gv - NSV : 0; f < gv; ++f) wait_bar(v_full + f % NSV, (f / NSV) & 1, &never);
                 }
                 for (int t = 0; t < 2; ++t)
                     if (nq_loaded[t]) wait_bar(q_full + t, (nq_loaded[t] - 1) & 1, &never);
@@ -847,13 +852,13 @@ __global__ void __launch_bounds__(Shape<D, MODE>::THREADS, 1)
             uint32_t gk = 0, gv = 0, np = 0, items = 0, turns = 0, merged = 0;   // ring positions; P tiles, items, turns, shares of single items of this row tile
             // K and V tiles are released by both threads; those of the other tile's steps at once
             const auto skip_k = [&]() {
-                ok = wait_bar(k_full + gk % NS, (gk / NS) & 1, abort);
-                if (ok) mbar_arrive(k_empty + gk++ % NS);
+                ok = wait_bar(k_full + gk % NSK, (gk / NSK) & 1, abort);
+                if (ok) mbar_arrive(k_empty + gk++ % NSK);
                 return ok;
             };
             const auto skip_v = [&]() {
-                ok = wait_bar(v_full + gv % NS, (gv / NS) & 1, abort);
-                if (ok) mbar_arrive(v_empty + gv++ % NS);
+                ok = wait_bar(v_full + gv % NSV, (gv / NSV) & 1, abort);
+                if (ok) mbar_arrive(v_empty + gv++ % NSV);
                 return ok;
             };
             for (uint32_t it = 0; ok; mbar_arrive(item_empty + it++ % ITEMS)) {
@@ -876,8 +881,8 @@ __global__ void __launch_bounds__(Shape<D, MODE>::THREADS, 1)
                 #pragma unroll 1
                 for (int j = first - stride; j < end && ok; j += stride) {
                     if (j >= first) {   // O_t (+)= P_t V, P_t in the first 64 columns of tile t's S
-                        const uint32_t s = gv % NS;
-                        ok = wait_bar(v_full + s, (gv / NS) & 1, abort) && wait_bar(p_full + t, np++ & 1, abort);
+                        const uint32_t s = gv % NSV;
+                        ok = wait_bar(v_full + s, (gv / NSV) & 1, abort) && wait_bar(p_full + t, np++ & 1, abort);
                         // the share of the single item before is still being read
                         if (ok && j == first && t == 1 && merged) ok = wait_bar(o_free, (merged - 1) & 1, abort);
                     }
@@ -885,7 +890,7 @@ __global__ void __launch_bounds__(Shape<D, MODE>::THREADS, 1)
                     if (j >= first) {
                         if (both && (t == 1 || turns > 0)) ok = wait_bar(turn + t, (turns - (t == 0)) & 1, abort);
                         if (!ok) break;
-                        const uint32_t s = gv++ % NS, vb = v_lo + s * (S::TILE >> 4);
+                        const uint32_t s = gv++ % NSV, vb = v_lo + s * (S::TILE >> 4);
                         tc_fence_after();
                         #pragma unroll
                         for (int kk = 0; kk < TK / 16; ++kk)
@@ -894,8 +899,8 @@ __global__ void __launch_bounds__(Shape<D, MODE>::THREADS, 1)
                         umma_commit(v_empty + s);
                     }
                     if (j + stride < end) {   // S_t = Q_t K^T
-                        const uint32_t s = gk % NS, kb = k_lo + s * (S::TILE >> 4);
-                        ok = wait_bar(k_full + s, (gk / NS) & 1, abort);
+                        const uint32_t s = gk % NSK, kb = k_lo + s * (S::TILE >> 4);
+                        ok = wait_bar(k_full + s, (gk / NSK) & 1, abort);
                         if (!ok) break;
                         ++gk;
                         tc_fence_after();
@@ -954,10 +959,11 @@ __global__ void __launch_bounds__(Shape<D, MODE>::THREADS, 1)
                     x.chunk = w.chunk;
                     x.len = w.len;
                     x.key0 = MODE == ROWS ? ck[w.s] : w.s;
-                    x.whole = w.j0 == 0 && w.j1 == w.steps;
-                    x.parts = w.j0 == 0 && w.j1 < w.steps
-                                  ? runs.owner(w.start + ((w.steps - 1) << w.shift)) - (int)blockIdx.x + 1
-                                  : 0;
+                    x.parts = 0;
+                    if (w.j0 > 0 || w.j1 < w.steps) {
+                        x.owner = runs.owner(w.start);
+                        x.parts = runs.owner(w.start + ((w.steps - 1) << w.shift)) - x.owner + 1;
+                    }
                     x.pos = pos;
                     pos += w.j1 - w.j0;
                 }
@@ -973,12 +979,12 @@ __global__ void __launch_bounds__(Shape<D, MODE>::THREADS, 1)
         const int ct = tid - 12 * 32;
         uint32_t gr = 0, gt = 0;   // raw tiles, key tiles so far
         bool good = true;
-        const auto convert = [&](uint8_t *dst, uint64_t *full, uint64_t *empty, int keep) {
+        const auto convert = [&](uint8_t *dst, uint64_t *full, uint64_t *empty, uint32_t stages, int keep) {
             const int s = gr % RS;
-            good = wait_on(raw_full + s, (gr / RS) & 1) && (gt < NS || wait_on(empty + gt % NS, (gt / NS - 1) & 1));
+            good = wait_on(raw_full + s, (gr / RS) & 1) && (gt < stages || wait_on(empty + gt % stages, (gt / stages - 1) & 1));
             if (!good) return;
             const uint8_t *src = sRaw + s * S::RAW;
-            uint8_t *out = dst + gt % NS * S::TILE;
+            uint8_t *out = dst + gt % stages * S::TILE;
             #pragma unroll
             for (int i = 0; i < TK * D / 16 / 128; ++i) {
                 const int chunk = i * 128 + ct, row = chunk / (D / 16), c = 2 * (chunk % (D / 16));
@@ -993,7 +999,7 @@ __global__ void __launch_bounds__(Shape<D, MODE>::THREADS, 1)
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
-                mbar_arrive(full + gt % NS);
+                mbar_arrive(full + gt % stages);
                 mbar_arrive(raw_empty + s);
             }
             ++gr;
@@ -1003,8 +1009,8 @@ __global__ void __launch_bounds__(Shape<D, MODE>::THREADS, 1)
             const Item &w = ring[it % ITEMS];
             if (w.j0 >= w.j1) break;
             for (int j = w.j0; j < w.j1 && good; ++j, ++gt) {
-                convert(sK, k_full, k_empty, TK);
-                if (good) convert(sV, v_full, v_empty, w.len - j * TK);
+                convert(sK, k_full, k_empty, NSK, TK);
+                if (good) convert(sV, v_full, v_empty, NSV, w.len - j * TK);
             }
         }
     }
@@ -1018,48 +1024,56 @@ __global__ void __launch_bounds__(Shape<D, MODE>::THREADS, 1)
     }
 }
 
-// Joins the parts of the items that several CTAs shared, in key order: part 0 is slot 1 of CTA blockIdx.x, part i slot 0 of CTA
-// blockIdx.x + i.  blockIdx.y: row tile and quarter of it (a lane per row); blockIdx.z: 32 columns, four per warp.
+// Joins the parts of the items that several CTAs shared, in key order: part 0 is slot 1 of the first CTA, part i slot 0 of the
+// i-th after it.  JOIN_Z blocks per part (blockIdx.x: CTA, blockIdx.y: slot), each with its share of the item's output: warps
+// take 32 rows by four columns, a lane per row.  Bound by the chain item -> maxima -> parts, so a warp should have one or two shares.
+constexpr int JOIN_Z = 8;
 template <int D, int MODE>
 __global__ void __launch_bounds__(256) attention_cross_join_kernel(const __grid_constant__ Args a) {
     pdl_trigger();
     pdl_wait();
     const AttentionCross &p = a.p;
-    const int n = __ldcg(a.desc + 2 * blockIdx.x + 1).x;
+    const int4 *desc = a.desc + 2 * (2 * blockIdx.x + blockIdx.y);
+    const int4 it = __ldcg(desc), of = __ldcg(desc + 1);
+    const int n = of.x, first = of.y, lane = threadIdx.x & 31;
     if (n == 0) return;
-    const int4 it = __ldcg(a.desc + 2 * blockIdx.x);
-    const int t = blockIdx.y >> 2, r = (blockIdx.y & 3) * 32 + (threadIdx.x & 31), col = blockIdx.z * 32 + (threadIdx.x >> 5) * 4;
-    const int r_tok = r / a.gc, r_head = r - r_tok * a.gc;
     const int head = it.w / a.chunks, chunk = it.w - head * a.chunks;
-    if (r_tok >= (t ? it.z : it.y) || r_tok >= a.tok || chunk * TQ + r_head >= a.group) return;
-    const auto slot = [&](int i) { return (long long)(2 * (blockIdx.x + i) + (i == 0 ? 1 : 0)) * 2 + t; };
-    float top = -INFINITY;
-    #pragma unroll 8
-    for (int i = 0; i < n; ++i) top = fmaxf(top, __ldcg(a.ml + slot(i) * 128 + r).x);
-    const float base = top == -INFINITY ? 0.f : top;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    float l = 0.f;
-    #pragma unroll 8
-    for (int i = 0; i < n; ++i) {
-        const float2 ml = __ldcg(a.ml + slot(i) * 128 + r);
-        const float *src = a.part + slot(i) * (D * 128) + (long long)col * 128 + r;
-        const float f = ex2(ml.x - base);
-        l = fmaf(ml.y, f, l);
-        acc.x = fmaf(__ldcg(src), f, acc.x);
-        acc.y = fmaf(__ldcg(src + 128), f, acc.y);
-        acc.z = fmaf(__ldcg(src + 256), f, acc.z);
-        acc.w = fmaf(__ldcg(src + 384), f, acc.w);
-    }
-    const long long row = it.x + t * a.tok + r_tok;
-    const int h = head * a.group + chunk * TQ + r_head;
-    if (MODE == ROWS) {
-        const float f = 1.f / l;
-        *reinterpret_cast<uint2 *>(p.o + row * p.ld_o + (long long)h * D + col) =
-            make_uint2(pack_bf16x2(acc.x * f, acc.y * f), pack_bf16x2(acc.z * f, acc.w * f));
-    } else {
-        constexpr float f = 1.f / Shape<D, MODE>::UP;
-        *reinterpret_cast<float4 *>(p.pre_o + (row * p.nq + h) * D + col) = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
-        if (col == 0) p.pre_ml[row * p.nq + h] = make_float2(top, l * f);
+    const int quarters_a = (min(it.y, a.tok) * a.gc + 31) >> 5, quarters_b = (min(it.z, a.tok) * a.gc + 31) >> 5;
+    const int units = (quarters_a + quarters_b) * (D / 4);
+    for (int u = (((int)blockIdx.x - first) * JOIN_Z + (int)blockIdx.z) * 8 + (threadIdx.x >> 5); u < units; u += n * JOIN_Z * 8) {
+        const int q = u / (D / 4), col = u % (D / 4) * 4, t = q >= quarters_a ? 1 : 0;
+        const int r = (t ? q - quarters_a : q) * 32 + lane, r_tok = r * a.inv_gc >> 16, r_head = r - r_tok * a.gc;
+        if (r_tok >= (t ? it.z : it.y) || r_tok >= a.tok || chunk * TQ + r_head >= a.group) continue;
+        const auto slot = [&](int i) { return (long long)(2 * (first + i) + (i == 0 ? 1 : 0)) * 2 + t; };
+        float top = -INFINITY;
+        #pragma unroll 8
+        for (int i = 0; i < n; ++i) top = fmaxf(top, __ldcg(a.ml + slot(i) * 128 + r).x);
+        const float base = top == -INFINITY ? 0.f : top;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        float l = 0.f;
+        #pragma unroll 8
+        for (int i = 0; i < n; ++i) {
+            const float2 ml = __ldcg(a.ml + slot(i) * 128 + r);
+            const float *src = a.part + slot(i) * (D * 128) + (long long)col * 128 + r;
+            const float f = ex2(ml.x - base);
+            l = fmaf(ml.y, f, l);
+            acc.x = fmaf(__ldcg(src), f, acc.x);
+            acc.y = fmaf(__ldcg(src + 128), f, acc.y);
+            acc.z = fmaf(__ldcg(src + 256), f, acc.z);
+            acc.w = fmaf(__ldcg(src + 384), f, acc.w);
+        }
+        const long long row = it.x + t * a.tok + r_tok;
+        const int h = head * a.group + chunk * TQ + r_head;
+        if (MODE == ROWS) {
+            const float f = 1.f / l;
+            *reinterpret_cast<uint2 *>(p.o + row * p.ld_o + (long long)h * D + col) =
+                make_uint2(pack_bf16x2(acc.x * f, acc.y * f), pack_bf16x2(acc.z * f, acc.w * f));
+        } else {
+            constexpr float f = 1.f / Shape<D, MODE>::UP;
+            *reinterpret_cast<float4 *>(p.pre_o + (row * p.nq + h) * D + col) =
+                make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
+            if (col == 0) p.pre_ml[row * p.nq + h] = make_float2(top, l * f);
+        }
     }
 }
 
@@ -1079,7 +1093,7 @@ cudaError_t launch(const AttentionCross &p, Args &a, int sms, long long most, cu
     }
     char *ws = static_cast<char *>(p.workspace);
     a.desc = reinterpret_cast<int4 *>(ws);
-    a.ml = reinterpret_cast<float2 *>(ws + up256((size_t)sms * 2 * sizeof(int4)));
+    a.ml = reinterpret_cast<float2 *>(ws + up256((size_t)sms * 4 * sizeof(int4)));
     a.part = reinterpret_cast<float *>(a.ml + (size_t)sms * 4 * 128);
     CUtensorMap tq, tk, tv;
     bool ok = make_tmap_heads(&tq, p.q, D, a.group, p.nkv, p.Tq, p.ld_q, a.gc, a.tok);
@@ -1098,14 +1112,14 @@ cudaError_t launch(const AttentionCross &p, Args &a, int sms, long long most, cu
     cudaLaunchConfig_t cfg = pdl_config(dim3(grid), dim3(S::THREADS), S::BYTES, st, at);
     cudaError_t e = cudaLaunchKernelEx(&cfg, attention_cross_kernel<D, MODE>, tq, tk, tv, a);
     if (e != cudaSuccess) return e;
-    cfg = pdl_config(dim3(grid, 8, D / 32), dim3(256), 0, st, at);
+    cfg = pdl_config(dim3(grid, 2, JOIN_Z), dim3(256), 0, st, at);
     return cudaLaunchKernelEx(&cfg, attention_cross_join_kernel<D, MODE>, a);
 }
 
 }  // namespace
 
 size_t attention_cross_workspace_bytes(int num_sms, int d) {
-    return up256((size_t)num_sms * 2 * sizeof(int4)) + (size_t)num_sms * 4 * 128 * (sizeof(float2) + d * sizeof(float));
+    return up256((size_t)num_sms * 4 * sizeof(int4)) + (size_t)num_sms * 4 * 128 * (sizeof(float2) + d * sizeof(float));
 }
 
 long long attention_cross_weight(int Tq, int max_keys, int n_segs, int nq, int nkv) {

@@ -410,12 +410,15 @@ __global__ void __launch_bounds__(Shape<D, F8, BLOCKS>::THREADS, 1)
     } shared[2];
     shared[0].b = shared[1].b = -1;
     const int trow = tid / (D / 4), tcol = tid % (D / 4) * 4;   // this thread's output in the sums of the joins
-    const auto store = [&](int b, int h, float4 v, float m, float l, float vs) {
+    // PRE, up to 8 heads: this thread's share of the prefix's part, loaded at the segment's beginning (early)
+    float2 pre_ml = make_float2(0.f, 0.f);
+    float4 pre_x = make_float4(0.f, 0.f, 0.f, 0.f);
+    const auto store = [&](int b, int h, float4 v, float m, float l, float vs, bool early) {
         if constexpr (PRE) {   // one more part
             const long long at = (long long)b * p.nq + h;
-            const float2 ml = __ldcg(p.pre_ml + at);
-            if (ml.y != 0.f) {   // (no value is read where the prefix is empty)
-                const float4 x = __ldcg(reinterpret_cast<const float4 *>(p.pre_o + at * D + tcol));
+            const float2 ml = early ? pre_ml : __ldcg(p.pre_ml + at);
+            if (ml.y != 0.f) {   // (no value is used where the prefix is empty)
+                const float4 x = early ? pre_x : __ldcg(reinterpret_cast<const float4 *>(p.pre_o + at * D + tcol));
                 const float top = fmaxf(m, ml.x), c = m == -INFINITY ? 0.f : ex2(m - top);
                 const float e = ml.x == -INFINITY ? 0.f : ex2(ml.x - top) * S::UP;
                 v = make_float4(fmaf(v.x, c, x.x * e), fmaf(v.y, c, x.y * e), fmaf(v.z, c, x.z * e), fmaf(v.w, c, x.w * e));
@@ -443,6 +446,13 @@ __global__ void __launch_bounds__(Shape<D, F8, BLOCKS>::THREADS, 1)
         const int kvh = kv_head(w.u), chunk = w.u - kvh * a.chunks, h0 = kvh * a.group + chunk * ROWS;
         const int rows = min(ROWS, a.group - chunk * ROWS);   // heads of the segment
 
+        if constexpr (PRE && BLOCKS == 1) {
+            if (trow < rows) {
+                const long long at = (long long)w.b * p.nq + h0 + trow;
+                pre_ml = __ldcg(p.pre_ml + at);
+                pre_x = __ldcg(reinterpret_cast<const float4 *>(p.pre_o + at * D + tcol));
+            }
+        }
         // q as the A operand: rows = heads, the contraction over d in steps of 16
         uint32_t qa[D / 16][WIDE ? 4 : 2];
         float scale0 = base_scale, scale1 = base_scale;
@@ -714,7 +724,7 @@ __global__ void __launch_bounds__(Shape<D, F8, BLOCKS>::THREADS, 1)
                     acc.w += x.w;
                 }
                 if (whole) {
-                    store(w.b, h0 + row, acc, mm, ll, vs);
+                    store(w.b, h0 + row, acc, mm, ll, vs, PRE && BLOCKS == 1);
                 } else {
                     *reinterpret_cast<float4 *>(a.part + ((long long)slot * ROWS + row) * D + tcol) = acc;
                     if (tcol == 0) a.ml[slot * ROWS + row] = make_float2(mm, ll);
@@ -802,7 +812,7 @@ __global__ void __launch_bounds__(Shape<D, F8, BLOCKS>::THREADS, 1)
                 for (int off = LPR / 2; off > 0; off >>= 1) ll += __shfl_xor_sync(0xffffffffu, ll, off);
                 if (r0 + trow < rows) {
                     if (final) {
-                        store(y.b, kvh * a.group + chunk * ROWS + row, acc, mm, ll, vs);
+                        store(y.b, kvh * a.group + chunk * ROWS + row, acc, mm, ll, vs, false);
                     } else {
                         *reinterpret_cast<float4 *>(a.part + head * D + tcol) = acc;
                         if (tcol == 0) a.ml[head] = make_float2(mm, ll);
