@@ -491,10 +491,11 @@ H3ENC_API h3enc_status h3enc_op_rope_append(const void *qkv, int64_t ld_qkv, int
  *   sequence's own tokens in place 0 of its first page), clamped and reported alike.
  *   weight_in, weight_out: of the own tokens; the prefixes' weights are not accumulated.
  *   workspace: h3enc_op_attention_decode_shared_workspace_bytes() bytes, with the rules of h3enc_op_attention_decode's.
- * The weights of a prefix's tokens enter the second sum in bf16 (e4m3: f16), off by up to 2^-8 (2^-11) of each.  A prefix's weights
- * below 2^-126 (e4m3: 2^-38) of the largest in its tiles count as 0.  Requires n_prefixes <= 1024, max_prefix <= 2^30;
- * n_kv_heads * ceil(heads per kv head / 128) * (n_seqs / max(128 / heads per kv head, 1) + n_prefixes) * (max_prefix / 128 + 1) above 2e9 is
- * H3ENC_ERR_UNSUPPORTED; the rest as for h3enc_op_attention_decode. */
+ * The weights of a prefix's tokens enter the second sum in bf16 (e4m3: f16), off by up to 2^-8 (2^-11) of each, and those
+ * below 2^-126 (e4m3: 2^-38) of the largest count as 0; where all sequences together would read less than 60 MB of prefixes,
+ * each reads its own again, with the rounding of h3enc_op_attention_decode.  Requires n_prefixes <= 1024, max_prefix <= 2^30;
+ * n_kv_heads * ceil(heads per kv head / 128) * (n_seqs / (2 max(128 / heads per kv head, 1)) + min(n_prefixes, n_seqs)) *
+ * (max_prefix / 64 + 4) above 2e9 is H3ENC_ERR_UNSUPPORTED; the rest as for h3enc_op_attention_decode. */
 H3ENC_API h3enc_status h3enc_op_attention_decode_shared(
     const void *q, int64_t ld_q, void *o, int64_t ld_o, const h3enc_kv_cache *cache, const int32_t *prefix_table,
     int32_t ld_prefix, const int32_t *prefix_lens, const int32_t *prefix_rows, int32_t n_prefixes, int32_t max_prefix,
@@ -510,19 +511,19 @@ H3ENC_API int64_t h3enc_op_attention_decode_shared_workspace_bytes(int32_t n_seq
 /* Cross attention: packed queries over packed keys and values of another length (an encoder's states through a
  * projection), without a mask; one query per sequence is a decode step.
  *   o[t] = sum_i p_i v_i, p = softmax_i(q[t] . k_i / sqrt(d)), for rows t of [cu_q[b], cu_q[b + 1]) over rows i of
- *   [cu_k[b], cu_k[b + 1]); q head h reads kv head h / (n_heads / n_kv_heads).  fp32, but p enters the second sum in bf16;
- *   o rounded to bf16 once.  No keys: zero rows.  Rows of no sequence are left as they were.
+ *   [cu_k[b], cu_k[b + 1]); q head h reads kv head h / (n_heads / n_kv_heads).  fp32, but p enters the second sum in bf16
+ *   (up to 32 rows of queries x heads per kv head and sequence on the average: with 16 bits); o rounded to bf16 once.  No keys: zero rows.  Rows of no sequence are left as they were.
  *   q [Tq, ld_q], o [Tq, ld_o]: head h at column h*d; k [Tk, ld_k], v [Tk, ld_v]: kv head g at column g*d (k and v may be
  *   columns of one projection).  o must not overlap q, k or v.
  *   cu_q, cu_k DEVICE int32 [n_seqs + 1], not running back; each may be NULL with n_seqs 1 (all rows).  Offsets outside
  *   [0, Tq] or [0, Tk] are clamped; that, or one that runs back, sets status bit 2 (rows of two sequences are undefined).
- *   workspace: h3enc_op_attention_cross_workspace_bytes() bytes, 256-byte aligned, of any content, reused by calls of any sizes.
- *   Calls (and graphs that hold them) sharing it must not overlap on the GPU.
+ *   workspace: h3enc_op_attention_cross_workspace_bytes() bytes, 256-byte aligned, zero-filled once before its first use and
+ *   then reused by calls of any sizes.  Calls (and graphs that hold them) sharing it must not overlap on the GPU.
  * The result does not depend on timing: the same inputs give the same bits on every run.  A bounded wait that runs out sets
  * status bit 1; the outputs are then undefined.
  * Requires head_dim in {64, 128}, n_seqs <= 1024, Tq and Tk <= 2^30, n_heads <= 65536, n_heads % n_kv_heads == 0, leading
  * dimensions that are multiples of 8 and below 2^39, operands 16-byte aligned; n_kv_heads * ceil(heads per kv head / 128) *
- * (Tq / max(128 / heads per kv head, 1) + n_seqs) * (Tk / 128 + 1) above 2e9 is H3ENC_ERR_UNSUPPORTED. */
+ * (Tq / (2 max(128 / heads per kv head, 1)) + min(n_seqs, Tq)) * (Tk / 64 + 4) above 2e9 is H3ENC_ERR_UNSUPPORTED. */
 H3ENC_API h3enc_status h3enc_op_attention_cross(const void *q, int64_t ld_q, const void *k, int64_t ld_k, const void *v,
                                                 int64_t ld_v, void *o, int64_t ld_o, int32_t Tq, int32_t Tk,
                                                 int32_t n_heads, int32_t n_kv_heads, int32_t head_dim, const int32_t *cu_q,

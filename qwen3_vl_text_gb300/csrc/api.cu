@@ -1817,7 +1817,11 @@ h3enc_status h3enc_op_attention_decode_shared(
                                                     "h3enc_op_attention_decode_shared_workspace_bytes() or not 256-byte "
                                                     "aligned", who);
     cudaError_t e = cudaSuccess;
-    if (n_prefixes > 0) {
+    p.prefix_table = prefix_table; p.ld_prefix = ld_prefix;
+    p.prefix_lens = prefix_lens; p.prefix_rows = prefix_rows; p.max_prefix = max_prefix;
+    if (n_prefixes > 0 && h3::attention_prefix_near(p)) {
+        p.n_prefixes = n_prefixes;
+    } else if (n_prefixes > 0) {
         char *ws = static_cast<char *>(workspace);
         h3::AttentionCross c{};
         c.q = p.q; c.ld_q = ld_q; c.Tq = n_seqs; c.max_keys = max_prefix;
@@ -1876,7 +1880,9 @@ h3enc_status h3enc_op_attention_cross(const void *q, int64_t ld_q, const void *k
     p.Tq = Tq; p.max_keys = Tk; p.n_segs = n_seqs; p.nq = n_heads; p.nkv = n_kv_heads; p.d = head_dim;
     p.cu_q = cu_q; p.cu_k = cu_k;
     p.workspace = workspace; p.status = status;
-    cudaError_t e = h3::launch_attention_cross(p, static_cast<cudaStream_t>(stream));
+    const int packed = h3::attention_packed_rows(Tq, Tk, n_seqs, n_heads, n_kv_heads);
+    cudaError_t e = packed ? h3::launch_attention_packed(p, packed, static_cast<cudaStream_t>(stream))
+                           : h3::launch_attention_cross(p, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? H3ENC_OK : cuda_fail(nullptr, e, "attention_cross launch");
 }
 

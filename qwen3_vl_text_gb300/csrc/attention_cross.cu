@@ -1091,7 +1091,7 @@ cudaError_t launch(const AttentionCross &p, Args &a, int sms, long long most, cu
         if (e != cudaSuccess) return e;
         ready[dev].store(true);
     }
-    char *ws = static_cast<char *>(p.workspace);
+    char *ws = static_cast<char *>(p.workspace) + kArrivalBytes;
     a.desc = reinterpret_cast<int4 *>(ws);
     a.ml = reinterpret_cast<float2 *>(ws + up256((size_t)sms * 4 * sizeof(int4)));
     a.part = reinterpret_cast<float *>(a.ml + (size_t)sms * 4 * 128);
@@ -1119,7 +1119,9 @@ cudaError_t launch(const AttentionCross &p, Args &a, int sms, long long most, cu
 }  // namespace
 
 size_t attention_cross_workspace_bytes(int num_sms, int d) {
-    return up256((size_t)num_sms * 4 * sizeof(int4)) + (size_t)num_sms * 4 * 128 * (sizeof(float2) + d * sizeof(float));
+    const size_t own = kArrivalBytes + up256((size_t)num_sms * 4 * sizeof(int4)) +
+                       (size_t)num_sms * 4 * 128 * (sizeof(float2) + d * sizeof(float));
+    return std::max(own, attention_packed_workspace_bytes(num_sms));
 }
 
 long long attention_cross_weight(int Tq, int max_keys, int n_segs, int nq, int nkv) {

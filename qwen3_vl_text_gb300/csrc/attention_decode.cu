@@ -23,6 +23,7 @@
 //    runs in f16, with q scaled by a power of two per head into f16's range and p by 2^14: f16 ends at
 //    2^-24, so the two halves then leave an error of at most 2^-39 of a warp's largest weight, far below the
 //    fp32 sums; unscaled, every weight under 2^-25 of the largest would be lost to o but counted in l.
+// The same kernel walks a shared prefix's tiles before a sequence's own, and packed queries over packed keys.
 // Measured (64 q heads over 8 kv heads of 128, pages of 64): 64 sequences of 5000 to 8192 tokens in bf16, 1.7 GB,
 // 248-251 us = 6.8 TB/s, the measured copy rate; in e4m3 139-140 us (6.0 TB/s: the conversions of every key and value
 // to f16 then take most of the time between two tiles); one sequence of 1025 tokens 7.3 us, which is
@@ -169,47 +170,69 @@ __device__ __forceinline__ uint32_t chunk_at(int r, int c) {
     else return r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
 }
 
-// Walks the tiles (of TK keys) of a run: segment (b, u) with u = kv head * chunks + chunk, tile j of it.
-template <int TK>
+// What stands in front of a sequence's own cached tokens, or in their place.
+enum { PLAIN = 0, PREFIX = 1, PACKED = 2 };
+
+// The sequences, in shared memory: keys; PREFIX: tokens of the prefix whose tiles precede the own ones, and its row of
+// the prefixes' page table; PACKED: first key, first row of q, rows of q.
+struct Seqs {
+    const int *pre, *lens, *plen, *pidx, *k0, *q0, *nq;
+};
+
+// Walks the tiles (of TK keys) of a run: segment (b, u) with u = kv head * chunks + chunk, tile j of it (the first pt are the prefix's).
+template <int TK, int EXT, int CH>
 struct Walk {
-    int b, u, j, len, tiles;
-    __device__ __forceinline__ void start(int t, const int *pre, const int *lens, int n_seqs) {
+    int b, u, j, len, tiles, plen, pt, chunks;
+    __device__ __forceinline__ void start(int t, const Seqs &q, int n_seqs, int group, int chunks_) {
         int lo = 0, hi = n_seqs;   // the b with pre[b] <= t < pre[b + 1]
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
-            if (pre[mid] <= t) lo = mid;
+            if (q.pre[mid] <= t) lo = mid;
             else hi = mid;
         }
         b = lo;
-        load(lens);
-        const int off = t - pre[b];
+        chunks = chunks_;
+        load(q, group);
+        const int off = t - q.pre[b];
         u = off / tiles;
         j = off - u * tiles;
     }
-    __device__ __forceinline__ void load(const int *lens) {
-        len = lens[b];
+    __device__ __forceinline__ void load(const Seqs &q, int group) {
+        len = q.lens[b];
         tiles = (len + TK - 1) / TK;
+        if constexpr (EXT == PREFIX) {
+            plen = q.plen[b];
+            pt = (plen + TK - 1) / TK;
+            tiles += pt;
+        }
+        if constexpr (EXT == PACKED) {
+            chunks = (q.nq[b] * group + CH - 1) / CH;
+            if (chunks == 0) tiles = 0;
+        }
     }
     // next segment (its tile 0); the caller knows that one follows
-    __device__ __forceinline__ void next(int units, const int *lens) {
+    __device__ __forceinline__ void next(const Seqs &q, int nkv, int group) {
         j = 0;
-        if (++u < units) return;
+        if (++u < nkv * chunks) return;
         u = 0;
         do {
             ++b;
-            load(lens);
+            load(q, group);
         } while (tiles == 0);
     }
 };
 
-// PRE: each sequence's tokens follow a prefix, whose part attention_cross.cu has left in pre_o and pre_ml.
-template <int D, bool F8, int BLOCKS, bool PRE>
+// EXT: PREFIX: each sequence's tokens follow a prefix, whose tiles are walked before the own ones, or (pre_o set) whose part
+// attention_cross.cu has left.  PACKED: packed rows of q over packed keys instead of a cache: the rows of a kv head's group of q
+// heads of all of a sequence's queries, CH at a time, share its keys.
+template <int D, bool F8, int BLOCKS, int EXT>
 __global__ void __launch_bounds__(Shape<D, F8, BLOCKS>::THREADS, 1)
     attention_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                             const Args a) {
     using S = Shape<D, F8, BLOCKS>;
     constexpr int STAGES = S::STAGES, CWARPS = S::CWARPS, TK = S::TK, NT = S::NT, ROWS = S::ROWS;
     constexpr bool WIDE = BLOCKS > 1, SPLIT = S::SPLIT;   // WIDE: a warp has more than 8 heads
+    constexpr int CH = EXT == PACKED ? 8 * BLOCKS : ROWS; // rows of a segment, at most
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     float *sm_o = reinterpret_cast<float *>(smem + S::OFF_O);
@@ -223,7 +246,9 @@ __global__ void __launch_bounds__(Shape<D, F8, BLOCKS>::THREADS, 1)
 
     const AttentionDecode &p = a.p;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int units = p.cache.nkv * a.chunks;
+    int *more = reinterpret_cast<int *>(smem + S::BYTES - 1024 + 15 - ((S::BYTES - 1024 + 15) & 15));   // [3][kMaxSeqs + 1], not PLAIN
+    int *plen = more, *pidx = more + kMaxSeqs + 1, *k0 = more, *q0 = pidx, *nq = pidx + kMaxSeqs + 1;
+    const Seqs sq{pre, lens, plen, pidx, k0, q0, nq};
 
     pdl_trigger();
     if (tid == 0) {
@@ -242,6 +267,20 @@ __global__ void __launch_bounds__(Shape<D, F8, BLOCKS>::THREADS, 1)
     }
     pdl_wait();
 
+    if constexpr (EXT == PREFIX) {
+        for (int i = tid; i < p.n_seqs; i += S::THREADS) plen[i] = pidx[i] = 0;
+        __syncthreads();
+        bool bad = false;
+        for (int g = tid; g < p.n_prefixes && !p.pre_o; g += S::THREADS) {
+            const int len = p.prefix_lens[g], c = min(max(len, 0), p.max_prefix);
+            const int f = p.prefix_rows ? p.prefix_rows[g] : 0, e = p.prefix_rows ? p.prefix_rows[g + 1] : p.n_seqs;
+            const int first = min(max(f, 0), p.n_seqs), end = min(max(e, 0), p.n_seqs);
+            bad |= len != c || f != first || e != end || end < first;
+            for (int b = first; b < end; ++b) plen[b] = c, pidx[b] = g;
+        }
+        if (bad && blockIdx.x == 0) report(p.status, ST_BOUNDS);
+        __syncthreads();
+    }
     // pre[b] = tiles of the sequences before b: four sequences per thread, scanned over the block
     {
         int n[4], sum = 0;
@@ -250,10 +289,25 @@ __global__ void __launch_bounds__(Shape<D, F8, BLOCKS>::THREADS, 1)
             const int b = 4 * tid + i;
             n[i] = 0;
             if (b < p.n_seqs) {
-                const int len = p.seq_lens[b], c = min(max(len, 0), p.max_len);
-                lens[b] = c;
-                if (len != c && blockIdx.x == 0) report(p.status, ST_BOUNDS);
-                n[i] = (c + TK - 1) / TK * units;
+                if constexpr (EXT == PACKED) {
+                    const auto range = [&](const int32_t *cu, int most, int &first) {   // [first, first + the result)
+                        const int f = cu ? cu[b] : 0, e = cu ? cu[b + 1] : most;
+                        first = min(max(f, 0), most);
+                        const int end = min(max(e, 0), most);
+                        if ((f != first || e != end || end < first) && blockIdx.x == 0) report(p.status, ST_BOUNDS);
+                        return max(end - first, 0);
+                    };
+                    nq[b] = range(p.cu_q, p.Tq, q0[b]);
+                    const int c = lens[b] = range(p.seq_lens, p.max_len, k0[b]);
+                    n[i] = (c + TK - 1) / TK * p.cache.nkv * ((nq[b] * a.group + CH - 1) / CH);
+                } else {
+                    const int len = p.seq_lens[b], c = min(max(len, 0), p.max_len);
+                    lens[b] = c;
+                    if (len != c && blockIdx.x == 0) report(p.status, ST_BOUNDS);
+                    n[i] = (c + TK - 1) / TK;
+                    if constexpr (EXT == PREFIX) n[i] += (plen[b] + TK - 1) / TK;
+                    n[i] *= p.cache.nkv * a.chunks;
+                }
             }
             sum += n[i];
         }
@@ -280,21 +334,22 @@ __global__ void __launch_bounds__(Shape<D, F8, BLOCKS>::THREADS, 1)
     // sequences without tokens: zero rows, or what their prefix gives
     for (int b = blockIdx.x; b < p.n_seqs; b += gridDim.x)
         if (pre[b + 1] == pre[b])
-            for (int i = tid; i < p.nq * D / 8; i += S::THREADS) {
-                uint4 x = make_uint4(0, 0, 0, 0);
-                if constexpr (PRE) {
-                    const long long at = (long long)b * p.nq + i / (D / 8);
-                    const float l = __ldcg(p.pre_ml + at).y;
-                    if (l != 0.f) {
-                        const float4 *v = reinterpret_cast<const float4 *>(p.pre_o + at * D + i % (D / 8) * 8);
-                        const float4 y = __ldcg(v), z = __ldcg(v + 1);
-                        const float f = (F8 ? p.cache.v_scale[i / (D / 8) / a.group] : 1.f) / l;
-                        x = make_uint4(pack_bf16x2(y.x * f, y.y * f), pack_bf16x2(y.z * f, y.w * f),
-                                       pack_bf16x2(z.x * f, z.y * f), pack_bf16x2(z.z * f, z.w * f));
+            for (int y = 0; y < (EXT == PACKED ? nq[b] : 1); ++y)
+                for (int i = tid; i < p.nq * D / 8; i += S::THREADS) {
+                    uint4 x = make_uint4(0, 0, 0, 0);
+                    if (EXT == PREFIX && p.pre_o) {
+                        const long long at = (long long)b * p.nq + i / (D / 8);
+                        const float l = __ldcg(p.pre_ml + at).y;
+                        if (l != 0.f) {
+                            const float4 *v = reinterpret_cast<const float4 *>(p.pre_o + at * D + i % (D / 8) * 8);
+                            const float4 y0 = __ldcg(v), y1 = __ldcg(v + 1);
+                            const float f = (F8 ? p.cache.v_scale[i / (D / 8) / a.group] : 1.f) / l;
+                            x = make_uint4(pack_bf16x2(y0.x * f, y0.y * f), pack_bf16x2(y0.z * f, y0.w * f),
+                                           pack_bf16x2(y1.x * f, y1.y * f), pack_bf16x2(y1.z * f, y1.w * f));
+                        }
                     }
+                    *reinterpret_cast<uint4 *>(p.o + (EXT == PACKED ? q0[b] + y : b) * p.ld_o + 8 * i) = x;
                 }
-                *reinterpret_cast<uint4 *>(p.o + b * p.ld_o + 8 * i) = x;
-            }
     if (blockIdx.x >= G) return;
     const unsigned run = T / G, longer = T - run * G;
     const int t0 = (int)(blockIdx.x * run + min(blockIdx.x, longer)), t1 = t0 + (int)(run + (blockIdx.x < longer));
@@ -302,10 +357,12 @@ __global__ void __launch_bounds__(Shape<D, F8, BLOCKS>::THREADS, 1)
         const unsigned split = longer * (run + 1);
         return (int)((unsigned)t < split ? (unsigned)t / (run + 1) : longer + ((unsigned)t - split) / run);
     };
-    const auto kv_head = [&](int u) { return a.chunks == 1 ? u : u / a.chunks; };
+    const auto kv_head = [&](int u, int chunks) { return chunks == 1 ? u : u / chunks; };
+    // rows of a segment, from row chunk * CH of its kv head's on
+    const auto rows_of = [&](int b, int chunk) { return min(CH, (EXT == PACKED ? nq[b] * a.group : a.group) - chunk * CH); };
 
-    Walk<TK> w;
-    w.start(t0, pre, lens, p.n_seqs);
+    Walk<TK, EXT, CH> w;
+    w.start(t0, sq, p.n_seqs, a.group, a.chunks);
 
     if (warp >= CWARPS) {
         // ------------------------------------------------ producers: q and K, V
@@ -318,19 +375,25 @@ __global__ void __launch_bounds__(Shape<D, F8, BLOCKS>::THREADS, 1)
         const int page_mask = (1 << p.cache.page_shift) - 1;
         struct Box {
             int page, place, head, n;   // n: boxes that the tile has
-            int b, u;                   // the tile's segment if it is the run's first of it, else b = -1
+            int b, u, chunks;           // the tile's segment if it is the run's first of it, else b = -1
         };
         const auto look_up = [&](int t) {
-            Box x{0, 0, 0, 0, -1, 0};
+            Box x{0, 0, 0, 0, -1, 0, 1};
             if (t >= t1) return x;
-            Walk<TK> v;
-            v.start(t, pre, lens, p.n_seqs);
-            const int key = v.j * TK + (my_box << a.box_shift);
-            x.n = min(boxes, (v.len - v.j * TK + (1 << a.box_shift) - 1) >> a.box_shift);
-            x.head = kv_head(v.u);
-            if (v.j == 0 || t == t0) x.b = v.b, x.u = v.u;
-            x.place = key & page_mask;
-            if (my_box < x.n) x.page = p.table[(long long)v.b * p.ld_table + (key >> p.cache.page_shift)];
+            Walk<TK, EXT, CH> v;
+            v.start(t, sq, p.n_seqs, a.group, a.chunks);
+            const bool front = EXT == PREFIX && v.j < v.pt;
+            const int key = (EXT == PREFIX && !front ? v.j - v.pt : v.j) * TK + (my_box << a.box_shift);
+            x.n = min(boxes, ((front ? v.plen : v.len) - (key - (my_box << a.box_shift)) + (1 << a.box_shift) - 1) >> a.box_shift);
+            x.head = kv_head(v.u, v.chunks);
+            if (v.j == 0 || t == t0) x.b = v.b, x.u = v.u, x.chunks = v.chunks;
+            if constexpr (EXT == PACKED) {
+                x.place = k0[v.b] + key;
+            } else {
+                x.place = key & page_mask;
+                const int32_t *table = front ? p.prefix_table + (long long)pidx[v.b] * p.ld_prefix : p.table + (long long)v.b * p.ld_table;
+                if (my_box < x.n) x.page = table[key >> p.cache.page_shift];
+            }
             return x;
         };
         int stage = 0, round = 0, segs = 0;
@@ -341,19 +404,22 @@ __global__ void __launch_bounds__(Shape<D, F8, BLOCKS>::THREADS, 1)
             for (int i = 0; i < per && tb + i < t1; ++i) {
                 // a segment's q rows come first, into one of two buffers
                 const int qb = __shfl_sync(0xffffffffu, cur.b, i * boxes), qu = __shfl_sync(0xffffffffu, cur.u, i * boxes);
+                const int qc = EXT == PACKED ? __shfl_sync(0xffffffffu, cur.chunks, i * boxes) : a.chunks;
                 if (qb >= 0 && !is_v) {
                     const int buf = segs & 1;
                     if (segs > 1) ok = mbar_wait(q_empty + buf, ((segs >> 1) - 1) & 1, abort);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
-                    const int head = kv_head(qu), chunk = qu - head * a.chunks;
-                    const int rows = min(ROWS, a.group - chunk * ROWS);
+                    const int head = kv_head(qu, qc), chunk = qu - head * qc;
+                    const int rows = rows_of(qb, chunk);
                     if (lane == 0) mbar_arrive_expect_tx(q_full + buf, rows * D * 2);
                     __syncwarp();
                     if (lane < rows)
                         bulk_load(smem + S::OFF_Q + (buf * ROWS + lane) * S::LDQ,
-                                  p.q + qb * p.ld_q + (long long)(head * a.group + chunk * ROWS + lane) * D, D * 2,
-                                  q_full + buf);
+                                  EXT == PACKED ? p.q + (q0[qb] + (chunk * CH + lane) / a.group) * p.ld_q +
+                                                      (long long)(head * a.group + (chunk * CH + lane) % a.group) * D
+                                                : p.q + qb * p.ld_q + (long long)(head * a.group + chunk * CH + lane) * D,
+                                  D * 2, q_full + buf);
                     ++segs;
                 }
                 if (round > 0) ok = mbar_wait(empty + stage, (round - 1) & 1, abort);
@@ -406,15 +472,21 @@ __global__ void __launch_bounds__(Shape<D, F8, BLOCKS>::THREADS, 1)
     // parts of segments that other CTAs share, joined at the end: [0] the run's first segment if it
     // began before the run, [1] its last if it goes on behind it
     struct Part {
-        int b, u, seg, seg_end;
+        int b, kvh, chunk, seg, seg_end;
     } shared[2];
     shared[0].b = shared[1].b = -1;
     const int trow = tid / (D / 4), tcol = tid % (D / 4) * 4;   // this thread's output in the sums of the joins
-    // PRE, up to 8 heads: this thread's share of the prefix's part, loaded at the segment's beginning (early)
+    // PREFIX, up to 8 heads: this thread's share of the prefix's part, loaded at the segment's beginning (early)
     float2 pre_ml = make_float2(0.f, 0.f);
     float4 pre_x = make_float4(0.f, 0.f, 0.f, 0.f);
-    const auto store = [&](int b, int h, float4 v, float m, float l, float vs, bool early) {
-        if constexpr (PRE) {   // one more part
+    const auto store = [&](int b, int kvh, int row, float4 v, float m, float l, float vs, bool early) {   // row of the kv head's
+        int h = kvh * a.group + row;
+        long long out = b;
+        if constexpr (EXT == PACKED) {
+            h = kvh * a.group + row % a.group;
+            out = q0[b] + row / a.group;
+        }
+        if (EXT == PREFIX && p.pre_o) {   // one more part
             const long long at = (long long)b * p.nq + h;
             const float2 ml = early ? pre_ml : __ldcg(p.pre_ml + at);
             if (ml.y != 0.f) {   // (no value is used where the prefix is empty)
@@ -427,7 +499,7 @@ __global__ void __launch_bounds__(Shape<D, F8, BLOCKS>::THREADS, 1)
             }
         }
         const float inv = 1.f / l, f = inv * vs;
-        *reinterpret_cast<uint2 *>(p.o + b * p.ld_o + (long long)h * D + tcol) =
+        *reinterpret_cast<uint2 *>(p.o + out * p.ld_o + (long long)h * D + tcol) =
             make_uint2(pack_bf16x2(v.x * f, v.y * f), pack_bf16x2(v.z * f, v.w * f));
         if (a.stat && tcol == 0) a.stat[(long long)b * p.nq + h] = make_float2(m, inv * S::UP);
     };
@@ -443,11 +515,11 @@ __global__ void __launch_bounds__(Shape<D, F8, BLOCKS>::THREADS, 1)
     for (int t = t0; t < t1; ++segs) {
         const int seg = t - w.j, seg_end = seg + w.tiles;   // this segment's tiles in the whole row of tiles
         const int j1 = min(w.tiles, t1 - seg);              // this run's part of it: [w.j, j1)
-        const int kvh = kv_head(w.u), chunk = w.u - kvh * a.chunks, h0 = kvh * a.group + chunk * ROWS;
-        const int rows = min(ROWS, a.group - chunk * ROWS);   // heads of the segment
+        const int kvh = kv_head(w.u, w.chunks), chunk = w.u - kvh * w.chunks, h0 = kvh * a.group + chunk * CH;
+        const int rows = rows_of(w.b, chunk);               // heads of the segment
 
-        if constexpr (PRE && BLOCKS == 1) {
-            if (trow < rows) {
+        if constexpr (EXT == PREFIX && BLOCKS == 1) {
+            if (trow < rows && p.pre_o) {
                 const long long at = (long long)w.b * p.nq + h0 + trow;
                 pre_ml = __ldcg(p.pre_ml + at);
                 pre_x = __ldcg(reinterpret_cast<const float4 *>(p.pre_o + at * D + tcol));
@@ -512,8 +584,9 @@ __global__ void __launch_bounds__(Shape<D, F8, BLOCKS>::THREADS, 1)
         for (; w.j < j1; ++w.j, ++t, turn = turn + 1 == S::GROUPS ? 0 : turn + 1) {
             if (SPLIT || turn == group) {
                 if (!mbar_wait(full + stage, round & 1, abort)) give_up();
-                const int key0 = w.j * TK + slice;
-                if (key0 < w.len) {
+                const bool front = EXT == PREFIX && w.j < w.pt;
+                const int key0 = (EXT == PREFIX && !front ? w.j - w.pt : w.j) * TK + slice, len = front ? w.plen : w.len;
+                if (key0 < len) {
                     const uint32_t kt = smem_u32(smem + stage * 2 * S::TILE), vt = kt + S::TILE;
                     float s[NT][4] = {};
                     if constexpr (F8) {
@@ -547,7 +620,7 @@ __global__ void __launch_bounds__(Shape<D, F8, BLOCKS>::THREADS, 1)
                             #pragma unroll
                             for (int k = 0; k < 4; ++k) s[n][k] += s2[n][k];
                     }
-                    const bool tail = key0 + S::KS > w.len;
+                    const bool tail = key0 + S::KS > len;
                     float x0 = -INFINITY, x1 = -INFINITY;
                     #pragma unroll
                     for (int n = 0; n < NT; ++n)
@@ -555,11 +628,11 @@ __global__ void __launch_bounds__(Shape<D, F8, BLOCKS>::THREADS, 1)
                         for (int k = 0; k < 2; ++k) {
                             s[n][k] *= scale0;
                             if (WIDE) s[n][2 + k] *= scale1;
-                            if (tail && key0 + 8 * n + 2 * tq + k >= w.len) s[n][k] = s[n][2 + k] = -INFINITY;
+                            if (tail && key0 + 8 * n + 2 * tq + k >= len) s[n][k] = s[n][2 + k] = -INFINITY;
                             x0 = fmaxf(x0, s[n][k]);
                             if (WIDE) x1 = fmaxf(x1, s[n][2 + k]);
                         }
-                    if (a.scores) {
+                    if (EXT != PACKED && a.scores && !front) {
                         #pragma unroll
                         for (int n = 0; n < NT; ++n) {
                             float *dst = a.scores + ((long long)w.b * p.nq + h0 + wrow + g) * a.ld_scores + key0 + 8 * n + 2 * tq;
@@ -621,7 +694,7 @@ __global__ void __launch_bounds__(Shape<D, F8, BLOCKS>::THREADS, 1)
                         // values behind the sequence may be anything (0 * NaN): cleared in the last slice
                         uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
                         if (tail) {
-                            const int left = w.len - key0 - 16 * y - 2 * tq;
+                            const int left = len - key0 - 16 * y - 2 * tq;
                             keep0 = (left > 0 ? 0xffffu : 0u) | (left > 1 ? 0xffff0000u : 0u);
                             keep1 = (left > 8 ? 0xffffu : 0u) | (left > 9 ? 0xffff0000u : 0u);
                         }
@@ -679,7 +752,7 @@ __global__ void __launch_bounds__(Shape<D, F8, BLOCKS>::THREADS, 1)
         const bool whole = seg >= t0 && seg_end <= t1;
         const float vs = F8 ? p.cache.v_scale[kvh] : 1.f;
         const int slot = 2 * blockIdx.x + (seg < t0 ? 0 : 1);
-        if (!whole) shared[seg < t0 ? 0 : 1] = Part{w.b, w.u, seg, seg_end};
+        if (!whole) shared[seg < t0 ? 0 : 1] = Part{w.b, kvh, chunk, seg, seg_end};
         #pragma unroll
         for (int r8 = 0; r8 < (WIDE ? 16 : 8); r8 += 8) {
             // the warps that share rows: all, or (SPLIT) those of a group
@@ -724,7 +797,7 @@ __global__ void __launch_bounds__(Shape<D, F8, BLOCKS>::THREADS, 1)
                     acc.w += x.w;
                 }
                 if (whole) {
-                    store(w.b, h0 + row, acc, mm, ll, vs, PRE && BLOCKS == 1);
+                    store(w.b, kvh, chunk * CH + row, acc, mm, ll, vs, BLOCKS == 1);
                 } else {
                     *reinterpret_cast<float4 *>(a.part + ((long long)slot * ROWS + row) * D + tcol) = acc;
                     if (tcol == 0) a.ml[slot * ROWS + row] = make_float2(mm, ll);
@@ -732,7 +805,7 @@ __global__ void __launch_bounds__(Shape<D, F8, BLOCKS>::THREADS, 1)
             }
             compute_sync<CWARPS * 32>();
         }
-        if (t < t1) w.next(units, lens);
+        if (t < t1) w.next(sq, p.cache.nkv, a.group);
     }
 
     // ---------------------------------------------------- join the parts of shared segments
@@ -768,8 +841,7 @@ __global__ void __launch_bounds__(Shape<D, F8, BLOCKS>::THREADS, 1)
         if (!s_last[x]) continue;
         const Part y = x ? shared[1] : shared[0];
         const int first = owner(y.seg), n = owner(y.seg_end - 1) - first + 1, begin = group_of(first, n);
-        const int kvh = kv_head(y.u), chunk = y.u - kvh * a.chunks;
-        const int rows = min(ROWS, a.group - chunk * ROWS);
+        const int kvh = y.kvh, chunk = y.chunk, rows = rows_of(y.b, chunk);
         const float vs = F8 ? p.cache.v_scale[kvh] : 1.f;
         // The parts begin, begin + STEP, ... (count of them): up to BATCH at a time, all their loads in flight.  A lane
         // takes four columns of each, and of one part (lane li: part li of the batch) the row's maximum and sum.
@@ -812,7 +884,7 @@ __global__ void __launch_bounds__(Shape<D, F8, BLOCKS>::THREADS, 1)
                 for (int off = LPR / 2; off > 0; off >>= 1) ll += __shfl_xor_sync(0xffffffffu, ll, off);
                 if (r0 + trow < rows) {
                     if (final) {
-                        store(y.b, kvh * a.group + chunk * ROWS + row, acc, mm, ll, vs, false);
+                        store(y.b, kvh, chunk * CH + row, acc, mm, ll, vs, false);
                     } else {
                         *reinterpret_cast<float4 *>(a.part + head * D + tcol) = acc;
                         if (tcol == 0) a.ml[head] = make_float2(mm, ll);
@@ -869,6 +941,7 @@ __global__ void __launch_bounds__(256) attention_weight_kernel(const AttentionDe
     }
 }
 
+constexpr double kPrefixAgain = 6e7;   // bytes
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 
 // Workspace: arrival counters, partial outputs, their (m, l), then with weights (m, 1/l) and scores.
@@ -878,7 +951,8 @@ struct Layout {
 };
 Layout layout(int ctas, int n_seqs, int nq, int max_len, bool weights) {
     Layout y;
-    y.part = 3 * MAX_CTAS * sizeof(uint32_t);
+    static_assert(3 * MAX_CTAS * sizeof(uint32_t) == kArrivalBytes, "");
+    y.part = kArrivalBytes;
     y.ml = y.part + (size_t)ctas * 2 * MAX_ROWS * 128 * sizeof(float);
     y.stat = y.ml + up256((size_t)ctas * 2 * MAX_ROWS * sizeof(float2));
     y.ld_scores = (max_len + WK - 1) / WK * WK;
@@ -887,22 +961,30 @@ Layout layout(int ctas, int n_seqs, int nq, int max_len, bool weights) {
     return y;
 }
 
-template <int D, bool F8, int BLOCKS, bool PRE>
+template <int D, bool F8, int BLOCKS, int EXT>
 cudaError_t launch_kernel(const CUtensorMap &tk, const CUtensorMap &tv, const Args &a, int grid, cudaStream_t st) {
     static std::atomic<bool> ready[kMaxDevices];   // the shared-memory opt-in, per device
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
-    constexpr int bytes = Shape<D, F8, BLOCKS>::BYTES;
+    constexpr int bytes = Shape<D, F8, BLOCKS>::BYTES + (EXT == PLAIN ? 0 : 3 * 4 * (kMaxSeqs + 1) + 32);
     static_assert(bytes <= 232448, "shared memory of one CTA");
     if (!ready[dev].load()) {
-        cudaError_t e = cudaFuncSetAttribute(attention_decode_kernel<D, F8, BLOCKS, PRE>,
+        cudaError_t e = cudaFuncSetAttribute(attention_decode_kernel<D, F8, BLOCKS, EXT>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e != cudaSuccess) return e;
         ready[dev].store(true);
     }
     cudaLaunchAttribute at[1];
     cudaLaunchConfig_t cfg = pdl_config(dim3(grid), dim3(Shape<D, F8, BLOCKS>::THREADS), bytes, st, at);
-    return cudaLaunchKernelEx(&cfg, attention_decode_kernel<D, F8, BLOCKS, PRE>, tk, tv, a);
+    return cudaLaunchKernelEx(&cfg, attention_decode_kernel<D, F8, BLOCKS, EXT>, tk, tv, a);
+}
+
+// With 8 * BLOCKS rows per segment.
+template <int D, bool F8, int EXT>
+cudaError_t launch_blocks(int blocks, const CUtensorMap &tk, const CUtensorMap &tv, const Args &a, int grid, cudaStream_t st) {
+    return blocks == 1 ? launch_kernel<D, F8, 1, EXT>(tk, tv, a, grid, st)
+                       : blocks == 2 ? launch_kernel<D, F8, 2, EXT>(tk, tv, a, grid, st)
+                                     : launch_kernel<D, F8, 4, EXT>(tk, tv, a, grid, st);
 }
 
 }  // namespace
@@ -945,18 +1027,17 @@ cudaError_t launch_attention_decode(const AttentionDecode &p, cudaStream_t st) {
     if (!make_tmap_cache(&tk, p.cache, p.cache.k) || !make_tmap_cache(&tv, p.cache, p.cache.v))
         return cudaErrorInvalidValue;
     // one CTA per SM, fewer where the lengths cannot hold as many tiles
-    const long long most = (long long)p.n_seqs * p.cache.nkv * a.chunks * ((p.max_len + (p.cache.f8 ? 127 : 63)) / (p.cache.f8 ? 128 : 64));
+    const int tile = p.cache.f8 ? 128 : 64;
+    const bool prefix = p.pre_o || p.n_prefixes > 0;
+    const long long tiles = (p.max_len + tile - 1) / tile + (p.pre_o ? 0 : (p.max_prefix + tile - 1) / tile);
+    const long long most = (long long)p.n_seqs * p.cache.nkv * a.chunks * tiles;
     const int grid = (int)std::min<long long>(sms, std::max<long long>(most, 1));
+    const int blocks = a.group <= 8 ? 1 : split ? 4 : 2;
     const auto run = [&](auto d, auto f8) {
         constexpr int D = decltype(d)::value;
         constexpr bool F8 = decltype(f8)::value;
-        const auto with = [&](auto pre) {
-            constexpr bool PRE = decltype(pre)::value;
-            return a.group <= 8 ? launch_kernel<D, F8, 1, PRE>(tk, tv, a, grid, st)
-                                : (split ? launch_kernel<D, F8, 4, PRE>(tk, tv, a, grid, st)
-                                         : launch_kernel<D, F8, 2, PRE>(tk, tv, a, grid, st));
-        };
-        return p.pre_o ? with(std::true_type{}) : with(std::false_type{});
+        return prefix ? launch_blocks<D, F8, PREFIX>(blocks, tk, tv, a, grid, st)
+                      : launch_blocks<D, F8, PLAIN>(blocks, tk, tv, a, grid, st);
     };
     const std::integral_constant<int, 128> d128;
     const std::integral_constant<int, 64> d64;
@@ -967,5 +1048,51 @@ cudaError_t launch_attention_decode(const AttentionDecode &p, cudaStream_t st) {
     cudaLaunchConfig_t cfg = pdl_config(dim3((p.max_len + WK - 1) / WK, p.n_seqs), dim3(256), 0, st, at);
     return cudaLaunchKernelEx(&cfg, attention_weight_kernel, p, (const float *)a.scores, (const float2 *)a.stat, a.ld_scores);
 }
+
+bool attention_prefix_near(const AttentionDecode &p) {
+    // What the sequences read again (from L2, where a prefix of this size stays) against the two launches and the wait for
+    // them that a pass over the prefixes costs.
+    const double again = 2.0 * p.n_seqs * p.max_prefix * p.cache.nkv * p.cache.d * (p.cache.f8 ? 1 : 2);
+    const double tiles = (double)p.n_seqs * p.nq * ((p.max_len + 63) / 64 + (p.max_prefix + 63) / 64);
+    return again <= kPrefixAgain && tiles < INT_MAX - 65;
+}
+
+int attention_packed_rows(int Tq, int Tk, int n_segs, int nq, int nkv) {
+    // Rows of a segment if the queries are spread evenly.  Up to 32: its keys are read once; beyond, 128 rows of a tcgen05 tile.
+    const long long group = nq / nkv, rows = group * ((Tq + n_segs - 1) / n_segs);
+    if (rows > 32) return 0;
+    const long long chunks = (Tq * group + 7) / 8 + n_segs;
+    return nkv * chunks * ((long long)Tk / 64 + 1) > INT_MAX - 65 ? 0 : (int)std::max(rows, 1LL);
+}
+
+cudaError_t launch_attention_packed(const AttentionCross &c, int rows, cudaStream_t st) {
+    if (c.Tq <= 0 || c.n_segs <= 0) return cudaSuccess;
+    const int sms = device_num_sms();
+    if (sms <= 0) return cudaErrorNoDevice;
+    const Layout y = layout(sms, c.n_segs, c.nq, 0, false);
+    Args a{};
+    AttentionDecode &p = a.p;
+    p.q = c.q; p.o = c.o; p.ld_q = c.ld_q; p.ld_o = c.ld_o;
+    p.cache.nkv = c.nkv; p.cache.d = c.d; p.cache.num_pages = 1; p.cache.page_shift = 30;
+    p.seq_lens = c.cu_k; p.cu_q = c.cu_q; p.Tq = c.Tq;
+    p.n_seqs = c.n_segs; p.nq = c.nq; p.max_len = c.max_keys; p.status = c.status;
+    a.group = c.nq / c.nkv;
+    a.chunks = 1;
+    a.box_shift = 6;
+    char *ws = static_cast<char *>(c.workspace);
+    a.count = reinterpret_cast<uint32_t *>(ws);
+    a.part = reinterpret_cast<float *>(ws + y.part);
+    a.ml = reinterpret_cast<float2 *>(ws + y.ml);
+    CUtensorMap tk, tv;
+    const bool any = c.max_keys > 0;   // (without any key nothing is loaded; a map still needs an address)
+    if (!make_tmap_packed(&tk, any ? c.k : c.q, c.d, any ? c.nkv : 1, any ? c.max_keys : 1, any ? c.ld_k : c.d) ||
+        !make_tmap_packed(&tv, any ? c.v : c.q, c.d, any ? c.nkv : 1, any ? c.max_keys : 1, any ? c.ld_v : c.d))
+        return cudaErrorInvalidValue;
+    const int blocks = rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
+    return c.d == 128 ? launch_blocks<128, false, PACKED>(blocks, tk, tv, a, sms, st)
+                      : launch_blocks<64, false, PACKED>(blocks, tk, tv, a, sms, st);
+}
+
+size_t attention_packed_workspace_bytes(int num_sms) { return layout(num_sms, 0, 1, 0, false).bytes; }
 
 }  // namespace h3

@@ -1263,6 +1263,19 @@ bool make_tmap_heads(CUtensorMap *m, const bf16 *base, int d, int group, int nkv
     return r == CUDA_SUCCESS;
 }
 
+bool make_tmap_packed(CUtensorMap *m, const bf16 *base, int d, int heads, long long rows, long long ld) {
+    PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)rows, (cuuint64_t)heads, 1};
+    const cuuint64_t strides[3] = {(cuuint64_t)ld * 2, (cuuint64_t)d * 2, (cuuint64_t)ld * 2};
+    const cuuint32_t box[4] = {64, 64, 1, 1};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<bf16 *>(base), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+}
+
 bool make_tmap_pages(CUtensorMap *m, const KvCache &c, const void *base, int places) {
     PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
     if (!fn) return false;

@@ -246,8 +246,15 @@ struct AttentionDecode {
     const float *weight_in;
     float *weight_out;
     long long ld_weight;
-    const float *pre_o;      // what launch_attention_cross left of a prefix in front of the tokens; NULL: none
+    // Prefixes in front of the tokens: pages and lengths (n_prefixes 0: none), sequences [prefix_rows[g], prefix_rows[g + 1]) behind
+    // prefix g; or (pre_o set) what launch_attention_cross left of them.
+    const int32_t *prefix_table, *prefix_lens, *prefix_rows;
+    int ld_prefix, n_prefixes, max_prefix;
+    const float *pre_o;
     const float2 *pre_ml;
+    // launch_attention_packed: rows [cu_q[b], cu_q[b + 1]) of the Tq of q, over keys [seq_lens[b], seq_lens[b + 1]) of max_len
+    const int32_t *cu_q;
+    int Tq;
     void *workspace;
     int32_t *status;
 };
@@ -273,6 +280,15 @@ size_t attention_cross_workspace_bytes(int num_sms, int d);
 // Bound on the steps (of a row tile and 128 keys) of a call; -1 where they pass 2e9.
 long long attention_cross_weight(int Tq, int max_keys, int n_segs, int nq, int nkv);
 cudaError_t launch_attention_cross(const AttentionCross &p, cudaStream_t st);
+// The same for few rows per kv head and segment, by the decoding kernel: how many (a plan from sizes that the host knows; any lengths are
+// right), 0 where launch_attention_cross is the one to take.  The workspace's first attention_packed_workspace_bytes() bytes
+// are its own: arrival counters, zero before the first call.
+int attention_packed_rows(int Tq, int Tk, int n_segs, int nq, int nkv);
+cudaError_t launch_attention_packed(const AttentionCross &p, int rows, cudaStream_t st);
+size_t attention_packed_workspace_bytes(int num_sms);
+constexpr size_t kArrivalBytes = 3 * 1024 * 4;   // the arrival counters at the head of an attention workspace
+// Tensor map of packed bf16 rows as [1][head][row][element], in boxes of 64 rows x 128 bytes of one head, swizzled by 128 bytes.
+bool make_tmap_packed(CUtensorMap *m, const bf16 *base, int d, int heads, long long rows, long long ld);
 // Tensor map of bf16 rows as [row][kv head][head of the group][element], read in boxes of `rows_box` rows x `heads_box` heads x 64
 // elements (heads_box 0: [row][head][element]), swizzled by 128 bytes.  False if the driver refuses it.
 bool make_tmap_heads(CUtensorMap *m, const bf16 *base, int d, int group, int nkv, long long rows, long long ld, int heads_box,
@@ -281,6 +297,9 @@ bool make_tmap_heads(CUtensorMap *m, const bf16 *base, int d, int group, int nkv
 // bytes, e4m3 whole rows without swizzle.
 bool make_tmap_pages(CUtensorMap *m, const KvCache &cache, const void *base, int places);
 
+// Whether sequences behind shared prefixes read them again each, in one launch, rather than in a pass over them that serves
+// all (launch_attention_cross).
+bool attention_prefix_near(const AttentionDecode &p);
 // Tensor map of the cache's keys or values (`base` = cache.k or cache.v) as [page][kv head][place]
 // [element], read in boxes of min(page_size, 64) places x 128 bytes (64 for e4m3 with d = 64) of one
 // head, swizzled by that width.  False if the driver refuses it.

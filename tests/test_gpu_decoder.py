@@ -317,8 +317,7 @@ def _check_cross(got, q, k, v, p_err=2.0 ** -8):
 
 
 def _cross_ws(d):
-    # of any content: filled with NaN bits
-    return torch.full((Q.h3enc_op_attention_cross_workspace_bytes(d),), 255, dtype=torch.uint8, device="cuda")
+    return torch.zeros(Q.h3enc_op_attention_cross_workspace_bytes(d), dtype=torch.uint8, device="cuda")
 
 
 CROSS = [
@@ -326,7 +325,8 @@ CROSS = [
     ([1] * 7, [0, 1, 127, 128, 129, 300, 256], 40, 2, 128), ([3, 0, 130, 1, 33], [128, 50, 0, 700, 5], 8, 8, 64),
     ([300], [513], 4, 2, 64), ([257, 129], [640, 77], 28, 4, 128), ([40], [333], 10, 10, 128), ([700], [129], 2, 1, 128),
     ([5, 9], [260, 1], 130, 1, 64), ([70], [200], 256, 2, 64), ([2] * 150, [3 + i % 200 for i in range(150)], 4, 1, 128),
-    ([1000], [64], 18, 18, 64), ([31], [9000], 5, 1, 128), ([513, 1], [1, 4097], 20, 4, 64)]
+    ([1000], [64], 18, 18, 64), ([3, 2, 0, 4], [90, 700, 64, 0], 8, 1, 128), ([2, 3], [5, 1500], 12, 1, 64), ([1, 0, 900], [3, 77, 200], 4, 2, 64),
+    ([32] * 3, [65, 1, 640], 6, 6, 128), ([1] * 1000 + [40], [1 + i % 9 for i in range(1000)] + [500], 2, 1, 64), ([31], [9000], 5, 1, 128), ([513, 1], [1, 4097], 20, 4, 64)]
 
 
 @pytest.mark.parametrize("qlens,klens,nq,nkv,d", CROSS)
@@ -484,8 +484,14 @@ SHARED = [
     ([33], [4000], [10] * 33, 12, 1, 128, E4M3, 16)]
 
 
+def _far_bound(n, nkv, d, dtype):
+    """A bound on the prefixes' lengths with which the call passes over them once for all (it goes by the bound)."""
+    return int(6e7 / (2 * n * nkv * d * (2 if dtype == BF16 else 1))) + 1
+
+
+@pytest.mark.parametrize("far", [False, True])
 @pytest.mark.parametrize("groups,plens,lens,nq,nkv,d,dtype,page", SHARED)
-def test_attention_decode_shared(groups, plens, lens, nq, nkv, d, dtype, page):
+def test_attention_decode_shared(groups, plens, lens, nq, nkv, d, dtype, page, far):
     g = _gen(sum(plens) + sum(lens) + nq)
     n, rows = len(lens), np.concatenate([[0], np.cumsum(groups)])
     assert rows[-1] == n
@@ -494,7 +500,9 @@ def test_attention_decode_shared(groups, plens, lens, nq, nkv, d, dtype, page):
     pages = len(plens) * pcols + n * cols + 2
     cache = _pool(g, pages, nkv, page, d, dtype, apart=16)
     ids = torch.randperm(pages, device="cuda", generator=g).to(torch.int32)
-    ptable = torch.cat([ids[:len(plens) * pcols].view(len(plens), pcols), ids.new_full((len(plens), 2), -1)], 1).contiguous()
+    if far:
+        max_prefix = max(max_prefix, _far_bound(n, nkv, d, dtype))
+    ptable = torch.cat([ids[:len(plens) * pcols].view(len(plens), pcols), ids.new_full((len(plens), 2 - (-max_prefix // page) - pcols), -1)], 1).contiguous()
     table = ids[len(plens) * pcols:][:n * cols].view(n, cols).contiguous()
 
     def tokens(ls):
@@ -553,21 +561,25 @@ def test_attention_decode_shared_without_prefixes_is_attention_decode():
     Q.h3enc_op_attention_decode_shared(q, b, cache, table[:0], _i32([]), 0, table, _i32(lens), nq, 128, ws)
     assert torch.equal(a, b)
     # sequences of no group, and a group whose prefix is empty, have none either
-    Q.h3enc_op_attention_decode_shared(q, c, cache, table[:2], _i32([0, 0]), 64, table, _i32(lens), nq, 128, ws,
-                                       prefix_rows=_i32([1, 2, 4]))
-    assert torch.equal(a, c)
+    for bound in (64, _far_bound(n, nkv, d, BF16)):
+        wide = table.new_zeros(2, -(-bound // page))
+        Q.h3enc_op_attention_decode_shared(q, c, cache, wide, _i32([0, 0]), bound, table, _i32(lens), nq, 128, ws,
+                                           prefix_rows=_i32([1, 2, 4]))
+        assert torch.equal(a, c)
     Q.h3enc_op_attention_decode(q, c, cache, table, _i32(lens), nq, 128, ws)      # the workspace serves both
     assert torch.equal(a, c)
 
 
+@pytest.mark.parametrize("far", [False, True])
 @pytest.mark.parametrize("dtype", [BF16, E4M3])
-def test_attention_decode_shared_reports_bad_pages_and_lengths(dtype):
+def test_attention_decode_shared_reports_bad_pages_and_lengths(dtype, far):
     """A page outside the cache reads as zero keys and values; a length outside its bound is clamped into it."""
     g = _gen(12)
     n, nq, nkv, d, page = 3, 4, 2, 64, 16
     cache = _pool(g, 30, nkv, page, d, dtype)
     ids = torch.randperm(30, device="cuda", generator=g).to(torch.int32)
-    ptable, table = ids[:8].view(1, 8).contiguous(), ids[8:14].view(3, 2).contiguous()
+    spare = _far_bound(n, nkv, d, dtype) // page + 1 if far else 0
+    ptable, table = torch.cat([ids[:8], ids.new_full((spare,), -1)]).view(1, -1), ids[8:14].view(3, 2).contiguous()
     pk, pv = ([torch.randn(120, nkv, d, device="cuda", generator=g)] for _ in range(2))
     k, v = ([torch.randn(20, nkv, d, device="cuda", generator=g) for _ in range(n)] for _ in range(2))
     (pk, pv), = _fill(cache, ptable, [120], pk, pv)
@@ -591,11 +603,13 @@ def test_attention_decode_shared_reports_bad_pages_and_lengths(dtype):
             want, _ = O.decoder.attend_prefix(_f64(q[b]).reshape(nq, d), kk, vv, *own[b])
             assert np.abs(_f64(o[b]).reshape(nq, d) - want).max() <= 2.0 ** -6
 
+    bound = page * spare if far else 120
     for page_no in (-1, 30, 2 ** 31 - 1, -(2 ** 31)):
-        check(page_no, 120, 120)
-    check(None, 121, 120)
-    check(None, -3, 120)
-    check(None, 2 ** 31 - 1, 33)
+        check(page_no, 120, bound)
+    check(None, -3, bound)
+    if not far:       # (the table holds no page for what a clamped length of that bound would read)
+        check(None, 121, 120)
+        check(None, 2 ** 31 - 1, 33)
 
 
 # ---------------------------------------------------------------- a run of them together
