@@ -75,20 +75,21 @@ struct Shape {
     static constexpr int THREADS = F8 ? 512 : 384;
     static constexpr int ATOM = TQ * 128;                  // 64 columns of a 128-row tile
     static constexpr int TILE = TK * D * 2;                // one operand tile
-    // K and V tiles held; e4m3: a K tile is free again as soon as its scores are done, a V tile only behind the softmax
-    static constexpr int NSK = (D == 128 ? 2 : 4) / (F8 ? 2 : 1), NSV = D == 128 ? 2 : 4;
-    static constexpr int RAW = TK * D;                     // one e4m3 tile
-    static constexpr int RS = F8 ? (D == 128 ? 3 : 8) : 0;
+    static constexpr int NSK = D == 128 ? 2 : F8 ? 3 : 4, NSV = NSK;   // K tiles, and V tiles, held
+    // An e4m3 tile arrives in the second half of its place, where (128 columns) a row's 128 bytes are those of the f16 row's own second
+    // half, so that a warp can convert its rows in place; 64 columns: beside the places.
+    static constexpr int RAW = TK * D;
+    static constexpr int RAWS = F8 && D == 64 ? NSK + NSV : 0;
     static constexpr int OFF_Q = 0;
     static constexpr int OFF_K = OFF_Q + 2 * TILE;
     static constexpr int OFF_V = OFF_K + NSK * TILE;
     static constexpr int OFF_RAW = OFF_V + NSV * TILE;
-    static constexpr int OFF_SEG = OFF_RAW + RS * RAW;     // pre, cq, ck
+    static constexpr int OFF_SEG = OFF_RAW + RAWS * RAW;   // pre, cq, ck
     static constexpr int OFF_ITEM = OFF_SEG + 3 * 4 * (kMaxSeqs + 4);  // ring of items
     static constexpr int OFF_ML = OFF_ITEM + ITEMS * (int)sizeof(Item);   // [128] (m, l) of tile B's share of a single tile's rows
     static constexpr int OFF_OUT = OFF_ML + 128 * 8;       // 32 rows x 64 bytes of output per softmax warp
     static constexpr int OFF_BAR = OFF_OUT + (MODE == ROWS ? 8 * 2048 : 0);
-    static constexpr int BARS = 2 * NSK + 2 * NSV + 18 + 2 * ITEMS + 2 * RS;
+    static constexpr int BARS = 2 * NSK + 2 * NSV + 18 + 2 * ITEMS + (F8 ? NSK + NSV : 0);
     static constexpr int READERS = 11 + (F8 ? 4 : 0);      // warps that read an item
     static constexpr int BYTES = OFF_BAR + BARS * 8 + 128 + 1024;   // + alignment of the base
     static constexpr float UP = F8 ? 8192.f : 1.f;         // weights, and so l and o, are held times this
@@ -285,10 +286,10 @@ __global__ void __launch_bounds__(Shape<D, MODE>::THREADS, 1)
                            const __grid_constant__ CUtensorMap tmV, const __grid_constant__ Args a) {
     using S = Shape<D, MODE>;
     constexpr bool F8 = S::F8;
-    constexpr int NSK = S::NSK, NSV = S::NSV, RS = S::RS;
+    constexpr int NSK = S::NSK, NSV = S::NSV;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-    uint8_t *sQ = smem + S::OFF_Q, *sK = smem + S::OFF_K, *sV = smem + S::OFF_V, *sRaw = smem + S::OFF_RAW;
+    uint8_t *sQ = smem + S::OFF_Q, *sK = smem + S::OFF_K, *sV = smem + S::OFF_V;
     int *pre = reinterpret_cast<int *>(smem + S::OFF_SEG), *cq = pre + kMaxSeqs + 4, *ck = cq + kMaxSeqs + 4;
     Item *ring = reinterpret_cast<Item *>(smem + S::OFF_ITEM);
     float2 *ml_s = reinterpret_cast<float2 *>(smem + S::OFF_ML);
@@ -297,8 +298,8 @@ __global__ void __launch_bounds__(Shape<D, MODE>::THREADS, 1)
     uint64_t *q_full = v_empty + NSV, *q_ready = q_full + 2, *q_empty = q_ready + 2;   // [2] row tile, from here on
     uint64_t *s_full = q_empty + 2, *p_full = s_full + 2, *pv_done = p_full + 2, *l_full = pv_done + 2, *o_free = l_full + 1;   // [1], [1]
     uint64_t *turn = o_free + 1, *drain = turn + 2, *item_full = drain + 2, *item_empty = item_full + ITEMS;
-    uint64_t *raw_full = item_empty + ITEMS, *raw_empty = raw_full + RS;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(raw_empty + RS);
+    uint64_t *k_raw = F8 ? item_empty + ITEMS : k_full, *v_raw = F8 ? k_raw + NSK : v_full;   // where TMA arrives
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(F8 ? v_raw + NSV : item_empty + ITEMS);
     volatile int *abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
     int *s_warp = reinterpret_cast<int *>(tmem_slot + 2);   // [20] scan of the warps' sums
 
@@ -331,9 +332,9 @@ __global__ void __launch_bounds__(Shape<D, MODE>::THREADS, 1)
             mbar_init(item_full + i, 1);
             mbar_init(item_empty + i, S::READERS);
         }
-        for (int i = 0; i < RS; ++i) {
-            mbar_init(raw_full + i, 1);
-            mbar_init(raw_empty + i, 4);
+        for (int i = 0; F8 && i < NSK; ++i) {
+            mbar_init(k_raw + i, 1);
+            mbar_init(v_raw + i, 1);
         }
         *abort = 0;
         fence_barrier_init();
@@ -427,6 +428,8 @@ __global__ void __launch_bounds__(Shape<D, MODE>::THREADS, 1)
         }
     }
 
+    const auto raw_k = [&](uint32_t s) { return D == 128 ? sK + s * S::TILE + S::RAW : smem + S::OFF_RAW + s * S::RAW; };
+    const auto raw_v = [&](uint32_t s) { return D == 128 ? sV + s * S::TILE + S::RAW : smem + S::OFF_RAW + (NSK + s) * S::RAW; };
     // A wait that runs out, in any warp, ends the CTA: *abort lets all other waits return, and no warp waits otherwise.
     const auto wait_on = [&](uint64_t *bar, uint32_t parity) {   // by a whole warp
         const bool good = __all_sync(0xffffffffu, wait_bar(bar, parity, abort));
@@ -720,7 +723,7 @@ __global__ void __launch_bounds__(Shape<D, MODE>::THREADS, 1)
         const int my_tile = lane >> tile_shift, my_box = lane & (boxes - 1);
         const int page_mask = MODE == ROWS ? 0 : (1 << p.cache.page_shift) - 1;
         bool ok = true;
-        uint32_t gk = 0, gv = 0, gr = 0, nq_loaded[2] = {0, 0};
+        uint32_t gk = 0, gv = 0, nq_loaded[2] = {0, 0};
         const auto wait = [&](uint64_t *bar, uint32_t parity) {
             ok = __all_sync(0xffffffffu, wait_bar(bar, parity, abort));
             return ok;
@@ -764,25 +767,14 @@ __global__ void __launch_bounds__(Shape<D, MODE>::THREADS, 1)
                     }
                 }
             };
-            const auto load_raw = [&](int j, const CUtensorMap *m) {
-                const int s = gr % (RS ? RS : 1), round = gr / (RS ? RS : 1);
-                if (round > 0 && !wait(raw_empty + s, (round - 1) & 1)) return;
-                load(j, m, sRaw + s * S::RAW, raw_full + s);
-                ++gr;
-            };
             for (int j = w.j0; j < w.j1; ++j) {
                 if (MODE != ROWS) {
                     if (j == batch + per) batch = j, page = next_page;
                     if (j == batch) next_page = look_up(j + per);
                 }
-                if constexpr (F8) {
-                    load_raw(j, &tmK);
-                    if (!ok) break;
-                } else {
-                    if (gk >= NSK && !wait(k_empty + gk % NSK, (gk / NSK - 1) & 1)) break;
-                    load(j, &tmK, sK + gk % NSK * S::TILE, k_full + gk % NSK);
-                    ++gk;
-                }
+                if (gk >= NSK && !wait(k_empty + gk % NSK, (gk / NSK - 1) & 1)) break;
+                load(j, &tmK, F8 ? raw_k(gk % NSK) : sK + gk % NSK * S::TILE, k_raw + gk % NSK);
+                ++gk;
                 if (j == w.j0) {
                     for (int t = 0; t < (w.active(1) ? 2 : 1); ++t) {   // (a single tile's rows for both)
                         if (nq_loaded[t] > 0 && !wait(q_empty + t, (nq_loaded[t] - 1) & 1)) break;
@@ -805,14 +797,9 @@ __global__ void __launch_bounds__(Shape<D, MODE>::THREADS, 1)
                     }
                     if (!ok) break;
                 }
-                if constexpr (F8) {
-                    load_raw(j, &tmV);
-                    if (!ok) break;
-                } else {
-                    if (gv >= NSV && !wait(v_empty + gv % NSV, (gv / NSV - 1) & 1)) break;
-                    load(j, &tmV, sV + gv % NSV * S::TILE, v_full + gv % NSV);
-                    ++gv;
-                }
+                if (gv >= NSV && !wait(v_empty + gv % NSV, (gv / NSV - 1) & 1)) break;
+                load(j, &tmV, F8 ? raw_v(gv % NSV) : sV + gv % NSV * S::TILE, v_raw + gv % NSV);
+                ++gv;
                 __syncwarp();
             }
         }
@@ -822,12 +809,8 @@ __global__ void __launch_bounds__(Shape<D, MODE>::THREADS, 1)
                 report(p.status, ST_TIMEOUT);
                 *abort = 1;
                 const int never = 0;
-                if constexpr (F8) {
-                    for (uint32_t f = gr > RS ? gr - RS : 0; f < gr; ++f) wait_bar(raw_full + f % RS, (f / RS) & 1, &never);
-                } else {
-                    for (uint32_t f = gk > NSK ? gk - NSK : 0; f < gk; ++f) wait_bar(k_full + f % NSK, (f / NSK) & 1, &never);
-                    for (uint32_t f = gv > NSV ? gv - NSV : 0; f < gv; ++f) wait_bar(v_full + f % NSV, (f / NSV) & 1, &never);
-                }
+                for (uint32_t f = gk > NSK ? gk - NSK : 0; f < gk; ++f) wait_bar(k_raw + f % NSK, (f / NSK) & 1, &never);
+                for (uint32_t f = gv > NSV ? gv - NSV : 0; f < gv; ++f) wait_bar(v_raw + f % NSV, (f / NSV) & 1, &never);
                 for (int t = 0; t < 2; ++t)
                     if (nq_loaded[t]) wait_bar(q_full + t, (nq_loaded[t] - 1) & 1, &never);
             }
@@ -976,41 +959,38 @@ __global__ void __launch_bounds__(Shape<D, MODE>::THREADS, 1)
         }
     } else if constexpr (F8) {
         // ------------------------------------------------ e4m3 -> f16
-        const int ct = tid - 12 * 32;
-        uint32_t gr = 0, gt = 0;   // raw tiles, key tiles so far
+        uint32_t gt = 0;   // key tiles so far
         bool good = true;
-        const auto convert = [&](uint8_t *dst, uint64_t *full, uint64_t *empty, uint32_t stages, int keep) {
-            const int s = gr % RS;
-            good = wait_on(raw_full + s, (gr / RS) & 1) && (gt < stages || wait_on(empty + gt % stages, (gt / stages - 1) & 1));
-            if (!good) return;
-            const uint8_t *src = sRaw + s * S::RAW;
-            uint8_t *out = dst + gt % stages * S::TILE;
+        // A warp takes 32 rows, all of them into registers before it writes one (in place).
+        const auto convert = [&](const uint8_t *src, uint8_t *out, uint64_t *raw, uint64_t *full, uint32_t phase, int keep) {
+            if (!(good = wait_on(raw, phase & 1))) return;
+            constexpr int N = D / 16;   // chunks of a lane, and of a row
+            uint4 x[N];
             #pragma unroll
-            for (int i = 0; i < TK * D / 16 / 128; ++i) {
-                const int chunk = i * 128 + ct, row = chunk / (D / 16), c = 2 * (chunk % (D / 16));
-                uint4 x = *reinterpret_cast<const uint4 *>(src + chunk * 16);
-                if (row >= keep) x = make_uint4(0, 0, 0, 0);   // values behind the segment may be anything (0 * NaN)
+            for (int i = 0; i < N; ++i) x[i] = *reinterpret_cast<const uint4 *>(src + (warp - 12) * 32 * D + (i * 32 + lane) * 16);
+            __syncwarp();
+            #pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int row = (warp - 12) * 32 + (i * 32 + lane) / N, c = 2 * (lane % N);
+                if (row >= keep) x[i] = make_uint4(0, 0, 0, 0);   // values behind the segment may be anything (0 * NaN)
                 uint8_t *at = out + (c >> 3) * S::ATOM + row * 128;
-                *reinterpret_cast<uint4 *>(at + (((c & 7) ^ (row & 7)) << 4)) =
-                    make_uint4(e4m3x2_f16x2(x.x), e4m3x2_f16x2(x.x >> 16), e4m3x2_f16x2(x.y), e4m3x2_f16x2(x.y >> 16));
-                *reinterpret_cast<uint4 *>(at + ((((c & 7) + 1) ^ (row & 7)) << 4)) =
-                    make_uint4(e4m3x2_f16x2(x.z), e4m3x2_f16x2(x.z >> 16), e4m3x2_f16x2(x.w), e4m3x2_f16x2(x.w >> 16));
+                *reinterpret_cast<uint4 *>(at + (((c & 7) ^ (row & 7)) << 4)) = make_uint4(
+                    e4m3x2_f16x2(x[i].x), e4m3x2_f16x2(x[i].x >> 16), e4m3x2_f16x2(x[i].y), e4m3x2_f16x2(x[i].y >> 16));
+                *reinterpret_cast<uint4 *>(at + ((((c & 7) + 1) ^ (row & 7)) << 4)) = make_uint4(
+                    e4m3x2_f16x2(x[i].z), e4m3x2_f16x2(x[i].z >> 16), e4m3x2_f16x2(x[i].w), e4m3x2_f16x2(x[i].w >> 16));
             }
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(full + gt % stages);
-                mbar_arrive(raw_empty + s);
-            }
-            ++gr;
+            if (lane == 0) mbar_arrive(full);
         };
         for (uint32_t it = 0; good; give_back(it++)) {
             if (!(good = wait_on(item_full + it % ITEMS, (it / ITEMS) & 1))) break;
             const Item &w = ring[it % ITEMS];
             if (w.j0 >= w.j1) break;
             for (int j = w.j0; j < w.j1 && good; ++j, ++gt) {
-                convert(sK, k_full, k_empty, NSK, TK);
-                if (good) convert(sV, v_full, v_empty, NSV, w.len - j * TK);
+                const uint32_t k = gt % NSK, v = gt % NSV;
+                convert(raw_k(k), sK + k * S::TILE, k_raw + k, k_full + k, gt / NSK, TK);
+                if (good) convert(raw_v(v), sV + v * S::TILE, v_raw + v, v_full + v, gt / NSV, w.len - j * TK);
             }
         }
     }

@@ -941,7 +941,7 @@ __global__ void __launch_bounds__(256) attention_weight_kernel(const AttentionDe
     }
 }
 
-constexpr double kPrefixAgain = 6e7;   // bytes
+constexpr double kPrefixAgain = 2e8;   // bytes
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 
 // Workspace: arrival counters, partial outputs, their (m, l), then with weights (m, 1/l) and scores.
