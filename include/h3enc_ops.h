@@ -490,10 +490,11 @@ H3ENC_API h3enc_status h3enc_op_rope_append(const void *qkv, int64_t ld_qkv, int
  *   of the prefixes, in the same cache, as page_table, seq_lens and max_len are the sequences' own (token 0 of a
  *   sequence's own tokens in place 0 of its first page), clamped and reported alike.
  *   weight_in, weight_out: of the own tokens; the prefixes' weights are not accumulated.
- *   workspace: h3enc_op_attention_decode_shared_workspace_bytes() bytes, with the rules of h3enc_op_attention_decode's.
+ *   workspace: h3enc_op_attention_decode_shared_workspace_bytes() bytes, with the rules of h3enc_op_attention_decode's
+ *   (zero-filled again after a call whose status reported a timeout).
  * The weights of a prefix's tokens enter the second sum in bf16 (e4m3: f16), off by up to 2^-8 (2^-11) of each, and those
- * below 2^-126 (e4m3: 2^-38) of the largest count as 0; where all sequences together would read less than 60 MB of prefixes,
- * each reads its own again, with the rounding of h3enc_op_attention_decode.  Requires n_prefixes <= 1024, max_prefix <= 2^30;
+ * below 2^-126 (e4m3: 2^-38) of the largest count as 0; where all sequences together would read at most 200 MB of prefixes
+ * (by max_prefix), each reads its own again in one launch, with the rounding of h3enc_op_attention_decode.  Requires n_prefixes <= 1024, max_prefix <= 2^30;
  * n_kv_heads * ceil(heads per kv head / 128) * (n_seqs / (2 max(128 / heads per kv head, 1)) + min(n_prefixes, n_seqs)) *
  * (max_prefix / 64 + 4) above 2e9 is H3ENC_ERR_UNSUPPORTED; the rest as for h3enc_op_attention_decode. */
 H3ENC_API h3enc_status h3enc_op_attention_decode_shared(
@@ -517,8 +518,8 @@ H3ENC_API int64_t h3enc_op_attention_decode_shared_workspace_bytes(int32_t n_seq
  *   columns of one projection).  o must not overlap q, k or v.
  *   cu_q, cu_k DEVICE int32 [n_seqs + 1], not running back; each may be NULL with n_seqs 1 (all rows).  Offsets outside
  *   [0, Tq] or [0, Tk] are clamped; that, or one that runs back, sets status bit 2 (rows of two sequences are undefined).
- *   workspace: h3enc_op_attention_cross_workspace_bytes() bytes, 256-byte aligned, zero-filled once before its first use and
- *   then reused by calls of any sizes.  Calls (and graphs that hold them) sharing it must not overlap on the GPU.
+ *   workspace: h3enc_op_attention_cross_workspace_bytes() bytes, 256-byte aligned, zero-filled once before its first use (and
+ *   again after a call whose status reported a timeout) and then reused by calls of any sizes.  Calls (and graphs that hold them) sharing it must not overlap on the GPU.
  * The result does not depend on timing: the same inputs give the same bits on every run.  A bounded wait that runs out sets
  * status bit 1; the outputs are then undefined.
  * Requires head_dim in {64, 128}, n_seqs <= 1024, Tq and Tk <= 2^30, n_heads <= 65536, n_heads % n_kv_heads == 0, leading

@@ -941,7 +941,10 @@ __global__ void __launch_bounds__(256) attention_weight_kernel(const AttentionDe
     }
 }
 
-constexpr double kPrefixAgain = 2e8;   // bytes
+// Bytes of prefixes that sequences read again each rather than in one pass for all.  64 q heads over 8 kv heads of 128, own tokens 50 to
+// 300: 8 sequences behind 4000 tokens (131 MB) 21 us against 30, 64 behind 700 (184 MB) 33 against 42; 4 behind 30,000 (492 MB) 51
+// against 50.
+constexpr double kPrefixAgain = 2e8;
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 
 // Workspace: arrival counters, partial outputs, their (m, l), then with weights (m, 1/l) and scores.
@@ -1031,7 +1034,8 @@ cudaError_t launch_attention_decode(const AttentionDecode &p, cudaStream_t st) {
     const bool prefix = p.pre_o || p.n_prefixes > 0;
     const long long tiles = (p.max_len + tile - 1) / tile + (p.pre_o ? 0 : (p.max_prefix + tile - 1) / tile);
     const long long most = (long long)p.n_seqs * p.cache.nkv * a.chunks * tiles;
-    const int grid = (int)std::min<long long>(sms, std::max<long long>(most, 1));
+    // (sequences without own tokens are given what their prefix left, a CTA each)
+    const int grid = (int)std::min<long long>(sms, std::max<long long>(std::max<long long>(most, p.pre_o ? p.n_seqs : 1), 1));
     const int blocks = a.group <= 8 ? 1 : split ? 4 : 2;
     const auto run = [&](auto d, auto f8) {
         constexpr int D = decltype(d)::value;

@@ -10,7 +10,7 @@ An e4m3 value is off by half a step: 2^-4 of the value, 2^-10 at least.
 Attention: with S1 = max_i sum_e |q_e k_ie| / sqrt(d), the fp32 score of d products is off by at most DELTA = 16 * 2^-24 * S1
 (16 accumulation steps of 16 products, and the same again for the base-2 exponent), so a weight by a factor of at most
 1 + 2 DELTA; it enters the value product in bf16, 2^-8 of it (f16 behind an e4m3 cache: 2^-11, and at least 2^-37
-absolutely; a sequence's own tokens: two halves, 2^-16).  With A = sum_i p_i |v_i| the output is off by A times that, 2^-18 A for
+absolutely; a sequence's own tokens, few queries, near prefixes: two halves, 2^-16).  With A = sum_i p_i |v_i| the output is off by A times that, 2^-18 A for
 fp32 sums and the joins, and half a step of bf16.  An accumulated weight is off by 2 DELTA + 2^-18 of sum_h p_h.
 """
 import numpy as np
@@ -375,6 +375,8 @@ def test_attention_cross_of_one_sequence_needs_no_offsets():
                  _f64(kv[:, 128:]).reshape(200, 2, 64))
     Q.h3enc_op_attention_cross(q, kv[:0, :128], kv[:0, 128:], a, 4, 2, 64, _cross_ws(64))       # no states at all
     assert not a.any()
+    Q.h3enc_op_attention_cross(q[:1], kv[:0, :128], kv[:0, 128:], b[:1], 4, 2, 64, _cross_ws(64))   # (few rows: another path)
+    assert not b[0].any() and b[1:].any()
     Q.h3enc_op_attention_cross(q[:0], kv[:, :128], kv[:, 128:], a[:0], 4, 2, 64, _cross_ws(64))
 
 
@@ -486,7 +488,7 @@ SHARED = [
 
 def _far_bound(n, nkv, d, dtype):
     """A bound on the prefixes' lengths with which the call passes over them once for all (it goes by the bound)."""
-    return int(6e7 / (2 * n * nkv * d * (2 if dtype == BF16 else 1))) + 1
+    return int(2e8 / (2 * n * nkv * d * (2 if dtype == BF16 else 1))) + 1
 
 
 @pytest.mark.parametrize("far", [False, True])
@@ -610,6 +612,61 @@ def test_attention_decode_shared_reports_bad_pages_and_lengths(dtype, far):
     if not far:       # (the table holds no page for what a clamped length of that bound would read)
         check(None, 121, 120)
         check(None, 2 ** 31 - 1, 33)
+
+
+@pytest.mark.parametrize("far", [False, True])
+def test_attention_decode_shared_without_own_tokens_or_own_pages(far):
+    """No own tokens at all: max_len 0 and a page table of no columns."""
+    g = _gen(14)
+    n, nq, nkv, d, page, P = 5, 4, 2, 64, 16, 50
+    cache = _pool(g, 8, nkv, page, d, BF16)
+    ptable = torch.full((1, 4 + (_far_bound(n, nkv, d, BF16) // page + 1 if far else 0)), -1, dtype=torch.int32, device="cuda")
+    ptable[0, :4] = torch.randperm(8, device="cuda", generator=g)[:4].to(torch.int32)
+    (k, v), = _fill(cache, ptable, [P], *([torch.randn(P, nkv, d, device="cuda", generator=g)] for _ in range(2)))
+    q, o = _randn(g, n, nq * d), torch.zeros(n, nq * d, device="cuda", dtype=torch.bfloat16)
+    ws = torch.zeros(Q.h3enc_op_attention_decode_shared_workspace_bytes(n, nq, 0), dtype=torch.uint8, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    Q.h3enc_op_attention_decode_shared(q, o, cache, ptable, _i32([P]), page * ptable.shape[1], ptable.new_zeros(n, 0), _i32([0] * n), nq,
+                                       0, ws, status=status)
+    assert int(status.item()) == 0
+    _check_cross(_f64(o).reshape(n, nq, d), _f64(q).reshape(n, nq, d), k, v)
+
+
+def test_attention_calls_on_two_streams_with_workspaces_of_their_own():
+    """Cross attention and attention behind a prefix at once: each as alone."""
+    g = _gen(15)
+    nq, nkv, d, page, n, P = 8, 2, 128, 64, 40, 9000
+    cache = _pool(g, P // page + 1 + n, nkv, page, d, BF16)
+    for t in cache.tensors[:2]:
+        t.copy_(_randn(g, *t.shape))
+    ids = torch.arange(P // page + 1 + n, device="cuda", dtype=torch.int32)
+    ptable, table = ids[:P // page + 1].view(1, -1), ids[P // page + 1:].view(n, 1)
+    q1, q2, kv = _randn(g, n, nq * d), _randn(g, 900, nq * d), _randn(g, 1500, 2 * nkv * d)
+    lens, outs = _i32([1 + i for i in range(n)]), []
+    for _ in range(2):
+        o1, o2 = torch.zeros_like(q1), torch.zeros_like(q2)
+        ws1 = torch.zeros(Q.h3enc_op_attention_decode_shared_workspace_bytes(n, nq, page), dtype=torch.uint8, device="cuda")
+        ws2 = _cross_ws(d)
+        outs.append((o1, o2, ws1, ws2))
+    plen = _i32([P])
+
+    def shared(o, ws):
+        Q.h3enc_op_attention_decode_shared(q1, o, cache, ptable, plen, page * ptable.shape[1], table, lens, nq, page, ws)
+
+    def cross(o, ws):
+        Q.h3enc_op_attention_cross(q2, kv[:, :nkv * d], kv[:, nkv * d:], o, nq, nkv, d, ws)
+
+    shared(outs[0][0], outs[0][2])
+    cross(outs[0][1], outs[0][3])
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(4):
+        with torch.cuda.stream(streams[0]):
+            shared(outs[1][0], outs[1][2])
+        with torch.cuda.stream(streams[1]):
+            cross(outs[1][1], outs[1][3])
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
 
 
 # ---------------------------------------------------------------- a run of them together
