@@ -1025,22 +1025,39 @@ __global__ void __launch_bounds__(256) attention_cross_join_kernel(const __grid_
         const int r = (t ? q - quarters_a : q) * 32 + lane, r_tok = r * a.inv_gc >> 16, r_head = r - r_tok * a.gc;
         if (r_tok >= (t ? it.z : it.y) || r_tok >= a.tok || chunk * TQ + r_head >= a.group) continue;
         const auto slot = [&](int i) { return (long long)(2 * (first + i) + (i == 0 ? 1 : 0)) * 2 + t; };
-        float top = -INFINITY;
-        #pragma unroll 8
-        for (int i = 0; i < n; ++i) top = fmaxf(top, __ldcg(a.ml + slot(i) * 128 + r).x);
-        const float base = top == -INFINITY ? 0.f : top;
+        // eight parts at a time, all their loads in flight
+        constexpr int BATCH = 8;
+        float top = -INFINITY, l = 0.f;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        float l = 0.f;
-        #pragma unroll 8
-        for (int i = 0; i < n; ++i) {
-            const float2 ml = __ldcg(a.ml + slot(i) * 128 + r);
-            const float *src = a.part + slot(i) * (D * 128) + (long long)col * 128 + r;
-            const float f = ex2(ml.x - base);
-            l = fmaf(ml.y, f, l);
-            acc.x = fmaf(__ldcg(src), f, acc.x);
-            acc.y = fmaf(__ldcg(src + 128), f, acc.y);
-            acc.z = fmaf(__ldcg(src + 256), f, acc.z);
-            acc.w = fmaf(__ldcg(src + 384), f, acc.w);
+        #pragma unroll 1
+        for (int i0 = 0; i0 < n; i0 += BATCH) {
+            float2 ml[BATCH];
+            float4 x[BATCH];
+            #pragma unroll
+            for (int k = 0; k < BATCH; ++k) {
+                ml[k] = make_float2(-INFINITY, 0.f);
+                x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (i0 + k < n) {
+                    const float *src = a.part + slot(i0 + k) * (D * 128) + (long long)col * 128 + r;
+                    ml[k] = __ldcg(a.ml + slot(i0 + k) * 128 + r);
+                    x[k] = make_float4(__ldcg(src), __ldcg(src + 128), __ldcg(src + 256), __ldcg(src + 384));
+                }
+            }
+            const float before = top;
+            #pragma unroll
+            for (int k = 0; k < BATCH; ++k) top = fmaxf(top, ml[k].x);
+            const float base = top == -INFINITY ? 0.f : top, c = ex2(before - base);
+            acc = make_float4(acc.x * c, acc.y * c, acc.z * c, acc.w * c);
+            l *= c;
+            #pragma unroll
+            for (int k = 0; k < BATCH; ++k) {
+                const float f = ex2(ml[k].x - base);
+                l = fmaf(ml[k].y, f, l);
+                acc.x = fmaf(x[k].x, f, acc.x);
+                acc.y = fmaf(x[k].y, f, acc.y);
+                acc.z = fmaf(x[k].z, f, acc.z);
+                acc.w = fmaf(x[k].w, f, acc.w);
+            }
         }
         const long long row = it.x + t * a.tok + r_tok;
         const int h = head * a.group + chunk * TQ + r_head;
