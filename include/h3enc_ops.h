@@ -432,7 +432,7 @@ H3ENC_API h3enc_status h3enc_op_cache_evict(const h3enc_kv_cache *cache, const i
                                             float *weight_out, int64_t ld_weight_out, int32_t *kept, int64_t ld_kept,
                                             int32_t *new_lens, int32_t *status, void *stream);
 
-/* Rotary positions, for h3enc_op_rope_append: the first rotary_dim elements of a head rotate in pairs, pair j by the angle
+/* Rotary positions, for h3enc_rope_make: the first rotary_dim elements of a head rotate in pairs, pair j by the angle
  * position * w_j with w_j = theta^(-2j / rotary_dim), scaled for contexts longer than original_len tokens:
  *   ROPE_LINEAR      w_j / factor
  *   ROPE_WAVELENGTH  with n_j = original_len w_j / 2 pi, the turns of pair j over the original context, and
@@ -444,7 +444,7 @@ H3ENC_API h3enc_status h3enc_op_cache_evict(const h3enc_kv_cache *cache, const i
  * as 64-bit fractions of a turn), but for w_j's own rounding to 53 bits. */
 enum { H3ENC_ROPE_PLAIN = 0, H3ENC_ROPE_LINEAR = 1, H3ENC_ROPE_WAVELENGTH = 2, H3ENC_ROPE_YARN = 3 };
 typedef struct {
-    int32_t rotary_dim;    /* a multiple of 16, at most head_dim */
+    int32_t rotary_dim;    /* a multiple of 16, 16 to 128; at most the head_dim that it is used with */
     int32_t interleaved;   /* 0: pairs (j, j + rotary_dim/2); 1: pairs (2j, 2j + 1) */
     int32_t scaling;       /* H3ENC_ROPE_* */
     int32_t original_len;  /* WAVELENGTH and YARN: >= 1 */
@@ -455,6 +455,17 @@ typedef struct {
     int32_t section[3];    /* {0, 0, 0}: one position per row; else three-axis positions, pair j by axis(j) of
                               h3enc_op_rope_table, and the sections sum to rotary_dim/2 */
 } h3enc_rope;
+
+/* The frequencies of an h3enc_rope as the kernel takes them: made once by h3enc_rope_make, for any number of calls. */
+typedef struct {
+    uint64_t turns[64];     /* 2^64 times the turns of pair j per position, modulo 2^64 */
+    uint64_t axis1, axis2;  /* bit j: pair j goes by the second / third axis */
+    float magnitude;
+    int32_t rotary_dim, interleaved, axes;
+} h3enc_rope_plan;
+
+/* HOST only (no device, no stream).  H3ENC_ERR_INVALID_ARG for parameters outside the ranges above. */
+H3ENC_API h3enc_status h3enc_rope_make(const h3enc_rope *rope, h3enc_rope_plan *plan);
 
 /* New rows of a packed projection normed, rotated and appended to their sequences in a cache, in one pass: what
  * h3enc_op_qk_norm_rope does with slots and tables that the caller makes, by page table, lengths and positions alone.
@@ -474,7 +485,7 @@ typedef struct {
  * 16-byte aligned, at least one of q_out, k_out and cache. */
 H3ENC_API h3enc_status h3enc_op_rope_append(const void *qkv, int64_t ld_qkv, int32_t T, int32_t n_heads,
                                             int32_t n_kv_heads, int32_t head_dim, const void *w_q, const void *w_k,
-                                            float eps, const h3enc_rope *rope, const int32_t *positions,
+                                            float eps, const h3enc_rope_plan *rope, const int32_t *positions,
                                             int64_t ld_positions, void *q_out, int64_t ld_q, void *k_out, int64_t ld_k,
                                             const h3enc_kv_cache *cache, const int32_t *page_table, int32_t ld_table,
                                             const int32_t *seq_lens, const int32_t *cu_rows, int32_t n_seqs,

@@ -31,7 +31,7 @@ __all__ = [
     "h3vis_last_error", "h3vis_launch_count", "h3vis_destroy", "VisionEncoder", "h3enc_op_attention", "h3enc_op_embed", "h3enc_op_vis_rank", "Encoder",
     "KERNEL_CLASSES", "KVCache", "h3enc_op_qk_norm_rope", "h3enc_op_attention_decode",
     "h3enc_op_attention_decode_workspace_bytes", "h3enc_op_cache_evict",
-    "Rope", "h3enc_op_rope_append", "h3enc_op_attention_decode_shared",
+    "Rope", "h3enc_rope_make", "h3enc_op_rope_append", "h3enc_op_attention_decode_shared",
     "h3enc_op_attention_decode_shared_workspace_bytes", "h3enc_op_attention_cross",
     "h3enc_op_attention_cross_workspace_bytes",
 ]
@@ -103,25 +103,34 @@ class KVCache(ctypes.Structure):
         self.device_index = k.get_device()
 
 
-class Rope(ctypes.Structure):
-    """h3enc_rope: which elements of a head rotate, in which pairs, and at which (scaled) frequencies.  scaling: "none",
-    "linear", "wavelength" or "yarn"; section: the three-axis positions' (t, h, w) shares of the rotary_dim / 2 pairs."""
+class _RopeParams(ctypes.Structure):
+    """h3enc_rope"""
     _fields_ = [("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("scaling", ctypes.c_int32),
                 ("original_len", ctypes.c_int32), ("theta", ctypes.c_double), ("factor", ctypes.c_double),
                 ("low_turns", ctypes.c_double), ("high_turns", ctypes.c_double), ("magnitude", ctypes.c_double),
                 ("section", ctypes.c_int32 * 3)]
+
+
+class Rope(ctypes.Structure):
+    """h3enc_rope_plan: which elements of a head rotate, in which pairs, and at which (scaled) frequencies; made once, for any
+    number of calls.  scaling: "none", "linear", "wavelength" or "yarn"; section: the three-axis positions' (t, h, w) shares of
+    the rotary_dim / 2 pairs."""
+    _fields_ = [("turns", ctypes.c_uint64 * 64), ("axis1", ctypes.c_uint64), ("axis2", ctypes.c_uint64),
+                ("magnitude", ctypes.c_float), ("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("axes", ctypes.c_int32)]
     SCALINGS = ("none", "linear", "wavelength", "yarn")
 
     def __init__(self, rotary_dim, theta, interleaved=False, scaling="none", factor=1.0, original_len=0, low_turns=0.0,
                  high_turns=0.0, magnitude=0.0, section=None):
+        super().__init__()
         if scaling not in self.SCALINGS:
             raise ValueError(f"Rope: scaling must be one of {self.SCALINGS}, not {scaling!r}")
         section = tuple(section) if section is not None else (0, 0, 0)
         if len(section) != 3 or not all(-2 ** 31 <= x < 2 ** 31 for x in (rotary_dim, original_len, *section)):
             raise ValueError("Rope: bad sizes")
-        super().__init__(rotary_dim, 1 if interleaved else 0, self.SCALINGS.index(scaling), original_len, theta, factor,
-                         low_turns, high_turns, magnitude, (ctypes.c_int32 * 3)(*section))
-        self.axes = 3 if any(section) else 1
+        params = _RopeParams(rotary_dim, 1 if interleaved else 0, self.SCALINGS.index(scaling), original_len, theta, factor,
+                             low_turns, high_turns, magnitude, (ctypes.c_int32 * 3)(*section))
+        _check(lib.h3enc_rope_make(params, self))
 
 
 def _load():
@@ -193,6 +202,7 @@ _SIGS = {
     "h3enc_op_attention_workspace_bytes": ([_I32], _I64),
     "h3enc_op_qk_norm_rope": ([_P, _I64, _I32, _I32, _I32, _I32, _P, _P, _F, _P, _P, _I32, _P, _I64, _P, _I64,
                                ctypes.POINTER(KVCache), _P, _P, _P], _I32),
+    "h3enc_rope_make": ([ctypes.POINTER(_RopeParams), ctypes.POINTER(Rope)], _I32),
     "h3enc_op_rope_append": ([_P, _I64, _I32, _I32, _I32, _I32, _P, _P, _F, ctypes.POINTER(Rope), _P, _I64, _P, _I64, _P,
                               _I64, ctypes.POINTER(KVCache), _P, _I32, _P, _P, _I32, _I32, _P, _P], _I32),
     "h3enc_op_attention_decode_shared": ([_P, _I64, _P, _I64, ctypes.POINTER(KVCache), _P, _I32, _P, _P, _I32, _I32, _P, _I32,
@@ -699,6 +709,11 @@ def h3enc_op_qk_norm_rope(qkv, T, n_heads, n_kv_heads, head_dim, w_q, w_k, eps, 
         None if sin_tab is None else _vec(who, "sin_tab", sin_tab, _F32T, dev, n), cs_stride, q_out, ld_q, k_out, ld_k,
         cache, None if slots is None else _vec(who, "slots", slots, _I32T, dev, T),
         None if status is None else _vec(who, "status", status, _I32T, dev, 1), raw(dev) if stream is None else _stream(stream)))
+
+
+def h3enc_rope_make(params, plan):
+    """h3enc_rope -> h3enc_rope_plan (what Rope(...) calls)."""
+    return _check(lib.h3enc_rope_make(params, plan))
 
 
 def h3enc_op_rope_append(qkv, T, n_heads, n_kv_heads, head_dim, w_q, w_k, eps, rope, positions=None, q_out=None,

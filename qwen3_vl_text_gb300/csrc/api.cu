@@ -1678,11 +1678,11 @@ SharedWorkspace shared_workspace(int sms, size_t decode, int32_t n_seqs, int32_t
     return y;
 }
 
-// The scaled frequencies of `r` as 64-bit fractions of a turn per position; false if it is not valid for heads of head_dim.
-bool take_rope(const h3enc_rope &r, int32_t head_dim, h3::RopeAppend *p) {
+// The scaled frequencies of `r` as 64-bit fractions of a turn per position; false if it is not valid.
+bool make_rope(const h3enc_rope &r, h3enc_rope_plan *p) {
     const auto positive = [](double x) { return x > 0 && std::isfinite(x); };
     const bool ramped = r.scaling == H3ENC_ROPE_WAVELENGTH || r.scaling == H3ENC_ROPE_YARN;
-    if (r.rotary_dim < 16 || r.rotary_dim % 16 || r.rotary_dim > head_dim || r.scaling < H3ENC_ROPE_PLAIN ||
+    if (r.rotary_dim < 16 || r.rotary_dim % 16 || r.rotary_dim > 2 * h3::kMaxHalfDim || r.scaling < H3ENC_ROPE_PLAIN ||
         r.scaling > H3ENC_ROPE_YARN || !positive(r.theta) || (r.scaling && !positive(r.factor)) ||
         !(r.magnitude == 0 || positive(r.magnitude)))
         return false;
@@ -1717,11 +1717,11 @@ bool take_rope(const h3enc_rope &r, int32_t head_dim, h3::RopeAppend *p) {
         }
         const double turns = w / two_pi;
         if (!std::isfinite(turns)) return false;
-        p->turns[j] = (unsigned long long)std::ldexp(turns - std::floor(turns), 64);
-        if (axes && j % 3 == 1 && j < 3 * r.section[1]) p->axis1 |= 1ull << j;
-        if (axes && j % 3 == 2 && j < 3 * r.section[2]) p->axis2 |= 1ull << j;
+        p->turns[j] = (uint64_t)std::ldexp(turns - std::floor(turns), 64);
+        if (axes && j % 3 == 1 && j < 3 * r.section[1]) p->axis1 |= uint64_t(1) << j;
+        if (axes && j % 3 == 2 && j < 3 * r.section[2]) p->axis2 |= uint64_t(1) << j;
     }
-    p->rot = r.rotary_dim;
+    p->rotary_dim = r.rotary_dim;
     p->interleaved = r.interleaved != 0;
     p->axes = axes ? 3 : 1;
     p->magnitude = (float)(r.magnitude > 0 ? r.magnitude
@@ -1733,8 +1733,16 @@ bool take_rope(const h3enc_rope &r, int32_t head_dim, h3::RopeAppend *p) {
 
 extern "C" {
 
+h3enc_status h3enc_rope_make(const h3enc_rope *rope, h3enc_rope_plan *plan) {
+    h3enc_rope_plan made{};
+    if (!rope || !plan || !make_rope(*rope, &made))
+        return fail(nullptr, H3ENC_ERR_INVALID_ARG, "rope_make: NULL or bad rotary parameters");
+    *plan = made;
+    return H3ENC_OK;
+}
+
 h3enc_status h3enc_op_rope_append(const void *qkv, int64_t ld_qkv, int32_t T, int32_t n_heads, int32_t n_kv_heads,
-                                  int32_t head_dim, const void *w_q, const void *w_k, float eps, const h3enc_rope *rope,
+                                  int32_t head_dim, const void *w_q, const void *w_k, float eps, const h3enc_rope_plan *rope,
                                   const int32_t *positions, int64_t ld_positions, void *q_out, int64_t ld_q, void *k_out,
                                   int64_t ld_k, const h3enc_kv_cache *cache, const int32_t *page_table, int32_t ld_table,
                                   const int32_t *seq_lens, const int32_t *cu_rows, int32_t n_seqs, int32_t max_len,
@@ -1745,8 +1753,16 @@ h3enc_status h3enc_op_rope_append(const void *qkv, int64_t ld_qkv, int32_t T, in
     if (s != H3ENC_OK) return s;
     h3::RopeAppend p{};
     p.axes = 1;
-    if (rope && !take_rope(*rope, head_dim, &p))
-        return fail(nullptr, H3ENC_ERR_INVALID_ARG, "%s: bad rotary parameters", who);
+    if (rope) {
+        if (rope->rotary_dim < 16 || rope->rotary_dim % 16 || rope->rotary_dim > head_dim || (rope->axes != 1 && rope->axes != 3) ||
+            (rope->axis1 & rope->axis2))
+            return fail(nullptr, H3ENC_ERR_INVALID_ARG, "%s: the rotary plan is not one of h3enc_rope_make, or rotates more than a head",
+                        who);
+        static_assert(sizeof(p.turns) == sizeof(rope->turns), "");
+        std::memcpy(p.turns, rope->turns, sizeof(p.turns));
+        p.axis1 = rope->axis1; p.axis2 = rope->axis2;
+        p.rot = rope->rotary_dim; p.interleaved = rope->interleaved; p.axes = rope->axes; p.magnitude = rope->magnitude;
+    }
     if (n_seqs < 0 || n_seqs > h3::kMaxSeqs || max_len < 0 || max_len > h3::kMaxCacheLen)
         return fail(nullptr, H3ENC_ERR_INVALID_ARG, "%s: bad sizes", who);
     if (cache) {

@@ -109,7 +109,7 @@ def test_rope_append_to_a_cache_refuses(Q, kw):
 
 
 @pytest.mark.parametrize("kw", [
-    dict(rotary_dim=0), dict(rotary_dim=8), dict(rotary_dim=40), dict(rotary_dim=80), dict(rotary_dim=-16), dict(theta=0.0),
+    dict(rotary_dim=0), dict(rotary_dim=8), dict(rotary_dim=40), dict(rotary_dim=144), dict(rotary_dim=-16), dict(theta=0.0),
     dict(theta=-2.0), dict(theta=math.inf), dict(theta=math.nan), dict(factor=0.0, scaling="linear"),
     dict(factor=math.nan, scaling="linear"), dict(magnitude=-1.0), dict(magnitude=math.nan), dict(magnitude=math.inf),
     dict(scaling="yarn", factor=4.0), dict(scaling="wavelength", factor=4.0, original_len=0),
@@ -117,21 +117,49 @@ def test_rope_append_to_a_cache_refuses(Q, kw):
     dict(scaling="wavelength", factor=4.0, original_len=64, low_turns=4.0, high_turns=4.0),
     dict(scaling="yarn", factor=4.0, original_len=64, low_turns=1.0), dict(section=(8, 8, 8)), dict(section=(40, -4, -4)),
     dict(section=(0, 0, 31)), dict(theta=1e-320)])
-def test_rope_append_refuses_rotary_parameters(Q, kw):
-    _refused(Q, 2, _append, rope=Q.Rope(**{**dict(rotary_dim=64, theta=1e4), **kw}))
+def test_rope_refuses_parameters(Q, kw):
+    with pytest.raises(Q.H3encError) as e:
+        Q.Rope(**{**dict(rotary_dim=64, theta=1e4), **kw})
+    assert e.value.code == 2 and Q.h3enc_last_error(None)
 
 
-def test_rope_append_refuses_an_unknown_scaling(Q):
+def test_rope_plans(Q):
+    """The frequencies of a plan are the oracle's, in turns; parameters and plans that are none are refused."""
+    for kw in (dict(), dict(interleaved=True), dict(scaling="linear", factor=4.0), dict(scaling="wavelength", factor=8.0, original_len=8192),
+               dict(scaling="yarn", factor=4.0, original_len=32768), dict(theta=0.5)):
+        kw = {**dict(theta=5e5), **kw}
+        plan = Q.Rope(96, **kw)
+        kw.pop("interleaved", None)
+        w, m = O.decoder.frequencies(96, **kw)
+        turns = np.array(plan.turns[:48], np.float64) / 2.0 ** 64
+        assert np.allclose(turns, w / (2 * math.pi) % 1, rtol=2.0 ** -50, atol=2.0 ** -52) and plan.magnitude == pytest.approx(m, rel=1e-7)
+        assert (plan.rotary_dim, plan.axes, plan.axis1, plan.axis2) == (96, 1, 0, 0)
+    plan = Q.Rope(128, 5e6, section=(24, 20, 20))
+    assert plan.axes == 3 and [(plan.axis1 >> j & 1) + 2 * (plan.axis2 >> j & 1) for j in range(64)] == [O.decoder.axis_of(j, (24, 20, 20)) for j in range(64)]
     for scaling in (-1, 4):
-        r = Q.Rope(64, 1e4)
-        r.scaling = scaling
-        _refused(Q, 2, _append, rope=r)
+        params = Q._RopeParams(64, 0, scaling, 0, 1e4, 1.0)
+        with pytest.raises(Q.H3encError):
+            Q.h3enc_rope_make(params, plan)
+    for args in ((None, plan), (Q._RopeParams(64, 0, 0, 0, 1e4), None)):
+        with pytest.raises(Q.H3encError):
+            Q.h3enc_rope_make(*args)
     with pytest.raises(ValueError):
         Q.Rope(64, 1e4, scaling="ntk")
     with pytest.raises(ValueError):
         Q.Rope(64, 1e4, section=(16, 16))
     with pytest.raises(ValueError):
         Q.Rope(2 ** 32 + 64, 1e4)
+
+
+def test_rope_append_refuses_plans(Q):
+    _refused(Q, 2, _append, rope=Q.Rope(80, 1e4))          # more than a head
+    for field, value in (("rotary_dim", 0), ("rotary_dim", 24), ("axes", 2), ("axes", 0)):
+        r = Q.Rope(64, 1e4)
+        setattr(r, field, value)
+        _refused(Q, 2, _append, rope=r)
+    r = Q.Rope(64, 1e4)
+    r.axis1 = r.axis2 = 1
+    _refused(Q, 2, _append, rope=r)
 
 
 def test_rope_append_needs_positions_without_lengths(Q):
@@ -177,12 +205,17 @@ def _wrong(torch, t, rows):
     return out
 
 
-def test_rope_append_checks_its_tensors(Q, recorded):
+@pytest.fixture
+def plans(Q):
+    return Q.Rope(64, 1e4, section=(12, 10, 10)), Q.Rope(64, 1e4)
+
+
+def test_rope_append_checks_its_tensors(Q, plans, recorded):
     torch = pytest.importorskip("torch")
     bf, i32 = dict(dtype=torch.bfloat16), dict(dtype=torch.int32)
     k = torch.zeros(5, 2, 16, 64, **bf)
     a = dict(qkv=torch.zeros(6, 512, **bf), T=6, n_heads=4, n_kv_heads=2, head_dim=64, w_q=torch.ones(64, **bf),
-             w_k=torch.ones(64, **bf), eps=1e-6, rope=Q.Rope(64, 1e4, section=(12, 10, 10)), positions=torch.zeros(3, 6, **i32),
+             w_k=torch.ones(64, **bf), eps=1e-6, rope=plans[0], positions=torch.zeros(3, 6, **i32),
              q_out=torch.zeros(6, 256, **bf), k_out=torch.zeros(6, 128, **bf), cache=Q.KVCache(k, k),
              page_table=torch.zeros(3, 4, **i32), seq_lens=torch.zeros(3, **i32), max_len=64, cu_rows=torch.zeros(4, **i32),
              status=torch.zeros(1, **i32))
@@ -196,7 +229,7 @@ def test_rope_append_checks_its_tensors(Q, recorded):
     _refuses(Q, Q.h3enc_op_rope_append, a, "seq_lens", torch.zeros(3))
     _refuses(Q, Q.h3enc_op_rope_append, a, "positions", torch.zeros(6, **i32))     # three axes wanted
     _refuses(Q, Q.h3enc_op_rope_append, a, "page_table", torch.zeros(2, 4, **i32))
-    a["rope"] = Q.Rope(64, 1e4)
+    a["rope"] = plans[1]
     a["positions"] = torch.zeros(6, **i32)
     Q.h3enc_op_rope_append(**a)
     a.update(rope=None, positions=None, cache=None, page_table=None, seq_lens=None, cu_rows=None, max_len=0, status=None)
