@@ -46,7 +46,8 @@ enum { ROWS = 0, PAGES = 1, PAGES8 = 2 };   // keys: packed rows, bf16 pages, e4
 __device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, const volatile int *abort) {
     const uint32_t a = smem_u32(bar);
     bool done = mbar_try_wait(a, parity);
-    const long long t0 = done ? 0 : clock64();
+    if (__builtin_expect(done, 1)) return true;
+    const long long t0 = clock64();
     #pragma unroll 1
     while (!done) {
         if (*abort || clock64() - t0 > kSpinLimitCycles) break;
@@ -408,7 +409,7 @@ __global__ void __launch_bounds__(Shape<D, MODE>::THREADS, 1)
     const Runs runs(T, G);
 
     // rows without any key: zeros, or (prefixes) an empty part
-    if (any_empty) {
+    if (__builtin_expect(any_empty, 0)) {
         const auto fill = [&](int t0, int t1) {
             const int step = gridDim.x * S::THREADS / 32, at = blockIdx.x * (S::THREADS / 32) + warp;
             for (int r = t0 + at; r < t1; r += step) {   // a row of every head per warp
@@ -433,7 +434,7 @@ __global__ void __launch_bounds__(Shape<D, MODE>::THREADS, 1)
     // A wait that runs out, in any warp, ends the CTA: *abort lets all other waits return, and no warp waits otherwise.
     const auto wait_on = [&](uint64_t *bar, uint32_t parity) {   // by a whole warp
         const bool good = __all_sync(0xffffffffu, wait_bar(bar, parity, abort));
-        if (!good && lane == 0) {
+        if (__builtin_expect(!good, 0) && lane == 0) {
             report(p.status, ST_TIMEOUT);
             *abort = 1;
         }
@@ -520,7 +521,7 @@ __global__ void __launch_bounds__(Shape<D, MODE>::THREADS, 1)
                     };
                     // scores behind the segment: -inf, in place
                     #pragma unroll 1
-                    for (int at = valid & ~31; at < TK; at += 32) {
+                    for (int at = valid & ~31; __builtin_expect(at < TK, 0); at += 32) {
                         uint32_t x[32];
                         tmem_ld32(tS + at, x);
                         tmem_ld_wait();
@@ -530,7 +531,7 @@ __global__ void __launch_bounds__(Shape<D, MODE>::THREADS, 1)
                         tmem_st32(tS + at, x);
                         tmem_st_wait();
                     }
-                    #pragma unroll
+                    #pragma unroll (F8 ? 1 : 2)
                     for (int at = 0; at < TK; at += HELD) {
                         load(at);
                         #pragma unroll
@@ -554,7 +555,7 @@ __global__ void __launch_bounds__(Shape<D, MODE>::THREADS, 1)
                     const float off = m_use == -INFINITY ? 0.f : S::UP_LOG2 - m_use;   // (only -inf scores so far: weights 0)
                     const uint64_t scale2 = f32x2(scale, scale), off2 = f32x2(off, off);
                     uint64_t rs2[4] = {0ull, 0ull, 0ull, 0ull};
-                    #pragma unroll
+                    #pragma unroll (F8 ? 1 : 2)
                     for (int at = 0; at < TK; at += HELD) {
                         if (F8) load(at);
                         #pragma unroll
@@ -581,7 +582,7 @@ __global__ void __launch_bounds__(Shape<D, MODE>::THREADS, 1)
                     }
                     l = l * alpha + rs;
                     // O is rescaled after the previous product of this tile has completed
-                    if (__any_sync(0xffffffffu, raise)) {
+                    if (__builtin_expect(__any_sync(0xffffffffu, raise), 0)) {
                         if (!(good = wait_on(pv_done + t, (c - 1) & 1))) break;
                         tc_fence_after();
                         #pragma unroll 1
@@ -596,7 +597,7 @@ __global__ void __launch_bounds__(Shape<D, MODE>::THREADS, 1)
                     }
                     tmem_st_wait();
                 }
-                if (!F8 && valid < TK && (t == 0 || w.n_b == 0)) {
+                if (!F8 && __builtin_expect(valid < TK, 0) && (t == 0 || w.n_b == 0)) {
                     // values behind the segment may be anything (0 * NaN): cleared by the warps of the first tile that
                     // uses them, before their P is announced
                     const uint32_t at = w.pos + (j - w.j0);
@@ -616,7 +617,7 @@ __global__ void __launch_bounds__(Shape<D, MODE>::THREADS, 1)
             ++items;
             const bool whole = w.parts == 0, single = w.n_b == 0, merge = single && w.active(1);
             float2 ml = make_float2(m_use, l);
-            if (single && t == 1) {
+            if (__builtin_expect(single && t == 1, 0)) {
                 // tile A's warps merge the two shares of a single tile; the last such item's must have been read
                 if (shares > 0) good = wait_on(o_free, (shares - 1) & 1);
                 ++shares;
@@ -629,7 +630,7 @@ __global__ void __launch_bounds__(Shape<D, MODE>::THREADS, 1)
             good = wait_on(pv_done + t, (c - 1) & 1);
             float f0 = 1.f, f1 = 0.f;
             if (t == 0 && w.active(1)) c_b += single ? (end - first) >> 1 : end - first;
-            if (merge) {   // (tile B's softmax has seen its products before the last)
+            if (__builtin_expect(merge, 0)) {   // (tile B's softmax has seen its products before the last)
                 good = good && wait_on(l_full, shares++ & 1) && wait_on(pv_done + 1, (c_b - 1) & 1);
                 const float2 y = ml_s[r];
                 const float top = fmaxf(ml.x, y.x), none = top == -INFINITY ? 0.f : top;
@@ -639,7 +640,7 @@ __global__ void __launch_bounds__(Shape<D, MODE>::THREADS, 1)
             }
             if (!good) break;
             tc_fence_after();
-            if (!whole && warp == 0 && lane == 0) {
+            if (__builtin_expect(!whole, 0) && warp == 0 && lane == 0) {
                 int4 *d = a.desc + 2 * (2 * blockIdx.x + (w.j0 == 0 ? 1 : 0));
                 d[0] = make_int4(w.row0, w.n_a, w.n_b, w.head * a.chunks + w.chunk);
                 d[1] = make_int4(w.parts, w.owner, 0, 0);
@@ -666,14 +667,14 @@ __global__ void __launch_bounds__(Shape<D, MODE>::THREADS, 1)
                 tmem_ld_wait();
                 #pragma unroll
                 for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * f0);
-                if (merge) {
+                if (__builtin_expect(merge, 0)) {
                     uint32_t y[32];
                     tmem_ld32(tO + 128 + col, y);
                     tmem_ld_wait();
                     #pragma unroll
                     for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(fmaf(__uint_as_float(y[i]), f1, __uint_as_float(x[i])));
                 }
-                if (!whole) {
+                if (__builtin_expect(!whole, 0)) {
                     float *dst = a.part + slot * (D * 128) + col * 128 + r;
                     if (live) {
                         #pragma unroll
@@ -850,13 +851,13 @@ __global__ void __launch_bounds__(Shape<D, MODE>::THREADS, 1)
                 const Item &w = ring[it % ITEMS];
                 if (w.j0 >= w.j1) break;
                 const bool both = w.n_b > 0;
-                if (!w.active(t)) {
+                if (__builtin_expect(!w.active(t), 0)) {
                     for (int j = w.j0; j < w.j1 && ok; ++j) ok = skip_k() && skip_v();
                     continue;
                 }
                 ok = wait_bar((F8 ? q_ready : q_full) + t, items & 1, abort);
                 const int begin = w.j0, first = w.first(t), stride = w.stride(), end = w.j1;
-                if (ok && first > begin) skip_k();
+                if (__builtin_expect(ok && first > begin, 0)) skip_k();
                 // The first scores, then each step's value product with the next step's scores.  A pair's tiles take turns (else both
                 // would do the same at the same time, and the tensor cores stand still during both softmaxes: 590 us
                 // in the case above).  Of a single tile's steps every other one is this thread's; each K and V tile between
@@ -896,13 +897,13 @@ __global__ void __launch_bounds__(Shape<D, MODE>::THREADS, 1)
                         umma_commit(s_full + t);
                         umma_commit(k_empty + s);
                         if (j + 2 * stride >= end) umma_commit(q_empty + t);   // the item's last scores of this tile
-                        if (!both) {
+                        if (__builtin_expect(!both, 0)) {
                             if (j + 1 >= begin) skip_v();
                             if (ok && j + 3 < end) skip_k();
                         }
                     } else if (both) {
                         mbar_arrive(turn + (t ^ 1));
-                    } else if (j + 1 < end) {
+                    } else if (__builtin_expect(j + 1 < end, 0)) {
                         skip_v();   // the other thread's last
                     }
                     turns += both && j >= first;

@@ -364,6 +364,26 @@ def test_attention_cross(qlens, klens, nq, nkv, d):
     assert torch.equal(again[live], o[live, :nq * d])
 
 
+@pytest.mark.parametrize("Tq,Tk,nq,nkv,d", [(4096, 300, 8, 1, 128), (2000, 1100, 10, 10, 64), (1000, 2500, 16, 4, 128)])
+def test_attention_cross_of_many_items_with_boundaries_inside(Tq, Tk, nq, nkv, d):
+    """More items than SMs: every boundary between two runs cuts one, whose two parts meet.  The same bits every time,
+    whichever part is last, also over a workspace that other sizes have used."""
+    g = _gen(Tq)
+    q, kv = _randn(g, Tq, nq * d), _randn(g, Tk, 2 * nkv * d)
+    k, v = kv[:, :nkv * d], kv[:, nkv * d:]
+    ws, outs = _cross_ws(d), []
+    for i in range(6):
+        o = torch.zeros(Tq, nq * d, device="cuda", dtype=torch.bfloat16)
+        Q.h3enc_op_attention_cross(q, k, v, o, nq, nkv, d, ws)
+        outs.append(o)
+        other = torch.zeros(1 + 700 * (i % 2), nq * d, device="cuda", dtype=torch.bfloat16)
+        Q.h3enc_op_attention_cross(q[:len(other)], k[i:], v[i:], other, nq, nkv, d, ws)
+    assert all(torch.equal(o, outs[0]) for o in outs)
+    rows = torch.cat([torch.arange(0, Tq, 97), torch.arange(Tq - 3, Tq)]).cuda()
+    _check_cross(_f64(outs[0][rows]).reshape(-1, nq, d), _f64(q[rows]).reshape(-1, nq, d), _f64(k).reshape(Tk, nkv, d),
+                 _f64(v).reshape(Tk, nkv, d))
+
+
 def test_attention_cross_of_one_sequence_needs_no_offsets():
     g = _gen(1)
     q, kv = _randn(g, 50, 256), _randn(g, 200, 256)
