@@ -384,6 +384,30 @@ def test_attention_cross_of_many_items_with_boundaries_inside(Tq, Tk, nq, nkv, d
                  _f64(v).reshape(Tk, nkv, d))
 
 
+@pytest.mark.parametrize("n,m,keys,nq,nkv,d", [(64, 40, 333, 10, 10, 128), (64, 40, 600, 10, 10, 64), (64, 90, 900, 4, 2, 128)])
+def test_attention_cross_of_many_whole_items(n, m, keys, nq, nkv, d):
+    """Most items lie whole in a run, single tiles (two halves merged) and pairs, after others of the same CTA, with
+    values behind the last segment that must not matter.  The same bits every time."""
+    g = _gen(n * m + d)
+    before, behind = 3, 5
+    q, kv = _randn(g, n * m + before + behind, nq * d), _randn(g, n * keys + before + behind, 2 * nkv * d)
+    kv[:before] = float("nan")
+    kv[-behind:] = float("nan")
+    k, v = kv[:, :nkv * d], kv[:, nkv * d:]
+    cu_q, cu_k = _i32(before + m * np.arange(n + 1)), _i32(before + keys * np.arange(n + 1))
+    ws, outs = _cross_ws(d), []
+    for i in range(8):
+        o = torch.zeros(len(q), nq * d, device="cuda", dtype=torch.bfloat16)
+        Q.h3enc_op_attention_cross(q, k, v, o, nq, nkv, d, ws, cu_q, cu_k)
+        outs.append(o)
+    assert all(torch.equal(o, outs[0]) for o in outs)
+    assert not outs[0][:before].any() and not outs[0][-behind:].any()
+    for s in (0, 1, n // 2, n - 1):
+        a, b = slice(before + m * s, before + m * (s + 1)), slice(before + keys * s, before + keys * (s + 1))
+        _check_cross(_f64(outs[0][a]).reshape(m, nq, d), _f64(q[a]).reshape(m, nq, d), _f64(k[b]).reshape(keys, nkv, d),
+                     _f64(v[b]).reshape(keys, nkv, d))
+
+
 def test_attention_cross_of_one_sequence_needs_no_offsets():
     g = _gen(1)
     q, kv = _randn(g, 50, 256), _randn(g, 200, 256)
