@@ -472,7 +472,7 @@ __global__ void __launch_bounds__(Shape<D, F8, BLOCKS>::THREADS, 1)
     // parts of segments that other CTAs share, joined at the end: [0] the run's first segment if it
     // began before the run, [1] its last if it goes on behind it
     struct Part {
-        int b, kvh, chunk, seg, seg_end;
+        int b, u, seg, seg_end;
     } shared[2];
     shared[0].b = shared[1].b = -1;
     const int trow = tid / (D / 4), tcol = tid % (D / 4) * 4;   // this thread's output in the sums of the joins
@@ -752,7 +752,7 @@ __global__ void __launch_bounds__(Shape<D, F8, BLOCKS>::THREADS, 1)
         const bool whole = seg >= t0 && seg_end <= t1;
         const float vs = F8 ? p.cache.v_scale[kvh] : 1.f;
         const int slot = 2 * blockIdx.x + (seg < t0 ? 0 : 1);
-        if (!whole) shared[seg < t0 ? 0 : 1] = Part{w.b, kvh, chunk, seg, seg_end};
+        if (!whole) shared[seg < t0 ? 0 : 1] = Part{w.b, w.u, seg, seg_end};
         #pragma unroll
         for (int r8 = 0; r8 < (WIDE ? 16 : 8); r8 += 8) {
             // the warps that share rows: all, or (SPLIT) those of a group
@@ -841,7 +841,8 @@ __global__ void __launch_bounds__(Shape<D, F8, BLOCKS>::THREADS, 1)
         if (!s_last[x]) continue;
         const Part y = x ? shared[1] : shared[0];
         const int first = owner(y.seg), n = owner(y.seg_end - 1) - first + 1, begin = group_of(first, n);
-        const int kvh = y.kvh, chunk = y.chunk, rows = rows_of(y.b, chunk);
+        const int chunks = EXT == PACKED ? (nq[y.b] * a.group + CH - 1) / CH : a.chunks, kvh = kv_head(y.u, chunks);
+        const int chunk = y.u - kvh * chunks, rows = rows_of(y.b, chunk);
         const float vs = F8 ? p.cache.v_scale[kvh] : 1.f;
         // The parts begin, begin + STEP, ... (count of them): up to BATCH at a time, all their loads in flight.  A lane
         // takes four columns of each, and of one part (lane li: part li of the batch) the row's maximum and sum.
