@@ -12,7 +12,7 @@
 // pair shares every step; a single tile is run as A and B too, A on the even steps and B on the odd ones, and their
 // results are merged at the end.  Items weigh 2 per step (single 1), and FIXED for their beginning and end; their weights are laid end
 // to end and cut into one equal run per CTA, one CTA per SM, whatever the lengths are (read on the device); a step goes to the run
-// that holds its first weight.  A run may end inside an item, whose parts (unnormalised output, running
+// that holds its first weight, or, where that is about as even, an item to the run that holds its first.  A run may end inside an item, whose parts (unnormalised output, running
 // maximum and sum, fp32) go to the workspace and are joined in key order by a second launch: the result does not depend
 // on timing.
 //   warps 0-3    softmax of tile A, 4-7 of tile B: a thread per row; the running maximum is raised lazily; an item's end:
@@ -199,6 +199,12 @@ __device__ __forceinline__ int seg_keys(const Segments &g, int s) {
 __device__ __forceinline__ int seg_tokens(const Segments &g, int s) { return max(g.cq[s + 1] - g.cq[s], 0); }
 
 constexpr int FIXED = 2;   // weight of an item's beginning and end (a pair's step: 2)
+// Weight that parts and their join cost (where there are pairs, and where not): packed rows' runs end between items where that makes
+// none longer by more than this.  64 q heads over 8 of 128, runs that cut items against whole ones, and the weight added: 4096 queries
+// over 1024 keys 131 and 118 us (5), 512 over 1024 37.3 and 24.3 (3), 512 over 4096 73 and 64 (10), 16 ragged prompts 181 and 173 (10);
+// 64 over 1024 16.9 and 23.5 (16), 256 over 4096 45 and 64 (38).  Single tiles, 16 queries each over 500 keys, 16 sequences 20.9 and
+// 15.2 (1), 30 over 1000 40.1 and 35.7 (5).
+constexpr int JOIN_PAIRS = 12, JOIN_SINGLES = 6;
 
 // Walks the items of a run [w0, end) of weights.
 template <int MODE>
@@ -209,6 +215,7 @@ struct Walk {
     // (n_b 0: single), steps of this run [j0, j1), first weight, weight of a step - 1
     int head, chunk, blk, tok0, n_a, n_b, j0, j1, start, shift;
     int w0, end;
+    bool snap;   // the run takes the items that begin in it, whole (packed rows only)
 
     __device__ __forceinline__ void load(const Segments &g, int tok) {
         len = seg_keys<MODE>(g, s);
@@ -216,7 +223,8 @@ struct Walk {
         n = seg_tokens(g, s);
         tiles = (n + tok - 1) / tok;
     }
-    __device__ __forceinline__ void begin(int first, int behind, const Segments &g, int n_segs, int tok, int chunks) {
+    __device__ __forceinline__ void begin(int first, int behind, bool whole, const Segments &g, int n_segs, int tok, int chunks) {
+        snap = MODE == ROWS && whole;
         w0 = first;
         end = behind;
         start = behind;
@@ -237,6 +245,8 @@ struct Walk {
         chunk = u - head * chunks;
         blk = min(off / pair, tiles >> 1);
         start = w0 - (off - blk * pair);
+        shift = 2 * blk + 1 < tiles ? 1 : 0;
+        if (MODE == ROWS && snap && start < w0) j1 = 0;   // the run before has it: on to the next
     }
     __device__ __forceinline__ int weight() const { return (steps << shift) + FIXED; }
     __device__ __forceinline__ bool next(const Segments &g, int tok, int chunks, int nkv) {
@@ -263,8 +273,8 @@ struct Walk {
             n_a = min(tok, n - tok0);
             n_b = shift ? min(tok, n - tok0 - tok) : 0;
             // step j belongs to the run that holds weight start + (j << shift)
-            j0 = max((w0 - start + shift) >> shift, 0);
-            j1 = min((end - start + shift) >> shift, steps);
+            j0 = MODE == ROWS && snap ? 0 : max((w0 - start + shift) >> shift, 0);
+            j1 = MODE == ROWS && snap ? steps : min((end - start + shift) >> shift, steps);
             if (j0 < j1) return true;
         }
     }
@@ -302,7 +312,8 @@ __global__ void __launch_bounds__(Shape<D, MODE>::THREADS, 1)
     uint64_t *k_raw = F8 ? item_empty + ITEMS : k_full, *v_raw = F8 ? k_raw + NSK : v_full;   // where TMA arrives
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(F8 ? v_raw + NSV : item_empty + ITEMS);
     volatile int *abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
-    int *s_warp = reinterpret_cast<int *>(tmem_slot + 2);   // [20] scan of the warps' sums
+    int *s_warp = reinterpret_cast<int *>(tmem_slot + 2);   // [16] scan of the warps' sums
+    int *s_items = s_warp + 16, *s_most = s_items + 1;      // items, the largest weight
 
     const AttentionCross &p = a.p;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -338,6 +349,7 @@ __global__ void __launch_bounds__(Shape<D, MODE>::THREADS, 1)
             mbar_init(v_raw + i, 1);
         }
         *abort = 0;
+        *s_items = *s_most = 0;
         fence_barrier_init();
         prefetch_tmap(&tmQ);
         prefetch_tmap(&tmK);
@@ -366,7 +378,7 @@ __global__ void __launch_bounds__(Shape<D, MODE>::THREADS, 1)
         }
         __syncthreads();
         const Segments g{pre, cq, ck};
-        int n[4], sum = 0;
+        int n[4], sum = 0, items = 0, most = 0;
         #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int s = 4 * tid + i;
@@ -374,7 +386,11 @@ __global__ void __launch_bounds__(Shape<D, MODE>::THREADS, 1)
             if (s < p.n_segs) {
                 const int tokens = seg_tokens(g, s), tiles = (tokens + a.tok - 1) / a.tok, keys = seg_keys<MODE>(g, s);
                 const int steps = (keys + TK - 1) / TK;
-                if (keys > 0) n[i] = units * ((tiles >> 1) * (2 * steps + FIXED) + (tiles & 1) * (steps + FIXED));
+                if (keys > 0) {
+                    n[i] = units * ((tiles >> 1) * (2 * steps + FIXED) + (tiles & 1) * (steps + FIXED));
+                    items += units * ((tiles + 1) >> 1);
+                    if (tiles > 0) most = max(most, (tiles > 1 ? 2 * steps : steps) + FIXED + (tiles > 1 ? 1 << 30 : 0));
+                }
                 any_empty |= tokens > 0 && keys == 0;
                 bad |= cq[s + 1] < cq[s] || (MODE == ROWS && ck[s + 1] < ck[s]);
             }
@@ -388,7 +404,17 @@ __global__ void __launch_bounds__(Shape<D, MODE>::THREADS, 1)
             const int v = __shfl_up_sync(0xffffffffu, inc, o);
             if (lane >= o) inc += v;
         }
-        if (lane == 31) s_warp[warp] = inc;
+        if (MODE == ROWS) {
+            items = __reduce_add_sync(0xffffffffu, items);
+            most = __reduce_max_sync(0xffffffffu, most);
+        }
+        if (lane == 31) {
+            s_warp[warp] = inc;
+            if (MODE == ROWS && items > 0) {
+                atomicAdd(s_items, items);
+                atomicMax(s_most, most);   // (bit 30: there are pairs)
+            }
+        }
         __syncthreads();
         int at = inc - sum;
         for (int w = 0; w < warp; ++w) at += s_warp[w];
@@ -407,6 +433,14 @@ __global__ void __launch_bounds__(Shape<D, MODE>::THREADS, 1)
     // A run has a step's weight at least: the parts of an item are then those of consecutive CTAs.
     const unsigned T = (unsigned)pre[p.n_segs], G = min(T / 2, gridDim.x);
     const Runs runs(T, G);
+    bool snap = false;
+    if (MODE == ROWS && G > 0) {
+        const int items = *s_items, most = *s_most & ~(1 << 30), run = (int)(T / G);
+        // what the longest run has more than its share if runs take whole items (all alike, at most one each, or any)
+        const int more = (long long)most * items == (long long)T ? (run / most + (run % most ? 1 : 0)) * most - run
+                                                                 : items <= (int)G ? most - run : most;
+        snap = more <= (*s_most >> 30 ? JOIN_PAIRS : JOIN_SINGLES);
+    }
 
     // rows without any key: zeros, or (prefixes) an empty part
     if (__builtin_expect(any_empty, 0)) {
@@ -925,7 +959,7 @@ __global__ void __launch_bounds__(Shape<D, MODE>::THREADS, 1)
             // ------------------------------------------------ the items of the run, handed to the other warps
             Walk<MODE> w;
             const bool any = blockIdx.x < G;
-            w.begin(any ? runs.first(blockIdx.x) : 0, any ? runs.first(blockIdx.x + 1) : 0, g, p.n_segs, a.tok, a.chunks);
+            w.begin(any ? runs.first(blockIdx.x) : 0, any ? runs.first(blockIdx.x + 1) : 0, snap, g, p.n_segs, a.tok, a.chunks);
             bool ok = true, more = true;
             int pos = 0;
             for (uint32_t it = 0; ok && more; ++it) {
