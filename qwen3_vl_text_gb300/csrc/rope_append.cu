@@ -223,6 +223,7 @@ cudaError_t launch_rope_append(const RopeAppend &p, cudaStream_t st) {
     // groups of a row: the power of two, up to a whole CTA's, that leaves the fewest of them idle in
     // the last turn (the largest of such); for few rows the largest, as it has the fewest turns
     const int groups = THREADS / (p.d / 16), heads = p.nq + 2 * p.nkv, sms = device_num_sms();
+    if (sms <= 0) return cudaErrorNoDevice;
     int gshift = 0, waste = 0;
     for (int g = 1; (1 << g) <= groups && (1 << (g - 1)) < heads; ++g) {
         const int idle = ((heads + (1 << g) - 1) >> g << g) - heads;

@@ -1,6 +1,9 @@
 """A decoder that reads an encoder's states, without a GPU: the oracle against hand-made cases, and every
 refusal of the entry points before they touch CUDA."""
 import math
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -365,3 +368,29 @@ def test_attention_cross_checks_its_tensors(Q, recorded):
     a.update(cu_q=None, cu_k=None)
     Q.h3enc_op_attention_cross(**a)
     assert recorded.args[13:16] == (None, None, 1)
+
+
+# ---------------------------------------------------------------- sound calls without a device
+
+_WITHOUT_DEVICE = """
+import sys
+sys.path.insert(0, {root!r}); sys.path.insert(0, {tests!r})
+import qwen3_vl_text_gb300 as Q
+import test_decoder_cpu as T
+for call in (lambda: T._append(Q), lambda: T._append(Q, T._cache(Q), Q.Rope(64, 1e4)), lambda: T._shared(Q, T._cache(Q)), lambda: T._cross(Q)):
+    try:
+        call()
+    except Q.H3encError as e:
+        assert e.code == 7, e
+    else:
+        raise AssertionError("no error")
+print("all refused")
+"""
+
+
+def test_sound_calls_without_a_device_are_errors(Q):
+    """In a process of its own, which sees no device wherever it runs: a division by its 0 SMs would end it."""
+    tests = os.path.dirname(os.path.abspath(__file__))
+    r = subprocess.run([sys.executable, "-c", _WITHOUT_DEVICE.format(root=os.path.dirname(tests), tests=tests)], capture_output=True,
+                       text=True, timeout=300, env={**os.environ, "CUDA_VISIBLE_DEVICES": "-1"})
+    assert r.returncode == 0 and "all refused" in r.stdout, (r.returncode, r.stdout, r.stderr)
