@@ -32,14 +32,14 @@
 #include <type_traits>
 
 #include "common.cuh"
+#include "cross_walk.h"
 #include "kernels.h"
 
 namespace h3 {
 
-namespace {
+using namespace cross;
 
-constexpr int TQ = 128, TK = 128;
-enum { ROWS = 0, PAGES = 1, PAGES8 = 2 };   // keys: packed rows, bf16 pages, e4m3 pages
+namespace {
 
 // mbar_wait in fewer instructions: the code of this kernel's roles competes for the SM's instruction cache (with waits, masks and
 // copies of loops written out at every place, 96 KB, every role waited for instructions).
@@ -187,109 +187,12 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint32_t b_l
         : "memory");
 }
 
-// The segments, in shared memory: tokens [cq[s], cq[s + 1]), keys [ck[s], ck[s + 1]) or (pages) the first ck[s] of s;
-// pre[s]: weight of the segments before s.
-struct Segments {
-    const int *pre, *cq, *ck;
-};
-template <int MODE>
-__device__ __forceinline__ int seg_keys(const Segments &g, int s) {
-    return MODE == ROWS ? max(g.ck[s + 1] - g.ck[s], 0) : g.ck[s];
-}
-__device__ __forceinline__ int seg_tokens(const Segments &g, int s) { return max(g.cq[s + 1] - g.cq[s], 0); }
-
-constexpr int FIXED = 2;   // weight of an item's beginning and end (a pair's step: 2)
 // Weight that parts and their join cost (where there are pairs, and where not): packed rows' runs end between items where that makes
 // none longer by more than this.  64 q heads over 8 of 128, runs that cut items against whole ones, and the weight added: 4096 queries
 // over 1024 keys 131 and 118 us (5), 512 over 1024 37.3 and 24.3 (3), 512 over 4096 73 and 64 (10), 16 ragged prompts 181 and 173 (10);
 // 64 over 1024 16.9 and 23.5 (16), 256 over 4096 45 and 64 (38).  Single tiles, 16 queries each over 500 keys, 16 sequences 20.9 and
 // 15.2 (1), 30 over 1000 40.1 and 35.7 (5).
 constexpr int JOIN_PAIRS = 12, JOIN_SINGLES = 6;
-
-// Walks the items of a run [w0, end) of weights.
-template <int MODE>
-struct Walk {
-    // the segment: index, keys, steps, tokens, tiles
-    int s, len, steps, n, tiles;
-    // the item: kv head and share of its group, block of two tiles, first token in the segment, tokens of its tiles
-    // (n_b 0: single), steps of this run [j0, j1), first weight, weight of a step - 1
-    int head, chunk, blk, tok0, n_a, n_b, j0, j1, start, shift;
-    int w0, end;
-    bool snap;   // the run takes the items that begin in it, whole (packed rows only)
-
-    __device__ __forceinline__ void load(const Segments &g, int tok) {
-        len = seg_keys<MODE>(g, s);
-        steps = (len + TK - 1) / TK;
-        n = seg_tokens(g, s);
-        tiles = (n + tok - 1) / tok;
-    }
-    __device__ __forceinline__ void begin(int first, int behind, bool whole, const Segments &g, int n_segs, int tok, int chunks) {
-        snap = MODE == ROWS && whole;
-        w0 = first;
-        end = behind;
-        start = behind;
-        j1 = -1;
-        if (first >= behind) return;
-        int lo = 0, hi = n_segs;   // the s with pre[s] <= w0 < pre[s + 1]
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (g.pre[mid] <= w0) lo = mid;
-            else hi = mid;
-        }
-        s = lo;
-        load(g, tok);
-        int off = w0 - g.pre[s];
-        const int pair = 2 * steps + FIXED, unit = (tiles >> 1) * pair + (tiles & 1) * (steps + FIXED), u = off / unit;
-        off -= u * unit;
-        head = u / chunks;
-        chunk = u - head * chunks;
-        blk = min(off / pair, tiles >> 1);
-        start = w0 - (off - blk * pair);
-        shift = 2 * blk + 1 < tiles ? 1 : 0;
-        if (MODE == ROWS && snap && start < w0) j1 = 0;   // the run before has it: on to the next
-    }
-    __device__ __forceinline__ int weight() const { return (steps << shift) + FIXED; }
-    __device__ __forceinline__ bool next(const Segments &g, int tok, int chunks, int nkv) {
-        while (true) {
-            if (j1 >= 0 && start < end) {   // on from the item before
-                start += weight();
-                if (start >= end) return false;
-                if (2 * ++blk >= tiles) {
-                    blk = 0;
-                    if (++chunk == chunks) {
-                        chunk = 0;
-                        if (++head == nkv) {
-                            head = 0;
-                            do ++s;
-                            while (g.pre[s + 1] == g.pre[s]);
-                            load(g, tok);
-                        }
-                    }
-                }
-            }
-            if (start >= end) return false;
-            shift = 2 * blk + 1 < tiles ? 1 : 0;
-            tok0 = blk * 2 * tok;
-            n_a = min(tok, n - tok0);
-            n_b = shift ? min(tok, n - tok0 - tok) : 0;
-            // step j belongs to the run that holds weight start + (j << shift)
-            j0 = MODE == ROWS && snap ? 0 : max((w0 - start + shift) >> shift, 0);
-            j1 = MODE == ROWS && snap ? steps : min((end - start + shift) >> shift, steps);
-            if (j0 < j1) return true;
-        }
-    }
-};
-
-// The runs: T / G weights each, one more for the first T % G.
-struct Runs {
-    unsigned run, longer;
-    __device__ __forceinline__ Runs(unsigned T, unsigned G) : run(G ? T / G : 0), longer(T - run * G) {}
-    __device__ __forceinline__ int first(unsigned c) const { return (int)(c * run + min(c, longer)); }
-    __device__ __forceinline__ int owner(unsigned w) const {
-        const unsigned split = longer * (run + 1);
-        return (int)(w < split ? w / (run + 1) : longer + (w - split) / run);
-    }
-};
 
 template <int D, int MODE>
 __global__ void __launch_bounds__(Shape<D, MODE>::THREADS, 1)
@@ -387,7 +290,7 @@ __global__ void __launch_bounds__(Shape<D, MODE>::THREADS, 1)
                 const int tokens = seg_tokens(g, s), tiles = (tokens + a.tok - 1) / a.tok, keys = seg_keys<MODE>(g, s);
                 const int steps = (keys + TK - 1) / TK;
                 if (keys > 0) {
-                    n[i] = units * ((tiles >> 1) * (2 * steps + FIXED) + (tiles & 1) * (steps + FIXED));
+                    n[i] = units * unit_weight(tiles, steps);
                     items += units * ((tiles + 1) >> 1);
                     if (tiles > 0) most = max(most, (tiles > 1 ? 2 * steps : steps) + FIXED + (tiles > 1 ? 1 << 30 : 0));
                 }
@@ -1157,12 +1060,7 @@ size_t attention_cross_workspace_bytes(int num_sms, int d) {
 }
 
 long long attention_cross_weight(int Tq, int max_keys, int n_segs, int nq, int nkv) {
-    const int group = nq / nkv, gc = std::min(group, TQ), chunks = (group + TQ - 1) / TQ, tok = TQ / gc;
-    // (every segment's last tile of rows may be partial)
-    const double tiles = (double)Tq / (2 * tok) + std::min(n_segs, Tq);
-    const double steps = (double)max_keys / TK + 1;
-    const double most = (double)nkv * chunks * tiles * (2 * steps + FIXED);
-    return most > 2e9 ? -1 : (long long)most + 1;
+    return weight_bound(Tq, max_keys, n_segs, nq, nkv);
 }
 
 cudaError_t launch_attention_cross(const AttentionCross &p, cudaStream_t st) {
