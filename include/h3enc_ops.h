@@ -528,7 +528,8 @@ H3ENC_API int64_t h3enc_op_attention_decode_shared_workspace_bytes(int32_t n_seq
  *   q [Tq, ld_q], o [Tq, ld_o]: head h at column h*d; k [Tk, ld_k], v [Tk, ld_v]: kv head g at column g*d (k and v may be
  *   columns of one projection).  o must not overlap q, k or v.
  *   cu_q, cu_k DEVICE int32 [n_seqs + 1], not running back; each may be NULL with n_seqs 1 (all rows).  Offsets outside
- *   [0, Tq] or [0, Tk] are clamped; that, or one that runs back, sets status bit 2 (rows of two sequences are undefined).
+ *   [0, Tq] or [0, Tk] are clamped; that, or one that runs back, sets status bit 2 (rows of two sequences are undefined,
+ *   nothing outside o's Tq rows is written).
  *   workspace: h3enc_op_attention_cross_workspace_bytes() bytes, 256-byte aligned, zero-filled once before its first use (and
  *   again after a call whose status reported a timeout) and then reused by calls of any sizes.  Calls (and graphs that hold them) sharing it must not overlap on the GPU.
  * The result does not depend on timing: the same inputs give the same bits on every run.  A bounded wait that runs out sets

@@ -268,18 +268,23 @@ __global__ void __launch_bounds__(Shape<D, MODE>::THREADS, 1)
     bool any_empty = false;
     const int units = p.nkv * a.chunks;
     {
-        bool bad = false;
+        bool bad = false, back = false;
         for (int i = tid; i <= p.n_segs; i += S::THREADS) {
             const int q = p.cu_q ? p.cu_q[i] : i ? p.Tq : 0;
-            cq[i] = min(max(q, 0), p.Tq);
+            cq[i] = clamped(q, p.Tq);
             bad |= q != cq[i];
+            back |= p.cu_q && i < p.n_segs && p.cu_q[i + 1] < q;
             if (MODE == ROWS || i < p.n_segs) {
                 const int k = MODE != ROWS ? p.key_lens[i] : p.cu_k ? p.cu_k[i] : i ? p.max_keys : 0;
-                ck[i] = min(max(k, 0), p.max_keys);
+                ck[i] = clamped(k, p.max_keys);
                 bad |= k != ck[i];
             }
         }
-        __syncthreads();
+        if (__builtin_expect(__syncthreads_or(back), 0)) {
+            if (tid == 0) ascend(cq, p.n_segs + 1);
+            bad = true;
+            __syncthreads();
+        }
         const Segments g{pre, cq, ck};
         int n[4], sum = 0, items = 0, most = 0;
         #pragma unroll
@@ -295,7 +300,7 @@ __global__ void __launch_bounds__(Shape<D, MODE>::THREADS, 1)
                     if (tiles > 0) most = max(most, (tiles > 1 ? 2 * steps : steps) + FIXED + (tiles > 1 ? 1 << 30 : 0));
                 }
                 any_empty |= tokens > 0 && keys == 0;
-                bad |= cq[s + 1] < cq[s] || (MODE == ROWS && ck[s + 1] < ck[s]);
+                bad |= MODE == ROWS && ck[s + 1] < ck[s];
             }
             sum += n[i];
         }

@@ -22,6 +22,13 @@ constexpr int TQ = 128, TK = 128;           // rows of a tile, keys of a step
 enum { ROWS = 0, PAGES = 1, PAGES8 = 2 };   // keys: packed rows, bf16 pages, e4m3 pages
 constexpr int FIXED = 2;   // weight of an item's beginning and end (a pair's step: 2)
 
+// Offsets come from the device and may be anything: each is held to [0, most] ...
+H3_WALK int clamped(int x, int most) { return min(max(x, 0), most); }
+// ... and those of queries then to none before it, so that no row of queries is in two segments: weight_bound holds for such.
+H3_WALK void ascend(int *v, int n) {
+    for (int i = 1; i < n; ++i) v[i] = max(v[i], v[i - 1]);
+}
+
 // Weight of the items of one kv head's share of a segment: pairs of row tiles and a last single one.
 H3_WALK int unit_weight(int tiles, int steps) { return (tiles >> 1) * (2 * steps + FIXED) + (tiles & 1) * (steps + FIXED); }
 

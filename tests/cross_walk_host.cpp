@@ -32,6 +32,13 @@ struct Case {
     std::vector<int> cq, ck;   // offsets as the kernel has them
 };
 
+// Offsets as the kernel takes them: of queries in order, of keys each by itself.
+std::vector<int> taken(std::vector<int> v, int most, bool in_order = true) {
+    for (int &x : v) x = clamped(x, most);
+    if (in_order) ascend(v.data(), (int)v.size());
+    return v;
+}
+
 // What the kernel does with a call's segments: weights laid end to end, cut into a run per CTA, walked.
 template <int MODE>
 void check(const Case &c, int sms, bool whole, bool every_step) {
@@ -128,6 +135,33 @@ int ascending(int cases) {
     return cases;
 }
 
+// Offsets of any values, as a device array may hold them: clamped and put in order like the kernel's.
+int any_offsets(int cases) {
+    for (int it = 0; it < cases; ++it) {
+        Case c;
+        const int S = 1 + below(it % 2 ? 8 : 1024), kind = it % 4;
+        c.nkv = 1 << below(4);
+        c.nq = c.nkv * (1 + below(16));
+        c.Tq = 1 + below(it % 3 ? 2000 : 40000);
+        c.Tk = 1 + below(it % 3 ? 5000 : 300000);
+        std::vector<int> q(S + 1), k(S + 1);
+        for (int s = 0; s <= S; ++s) {
+            const auto value = [&](int most) {
+                if (kind == 0) return s % 2 ? most : 0;                       // back to the beginning every second time
+                if (kind == 1) return (int)(rng() - (1u << 31));              // anything
+                if (kind == 2) return s % 3 == 1 ? most - below(5) : below(most + 1);
+                return (int)((long long)most * s / S) - (below(20) ? 0 : below(most + 1));   // in order, but for some
+            };
+            q[s] = value(c.Tq);
+            k[s] = value(c.Tk);
+        }
+        c.cq = taken(q, c.Tq);
+        c.ck = taken(k, c.Tk, false);
+        check_all(c, it % 5 ? 1 + below(152) : 152, true);
+    }
+    return cases;
+}
+
 }  // namespace
 
-int main() { printf("ok %d\n", ascending(1500)); }
+int main(int argc, char **argv) { printf("ok %d\n", argc > 1 ? any_offsets(400) : ascending(1500)); }

@@ -23,3 +23,10 @@ def _run(program, *args):
 def test_runs_of_segments_in_order(program):
     """Every step once, cut or whole, over 1500 calls; memory that a walk does not set is filled with another pattern."""
     _run(program)
+
+
+def test_runs_of_any_offsets(program):
+    """Offsets that run back or lie outside: the weights stay within the bound that the call is accepted by (so 32 bits hold
+    them), and every item within its tensors.  1024 offsets that go between 0 and 16,384 queries, and 0 and 200,000 keys,
+    in turns would come to 6.6e9 (64 heads over 8) where the bound is 3.8e7."""
+    _run(program, "any")

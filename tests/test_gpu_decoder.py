@@ -478,6 +478,36 @@ def test_attention_cross_reports_bad_offsets(cu_q, cu_k):
         _check_cross(_f64(o[:3]).reshape(3, 2, 64), _f64(q[:3]).reshape(3, 2, 64), *(_f64(k[:cu_k[1]]).reshape(-1, 2, 64),) * 2)
 
 
+@pytest.mark.parametrize("cu_q,cu_k,sound", [([0, 300, 100, 400], [0, 200, 300, 500], []), ([0, 150, 250, 400], [0, 300, 200, 500], [0]),
+                                             ([0, 150, 250, 401], [0, 200, 300, 500], [0, 1]), ([-7, 150, 250, 400], [0, 200, 300, 500], [1, 2]),
+                                             ([0, 150, 250, 400], [0, 200, 300, 2 ** 31 - 1], [0, 1]),
+                                             ([2 ** 31 - 1, -5, 400, 400], [9, 9, -9, 500], [])])
+def test_attention_cross_of_many_rows_reports_bad_offsets(cu_q, cu_k, sound):
+    """As the test above with over 32 rows per kv head and sequence, which another kernel takes."""
+    g = _gen(16)
+    q, k = _randn(g, 400, 256), _randn(g, 500, 128)
+    o = torch.full((410, 256), 7.0, device="cuda", dtype=torch.bfloat16)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    Q.h3enc_op_attention_cross(q, k, k, o[:400], 4, 2, 64, _cross_ws(64), _i32(cu_q), _i32(cu_k), status)
+    assert int(status.item()) == 2 and (o[400:] == 7).all() and np.isfinite(_f64(o)).all()
+    for s in sound:
+        a, b = slice(cu_q[s], cu_q[s + 1]), slice(cu_k[s], cu_k[s + 1])
+        _check_cross(_f64(o[a]).reshape(-1, 4, 64), _f64(q[a]).reshape(-1, 4, 64), *(_f64(k[b]).reshape(-1, 2, 64),) * 2)
+
+
+def test_attention_cross_of_offsets_between_the_ends():
+    """Every second offset back at 0: no row is in more than one sequence, so the weights stay within the call's bound (each
+    sequence by itself, they would pass 32 bits; tests/cross_walk_host.cpp walks such calls on the host)."""
+    g = _gen(17)
+    n, Tq, Tk, d = 1024, 16384, 100000, 64
+    q, kv = _randn(g, Tq, 64 * d), _randn(g, Tk, 16 * d)
+    o = torch.full((Tq + 8, 64 * d), 7.0, device="cuda", dtype=torch.bfloat16)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    cu_q, cu_k = (_i32([x * (i % 2) for i in range(n + 1)]) for x in (Tq, Tk))
+    Q.h3enc_op_attention_cross(q, kv[:, :8 * d], kv[:, 8 * d:], o[:Tq], 64, 8, d, _cross_ws(d), cu_q, cu_k, status)
+    assert int(status.item()) == 2 and (o[Tq:] == 7).all() and bool(torch.isfinite(o).all())
+
+
 def test_attention_cross_captured_and_replayed_with_other_lengths():
     g = _gen(5)
     nq, nkv, d = 8, 2, 128
