@@ -36,6 +36,7 @@
 #include <type_traits>
 
 #include "common.cuh"
+#include "cross_walk.h"
 #include "kernels.h"
 
 namespace h3 {
@@ -281,6 +282,22 @@ __global__ void __launch_bounds__(Shape<D, F8, BLOCKS>::THREADS, 1)
         if (bad && blockIdx.x == 0) report(p.status, ST_BOUNDS);
         __syncthreads();
     }
+    if constexpr (EXT == PACKED) {
+        static_assert(TK == 64, "cross::packed_tiles");
+        bool bad = false, back = false;
+        for (int i = tid; i <= p.n_seqs; i += S::THREADS) {
+            const int q = p.cu_q ? p.cu_q[i] : i ? p.Tq : 0, k = p.seq_lens ? p.seq_lens[i] : i ? p.max_len : 0;
+            q0[i] = cross::clamped(q, p.Tq);
+            k0[i] = cross::clamped(k, p.max_len);
+            bad |= q != q0[i] || k != k0[i];
+            back |= p.cu_q && i < p.n_seqs && p.cu_q[i + 1] < q;
+        }
+        if ((bad || back) && blockIdx.x == 0) report(p.status, ST_BOUNDS);
+        if (__builtin_expect(__syncthreads_or(back), 0)) {
+            if (tid == 0) cross::ascend(q0, p.n_seqs + 1);
+            __syncthreads();
+        }
+    }
     // pre[b] = tiles of the sequences before b: four sequences per thread, scanned over the block
     {
         int n[4], sum = 0;
@@ -290,16 +307,10 @@ __global__ void __launch_bounds__(Shape<D, F8, BLOCKS>::THREADS, 1)
             n[i] = 0;
             if (b < p.n_seqs) {
                 if constexpr (EXT == PACKED) {
-                    const auto range = [&](const int32_t *cu, int most, int &first) {   // [first, first + the result)
-                        const int f = cu ? cu[b] : 0, e = cu ? cu[b + 1] : most;
-                        first = min(max(f, 0), most);
-                        const int end = min(max(e, 0), most);
-                        if ((f != first || e != end || end < first) && blockIdx.x == 0) report(p.status, ST_BOUNDS);
-                        return max(end - first, 0);
-                    };
-                    nq[b] = range(p.cu_q, p.Tq, q0[b]);
-                    const int c = lens[b] = range(p.seq_lens, p.max_len, k0[b]);
-                    n[i] = (c + TK - 1) / TK * p.cache.nkv * ((nq[b] * a.group + CH - 1) / CH);
+                    nq[b] = q0[b + 1] - q0[b];
+                    lens[b] = max(k0[b + 1] - k0[b], 0);
+                    if (k0[b + 1] < k0[b] && blockIdx.x == 0) report(p.status, ST_BOUNDS);
+                    n[i] = cross::packed_tiles(nq[b], lens[b], a.group, p.cache.nkv, CH);
                 } else {
                     const int len = p.seq_lens[b], c = min(max(len, 0), p.max_len);
                     lens[b] = c;
@@ -1069,8 +1080,7 @@ int attention_packed_rows(int Tq, int Tk, int n_segs, int nq, int nkv) {
     // and 14.8; 64 over 1024 29 and 16.5.
     const long long group = nq / nkv, rows = group * ((Tq + n_segs - 1) / n_segs);
     if (rows > 32) return 0;
-    const long long chunks = (Tq * group + 7) / 8 + n_segs;
-    return nkv * chunks * ((long long)Tk / 64 + 1) > INT_MAX - 65 ? 0 : (int)std::max(rows, 1LL);
+    return cross::packed_bound(Tq, Tk, n_segs, nq, nkv) < 0 ? 0 : (int)std::max(rows, 1LL);
 }
 
 cudaError_t launch_attention_packed(const AttentionCross &c, int rows, cudaStream_t st) {

@@ -138,5 +138,16 @@ inline long long weight_bound(int Tq, int max_keys, int n_segs, int nq, int nkv)
     return most > 2e9 ? -1 : (long long)most + 1;
 }
 
+// Few rows, by attention_decode.cu: tiles of 64 keys that a segment of `tokens` queries over `keys` keys takes, the rows of each
+// kv head (its group of q heads of every query) `rows` at a time ...
+H3_WALK int packed_tiles(int tokens, int keys, int group, int nkv, int rows) {
+    return (keys + 63) / 64 * nkv * ((tokens * group + rows - 1) / rows);
+}
+// ... and a bound on all segments', 8 rows at a time; -1 where 32 bits do not hold it and the runs' look-ahead.
+inline long long packed_bound(int Tq, int Tk, int n_segs, int nq, int nkv) {
+    const long long chunks = ((long long)Tq * (nq / nkv) + 7) / 8 + n_segs, most = nkv * chunks * ((long long)Tk / 64 + 1);
+    return most > 2147483647LL - 65 ? -1 : most;
+}
+
 }  // namespace cross
 }  // namespace h3

@@ -113,6 +113,13 @@ void check_all(const Case &c, int sms, bool every_step) {
     Case p = c;   // pages: the first ck[s] keys of row s of a table
     for (size_t s = 0; s + 1 < c.ck.size(); ++s) p.ck[s] = std::max(c.ck[s + 1] - c.ck[s], 0);
     check<PAGES>(p, sms, false, every_step);
+
+    const long long bound = packed_bound(c.Tq, c.Tk, (int)c.cq.size() - 1, c.nq, c.nkv);
+    long long tiles = 0;
+    for (size_t s = 0; s + 1 < c.cq.size() && bound >= 0 && (long long)c.Tq * (c.nq / c.nkv) <= 32768; ++s) {
+        tiles += packed_tiles(c.cq[s + 1] - c.cq[s], p.ck[s], c.nq / c.nkv, c.nkv, 8);
+        if (tiles > bound) wrong("%lld tiles of the first %zu segments, bound %lld", tiles, s + 1, bound);
+    }
 }
 
 // Segments that follow one another, empty ones among them.

@@ -508,6 +508,22 @@ def test_attention_cross_of_offsets_between_the_ends():
     assert int(status.item()) == 2 and (o[Tq:] == 7).all() and bool(torch.isfinite(o).all())
 
 
+def test_attention_cross_of_few_rows_and_offsets_between_the_ends():
+    """The same with so few rows that the decoding kernel takes them: 4096 queries of one head by each of 512 sequences would
+    be 3.3e10 tiles.  The workspace still serves a sound call."""
+    g = _gen(18)
+    n, Tq, Tk, d = 1024, 4096, 500000, 64
+    q, kv = _randn(g, Tq, 8 * d), _randn(g, Tk, 16 * d)
+    o = torch.full((Tq + 8, 8 * d), 7.0, device="cuda", dtype=torch.bfloat16)
+    status, ws = torch.zeros(1, dtype=torch.int32, device="cuda"), _cross_ws(d)
+    cu_q, cu_k = (_i32([x * (i % 2) for i in range(n + 1)]) for x in (Tq, Tk))
+    Q.h3enc_op_attention_cross(q, kv[:, :8 * d], kv[:, 8 * d:], o[:Tq], 8, 8, d, ws, cu_q, cu_k, status)
+    assert int(status.item()) == 2 and (o[Tq:] == 7).all() and bool(torch.isfinite(o).all())
+    Q.h3enc_op_attention_cross(q[:8], kv[:900, :8 * d], kv[:900, 8 * d:], o[:8], 8, 8, d, ws, _i32([0, 3, 8]), _i32([0, 200, 900]))
+    for a, b in ((slice(0, 3), slice(0, 200)), (slice(3, 8), slice(200, 900))):
+        _check_cross(_f64(o[a]).reshape(-1, 8, d), _f64(q[a]).reshape(-1, 8, d), *(_f64(t).reshape(-1, 8, d) for t in (kv[b, :8 * d], kv[b, 8 * d:])))
+
+
 def test_attention_cross_captured_and_replayed_with_other_lengths():
     g = _gen(5)
     nq, nkv, d = 8, 2, 128
