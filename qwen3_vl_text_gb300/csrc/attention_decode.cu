@@ -269,17 +269,26 @@ __global__ void __launch_bounds__(Shape<D, F8, BLOCKS>::THREADS, 1)
     pdl_wait();
 
     if constexpr (EXT == PREFIX) {
-        for (int i = tid; i < p.n_seqs; i += S::THREADS) plen[i] = pidx[i] = 0;
-        __syncthreads();
+        // The group of each sequence, by a search of the offsets: every CTA has to find the same (the runs are cut by these lengths,
+        // and the workspace's counters count their parts), also of offsets that run back.
+        int *rows = nq;
         bool bad = false;
-        for (int g = tid; g < p.n_prefixes && !p.pre_o; g += S::THREADS) {
-            const int len = p.prefix_lens[g], c = min(max(len, 0), p.max_prefix);
-            const int f = p.prefix_rows ? p.prefix_rows[g] : 0, e = p.prefix_rows ? p.prefix_rows[g + 1] : p.n_seqs;
-            const int first = min(max(f, 0), p.n_seqs), end = min(max(e, 0), p.n_seqs);
-            bad |= len != c || f != first || e != end || end < first;
-            for (int b = first; b < end; ++b) plen[b] = c, pidx[b] = g;
+        for (int i = tid; i <= p.n_prefixes && !p.pre_o; i += S::THREADS) {
+            const int r = p.prefix_rows ? p.prefix_rows[i] : i ? p.n_seqs : 0;
+            rows[i] = cross::clamped(r, p.n_seqs);
+            bad |= r != rows[i];
+            if (i < p.n_prefixes) {
+                const int len = p.prefix_lens[i];
+                bad |= len != cross::clamped(len, p.max_prefix) || (p.prefix_rows && p.prefix_rows[i + 1] < r);
+            }
         }
         if (bad && blockIdx.x == 0) report(p.status, ST_BOUNDS);
+        __syncthreads();
+        for (int b = tid; b < p.n_seqs; b += S::THREADS) {
+            const int at = cross::group_of(rows, p.n_prefixes, b);
+            plen[b] = at < 0 ? 0 : cross::clamped(p.prefix_lens[at], p.max_prefix);
+            pidx[b] = max(at, 0);
+        }
         __syncthreads();
     }
     if constexpr (EXT == PACKED) {

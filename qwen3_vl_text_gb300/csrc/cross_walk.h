@@ -29,6 +29,18 @@ H3_WALK void ascend(int *v, int n) {
     for (int i = 1; i < n; ++i) v[i] = max(v[i], v[i - 1]);
 }
 
+// The group [rows[g], rows[g + 1]) of n that sequence b is in, -1: none.  Of offsets that run back some group that holds b
+// or none, the same for every caller.
+H3_WALK int group_of(const int *rows, int n, int b) {
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (rows[mid] <= b) lo = mid;
+        else hi = mid;
+    }
+    return n > 0 && rows[lo] <= b && b < rows[lo + 1] ? lo : -1;
+}
+
 // Weight of the items of one kv head's share of a segment: pairs of row tiles and a last single one.
 H3_WALK int unit_weight(int tiles, int steps) { return (tiles >> 1) * (2 * steps + FIXED) + (tiles & 1) * (steps + FIXED); }
 

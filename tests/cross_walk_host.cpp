@@ -114,6 +114,14 @@ void check_all(const Case &c, int sms, bool every_step) {
     for (size_t s = 0; s + 1 < c.ck.size(); ++s) p.ck[s] = std::max(c.ck[s + 1] - c.ck[s], 0);
     check<PAGES>(p, sms, false, every_step);
 
+    for (int b = -1; b < (int)c.cq.size() + 3; ++b) {   // (as offsets of sequences)
+        const int S = (int)c.cq.size() - 1, at = group_of(c.cq.data(), S, b);
+        int want = -1;
+        for (int i = 0; i < S; ++i)
+            if (c.cq[i] <= b && b < c.cq[i + 1]) want = i;
+        if (at != want) wrong("sequence %d in group %d, not %d", b, at, want);
+    }
+
     const long long bound = packed_bound(c.Tq, c.Tk, (int)c.cq.size() - 1, c.nq, c.nkv);
     long long tiles = 0;
     for (size_t s = 0; s + 1 < c.cq.size() && bound >= 0 && (long long)c.Tq * (c.nq / c.nkv) <= 32768; ++s) {
@@ -161,6 +169,11 @@ int any_offsets(int cases) {
             };
             q[s] = value(c.Tq);
             k[s] = value(c.Tk);
+        }
+        const std::vector<int> back = taken(q, c.Tq, false);
+        for (int b = 0; b < 50; ++b) {
+            const int at = group_of(back.data(), S, b);
+            if (at >= S || (at >= 0 && (back[at] > b || back[at + 1] <= b))) wrong("sequence %d in group %d", b, at);
         }
         c.cq = taken(q, c.Tq);
         c.ck = taken(k, c.Tk, false);

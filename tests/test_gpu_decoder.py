@@ -706,6 +706,45 @@ def test_attention_decode_shared_reports_bad_pages_and_lengths(dtype, far):
 
 
 @pytest.mark.parametrize("far", [False, True])
+def test_attention_decode_shared_of_groups_that_run_back(far):
+    """Offsets of groups that overlap: reported, nothing written outside, and the workspace is fit for the next call (its arrival
+    counters are zero again: every CTA has seen the same lengths).  Then one group of very many, and empty groups."""
+    g = _gen(19)
+    n, nq, nkv, d, page, P = 300, 4, 2, 64, 16, 64
+    cache = _pool(g, 6 * 4 + n * 2, nkv, page, d, BF16)
+    ids = torch.randperm(6 * 4 + n * 2, device="cuda", generator=g).to(torch.int32)
+    far_cols = _far_bound(n, nkv, d, BF16) // page + 1 if far else 0
+    ptable = torch.cat([ids[:24].view(6, 4), ids.new_full((6, far_cols), -1)], 1).contiguous()
+    table, plens, lens = ids[24:].view(n, 2).contiguous(), [64, 1, 33, 0, 50, 17], [b % 30 for b in range(n)]
+
+    def tokens(ls):
+        return [torch.randn(x, nkv, d, device="cuda", generator=g) for x in ls], [torch.randn(x, nkv, d, device="cuda", generator=g) for x in ls]
+
+    pre, own = _fill(cache, ptable, plens, *tokens(plens)), _fill(cache, table, lens, *tokens(lens))
+    q, o = _randn(g, n, nq * d), torch.full((n + 2, nq * d), 7.0, device="cuda", dtype=torch.bfloat16)
+    ws = torch.zeros(Q.h3enc_op_attention_decode_shared_workspace_bytes(n, nq, 32), dtype=torch.uint8, device="cuda")
+
+    def run(rows):
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        Q.h3enc_op_attention_decode_shared(q, o[:n], cache, ptable, _i32(plens), P + page * far_cols, table, _i32(lens), nq, 32, ws,
+                                           prefix_rows=_i32(rows), status=status)
+        assert (o[n:] == 7).all() and not ws[:3 * 1024 * 4].any()
+        return int(status.item())
+
+    for rows in ([0, 300, 0, 300, 0, 300, 0], [300, 250, 200, 150, 100, 50, 0], [0, 200, 100, 250, 150, 300, 300],
+                 [-5, 100, 2 ** 31 - 1, -(2 ** 31), 7, 250, 400]):
+        assert run(rows) == 2
+    for rows in ([0, 300, 300, 300, 300, 300, 300], [0, 0, 0, 299, 299, 299, 300], [3, 50, 100, 150, 200, 250, 290]):
+        assert run(rows) == 0
+        for b in [0, 2, 3, 49, 50, 151, 249, 250, 289, 290, 298, 299]:
+            at = [i for i in range(6) if rows[i] <= b < rows[i + 1]]
+            pk, pv = pre[at[0]] if at else (pre[0][0][:0], pre[0][1][:0])
+            want, _ = O.decoder.attend_prefix(_f64(q[b]).reshape(nq, d), pk, pv, *own[b]) if len(pk) + lens[b] else (np.zeros((nq, d)), 0)
+            # (|v| is at most 5 and each of the weights off by 2^-8 at most, and the output by half a step of values below 4)
+            assert np.abs(_f64(o[b]).reshape(nq, d) - want).max() <= 5 * 2.0 ** -8 + 2.0 ** -7
+
+
+@pytest.mark.parametrize("far", [False, True])
 def test_attention_decode_shared_without_own_tokens_or_own_pages(far):
     """No own tokens at all: max_len 0 and a page table of no columns."""
     g = _gen(14)
