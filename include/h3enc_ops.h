@@ -503,9 +503,11 @@ H3ENC_API h3enc_status h3enc_op_rope_append(const void *qkv, int64_t ld_qkv, int
  *   weight_in, weight_out: of the own tokens; the prefixes' weights are not accumulated.
  *   workspace: h3enc_op_attention_decode_shared_workspace_bytes() bytes, with the rules of h3enc_op_attention_decode's
  *   (zero-filled again after a call whose status reported a timeout).
- * The weights of a prefix's tokens enter the second sum in bf16 (e4m3: f16), off by up to 2^-8 (2^-11) of each, and those
- * below 2^-126 (e4m3: 2^-38) of the largest count as 0; where all sequences together would read at most 200 MB of prefixes
- * (by max_prefix), each reads its own again in one launch, with the rounding of h3enc_op_attention_decode.  Requires n_prefixes <= 1024, max_prefix <= 2^30;
+ * The weights of a prefix's tokens enter the second sum with 16 bits, as the own tokens' do (e4m3: in f16, off by up to 2^-11
+ * of each, where the own tokens' have 22), and those below 2^-126 (e4m3: 2^-38) of the largest count as 0, also times an infinite
+ * value (as all below 2^-108 may there), which is NaN; where all sequences together would read at most 200 MB of prefixes (by
+ * max_prefix), each reads its own again in one launch, with the rounding of h3enc_op_attention_decode.
+ * Requires n_prefixes <= 1024, max_prefix <= 2^30;
  * n_kv_heads * ceil(heads per kv head / 128) * (n_seqs / (2 max(128 / heads per kv head, 1)) + min(n_prefixes, n_seqs)) *
  * (max_prefix / 64 + 4) above 2e9 is H3ENC_ERR_UNSUPPORTED; the rest as for h3enc_op_attention_decode. */
 H3ENC_API h3enc_status h3enc_op_attention_decode_shared(

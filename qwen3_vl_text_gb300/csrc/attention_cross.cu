@@ -22,9 +22,9 @@
 //                cores work on one tile while the other's softmax runs; P is read from TMEM (allocated by warp 8)
 //   warp 11      finds the items of the run and hands them to the others through a ring
 //   warps 12-15  (e4m3 pages) convert raw tiles to f16 ones
-// P enters the value product in bf16 (off by up to 2^-8 of each weight, as the rounded output is of itself; a second product for
-// the remainder would halve the rate where the tensor core bounds); e4m3 pages: in f16 (2^-11), times 2^13, as f16 ends at
-// 2^-24.  Rows of no token are computed on what lies in shared memory and never stored.
+// P enters the value product in bf16 (packed rows: off by up to 2^-8 of each weight, as the rounded output is of itself) or as two halves of bf16
+// (bf16 pages: 2^-16); e4m3 pages: in f16 (2^-11), times 2^13, as f16 ends at 2^-24.  Shape::SPLIT has what each costs.  Rows of
+// no token are computed on what lies in shared memory and never stored.
 #include <algorithm>
 #include <atomic>
 #include <climits>
@@ -93,6 +93,15 @@ struct Shape {
     static constexpr int BARS = 2 * NSK + 2 * NSV + 18 + 2 * ITEMS + (F8 ? NSK + NSV : 0);
     static constexpr int READERS = 11 + (F8 ? 4 : 0);      // warps that read an item
     static constexpr int BYTES = OFF_BAR + BARS * 8 + 128 + 1024;   // + alignment of the base
+    // bf16 pages: P as two bf16 halves, as the decoding kernel has it, so that a prefix's weights keep 16 bits whichever kernel reads it.
+    // 64 sequences behind 8192 tokens 71.2 -> 74.9 us; error against 64 bits 2.20e-3 -> 1.66e-3, that of the output's rounding alone.
+    // Packed rows, which the tensor core bounds, would pay 37% (4096 queries over 1024 keys 119 -> 165 us, over 4096 406 -> 567, 16
+    // ragged prompts 175 -> 238; 2.28e-3 -> 1.66e-3), e4m3 pages 9% for an error that stays 1.66e-3.
+    static constexpr bool SPLIT = MODE == PAGES;
+    // Scores held at a time: with e4m3 or split weights too few registers for a row, S is read twice (a whole row: 81 us in that case).
+    static constexpr int HELD = MODE == ROWS ? TK : 64;
+    // Column behind the tile's first score of the weights of keys 16 kk to 16 kk + 15; their second halves lie HELD / 2 further.
+    static constexpr __device__ int p_at(int kk) { return kk * 16 / HELD * HELD + kk * 16 % HELD / 2; }
     static constexpr float UP = F8 ? 8192.f : 1.f;         // weights, and so l and o, are held times this
     static constexpr float UP_LOG2 = F8 ? 13.f : 0.f;
     // the maximum is raised when it grew by more than this (log2): weights reach 2^8, f16 ones 2^15 with UP
@@ -144,6 +153,11 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
+// Two values of 0 or more cut to bf16, and the negative of one.
+__device__ __forceinline__ uint32_t cut_bf16x2(float lo, float hi) {
+    return __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x7632);
+}
+__device__ __forceinline__ float minus_cut(float x) { return __uint_as_float((__float_as_uint(x) & 0xffff0000u) | 0x80000000u); }
 // Two e4m3 bytes -> two f16 (exact).
 __device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t two) {
     uint32_t r;
@@ -451,7 +465,7 @@ __global__ void __launch_bounds__(Shape<D, MODE>::THREADS, 1)
                 const int valid = w.len - j * TK;    // keys of the tile
                 if (busy) {
                     tc_fence_after();
-                    constexpr int HELD = F8 ? 64 : TK;   // scores held at a time (e4m3: too few registers for a row, S is read twice)
+                    constexpr int HELD = S::HELD;
                     uint32_t v[HELD];
                     float mx[8];
                     #pragma unroll
@@ -473,7 +487,7 @@ __global__ void __launch_bounds__(Shape<D, MODE>::THREADS, 1)
                         tmem_st32(tS + at, x);
                         tmem_st_wait();
                     }
-                    #pragma unroll (F8 ? 1 : 2)
+                    #pragma unroll 1
                     for (int at = 0; at < TK; at += HELD) {
                         load(at);
                         #pragma unroll
@@ -493,13 +507,13 @@ __global__ void __launch_bounds__(Shape<D, MODE>::THREADS, 1)
                         m_use = mt;
                         raise = true;
                     }
-                    // P = 2^(s * scale - m) (times UP), packed in pairs over the first 64 columns of this row of S
+                    // P = 2^(s * scale - m) (times UP), packed in pairs over the scores it comes from
                     const float off = m_use == -INFINITY ? 0.f : S::UP_LOG2 - m_use;   // (only -inf scores so far: weights 0)
                     const uint64_t scale2 = f32x2(scale, scale), off2 = f32x2(off, off);
                     uint64_t rs2[4] = {0ull, 0ull, 0ull, 0ull};
-                    #pragma unroll (F8 ? 1 : 2)
+                    #pragma unroll 1
                     for (int at = 0; at < TK; at += HELD) {
-                        if (F8) load(at);
+                        if (HELD < TK) load(at);
                         #pragma unroll
                         for (int q = 0; q < HELD; q += 32) {
                             uint32_t pk[16];
@@ -510,9 +524,26 @@ __global__ void __launch_bounds__(Shape<D, MODE>::THREADS, 1)
                                                   off2), x0, x1);
                                 const float p0 = ex2(x0), p1 = ex2(x1);
                                 rs2[i & 3] = fadd2(rs2[i & 3], f32x2(p0, p1));
-                                pk[i] = F8 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
+                                if constexpr (F8) pk[i] = pack_f16x2(p0, p1);
+                                else pk[i] = S::SPLIT ? cut_bf16x2(p0, p1) : pack_bf16x2(p0, p1);
+                                if (S::SPLIT) {
+                                    v[q + 2 * i] = __float_as_uint(p0);
+                                    v[q + 2 * i + 1] = __float_as_uint(p1);
+                                }
                             }
-                            tmem_st16(tS + (at + q) / 2, pk);
+                            tmem_st16(tS + at + q / 2, pk);
+                            if constexpr (S::SPLIT) {
+                                // what the cut left, larger by 2^-18 of the weight: above 0, as is then its product with an infinite value
+                                constexpr float up = 1.f + 0x1p-18f;
+                                #pragma unroll
+                                for (int i = 0; i < 16; ++i) {
+                                    const float p0 = __uint_as_float(v[q + 2 * i]), p1 = __uint_as_float(v[q + 2 * i + 1]);
+                                    float x0, x1;
+                                    f32x2_split(ffma2(f32x2(p0, p1), f32x2(up, up), f32x2(minus_cut(p0), minus_cut(p1))), x0, x1);
+                                    pk[i] = pack_bf16x2(x0, x1);
+                                }
+                                tmem_st16(tS + at + HELD / 2 + q / 2, pk);
+                            }
                         }
                     }
                     float rs = 0.f;
@@ -806,7 +837,7 @@ __global__ void __launch_bounds__(Shape<D, MODE>::THREADS, 1)
                 // two of its own is released before it waits for a later one (they arrive in the order K, V, K, V, ...).
                 #pragma unroll 1
                 for (int j = first - stride; j < end && ok; j += stride) {
-                    if (j >= first) {   // O_t (+)= P_t V, P_t in the first 64 columns of tile t's S
+                    if (j >= first) {   // O_t (+)= P_t V, P_t in the columns of tile t's S
                         const uint32_t s = gv % NSV;
                         ok = wait_bar(v_full + s, (gv / NSV) & 1, abort) && wait_bar(p_full + t, np++ & 1, abort);
                         // the share of the single item before is still being read
@@ -820,7 +851,12 @@ __global__ void __launch_bounds__(Shape<D, MODE>::THREADS, 1)
                         tc_fence_after();
                         #pragma unroll
                         for (int kk = 0; kk < TK / 16; ++kk)
-                            mma_ts(tO, tS + kk * 8, vb + kk * (2048 >> 4), idesc_o, j > first || kk > 0);
+                            mma_ts(tO, tS + S::p_at(kk), vb + kk * (2048 >> 4), idesc_o, j > first || kk > 0);
+                        if (S::SPLIT) {   // the weights' second halves
+                            #pragma unroll
+                            for (int kk = 0; kk < TK / 16; ++kk)
+                                mma_ts(tO, tS + S::p_at(kk) + S::HELD / 2, vb + kk * (2048 >> 4), idesc_o, true);
+                        }
                         umma_commit(pv_done + t);
                         umma_commit(v_empty + s);
                     }

@@ -705,6 +705,92 @@ def test_attention_decode_shared_reports_bad_pages_and_lengths(dtype, far):
         check(None, 2 ** 31 - 1, 33)
 
 
+def _rounded_weights(q, k, v, dtype):
+    """One token's output if the weights, relative to the largest, were rounded to one number of 16 bits (a planted mistake)."""
+    (nq, d), nkv = q.shape, k.shape[1]
+    o = np.zeros(q.shape)
+    for h in range(nq):
+        s = k[:, h * nkv // nq] @ q[h] / d ** 0.5
+        e = np.exp(s - s.max())
+        p = torch.from_numpy(e * 2.0 ** 13).to(dtype).double().numpy() * 2.0 ** -13
+        o[h] = p @ v[:, h * nkv // nq] / e.sum()
+    return o
+
+
+# Off by 2^-16 of a weight in two halves of bf16 (and 2^-18 where the first is cut), 2^-22 in two of f16, 2^-11 in one.
+@pytest.mark.parametrize("dtype,far,p_err", [(BF16, False, 2.0 ** -16), (BF16, True, 2.0 ** -16 + 2.0 ** -18), (E4M3, False, 2.0 ** -22),
+                                             (E4M3, True, 2.0 ** -11)])
+@pytest.mark.parametrize("nq,nkv,d", [(8, 2, 128), (40, 2, 64)])
+def test_attention_decode_shared_keeps_the_bits_of_weights(dtype, far, p_err, nq, nkv, d):
+    g = _gen(20 + nq)
+    n, page, P = 12, 64, 900
+    cols = -(-P // page)
+    bound = max(P, _far_bound(n, nkv, d, dtype)) if far else P
+    cache = _pool(g, cols + n, nkv, page, d, dtype)
+    ids = torch.randperm(cols + n, device="cuda", generator=g).to(torch.int32)
+    ptable, table = torch.cat([ids[:cols], ids.new_full((-(-bound // page) - cols,), -1)]).view(1, -1), ids[cols:].view(n, 1).contiguous()
+    lens = [(7 * b) % 60 for b in range(n)]
+    rnd = lambda ls: [torch.randn(x, nkv, d, device="cuda", generator=g) for x in ls]   # noqa: E731
+    (pk, pv), = _fill(cache, ptable, [P], rnd([P]), rnd([P]))
+    own = _fill(cache, table, lens, rnd(lens), rnd(lens))
+    q, o = _randn(g, n, nq * d), torch.zeros(n, nq * d, device="cuda", dtype=torch.bfloat16)
+    ws = torch.zeros(Q.h3enc_op_attention_decode_shared_workspace_bytes(n, nq, page), dtype=torch.uint8, device="cuda")
+    Q.h3enc_op_attention_decode_shared(q, o, cache, ptable, _i32([P]), bound, table, _i32(lens), nq, page, ws)
+    caught = 0
+    for b in range(n):
+        k, v, qf = np.concatenate([pk, own[b][0]]), np.concatenate([pv, own[b][1]]), _f64(q[b]).reshape(nq, d)
+        want, A = O.decode.attend_one(qf, k, v)[0], O.decode.attend_one(qf, k, np.abs(v))[0]
+        noise = A * (2 * 16 * 2.0 ** -24 * _score_bound(qf[None], k) + p_err + 2.0 ** -18) * (1 + 2.0 ** -7)
+        if dtype == E4M3 and far:
+            noise += 2.0 ** -37 * np.abs(pv).sum(0).repeat(nq // nkv, 0)
+        _check_bf16(_f64(o[b]).reshape(nq, d), want, noise)
+        caught += (np.abs(_rounded_weights(qf, k, v, torch.bfloat16) - want) > 2.0 ** -8 * np.abs(want) + noise).sum()
+    assert caught > 0 or p_err == 2.0 ** -11       # (one rounding to bf16 would be seen)
+
+
+def test_attention_decode_shared_infinite_values_of_a_prefix():
+    """Both ways of reading a prefix: an infinite value where every weight is above 0 is an infinite output of that column; a
+    score of -inf is a weight of 0; keys of -inf alone in a run of tiles leave the others as they are."""
+    g = _gen(22)
+    n, nq, nkv, d, page, P = 9, 8, 1, 64, 64, 700
+    cols = -(-P // page)
+    cache = _pool(g, cols + n, nkv, page, d, BF16)
+    for far in (False, True):
+        bound = _far_bound(n, nkv, d, BF16) if far else P
+        ptable = torch.full((1, -(-bound // page)), -1, dtype=torch.int32, device="cuda")
+        ptable[0, :cols] = torch.arange(cols, device="cuda")
+        table, lens = _i32([[cols + b] for b in range(n)]), [0, 1, 5, 64, 33, 0, 2, 9, 17]
+        rnd = lambda ls: [torch.randn(x, nkv, d, device="cuda", generator=g) for x in ls]   # noqa: E731
+        pk, pv = rnd([P])[0], rnd([P])[0]
+        pv[17, 0, 5], pv[690, 0, 6] = float("inf"), float("-inf")
+        pk[:140, 0, 0], pk[256:384, 0, 0], pk[699, 0, 0] = float("-inf"), float("-inf"), float("-inf")
+        for masked in (False, True):
+            k = pk.clone()
+            if not masked:
+                k[:, 0, 0] = 0
+            v = pv.clone()
+            if masked:
+                v[17, 0, 5] = 0
+            (kf, vf), = _fill(cache, ptable, [P], [k], [v])
+            own = _fill(cache, table, lens, rnd(lens), rnd(lens))
+            q = _randn(g, n, nq * d).abs() + 0.25
+            o = torch.zeros(n, nq * d, device="cuda", dtype=torch.bfloat16)
+            ws = torch.zeros(Q.h3enc_op_attention_decode_shared_workspace_bytes(n, nq, page), dtype=torch.uint8, device="cuda")
+            Q.h3enc_op_attention_decode_shared(q, o, cache, ptable, _i32([P]), bound, table, _i32(lens), nq, page, ws)
+            got, vf = _f64(o).reshape(n, nq, d), vf.copy()
+            assert (got[..., 6] == -np.inf).all() and (masked or (got[..., 5] == np.inf).all())
+            got[..., 6], vf[..., 6] = 0, 0
+            seen = np.isfinite(kf[:, 0, 0])
+            if not masked:
+                got[..., 5], vf[..., 5] = 0, 0
+            for b in range(n):
+                kk, vv = np.concatenate([kf[seen], own[b][0]]), np.concatenate([vf[seen], own[b][1]])
+                vv[..., 6] = 0
+                if not masked:
+                    vv[..., 5] = 0
+                _check_cross(got[b][None], _f64(q[b]).reshape(1, nq, d), kk, vv, 2.0 ** -16 + 2.0 ** -18)
+
+
 @pytest.mark.parametrize("far", [False, True])
 def test_attention_decode_shared_of_groups_that_run_back(far):
     """Offsets of groups that overlap: reported, nothing written outside, and the workspace is fit for the next call (its arrival
