@@ -478,6 +478,75 @@ def test_attention_cross_reports_bad_offsets(cu_q, cu_k):
         _check_cross(_f64(o[:3]).reshape(3, 2, 64), _f64(q[:3]).reshape(3, 2, 64), *(_f64(k[:cu_k[1]]).reshape(-1, 2, 64),) * 2)
 
 
+# The next ones are the three tests around them at sizes that the tcgen05 kernel takes (over 32 rows per kv head and sequence): cut into parts
+# of single steps (one head), and whole items of many heads, pairs of row tiles (200 rows) and single ones (100), whose halves meet.
+MANY_ROWS = [(200, 1), (200, 160), (100, 1), (100, 160)]
+
+
+@pytest.mark.parametrize("rows,heads", MANY_ROWS)
+def test_attention_cross_of_many_rows_infinite_and_masked_values(rows, heads):
+    g = _gen(23 + rows + heads)
+    L, d = 300, 64
+    q, k, v = _randn(g, rows, heads * d), _randn(g, L + 200, heads * d), _randn(g, L + 200, heads * d)
+    k[L:], v[L:] = float("nan"), float("inf")
+    vh = v.view(L + 200, heads, d)
+    vh[17, :, 5], vh[200, :, 6] = float("inf"), float("-inf")
+    o = torch.zeros(rows, heads * d, device="cuda", dtype=torch.bfloat16)
+    Q.h3enc_op_attention_cross(q, k, v, o, heads, heads, d, _cross_ws(d), _i32([0, rows, rows]), _i32([0, L, L + 200]))
+    got = _f64(o).reshape(rows, heads, d)
+    assert (got[..., 5] == np.inf).all() and (got[..., 6] == -np.inf).all()
+    clean = v[:L].clone()
+    clean.view(L, heads, d)[..., 5:7] = 0
+    got[..., 5:7] = 0
+    qf, kf, vf = (_f64(t).reshape(-1, heads, d) for t in (q, k[:L], clean))
+    _check_cross(got, qf, kf, vf)
+    # keys that every query scores -inf: two whole tiles (one of each half of a single tile's steps), and a part of the last
+    for first, last in ((140, 290), (256, 290)):
+        q2, k2 = q.abs() + 0.5, k[:L].clone()
+        k2.view(L, heads, d)[:first, :, 0], k2.view(L, heads, d)[last:, :, 0] = float("-inf"), float("-inf")
+        Q.h3enc_op_attention_cross(q2, k2, clean, o, heads, heads, d, _cross_ws(d))
+        _check_cross(_f64(o).reshape(rows, heads, d), _f64(q2).reshape(rows, heads, d), kf[first:last], vf[first:last])
+
+
+@pytest.mark.parametrize("rows,heads", MANY_ROWS)
+@pytest.mark.parametrize("d,L", [(128, 2000), (64, 700)])
+def test_attention_cross_of_many_rows_far_apart_scores(rows, heads, d, L):
+    """Keys far above the others for some rows, in the first, a middle and the last tile, growing: the sums before each are rescaled."""
+    g = _gen(24 + rows + heads + d)
+    q, v = _randn(g, rows, heads * d), _randn(g, L, heads * d)
+    for places in ((0,), (L // 2,), (L - 1,), (5, 200, L // 2, L - 40)):
+        k = _randn(g, L, heads * d)
+        for i, at in enumerate(places):
+            k[at] = (q[(3, 17, 64, rows - 1)[i]].float() * (20 if len(places) == 1 else 4 + 6 * i)).to(torch.bfloat16)
+            k[(at + 31) % L] = (q[3].float() * (4 + 3 * i)).to(torch.bfloat16)
+        o = torch.zeros(rows, heads * d, device="cuda", dtype=torch.bfloat16)
+        Q.h3enc_op_attention_cross(q, k, v, o, heads, heads, d, _cross_ws(d))
+        some = sorted({0, 1, heads // 2, heads - 1} & set(range(heads)))   # heads that are compared
+        qf, kf, vf, got = (_f64(t.view(-1, heads, d)[:, some]) for t in (q, k, v, o))
+        for h in range(len(some)):       # (each head's own bound on scores)
+            _check_cross(got[:, h:h + 1], qf[:, h:h + 1], kf[:, h:h + 1], vf[:, h:h + 1])
+
+
+@pytest.mark.parametrize("qlens,klens,nq,nkv,d", [([1] * 5, [900, 3, 65, 700, 1000], 16, 2, 128), ([8], [900], 4, 1, 64), ([31], [900], 5, 5, 128),
+                                                  ([2, 2], [900, 901], 32, 2, 64)])
+def test_attention_cross_of_few_rows_keeps_the_bits_of_weights(qlens, klens, nq, nkv, d):
+    g = _gen(25 + nq)
+    q, kv = _randn(g, sum(qlens), nq * d), _randn(g, sum(klens), 2 * nkv * d)
+    o = torch.zeros(sum(qlens), nq * d, device="cuda", dtype=torch.bfloat16)
+    cu_q, cu_k = (np.concatenate([[0], np.cumsum(x)]) for x in (qlens, klens))
+    Q.h3enc_op_attention_cross(q, kv[:, :nkv * d], kv[:, nkv * d:], o, nq, nkv, d, _cross_ws(d), _i32(cu_q), _i32(cu_k))
+    caught = 0
+    for s in range(len(qlens)):
+        kf, vf = _f64(kv[cu_k[s]:cu_k[s + 1]]).reshape(-1, 2, nkv, d).transpose(1, 0, 2, 3)
+        for t in range(cu_q[s], cu_q[s + 1]):
+            qf, got = (_f64(x[t]).reshape(1, nq, d) for x in (q, o))
+            _check_cross(got, qf, kf, vf, 2.0 ** -16)
+            want, A = O.decoder.cross(qf, kf, vf)[0], O.decoder.cross(qf, kf, np.abs(vf))[0]
+            noise = A * (2 * 16 * 2.0 ** -24 * _score_bound(qf, kf) + 2.0 ** -16 + 2.0 ** -18) * (1 + 2.0 ** -7)
+            caught += (np.abs(_rounded_weights(qf[0], kf, vf, torch.bfloat16) - want) > 2.0 ** -8 * np.abs(want) + noise).sum()
+    assert caught > 0       # (one rounding to bf16 would be seen)
+
+
 @pytest.mark.parametrize("cu_q,cu_k,sound", [([0, 300, 100, 400], [0, 200, 300, 500], []), ([0, 150, 250, 400], [0, 300, 200, 500], [0]),
                                              ([0, 150, 250, 401], [0, 200, 300, 500], [0, 1]), ([-7, 150, 250, 400], [0, 200, 300, 500], [1, 2]),
                                              ([0, 150, 250, 400], [0, 200, 300, 2 ** 31 - 1], [0, 1]),
