@@ -487,7 +487,7 @@ __global__ void __launch_bounds__(Shape<D, MODE>::THREADS, 1)
                         tmem_st32(tS + at, x);
                         tmem_st_wait();
                     }
-                    #pragma unroll 1
+                    #pragma unroll (HELD < TK ? 1 : 2)
                     for (int at = 0; at < TK; at += HELD) {
                         load(at);
                         #pragma unroll
@@ -511,7 +511,7 @@ __global__ void __launch_bounds__(Shape<D, MODE>::THREADS, 1)
                     const float off = m_use == -INFINITY ? 0.f : S::UP_LOG2 - m_use;   // (only -inf scores so far: weights 0)
                     const uint64_t scale2 = f32x2(scale, scale), off2 = f32x2(off, off);
                     uint64_t rs2[4] = {0ull, 0ull, 0ull, 0ull};
-                    #pragma unroll 1
+                    #pragma unroll (HELD < TK ? 1 : 2)
                     for (int at = 0; at < TK; at += HELD) {
                         if (HELD < TK) load(at);
                         #pragma unroll
