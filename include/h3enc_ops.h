@@ -526,9 +526,9 @@ H3ENC_API int64_t h3enc_op_attention_decode_shared_workspace_bytes(int32_t n_seq
  * projection), without a mask; one query per sequence is a decode step.
  *   o[t] = sum_i p_i v_i, p = softmax_i(q[t] . k_i / sqrt(d)), for rows t of [cu_q[b], cu_q[b + 1]) over rows i of
  *   [cu_k[b], cu_k[b + 1]); q head h reads kv head h / (n_heads / n_kv_heads).  fp32, but p enters the second sum in bf16
- *   (up
- *   to 32 rows of queries x heads per kv head and sequence on the average: with 16 bits); o rounded to bf16 once.  Weights below 2^-126 of
- *   the largest count as 0, also times an infinite value, which is NaN.  No keys: zero rows.  Rows of no sequence are left as they were.
+ *   (up to 32 rows of queries x heads per kv head and sequence on the average: with 16 bits); o rounded to bf16 once.  Weights
+ *   below 2^-126 of the largest count as 0, also times an infinite value, which is NaN.  No keys: zero rows.  Rows of no
+ *   sequence are left as they were.
  *   q [Tq, ld_q], o [Tq, ld_o]: head h at column h*d; k [Tk, ld_k], v [Tk, ld_v]: kv head g at column g*d (k and v may be
  *   columns of one projection).  o must not overlap q, k or v.
  *   cu_q, cu_k DEVICE int32 [n_seqs + 1], not running back; each may be NULL with n_seqs 1 (all rows).  Offsets outside

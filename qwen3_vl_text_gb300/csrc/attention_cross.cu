@@ -204,8 +204,9 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint32_t b_l
 // Weight that parts and their join cost (where there are pairs, and where not): packed rows' runs end between items where that makes
 // none longer by more than this.  64 q heads over 8 of 128, runs that cut items against whole ones, and the weight added: 4096 queries
 // over 1024 keys 131 and 118 us (5), 512 over 1024 37.3 and 24.3 (3), 512 over 4096 73 and 64 (10), 16 ragged prompts 181 and 173 (10);
-// 64 over 1024 16.9 and 23.5 (16), 256 over 4096 45 and 64 (38).  Single tiles, 16 queries each over 500 keys, 16 sequences 20.9 and
-// 15.2 (1), 30 over 1000 40.1 and 35.7 (5).
+// 64 over 1024 16.9 and 23.5 (16), 256 over 4096 45 and 64 (38).  Single tiles, 16 queries each over 500 keys, 16 sequences 21.3 and
+// 15.6 (1), 30 over 1000 40.1 and 36.2 (5); 1 over 1000 13.3 and 17.4 (8), 4 of 100 queries of 10 heads over 4096 26.1 and 40.0 (26);
+// 9 of 64 queries of 10 heads over 2000 28.3 and 27.1 (8: the rule misses it).
 constexpr int JOIN_PAIRS = 12, JOIN_SINGLES = 6;
 
 template <int D, int MODE>
@@ -794,7 +795,7 @@ __global__ void __launch_bounds__(Shape<D, MODE>::THREADS, 1)
         // ------------------------------------------------ products: one thread for each row tile
         // A product of 128 x 128 x 16 takes 64 cycles, and its issue about as long; a wait or a commit costs the issuing
         // thread 50 to 90 more, so with one thread for both tiles the tensor cores stood still a third of the time (4096
-        // tokens over 4096 keys, 64 heads over 8 of 128: 440 us; two threads made it 392).
+        // tokens over 4096 keys, 64 heads over 8 of 128, as it was then: 440 us, with two threads 392).
         constexpr uint32_t kind = F8 ? 0u : (1u << 7) | (1u << 10);   // A and B f16, or bf16
         constexpr uint32_t base = (1u << 4) | kind | ((uint32_t)(TQ >> 4) << 24);
         constexpr uint32_t idesc_s = base | ((uint32_t)(TK >> 3) << 17);

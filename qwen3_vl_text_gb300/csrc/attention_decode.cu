@@ -963,8 +963,9 @@ __global__ void __launch_bounds__(256) attention_weight_kernel(const AttentionDe
 }
 
 // Bytes of prefixes that sequences read again each rather than in one pass for all.  64 q heads over 8 kv heads of 128, own tokens 50 to
-// 300: 8 sequences behind 4000 tokens (131 MB) 21 us against 30, 64 behind 700 (184 MB) 33 against 42; 4 behind 30,000 (492 MB) 51
-// against 50.
+// 300: 8 sequences behind 4000 tokens (131 MB) 22 us against 29, 64 behind 700 (184 MB) 37 against 44; 16 behind 4000 (262 MB) 33 against
+// 31, 16 behind 8000 (524 MB) 52 against 35.  e4m3: 8 behind 4000 (66 MB) 22 against 33, 16 behind 4000 (131 MB) 33 against 34, 16 behind
+// 8000 (262 MB) 50 against 38.
 constexpr double kPrefixAgain = 2e8;
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 
@@ -1083,10 +1084,15 @@ bool attention_prefix_near(const AttentionDecode &p) {
 }
 
 int attention_packed_rows(int Tq, int Tk, int n_segs, int nq, int nkv) {
-    // Rows of a segment if the queries are spread evenly.  Up to 32 this kernel reads the keys once, in one launch; beyond, a tcgen05
-    // tile of 128 rows does.  64 q heads over 8 of 128, this kernel against the other: 1 query over 1024 keys 7.3 us and 12.4, 64
-    // sequences of 1 over 77 to 512 21 and 29; 8 queries (64 rows) over 100 keys 11.7 and 9.1, over 1024 14.2 and 12.4, over 4096 24.6
-    // and 14.8; 64 over 1024 29 and 16.5.
+    // Rows of a segment if the queries are spread evenly.  Up to 32 this kernel reads the keys once, in one launch, and keeps 16 bits of
+    // a weight; beyond, a tcgen05 tile of 128 rows does (8 bits).  By time alone the limit would be 16.  This kernel against the
+    // other, us, 64 q heads over 8 of 128 (8 over 8 the same within 0.3, as are 32 over 32 with as many segments), sequences x keys:
+    //   rows       8            16           24           32           64
+    //   1 x 1024   7.8   12.3   10.0  12.3   12.8  12.3   14.5  12.2   14.8  13.2
+    //   1 x 4096   11.3  14.7   15.7  14.7   21.7  14.6   25.0  14.9   25.6  15.5
+    //   64 x 128   14.0  20.9   19.0  20.9   23.6  21.0   25.8  21.1   38.8  21.0
+    //   16 x 1024  15.2  18.1   20.4  18.1   28.1  18.2   30.5  18.2   44.9  18.1
+    //   64 x 4096  164   171    171   173    209   174    214   175    406   182
     const long long group = nq / nkv, rows = group * ((Tq + n_segs - 1) / n_segs);
     if (rows > 32) return 0;
     return cross::packed_bound(Tq, Tk, n_segs, nq, nkv) < 0 ? 0 : (int)std::max(rows, 1LL);

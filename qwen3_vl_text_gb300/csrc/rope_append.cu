@@ -43,7 +43,8 @@ __device__ __forceinline__ int sequence_of(const int32_t *cu, int n_seqs, int t,
 // halves of eight pairs, with pairs (2j, 2j + 1) any chunk holds whole pairs), the others hold the chunks that are not rotated.
 // Each row has 1 << gshift groups of a CTA, which take its heads in turn (blockIdx.y: every gridDim.y-th turn).
 // A CTA takes `share` rows, GROUPS >> gshift at a time, and finds places and angles of all of them at its beginning: with
-// that chain in front of every two rows of 80 heads of 128, 5600 rows took 63 us instead of 53 (4.5 TB/s; 8192 rows 68 us, 5.2).
+// that chain in front of every two rows of 80 heads of 128, 5600 rows took 63 us instead of 53 (4.5 TB/s; 8192 rows 68 us, 5.2).  Not
+// HBM's limit: kv_cache.cu's kernel, which is given slots and tables, takes 61.7 us for those 8192 rows.
 // BATCH: head vectors a group loads before it works on the first.
 template <int D, int BATCH>
 __global__ void __launch_bounds__(THREADS, BATCH == 1 ? 4 : 3)
@@ -230,8 +231,9 @@ cudaError_t launch_rope_append(const RopeAppend &p, cudaStream_t st) {
         if (idle <= waste || p.T < sms) gshift = g, waste = idle;
     }
     const int per_cta = groups >> gshift;
-    // rows of a CTA: four rounds of the three resident CTAs per SM (one, two and three rounds: 55.6, 54.9 and 56.1 us in that
-    // case; 8192 rows 73.1, 71.9 and 67.8 against 67.9), up to what a CTA has places for
+    // rows of a CTA: up to four rounds of the three resident CTAs per SM (one, two and three rounds: 55.6, 54.9 and 56.1 us in that
+    // case; 8192 rows 73.1, 71.9 and 67.8 against 67.9), in whole groups of rows and up to what a CTA has places for: 5580 rows are
+    // 1395 CTAs, 3.06 rounds, 8192 are 1366
     int share = (p.T + 12 * sms - 1) / (12 * sms);
     share = std::min((share + per_cta - 1) / per_cta * per_cta, groups);
     const int rows = (p.T + share - 1) / share;
