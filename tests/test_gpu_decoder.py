@@ -10,7 +10,7 @@ An e4m3 value is off by half a step: 2^-4 of the value, 2^-10 at least.
 Attention: with S1 = max_i sum_e |q_e k_ie| / sqrt(d), the fp32 score of d products is off by at most DELTA = 16 * 2^-24 * S1
 (16 accumulation steps of 16 products, and the same again for the base-2 exponent), so a weight by a factor of at most
 1 + 2 DELTA; it enters the value product in bf16, 2^-8 of it (f16 behind an e4m3 cache: 2^-11, and at least 2^-37
-absolutely; a sequence's own tokens, few queries, near prefixes: two halves, 2^-16).  With A = sum_i p_i |v_i| the output is off by A times that, 2^-18 A for
+absolutely; a sequence's own tokens, few queries, near prefixes and those in bf16: two halves, 2^-16).  With A = sum_i p_i |v_i| the output is off by A times that, 2^-18 A for
 fp32 sums and the joins, and half a step of bf16.  An accumulated weight is off by 2 DELTA + 2^-18 of sum_h p_h.
 """
 import numpy as np
